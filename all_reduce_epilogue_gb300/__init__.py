@@ -13,6 +13,14 @@ Operations (the same names as the C ABI, without the ``are_`` prefix):
   into every rank view.
 * ``allreduce_rmsnorm(partials, residual, gamma, eps, out, ws)``
   all-reduce + residual + RMSNorm in one Lamport-synchronised kernel.
+* ``allreduce_rmsnorm_quant_groups(partials, residual, gamma, eps, out_q,
+  out_scale, ws, group)``  the same with FP8 codes and a scale per group of
+  columns.
+* ``allreduce_rmsnorm_backward(dy, h, gamma, eps, dh, dgamma, ws)``  its
+  backward pass.
+* ``gemm_ar_qweight(x, w, out, ws)``, ``gemm_ar_qweight_qx(xq, xscale, w, out,
+  ws)``  the row-parallel linear of a few tokens with 4-bit weights
+  (``QWeight``), all-reduced; tokens in bf16 or in FP8 codes with scales.
 """
 from __future__ import annotations
 
@@ -27,6 +35,9 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libare.so")
 OK, EINVAL, ENOMEM, ECUDA, ETIMEOUT, EBUSY, ENODEV, ECAPACITY, ECAPTURE = range(9)
 # ops
 OP_GEMM_RS, OP_GEMM_AR, OP_ALLREDUCE_RMSNORM = 1, 2, 3
+OP_ALLREDUCE_RMSNORM_BACKWARD, OP_GEMM_AR_QWEIGHT = 4, 5
+# scale formats (are_scale_format)
+SCALE_F32, SCALE_E8M0 = 0, 1
 # debug flags
 DEBUG_NO_REARM, DEBUG_LOG_PIECES, DEBUG_COUNT_CANON, DEBUG_SKIP_PUBLISH, DEBUG_SKIP_STAGE = 1, 2, 4, 8, 16
 DEBUG_SINGLE_CTA, DEBUG_WAIT_PROFILE, DEBUG_AR_ONESHOT, DEBUG_AR_LAMPORT, DEBUG_PAIR_CTA = 32, 64, 128, 256, 512
@@ -39,7 +50,8 @@ CHUNK_CAP = 64          # chunk counters per owner segment in the workspace
 CHUNK_Q = 1 << 32       # counter advance per completed chunk
 # kernels (are_kernel), as reported by Workspace.last_launch()
 KERNEL_NAMES = {0: "none", 1: "memset", 2: "gemm_reduce_kernel", 3: "gemm_pair_kernel", 4: "ar_rmsnorm_kernel",
-                5: "ar_oneshot_kernel"}
+                5: "ar_oneshot_kernel", 6: "norm_quant_rows_kernel", 7: "norm_backward_rows_kernel",
+                8: "qweight_kernel"}
 PIECE_WORDS = 64
 TILE_M, TILE_N = 128, 256
 
@@ -51,6 +63,8 @@ EXPORTS = [
     "are_get_device_status", "are_debug_snapshot", "are_debug_last_launch",
     "are_gemm_rs", "are_gemm_ar", "are_allreduce_rmsnorm", "are_allreduce_add_rmsnorm", "are_allreduce_rmsnorm_quant",
     "are_allreduce_rmsnorm_noalloc", "are_noalloc_device_status",
+    "are_allreduce_rmsnorm_quant_groups", "are_allreduce_rmsnorm_backward", "are_gemm_ar_qweight",
+    "are_gemm_ar_qweight_qx",
 ]
 
 
@@ -137,6 +151,15 @@ def load_library(path: str = LIB_PATH):
     lib.are_allreduce_rmsnorm_quant.argtypes = [vp, vp, vp, ctypes.c_float, vp, vp, vp, i32, i64, i64, vp, vp]
     lib.are_allreduce_rmsnorm_noalloc.restype = i32
     lib.are_allreduce_rmsnorm_noalloc.argtypes = [vp, vp, vp, ctypes.c_float, vp, i32, i64, i64, vp]
+    f32 = ctypes.c_float
+    lib.are_allreduce_rmsnorm_quant_groups.restype = i32
+    lib.are_allreduce_rmsnorm_quant_groups.argtypes = [vp, vp, vp, f32, i32, i32, vp, vp, vp, i32, i64, i64, vp, vp]
+    lib.are_allreduce_rmsnorm_backward.restype = i32
+    lib.are_allreduce_rmsnorm_backward.argtypes = [vp, vp, vp, f32, vp, vp, vp, i32, i64, i64, vp, vp]
+    lib.are_gemm_ar_qweight.restype = i32
+    lib.are_gemm_ar_qweight.argtypes = [vp, vp, i32, vp, i32, i64, i64, i64, vp, vp]
+    lib.are_gemm_ar_qweight_qx.restype = i32
+    lib.are_gemm_ar_qweight_qx.argtypes = [vp, vp, i32, i32, vp, i32, vp, i32, i64, i64, i64, vp, vp]
     _lib = lib
     return lib
 
@@ -168,6 +191,11 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+
 def _ptrs(tensors) -> ctypes.Array:
     return (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
 
@@ -188,6 +216,7 @@ class Workspace:
         lib = load_library()
         caps = _Caps(R_max, M_max, N_max, K_max, timeout_ns, debug_flags, 0)
         h = ctypes.c_void_p()
+        self.device_index = _current_device()
         _check(lib.are_workspace_create(ctypes.byref(h), ctypes.byref(caps)), "are_workspace_create")
         self._h = h
         self.caps = dict(R_max=R_max, M_max=M_max, N_max=N_max, K_max=K_max)
@@ -417,3 +446,198 @@ def noalloc_device_status() -> dict:
     if rc not in (OK, ETIMEOUT):
         raise AreError(rc, "are_noalloc_device_status")
     return {"status": rc, "code": st.code, "where": st.where, "a": st.a, "b": st.b}
+
+
+# Argument checks of the operations below: type, shape, contiguity, and the
+# workspace's device.
+def _need(t, dtype, shape, dev: int, what: str):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _need_one_of(t, dtypes, shape, dev: int, what: str):
+    _need(t, t.dtype if t.dtype in dtypes else dtypes[0], shape, dev, what)
+
+
+def _ranks(tensors, what: str) -> int:
+    if not 1 <= len(tensors) <= 8:
+        raise ValueError(f"{what}: 1 to 8 ranks, got {len(tensors)}")
+    return len(tensors)
+
+
+def _matrix(t, what: str):
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _group_of(group: int, what: str) -> int:
+    if group not in (32, 64, 128):
+        raise ValueError(f"{what} must be 32, 64 or 128, got {group}")
+    return group
+
+
+def _on_stream(stream, dev: int) -> int:
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is on CUDA device {stream.device_index}, the workspace on {dev}")
+    return stream.cuda_stream
+
+
+def _scale_kinds():
+    import torch
+    return {torch.float32: SCALE_F32, torch.uint8: SCALE_E8M0, torch.float8_e8m0fnu: SCALE_E8M0}
+
+
+def allreduce_rmsnorm_quant_groups(partials: Sequence, residual, gamma, eps: float, out_q, out_scale, ws: Workspace,
+                                   group: int = 128, residual_out=None, stream=None):
+    """FP8 E4M3 codes of y = rmsnorm(sum_r partials[r] + residual) * gamma with
+    one scale per ``group`` (32, 64, 128) columns: y ~= e4m3(out_q) * scale.
+
+    ``out_q``: [M, N] uint8 or float8_e4m3fn.  ``out_scale``:
+    [M, ceil(N / group)], float32 (max / 448) or uint8 / float8_e8m0fnu (the
+    power of two above it).  ``residual_out`` (may be ``residual``): bf16 sum."""
+    import torch
+    dev, bf16 = ws.device_index, torch.bfloat16
+    R = _ranks(partials, "partials")
+    shape = _matrix(partials[0], "partials")
+    M, N = shape
+    for t in partials:
+        _need(t, bf16, shape, dev, "partials")
+    if residual is not None:
+        _need(residual, bf16, shape, dev, "residual")
+    if residual_out is not None:
+        _need(residual_out, bf16, shape, dev, "residual_out")
+    _need(gamma, torch.float32, (N,), dev, "gamma")
+    _need_one_of(out_q, (torch.uint8, torch.float8_e4m3fn), shape, dev, "out_q")
+    kinds = _scale_kinds()
+    _need_one_of(out_scale, tuple(kinds), (M, -(-N // _group_of(group, "group"))), dev, "out_scale")
+    rc = load_library().are_allreduce_rmsnorm_quant_groups(
+        _ptrs(partials), residual.data_ptr() if residual is not None else None, gamma.data_ptr(), eps,
+        kinds[out_scale.dtype], group, out_q.data_ptr(), out_scale.data_ptr(),
+        residual_out.data_ptr() if residual_out is not None else None, R, M, N, ws.handle, _on_stream(stream, dev))
+    _check(rc, "are_allreduce_rmsnorm_quant_groups")
+
+
+def allreduce_rmsnorm_backward(dy: Sequence, h, gamma, eps: float, dh, dgamma, ws: Workspace, dres=None, stream=None):
+    """Backward pass of all-reduce + residual + RMSNorm.
+
+    ``dy``: R bf16 [M, N] partials of the output's gradient, summed first;
+    ``h``: the updated residual (``residual_out`` of the forward call);
+    ``dres``: the gradient of that residual, or None.  Writes ``dh`` (bf16; may
+    be ``dres``), the gradient of every partial and of the incoming residual,
+    and ``dgamma`` (float32 [N], or None)."""
+    import torch
+    dev, bf16 = ws.device_index, torch.bfloat16
+    R = _ranks(dy, "dy")
+    shape = _matrix(dy[0], "dy")
+    M, N = shape
+    for t in dy:
+        _need(t, bf16, shape, dev, "dy")
+    _need(h, bf16, shape, dev, "h")
+    _need(dh, bf16, shape, dev, "dh")
+    if dres is not None:
+        _need(dres, bf16, shape, dev, "dres")
+    _need(gamma, torch.float32, (N,), dev, "gamma")
+    if dgamma is not None:
+        _need(dgamma, torch.float32, (N,), dev, "dgamma")
+    rc = load_library().are_allreduce_rmsnorm_backward(
+        _ptrs(dy), h.data_ptr(), gamma.data_ptr(), eps, dres.data_ptr() if dres is not None else None, dh.data_ptr(),
+        dgamma.data_ptr() if dgamma is not None else None, R, M, N, ws.handle, _on_stream(stream, dev))
+    _check(rc, "are_allreduce_rmsnorm_backward")
+
+
+class QWeight:
+    """One rank's 4-bit weights: weight (n, k) = (u - zero[n, k // group]) *
+    scale[n, k // group].
+
+    ``codes``: uint8 [N, K / 2], byte i of a row holds k = 2i in its lower and
+    2i + 1 in its upper four bits; ``scale``: bf16 [N, ceil(K / group)];
+    ``zero``: uint8 of the same shape, values 0..15, or None (8 everywhere);
+    ``group``: 32, 64 or 128."""
+
+    __slots__ = ("codes", "scale", "zero", "group", "N", "K")
+
+    def __init__(self, codes, scale, zero=None, group: int = 128):
+        import torch
+        dev = codes.get_device()
+        N, half = _matrix(codes, "codes")
+        self.N, self.K, self.group = N, 2 * half, _group_of(group, "group")
+        _need(codes, torch.uint8, (N, half), dev, "codes")
+        groups = (N, -(-self.K // group))
+        _need(scale, torch.bfloat16, groups, dev, "scale")
+        if zero is not None:
+            _need(zero, torch.uint8, groups, dev, "zero")
+        self.codes, self.scale, self.zero = codes, scale, zero
+
+
+def _qweights(w: Sequence, R: int, M: int, K: int, out, dev: int):
+    """The C arrays of the weights and of the output views."""
+    import torch
+    N, group = w[0].N, w[0].group
+    if len(w) != R:
+        raise ValueError(f"{R} ranks of tokens, {len(w)} of weights")
+    ptrs = []
+    for q in w:
+        if q.N != N or q.K != K or q.group != group or q.codes.get_device() != dev:
+            raise ValueError(f"every rank's weights must be [{N}, {K}] in groups of {group} on CUDA device {dev}")
+        ptrs += (q.codes.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr() if q.zero is not None else None)
+    if isinstance(out, (list, tuple)):
+        if len(out) != R:
+            raise ValueError(f"{R} ranks, {len(out)} output views")
+        for t in out:
+            _need(t, torch.bfloat16, (M, N), dev, "out")
+        views = _ptrs(out)
+    else:
+        _need(out, torch.bfloat16, (M, N), dev, "out")
+        views = (ctypes.c_void_p * R)(*[out.data_ptr()] * R)
+    return (ctypes.c_void_p * (3 * R))(*ptrs), group, views, N
+
+
+def gemm_ar_qweight(x: Sequence, w: Sequence, out, ws: Workspace, stream=None):
+    """Every view out[v] = bf16(sum_r x[r] @ w[r].T) with 4-bit weights.
+
+    ``x``: R bf16 [M, K] token tensors; ``w``: R ``QWeight``; ``out``: one
+    bf16 [M, N] tensor, or a list of R views (they may alias)."""
+    import torch
+    dev = ws.device_index
+    R = _ranks(x, "x")
+    shape = _matrix(x[0], "x")
+    M, K = shape
+    for t in x:
+        _need(t, torch.bfloat16, shape, dev, "x")
+    weights, group, views, N = _qweights(w, R, M, K, out, dev)
+    rc = load_library().are_gemm_ar_qweight(_ptrs(x), weights, group, views, R, M, N, K, ws.handle,
+                                            _on_stream(stream, dev))
+    _check(rc, "are_gemm_ar_qweight")
+
+
+def gemm_ar_qweight_qx(xq: Sequence, xscale: Sequence, w: Sequence, out, ws: Workspace, xgroup: int = 128,
+                       stream=None):
+    """As ``gemm_ar_qweight`` with tokens e4m3(xq[r]) * xscale[r], as
+    ``allreduce_rmsnorm_quant_groups`` writes them.
+
+    ``xq``: R [M, K] uint8 or float8_e4m3fn tensors; ``xscale``: R tensors
+    [M, ceil(K / xgroup)], float32 or uint8 / float8_e8m0fnu (all of one
+    kind)."""
+    import torch
+    dev = ws.device_index
+    R = _ranks(xq, "xq")
+    shape = _matrix(xq[0], "xq")
+    M, K = shape
+    if len(xscale) != R:
+        raise ValueError(f"{R} ranks of codes, {len(xscale)} of scales")
+    kinds = _scale_kinds()
+    sshape, sdt = (M, -(-K // _group_of(xgroup, "xgroup"))), xscale[0].dtype
+    if sdt not in kinds:
+        raise ValueError(f"xscale must be float32, uint8 or float8_e8m0fnu, got {sdt}")
+    for t, f in zip(xq, xscale):
+        _need_one_of(t, (torch.uint8, torch.float8_e4m3fn), shape, dev, "xq")
+        _need(f, sdt, sshape, dev, "xscale")
+    weights, group, views, N = _qweights(w, R, M, K, out, dev)
+    rc = load_library().are_gemm_ar_qweight_qx(_ptrs(xq), _ptrs(xscale), kinds[sdt], xgroup, weights, group, views, R,
+                                               M, N, K, ws.handle, _on_stream(stream, dev))
+    _check(rc, "are_gemm_ar_qweight_qx")

@@ -37,6 +37,7 @@ struct are_ws {
     size_t piece_words = 0;
     uint32_t* d_staging = nullptr;
     size_t staging_words = 0;
+    float* d_dgamma = nullptr;        // backward: the blocks' partial dgamma sums
     int ar_resident[kArMaxPpt + 1] = {0};
     uint64_t oneshot_max_bytes = 0;   // set at creation
     std::mutex mu;
@@ -94,6 +95,7 @@ void free_ws(are_ws* ws) {
     cudaFree(ws->d_part);
     cudaFree(ws->d_pieces);
     cudaFree(ws->d_staging);
+    cudaFree(ws->d_dgamma);
     cudaFree(ws->d_chunk_ctr);
     cudaFree(ws->d_cons);
     if (ws->h_chunk_gen) cudaFreeHost(ws->h_chunk_gen);
@@ -416,6 +418,14 @@ are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K) {
         case ARE_OP_ALLREDUCE_RMSNORM:
             if (N % 8 || N > 32768) return ARE_EINVAL;
             return ARE_OK;
+        case ARE_OP_ALLREDUCE_RMSNORM_BACKWARD:
+            if (N % 8 || N > kBackwardMaxN) return ARE_EINVAL;
+            return ARE_OK;
+        case ARE_OP_GEMM_AR_QWEIGHT:
+            if (K < 0 || K >= kLim || K % 32 || N % 8) return ARE_EINVAL;
+            // CTAs of 16 rows x 8 tokens, the smallest tiles, count below 2^31
+            if (ceil_div(M, 8) * ceil_div(N, 16) >= kLim / kMaxRanks) return ARE_EINVAL;
+            return ARE_OK;
         default:
             return ARE_EINVAL;
     }
@@ -471,6 +481,9 @@ are_status are_workspace_create(are_ws** out, const are_caps* caps) {
         for (int ppt = 1; ppt <= kArMaxPpt; ++ppt) ws->ar_resident[ppt] = ar_rmsnorm_resident_blocks(ppt, ws->num_sms);
         if (e == cudaSuccess) e = ar_oneshot_prepare();
     }
+    if (e == cudaSuccess) e = cudaMalloc(&ws->d_dgamma, norm_backward_scratch_words(caps->N_max, ws->num_sms) * 4);
+    if (e == cudaSuccess) e = rows_prepare();
+    if (e == cudaSuccess) e = qweight_prepare();
     if (e != cudaSuccess) {
         are_status st = from_cuda(e);
         free_ws(ws);
@@ -707,6 +720,193 @@ are_status are_allreduce_rmsnorm_quant(const are_bf16* const partials[], const a
                                        int64_t M, int64_t N, are_ws* ws, void* stream) {
     return allreduce_rmsnorm_call(partials, residual, gamma, eps, nullptr, residual_out, out_q, out_scale, R, M, N,
                                   ws, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks that the operations below share: the workspace's device is the current one.
+bool on_device(const are_ws* ws) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == ws->device;
+}
+
+bool aligned_to(const void* p, uintptr_t bytes) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+int log2_group(int group) { return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : -1; }
+
+bool scale_format_ok(int f) { return f == ARE_SCALE_F32 || f == ARE_SCALE_E8M0; }
+
+// A scale tensor has no alignment but its element's.
+bool scale_ptr_ok(const void* p, int format) { return aligned_to(p, format == ARE_SCALE_F32 ? 4 : 1); }
+
+void rows_common(RowsParams& p, const are_ws* ws, const are_bf16* const parts[], const float* gamma, float eps, int R,
+                 int64_t M, int64_t N) {
+    std::memset(&p, 0, sizeof(p));
+    for (int r = 0; r < R; ++r) p.src[r] = parts[r];
+    p.nsrc = R;
+    p.gamma = gamma;
+    p.status = ws->d_status;
+    p.M = M;
+    p.R = R;
+    p.N = (int)N;
+    p.eps = eps;
+    p.inv_n = 1.0f / (float)N;
+    p.timeout_ns = ws->timeout_ns;
+}
+
+are_status qweight_call(const void* const x[], const void* const xscale[], int scale_format, int xgroup, bool qx,
+                        const are_qweight w[], int group, are_bf16* const out[], int R, int64_t M, int64_t N, int64_t K,
+                        are_ws* ws, void* stream) {
+    if (!ws || !x || !w || !out || (qx && !xscale)) return ARE_EINVAL;
+    are_status st = are_supports(ARE_OP_GEMM_AR_QWEIGHT, R, M, N, K);
+    if (st != ARE_OK) return st;
+    if (log2_group(group) < 0 || (qx && (log2_group(xgroup) < 0 || !scale_format_ok(scale_format)))) return ARE_EINVAL;
+    const bool reads = M > 0 && N > 0 && K > 0;
+    for (int r = 0; r < R; ++r) {
+        if (!ptr_ok(x[r], M * K) || !ptr_ok(w[r].codes, N * K) || !ptr_ok(out[r], M * N)) return ARE_EINVAL;
+        if (reads && (!aligned_to(w[r].scale, 2) || (qx && !scale_ptr_ok(xscale[r], scale_format)))) return ARE_EINVAL;
+    }
+    TryLock lk(ws->mu);
+    if (!lk.ok) return ARE_EBUSY;
+    if (!on_device(ws)) return ARE_EINVAL;
+    if (R > ws->caps.R_max) return ARE_ECAPACITY;
+    ws->last = are_launch_info{};
+    if (M == 0 || N == 0) return ARE_OK;
+
+    QweightParams p;
+    std::memset(&p, 0, sizeof(p));
+    for (int v = 0; v < R; ++v) {
+        bool dup = false;
+        for (int u = 0; u < p.nviews; ++u) dup |= p.views[u] == out[v];
+        if (!dup) p.views[p.nviews++] = out[v];
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (K == 0) {  // empty contraction: the result is zero
+        ws->last.kernel = ARE_KERNEL_MEMSET;
+        for (int v = 0; v < p.nviews; ++v) {
+            cudaError_t e = cudaMemsetAsync(p.views[v], 0, (size_t)M * N * 2, s);
+            if (e != cudaSuccess) return from_cuda(e);
+        }
+        return ARE_OK;
+    }
+    for (int r = 0; r < R; ++r) {
+        p.x[r] = x[r];
+        p.xscale[r] = qx ? xscale[r] : nullptr;
+        p.codes[r] = w[r].codes;
+        p.scale[r] = w[r].scale;
+        p.zero[r] = w[r].zero;
+    }
+    p.R = R;
+    p.M = (int)M;
+    p.N = (int)N;
+    p.K = (int)K;
+    p.group_shift = log2_group(group);
+    p.groups = (int)ceil_div(K, group);
+    if (qx) {
+        p.xgroup_shift = log2_group(xgroup);
+        p.xgroups = (int)ceil_div(K, xgroup);
+        p.xpow2 = scale_format == ARE_SCALE_E8M0;
+    }
+    int grid = 0, variant = 0, cluster = 0;
+    const cudaError_t e = launch_qweight(p, qx, ws->num_sms, &grid, &variant, &cluster, s);
+    ws->last = are_launch_info{ARE_KERNEL_QWEIGHT, grid, 256, cluster, 0, variant, 0, 0};
+    return from_cuda(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+are_status are_allreduce_rmsnorm_quant_groups(const are_bf16* const partials[], const are_bf16* residual,
+                                              const float* gamma, float eps, int scale_format, int group,
+                                              uint8_t* out_q, void* out_scale, are_bf16* residual_out, int R,
+                                              int64_t M, int64_t N, are_ws* ws, void* stream) {
+    if (!ws || !partials) return ARE_EINVAL;
+    are_status st = are_supports(ARE_OP_ALLREDUCE_RMSNORM, R, M, N, 0);
+    if (st != ARE_OK) return st;
+    if (!scale_format_ok(scale_format) || log2_group(group) < 0) return ARE_EINVAL;
+    for (int r = 0; r < R; ++r)
+        if (!ptr_ok(partials[r], M * N)) return ARE_EINVAL;
+    if ((residual && !aligned16(residual)) || (residual_out && !aligned16(residual_out)) || !ptr_ok(gamma, N) ||
+        !ptr_ok(out_q, M * N) || (M * N > 0 && !scale_ptr_ok(out_scale, scale_format)))
+        return ARE_EINVAL;
+    if (!(eps > 0.f) || !std::isfinite(eps)) return ARE_EINVAL;
+    TryLock lk(ws->mu);
+    if (!lk.ok) return ARE_EBUSY;
+    if (!on_device(ws)) return ARE_EINVAL;
+    if (R > ws->caps.R_max) return ARE_ECAPACITY;
+    ws->last = are_launch_info{};
+    if (M == 0 || N == 0) return ARE_OK;
+
+    RowsParams p;
+    rows_common(p, ws, partials, gamma, eps, R, M, N);
+    if (residual) {
+        p.src[p.nsrc++] = residual;
+        p.has_res = 1;
+    }
+    p.res_out = residual_out;
+    p.out_q = out_q;
+    p.out_scale = out_scale;
+    p.groups = (int)ceil_div(N, group);
+    p.group_packs = group / 8;
+    const RowsPlan plan = rows_plan(p, ws->num_sms);
+    ws->last = are_launch_info{ARE_KERNEL_NORM_QUANT_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
+    return from_cuda(launch_norm_quant_rows(p, plan, scale_format == ARE_SCALE_E8M0,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+are_status are_allreduce_rmsnorm_backward(const are_bf16* const dy[], const are_bf16* h, const float* gamma, float eps,
+                                          const are_bf16* dres, are_bf16* dh, float* dgamma, int R, int64_t M,
+                                          int64_t N, are_ws* ws, void* stream) {
+    if (!ws || !dy) return ARE_EINVAL;
+    are_status st = are_supports(ARE_OP_ALLREDUCE_RMSNORM_BACKWARD, R, M, N, 0);
+    if (st != ARE_OK) return st;
+    for (int r = 0; r < R; ++r)
+        if (!ptr_ok(dy[r], M * N)) return ARE_EINVAL;
+    if (!ptr_ok(h, M * N) || (dres && !aligned16(dres)) || !ptr_ok(dh, M * N) || !ptr_ok(gamma, N) ||
+        (dgamma && !aligned16(dgamma)))
+        return ARE_EINVAL;
+    if (!(eps > 0.f) || !std::isfinite(eps)) return ARE_EINVAL;
+    TryLock lk(ws->mu);
+    if (!lk.ok) return ARE_EBUSY;
+    if (!on_device(ws)) return ARE_EINVAL;
+    if (R > ws->caps.R_max || N > ws->caps.N_max) return ARE_ECAPACITY;
+    ws->last = are_launch_info{};
+    if (N == 0) return ARE_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0) {  // a sum over no rows
+        if (!dgamma) return ARE_OK;
+        ws->last.kernel = ARE_KERNEL_MEMSET;
+        return from_cuda(cudaMemsetAsync(dgamma, 0, (size_t)N * 4, s));
+    }
+
+    RowsParams p;
+    rows_common(p, ws, dy, gamma, eps, R, M, N);
+    p.src[p.nsrc++] = h;
+    if (dres) {
+        p.src[p.nsrc++] = dres;
+        p.has_res = 1;
+    }
+    p.res_out = dh;
+    p.gamma_in_smem = 1;
+    const RowsPlan plan = rows_plan(p, ws->num_sms);
+    ws->last = are_launch_info{ARE_KERNEL_NORM_BACKWARD_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
+    return from_cuda(launch_norm_backward_rows(p, plan, ws->d_dgamma, dgamma, s));
+}
+
+are_status are_gemm_ar_qweight(const are_bf16* const x[], const are_qweight w[], int group, are_bf16* const out[], int R,
+                               int64_t M, int64_t N, int64_t K, are_ws* ws, void* stream) {
+    return qweight_call(reinterpret_cast<const void* const*>(x), nullptr, ARE_SCALE_F32, 128, false, w, group, out, R, M,
+                        N, K, ws, stream);
+}
+
+are_status are_gemm_ar_qweight_qx(const uint8_t* const xq[], const void* const xscale[], int scale_format, int xgroup,
+                                  const are_qweight w[], int group, are_bf16* const out[], int R, int64_t M, int64_t N,
+                                  int64_t K, are_ws* ws, void* stream) {
+    return qweight_call(reinterpret_cast<const void* const*>(xq), xscale, scale_format, xgroup, true, w, group, out, R,
+                        M, N, K, ws, stream);
 }
 
 }  // extern "C"

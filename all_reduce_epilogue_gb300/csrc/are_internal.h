@@ -79,6 +79,75 @@ int ar_oneshot_threads();
 // Fill n 32-bit words with v.
 cudaError_t launch_fill_u32(uint32_t* dst, uint32_t v, size_t n, cudaStream_t stream);
 
+// ------------------------------------------------------------------ row-streaming norm kernels
+constexpr int kRowSources = kMaxRanks + 2;
+constexpr int64_t kBackwardMaxN = 16384;  // widest row whose dgamma sums fit a block's registers
+
+struct RowsParams {
+    const uint16_t* src[kRowSources];  // bf16 [M, N] each: the R partials, then residual (forward) or h and d_res (backward)
+    const float* gamma;                // fp32 [N]
+    uint16_t* res_out;                 // bf16 [M, N]: h or nullptr (forward); dh (backward)
+    uint8_t* out_q;                    // forward: FP8 E4M3 codes [M, N]
+    void* out_scale;                   // forward: [M, groups] fp32 or E8M0 bytes
+    float* dgamma;                     // backward: partial sums [grid, N], or nullptr
+    DevStatus* status;
+    int64_t M;
+    int R;
+    int N;
+    int nsrc;           // sources in use
+    int has_res;        // the last source (residual, d_res) is there
+    int groups;         // forward: scales a row
+    int group_packs;    // forward: 8-column packs a group (4, 8, 16)
+    int gamma_in_smem;
+    int nt;             // consumer threads, a multiple of 32 (set by rows_plan)
+    int slices;         // slices of nt packs a row (set by rows_plan)
+    int stages;         // ring stages (set by rows_plan)
+    int stage_bytes;    // (set by rows_plan)
+    float eps;
+    float inv_n;
+    uint64_t timeout_ns;
+};
+
+struct RowsPlan {
+    int ppt;      // packs of a row a thread owns at most (template variant)
+    int threads;  // nt + the producer warp
+    int grid;
+    size_t smem;
+};
+
+// Fills p's plan fields from p.N, p.M, p.nsrc and p.gamma_in_smem.
+RowsPlan rows_plan(RowsParams& p, int num_sms);
+cudaError_t rows_prepare();
+cudaError_t launch_norm_quant_rows(const RowsParams& p, const RowsPlan& plan, bool pow2, cudaStream_t stream);
+// scratch: norm_backward_scratch_words() floats; dgamma may be nullptr.
+cudaError_t launch_norm_backward_rows(RowsParams& p, const RowsPlan& plan, float* scratch, float* dgamma,
+                                      cudaStream_t stream);
+size_t norm_backward_scratch_words(int64_t n_max, int num_sms);
+
+// ------------------------------------------------------------------ 4-bit weights, few tokens
+struct QweightParams {
+    const void* x[kMaxRanks];            // bf16 [M, K], or FP8 E4M3 codes [M, K]
+    const void* xscale[kMaxRanks];       // fp32 or E8M0 [M, xgroups] (8-bit tokens)
+    const uint8_t* codes[kMaxRanks];     // [N, K/2], the lower four bits first
+    const uint16_t* scale[kMaxRanks];    // bf16 [N, groups]
+    const uint8_t* zero[kMaxRanks];      // [N, groups] or nullptr (8)
+    uint16_t* views[kMaxRanks];          // distinct outputs, bf16 [M, N]
+    int R, nviews;
+    int M, N, K;
+    int group_shift, groups;             // log2 of the weight group, groups a row
+    int xgroup_shift, xgroups;
+    int xpow2;
+    int splits;                          // K splits of a rank; cluster = R * splits
+    int split_k;                         // K range of a split
+    int tile_k;                          // K range of a shared-memory tile
+    int tiles_m;
+    uint32_t smem;
+};
+
+cudaError_t qweight_prepare();
+// Chooses the launch shape and launches; `variant` and `grid` report it.
+cudaError_t launch_qweight(QweightParams& p, bool qx, int num_sms, int* grid, int* variant, int* cluster, cudaStream_t s);
+
 // ------------------------------------------------------------------ GEMM + reduce
 constexpr int kBM = 128;
 constexpr int kBN = 256;

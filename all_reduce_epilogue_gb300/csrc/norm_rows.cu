@@ -1,0 +1,527 @@
+// Row-streaming kernels around the residual add and RMSNorm after an
+// all-reduce: the group-quantised forward (FP8 E4M3 codes with one scale per
+// group of columns) and the backward pass.
+//
+// Forward, per row i (partials x_r, residual e, width N):
+//   h = sum_{r=0..R-1} x_r + e          (fp32, r ascending; the sum starts at
+//                                        +0.0, so an all -0.0 sum is +0.0)
+//   y = h * rsqrt(mean(h^2) + eps) * gamma
+//   per group of G columns: a = max|y|,  scale = a / 448 or a power of two,
+//   code = e4m3(y * (1 / scale))
+// Backward (dy = sum_r dy_r the all-reduced output gradient, d_res the
+// gradient of the updated residual, inv = rsqrt(mean(h^2) + eps)):
+//   dh      = inv * dy * gamma - h * inv^3 * mean(dy * gamma * h) + d_res
+//   dgamma  = sum_i dy_i * h_i * inv_i
+//
+// Both are bound by HBM: every input byte is read once, every output written
+// once, and one row's sums decide nothing about another's.  A block owns whole
+// rows (row = block, block + grid, ...).  One producer warp streams the row's
+// sources (R partials, residual / h, gradient of the residual) with 1D bulk
+// copies into a ring of stages, stage (row, k) holding the k-th slice of
+// blockDim-32 packs of 8 columns of every source; consumer thread t owns pack
+// t of every slice, so a row lives in registers between the two passes over
+// it (statistics, then outputs) and the ring already fills with the next row
+// meanwhile.  A thread owns the same columns in every row, which lets the
+// backward pass keep its dgamma sums in registers until the block ends.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "are_internal.h"
+#include "ptx.cuh"
+
+namespace are {
+namespace {
+
+constexpr int kMaxStages = 16;
+constexpr size_t kRowsSmemLimit = 227 * 1024;   // one block per SM
+constexpr size_t kRowsSmemPair = 113 * 1024;    // two blocks per SM
+constexpr int kRedWords = 2 * 2 * 32;           // [buffer][statistic][warp]
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    f[4] = __uint_as_float(v.z << 16); f[5] = __uint_as_float(v.z & 0xFFFF0000u);
+    f[6] = __uint_as_float(v.w << 16); f[7] = __uint_as_float(v.w & 0xFFFF0000u);
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+struct Ring {
+    uint8_t* stage;
+    uint64_t* full;
+    uint64_t* empty;
+    float* red;
+    float* gamma;               // N fp32 (backward)
+    volatile uint32_t* abort;
+};
+
+__device__ __forceinline__ Ring carve(uint8_t* base, const RowsParams& p) {
+    Ring g;
+    g.stage = base;
+    g.gamma = reinterpret_cast<float*>(base + (size_t)p.stages * p.stage_bytes);
+    g.red = g.gamma + (p.gamma_in_smem ? p.N : 0);
+    g.full = reinterpret_cast<uint64_t*>(g.red + kRedWords);
+    g.empty = g.full + kMaxStages;
+    g.abort = reinterpret_cast<volatile uint32_t*>(g.empty + kMaxStages);
+    return g;
+}
+
+// Bounded wait on a barrier phase; after a timeout every wait of the block
+// returns at once, and the block runs to its end without waiting.
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, const Ring& g, const RowsParams& p) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (*g.abort) return false;
+        if (ptx::globaltimer() - t0 > p.timeout_ns) {
+            record_error(p.status, ARE_DEV_PIPE_TIMEOUT, blockIdx.x, -5, -1);
+            *g.abort = 1u;
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void consumer_bar(int nt) {
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"r"(nt) : "memory");
+}
+
+__device__ __forceinline__ void ring_init(const Ring& g, const RowsParams& p) {
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            ptx::mbar_init(&g.full[s], 1);
+            ptx::mbar_init(&g.empty[s], p.nt / 32);
+        }
+        *g.abort = 0u;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_shared();
+    }
+    for (int i = threadIdx.x; i < kRedWords; i += blockDim.x) g.red[i] = 0.f;
+    __syncthreads();
+}
+
+// The producer warp: lane i copies source i's slice.
+__device__ __forceinline__ void produce(const Ring& g, const RowsParams& p) {
+    const int lane = threadIdx.x & 31;
+    const uint64_t pol = ptx::policy_evict_first();
+    const uint16_t* src = lane < p.nsrc ? p.src[lane] : nullptr;
+    int s = 0;
+    uint32_t ph = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t row = blockIdx.x; row < p.M && ok; row += gridDim.x) {
+        for (int k = 0; k < p.slices; ++k) {
+            ok = ring_wait(&g.empty[s], ph ^ 1u, g, p);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            const int c0 = k * p.nt * 8;
+            const uint32_t bytes = (uint32_t)min(p.nt * 8, p.N - c0) * 2u;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&g.full[s], bytes * (uint32_t)p.nsrc);
+            __syncwarp();
+            if (src)
+                ptx::bulk_load_hint(g.stage + (size_t)s * p.stage_bytes + (size_t)lane * p.nt * 16,
+                                    src + row * (int64_t)p.N + c0, bytes, &g.full[s], pol);
+            ++issued;
+            if (++s == p.stages) { s = 0; ph ^= 1u; }
+        }
+    }
+    // the block must not end before its copies have landed (they have, unless a wait ran out)
+    if (lane == 0 && !ok) {
+        const int n = issued < p.stages ? (int)issued : p.stages;
+        for (int i = 1; i <= n; ++i) {
+            const int64_t j = issued - i;
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(&g.full[j % p.stages], (uint32_t)(j / p.stages) & 1u))
+                if (ptx::globaltimer() - t0 > p.timeout_ns) break;
+        }
+    }
+}
+
+// Sum of the R partials of this thread's pack, r ascending from +0.0.
+__device__ __forceinline__ void sum_ranks(const uint8_t* at, int R, size_t step, float (&f)[8]) {
+    unpack8(*reinterpret_cast<const uint4*>(at), f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 0.f + f[i];
+#pragma unroll
+    for (int r = 1; r < kMaxRanks; ++r) {
+        if (r < R) {
+            float v[8];
+            unpack8(*reinterpret_cast<const uint4*>(at + r * step), v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] += v[i];
+        }
+    }
+}
+
+// Sum over the consumer threads of one statistic, the same bits in every
+// thread.  `red` holds one word per warp, zero behind the last one.
+__device__ __forceinline__ float red_total(const float* red, int nwarps) {
+    float t = 0.f;
+    for (int w = 0; w < nwarps; w += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(red + w);
+        t += (v.x + v.y) + (v.z + v.w);
+    }
+    return t;
+}
+
+// ------------------------------------------------------------ quantised forward
+// Scale of a group whose largest |y| has the bit pattern `a` (finite), and the
+// factor that takes y to code range.
+struct GroupScale {
+    float inv;
+    uint32_t stored;  // fp32 bits, or the E8M0 byte
+};
+
+template <bool POW2>
+__device__ __forceinline__ GroupScale group_scale(uint32_t a) {
+    GroupScale s;
+    if (POW2) {
+        // the smallest power of two X with a / X <= 448 = 1.75 * 2^8, as a biased exponent >= 0
+        int e = (int)(a >> 23) - 8 + ((a & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+        e = a == 0 ? 127 : max(e, 0);
+        s.stored = (uint32_t)e;
+        s.inv = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e), e <= 247
+    } else {
+        // at least 2^-126, so that its reciprocal is finite
+        const float sc = a == 0 ? 1.f : fmaxf(__fdiv_rn(__uint_as_float(a), 448.f), 1.17549435e-38f);
+        s.stored = __float_as_uint(sc);
+        s.inv = __frcp_rn(sc);
+    }
+    return s;
+}
+
+template <int PPT, bool POW2, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS)
+    norm_quant_rows_kernel(const __grid_constant__ RowsParams p) {
+    extern __shared__ __align__(128) uint8_t rows_smem[];
+    const Ring g = carve(rows_smem, p);
+    ring_init(g, p);
+    if (threadIdx.x >= p.nt) {
+        produce(g, p);
+        return;
+    }
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5, nwarps = p.nt >> 5;
+    const int P = p.N >> 3;
+    const size_t step = (size_t)p.nt * 16;
+    constexpr bool kGammaRegs = PPT <= 4;
+    float gam[kGammaRegs ? PPT : 1][8];
+    if (kGammaRegs) {
+#pragma unroll
+        for (int k = 0; k < PPT; ++k) {
+            const int pk = t + k * p.nt;
+            if (pk < P) {
+                *reinterpret_cast<float4*>(&gam[k][0]) = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2);
+                *reinterpret_cast<float4*>(&gam[k][4]) = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2 + 1);
+            }
+        }
+    }
+    int s = 0, buf = 0;
+    uint32_t ph = 0;
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, buf ^= 1) {
+        float h[PPT][8];
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < PPT; ++k) {
+            if (k < p.slices) {
+                const int pk = t + k * p.nt;
+                ring_wait(&g.full[s], ph, g, p);
+                const uint8_t* at = g.stage + (size_t)s * p.stage_bytes + t * 16;
+                if (pk < P) {
+                    sum_ranks(at, p.R, step, h[k]);
+                    if (p.has_res) {
+                        float e[8];
+                        unpack8(*reinterpret_cast<const uint4*>(at + p.R * step), e);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) h[k][i] += e[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ss = fmaf(h[k][i], h[k][i], ss);
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&g.empty[s]);
+                if (++s == p.stages) { s = 0; ph ^= 1u; }
+                if (p.res_out && pk < P) ptx::st_stream_v4(p.res_out + row * (int64_t)p.N + pk * 8, pack8(h[k]));
+            }
+        }
+        // one barrier a row: the next row's partial sums go to the other buffer
+        float* red = g.red + buf * 64;
+        ss = warp_sum(ss);
+        if (lane == 0) red[w] = ss;
+        consumer_bar(p.nt);
+        const float inv = rsqrtf(red_total(red, nwarps) * p.inv_n + p.eps);
+#pragma unroll
+        for (int k = 0; k < PPT; ++k) {
+            if (k < p.slices) {
+                const int pk = t + k * p.nt;
+                const bool in = pk < P;
+                float gk[8];
+                if (kGammaRegs) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) gk[i] = gam[kGammaRegs ? k : 0][i];
+                } else if (in) {
+                    *reinterpret_cast<float4*>(&gk[0]) = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2);
+                    *reinterpret_cast<float4*>(&gk[4]) = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2 + 1);
+                }
+                // largest |y| as a bit pattern: infinities and NaN sort above every finite value
+                uint32_t a = 0;
+                if (in) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        h[k][i] = h[k][i] * inv * gk[i];
+                        a = max(a, __float_as_uint(h[k][i]) & 0x7FFFFFFFu);
+                    }
+                }
+                // a group is 4, 8 or 16 neighbouring lanes (p.nt is a multiple of 32)
+                for (int o = 1; o < p.group_packs; o <<= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+                if (in) {
+                    uint2 q;
+                    uint32_t stored;
+                    if (a < 0x7F800000u) {
+                        const GroupScale gs = group_scale<POW2>(a);
+                        stored = gs.stored;
+                        uint32_t c[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(
+                                make_float2(h[k][2 * i] * gs.inv, h[k][2 * i + 1] * gs.inv), __NV_SATFINITE, __NV_E4M3);
+                        q = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+                    } else {  // not finite: NaN codes under a NaN scale
+                        stored = POW2 ? 0xFFu : 0x7FC00000u;
+                        q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                    }
+                    ptx::st_stream_v2(p.out_q + row * (int64_t)p.N + pk * 8, q);
+                    if ((lane & (p.group_packs - 1)) == 0) {
+                        const int64_t at = row * (int64_t)p.groups + pk / p.group_packs;
+                        if (POW2) static_cast<uint8_t*>(p.out_scale)[at] = (uint8_t)stored;
+                        else static_cast<uint32_t*>(p.out_scale)[at] = stored;
+                    }
+                }
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------------------- backward
+template <int PPT, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(const __grid_constant__ RowsParams p) {
+    extern __shared__ __align__(128) uint8_t rows_smem[];
+    const Ring g = carve(rows_smem, p);
+    ring_init(g, p);
+    if (threadIdx.x >= p.nt) {
+        produce(g, p);
+        return;
+    }
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5, nwarps = p.nt >> 5;
+    const int P = p.N >> 3;
+    const size_t step = (size_t)p.nt * 16;
+    // a thread reads only the gamma words that it writes here: no barrier
+#pragma unroll
+    for (int k = 0; k < PPT; ++k) {
+        const int pk = t + k * p.nt;
+        if (pk < P) {
+            reinterpret_cast<float4*>(g.gamma)[pk * 2] = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2);
+            reinterpret_cast<float4*>(g.gamma)[pk * 2 + 1] = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2 + 1);
+        }
+    }
+    float dg[PPT][8];
+#pragma unroll
+    for (int k = 0; k < PPT; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dg[k][i] = 0.f;
+    int s = 0, buf = 0;
+    uint32_t ph = 0;
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, buf ^= 1) {
+        float dy[PPT][8];
+        uint4 hv[PPT], ev[PPT];
+        float c1 = 0.f, c2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < PPT; ++k) {
+            if (k < p.slices) {
+                const int pk = t + k * p.nt;
+                ring_wait(&g.full[s], ph, g, p);
+                const uint8_t* at = g.stage + (size_t)s * p.stage_bytes + t * 16;
+                if (pk < P) {
+                    sum_ranks(at, p.R, step, dy[k]);
+                    hv[k] = *reinterpret_cast<const uint4*>(at + p.R * step);
+                    if (p.has_res) ev[k] = *reinterpret_cast<const uint4*>(at + (p.R + 1) * step);
+                    float h[8], gk[8];
+                    unpack8(hv[k], h);
+                    *reinterpret_cast<float4*>(&gk[0]) = reinterpret_cast<const float4*>(g.gamma)[pk * 2];
+                    *reinterpret_cast<float4*>(&gk[4]) = reinterpret_cast<const float4*>(g.gamma)[pk * 2 + 1];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        c1 = fmaf(h[i], h[i], c1);
+                        c2 = fmaf(dy[k][i] * gk[i], h[i], c2);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&g.empty[s]);
+                if (++s == p.stages) { s = 0; ph ^= 1u; }
+            }
+        }
+        float* red = g.red + buf * 64;
+        c1 = warp_sum(c1);
+        c2 = warp_sum(c2);
+        if (lane == 0) {
+            red[w] = c1;
+            red[32 + w] = c2;
+        }
+        consumer_bar(p.nt);
+        const float inv = rsqrtf(red_total(red, nwarps) * p.inv_n + p.eps);
+        const float m = inv * (red_total(red + 32, nwarps) * p.inv_n) * inv;  // inv^2 * mean(dy gamma h)
+#pragma unroll
+        for (int k = 0; k < PPT; ++k) {
+            if (k < p.slices) {
+                const int pk = t + k * p.nt;
+                if (pk < P) {
+                    float h[8], gk[8], e[8], o[8];
+                    unpack8(hv[k], h);
+                    *reinterpret_cast<float4*>(&gk[0]) = reinterpret_cast<const float4*>(g.gamma)[pk * 2];
+                    *reinterpret_cast<float4*>(&gk[4]) = reinterpret_cast<const float4*>(g.gamma)[pk * 2 + 1];
+                    if (p.has_res) unpack8(ev[k], e);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float v = inv * fmaf(-h[i], m, dy[k][i] * gk[i]);
+                        o[i] = p.has_res ? v + e[i] : v;
+                        dg[k][i] = fmaf(dy[k][i], h[i] * inv, dg[k][i]);
+                    }
+                    ptx::st_stream_v4(p.res_out + row * (int64_t)p.N + pk * 8, pack8(o));
+                }
+            }
+        }
+    }
+    if (p.dgamma) {
+        float* to = p.dgamma + (size_t)blockIdx.x * p.N;
+#pragma unroll
+        for (int k = 0; k < PPT; ++k) {
+            const int pk = t + k * p.nt;
+            if (pk < P) {
+                *reinterpret_cast<float4*>(to + pk * 8) = *reinterpret_cast<const float4*>(&dg[k][0]);
+                *reinterpret_cast<float4*>(to + pk * 8 + 4) = *reinterpret_cast<const float4*>(&dg[k][4]);
+            }
+        }
+    }
+}
+
+// dgamma[j] = sum over the blocks' partial rows, in an order that the number
+// of rows alone decides: 32 strands of every 32nd row, then the strands in turn.
+__global__ void __launch_bounds__(256) dgamma_sum_kernel(const float* part, float* dgamma, int rows, int N) {
+    __shared__ float4 sum[32][9];
+    const int c = threadIdx.x & 7, strand = threadIdx.x >> 3;
+    const int col = (blockIdx.x * 8 + c) * 4;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < N) {
+#pragma unroll 4
+        for (int r = strand; r < rows; r += 32) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(part + (size_t)r * N + col));
+            a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+        }
+    }
+    sum[strand][c] = a;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int cc = threadIdx.x >> 2, j = threadIdx.x & 3;
+        float t = 0.f;
+        for (int r = 0; r < 32; ++r) t += reinterpret_cast<const float*>(&sum[r][cc])[j];
+        const int out = blockIdx.x * 32 + threadIdx.x;
+        if (out < N) dgamma[out] = t;
+    }
+}
+
+// Slices of a row and consumer threads: a thread holds up to 4 packs of 8
+// columns (8 from N = 16384 on), and about 256 threads a block.
+int packs_per_thread(int P) { return P <= 256 ? 1 : P <= 512 ? 2 : P <= 2048 ? 4 : 8; }
+
+template <typename F>
+cudaError_t opt_in(F f) {
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowsSmemLimit);
+}
+
+}  // namespace
+
+RowsPlan rows_plan(RowsParams& p, int num_sms) {
+    RowsPlan plan;
+    const int P = p.N / 8;
+    plan.ppt = packs_per_thread(P);
+    p.nt = ((P + plan.ppt - 1) / plan.ppt + 31) / 32 * 32;
+    p.slices = (P + p.nt - 1) / p.nt;
+    p.stage_bytes = p.nsrc * p.nt * 16;
+    const int blocks = p.nt <= 256 && p.M > num_sms ? 2 : 1;
+    const size_t fixed = (p.gamma_in_smem ? (size_t)p.N * 4 : 0) + kRedWords * 4 + 2 * kMaxStages * 8 + 16;
+    const size_t room = (blocks == 2 ? kRowsSmemPair : kRowsSmemLimit) - fixed;
+    p.stages = (int)(room / p.stage_bytes);
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    plan.smem = fixed + (size_t)p.stages * p.stage_bytes;
+    plan.threads = p.nt + 32;
+    plan.grid = (int)(p.M < (int64_t)blocks * num_sms ? p.M : (int64_t)blocks * num_sms);
+    return plan;
+}
+
+// The kernel of a plan: blocks of up to 288 threads leave room for two on an SM.
+template <bool POW2>
+void (*quant_kernel(int ppt, int threads))(RowsParams) {
+    switch (ppt) {
+        case 1: return norm_quant_rows_kernel<1, POW2, 288, 2>;
+        case 2: return norm_quant_rows_kernel<2, POW2, 288, 2>;
+        case 4: return threads <= 288 ? norm_quant_rows_kernel<4, POW2, 288, 2> : norm_quant_rows_kernel<4, POW2, 544, 1>;
+        default: return norm_quant_rows_kernel<8, POW2, 544, 1>;
+    }
+}
+
+void (*backward_kernel(int ppt, int threads))(RowsParams) {
+    switch (ppt) {
+        case 1: return norm_backward_rows_kernel<1, 288, 2>;
+        case 2: return norm_backward_rows_kernel<2, 288, 2>;
+        default: return threads <= 288 ? norm_backward_rows_kernel<4, 288, 2> : norm_backward_rows_kernel<4, 544, 1>;
+    }
+}
+
+cudaError_t rows_prepare() {
+    cudaError_t e = cudaSuccess;
+    for (int ppt = 1; ppt <= 8; ppt *= 2)
+        for (int threads = 288; threads <= 544; threads += 256) {
+            if (e == cudaSuccess) e = opt_in(quant_kernel<false>(ppt, threads));
+            if (e == cudaSuccess) e = opt_in(quant_kernel<true>(ppt, threads));
+            if (e == cudaSuccess) e = opt_in(backward_kernel(ppt, threads));
+        }
+    return e;
+}
+
+cudaError_t launch_norm_quant_rows(const RowsParams& p, const RowsPlan& plan, bool pow2, cudaStream_t s) {
+    auto* kernel = pow2 ? quant_kernel<true>(plan.ppt, plan.threads) : quant_kernel<false>(plan.ppt, plan.threads);
+    kernel<<<plan.grid, plan.threads, plan.smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_norm_backward_rows(RowsParams& p, const RowsPlan& plan, float* scratch, float* dgamma,
+                                      cudaStream_t s) {
+    // a single block's sums are the result
+    p.dgamma = dgamma == nullptr ? nullptr : plan.grid == 1 ? dgamma : scratch;
+    backward_kernel(plan.ppt, plan.threads)<<<plan.grid, plan.threads, plan.smem, s>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && dgamma != nullptr && plan.grid > 1) {
+        dgamma_sum_kernel<<<(p.N + 31) / 32, 256, 0, s>>>(scratch, dgamma, plan.grid, p.N);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+size_t norm_backward_scratch_words(int64_t n_max, int num_sms) {
+    return (size_t)(n_max < kBackwardMaxN ? n_max : kBackwardMaxN) * 2 * num_sms;
+}
+
+}  // namespace are

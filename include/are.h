@@ -40,8 +40,10 @@
  *    time: calls on different streams with the same workspace race on the
  *    device, and a call made while another host thread is inside the library
  *    with the same workspace returns ARE_EBUSY.
- *  - are_gemm_rs, are_gemm_ar, are_allreduce_rmsnorm, are_allreduce_add_rmsnorm
- *    and are_allreduce_rmsnorm_quant may be captured into a CUDA graph once
+ *  - are_gemm_rs, are_gemm_ar, are_allreduce_rmsnorm, are_allreduce_add_rmsnorm,
+ *    are_allreduce_rmsnorm_quant, are_allreduce_rmsnorm_quant_groups,
+ *    are_allreduce_rmsnorm_backward, are_gemm_ar_qweight and
+ *    are_gemm_ar_qweight_qx may be captured into a CUDA graph once
  *    their workspace exists: they only enqueue work on `stream` (kernels;
  *    memsets for an empty contraction), and the state they leave for the next call
  *    (tile masks at 0, staging words at -0.0) is restored inside those
@@ -97,7 +99,9 @@ typedef enum are_status {
 typedef enum are_op {
     ARE_OP_GEMM_RS = 1,
     ARE_OP_GEMM_AR = 2,
-    ARE_OP_ALLREDUCE_RMSNORM = 3
+    ARE_OP_ALLREDUCE_RMSNORM = 3,
+    ARE_OP_ALLREDUCE_RMSNORM_BACKWARD = 4,
+    ARE_OP_GEMM_AR_QWEIGHT = 5
 } are_op;
 
 /* Workspace capacities.  Buffers are sized from these once, at creation, so
@@ -176,7 +180,10 @@ typedef enum are_kernel {
     ARE_KERNEL_GEMM_ONE_CTA = 2,  /* GEMM + reduce, one CTA per 128x256 tile */
     ARE_KERNEL_GEMM_PAIR = 3,     /* GEMM + reduce, CTA pairs (cta_group::2) per 256x256 block */
     ARE_KERNEL_AR_LAMPORT = 4,    /* AR+RMSNorm, two phases meeting through -0.0-armed staging words */
-    ARE_KERNEL_AR_ONESHOT = 5     /* AR+RMSNorm, one-shot (no staging) */
+    ARE_KERNEL_AR_ONESHOT = 5,    /* AR+RMSNorm, one-shot (no staging) */
+    ARE_KERNEL_NORM_QUANT_ROWS = 6,    /* AR+RMSNorm with scales per group of columns */
+    ARE_KERNEL_NORM_BACKWARD_ROWS = 7, /* AR+RMSNorm backward */
+    ARE_KERNEL_QWEIGHT = 8             /* 4-bit weights, few tokens */
 } are_kernel;
 
 typedef struct are_launch_info {
@@ -211,7 +218,10 @@ ARE_API const char* are_status_string(are_status s);
  *           start on 8-row boundaries).
  *  GEMM_AR: 1 <= R <= 8; K % 8 == 0; N % 8 == 0.
  *  ALLREDUCE_RMSNORM: 1 <= R <= 8; N % 8 == 0 (16-byte packs); N <= 32768.
- * K is ignored for ALLREDUCE_RMSNORM.  Pure host function: no device needed. */
+ *  ALLREDUCE_RMSNORM_BACKWARD: as ALLREDUCE_RMSNORM, with N <= 16384.
+ *  GEMM_AR_QWEIGHT: 1 <= R <= 8; K % 32 == 0 (16-byte rows of codes); N % 8 == 0;
+ *           ceil(M / 8) * ceil(N / 16) < 2^28.
+ * K is ignored for the two ALLREDUCE_RMSNORM operations.  Pure host function: no device needed. */
 ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
 
 /* Create a workspace on the current CUDA device: tile masks, the per-rank
@@ -439,6 +449,108 @@ ARE_API are_status are_allreduce_rmsnorm_quant(const are_bf16* const partials[],
                                                const float* gamma, float eps, uint8_t* out_q, float* out_scale,
                                                are_bf16* residual_out, int R, int64_t M, int64_t N, are_ws* ws,
                                                void* stream);
+
+/* How a scale tensor is stored. */
+typedef enum are_scale_format {
+    ARE_SCALE_F32 = 0,  /* fp32 */
+    ARE_SCALE_E8M0 = 1  /* one byte b, the power of two 2^(b - 127); 255 is NaN (OCP MX, E8M0) */
+} are_scale_format;
+
+/*
+ * All-reduce + residual add + RMSNorm with FP8 codes and one scale per group of
+ * columns, the form that block-scaled 8-bit products read (the pages list
+ * quantising variants of the fused kernel without defining one: ROCm/aiter PR
+ * #4977, "Known gaps / follow-ups").
+ *  partials, residual, gamma, eps, residual_out: as are_allreduce_add_rmsnorm;
+ *                 residual_out receives the same bits (in place allowed).
+ *  scale_format : are_scale_format
+ *  group        : 32, 64 or 128 columns; the last group of a row may be shorter
+ *  out_q        : FP8 E4M3 codes [M, N] (OCP e4m3fn)
+ *  out_scale    : [M, ceil(N / group)], fp32 or E8M0 bytes; aligned to its element
+ *  Result       : y as in are_allreduce_rmsnorm (fp32, before its bf16
+ *                 rounding); a = max |y| of the group;
+ *                 ARE_SCALE_F32:  scale = a / 448, correctly rounded, at least 2^-126;
+ *                 ARE_SCALE_E8M0: scale = the smallest power of two, at least
+ *                 2^-127, with a / scale <= 448;
+ *                 1 for a group of zeros;
+ *                 code = e4m3(y * (1 / scale)), the reciprocal and the product
+ *                 rounded to fp32, then to nearest even, saturating to +-448.
+ *                 A group that holds a value that is not finite has a NaN
+ *                 scale and NaN codes.
+ * Needs no capacity of the workspace but R <= R_max.
+ */
+ARE_API are_status are_allreduce_rmsnorm_quant_groups(const are_bf16* const partials[], const are_bf16* residual,
+                                                      const float* gamma, float eps, int scale_format, int group,
+                                                      uint8_t* out_q, void* out_scale, are_bf16* residual_out, int R,
+                                                      int64_t M, int64_t N, are_ws* ws, void* stream);
+
+/*
+ * Backward pass of all-reduce + residual add + RMSNorm.  (The pages have no
+ * training path.)  The normalised output feeds R column-parallel products, so
+ * its gradient arrives as R bf16 partials and is all-reduced first:
+ *  dy[r]   : bf16 [M, N], r < R; dy = sum_{r=0..R-1} f32(dy[r]) in that order
+ *  h       : bf16 [M, N], the updated residual that the forward call returned
+ *            as residual_out; the statistics are recomputed from it
+ *  gamma, eps: as in the forward call
+ *  dres    : bf16 [M, N] or NULL (zero): the gradient of residual_out
+ *  dh      : bf16 [M, N]; may be the same buffer as dres (in place): each row
+ *            of dres is read before that row of dh is written, by the same block.
+ *            It must not alias dy[r] or h.
+ *  dgamma  : fp32 [N] or NULL (gamma is frozen); overwritten
+ *  Result  : inv = rsqrt(mean_j(h_j^2) + eps), per row;
+ *            dh = bf16( inv * dy * gamma - h * inv^3 * mean_j(dy_j gamma_j h_j) + dres ),
+ *            the gradient of every partial and of the incoming residual alike;
+ *            dgamma_j = sum_i dy_ij * h_ij * inv_i, in fp32, in an order that
+ *            depends on M, N and the device's SM count alone.
+ * M == 0 writes dgamma = 0.  Uses a buffer of the workspace for partial sums of
+ * dgamma: N must not exceed N_max (ARE_ECAPACITY), R not R_max.
+ */
+ARE_API are_status are_allreduce_rmsnorm_backward(const are_bf16* const dy[], const are_bf16* h, const float* gamma,
+                                                  float eps, const are_bf16* dres, are_bf16* dh, float* dgamma, int R,
+                                                  int64_t M, int64_t N, are_ws* ws, void* stream);
+
+/* 4-bit weights of one rank, output row by output row: weight (n, k) is
+ * (u - zero[n][k / group]) * scale[n][k / group], u its 4-bit code. */
+typedef struct are_qweight {
+    const uint8_t* codes;  /* [N, K / 2]: byte i of a row holds k = 2i in its lower, 2i + 1 in its upper four bits */
+    const are_bf16* scale; /* bf16 [N, ceil(K / group)], 2-byte aligned */
+    const uint8_t* zero;   /* [N, ceil(K / group)], 0..15, any alignment; NULL = 8 everywhere */
+} are_qweight;
+
+/*
+ * Row-parallel linear of a few tokens with 4-bit weights, all-reduced.
+ * (The pages' fp8 GEMM feeding an all-reduce is the same layer in another
+ * precision: ROCm/mori PR #662, description.)
+ *  x[r]    : bf16 [M, K], r < R
+ *  w[r]    : rank r's weights (a HOST array of R structs of device pointers,
+ *            copied before the call returns)
+ *  group   : 32, 64 or 128 consecutive k; the last group may be shorter
+ *  out[v]  : bf16 [M, N] for every rank view v < R, as in are_gemm_ar (views
+ *            may alias; identical pointers are written once)
+ *  Result  : out[v][m][n] = bf16( sum_r sum_k x[r][m][k] * w_r(n, k) ); the
+ *            codes enter exactly, group sums, scales and the sum over k and
+ *            over r = 0..R-1 are in fp32, and the result is rounded once
+ *            (a rank's partial is not rounded, as in are_gemm_rs).
+ * K == 0 writes zeros.  Any M is computed; it is made for few (up to 64 tokens
+ * read the weights once).  Needs no capacity of the workspace but R <= R_max.
+ */
+ARE_API are_status are_gemm_ar_qweight(const are_bf16* const x[], const are_qweight w[], int group,
+                                       are_bf16* const out[], int R, int64_t M, int64_t N, int64_t K, are_ws* ws,
+                                       void* stream);
+
+/*
+ * The same with tokens in 8 bits, as are_allreduce_rmsnorm_quant_groups writes
+ * them: token (m, k) of rank r is e4m3(xq[r][m][k]) * xscale[r][m][k / xgroup].
+ *  xq[r]       : FP8 E4M3 codes [M, K]
+ *  xscale[r]   : [M, ceil(K / xgroup)], fp32 or E8M0 bytes; aligned to its element
+ *  scale_format: are_scale_format
+ *  xgroup      : 32, 64 or 128, independent of `group`
+ * The other arguments and the arithmetic are as for are_gemm_ar_qweight; the
+ * token scales are applied in fp32 to the group sums.
+ */
+ARE_API are_status are_gemm_ar_qweight_qx(const uint8_t* const xq[], const void* const xscale[], int scale_format,
+                                          int xgroup, const are_qweight w[], int group, are_bf16* const out[], int R,
+                                          int64_t M, int64_t N, int64_t K, are_ws* ws, void* stream);
 
 /*
  * All-reduce + residual + RMSNorm that allocates nothing.

@@ -1,0 +1,212 @@
+"""The few-token linear with 4-bit weights and group scales, summed over R ranks."""
+import pytest
+import torch
+
+import all_reduce_epilogue_gb300 as are
+from tests import ops_ref as ref
+from tests.gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ws():
+    need_gpu()
+    with are.Workspace(R_max=8, M_max=1, N_max=8) as w:
+        yield w
+
+
+def weights(R, N, K, group, zero, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    G = -(-K // group)
+    out = []
+    for _ in range(R):
+        c = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+        s = (torch.rand((N, G), generator=g, device="cuda") * 0.02 + 0.001).to(torch.bfloat16)
+        z = torch.randint(0, 16, (N, G), generator=g, device="cuda", dtype=torch.uint8) if zero else None
+        out.append((c, s, z))
+    return out, g
+
+
+def tokens8(x, xgroup, pow2):
+    xg = ref.grouped(x, xgroup)
+    a = xg.abs().amax(-1)
+    if pow2:
+        s = ref.pow2_byte(a).to(torch.uint8)
+        f = ref.e8m0_value(s)
+    else:
+        s = torch.where(a > 0, a / 448, 1.0).float()
+        f = s.double()
+    q = (xg / f[..., None]).flatten(-2)[..., :x.shape[-1]].float().clamp(-448, 448).to(torch.float8_e4m3fn)
+    val = (ref.grouped(q.double(), xgroup) * f[..., None]).flatten(-2)[..., :x.shape[-1]]
+    return q.contiguous(), s.contiguous(), val
+
+
+def run(ws, x, w, group, xgroup=None, pow2=False, out=None):
+    qw = [are.QWeight(*t, group) for t in w]
+    M, N = x[0].shape[0], qw[0].N
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda") if out is None else out
+    if xgroup is None:
+        are.gemm_ar_qweight(x, qw, out, ws)
+        vals = x
+    else:
+        t = [tokens8(v.float(), xgroup, pow2) for v in x]
+        are.gemm_ar_qweight_qx([v[0] for v in t], [v[1] for v in t], qw, out, ws, xgroup=xgroup)
+        vals = [v[2] for v in t]
+    assert ws.device_status()["code"] == 0
+    return out, vals
+
+
+# one token and one row of groups; ragged N, K and last groups; every token tile; K splits, several K tiles
+SHAPES = [(1, 1, 8, 32), (2, 1, 256, 128), (8, 1, 1032, 2048), (1, 1, 4096, 4096), (3, 5, 136, 160), (4, 8, 520, 544),
+          (5, 9, 264, 1056), (6, 16, 72, 800), (7, 17, 200, 288), (8, 33, 1000, 320), (8, 64, 136, 2080), (1, 64, 4104, 96),
+          (2, 65, 128, 608), (1, 200, 72, 352), (1, 3, 16, 16384), (2, 20, 2048, 4128)]
+
+
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("R,M,N,K", SHAPES)
+def test_against_64_bits(ws, R, M, N, K, zero):
+    for group in (32, 64, 128):
+        w, g = weights(R, N, K, group, zero, R + M + N + K + group)
+        x = [torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(R)]
+        y, _ = run(ws, x, w, group)
+        want, tol = ref.linear64(x, w, group)
+        ref.check(y, want, tol, f"group {group}")
+        assert ws.last_launch()["kernel"] == "qweight_kernel"
+
+
+@pytest.mark.parametrize("xgroup,pow2", [(32, True), (64, False), (128, False), (128, True)])
+@pytest.mark.parametrize("R,M,N,K", SHAPES)
+def test_8_bit_tokens_against_64_bits(ws, R, M, N, K, xgroup, pow2):
+    for group in (32, 128):
+        w, g = weights(R, N, K, group, group == 32, R + M + N + K + group)
+        x = [torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16) * 3 for _ in range(R)]
+        x[0][0] = 0
+        y, vals = run(ws, x, w, group, xgroup, pow2)
+        want, tol = ref.linear64(vals, w, group)
+        ref.check(y, want, tol, f"group {group}")
+
+
+def test_codes_enter_exactly(ws):
+    """Integers in, integers out: one-hot tokens return columns of the weights, bit for bit."""
+    N, K, group = 64, 256, 64
+    w, _ = weights(1, N, K, group, True, 3)
+    w[0][1].fill_(1.0)
+    x = torch.zeros((64, K), dtype=torch.bfloat16, device="cuda")
+    at = torch.randperm(K, device="cuda")[:64]
+    x[torch.arange(64, device="cuda"), at] = 1
+    y, _ = run(ws, [x], w, group)
+    assert torch.equal(y.double(), ref.dequant64(*w[0], group)[:, at].T)
+
+
+def test_outliers_and_extreme_scales(ws):
+    """A token channel 10^4 times the others; group scales of 2^-100 and 2^20; a token of 10^30."""
+    N, K, group = 40, 512, 128
+    w, g = weights(2, N, K, group, True, 4)
+    x = [torch.randn((5, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    x[0][:, 17] *= 1e4
+    x[1][3] *= 1e30
+    w[0][1][:, 1] = 2.0 ** -100
+    w[1][1][5] = 2.0 ** 20
+    y, _ = run(ws, x, w, group)
+    want, tol = ref.linear64(x, w, group)
+    ref.check(y, want, tol, "out")
+
+
+def test_values_that_are_not_finite(ws):
+    """A token's NaN or infinity stays in that token's outputs."""
+    w, g = weights(2, 64, 256, 128, False, 5)
+    w[0][0].fill_(0x99)  # every weight of rank 0: 1 * scale
+    x = [torch.randn((6, 256), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    x[1][2, 100] = float("nan")
+    x[0][4, 3] = float("inf")
+    y, _ = run(ws, x, w, 128)
+    assert y[2].isnan().all() and (y[4] == float("inf")).all()
+    keep = [0, 1, 3, 5]
+    want, tol = ref.linear64([t[keep] for t in x], w, 128)
+    ref.check(y[keep], want, tol, "out")
+
+
+def test_views_guards_stream_and_repeat(ws):
+    R, M, N, K = 4, 3, 136, 320
+    w, g = weights(R, N, K, 64, True, 6)
+    x = [torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(R)]
+    y, _ = run(ws, x, w, 64)
+    big = [torch.full((M + 2, N), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    are.gemm_ar_qweight(x, [are.QWeight(*t, 64) for t in w], [big[v % 2][:M] for v in range(R)], ws, stream=s)
+    torch.cuda.synchronize()
+    for b in big:
+        assert torch.equal(b[:M], y) and (b[M:] == 5).all()
+
+
+def test_graph_replays(ws):
+    R, M, N, K = 8, 2, 1024, 512
+    w, g = weights(R, N, K, 128, True, 7)
+    qw = [are.QWeight(*t, 128) for t in w]
+    x = [torch.zeros((M, K), dtype=torch.bfloat16, device="cuda") for _ in range(R)]
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    are.gemm_ar_qweight(x, qw, out, ws)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        are.gemm_ar_qweight(x, qw, out, ws)
+    for _ in range(3):
+        for t in x:
+            t.normal_(generator=g)
+        gr.replay()
+        torch.cuda.synchronize()
+        want, tol = ref.linear64(x, w, 128)
+        ref.check(out, want, tol, "out")
+
+
+def test_offsets_past_32_bits(ws):
+    """More than 2^32 weights: the last rows."""
+    N, K = (1 << 19) + 8, 8224
+    codes = torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda")
+    scale = torch.ones((N, 257), dtype=torch.bfloat16, device="cuda")
+    w, g = weights(1, 16, K, 32, False, 8)
+    codes[-16:], scale[-16:] = w[0][0], w[0][1]
+    x = torch.randn((2, K), generator=g, device="cuda").to(torch.bfloat16)
+    y, _ = run(ws, [x], [(codes, scale, None)], 32)
+    want, tol = ref.linear64([x], w, 32)
+    ref.check(y[:, -16:], want, tol, "last rows")
+
+
+def test_empty(ws):
+    w, _ = weights(2, 64, 128, 128, True, 9)
+    x = [torch.empty((0, 128), dtype=torch.bfloat16, device="cuda")] * 2
+    assert run(ws, x, w, 128)[0].shape == (0, 64)
+    z = are.QWeight(torch.empty((64, 0), dtype=torch.uint8, device="cuda"),
+                    torch.empty((64, 0), dtype=torch.bfloat16, device="cuda"))
+    out = torch.full((3, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    are.gemm_ar_qweight([torch.empty((3, 0), dtype=torch.bfloat16, device="cuda")], [z], out, ws)
+    assert (out == 0).all() and ws.last_launch()["kernel"] == "memset"
+
+
+def test_refusals(ws):
+    w, g = weights(2, 64, 128, 128, True, 9)
+    qw = [are.QWeight(*t, 128) for t in w]
+    x = [torch.randn((3, 128), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    out = torch.empty((3, 64), dtype=torch.bfloat16, device="cuda")
+    c, s, z = w[0]
+    for a in ((c, s, z, 96), (c, s, z, 64), (c.int(), s, z, 128), (c, s.float(), z, 128), (c, s, z.int(), 128),
+              (c, s, z[:3], 128), (c.t(), s, z, 128)):
+        with pytest.raises(ValueError):
+            are.QWeight(*a)
+    for a in (([], qw, out), (x, qw[:1], out), (x[:1], qw, out), ([t.float() for t in x], qw, out),
+              ([t[:, :96] for t in x], qw, out), (x, qw, out[:2]), (x, qw, out.float()), (x, qw, [out]),
+              ([t.cpu() for t in x], qw, out)):
+        with pytest.raises(ValueError):
+            are.gemm_ar_qweight(*a, ws)
+    odd = are.QWeight(torch.zeros((64, 24), dtype=torch.uint8, device="cuda"),
+                      torch.ones((64, 1), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(are.AreError):  # K = 48
+        are.gemm_ar_qweight([torch.zeros((3, 48), dtype=torch.bfloat16, device="cuda")], [odd], out, ws)
+    xq = [t.to(torch.float8_e4m3fn) for t in x]
+    xs = [torch.ones((3, 1), device="cuda") for _ in x]
+    for a, k in (((xq, xs[:1], qw, out), {}), ((xq, xs, qw, out), dict(xgroup=64)), ((xq, xs, qw, out), dict(xgroup=16)),
+                 ((x, xs, qw, out), {}), ((xq, [xs[0], xs[1].to(torch.uint8)], qw, out), {}),
+                 ((xq, [t.double() for t in xs], qw, out), {})):
+        with pytest.raises(ValueError):
+            are.gemm_ar_qweight_qx(*a, ws, **k)
