@@ -37,6 +37,7 @@ struct are_ws {
     size_t piece_words = 0;
     uint32_t* d_staging = nullptr;
     size_t staging_words = 0;
+    QweightDevice qweight{};          // resident clusters of the 4-bit kernel
     float* d_dgamma = nullptr;        // backward: the blocks' partial dgamma sums
     int ar_resident[kArMaxPpt + 1] = {0};
     uint64_t oneshot_max_bytes = 0;   // set at creation
@@ -483,7 +484,7 @@ are_status are_workspace_create(are_ws** out, const are_caps* caps) {
     }
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_dgamma, norm_backward_scratch_words(caps->N_max, ws->num_sms) * 4);
     if (e == cudaSuccess) e = rows_prepare();
-    if (e == cudaSuccess) e = qweight_prepare();
+    if (e == cudaSuccess) e = qweight_prepare(ws->qweight);
     if (e != cudaSuccess) {
         are_status st = from_cuda(e);
         free_ws(ws);
@@ -810,7 +811,7 @@ are_status qweight_call(const void* const x[], const void* const xscale[], int s
         p.xpow2 = scale_format == ARE_SCALE_E8M0;
     }
     int grid = 0, variant = 0, cluster = 0;
-    const cudaError_t e = launch_qweight(p, qx, ws->num_sms, &grid, &variant, &cluster, s);
+    const cudaError_t e = launch_qweight(p, qx, ws->qweight, &grid, &variant, &cluster, s);
     ws->last = are_launch_info{ARE_KERNEL_QWEIGHT, grid, 256, cluster, 0, variant, 0, 0};
     return from_cuda(e);
 }

@@ -139,14 +139,20 @@ struct QweightParams {
     int xpow2;
     int splits;                          // K splits of a rank; cluster = R * splits
     int split_k;                         // K range of a split
-    int tile_k;                          // K range of a shared-memory tile
+    int tile_k, tiles_k;                 // K range of a shared-memory tile, tiles of a split
     int tiles_m;
-    uint32_t smem;
+    int run;                             // 16-row groups of a cluster
 };
 
-cudaError_t qweight_prepare();
-// Chooses the launch shape and launches; `variant` and `grid` report it.
-cudaError_t launch_qweight(QweightParams& p, bool qx, int num_sms, int* grid, int* variant, int* cluster, cudaStream_t s);
+// What the launch shape depends on: resident clusters by cluster size.
+struct QweightDevice {
+    int clusters[kMaxRanks + 1];
+};
+
+cudaError_t qweight_prepare(QweightDevice& dev);
+// Chooses the launch shape and launches; `grid`, `variant` and `cluster` report it.
+cudaError_t launch_qweight(QweightParams& p, bool qx, const QweightDevice& dev, int* grid, int* variant, int* cluster,
+                           cudaStream_t s);
 
 // ------------------------------------------------------------------ GEMM + reduce
 constexpr int kBM = 128;

@@ -17,10 +17,14 @@
 // 128.0; the tokens are laid into shared memory in the same order of k, so
 // nothing is shuffled.
 //
-// One cluster computes one tile of output rows: its CTAs take the ranks (and
-// splits of K where R is small) and add their fp32 sums over distributed
-// shared memory, r ascending, so no partial sum goes through global memory and
-// the order never varies.
+// A cluster owns a run of 16-row groups; each of its CTAs takes one rank's (or,
+// where R is small, part of a rank's) K range for all of them, so that its
+// tokens go to shared memory once.  The (group, 256 of K) items of a CTA are
+// dealt to its warps in equal contiguous runs.  At the end the CTAs add their
+// fp32 sums over distributed shared memory, r ascending: no partial sum goes
+// through global memory and the order never varies.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -33,12 +37,13 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kItemK = 256;               // codes of a row in one ring slot
-constexpr int kRowBytes = kItemK / 2 + 16;  // 144: 36 words, 8 rows start in 8 different bank quads
+constexpr int kItemK = 256;                 // codes of a row in one ring slot
+constexpr int kRowBytes = kItemK / 2 + 16;  // 144: 36 words, so that 8 rows start in 8 different bank quads
 constexpr int kSlotBytes = 16 * kRowBytes;
-constexpr int kDepth = 4;                 // ring slots of a warp
+constexpr int kDepth = 3;                   // ring slots of a warp, and the length of the unrolled loop
 constexpr int kRingBytes = kWarps * kDepth * kSlotBytes;
-constexpr int kMaxSmem = 227 * 1024;
+constexpr int kRedLd = 20;                  // floats between a sum's tokens: 8 rows of 4 token pairs in 32 banks
+constexpr int kMaxSmem = 113 * 1024;        // two CTAs an SM
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src),
@@ -59,6 +64,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same on a zero accumulator.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
     __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
     return *reinterpret_cast<uint32_t*>(&r);
@@ -67,7 +81,9 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
 // The codes i and i + 4 of a word as the bf16 pair 128 + u, then u - z exactly.
 template <int I>
 __device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t z2) {
-    return sub2(((w >> (4 * I)) & 0x000F000Fu) | 0x43004300u, z2);
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * I)), "r"(0x000F000Fu), "r"(0x43004300u));
+    return sub2(v, z2);
 }
 
 __device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t v) {
@@ -93,61 +109,99 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
     return v;
 }
 
-// TT: token tiles of 8.  QX: tokens in 8 bits with scales.
-template <int TT, bool QX>
-__global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_constant__ QweightParams p, int ks_shift) {
+// TT: token tiles of 8.  QX: tokens in 8 bits with scales.  WSTEPS: steps of
+// 32 k in a weight group; STEPS: those that share both scales, the smaller of
+// the weight and the token group.
+template <int TT, bool QX, int WSTEPS, int STEPS>
+__global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_constant__ QweightParams p) {
     extern __shared__ __align__(128) uint8_t qw_smem[];
     constexpr int TOK = TT * 8;
+    constexpr int NS = 4 / WSTEPS;  // an item has 8 / WSTEPS weight groups x 2 row halves, NS for each of a row's lanes
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
-    const int KS = 1 << ks_shift, BN = (kWarps >> ks_shift) * 16;
-    const int rowgroup = warp >> ks_shift, ks = warp & (KS - 1);
     const int cluster = p.R * p.splits;
     const int q = (int)(blockIdx.x % cluster);
     const int tile = (int)(blockIdx.x / cluster);
-    const int m0 = (tile % p.tiles_m) * TOK, n0 = (tile / p.tiles_m) * BN;
+    const int m0 = (tile % p.tiles_m) * TOK, group0 = (tile / p.tiles_m) * p.run;
+    const int groups = min(p.run, (p.N + 15) / 16 - group0);  // of 16 rows
     const int r = q / p.splits;
     const int kbeg = (q % p.splits) * p.split_k, kend = min(p.K, kbeg + p.split_k);
-    const int len = max(kend - kbeg, 0);
-    const int tiles = (len + p.tile_k - 1) / p.tile_k;
-    const int items = p.tile_k / (kItemK * KS);  // of a warp in a tile
-    const int granule = QX ? min(p.group_shift, p.xgroup_shift) : p.group_shift;
 
     uint8_t* ring = qw_smem + warp * (kDepth * kSlotBytes);
-    uint8_t* xs = qw_smem + kRingBytes;                                    // [tile_k / 32][TOK][4] units of 8 k
-    uint32_t* wsc = reinterpret_cast<uint32_t*>(xs + TOK * p.tile_k * 2);  // [groups of the tile][BN]: scale | 128 + zero
-    float* xsc = reinterpret_cast<float*>(wsc + (p.tile_k >> p.group_shift) * BN);  // [xgroups of the tile][TOK]
+    uint8_t* xs = qw_smem + kRingBytes;                                // [tile_k / 32][TOK][4] units of 8 k
+    float* red = reinterpret_cast<float*>(xs + TOK * p.tile_k * 2);    // [slot][TOK][kRedLd]
+    float* xsc = red + (p.run + kWarps) * TOK * kRedLd;                // [token groups of the tile][TOK]
 
-    // asynchronous copies of this warp's codes, item by item
-    const uint8_t* codes = p.codes[r];
-    const int total = tiles * items;
-    auto fetch = [&](int i) {
-        if (i < total) {
-            const int k0 = kbeg + (i * KS + ks) * kItemK;
-            uint8_t* slot = ring + (i % kDepth) * kSlotBytes;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = j * 4 + (lane >> 3), col = (lane & 7) * 16;
-                const int n = n0 + rowgroup * 16 + row, k = k0 + col * 2;
-                const bool ok = n < p.N && k < kend;
-                cp_async16(slot + row * kRowBytes + col, codes + (ok ? ((int64_t)n * p.K + k) / 2 : 0), ok);
+    // this warp's items of a K tile: [first, first + count), item = group * per + K index
+    const int per = p.tile_k / kItemK, all = groups * per;
+    const int first = warp * all / kWarps, count = (warp + 1) * all / kWarps - first;
+
+    // ---- the stream of items, two ahead of their use: codes by asynchronous copies (16 rows of 128
+    // bytes, 8 lanes a row, 4 rows apart), the weight scales and zero points by loads.  Lane c of a
+    // row quad loads row half c & 1 of the weight groups (c >> 1) + 2j.  N is a multiple of 8: a row
+    // half exists or not for all lanes.
+    const int64_t row4 = (int64_t)p.K * 2;  // bytes of four rows of codes
+    const uint8_t* fcodes = nullptr;
+    int64_t fscale = 0;
+    int ftl = -1, fleft = 0, fkk = 0, fgl = 0, fk = 0;
+    bool ffull = false;
+    uint32_t sreg[kDepth][NS], zreg[kDepth][NS];
+    auto seek = [&]() {  // pointers of group fgl, K index fkk of tile ftl
+        const int n = (group0 + fgl) * 16;
+        fk = kbeg + ftl * p.tile_k + fkk * kItemK;
+        ffull = n + 16 <= p.N;
+        fcodes = p.codes[r] + (((int64_t)(n + (lane >> 3)) * p.K + fk) >> 1) + (lane & 7) * 16;
+        fscale = (int64_t)(n + g + 8 * (c & 1)) * p.groups + (fk >> p.group_shift) + (c >> 1);
+    };
+    auto fetch = [&](uint32_t (&sv)[NS], uint32_t (&zv)[NS], uint8_t* to) {
+        if (fleft == 0) {
+            if (count > 0 && ftl + 1 < p.tiles_k) {
+                ++ftl;
+                fleft = count;
+                fgl = first / per;
+                fkk = first % per;
+                seek();
+            } else {
+                cp_commit();
+                return;
             }
         }
+        const bool kin = fk + (lane & 7) * 32 < kend;
+        const uint8_t* from = kin ? fcodes : p.codes[r];
+        const int64_t step = kin ? row4 : 0;
+        uint8_t* at = to + (lane >> 3) * kRowBytes + (lane & 7) * 16;
+        cp_async16(at, from, kin);
+        cp_async16(at + 4 * kRowBytes, from + step, kin);
+        cp_async16(at + 8 * kRowBytes, ffull ? from + 2 * step : from, kin && ffull);
+        cp_async16(at + 12 * kRowBytes, ffull ? from + 3 * step : from, kin && ffull);
         cp_commit();
+        const bool nin = ffull || (c & 1) == 0;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            sv[j] = 0u;  // what does not exist weighs nothing
+            zv[j] = 8u;
+            if (nin && fk + ((c >> 1) + 2 * j) * (WSTEPS * 32) < kend) {
+                sv[j] = __ldg(p.scale[r] + fscale + 2 * j);
+                if (p.zero[r]) zv[j] = __ldg(p.zero[r] + fscale + 2 * j);
+            }
+        }
+        fk += kItemK;
+        fcodes += kItemK / 2;
+        fscale += 8 / WSTEPS;
+        --fleft;
+        if (++fkk == per) {
+            fkk = 0;
+            ++fgl;
+            seek();
+        }
     };
-#pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) fetch(i);
+    fetch(sreg[0], zreg[0], ring);
+    fetch(sreg[1], zreg[1], ring + kSlotBytes);
 
-    float acc[TT][4];
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
-
-    for (int tl = 0; tl < tiles; ++tl) {
+    // ---- a K tile's tokens, in bf16 and in the order of the weight pairs; token scales
+    auto stage = [&](int tl) {
         const int t0 = kbeg + tl * p.tile_k;
         if (tl) __syncthreads();
-        // the tile's tokens
         for (int u = threadIdx.x; u < TOK * p.tile_k / 8; u += kThreads) {
             const int m = m0 + (u >> 2) % TOK, k = t0 + u / (4 * TOK) * 32 + (u & 3) * 8;
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -165,201 +219,266 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
             }
             *reinterpret_cast<uint4*>(xs + u * 16) = v;
         }
-        // its weight scales and zero points; groups and rows that do not exist weigh nothing
-        const int tg = p.tile_k >> p.group_shift, g0 = t0 >> p.group_shift;
-        for (int u = threadIdx.x; u < tg * BN; u += kThreads) {
-            const int gi = u % tg, n = u / tg;
-            uint32_t v = 0x43080000u;
-            if (n0 + n < p.N && g0 + gi < p.groups) {
-                const int64_t at = (int64_t)(n0 + n) * p.groups + g0 + gi;
-                v = __ldg(p.scale[r] + at);
-                v |= (0x4300u + (p.zero[r] ? (uint32_t)__ldg(p.zero[r] + at) : 8u)) << 16;
-            }
-            wsc[gi * BN + n] = v;
-        }
         if (QX) {
             const int xg = p.tile_k >> p.xgroup_shift, x0 = t0 >> p.xgroup_shift;
             for (int u = threadIdx.x; u < xg * TOK; u += kThreads) {
-                const int gi = u % xg, m = u / xg;
+                const int m = u % TOK, gi = u / TOK;
                 float v = 0.f;
                 if (m0 + m < p.M && x0 + gi < p.xgroups) {
                     const int64_t at = (int64_t)(m0 + m) * p.xgroups + x0 + gi;
                     v = p.xpow2 ? e8m0_to_float(__ldg(static_cast<const uint8_t*>(p.xscale[r]) + at))
                                 : __ldg(static_cast<const float*>(p.xscale[r]) + at);
                 }
-                xsc[gi * TOK + m] = v;
+                xsc[u] = v;
             }
         }
         __syncthreads();
+    };
 
-        for (int it = 0; it < items; ++it) {
-            const int i = tl * items + it;
-            cp_wait<kDepth - 2>();
-            __syncwarp();
-            const int kt = (it * KS + ks) * kItemK;  // within the tile
-            if (t0 + kt < kend) {
-                const uint8_t* slot = ring + (i % kDepth) * kSlotBytes;
-                float d[TT][4];
+    float acc[TT][4];
 #pragma unroll
-                for (int st = 0; st < kItemK / 32; ++st) {
-                    const int k = kt + st * 32;
-                    const int gi = k >> p.group_shift;
-                    if ((st & ((1 << (granule - 5)) - 1)) == 0) {
+    for (int t = 0; t < TT; ++t)
 #pragma unroll
-                        for (int t = 0; t < TT; ++t)
+        for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
+    int tl = -1, left = 0, gl = 0, kk = 0;
+    // One item.  PH: its ring slot and the place of its scales, fixed in the unrolled loop (moving a
+    // register whose load is in flight would wait for it).
+    auto item = [&](auto ph) {
+        constexpr int PH = decltype(ph)::value;
+        constexpr int NEXT = (PH + 2) % kDepth;
+        if (left == 0) {
+            stage(++tl);
+            left = count;
+            gl = first / per;
+            kk = first % per;
+        }
+        cp_wait<kDepth - 2>();
+        __syncwarp();  // every lane's copies have landed, and every lane has left the slot refilled next
+        fetch(sreg[NEXT], zreg[NEXT], ring + NEXT * kSlotBytes);
+        const uint8_t* at = ring + PH * kSlotBytes + g * kRowBytes + c * 4;
+        uint32_t word[NS];  // scale | 128 + zero, as two bf16
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) d[t][j] = 0.f;
-                    }
-                    const uint32_t slo = wsc[gi * BN + rowgroup * 16 + g], shi = wsc[gi * BN + rowgroup * 16 + g + 8];
-                    const uint32_t zlo = __byte_perm(slo, slo, 0x3232), zhi = __byte_perm(shi, shi, 0x3232);
-                    const uint32_t wlo = *reinterpret_cast<const uint32_t*>(slot + g * kRowBytes + (st * 4 + c) * 4);
-                    const uint32_t whi = *reinterpret_cast<const uint32_t*>(slot + (g + 8) * kRowBytes + (st * 4 + c) * 4);
-                    const uint32_t a0[4] = {codes2<0>(wlo, zlo), codes2<0>(whi, zhi), codes2<1>(wlo, zlo), codes2<1>(whi, zhi)};
-                    const uint32_t a1[4] = {codes2<2>(wlo, zlo), codes2<2>(whi, zhi), codes2<3>(wlo, zlo), codes2<3>(whi, zhi)};
+        for (int j = 0; j < NS; ++j) word[j] = sreg[PH][j] | ((0x4300u + zreg[PH][j]) << 16);
+        const int kt = kk * kItemK;
+        if (kbeg + tl * p.tile_k + kt < kend) {
+            const uint8_t* xat = xs + (kt >> 5) * (TOK * 64) + lane * 16;
+            float d[TT][4];
+            uint32_t slo = 0, shi = 0, zlo = 0, zhi = 0;
+#pragma unroll
+            for (int st = 0; st < kItemK / 32; ++st) {
+                if (st % WSTEPS == 0) {
+                    const int gi = st / WSTEPS;  // lane 2 * (gi & 1) + half of the quad has it at j = gi / 2
+                    slo = __shfl_sync(0xFFFFFFFFu, word[gi / 2], (lane & 28) + (gi & 1) * 2);
+                    shi = __shfl_sync(0xFFFFFFFFu, word[gi / 2], (lane & 28) + (gi & 1) * 2 + 1);
+                    zlo = __byte_perm(slo, slo, 0x3232);
+                    zhi = __byte_perm(shi, shi, 0x3232);
+                }
+                const uint32_t wlo = *reinterpret_cast<const uint32_t*>(at + st * 16);
+                const uint32_t whi = *reinterpret_cast<const uint32_t*>(at + 8 * kRowBytes + st * 16);
+                const uint32_t a0[4] = {codes2<0>(wlo, zlo), codes2<0>(whi, zhi), codes2<1>(wlo, zlo), codes2<1>(whi, zhi)};
+                const uint32_t a1[4] = {codes2<2>(wlo, zlo), codes2<2>(whi, zhi), codes2<3>(wlo, zlo), codes2<3>(whi, zhi)};
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    const uint4 b = *reinterpret_cast<const uint4*>(xat + st * (TOK * 64) + t * 512);
+                    if (st % STEPS == 0) mma16816_first(d[t], a0, b.x, b.y);
+                    else mma16816(d[t], a0, b.x, b.y);
+                    mma16816(d[t], a1, b.z, b.w);
+                }
+                if (st % STEPS == STEPS - 1) {
+                    const float fl = __uint_as_float(slo << 16), fh = __uint_as_float(shi << 16);
 #pragma unroll
                     for (int t = 0; t < TT; ++t) {
-                        const uint4 b = *reinterpret_cast<const uint4*>(xs + ((((k >> 5) * TOK + t * 8 + g) << 2) + c) * 16);
-                        mma16816(d[t], a0, b.x, b.y);
-                        mma16816(d[t], a1, b.z, b.w);
-                    }
-                    if (((st + 1) & ((1 << (granule - 5)) - 1)) == 0) {
-                        const float fl = __uint_as_float(slo << 16), fh = __uint_as_float(shi << 16);
-#pragma unroll
-                        for (int t = 0; t < TT; ++t) {
-                            if (QX) {
-                                const float2 x2 = *reinterpret_cast<const float2*>(xsc + (k >> p.xgroup_shift) * TOK + t * 8 + 2 * c);
-                                acc[t][0] = fmaf(fl * x2.x, d[t][0], acc[t][0]);
-                                acc[t][1] = fmaf(fl * x2.y, d[t][1], acc[t][1]);
-                                acc[t][2] = fmaf(fh * x2.x, d[t][2], acc[t][2]);
-                                acc[t][3] = fmaf(fh * x2.y, d[t][3], acc[t][3]);
-                            } else {
-                                acc[t][0] = fmaf(fl, d[t][0], acc[t][0]);
-                                acc[t][1] = fmaf(fl, d[t][1], acc[t][1]);
-                                acc[t][2] = fmaf(fh, d[t][2], acc[t][2]);
-                                acc[t][3] = fmaf(fh, d[t][3], acc[t][3]);
-                            }
+                        if (QX) {
+                            const float2 x2 = *reinterpret_cast<const float2*>(
+                                xsc + ((kt + st * 32) >> p.xgroup_shift) * TOK + t * 8 + 2 * c);
+                            acc[t][0] = fmaf(fl * x2.x, d[t][0], acc[t][0]);
+                            acc[t][1] = fmaf(fl * x2.y, d[t][1], acc[t][1]);
+                            acc[t][2] = fmaf(fh * x2.x, d[t][2], acc[t][2]);
+                            acc[t][3] = fmaf(fh * x2.y, d[t][3], acc[t][3]);
+                        } else {
+                            acc[t][0] = fmaf(fl, d[t][0], acc[t][0]);
+                            acc[t][1] = fmaf(fl, d[t][1], acc[t][1]);
+                            acc[t][2] = fmaf(fh, d[t][2], acc[t][2]);
+                            acc[t][3] = fmaf(fh, d[t][3], acc[t][3]);
                         }
                     }
                 }
             }
-            __syncwarp();  // every lane has read the slot that the next copies overwrite
-            fetch(i + kDepth - 1);
         }
+        --left;
+        if (++kk == per || left == 0) {
+            // the warp leaves a group: its sums go to the slot of (group, warp), which no other
+            // warp touches; along a CTA's items either index grows, so group + warp is unique
+            float* to = red + (gl + warp) * TOK * kRedLd + g;
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                float* e = to + (t * 8 + 2 * c) * kRedLd;
+                if (tl == 0) {
+                    e[0] = acc[t][0]; e[kRedLd] = acc[t][1]; e[8] = acc[t][2]; e[kRedLd + 8] = acc[t][3];
+                } else {
+                    e[0] += acc[t][0]; e[kRedLd] += acc[t][1]; e[8] += acc[t][2]; e[kRedLd + 8] += acc[t][3];
+                }
+                acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+            }
+            kk = 0;
+            ++gl;
+        }
+    };
+    if (count == 0) {  // a warp without items helps to stage the tokens
+        for (int i = 0; i < p.tiles_k; ++i) stage(i);
+    } else {
+        const int total = p.tiles_k * count;
+        int i = 0;
+        for (; i + kDepth <= total; i += kDepth) {
+            item(std::integral_constant<int, 0>{});
+            item(std::integral_constant<int, 1>{});
+            item(std::integral_constant<int, 2>{});
+        }
+        if (i < total) item(std::integral_constant<int, 0>{});
+        if (i + 1 < total) item(std::integral_constant<int, 1>{});
     }
     cp_wait<0>();
     __syncthreads();
 
-    // this CTA's sums, [ks][token][row]; a token's rows are padded so that the four tokens a
-    // store touches start in four different bank groups
-    float* red = reinterpret_cast<float*>(qw_smem);
-    const int ld = BN + 4;
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        float* at = red + (size_t)ks * TOK * ld + rowgroup * 16 + g;
-        const int m = t * 8 + 2 * c;
-        at[m * ld] = acc[t][0];
-        at[(m + 1) * ld] = acc[t][1];
-        at[m * ld + 8] = acc[t][2];
-        at[(m + 1) * ld + 8] = acc[t][3];
-    }
-    if (KS > 1) {
-        __syncthreads();
-        for (int u = threadIdx.x; u < TOK * BN; u += kThreads) {
-            const int at = u / BN * ld + u % BN;
-            float v = red[at];
-            for (int j = 1; j < KS; ++j) v += red[j * TOK * ld + at];
-            red[at] = v;
+    // ---- the sums: of a group over the CTA's warps (into the slot of its first warp), then over the
+    // cluster, r ascending.  Item i belongs to warp (8 (i + 1) - 1) / all.
+    const int toks = min(TOK, p.M - m0);
+    auto warp_of = [&](int i) { return (kWarps * (i + 1) - 1) / all; };
+    for (int a = warp; a < groups; a += kWarps) {
+        const int w0 = warp_of(a * per), w1 = warp_of(a * per + per - 1);
+        for (int w = w0 + 1; w <= w1; ++w) {
+            if ((w + 1) * all / kWarps == w * all / kWarps) continue;  // a warp without items
+            for (int m = lane >> 4; m < toks; m += 2)
+                red[((a + w0) * TOK + m) * kRedLd + (lane & 15)] += red[((a + w) * TOK + m) * kRedLd + (lane & 15)];
         }
     }
     __syncwarp();
     ptx::cluster_sync();
-    const int toks = min(TOK, p.M - m0), half = BN / 2;
     const uint32_t base = ptx::smem_u32(red);
-    for (int u = q * kThreads + threadIdx.x; u < toks * half; u += cluster * kThreads) {
-        const int m = u / half, n = (u % half) * 2;
-        if (n0 + n < p.N) {
-            float2 s = make_float2(0.f, 0.f);
-            for (int j = 0; j < cluster; ++j) {
-                const float2 v = ld_cluster_f2(ptx::mapa_shared(base + (uint32_t)(m * ld + n) * 4u, (uint32_t)j));
-                s.x += v.x;
-                s.y += v.y;
+    for (int a = q + cluster * warp; a < groups; a += cluster * kWarps) {
+        const int n = (group0 + a) * 16 + (lane & 7) * 2;
+        const int s0 = a + warp_of(a * per);
+        if (n < p.N) {
+            for (int m = lane >> 3; m < toks; m += 4) {
+                const uint32_t addr = base + (uint32_t)((s0 * TOK + m) * kRedLd + (lane & 7) * 2) * 4u;
+                float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < kMaxRanks; ++j) {
+                    if (j < cluster) {
+                        const float2 v = ld_cluster_f2(ptx::mapa_shared(addr, (uint32_t)j));
+                        s.x += v.x;
+                        s.y += v.y;
+                    }
+                }
+                const __nv_bfloat162 o = __floats2bfloat162_rn(s.x, s.y);
+                for (int v = 0; v < p.nviews; ++v)
+                    *reinterpret_cast<__nv_bfloat162*>(p.views[v] + (int64_t)(m0 + m) * p.N + n) = o;
             }
-            const __nv_bfloat162 o = __floats2bfloat162_rn(s.x, s.y);
-            for (int v = 0; v < p.nviews; ++v)
-                *reinterpret_cast<__nv_bfloat162*>(p.views[v] + (int64_t)(m0 + m) * p.N + n0 + n) = o;
         }
     }
     __syncwarp();
     ptx::cluster_sync();  // no CTA leaves while another reads its sums
 }
 
-typedef void (*Kernel)(QweightParams, int);
+typedef void (*Kernel)(QweightParams);
 
-Kernel kernel_of(int tt, bool qx) {
-    switch (tt) {
-        case 1: return qx ? qweight_kernel<1, true> : qweight_kernel<1, false>;
-        case 2: return qx ? qweight_kernel<2, true> : qweight_kernel<2, false>;
-        case 4: return qx ? qweight_kernel<4, true> : qweight_kernel<4, false>;
-        default: return qx ? qweight_kernel<8, true> : qweight_kernel<8, false>;
-    }
+template <int TT, bool QX, int WSTEPS>
+Kernel kernel_of(int steps) {
+    if constexpr (!QX || WSTEPS == 1) return qweight_kernel<TT, QX, WSTEPS, WSTEPS>;
+    else if constexpr (WSTEPS == 2) return steps == 1 ? qweight_kernel<TT, QX, 2, 1> : qweight_kernel<TT, QX, 2, 2>;
+    else return steps == 1 ? qweight_kernel<TT, QX, 4, 1> : steps == 2 ? qweight_kernel<TT, QX, 4, 2> : qweight_kernel<TT, QX, 4, 4>;
+}
+template <int TT, bool QX>
+Kernel kernel_of(int wsteps, int steps) {
+    return wsteps == 1 ? kernel_of<TT, QX, 1>(steps) : wsteps == 2 ? kernel_of<TT, QX, 2>(steps) : kernel_of<TT, QX, 4>(steps);
+}
+template <int TT>
+Kernel kernel_of(bool qx, int wsteps, int steps) {
+    return qx ? kernel_of<TT, true>(wsteps, steps) : kernel_of<TT, false>(wsteps, steps);
+}
+// The kernel of a token tile and of the groups' sizes in steps of 32; steps <= wsteps.
+Kernel kernel_of(int tt, bool qx, int wsteps, int steps) {
+    return tt == 1 ? kernel_of<1>(qx, wsteps, steps) : tt == 2 ? kernel_of<2>(qx, wsteps, steps) : kernel_of<4>(qx, wsteps, steps);
+}
+
+void cluster_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int cluster, size_t smem) {
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cluster;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
 }
 
 }  // namespace
 
-cudaError_t qweight_prepare() {
+cudaError_t qweight_prepare(QweightDevice& dev) {
     cudaError_t e = cudaSuccess;
-    for (int tt = 1; tt <= 8; tt *= 2)
+    for (int tt = 1; tt <= 4; tt *= 2)
         for (int qx = 0; qx < 2; ++qx)
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(kernel_of(tt, qx != 0), cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+            for (int wsteps = 1; wsteps <= 4; wsteps *= 2)
+                for (int steps = 1; steps <= wsteps; steps *= 2)
+                    if (e == cudaSuccess)
+                        e = cudaFuncSetAttribute(kernel_of(tt, qx != 0, wsteps, steps),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    // clusters of each size that are resident at once, at the largest shared memory a launch takes
+    for (int c = 1; c <= kMaxRanks && e == cudaSuccess; ++c) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr;
+        cluster_config(cfg, attr, c, kMaxSmem);
+        cfg.gridDim = dim3((unsigned)c);
+        e = cudaOccupancyMaxActiveClusters(&dev.clusters[c], kernel_of(4, true, 1, 1), &cfg);
+        if (e == cudaSuccess && dev.clusters[c] < 1) dev.clusters[c] = 1;
+    }
     return e;
 }
 
-cudaError_t launch_qweight(QweightParams& p, bool qx, int num_sms, int* grid, int* variant, int* cluster,
+cudaError_t launch_qweight(QweightParams& p, bool qx, const QweightDevice& dev, int* grid, int* variant, int* cluster,
                            cudaStream_t s) {
-    const int tt = p.M <= 8 ? 1 : p.M <= 16 ? 2 : p.M <= 32 ? 4 : 8;
+    const int tt = p.M <= 8 ? 1 : p.M <= 16 ? 2 : 4;
     const int tok = tt * 8;
     p.tiles_m = (p.M + tok - 1) / tok;
-    // Splits of K: as many as the cluster has room for and 512 of K each.
-    p.splits = 8 / p.R;
-    while (p.splits > 1 && p.K < p.splits * 512) --p.splits;
-    const int range = (p.K + p.splits - 1) / p.splits;
-    // Warps share a row tile's K range (fewer rows a CTA) while there are fewer than two CTAs an SM.
-    int ks = 0;
-    auto ctas = [&](int k) {
-        const int bn = 128 >> k;
-        return (int64_t)((p.N + bn - 1) / bn) * p.tiles_m * p.R * p.splits;
-    };
-    while (ks < 3 && ctas(ks) < 2 * num_sms && (kItemK << (ks + 1)) <= range && tok << ks <= 64) ++ks;
-    const int unit = kItemK << ks;
-    p.split_k = (range + unit - 1) / unit * unit;
-    // tokens of a tile: up to 32 KB
-    p.tile_k = 16384 / tok / unit * unit;
-    if (p.tile_k < unit) p.tile_k = unit;
-    if (p.tile_k > p.split_k) p.tile_k = p.split_k;
-    const int bn = 128 >> ks;
-    size_t smem = kRingBytes + (size_t)tok * p.tile_k * 2 + (size_t)(p.tile_k >> p.group_shift) * bn * 4 +
-                  (qx ? (size_t)(p.tile_k >> p.xgroup_shift) * tok * 4 : 0);
-    const size_t red = (size_t)(tok << ks) * (bn + 4) * 4;
-    if (smem < red) smem = red;
-    p.smem = (uint32_t)smem;
-
+    const int groups = (p.N + 15) / 16;
+    // Splits of a rank's K: those that leave the busiest CTA the fewest items (an item is 16 rows
+    // by 256 of K), where a split also costs about one item more to join.
+    const int items_k = (p.K + kItemK - 1) / kItemK;
+    int64_t best = 0;
+    for (int sp = 1; sp * p.R <= kMaxRanks && sp <= items_k; ++sp) {
+        const int64_t rounds = (int64_t)((groups + dev.clusters[sp * p.R] - 1) / dev.clusters[sp * p.R]) * p.tiles_m;
+        const int64_t cost = rounds * ((items_k + sp - 1) / sp) + sp;
+        if (sp == 1 || cost < best) {
+            best = cost;
+            p.splits = sp;
+        }
+    }
     *cluster = p.R * p.splits;
-    *grid = (int)ctas(ks);
-    *variant = tt * 8 + (1 << ks);
+    p.split_k = (items_k + p.splits - 1) / p.splits * kItemK;
+    // Groups a cluster: an even share for every resident cluster, as far as their sums fit shared memory.
+    const int slot = tok * kRedLd * 4;
+    const int most = 36 * 1024 / slot - kWarps;
+    p.run = (groups + dev.clusters[*cluster] - 1) / dev.clusters[*cluster];
+    if (p.run > most) p.run = most;
+    // K tile: as long as the tokens fit what is left
+    const int xstep = kItemK * tok * 2 + (qx ? (kItemK >> p.xgroup_shift) * tok * 4 : 0);
+    const int room = (kMaxSmem - kRingBytes - (p.run + kWarps) * slot) / xstep;  // items of K
+    const int split_items = p.split_k / kItemK;
+    p.tiles_k = (split_items + room - 1) / room;
+    const int tile_items = (split_items + p.tiles_k - 1) / p.tiles_k;
+    p.tile_k = tile_items * kItemK;
+    const size_t smem = (size_t)kRingBytes + (size_t)(p.run + kWarps) * slot + (size_t)tile_items * xstep;
+
+    const int runs = (groups + p.run - 1) / p.run;
+    *grid = runs * p.tiles_m * *cluster;
+    *variant = tt;
+    const int shift = qx && p.xgroup_shift < p.group_shift ? p.xgroup_shift : p.group_shift;
     cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    cluster_config(cfg, attr, *cluster, smem);
     cfg.gridDim = dim3((unsigned)*grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)*cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel_of(tt, qx), p, ks);
+    return cudaLaunchKernelEx(&cfg, kernel_of(tt, qx, 1 << (p.group_shift - 5), 1 << (shift - 5)), p);
 }
 
 }  // namespace are
