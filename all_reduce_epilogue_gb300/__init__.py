@@ -26,6 +26,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import Optional, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -449,7 +450,9 @@ def noalloc_device_status() -> dict:
 
 
 # Argument checks of the operations below: type, shape, contiguity, and the
-# workspace's device.
+# workspace's device.  The host's time is most of a one-token call's, so ranks
+# are checked attribute by attribute through ``map`` (about half the time of a
+# loop over the tensors).
 def _need(t, dtype, shape, dev: int, what: str):
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {dev}, "
@@ -458,6 +461,33 @@ def _need(t, dtype, shape, dev: int, what: str):
 
 def _need_one_of(t, dtypes, shape, dev: int, what: str):
     _need(t, t.dtype if t.dtype in dtypes else dtypes[0], shape, dev, what)
+
+
+def _need_all(tensors, dtype, shape, dev: int, what: str):
+    T = _tensor_type()
+    n = len(tensors)
+    if (list(map(T.get_device, tensors)) != [dev] * n or not all(map(T.is_contiguous, tensors))
+            or [t.dtype for t in tensors] != [dtype] * n or [t.shape for t in tensors] != [shape] * n):
+        for t in tensors:
+            _need(t, dtype, shape, dev, what)
+
+
+def _tensor_type():
+    import torch
+    return torch.Tensor
+
+
+def _addresses(tensors) -> array:
+    """The tensors' addresses, as the C array of pointers that the ABI takes."""
+    return array("Q", map(_tensor_type().data_ptr, tensors))
+
+
+def _at(a: array) -> int:
+    return a.buffer_info()[0]
+
+
+def _address(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _ranks(tensors, what: str) -> int:
@@ -481,15 +511,21 @@ def _group_of(group: int, what: str) -> int:
 def _on_stream(stream, dev: int) -> int:
     import torch
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev)  # current_stream(dev).cuda_stream without its wrapper
     if stream.device_index != dev:
         raise ValueError(f"the stream is on CUDA device {stream.device_index}, the workspace on {dev}")
     return stream.cuda_stream
 
 
-def _scale_kinds():
-    import torch
-    return {torch.float32: SCALE_F32, torch.uint8: SCALE_E8M0, torch.float8_e8m0fnu: SCALE_E8M0}
+_kinds: dict = {}
+
+
+def _scale_kinds() -> dict:
+    """The scale format of each type that a scale tensor may have."""
+    if not _kinds:
+        import torch
+        _kinds.update({torch.float32: SCALE_F32, torch.uint8: SCALE_E8M0, torch.float8_e8m0fnu: SCALE_E8M0})
+    return _kinds
 
 
 def allreduce_rmsnorm_quant_groups(partials: Sequence, residual, gamma, eps: float, out_q, out_scale, ws: Workspace,
@@ -505,8 +541,7 @@ def allreduce_rmsnorm_quant_groups(partials: Sequence, residual, gamma, eps: flo
     R = _ranks(partials, "partials")
     shape = _matrix(partials[0], "partials")
     M, N = shape
-    for t in partials:
-        _need(t, bf16, shape, dev, "partials")
+    _need_all(partials, bf16, shape, dev, "partials")
     if residual is not None:
         _need(residual, bf16, shape, dev, "residual")
     if residual_out is not None:
@@ -515,10 +550,10 @@ def allreduce_rmsnorm_quant_groups(partials: Sequence, residual, gamma, eps: flo
     _need_one_of(out_q, (torch.uint8, torch.float8_e4m3fn), shape, dev, "out_q")
     kinds = _scale_kinds()
     _need_one_of(out_scale, tuple(kinds), (M, -(-N // _group_of(group, "group"))), dev, "out_scale")
+    parts = _addresses(partials)
     rc = load_library().are_allreduce_rmsnorm_quant_groups(
-        _ptrs(partials), residual.data_ptr() if residual is not None else None, gamma.data_ptr(), eps,
-        kinds[out_scale.dtype], group, out_q.data_ptr(), out_scale.data_ptr(),
-        residual_out.data_ptr() if residual_out is not None else None, R, M, N, ws.handle, _on_stream(stream, dev))
+        _at(parts), _address(residual), gamma.data_ptr(), eps, kinds[out_scale.dtype], group, out_q.data_ptr(),
+        out_scale.data_ptr(), _address(residual_out), R, M, N, ws.handle, _on_stream(stream, dev))
     _check(rc, "are_allreduce_rmsnorm_quant_groups")
 
 
@@ -535,8 +570,7 @@ def allreduce_rmsnorm_backward(dy: Sequence, h, gamma, eps: float, dh, dgamma, w
     R = _ranks(dy, "dy")
     shape = _matrix(dy[0], "dy")
     M, N = shape
-    for t in dy:
-        _need(t, bf16, shape, dev, "dy")
+    _need_all(dy, bf16, shape, dev, "dy")
     _need(h, bf16, shape, dev, "h")
     _need(dh, bf16, shape, dev, "dh")
     if dres is not None:
@@ -544,9 +578,10 @@ def allreduce_rmsnorm_backward(dy: Sequence, h, gamma, eps: float, dh, dgamma, w
     _need(gamma, torch.float32, (N,), dev, "gamma")
     if dgamma is not None:
         _need(dgamma, torch.float32, (N,), dev, "dgamma")
+    parts = _addresses(dy)
     rc = load_library().are_allreduce_rmsnorm_backward(
-        _ptrs(dy), h.data_ptr(), gamma.data_ptr(), eps, dres.data_ptr() if dres is not None else None, dh.data_ptr(),
-        dgamma.data_ptr() if dgamma is not None else None, R, M, N, ws.handle, _on_stream(stream, dev))
+        _at(parts), h.data_ptr(), gamma.data_ptr(), eps, _address(dres), dh.data_ptr(), _address(dgamma), R, M, N,
+        ws.handle, _on_stream(stream, dev))
     _check(rc, "are_allreduce_rmsnorm_backward")
 
 
@@ -559,7 +594,7 @@ class QWeight:
     ``zero``: uint8 of the same shape, values 0..15, or None (8 everywhere);
     ``group``: 32, 64 or 128."""
 
-    __slots__ = ("codes", "scale", "zero", "group", "N", "K")
+    __slots__ = ("codes", "scale", "zero", "group", "N", "K", "_key")
 
     def __init__(self, codes, scale, zero=None, group: int = 128):
         import torch
@@ -572,29 +607,30 @@ class QWeight:
         if zero is not None:
             _need(zero, torch.uint8, groups, dev, "zero")
         self.codes, self.scale, self.zero = codes, scale, zero
+        self._key = (N, self.K, group, dev)
 
 
 def _qweights(w: Sequence, R: int, M: int, K: int, out, dev: int):
-    """The C arrays of the weights and of the output views."""
+    """The C arrays of the weights and of the output views, and the weights' N and group."""
     import torch
     N, group = w[0].N, w[0].group
     if len(w) != R:
         raise ValueError(f"{R} ranks of tokens, {len(w)} of weights")
-    ptrs = []
-    for q in w:
-        if q.N != N or q.K != K or q.group != group or q.codes.get_device() != dev:
-            raise ValueError(f"every rank's weights must be [{N}, {K}] in groups of {group} on CUDA device {dev}")
-        ptrs += (q.codes.data_ptr(), q.scale.data_ptr(), q.zero.data_ptr() if q.zero is not None else None)
+    if [q._key for q in w] != [(N, K, group, dev)] * R:
+        raise ValueError(f"every rank's weights must be [{N}, {K}] in groups of {group} on CUDA device {dev}")
+    if w[0].zero is not None and all([q.zero is not None for q in w]):
+        weights = _addresses([t for q in w for t in (q.codes, q.scale, q.zero)])
+    else:
+        weights = array("Q", [v or 0 for q in w for v in (q.codes.data_ptr(), q.scale.data_ptr(), _address(q.zero))])
     if isinstance(out, (list, tuple)):
         if len(out) != R:
             raise ValueError(f"{R} ranks, {len(out)} output views")
-        for t in out:
-            _need(t, torch.bfloat16, (M, N), dev, "out")
-        views = _ptrs(out)
+        _need_all(out, torch.bfloat16, (M, N), dev, "out")
+        views = _addresses(out)
     else:
         _need(out, torch.bfloat16, (M, N), dev, "out")
-        views = (ctypes.c_void_p * R)(*[out.data_ptr()] * R)
-    return (ctypes.c_void_p * (3 * R))(*ptrs), group, views, N
+        views = array("Q", [out.data_ptr()]) * R
+    return weights, group, views, N
 
 
 def gemm_ar_qweight(x: Sequence, w: Sequence, out, ws: Workspace, stream=None):
@@ -607,10 +643,10 @@ def gemm_ar_qweight(x: Sequence, w: Sequence, out, ws: Workspace, stream=None):
     R = _ranks(x, "x")
     shape = _matrix(x[0], "x")
     M, K = shape
-    for t in x:
-        _need(t, torch.bfloat16, shape, dev, "x")
+    _need_all(x, torch.bfloat16, shape, dev, "x")
     weights, group, views, N = _qweights(w, R, M, K, out, dev)
-    rc = load_library().are_gemm_ar_qweight(_ptrs(x), weights, group, views, R, M, N, K, ws.handle,
+    tokens = _addresses(x)
+    rc = load_library().are_gemm_ar_qweight(_at(tokens), _at(weights), group, _at(views), R, M, N, K, ws.handle,
                                             _on_stream(stream, dev))
     _check(rc, "are_gemm_ar_qweight")
 
@@ -620,7 +656,7 @@ def gemm_ar_qweight_qx(xq: Sequence, xscale: Sequence, w: Sequence, out, ws: Wor
     """As ``gemm_ar_qweight`` with tokens e4m3(xq[r]) * xscale[r], as
     ``allreduce_rmsnorm_quant_groups`` writes them.
 
-    ``xq``: R [M, K] uint8 or float8_e4m3fn tensors; ``xscale``: R tensors
+    ``xq``: R [M, K] tensors, all uint8 or all float8_e4m3fn; ``xscale``: R tensors
     [M, ceil(K / xgroup)], float32 or uint8 / float8_e8m0fnu (all of one
     kind)."""
     import torch
@@ -634,10 +670,11 @@ def gemm_ar_qweight_qx(xq: Sequence, xscale: Sequence, w: Sequence, out, ws: Wor
     sshape, sdt = (M, -(-K // _group_of(xgroup, "xgroup"))), xscale[0].dtype
     if sdt not in kinds:
         raise ValueError(f"xscale must be float32, uint8 or float8_e8m0fnu, got {sdt}")
-    for t, f in zip(xq, xscale):
-        _need_one_of(t, (torch.uint8, torch.float8_e4m3fn), shape, dev, "xq")
-        _need(f, sdt, sshape, dev, "xscale")
+    codes = xq[0].dtype
+    _need_all(xq, codes if codes is torch.float8_e4m3fn else torch.uint8, shape, dev, "xq")
+    _need_all(xscale, sdt, sshape, dev, "xscale")
     weights, group, views, N = _qweights(w, R, M, K, out, dev)
-    rc = load_library().are_gemm_ar_qweight_qx(_ptrs(xq), _ptrs(xscale), kinds[sdt], xgroup, weights, group, views, R,
-                                               M, N, K, ws.handle, _on_stream(stream, dev))
+    tokens, scales = _addresses(xq), _addresses(xscale)
+    rc = load_library().are_gemm_ar_qweight_qx(_at(tokens), _at(scales), kinds[sdt], xgroup, _at(weights), group,
+                                               _at(views), R, M, N, K, ws.handle, _on_stream(stream, dev))
     _check(rc, "are_gemm_ar_qweight_qx")

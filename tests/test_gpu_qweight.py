@@ -210,3 +210,28 @@ def test_refusals(ws):
                  ((xq, [t.double() for t in xs], qw, out), {})):
         with pytest.raises(ValueError):
             are.gemm_ar_qweight_qx(*a, ws, **k)
+
+
+def test_zero_points_of_some_ranks(ws):
+    """Ranks with and without zero points in one call (a CTA may take several ranks)."""
+    for R, N, K in ((8, 72, 320), (8, 4096, 512), (3, 2048, 256)):
+        w, g = weights(R, N, K, 64, True, R + N)
+        w = [(c, s, z if r % 2 else None) for r, (c, s, z) in enumerate(w)]
+        x = [torch.randn((2, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(R)]
+        y, _ = run(ws, x, w, 64)
+        want, tol = ref.linear64(x, w, 64)
+        ref.check(y, want, tol, f"R {R}")
+
+
+def test_tokens_of_any_magnitude(ws):
+    """Tokens from bf16's smallest to near its largest values, each its own magnitude, and zeros."""
+    w, g = weights(2, 64, 512, 128, True, 12)
+    x = [torch.randn((9, 512), generator=g, device="cuda") for _ in range(2)]
+    for i, e in enumerate((-130, -126, -100, -30, 0, 40, 100, 115)):
+        for t in x:
+            t[i] *= 2.0 ** e
+    x[0][8], x[1][8] = 0, 0
+    x = [t.to(torch.bfloat16) for t in x]
+    y, _ = run(ws, x, w, 128)
+    want, tol = ref.linear64(x, w, 128)
+    ref.check(y, want, tol + 2.0 ** -133, "out")  # bf16's smallest step
