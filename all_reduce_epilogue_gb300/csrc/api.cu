@@ -891,7 +891,7 @@ are_status are_allreduce_rmsnorm_backward(const are_bf16* const dy[], const are_
         p.has_res = 1;
     }
     p.res_out = dh;
-    p.gamma_in_smem = 1;
+    p.backward = 1;
     const RowsPlan plan = rows_plan(p, ws->num_sms);
     ws->last = are_launch_info{ARE_KERNEL_NORM_BACKWARD_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
     return from_cuda(launch_norm_backward_rows(p, plan, ws->d_dgamma, dgamma, s));

@@ -98,7 +98,7 @@ struct RowsParams {
     int has_res;        // the last source (residual, d_res) is there
     int groups;         // forward: scales a row
     int group_packs;    // forward: 8-column packs a group (4, 8, 16)
-    int gamma_in_smem;
+    int backward;       // the backward pass (gamma in shared memory, fewer threads)
     int nt;             // consumer threads, a multiple of 32 (set by rows_plan)
     int slices;         // slices of nt packs a row (set by rows_plan)
     int stages;         // ring stages (set by rows_plan)
@@ -115,7 +115,7 @@ struct RowsPlan {
     size_t smem;
 };
 
-// Fills p's plan fields from p.N, p.M, p.nsrc and p.gamma_in_smem.
+// Fills p's plan fields from p.N, p.M, p.nsrc and p.backward.
 RowsPlan rows_plan(RowsParams& p, int num_sms);
 cudaError_t rows_prepare();
 cudaError_t launch_norm_quant_rows(const RowsParams& p, const RowsPlan& plan, bool pow2, cudaStream_t stream);

@@ -72,7 +72,7 @@ __device__ __forceinline__ Ring carve(uint8_t* base, const RowsParams& p) {
     Ring g;
     g.stage = base;
     g.gamma = reinterpret_cast<float*>(base + (size_t)p.stages * p.stage_bytes);
-    g.red = g.gamma + (p.gamma_in_smem ? p.N : 0);
+    g.red = g.gamma + (p.backward ? p.N : 0);
     g.full = reinterpret_cast<uint64_t*>(g.red + kRedWords);
     g.empty = g.full + kMaxStages;
     g.abort = reinterpret_cast<volatile uint32_t*>(g.empty + kMaxStages);
@@ -151,11 +151,12 @@ __device__ __forceinline__ void produce(const Ring& g, const RowsParams& p) {
     }
 }
 
-// Sum of the R partials of this thread's pack, r ascending from +0.0.
+// Sum of the R partials of this thread's pack, r ascending from +0.0.  ONE: R is
+// 1, the common case of the backward pass, without the code of the other ranks.
+template <bool ONE>
 __device__ __forceinline__ void sum_ranks(const uint8_t* at, int R, size_t step, float (&f)[8]) {
     unpack8(*reinterpret_cast<const uint4*>(at), f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 0.f + f[i];
+    if (ONE) return;
 #pragma unroll
     for (int r = 1; r < kMaxRanks; ++r) {
         if (r < R) {
@@ -241,7 +242,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
                 ring_wait(&g.full[s], ph, g, p);
                 const uint8_t* at = g.stage + (size_t)s * p.stage_bytes + t * 16;
                 if (pk < P) {
-                    sum_ranks(at, p.R, step, h[k]);
+                    sum_ranks<false>(at, p.R, step, h[k]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[k][i] += 0.f;  // a sum of -0.0 counts as +0.0
                     if (p.has_res) {
                         float e[8];
                         unpack8(*reinterpret_cast<const uint4*>(at + p.R * step), e);
@@ -316,11 +319,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
 }
 
 // --------------------------------------------------------------------- backward
-template <int PPT, int THREADS, int BLOCKS>
+template <int PPT, bool ONE, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(const __grid_constant__ RowsParams p) {
     extern __shared__ __align__(128) uint8_t rows_smem[];
     const Ring g = carve(rows_smem, p);
     ring_init(g, p);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // dgamma_sum_kernel may come up; it waits for the grid's end
     if (threadIdx.x >= p.nt) {
         produce(g, p);
         return;
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
                 ring_wait(&g.full[s], ph, g, p);
                 const uint8_t* at = g.stage + (size_t)s * p.stage_bytes + t * 16;
                 if (pk < P) {
-                    sum_ranks(at, p.R, step, dy[k]);
+                    sum_ranks<ONE>(at, p.R, step, dy[k]);
                     hv[k] = *reinterpret_cast<const uint4*>(at + p.R * step);
                     if (p.has_res) ev[k] = *reinterpret_cast<const uint4*>(at + (p.R + 1) * step);
                     float h[8], gk[8];
@@ -382,22 +386,22 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
         }
         consumer_bar(p.nt);
         const float inv = rsqrtf(red_total(red, nwarps) * p.inv_n + p.eps);
-        const float m = inv * (red_total(red + 32, nwarps) * p.inv_n) * inv;  // inv^2 * mean(dy gamma h)
+        const float m = inv * (red_total(red + 32, nwarps) * p.inv_n) * inv;  // inv^2 * mean(dy gamma h): dh = inv dy gamma - m (h inv) + d_res
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
             if (k < p.slices) {
                 const int pk = t + k * p.nt;
                 if (pk < P) {
-                    float h[8], gk[8], e[8], o[8];
+                    float h[8], gk[8], e[8] = {}, o[8];
                     unpack8(hv[k], h);
                     *reinterpret_cast<float4*>(&gk[0]) = reinterpret_cast<const float4*>(g.gamma)[pk * 2];
                     *reinterpret_cast<float4*>(&gk[4]) = reinterpret_cast<const float4*>(g.gamma)[pk * 2 + 1];
                     if (p.has_res) unpack8(ev[k], e);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float v = inv * fmaf(-h[i], m, dy[k][i] * gk[i]);
-                        o[i] = p.has_res ? v + e[i] : v;
-                        dg[k][i] = fmaf(dy[k][i], h[i] * inv, dg[k][i]);
+                        const float xh = h[i] * inv;
+                        o[i] = fmaf(dy[k][i] * gk[i], inv, fmaf(-xh, m, e[i]));
+                        dg[k][i] = fmaf(dy[k][i], xh, dg[k][i]);
                     }
                     ptx::st_stream_v4(p.res_out + row * (int64_t)p.N + pk * 8, pack8(o));
                 }
@@ -417,34 +421,52 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
     }
 }
 
-// dgamma[j] = sum over the blocks' partial rows, in an order that the number
-// of rows alone decides: 32 strands of every 32nd row, then the strands in turn.
+// dgamma[j] = sum over the blocks' partial rows, in an order that the number of
+// rows alone decides: 64 strands of every 64th row, halved six times.  It is
+// launched while the row kernel runs (programmatic dependent launch) and waits
+// for it here, which hides its launch.
 __global__ void __launch_bounds__(256) dgamma_sum_kernel(const float* part, float* dgamma, int rows, int N) {
-    __shared__ float4 sum[32][9];
-    const int c = threadIdx.x & 7, strand = threadIdx.x >> 3;
-    const int col = (blockIdx.x * 8 + c) * 4;
+    __shared__ float4 sum[8][4];
+    const int c = threadIdx.x & 3, strand = threadIdx.x >> 2;
+    const int col = (blockIdx.x * 4 + c) * 4;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col < N) {
-#pragma unroll 4
-        for (int r = strand; r < rows; r += 32) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(part + (size_t)r * N + col));
-            a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+        float4 v[5];
+        for (int r0 = strand; r0 < rows; r0 += 5 * 64) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+                v[i] = r0 + i * 64 < rows ? __ldcg(reinterpret_cast<const float4*>(part + (size_t)(r0 + i * 64) * N + col))
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                a.x += v[i].x; a.y += v[i].y; a.z += v[i].z; a.w += v[i].w;
+            }
         }
     }
-    sum[strand][c] = a;
+    for (int o = 4; o < 32; o <<= 1) {  // the 8 strands of a warp
+        a.x += __shfl_xor_sync(0xFFFFFFFFu, a.x, o);
+        a.y += __shfl_xor_sync(0xFFFFFFFFu, a.y, o);
+        a.z += __shfl_xor_sync(0xFFFFFFFFu, a.z, o);
+        a.w += __shfl_xor_sync(0xFFFFFFFFu, a.w, o);
+    }
+    if ((threadIdx.x & 31) < 4) sum[threadIdx.x >> 5][c] = a;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        const int cc = threadIdx.x >> 2, j = threadIdx.x & 3;
+    if (threadIdx.x < 16) {
+        const int out = blockIdx.x * 16 + threadIdx.x;
         float t = 0.f;
-        for (int r = 0; r < 32; ++r) t += reinterpret_cast<const float*>(&sum[r][cc])[j];
-        const int out = blockIdx.x * 32 + threadIdx.x;
+        for (int w = 0; w < 8; ++w) t += reinterpret_cast<const float*>(sum[w])[threadIdx.x];
         if (out < N) dgamma[out] = t;
     }
 }
 
-// Slices of a row and consumer threads: a thread holds up to 4 packs of 8
-// columns (8 from N = 16384 on), and about 256 threads a block.
+// Packs a thread holds, of a row of P.  Forward: about 256 threads a block.
+// Backward, whose state is 24 registers a pack: up to 2 packs in blocks like
+// the forward's; 3 and 4 in blocks of at most 256 threads with the producer's,
+// so that two blocks of 128 registers a thread share an SM; rows too wide for
+// that take the SM for one block.
 int packs_per_thread(int P) { return P <= 256 ? 1 : P <= 512 ? 2 : P <= 2048 ? 4 : 8; }
+int backward_packs_per_thread(int P) { return P <= 256 ? 1 : P <= 512 ? 2 : P <= 672 ? 3 : P <= 1024 ? 4 : 8; }
 
 template <typename F>
 cudaError_t opt_in(F f) {
@@ -456,12 +478,12 @@ cudaError_t opt_in(F f) {
 RowsPlan rows_plan(RowsParams& p, int num_sms) {
     RowsPlan plan;
     const int P = p.N / 8;
-    plan.ppt = packs_per_thread(P);
+    plan.ppt = p.backward ? backward_packs_per_thread(P) : packs_per_thread(P);
     p.nt = ((P + plan.ppt - 1) / plan.ppt + 31) / 32 * 32;
     p.slices = (P + p.nt - 1) / p.nt;
     p.stage_bytes = p.nsrc * p.nt * 16;
-    const int blocks = p.nt <= 256 && p.M > num_sms ? 2 : 1;
-    const size_t fixed = (p.gamma_in_smem ? (size_t)p.N * 4 : 0) + kRedWords * 4 + 2 * kMaxStages * 8 + 16;
+    const int blocks = p.nt <= (p.backward && plan.ppt > 2 ? 224 : 256) && p.M > num_sms ? 2 : 1;
+    const size_t fixed = (p.backward ? (size_t)p.N * 4 : 0) + kRedWords * 4 + 2 * kMaxStages * 8 + 16;
     const size_t room = (blocks == 2 ? kRowsSmemPair : kRowsSmemLimit) - fixed;
     p.stages = (int)(room / p.stage_bytes);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
@@ -482,22 +504,29 @@ void (*quant_kernel(int ppt, int threads))(RowsParams) {
     }
 }
 
+template <bool ONE>
 void (*backward_kernel(int ppt, int threads))(RowsParams) {
     switch (ppt) {
-        case 1: return norm_backward_rows_kernel<1, 288, 2>;
-        case 2: return norm_backward_rows_kernel<2, 288, 2>;
-        default: return threads <= 288 ? norm_backward_rows_kernel<4, 288, 2> : norm_backward_rows_kernel<4, 544, 1>;
+        case 1: return norm_backward_rows_kernel<1, ONE, 288, 2>;
+        case 2: return norm_backward_rows_kernel<2, ONE, 288, 2>;
+        case 3: return norm_backward_rows_kernel<3, ONE, 256, 2>;
+        case 4: return threads <= 256 ? norm_backward_rows_kernel<4, ONE, 256, 2> : norm_backward_rows_kernel<4, ONE, 288, 1>;
+        default: return norm_backward_rows_kernel<8, ONE, 288, 1>;
     }
 }
 
 cudaError_t rows_prepare() {
     cudaError_t e = cudaSuccess;
-    for (int ppt = 1; ppt <= 8; ppt *= 2)
-        for (int threads = 288; threads <= 544; threads += 256) {
+    for (int ppt : {1, 2, 4, 8})
+        for (int threads : {288, 544}) {
             if (e == cudaSuccess) e = opt_in(quant_kernel<false>(ppt, threads));
             if (e == cudaSuccess) e = opt_in(quant_kernel<true>(ppt, threads));
-            if (e == cudaSuccess) e = opt_in(backward_kernel(ppt, threads));
         }
+    for (int ppt : {1, 2, 3, 4, 8})
+        for (int threads : {256, 288})
+            for (bool one : {false, true})
+                if (e == cudaSuccess)
+                    e = opt_in(one ? backward_kernel<true>(ppt, threads) : backward_kernel<false>(ppt, threads));
     return e;
 }
 
@@ -511,11 +540,20 @@ cudaError_t launch_norm_backward_rows(RowsParams& p, const RowsPlan& plan, float
                                       cudaStream_t s) {
     // a single block's sums are the result
     p.dgamma = dgamma == nullptr ? nullptr : plan.grid == 1 ? dgamma : scratch;
-    backward_kernel(plan.ppt, plan.threads)<<<plan.grid, plan.threads, plan.smem, s>>>(p);
+    auto* kernel = p.R == 1 ? backward_kernel<true>(plan.ppt, plan.threads) : backward_kernel<false>(plan.ppt, plan.threads);
+    kernel<<<plan.grid, plan.threads, plan.smem, s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && dgamma != nullptr && plan.grid > 1) {
-        dgamma_sum_kernel<<<(p.N + 31) / 32, 256, 0, s>>>(scratch, dgamma, plan.grid, p.N);
-        e = cudaGetLastError();
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(p.N + 15) / 16);
+        cfg.blockDim = dim3(256);
+        cfg.stream = s;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, dgamma_sum_kernel, static_cast<const float*>(scratch), dgamma, plan.grid, p.N);
     }
     return e;
 }
