@@ -211,6 +211,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
     extern __shared__ __align__(128) uint8_t rows_smem[];
     const Ring g = carve(rows_smem, p);
     ring_init(g, p);
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
     if (threadIdx.x >= p.nt) {
         produce(g, p);
         return;
@@ -324,7 +326,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
     extern __shared__ __align__(128) uint8_t rows_smem[];
     const Ring g = carve(rows_smem, p);
     ring_init(g, p);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // dgamma_sum_kernel may come up; it waits for the grid's end
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
     if (threadIdx.x >= p.nt) {
         produce(g, p);
         return;
@@ -422,14 +425,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
 }
 
 // dgamma[j] = sum over the blocks' partial rows, in an order that the number of
-// rows alone decides: 64 strands of every 64th row, halved six times.  It is
-// launched while the row kernel runs (programmatic dependent launch) and waits
-// for it here, which hides its launch.
+// rows alone decides: 64 strands of every 64th row, then the strands.
 __global__ void __launch_bounds__(256) dgamma_sum_kernel(const float* part, float* dgamma, int rows, int N) {
     __shared__ float4 sum[8][4];
     const int c = threadIdx.x & 3, strand = threadIdx.x >> 2;
     const int col = (blockIdx.x * 4 + c) * 4;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col < N) {
         float4 v[5];
@@ -467,6 +469,24 @@ __global__ void __launch_bounds__(256) dgamma_sum_kernel(const float* part, floa
 // that take the SM for one block.
 int packs_per_thread(int P) { return P <= 256 ? 1 : P <= 512 ? 2 : P <= 2048 ? 4 : 8; }
 int backward_packs_per_thread(int P) { return P <= 256 ? 1 : P <= 512 ? 2 : P <= 672 ? 3 : P <= 1024 ? 4 : 8; }
+
+// Launches on the programmatic dependency: the kernel comes up while the one
+// before it in the stream runs out, and waits for its end before it touches
+// global memory (grid_wait).  That hides the launch and the prologue.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
 
 template <typename F>
 cudaError_t opt_in(F f) {
@@ -532,8 +552,7 @@ cudaError_t rows_prepare() {
 
 cudaError_t launch_norm_quant_rows(const RowsParams& p, const RowsPlan& plan, bool pow2, cudaStream_t s) {
     auto* kernel = pow2 ? quant_kernel<true>(plan.ppt, plan.threads) : quant_kernel<false>(plan.ppt, plan.threads);
-    kernel<<<plan.grid, plan.threads, plan.smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(kernel, plan.grid, plan.threads, plan.smem, s, p);
 }
 
 cudaError_t launch_norm_backward_rows(RowsParams& p, const RowsPlan& plan, float* scratch, float* dgamma,
@@ -541,20 +560,9 @@ cudaError_t launch_norm_backward_rows(RowsParams& p, const RowsPlan& plan, float
     // a single block's sums are the result
     p.dgamma = dgamma == nullptr ? nullptr : plan.grid == 1 ? dgamma : scratch;
     auto* kernel = p.R == 1 ? backward_kernel<true>(plan.ppt, plan.threads) : backward_kernel<false>(plan.ppt, plan.threads);
-    kernel<<<plan.grid, plan.threads, plan.smem, s>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && dgamma != nullptr && plan.grid > 1) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(p.N + 15) / 16);
-        cfg.blockDim = dim3(256);
-        cfg.stream = s;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, dgamma_sum_kernel, static_cast<const float*>(scratch), dgamma, plan.grid, p.N);
-    }
+    cudaError_t e = launch_dependent(kernel, plan.grid, plan.threads, plan.smem, s, p);
+    if (e == cudaSuccess && dgamma != nullptr && plan.grid > 1)
+        e = launch_dependent(dgamma_sum_kernel, (p.N + 15) / 16, 256, 0, s, scratch, dgamma, plan.grid, p.N);
     return e;
 }
 

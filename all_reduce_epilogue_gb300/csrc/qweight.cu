@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
             seek();
         }
     };
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
     fetch(sreg[0], zreg[0], ring);
     fetch(sreg[1], zreg[1], ring + kSlotBytes);
 
@@ -401,15 +403,18 @@ Kernel kernel_of(int tt, bool qx, int wsteps, int steps) {
     return tt == 1 ? kernel_of<1>(qx, wsteps, steps) : tt == 2 ? kernel_of<2>(qx, wsteps, steps) : kernel_of<4>(qx, wsteps, steps);
 }
 
-void cluster_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int cluster, size_t smem) {
+void cluster_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int cluster, size_t smem) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)cluster;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    // the kernel comes up while the one before it runs out, and waits for its end (grid_wait)
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
 }
 
 }  // namespace
@@ -426,7 +431,7 @@ cudaError_t qweight_prepare(QweightDevice& dev) {
     // clusters of each size that are resident at once, at the largest shared memory a launch takes
     for (int c = 1; c <= kMaxRanks && e == cudaSuccess; ++c) {
         cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr;
+        cudaLaunchAttribute attr[2];
         cluster_config(cfg, attr, c, kMaxSmem);
         cfg.gridDim = dim3((unsigned)c);
         e = cudaOccupancyMaxActiveClusters(&dev.clusters[c], kernel_of(4, true, 1, 1), &cfg);
@@ -474,7 +479,7 @@ cudaError_t launch_qweight(QweightParams& p, bool qx, const QweightDevice& dev, 
     *variant = tt;
     const int shift = qx && p.xgroup_shift < p.group_shift ? p.xgroup_shift : p.group_shift;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
+    cudaLaunchAttribute attr[2];
     cluster_config(cfg, attr, *cluster, smem);
     cfg.gridDim = dim3((unsigned)*grid);
     cfg.stream = s;
