@@ -803,6 +803,7 @@ are_status qweight_call(const void* const x[], const void* const xscale[], int s
     p.M = (int)M;
     p.N = (int)N;
     p.K = (int)K;
+    p.qx = qx;
     p.group_shift = log2_group(group);
     p.groups = (int)ceil_div(K, group);
     if (qx) {
@@ -811,7 +812,7 @@ are_status qweight_call(const void* const x[], const void* const xscale[], int s
         p.xpow2 = scale_format == ARE_SCALE_E8M0;
     }
     int grid = 0, variant = 0, cluster = 0;
-    const cudaError_t e = launch_qweight(p, qx, ws->qweight, &grid, &variant, &cluster, s);
+    const cudaError_t e = launch_qweight(p, ws->qweight, &grid, &variant, &cluster, s);
     ws->last = are_launch_info{ARE_KERNEL_QWEIGHT, grid, 256, cluster, 0, variant, 0, 0};
     return from_cuda(e);
 }

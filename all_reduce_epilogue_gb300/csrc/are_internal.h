@@ -135,13 +135,17 @@ struct QweightParams {
     int R, nviews;
     int M, N, K;
     int group_shift, groups;             // log2 of the weight group, groups a row
-    int xgroup_shift, xgroups;
+    int qx;                              // tokens in 8 bits
+    int xgroup_shift, xgroups;           // of the token scales
     int xpow2;
-    int splits;                          // K splits of a rank; cluster = R * splits
+    // set by launch_qweight:
+    int cluster;                         // CTAs a cluster: R * splits
+    int splits;                          // K splits of a rank
     int split_k;                         // K range of a split
     int tile_k, tiles_k;                 // K range of a shared-memory tile, tiles of a split
-    int tiles_m;
-    int run;                             // 16-row groups of a cluster
+    int tiles_m;                         // token tiles
+    int run;                             // row groups of a cluster
+    int rtoks;                           // tokens of a tile that have sums, even
 };
 
 // What the launch shape depends on: resident clusters by cluster size.
@@ -151,7 +155,7 @@ struct QweightDevice {
 
 cudaError_t qweight_prepare(QweightDevice& dev);
 // Chooses the launch shape and launches; `grid`, `variant` and `cluster` report it.
-cudaError_t launch_qweight(QweightParams& p, bool qx, const QweightDevice& dev, int* grid, int* variant, int* cluster,
+cudaError_t launch_qweight(QweightParams& p, const QweightDevice& dev, int* grid, int* variant, int* cluster,
                            cudaStream_t s);
 
 // ------------------------------------------------------------------ GEMM + reduce

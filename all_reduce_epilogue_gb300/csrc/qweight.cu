@@ -4,27 +4,37 @@
 //   g = k / group,
 // with tokens x in bf16, or in FP8 E4M3 codes times a scale per group of k.
 //
-// Bound by the weights' bytes: M tokens use each of them M times.  So the
-// codes are read once, straight into a ring of shared memory per warp (16-byte
-// asynchronous copies, no barrier between warps), and meet the tokens in
-// m16n8k16 tensor instructions whose 16 rows are weight rows and whose 8
-// columns are tokens.  Integers u - z are exact in bf16, so every product is
-// exact and the group scales are applied in fp32, once per group, to the
-// tensor instruction's fp32 sums: no weight is ever rounded.
+// Bound by the weights' bytes: M tokens use each of them M times.  What
+// competes with the bytes is the integer work of unpacking the codes, so that
+// is made as small as it gets:
+//  * A code in bits 0..3 of an fp16 is the subnormal u * 2^-24, in bits 4..7
+//    u * 2^-20, exactly.  So a word of 8 codes becomes four operand registers
+//    of m16n8k16 tensor instructions (16 rows of weights, 16 of k, 8 tokens,
+//    fp32 sums) by four masks and a shift: the pairs (0, 4) (1, 5) (2, 6)
+//    (3, 7).  The tokens are staged in that order, the odd k times 2^-4.
+//    (Codes made into integers in fp16 take 9 instructions a word and in bf16
+//    11; FP8 operands would take 3, but FP8 mma.sync is not native here: it
+//    measured 36 cycles a sub-core for 32 of k, fp16 8.2 for 16.)
+//  * FP8 tokens are exact in fp16.  bf16 tokens, and FP8 ones with power-of-two
+//    scales, are scaled, per token and 256 of k, by the power of two that takes
+//    the largest to 2^14..2^15, which their scale in fp32 undoes: what is 2^-27
+//    times the largest or more stays exact, what is smaller is off by at most
+//    2^-35 of the largest, below the fp32 sums' own rounding.
+//  * The zero point leaves the sums: sum (u - z) x = sum u x - z sum x, with
+//    sum x per token and group in fp32.  The scales are applied in fp32, once
+//    per group, to the tensor instruction's fp32 sums.  No weight is rounded.
+//  * bf16 values that are not finite are staged as zeros, and their tokens'
+//    outputs get the products that hold them one by one at the end.
 //
-// A word of 8 codes gives the pairs (k, k+4), k = 0..3, of one MMA operand
-// register by a shift and a masked OR that places a code in the mantissa of
-// 128.0; the tokens are laid into shared memory in the same order of k, so
-// nothing is shuffled.
-//
-// A cluster owns a run of 16-row groups; each of its CTAs takes one rank's (or,
-// where R is small, part of a rank's) K range for all of them, so that its
-// tokens go to shared memory once.  The (group, 256 of K) items of a CTA are
-// dealt to its warps in equal contiguous runs.  At the end the CTAs add their
+// The codes are read once, into a ring of shared memory per warp (16-byte
+// asynchronous copies ahead of their use, no barrier between warps).  A cluster
+// owns a run of row groups; each of its CTAs takes one rank's (or, where R is
+// small, part of a rank's) K range for all of them.  Up to 8 tokens, the
+// (group, K) items of a CTA are dealt to its warps in equal contiguous runs of
+// 16-row groups; with more, a warp owns 32 rows, which share the tokens'
+// operands, and their sums stay in registers.  At the end the CTAs add their
 // fp32 sums over distributed shared memory, r ascending: no partial sum goes
 // through global memory and the order never varies.
-#include <type_traits>
-
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -37,18 +47,30 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kItemK = 256;                 // codes of a row in one ring slot
-constexpr int kRowBytes = kItemK / 2 + 16;  // 144: 36 words, so that 8 rows start in 8 different bank quads
-constexpr int kSlotBytes = 16 * kRowBytes;
-constexpr int kDepth = 3;                   // ring slots of a warp, and the length of the unrolled loop
-constexpr int kRingBytes = kWarps * kDepth * kSlotBytes;
-constexpr int kRedLd = 20;                  // floats between a sum's tokens: 8 rows of 4 token pairs in 32 banks
-constexpr int kMaxSmem = 113 * 1024;        // two CTAs an SM
+constexpr int kMaxSmem = 113 * 1024;       // two CTAs an SM
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src),
-                 "r"(valid ? 16 : 0)
+// The shape of the kernel for TT token tiles of 8.  An item (a ring slot) is 2 KB of codes.
+template <int TT>
+struct Shape {
+    static constexpr int TOK = TT * 8;
+    static constexpr bool OWN = TT >= 2;              // a warp owns its rows
+    static constexpr int RT = OWN ? 2 : 1;            // 16-row tiles of a group
+    static constexpr int ROWS = RT * 16;
+    static constexpr int ITEM = OWN ? 128 : 256;      // k of a slot
+    static constexpr int DEPTH = 3;                   // ring slots of a warp
+    static constexpr int PITCH = ITEM / 2 + 16;       // bytes: reads of 8 rows start in 8 different bank quads
+    static constexpr int SLOT = ROWS * PITCH;
+    static constexpr int RING = kWarps * DEPTH * SLOT;
+    static constexpr int LD = ROWS + 4;               // floats between a sum's tokens: 4 token pairs x 8 rows in 32 banks
+    static constexpr int UNITS = 8;                   // units of 8 k a thread stages of a K tile
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
                  : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -56,104 +78,174 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// Loads under a predicate: a register keeps its value where it is false, and no
+// branch stands between one load and the next (a branch each had every load
+// wait for the one before: 12 thousand cycles for 24 of them).
+__device__ __forceinline__ void ldg_if(uint4& v, const void* p, bool on) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+        : "l"(p), "r"((uint32_t)on));
+}
+__device__ __forceinline__ void ldg_if(uint2& v, const void* p, bool on) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+                 : "+r"(v.x), "+r"(v.y)
+                 : "l"(p), "r"((uint32_t)on));
+}
+__device__ __forceinline__ void ldg_u16_if(uint32_t& v, const void* p, bool on) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u16 %0, [%1];\n\t}"
+                 : "+r"(v)
+                 : "l"(p), "r"((uint32_t)on));
+}
+__device__ __forceinline__ void ldg_u8_if(uint32_t& v, const void* p, bool on) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u8 %0, [%1];\n\t}"
+                 : "+r"(v)
+                 : "l"(p), "r"((uint32_t)on));
 }
 
-// The same on a zero accumulator.
-__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
 }
-
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
-    __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<uint32_t*>(&r);
-}
-
-// The codes i and i + 4 of a word as the bf16 pair 128 + u, then u - z exactly.
-template <int I>
-__device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t z2) {
+__device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
     uint32_t v;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * I)), "r"(0x000F000Fu), "r"(0x43004300u));
-    return sub2(v, z2);
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
-__device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t v) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);  // exact: 4 significant bits
-    return *reinterpret_cast<const uint32_t*>(&b);
+// d (+)= a (weights) * b (tokens).
+template <bool FIRST>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
+    if (FIRST)
+        asm(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ float e8m0_to_float(uint32_t b) {
     return __uint_as_float(b == 255u ? 0x7FC00000u : b == 0u ? 0x00400000u : b << 23);
 }
 
-// 8 consecutive k of a token in the order of the weight pairs: 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ uint4 pair_order(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
-    return make_uint4(__byte_perm(w0, w2, 0x5410), __byte_perm(w0, w2, 0x7632), __byte_perm(w1, w3, 0x5410),
-                      __byte_perm(w1, w3, 0x7632));
+// Two floats of tokens as fp16.
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 fp8x2_to_float2(uint32_t v) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// 8 FP8 codes (x, y) times a power of two (z, E8M0) as bf16: exact from 2^-133 on.
+__device__ __forceinline__ uint4 codes_to_bf16(uint4 v) {
+    const float f = e8m0_to_float(v.z);
+    const float2 e[4] = {fp8x2_to_float2(v.x), fp8x2_to_float2(v.x >> 16), fp8x2_to_float2(v.y), fp8x2_to_float2(v.y >> 16)};
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(e[i].x * f, e[i].y * f);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// A word's codes: pairs (0, 4) and (2, 6) times 2^-24, (1, 5) and (3, 7) times 2^-20.
+template <int HALF>
+__device__ __forceinline__ void codes8(uint32_t w, uint32_t (&a0)[4], uint32_t (&a1)[4]) {
+    a0[HALF] = w & 0x000F000Fu;
+    a0[2 + HALF] = w & 0x00F000F0u;
+    w >>= 8;
+    a1[HALF] = w & 0x000F000Fu;
+    a1[2 + HALF] = w & 0x00F000F0u;
 }
 
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
+// A token's power of two, 2^(141 - top) with `top` the biased exponent of its
+// largest value (at most 2^127; 1 for zeros), and what undoes it.
+__device__ __forceinline__ float scale_of(uint32_t top) {
+    return top == 0u ? 1.f : __uint_as_float(min(268u - top, 254u) << 23);
+}
+__device__ __forceinline__ float unscale_of(uint32_t top) {
+    return top == 0u ? 1.f : top < 15u ? __uint_as_float(0x00400000u) : __uint_as_float((top - 14u) << 23);
 }
 
-// TT: token tiles of 8.  QX: tokens in 8 bits with scales.  WSTEPS: steps of
-// 32 k in a weight group; STEPS: those that share both scales, the smaller of
-// the weight and the token group.
+// TT: token tiles of 8.  QX: tokens in 8 bits with fp32 scales, which are applied
+// with the weights' (power-of-two scales go into the staged tokens, exactly).
+// WSTEPS: steps of 32 k in a weight group; STEPS: those that share both scales,
+// the smaller of the weight and the token group.
 template <int TT, bool QX, int WSTEPS, int STEPS>
 __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_constant__ QweightParams p) {
     extern __shared__ __align__(128) uint8_t qw_smem[];
-    constexpr int TOK = TT * 8;
-    constexpr int NS = 4 / WSTEPS;  // an item has 8 / WSTEPS weight groups x 2 row halves, NS for each of a row's lanes
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    using S = Shape<TT>;
+    constexpr int TOK = S::TOK, RT = S::RT, ROWS = S::ROWS, ITEM = S::ITEM, PITCH = S::PITCH, LD = S::LD;
+    constexpr bool OWN = S::OWN;
+    constexpr bool WIDE = STEPS == 4;       // a lane reads its 32 codes of 128 at once: all of them share the scales
+    constexpr int SLOT = S::SLOT, DEPTH = S::DEPTH, UNITS = S::UNITS;
+    constexpr int GRAIN = STEPS * 32;       // k that share both scales
+    constexpr float UNIT = QX ? 0x1p24f : 0x1p12f;  // what the sums lack (half of it is in the staged scales: none under- or overflows)
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     const int g = lane >> 2, c = lane & 3;
-    const int cluster = p.R * p.splits;
-    const int q = (int)(blockIdx.x % cluster);
-    const int tile = (int)(blockIdx.x / cluster);
-    const int m0 = (tile % p.tiles_m) * TOK, group0 = (tile / p.tiles_m) * p.run;
-    const int groups = min(p.run, (p.N + 15) / 16 - group0);  // of 16 rows
+    const int q = (int)(blockIdx.x % p.cluster);
+    const int tile = (int)(blockIdx.x / p.cluster);
+    const int m0 = tile % p.tiles_m * TOK, group0 = tile / p.tiles_m * p.run;
+    const int groups = min(p.run, (p.N + ROWS - 1) / ROWS - group0);  // of ROWS rows
     const int r = q / p.splits;
-    const int kbeg = (q % p.splits) * p.split_k, kend = min(p.K, kbeg + p.split_k);
+    const int kbeg = q % p.splits * p.split_k, kend = min(p.K, kbeg + p.split_k);  // never empty
+    const int toks = min(TOK, p.M - m0);
 
-    uint8_t* ring = qw_smem + warp * (kDepth * kSlotBytes);
-    uint8_t* xs = qw_smem + kRingBytes;                                // [tile_k / 32][TOK][4] units of 8 k
-    float* red = reinterpret_cast<float*>(xs + TOK * p.tile_k * 2);    // [slot][TOK][kRedLd]
-    float* xsc = red + (p.run + kWarps) * TOK * kRedLd;                // [token groups of the tile][TOK]
+    const uint32_t ring = ptx::smem_u32(qw_smem) + warp * (DEPTH * SLOT);
+    uint8_t* xs = qw_smem + S::RING;                                 // [k / 32][TT][lane] units of 8 k
+    float* xsum = reinterpret_cast<float*>(xs + 2 * TOK * p.tile_k);         // [k / GRAIN][TOK]: sum x * 2^-24
+    float* xsc = xsum + p.tile_k / GRAIN * TOK;                              // [k >> fshift][TOK]: the tokens' scales
+    const int fshift = QX ? p.xgroup_shift : 8, frows = QX ? p.tile_k >> fshift : (p.tile_k + 255) >> 8;
+    const int wrows = p.run * ROWS + 1;                                      // odd: a row's groups fall into different banks
+    uint32_t* wsc = reinterpret_cast<uint32_t*>(xsc + frows * TOK);          // [k >> group][wrows]: scale | zero point << 16, in bf16
+    uint32_t* bad = wsc + (((p.tile_k >> p.group_shift) * wrows + 3) & ~3);  // bit m: token m has a value that is not finite
+    // OWN: the ring's place, when the products are done.  Else [group + warp][rtoks][LD].
+    float* red = reinterpret_cast<float*>(OWN ? qw_smem : reinterpret_cast<uint8_t*>(bad + 4));
 
     // this warp's items of a K tile: [first, first + count), item = group * per + K index
-    const int per = p.tile_k / kItemK, all = groups * per;
-    const int first = warp * all / kWarps, count = (warp + 1) * all / kWarps - first;
+    const int per = p.tile_k / ITEM, all = groups * per;
+    const int first = OWN ? warp * per : warp * all / kWarps;
+    const int count = OWN ? (warp < groups ? per : 0) : (warp + 1) * all / kWarps - first;
 
-    // ---- the stream of items, two ahead of their use: codes by asynchronous copies (16 rows of 128
-    // bytes, 8 lanes a row, 4 rows apart), the weight scales and zero points by loads.  Lane c of a
-    // row quad loads row half c & 1 of the weight groups (c >> 1) + 2j.  N is a multiple of 8: a row
-    // half exists or not for all lanes.
-    const int64_t row4 = (int64_t)p.K * 2;  // bytes of four rows of codes
+    // ---- the stream of codes, DEPTH - 1 items ahead of their use, by asynchronous copies.  N is a
+    // multiple of 8: 8 rows exist or not.
+    constexpr int LPR = ITEM / 32, RPI = 32 / LPR, CP = ROWS / RPI;  // lanes a row of codes, rows an instruction, instructions
+    const int64_t rstep = (int64_t)RPI * (p.K >> 1);
+    const int64_t lane_off = (int64_t)(lane / LPR) * (p.K >> 1) + lane % LPR * 16;
+    const uint32_t lane_to = (uint32_t)(lane / LPR * PITCH + lane % LPR * 16);
     const uint8_t* fcodes = nullptr;
-    int64_t fscale = 0;
-    int ftl = -1, fleft = 0, fkk = 0, fgl = 0, fk = 0;
-    bool ffull = false;
-    uint32_t sreg[kDepth][NS], zreg[kDepth][NS];
-    auto seek = [&]() {  // pointers of group fgl, K index fkk of tile ftl
-        const int n = (group0 + fgl) * 16;
-        fk = kbeg + ftl * p.tile_k + fkk * kItemK;
-        ffull = n + 16 <= p.N;
-        fcodes = p.codes[r] + (((int64_t)(n + (lane >> 3)) * p.K + fk) >> 1) + (lane & 7) * 16;
-        fscale = (int64_t)(n + g + 8 * (c & 1)) * p.groups + (fk >> p.group_shift) + (c >> 1);
+    int ftl = -1, fleft = 0, fkk = 0, fgl = 0, fk = 0, fn = 0;
+    auto seek = [&]() {  // group fgl, K index fkk of tile ftl
+        const int n = (group0 + fgl) * ROWS;
+        fk = kbeg + ftl * p.tile_k + fkk * ITEM;
+        fn = p.N - n;
+        fcodes = p.codes[r] + (((int64_t)n * p.K + fk) >> 1) + lane_off;
     };
-    auto fetch = [&](uint32_t (&sv)[NS], uint32_t (&zv)[NS], uint8_t* to) {
+    auto fetch = [&](uint32_t slot) {
         if (fleft == 0) {
             if (count > 0 && ftl + 1 < p.tiles_k) {
                 ++ftl;
@@ -166,28 +258,21 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
                 return;
             }
         }
-        const bool kin = fk + (lane & 7) * 32 < kend;
-        const uint8_t* from = kin ? fcodes : p.codes[r];
-        const int64_t step = kin ? row4 : 0;
-        uint8_t* at = to + (lane >> 3) * kRowBytes + (lane & 7) * 16;
-        cp_async16(at, from, kin);
-        cp_async16(at + 4 * kRowBytes, from + step, kin);
-        cp_async16(at + 8 * kRowBytes, ffull ? from + 2 * step : from, kin && ffull);
-        cp_async16(at + 12 * kRowBytes, ffull ? from + 3 * step : from, kin && ffull);
-        cp_commit();
-        const bool nin = ffull || (c & 1) == 0;
+        const uint32_t to = slot + lane_to;
+        if (fn >= ROWS && fk + ITEM <= kend) {
 #pragma unroll
-        for (int j = 0; j < NS; ++j) {
-            sv[j] = 0u;  // what does not exist weighs nothing
-            zv[j] = 8u;
-            if (nin && fk + ((c >> 1) + 2 * j) * (WSTEPS * 32) < kend) {
-                sv[j] = __ldg(p.scale[r] + fscale + 2 * j);
-                if (p.zero[r]) zv[j] = __ldg(p.zero[r] + fscale + 2 * j);
+            for (int j = 0; j < CP; ++j) cp_async16(to + j * RPI * PITCH, fcodes + j * rstep);
+        } else {  // rows or K that end within the item: zeros
+            const bool kin = fk + lane % LPR * 32 < kend;
+#pragma unroll
+            for (int j = 0; j < CP; ++j) {
+                const bool in = kin && j * RPI < fn;
+                cp_async16(to + j * RPI * PITCH, in ? fcodes + j * rstep : p.codes[r], in);
             }
         }
-        fk += kItemK;
-        fcodes += kItemK / 2;
-        fscale += 8 / WSTEPS;
+        cp_commit();
+        fk += ITEM;
+        fcodes += ITEM / 2;
         --fleft;
         if (++fkk == per) {
             fkk = 0;
@@ -195,187 +280,357 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
             seek();
         }
     };
+
     ptx::grid_launch_dependents();
     ptx::grid_wait();
-    fetch(sreg[0], zreg[0], ring);
-    fetch(sreg[1], zreg[1], ring + kSlotBytes);
+    fetch(ring);
+    fetch(ring + SLOT);
 
-    // ---- a K tile's tokens, in bf16 and in the order of the weight pairs; token scales
+    // ---- a K tile's tokens and weight scales into shared memory.  A warp takes a token's 256 k at a time, a unit of 8 k a
+    // lane; its (at most UNITS) loads are in flight together.
+    int tokp = 1;
+    while (tokp < toks) tokp <<= 1;
+    // The rows' scales and zero points: neighbouring lanes take a row's neighbouring groups (lanes on rows
+    // of their own would touch a sector each with every load); what does not exist weighs nothing.
+    constexpr int WUNITS = 16;
+    const bool zeros = p.zero[r] != nullptr;
+    const int tg = p.tile_k >> p.group_shift;
+    int tsh = 0;
+    while (1 << tsh < tg) ++tsh;
+    const int wunits = p.run * ROWS << tsh;
+    uint32_t sv[WUNITS], zv[WUNITS];
+    auto load_scales = [&](int t0, int u0) {
+#pragma unroll
+        for (int j = 0; j < WUNITS; ++j) {
+            const int u = u0 + j * kThreads, gi = u & ((1 << tsh) - 1), n = group0 * ROWS + (u >> tsh);
+            sv[j] = 0u;
+            zv[j] = 8u;
+            const bool in = u < wunits && n < p.N && gi < tg && (t0 >> p.group_shift) + gi < p.groups;
+            const int64_t at = (int64_t)n * p.groups + (t0 >> p.group_shift) + gi;
+            ldg_u16_if(sv[j], p.scale[r] + at, in);
+            ldg_u8_if(zv[j], p.zero[r] + at, in && zeros);
+        }
+    };
     auto stage = [&](int tl) {
         const int t0 = kbeg + tl * p.tile_k;
-        if (tl) __syncthreads();
-        for (int u = threadIdx.x; u < TOK * p.tile_k / 8; u += kThreads) {
-            const int m = m0 + (u >> 2) % TOK, k = t0 + u / (4 * TOK) * 32 + (u & 3) * 8;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (m < p.M && k < kend) {
-                if (QX) {
-                    const uint2 b = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.x[r]) +
-                                                                         (int64_t)m * p.K + k));
-                    v = pair_order(fp8x2_to_bf16x2(b.x), fp8x2_to_bf16x2(b.x >> 16), fp8x2_to_bf16x2(b.y),
-                                   fp8x2_to_bf16x2(b.y >> 16));
-                } else {
-                    const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x[r]) +
-                                                                         (int64_t)m * p.K + k));
-                    v = pair_order(b.x, b.y, b.z, b.w);
+        const int todo = ((p.tile_k + 255) >> 8) * tokp;  // (256 k, token) rows, the token innermost
+        uint4 v[UNITS];
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            const int i = warp + j * kWarps, m = i & (tokp - 1), k = t0 + i / tokp * 256 + lane * 8;
+            const bool in = i < todo && m < toks && k < kend;
+            const int64_t at = (int64_t)(m0 + m) * p.K + k;
+            if (QX || p.qx) {
+                uint2 b = make_uint2(0u, 0u);
+                ldg_if(b, static_cast<const uint8_t*>(p.x[r]) + at, in);
+                v[j].x = b.x;
+                v[j].y = b.y;
+                if (!QX) ldg_u8_if(v[j].z, static_cast<const uint8_t*>(p.xscale[r]) + (int64_t)(m0 + m) * p.xgroups + (k >> p.xgroup_shift), in);
+            } else {
+                ldg_if(v[j], static_cast<const uint16_t*>(p.x[r]) + at, in);
+            }
+        }
+        load_scales(t0, threadIdx.x);  // in flight with the tokens
+        if (tl) __syncthreads();       // every warp is done with the tile before
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            const int i = warp + j * kWarps;
+            if (i >= todo) break;
+            const int m = i & (tokp - 1), k = i / tokp * 256 + lane * 8;  // within the tile
+            if (m >= toks || i / tokp * 256 >= p.tile_k) continue;
+            float x[8];  // even and odd k: 0 2 4 6 1 3 5 7
+            if (QX) {
+                const float2 e[4] = {fp8x2_to_float2(v[j].x), fp8x2_to_float2(v[j].x >> 16), fp8x2_to_float2(v[j].y),
+                                     fp8x2_to_float2(v[j].y >> 16)};
+#pragma unroll
+                for (int e4 = 0; e4 < 4; ++e4) {
+                    x[e4] = e[e4].x;
+                    x[4 + e4] = e[e4].y;
+                }
+            } else {
+                if (p.qx) v[j] = codes_to_bf16(v[j]);
+                // the largest exponent
+                uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7F807F80u, w[1] & 0x7F807F80u), __vmaxu2(w[2] & 0x7F807F80u, w[3] & 0x7F807F80u));
+                top = __reduce_max_sync(0xFFFFFFFFu, max(top >> 23, top >> 7 & 0xFFu));
+                if (top == 255u) {  // values that are not finite: zeros here, and the token is noted
+                    if (lane == 0) atomicOr(&bad[m >> 5], 1u << (m & 31));
+                    top = 0u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0x0000FFFFu;
+                        if ((w[e] & 0x00007F80u) == 0x00007F80u) w[e] &= 0xFFFF0000u;
+                        top = __vmaxu2(top, w[e] & 0x7F807F80u);
+                    }
+                    top = __reduce_max_sync(0xFFFFFFFFu, max(top >> 23, top >> 7 & 0xFFu));
+                }
+                const float mul = scale_of(top);
+                if (lane == 0) xsc[(k >> 8) * TOK + m] = unscale_of(top) * 0x1p12f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = bf_lo(w[e]) * mul;
+                    x[4 + e] = bf_hi(w[e]) * mul;
                 }
             }
-            *reinterpret_cast<uint4*>(xs + u * 16) = v;
+            // step st = 32 k, or lane c's word st of 128 k
+            const int st = WIDE ? (k >> 7) * 4 + (lane & 3) : k >> 5, c4 = WIDE ? lane >> 2 & 3 : lane & 3;
+            if (k < p.tile_k)
+                *reinterpret_cast<uint4*>(xs + (((st * TT + (m >> 3)) * 8 + (m & 7)) * 4 + c4) * 16) =
+                    make_uint4(f16x2(x[0], x[2]), f16x2(x[4] * 0.0625f, x[6] * 0.0625f), f16x2(x[1], x[3]),
+                               f16x2(x[5] * 0.0625f, x[7] * 0.0625f));
+            // sum x over each GRAIN of k, in the weights' unit
+            float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+#pragma unroll
+            for (int o = 1; o < GRAIN / 8; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            if ((lane & (GRAIN / 8 - 1)) == 0 && k < p.tile_k) xsum[k / GRAIN * TOK + m] = sum * 0x1p-24f;
         }
         if (QX) {
-            const int xg = p.tile_k >> p.xgroup_shift, x0 = t0 >> p.xgroup_shift;
-            for (int u = threadIdx.x; u < xg * TOK; u += kThreads) {
+            const int x0 = t0 >> p.xgroup_shift;
+            for (int u = threadIdx.x; u < frows * TOK; u += kThreads) {
                 const int m = u % TOK, gi = u / TOK;
-                float v = 0.f;
-                if (m0 + m < p.M && x0 + gi < p.xgroups) {
-                    const int64_t at = (int64_t)(m0 + m) * p.xgroups + x0 + gi;
-                    v = p.xpow2 ? e8m0_to_float(__ldg(static_cast<const uint8_t*>(p.xscale[r]) + at))
-                                : __ldg(static_cast<const float*>(p.xscale[r]) + at);
-                }
-                xsc[u] = v;
+                const bool in = m < toks && x0 + gi < p.xgroups;
+                xsc[u] = in ? __ldg(static_cast<const float*>(p.xscale[r]) + (int64_t)(m0 + m) * p.xgroups + x0 + gi) : 0.f;
+            }
+        }
+        for (int u0 = threadIdx.x; u0 < wunits; u0 += WUNITS * kThreads) {
+            if (u0 != threadIdx.x) load_scales(t0, u0);
+#pragma unroll
+            for (int j = 0; j < WUNITS; ++j) {
+                const int u = u0 + j * kThreads, gi = u & ((1 << tsh) - 1);
+                if (u < wunits && gi < tg) wsc[gi * wrows + (u >> tsh)] = sv[j] | (__float_as_uint((float)zv[j]) & 0xFFFF0000u);  // 0..255: exact in bf16
             }
         }
         __syncthreads();
     };
+    if (threadIdx.x < 2) bad[threadIdx.x] = 0u;
+    if (toks < TOK) {  // tokens that do not exist: zeros, which no tile overwrites
+        for (int u = threadIdx.x; u < TOK * p.tile_k / 8; u += kThreads)
+            *reinterpret_cast<uint4*>(xs + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+        for (int u = threadIdx.x; u < p.tile_k / GRAIN * TOK; u += kThreads) xsum[u] = 0.f;
+        for (int u = threadIdx.x; u < frows * TOK; u += kThreads) xsc[u] = 0.f;
+    }
+    __syncthreads();
 
-    float acc[TT][4];
+    float acc[RT][TT][4];
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
+    for (int a = 0; a < RT; ++a)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
-    int tl = -1, left = 0, gl = 0, kk = 0;
-    // One item.  PH: its ring slot and the place of its scales, fixed in the unrolled loop (moving a
-    // register whose load is in flight would wait for it).
-    auto item = [&](auto ph) {
-        constexpr int PH = decltype(ph)::value;
-        constexpr int NEXT = (PH + 2) % kDepth;
-        if (left == 0) {
-            stage(++tl);
-            left = count;
-            gl = first / per;
-            kk = first % per;
-        }
-        cp_wait<kDepth - 2>();
-        __syncwarp();  // every lane's copies have landed, and every lane has left the slot refilled next
-        fetch(sreg[NEXT], zreg[NEXT], ring + NEXT * kSlotBytes);
-        const uint8_t* at = ring + PH * kSlotBytes + g * kRowBytes + c * 4;
-        uint32_t word[NS];  // scale | 128 + zero, as two bf16
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int j = 0; j < NS; ++j) word[j] = sreg[PH][j] | ((0x4300u + zreg[PH][j]) << 16);
-        const int kt = kk * kItemK;
-        if (kbeg + tl * p.tile_k + kt < kend) {
-            const uint8_t* xat = xs + (kt >> 5) * (TOK * 64) + lane * 16;
-            float d[TT][4];
-            uint32_t slo = 0, shi = 0, zlo = 0, zhi = 0;
+            for (int j = 0; j < 4; ++j) acc[a][t][j] = 0.f;
+    const uint32_t xs_addr = ptx::smem_u32(xs) + lane * 16u;
+    uint32_t cur = ring;
+    const uint32_t ring_end = ring + DEPTH * SLOT;
+#pragma unroll 1
+    for (int tl = 0; tl < p.tiles_k; ++tl) {
+        stage(tl);
+        const int ktile = kbeg + tl * p.tile_k;
+        int gl = first / per, kk = first % per;
+#pragma unroll 1
+        for (int left = count; left > 0; --left) {
+            cp_wait<DEPTH - 2>();
+            __syncwarp();  // every lane's copies have landed, and every lane has left the slot refilled now
+            const uint32_t next = cur + SLOT == ring_end ? ring : cur + SLOT;
+            fetch(next + SLOT == ring_end ? ring : next + SLOT);
+            const uint32_t at = cur + g * PITCH + c * (WIDE ? 16 : 4);
+            cur = next;
+            if (ktile + kk * ITEM < kend) {
 #pragma unroll
-            for (int st = 0; st < kItemK / 32; ++st) {
-                if (st % WSTEPS == 0) {
-                    const int gi = st / WSTEPS;  // lane 2 * (gi & 1) + half of the quad has it at j = gi / 2
-                    slo = __shfl_sync(0xFFFFFFFFu, word[gi / 2], (lane & 28) + (gi & 1) * 2);
-                    shi = __shfl_sync(0xFFFFFFFFu, word[gi / 2], (lane & 28) + (gi & 1) * 2 + 1);
-                    zlo = __byte_perm(slo, slo, 0x3232);
-                    zhi = __byte_perm(shi, shi, 0x3232);
-                }
-                const uint32_t wlo = *reinterpret_cast<const uint32_t*>(at + st * 16);
-                const uint32_t whi = *reinterpret_cast<const uint32_t*>(at + 8 * kRowBytes + st * 16);
-                const uint32_t a0[4] = {codes2<0>(wlo, zlo), codes2<0>(whi, zhi), codes2<1>(wlo, zlo), codes2<1>(whi, zhi)};
-                const uint32_t a1[4] = {codes2<2>(wlo, zlo), codes2<2>(whi, zhi), codes2<3>(wlo, zlo), codes2<3>(whi, zhi)};
+                for (int blk = 0; blk < ITEM / 128; ++blk) {
+                    const int kt = kk * ITEM + blk * 128;  // within the tile
+                    // 128 k of the rows
+                    uint32_t a[RT][4][2][4];
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    const uint4 b = *reinterpret_cast<const uint4*>(xat + st * (TOK * 64) + t * 512);
-                    if (st % STEPS == 0) mma16816_first(d[t], a0, b.x, b.y);
-                    else mma16816(d[t], a0, b.x, b.y);
-                    mma16816(d[t], a1, b.z, b.w);
-                }
-                if (st % STEPS == STEPS - 1) {
-                    const float fl = __uint_as_float(slo << 16), fh = __uint_as_float(shi << 16);
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) {
-                        if (QX) {
-                            const float2 x2 = *reinterpret_cast<const float2*>(
-                                xsc + ((kt + st * 32) >> p.xgroup_shift) * TOK + t * 8 + 2 * c);
-                            acc[t][0] = fmaf(fl * x2.x, d[t][0], acc[t][0]);
-                            acc[t][1] = fmaf(fl * x2.y, d[t][1], acc[t][1]);
-                            acc[t][2] = fmaf(fh * x2.x, d[t][2], acc[t][2]);
-                            acc[t][3] = fmaf(fh * x2.y, d[t][3], acc[t][3]);
+                    for (int rt = 0; rt < RT; ++rt) {
+                        uint32_t lo[4], hi[4];
+                        const uint32_t from = at + rt * 16 * PITCH + blk * 64;
+                        if (WIDE) {
+                            const uint4 l4 = ld_shared_v4(from), h4 = ld_shared_v4(from + 8 * PITCH);
+                            lo[0] = l4.x; lo[1] = l4.y; lo[2] = l4.z; lo[3] = l4.w;
+                            hi[0] = h4.x; hi[1] = h4.y; hi[2] = h4.z; hi[3] = h4.w;
                         } else {
-                            acc[t][0] = fmaf(fl, d[t][0], acc[t][0]);
-                            acc[t][1] = fmaf(fl, d[t][1], acc[t][1]);
-                            acc[t][2] = fmaf(fh, d[t][2], acc[t][2]);
-                            acc[t][3] = fmaf(fh, d[t][3], acc[t][3]);
+#pragma unroll
+                            for (int st = 0; st < 4; ++st) {
+                                lo[st] = ld_shared(from + st * 16);
+                                hi[st] = ld_shared(from + 8 * PITCH + st * 16);
+                            }
+                        }
+#pragma unroll
+                        for (int st = 0; st < 4; ++st) {
+                            codes8<0>(lo[st], a[rt][st][0], a[rt][st][1]);
+                            codes8<1>(hi[st], a[rt][st][0], a[rt][st][1]);
+                        }
+                    }
+                    // the rows' scales and zero points, once for all tokens
+                    float ws[4 / WSTEPS][RT][2], wz[4 / WSTEPS][RT][2];
+                    const uint32_t* words = wsc + (kt >> p.group_shift) * wrows + gl * ROWS + g;
+#pragma unroll
+                    for (int i = 0; i < 4 / WSTEPS; ++i)
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const uint32_t word = words[i * wrows + rt * 16 + half * 8];
+                                ws[i][rt][half] = __uint_as_float(word << 16);
+                                wz[i][rt][half] = __uint_as_float(word & 0xFFFF0000u);
+                            }
+                    // TB token tiles at a time, CH chains of sums each: a dependent instruction waits for
+                    // the one before it
+                    constexpr int TB = TT == 2 ? 2 : 1, CH = OWN ? 1 : 2;  // OWN: its two row tiles are two chains
+#pragma unroll
+                    for (int tb = 0; tb < TT; tb += TB) {
+                        const uint32_t xat = xs_addr + (uint32_t)(((kt >> 5) * TT + tb) * 512);
+                        uint4 b[TB][4];
+#pragma unroll
+                        for (int st = 0; st < 4; ++st)
+#pragma unroll
+                            for (int t = 0; t < TB; ++t) b[t][st] = ld_shared_v4(xat + st * TT * 512 + t * 512);
+                        float d[TB][RT][CH][4];
+#pragma unroll
+                        for (int st = 0; st < 4; ++st) {
+#pragma unroll
+                            for (int t = 0; t < TB; ++t)
+#pragma unroll
+                                for (int rt = 0; rt < RT; ++rt) {
+                                    if (st % STEPS == 0) mma<true>(d[t][rt][0], a[rt][st][0], b[t][st].x, b[t][st].y);
+                                    else mma<false>(d[t][rt][0], a[rt][st][0], b[t][st].x, b[t][st].y);
+                                    if (CH == 2 && st % STEPS == 0) mma<true>(d[t][rt][CH - 1], a[rt][st][1], b[t][st].z, b[t][st].w);
+                                    else mma<false>(d[t][rt][CH - 1], a[rt][st][1], b[t][st].z, b[t][st].w);
+                                }
+                            if (st % STEPS != STEPS - 1) continue;
+#pragma unroll
+                            for (int t = 0; t < TB; ++t) {
+                                const int tok = (tb + t) * 8 + 2 * c;
+                                const float2 sum = *reinterpret_cast<const float2*>(xsum + ((kt + st * 32) / GRAIN) * TOK + tok);
+                                const float2 f = *reinterpret_cast<const float2*>(xsc + ((kt + st * 32) >> fshift) * TOK + tok);
+#pragma unroll
+                                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                                    for (int half = 0; half < 2; ++half) {
+                                        const float s = ws[st / WSTEPS][rt][half], z = wz[st / WSTEPS][rt][half];
+                                        const float(&d2)[CH][4] = d[t][rt];
+                                        float y0 = d2[0][half * 2], y1 = d2[0][half * 2 + 1];
+                                        if (CH == 2) {
+                                            y0 += d2[CH - 1][half * 2];
+                                            y1 += d2[CH - 1][half * 2 + 1];
+                                        }
+                                        float* e = &acc[rt][tb + t][half * 2];
+                                        e[0] = fmaf(s * f.x, fmaf(-z, sum.x, y0), e[0]);
+                                        e[1] = fmaf(s * f.y, fmaf(-z, sum.y, y1), e[1]);
+                                    }
+                            }
                         }
                     }
                 }
             }
-        }
-        --left;
-        if (++kk == per || left == 0) {
-            // the warp leaves a group: its sums go to the slot of (group, warp), which no other
-            // warp touches; along a CTA's items either index grows, so group + warp is unique
-            float* to = red + (gl + warp) * TOK * kRedLd + g;
+            if (!OWN && (++kk == per || left == 1)) {
+                // the warp leaves a group: its sums go to the slot of (group, warp), which no other
+                // warp touches; along a CTA's items either index grows, so group + warp is unique
+                float* to = red + (gl + warp) * p.rtoks * LD + g;
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                float* e = to + (t * 8 + 2 * c) * kRedLd;
-                if (tl == 0) {
-                    e[0] = acc[t][0]; e[kRedLd] = acc[t][1]; e[8] = acc[t][2]; e[kRedLd + 8] = acc[t][3];
-                } else {
-                    e[0] += acc[t][0]; e[kRedLd] += acc[t][1]; e[8] += acc[t][2]; e[kRedLd + 8] += acc[t][3];
+                for (int t = 0; t < TT; ++t) {
+                    float* e = to + (t * 8 + 2 * c) * LD;
+                    float* v = acc[0][t];
+                    if (t * 8 + 2 * c >= p.rtoks) {
+                    } else if (tl == 0) {
+                        e[0] = v[0] * UNIT; e[LD] = v[1] * UNIT; e[8] = v[2] * UNIT; e[LD + 8] = v[3] * UNIT;
+                    } else {
+                        e[0] = fmaf(v[0], UNIT, e[0]); e[LD] = fmaf(v[1], UNIT, e[LD]);
+                        e[8] = fmaf(v[2], UNIT, e[8]); e[LD + 8] = fmaf(v[3], UNIT, e[LD + 8]);
+                    }
+                    v[0] = v[1] = v[2] = v[3] = 0.f;
                 }
-                acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+                kk = 0;
+                ++gl;
+            } else if (OWN) {
+                ++kk;
             }
-            kk = 0;
-            ++gl;
         }
-    };
-    if (count == 0) {  // a warp without items helps to stage the tokens
-        for (int i = 0; i < p.tiles_k; ++i) stage(i);
-    } else {
-        const int total = p.tiles_k * count;
-        int i = 0;
-        for (; i + kDepth <= total; i += kDepth) {
-            item(std::integral_constant<int, 0>{});
-            item(std::integral_constant<int, 1>{});
-            item(std::integral_constant<int, 2>{});
-        }
-        if (i < total) item(std::integral_constant<int, 0>{});
-        if (i + 1 < total) item(std::integral_constant<int, 1>{});
     }
     cp_wait<0>();
     __syncthreads();
 
     // ---- the sums: of a group over the CTA's warps (into the slot of its first warp), then over the
     // cluster, r ascending.  Item i belongs to warp (8 (i + 1) - 1) / all.
-    const int toks = min(TOK, p.M - m0);
-    auto warp_of = [&](int i) { return (kWarps * (i + 1) - 1) / all; };
-    for (int a = warp; a < groups; a += kWarps) {
-        const int w0 = warp_of(a * per), w1 = warp_of(a * per + per - 1);
-        for (int w = w0 + 1; w <= w1; ++w) {
-            if ((w + 1) * all / kWarps == w * all / kWarps) continue;  // a warp without items
-            for (int m = lane >> 4; m < toks; m += 2)
-                red[((a + w0) * TOK + m) * kRedLd + (lane & 15)] += red[((a + w) * TOK + m) * kRedLd + (lane & 15)];
+    auto slot_of = [&](int a) { return OWN ? a : a + (kWarps * (a * per + 1) - 1) / all; };
+    if (OWN) {
+        if (count > 0) {
+            float* to = red + warp * p.rtoks * LD + g;
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    if (t * 8 + 2 * c >= p.rtoks) break;
+                    float* e = to + (t * 8 + 2 * c) * LD + rt * 16;
+                    e[0] = acc[rt][t][0] * UNIT; e[LD] = acc[rt][t][1] * UNIT;
+                    e[8] = acc[rt][t][2] * UNIT; e[LD + 8] = acc[rt][t][3] * UNIT;
+                }
+            }
+        }
+    } else {
+        for (int a = warp; a < groups; a += kWarps) {
+            const int s0 = slot_of(a), w0 = s0 - a, w1 = (kWarps * (a * per + per) - 1) / all;
+            for (int w = w0 + 1; w <= w1; ++w) {
+                if ((w + 1) * all / kWarps == w * all / kWarps) continue;  // a warp without items
+                for (int m = lane >> 4; m < toks; m += 2)
+                    red[(s0 * p.rtoks + m) * LD + (lane & 15)] += red[((a + w) * p.rtoks + m) * LD + (lane & 15)];
+            }
         }
     }
     __syncwarp();
     ptx::cluster_sync();
-    const uint32_t base = ptx::smem_u32(red);
-    for (int a = q + cluster * warp; a < groups; a += cluster * kWarps) {
-        const int n = (group0 + a) * 16 + (lane & 7) * 2;
-        const int s0 = a + warp_of(a * per);
-        if (n < p.N) {
-            for (int m = lane >> 3; m < toks; m += 4) {
-                const uint32_t addr = base + (uint32_t)((s0 * TOK + m) * kRedLd + (lane & 7) * 2) * 4u;
-                float2 s = make_float2(0.f, 0.f);
+    constexpr int PAIRS = ROWS / 2;  // pairs of rows of a group
+    const uint32_t base = ptx::smem_u32(red), bad_addr = ptx::smem_u32(bad);
+    uint32_t any[2] = {0u, 0u};
+    if (!QX) {
 #pragma unroll
-                for (int j = 0; j < kMaxRanks; ++j) {
-                    if (j < cluster) {
-                        const float2 v = ld_cluster_f2(ptx::mapa_shared(addr, (uint32_t)j));
-                        s.x += v.x;
-                        s.y += v.y;
+        for (int j = 0; j < kMaxRanks; ++j)
+            if (j < p.cluster) {
+                any[0] |= ld_cluster(ptx::mapa_shared(bad_addr, (uint32_t)j));
+                if (TOK > 32) any[1] |= ld_cluster(ptx::mapa_shared(bad_addr + 4u, (uint32_t)j));
+            }
+    }
+    // the cluster's threads take the (token, group, pair) in turn
+    for (int u = q * kThreads + threadIdx.x; u < groups * PAIRS * toks; u += p.cluster * kThreads) {
+        const int pair = u % PAIRS, a = u / PAIRS % groups, m = u / PAIRS / groups;
+        const int n = (group0 + a) * ROWS + pair * 2;
+        if (n < p.N) {
+            const uint32_t addr = base + (uint32_t)((slot_of(a) * p.rtoks + m) * LD + pair * 2) * 4u;
+            float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < kMaxRanks; ++j) {
+                if (j < p.cluster) {
+                    const float2 v = ld_cluster_f2(ptx::mapa_shared(addr, (uint32_t)j));
+                    s.x += v.x;
+                    s.y += v.y;
+                }
+            }
+            if (!QX && (any[m >> 5] >> (m & 31) & 1u)) {  // products of values that are not finite
+                for (int j = 0; j < p.cluster; ++j) {
+                    const int rj = j / p.splits, k0 = j % p.splits * p.split_k, k1 = min(p.K, k0 + p.split_k);
+                    const int64_t row = (int64_t)(m0 + m) * p.K;
+                    for (int k = k0; k < k1; ++k) {
+                        float xv;
+                        if (p.qx)
+                            xv = fp8x2_to_float2(__ldg(static_cast<const uint8_t*>(p.x[rj]) + row + k)).x *
+                                 e8m0_to_float(__ldg(static_cast<const uint8_t*>(p.xscale[rj]) + (int64_t)(m0 + m) * p.xgroups + (k >> p.xgroup_shift)));
+                        else xv = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p.x[rj]) + row + k) << 16);
+                        if ((__float_as_uint(xv) & 0x7F800000u) != 0x7F800000u) continue;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int64_t at = (int64_t)(n + i) * p.groups + (k >> p.group_shift);
+                            const uint32_t byte = __ldg(p.codes[rj] + (((int64_t)(n + i) * p.K + k) >> 1));
+                            const int u = (int)(k & 1 ? byte >> 4 : byte & 15u), z = p.zero[rj] ? __ldg(p.zero[rj] + at) : 8;
+                            const float w = (float)(u - z) * __uint_as_float((uint32_t)__ldg(p.scale[rj] + at) << 16);
+                            (i ? s.y : s.x) += xv * w;
+                        }
                     }
                 }
-                const __nv_bfloat162 o = __floats2bfloat162_rn(s.x, s.y);
-                for (int v = 0; v < p.nviews; ++v)
-                    *reinterpret_cast<__nv_bfloat162*>(p.views[v] + (int64_t)(m0 + m) * p.N + n) = o;
             }
+            const __nv_bfloat162 o = __floats2bfloat162_rn(s.x, s.y);
+            for (int v = 0; v < p.nviews; ++v)
+                *reinterpret_cast<__nv_bfloat162*>(p.views[v] + (int64_t)(m0 + m) * p.N + n) = o;
         }
     }
     __syncwarp();
@@ -417,6 +672,15 @@ void cluster_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int
     cfg.numAttrs = 2;
 }
 
+struct HostShape {
+    int rows, item, ring, ld, units;
+};
+template <int TT>
+HostShape host_shape() {
+    using S = Shape<TT>;
+    return {S::ROWS, S::ITEM, S::RING, S::LD, S::UNITS};
+}
+
 }  // namespace
 
 cudaError_t qweight_prepare(QweightDevice& dev) {
@@ -434,56 +698,77 @@ cudaError_t qweight_prepare(QweightDevice& dev) {
         cudaLaunchAttribute attr[2];
         cluster_config(cfg, attr, c, kMaxSmem);
         cfg.gridDim = dim3((unsigned)c);
-        e = cudaOccupancyMaxActiveClusters(&dev.clusters[c], kernel_of(4, true, 1, 1), &cfg);
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&dev.clusters[c], kernel_of(2, true, 1, 1), &cfg);
         if (e == cudaSuccess && dev.clusters[c] < 1) dev.clusters[c] = 1;
     }
     return e;
 }
 
-cudaError_t launch_qweight(QweightParams& p, bool qx, const QweightDevice& dev, int* grid, int* variant, int* cluster,
+cudaError_t launch_qweight(QweightParams& p, const QweightDevice& dev, int* grid, int* variant, int* cluster,
                            cudaStream_t s) {
+    // Up to 32 tokens a CTA; more are further tiles, whose weights come from L2 (64 tokens in one tile
+    // need 200 registers a thread: spilled to 128 they took 139 us at R = 8, N = 7168, K = 2048).
     const int tt = p.M <= 8 ? 1 : p.M <= 16 ? 2 : 4;
-    const int tok = tt * 8;
+    const int tok = tt * 8, wsteps = 1 << (p.group_shift - 5);
+    const HostShape shape = tt == 1 ? host_shape<1>() : tt == 2 ? host_shape<2>() : host_shape<4>();
+    const int rows = shape.rows, item = shape.item, ring = shape.ring, ld = shape.ld;
+    const bool own = tt >= 2;
+    const bool qx = p.qx && !p.xpow2;
+    const int shift = qx && p.xgroup_shift < p.group_shift ? p.xgroup_shift : p.group_shift;
     p.tiles_m = (p.M + tok - 1) / tok;
-    const int groups = (p.N + 15) / 16;
-    // Splits of a rank's K: those that leave the busiest CTA the fewest items (an item is 16 rows
-    // by 256 of K), where a split also costs about one item more to join.
-    const int items_k = (p.K + kItemK - 1) / kItemK;
+    const int64_t groups = (p.N + rows - 1) / rows;
+    p.rtoks = p.M < tok ? (p.M + 1) / 2 * 2 : tok;
+    const int slot = own ? 0 : p.rtoks * ld * 4;                // bytes of a group's sums beside the ring
+    const int most = own ? kWarps : 24;                         // groups a CTA has room for
+    // Splits of a rank's K: those that leave the busiest CTA the fewest items, where a CTA more in
+    // the cluster's sum counts as one, and its start and end as four.
+    const int items_k = (p.K + item - 1) / item;
     int64_t best = 0;
     for (int sp = 1; sp * p.R <= kMaxRanks && sp <= items_k; ++sp) {
-        const int64_t rounds = (int64_t)((groups + dev.clusters[sp * p.R] - 1) / dev.clusters[sp * p.R]) * p.tiles_m;
-        const int64_t cost = rounds * ((items_k + sp - 1) / sp) + sp;
-        if (sp == 1 || cost < best) {
+        const int per = (items_k + sp - 1) / sp;
+        if ((items_k + per - 1) / per != sp) continue;  // a split would be empty
+        const int resident = dev.clusters[sp * p.R];
+        int64_t run = own ? kWarps : (groups * p.tiles_m + resident - 1) / resident;
+        if (run > most) run = most;
+        const int64_t waves = ((groups + run - 1) / run * p.tiles_m + resident - 1) / resident;
+        const int64_t cost = waves * (run * per + 4) + sp;
+        if (best == 0 || cost < best) {
             best = cost;
             p.splits = sp;
+            p.split_k = per * item;
+            p.run = (int)run;
         }
     }
-    *cluster = p.R * p.splits;
-    p.split_k = (items_k + p.splits - 1) / p.splits * kItemK;
-    // Groups a cluster: an even share for every resident cluster, as far as their sums fit shared memory.
-    const int slot = tok * kRedLd * 4;
-    const int most = 36 * 1024 / slot - kWarps;
-    p.run = (groups + dev.clusters[*cluster] - 1) / dev.clusters[*cluster];
-    if (p.run > most) p.run = most;
-    // K tile: as long as the tokens fit what is left
-    const int xstep = kItemK * tok * 2 + (qx ? (kItemK >> p.xgroup_shift) * tok * 4 : 0);
-    const int room = (kMaxSmem - kRingBytes - (p.run + kWarps) * slot) / xstep;  // items of K
-    const int split_items = p.split_k / kItemK;
+    p.cluster = p.R * p.splits;
+    // K tile: at most `units` units of 8 k a thread, and as long as the tokens fit what the rest
+    // leaves; a multiple of an item and of 128
+    // (an item of 128 k holds its groups' scales whole: 128 is the largest group)
+    const int xstep = item * tok * 2 + (item >> shift) * tok * 4 + (qx ? item >> p.xgroup_shift : (item + 255) / 256) * tok * 4 +
+                      (item >> p.group_shift) * (p.run * rows + 1) * 4;
+    const int fixed = ring + 32 + (own ? 0 : (p.run + kWarps) * slot);
+    int room = (kMaxSmem - fixed) / xstep;
+    if (room > shape.units * 8 * kThreads / (tok * item)) room = shape.units * 8 * kThreads / (tok * item);
+    if (room < 1) return cudaErrorInvalidValue;
+    const int split_items = p.split_k / item;
     p.tiles_k = (split_items + room - 1) / room;
     const int tile_items = (split_items + p.tiles_k - 1) / p.tiles_k;
-    p.tile_k = tile_items * kItemK;
-    const size_t smem = (size_t)kRingBytes + (size_t)(p.run + kWarps) * slot + (size_t)tile_items * xstep;
+    p.tiles_k = (split_items + tile_items - 1) / tile_items;
+    p.tile_k = tile_items * item;
+    size_t smem = (size_t)fixed + (size_t)tile_items * xstep;
+    const size_t sums = own ? (size_t)kWarps * p.rtoks * ld * 4 : 0;
+    if (smem < sums) smem = sums;
 
-    const int runs = (groups + p.run - 1) / p.run;
-    *grid = runs * p.tiles_m * *cluster;
+    const int64_t runs = (groups + p.run - 1) / p.run;
+    *cluster = p.cluster;
+    *grid = (int)(runs * p.tiles_m * p.cluster);
     *variant = tt;
-    const int shift = qx && p.xgroup_shift < p.group_shift ? p.xgroup_shift : p.group_shift;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    cluster_config(cfg, attr, *cluster, smem);
+    cluster_config(cfg, attr, p.cluster, smem);
     cfg.gridDim = dim3((unsigned)*grid);
     cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, kernel_of(tt, qx, 1 << (p.group_shift - 5), 1 << (shift - 5)), p);
+    return cudaLaunchKernelEx(&cfg, kernel_of(tt, qx, wsteps, 1 << (shift - 5)), p);
 }
 
 }  // namespace are
