@@ -281,6 +281,13 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
         }
     };
 
+    if (threadIdx.x < 2) bad[threadIdx.x] = 0u;
+    if (toks < TOK) {  // tokens that do not exist: zeros, which no tile overwrites
+        for (int u = threadIdx.x; u < TOK * p.tile_k / 8; u += kThreads)
+            *reinterpret_cast<uint4*>(xs + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+        for (int u = threadIdx.x; u < p.tile_k / GRAIN * TOK; u += kThreads) xsum[u] = 0.f;
+        for (int u = threadIdx.x; u < frows * TOK; u += kThreads) xsc[u] = 0.f;
+    }
     ptx::grid_launch_dependents();
     ptx::grid_wait();
     fetch(ring);
@@ -288,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
 
     // ---- a K tile's tokens and weight scales into shared memory.  A warp takes a token's 256 k at a time, a unit of 8 k a
     // lane; its (at most UNITS) loads are in flight together.
-    int tokp = 1;
-    while (tokp < toks) tokp <<= 1;
+    int tokp = 1, toksh = 0;
+    while (tokp < toks) tokp <<= 1, ++toksh;
     // The rows' scales and zero points: neighbouring lanes take a row's neighbouring groups (lanes on rows
     // of their own would touch a sector each with every load); what does not exist weighs nothing.
     constexpr int WUNITS = 16;
@@ -297,18 +304,25 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
     const int tg = p.tile_k >> p.group_shift;
     int tsh = 0;
     while (1 << tsh < tg) ++tsh;
-    const int wunits = p.run * ROWS << tsh;
+    // a thread's group of the tile is fixed; its rows are wstep apart
+    const int wgi = threadIdx.x & ((1 << tsh) - 1), wrow = threadIdx.x >> tsh, wstep = kThreads >> tsh;
+    const int wleft = min(p.run * ROWS, p.N - group0 * ROWS);
+    const int64_t wat = (int64_t)(group0 * ROWS + wrow) * p.groups + wgi, wjump = (int64_t)wstep * p.groups;
     uint32_t sv[WUNITS], zv[WUNITS];
-    auto load_scales = [&](int t0, int u0) {
+    auto load_scales = [&](int t0, int round) {
+        const bool on = wgi < tg && (t0 >> p.group_shift) + wgi < p.groups;
+        const int64_t at = wat + (t0 >> p.group_shift) + round * WUNITS * wjump;
+        const uint16_t* sp = p.scale[r] + at;
+        const uint8_t* zp = p.zero[r] + at;
 #pragma unroll
         for (int j = 0; j < WUNITS; ++j) {
-            const int u = u0 + j * kThreads, gi = u & ((1 << tsh) - 1), n = group0 * ROWS + (u >> tsh);
+            const bool in = on && wrow + (round * WUNITS + j) * wstep < wleft;
             sv[j] = 0u;
             zv[j] = 8u;
-            const bool in = u < wunits && n < p.N && gi < tg && (t0 >> p.group_shift) + gi < p.groups;
-            const int64_t at = (int64_t)n * p.groups + (t0 >> p.group_shift) + gi;
-            ldg_u16_if(sv[j], p.scale[r] + at, in);
-            ldg_u8_if(zv[j], p.zero[r] + at, in && zeros);
+            ldg_u16_if(sv[j], sp, in);
+            ldg_u8_if(zv[j], zp, in && zeros);
+            sp += wjump;
+            zp += wjump;
         }
     };
     auto stage = [&](int tl) {
@@ -318,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
             v[j] = make_uint4(0u, 0u, 0u, 0u);
-            const int i = warp + j * kWarps, m = i & (tokp - 1), k = t0 + i / tokp * 256 + lane * 8;
+            const int i = warp + j * kWarps, m = i & (tokp - 1), k = t0 + (i >> toksh) * 256 + lane * 8;
             const bool in = i < todo && m < toks && k < kend;
             const int64_t at = (int64_t)(m0 + m) * p.K + k;
             if (QX || p.qx) {
@@ -331,59 +345,88 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
                 ldg_if(v[j], static_cast<const uint16_t*>(p.x[r]) + at, in);
             }
         }
-        load_scales(t0, threadIdx.x);  // in flight with the tokens
-        if (tl) __syncthreads();       // every warp is done with the tile before
+        load_scales(t0, 0);            // in flight with the tokens
+        __syncthreads();               // every warp is done with the tile before (first: with clearing)
+        // two rows at a time, so that one's steps fill the waits of the other's
 #pragma unroll
-        for (int j = 0; j < UNITS; ++j) {
-            const int i = warp + j * kWarps;
-            if (i >= todo) break;
-            const int m = i & (tokp - 1), k = i / tokp * 256 + lane * 8;  // within the tile
-            if (m >= toks || i / tokp * 256 >= p.tile_k) continue;
-            float x[8];  // even and odd k: 0 2 4 6 1 3 5 7
-            if (QX) {
-                const float2 e[4] = {fp8x2_to_float2(v[j].x), fp8x2_to_float2(v[j].x >> 16), fp8x2_to_float2(v[j].y),
-                                     fp8x2_to_float2(v[j].y >> 16)};
+        for (int j0 = 0; j0 < UNITS; j0 += 2) {
+            if (warp + j0 * kWarps >= todo) break;
+            float x[2][8], sum[2];  // the even k, 0 2 4 6, times 1; and the odd
+            int m[2], k[2];         // k within the tile
+            bool in[2];
+            uint32_t top[2] = {0u, 0u};
 #pragma unroll
-                for (int e4 = 0; e4 < 4; ++e4) {
-                    x[e4] = e[e4].x;
-                    x[4 + e4] = e[e4].y;
-                }
-            } else {
-                if (p.qx) v[j] = codes_to_bf16(v[j]);
-                // the largest exponent
-                uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-                uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7F807F80u, w[1] & 0x7F807F80u), __vmaxu2(w[2] & 0x7F807F80u, w[3] & 0x7F807F80u));
-                top = __reduce_max_sync(0xFFFFFFFFu, max(top >> 23, top >> 7 & 0xFFu));
-                if (top == 255u) {  // values that are not finite: zeros here, and the token is noted
-                    if (lane == 0) atomicOr(&bad[m >> 5], 1u << (m & 31));
-                    top = 0u;
+            for (int e = 0; e < 2; ++e) {
+                const int i = warp + (j0 + e) * kWarps;
+                m[e] = i & (tokp - 1);
+                k[e] = (i >> toksh) * 256 + lane * 8;
+                in[e] = i < todo && m[e] < toks && k[e] < p.tile_k;
+                uint4& w = v[j0 + e];
+                if (QX) {
+                    const float2 f[4] = {fp8x2_to_float2(w.x), fp8x2_to_float2(w.x >> 16), fp8x2_to_float2(w.y), fp8x2_to_float2(w.y >> 16)};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0x0000FFFFu;
-                        if ((w[e] & 0x00007F80u) == 0x00007F80u) w[e] &= 0xFFFF0000u;
-                        top = __vmaxu2(top, w[e] & 0x7F807F80u);
+                    for (int i4 = 0; i4 < 4; ++i4) {
+                        x[e][i4] = f[i4].x;
+                        x[e][4 + i4] = f[i4].y;
                     }
-                    top = __reduce_max_sync(0xFFFFFFFFu, max(top >> 23, top >> 7 & 0xFFu));
-                }
-                const float mul = scale_of(top);
-                if (lane == 0) xsc[(k >> 8) * TOK + m] = unscale_of(top) * 0x1p12f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[e] = bf_lo(w[e]) * mul;
-                    x[4 + e] = bf_hi(w[e]) * mul;
+                } else {
+                    if (p.qx) w = codes_to_bf16(w);
+                    top[e] = __vmaxu2(__vmaxu2(w.x & 0x7F807F80u, w.y & 0x7F807F80u), __vmaxu2(w.z & 0x7F807F80u, w.w & 0x7F807F80u));
                 }
             }
-            // step st = 32 k, or lane c's word st of 128 k
-            const int st = WIDE ? (k >> 7) * 4 + (lane & 3) : k >> 5, c4 = WIDE ? lane >> 2 & 3 : lane & 3;
-            if (k < p.tile_k)
-                *reinterpret_cast<uint4*>(xs + (((st * TT + (m >> 3)) * 8 + (m & 7)) * 4 + c4) * 16) =
-                    make_uint4(f16x2(x[0], x[2]), f16x2(x[4] * 0.0625f, x[6] * 0.0625f), f16x2(x[1], x[3]),
-                               f16x2(x[5] * 0.0625f, x[7] * 0.0625f));
-            // sum x over each GRAIN of k, in the weights' unit
-            float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+            if (!QX) {
+                // the largest exponents
 #pragma unroll
-            for (int o = 1; o < GRAIN / 8; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-            if ((lane & (GRAIN / 8 - 1)) == 0 && k < p.tile_k) xsum[k / GRAIN * TOK + m] = sum * 0x1p-24f;
+                for (int e = 0; e < 2; ++e) top[e] = __reduce_max_sync(0xFFFFFFFFu, max(top[e] >> 23, top[e] >> 7 & 0xFFu));
+                if (top[0] == 255u || top[1] == 255u) {
+                    // values that are not finite: zeros here, and their tokens are noted
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (top[e] != 255u) continue;
+                        if (lane == 0) atomicOr(&bad[m[e] >> 5], 1u << (m[e] & 31));
+                        uint32_t* w = &v[j0 + e].x;
+                        uint32_t t = 0u;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0x0000FFFFu;
+                            if ((w[i] & 0x00007F80u) == 0x00007F80u) w[i] &= 0xFFFF0000u;
+                            t = __vmaxu2(t, w[i] & 0x7F807F80u);
+                        }
+                        top[e] = __reduce_max_sync(0xFFFFFFFFu, max(t >> 23, t >> 7 & 0xFFu));
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float mul = scale_of(top[e]);
+                    const uint32_t w[4] = {v[j0 + e].x, v[j0 + e].y, v[j0 + e].z, v[j0 + e].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[e][i] = bf_lo(w[i]) * mul;
+                        x[e][4 + i] = bf_hi(w[i]) * mul;
+                    }
+                    // (a row's first lane is in the tile wherever the row has a lane in it)
+                    if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = unscale_of(top[e]) * 0x1p12f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // step st = 32 k, or lane c's word st of 128 k
+                const int st = WIDE ? (k[e] >> 7) * 4 + (lane & 3) : k[e] >> 5, c4 = WIDE ? lane >> 2 & 3 : lane & 3;
+                const float(&y)[8] = x[e];
+                if (in[e])
+                    *reinterpret_cast<uint4*>(xs + (((st * TT + (m[e] >> 3)) * 8 + (m[e] & 7)) * 4 + c4) * 16) =
+                        make_uint4(f16x2(y[0], y[2]), f16x2(y[4] * 0.0625f, y[6] * 0.0625f), f16x2(y[1], y[3]),
+                                   f16x2(y[5] * 0.0625f, y[7] * 0.0625f));
+                sum[e] = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+            }
+            // sum x over each GRAIN of k, in the weights' unit
+#pragma unroll
+            for (int o = 1; o < GRAIN / 8; o <<= 1)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], o);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if ((lane & (GRAIN / 8 - 1)) == 0 && in[e]) xsum[k[e] / GRAIN * TOK + m[e]] = sum[e] * 0x1p-24f;
         }
         if (QX) {
             const int x0 = t0 >> p.xgroup_shift;
@@ -393,25 +436,16 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
                 xsc[u] = in ? __ldg(static_cast<const float*>(p.xscale[r]) + (int64_t)(m0 + m) * p.xgroups + x0 + gi) : 0.f;
             }
         }
-        for (int u0 = threadIdx.x; u0 < wunits; u0 += WUNITS * kThreads) {
-            if (u0 != threadIdx.x) load_scales(t0, u0);
+        for (int round = 0; round * WUNITS * wstep < p.run * ROWS; ++round) {
+            if (round) load_scales(t0, round);
+            uint32_t* to = wsc + wgi * wrows + wrow + round * WUNITS * wstep;
 #pragma unroll
-            for (int j = 0; j < WUNITS; ++j) {
-                const int u = u0 + j * kThreads, gi = u & ((1 << tsh) - 1);
-                if (u < wunits && gi < tg) wsc[gi * wrows + (u >> tsh)] = sv[j] | (__float_as_uint((float)zv[j]) & 0xFFFF0000u);  // 0..255: exact in bf16
-            }
+            for (int j = 0; j < WUNITS; ++j)
+                if (wgi < tg && wrow + (round * WUNITS + j) * wstep < p.run * ROWS)
+                    to[j * wstep] = sv[j] | (__float_as_uint((float)zv[j]) & 0xFFFF0000u);  // 0..255: exact in bf16
         }
         __syncthreads();
     };
-    if (threadIdx.x < 2) bad[threadIdx.x] = 0u;
-    if (toks < TOK) {  // tokens that do not exist: zeros, which no tile overwrites
-        for (int u = threadIdx.x; u < TOK * p.tile_k / 8; u += kThreads)
-            *reinterpret_cast<uint4*>(xs + u * 16) = make_uint4(0u, 0u, 0u, 0u);
-        for (int u = threadIdx.x; u < p.tile_k / GRAIN * TOK; u += kThreads) xsum[u] = 0.f;
-        for (int u = threadIdx.x; u < frows * TOK; u += kThreads) xsc[u] = 0.f;
-    }
-    __syncthreads();
-
     float acc[RT][TT][4];
 #pragma unroll
     for (int a = 0; a < RT; ++a)
