@@ -15,11 +15,13 @@
 //    (Codes made into integers in fp16 take 9 instructions a word and in bf16
 //    11; FP8 operands would take 3, but FP8 mma.sync is not native here: it
 //    measured 36 cycles a sub-core for 32 of k, fp16 8.2 for 16.)
-//  * FP8 tokens are exact in fp16.  bf16 tokens, and FP8 ones with power-of-two
-//    scales, are scaled, per token and 256 of k, by the power of two that takes
-//    the largest to 2^14..2^15, which their scale in fp32 undoes: what is 2^-27
-//    times the largest or more stays exact, what is smaller is off by at most
-//    2^-35 of the largest, below the fp32 sums' own rounding.
+//  * FP8 tokens are exact in fp16, and so are FP8 ones times power-of-two
+//    scales relative to their 256 of k's largest (what is 2^-30 below it is
+//    off by at most 2^-34 of it).  bf16 tokens are scaled, per token and 256 of
+//    k, by the power of two that takes the largest to 2^14..2^15, which their
+//    scale in fp32 undoes: what is 2^-27 times the largest or more stays exact,
+//    what is smaller is off by at most 2^-35 of it, below the fp32 sums' own
+//    rounding.
 //  * The zero point leaves the sums: sum (u - z) x = sum u x - z sum x, with
 //    sum x per token and group in fp32.  The scales are applied in fp32, once
 //    per group, to the tensor instruction's fp32 sums.  No weight is rounded.
@@ -148,6 +150,12 @@ __device__ __forceinline__ float e8m0_to_float(uint32_t b) {
     return __uint_as_float(b == 255u ? 0x7FC00000u : b == 0u ? 0x00400000u : b << 23);
 }
 
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 h2_of(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+__device__ __forceinline__ uint32_t fp8x2_to_f16x2(uint32_t v) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 // Two floats of tokens as fp16.
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -156,18 +164,6 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 __device__ __forceinline__ float2 fp8x2_to_float2(uint32_t v) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-// 8 FP8 codes (x, y) times a power of two (z, E8M0) as bf16: exact from 2^-133 on.
-__device__ __forceinline__ uint4 codes_to_bf16(uint4 v) {
-    const float f = e8m0_to_float(v.z);
-    const float2 e[4] = {fp8x2_to_float2(v.x), fp8x2_to_float2(v.x >> 16), fp8x2_to_float2(v.y), fp8x2_to_float2(v.y >> 16)};
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(e[i].x * f, e[i].y * f);
-        w[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -348,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
         load_scales(t0, 0);            // in flight with the tokens
         __syncthreads();               // every warp is done with the tile before (first: with clearing)
         // two rows at a time, so that one's steps fill the waits of the other's
+        if (QX || !p.qx)
 #pragma unroll
         for (int j0 = 0; j0 < UNITS; j0 += 2) {
             if (warp + j0 * kWarps >= todo) break;
@@ -370,7 +367,6 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
                         x[e][4 + i4] = f[i4].y;
                     }
                 } else {
-                    if (p.qx) w = codes_to_bf16(w);
                     top[e] = __vmaxu2(__vmaxu2(w.x & 0x7F807F80u, w.y & 0x7F807F80u), __vmaxu2(w.z & 0x7F807F80u, w.w & 0x7F807F80u));
                 }
             }
@@ -420,6 +416,46 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
                 sum[e] = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
             }
             // sum x over each GRAIN of k, in the weights' unit
+#pragma unroll
+            for (int o = 1; o < GRAIN / 8; o <<= 1)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], o);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if ((lane & (GRAIN / 8 - 1)) == 0 && in[e]) xsum[k[e] / GRAIN * TOK + m[e]] = sum[e] * 0x1p-24f;
+        }
+        // FP8 codes under power-of-two scales: in fp16, times the scale over the row's largest and 2^6
+        if (!QX && p.qx)
+#pragma unroll
+        for (int j0 = 0; j0 < UNITS; j0 += 2) {
+            if (warp + j0 * kWarps >= todo) break;
+            float sum[2];
+            int m[2], k[2];
+            bool in[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = warp + (j0 + e) * kWarps;
+                m[e] = i & (tokp - 1);
+                k[e] = (i >> toksh) * 256 + lane * 8;
+                in[e] = i < todo && m[e] < toks && k[e] < p.tile_k;
+                const uint4 w = v[j0 + e];
+                const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, w.z == 255u ? 0u : w.z);
+                // 2^(z - top + 6): below 2^-24 it is nothing; a NaN scale
+                const uint32_t d = top - w.z;
+                const uint32_t mul = w.z == 255u ? 0x7FFFu : d <= 20u ? (21u - d) << 10 : d <= 30u ? 0x400u >> (d - 20u) : 0u;
+                const __half2 mul2 = h2_of(mul * 0x10001u), odd2 = __hmul2(mul2, __float2half2_rn(0.0625f));
+                const uint32_t h[4] = {fp8x2_to_f16x2(w.x), fp8x2_to_f16x2(w.x >> 16), fp8x2_to_f16x2(w.y), fp8x2_to_f16x2(w.y >> 16)};
+                const __half2 y0 = __hmul2(h2_of(__byte_perm(h[0], h[2], 0x5410)), mul2), y1 = __hmul2(h2_of(__byte_perm(h[0], h[2], 0x7632)), odd2);
+                const __half2 y2 = __hmul2(h2_of(__byte_perm(h[1], h[3], 0x5410)), mul2), y3 = __hmul2(h2_of(__byte_perm(h[1], h[3], 0x7632)), odd2);
+                const int st = WIDE ? (k[e] >> 7) * 4 + (lane & 3) : k[e] >> 5, c4 = WIDE ? lane >> 2 & 3 : lane & 3;
+                if (in[e])
+                    *reinterpret_cast<uint4*>(xs + (((st * TT + (m[e] >> 3)) * 8 + (m[e] & 7)) * 4 + c4) * 16) =
+                        make_uint4(h2_bits(y0), h2_bits(y1), h2_bits(y2), h2_bits(y3));
+                const float2 f0 = __half22float2(y0), f1 = __half22float2(y1), f2 = __half22float2(y2), f3 = __half22float2(y3);
+                sum[e] = ((f0.x + f0.y) + (f2.x + f2.y)) + ((f1.x + f1.y) + (f3.x + f3.y)) * 16.f;
+                // 2^(top - 127) / 2^6 * 2^12 (above 2^127: such tokens overflow fp32 themselves)
+                if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = e8m0_to_float(top) * 64.f;
+            }
 #pragma unroll
             for (int o = 1; o < GRAIN / 8; o <<= 1)
 #pragma unroll
@@ -645,11 +681,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
                     const int rj = j / p.splits, k0 = j % p.splits * p.split_k, k1 = min(p.K, k0 + p.split_k);
                     const int64_t row = (int64_t)(m0 + m) * p.K;
                     for (int k = k0; k < k1; ++k) {
-                        float xv;
-                        if (p.qx)
-                            xv = fp8x2_to_float2(__ldg(static_cast<const uint8_t*>(p.x[rj]) + row + k)).x *
-                                 e8m0_to_float(__ldg(static_cast<const uint8_t*>(p.xscale[rj]) + (int64_t)(m0 + m) * p.xgroups + (k >> p.xgroup_shift)));
-                        else xv = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p.x[rj]) + row + k) << 16);
+                        const float xv = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p.x[rj]) + row + k) << 16);
                         if ((__float_as_uint(xv) & 0x7F800000u) != 0x7F800000u) continue;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {

@@ -235,3 +235,30 @@ def test_tokens_of_any_magnitude(ws):
     y, _ = run(ws, x, w, 128)
     want, tol = ref.linear64(x, w, 128)
     ref.check(y, want, tol + 2.0 ** -133, "out")  # bf16's smallest step
+
+
+@pytest.mark.parametrize("M", [1, 9, 40])
+def test_power_of_two_scales_of_any_size(ws, M):
+    """E8M0 token scales that differ by 2^40 within a row, the smallest and large ones, NaN scales and NaN codes."""
+    R, N, K, group = 2, 72, 544, 128
+    w, g = weights(R, N, K, group, True, 21 + M)
+    qw = [are.QWeight(*t, group) for t in w]
+    xq = [torch.randint(0, 256, (M, K), generator=g, device="cuda", dtype=torch.uint8) for _ in range(R)]
+    for q in xq:
+        q[(q & 0x7F) == 0x7F] = 0x38
+    xs = [torch.randint(107, 148, (M, 17), generator=g, device="cuda", dtype=torch.uint8) for _ in range(R)]
+    xs[0][0, :9] = 3            # 2^-124
+    xs[1][0, :] = 5
+    xs[0][M // 2, 11] = 230     # 2^103
+    nan = []
+    if M > 1:
+        xs[1][M - 1, 16] = 255  # the last, short group's scale is NaN
+        xq[0][1, 100] = 0xFF    # a NaN code
+        nan = [1, M - 1]
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    are.gemm_ar_qweight_qx(xq, xs, qw, out, ws, xgroup=32)
+    val = [q.view(torch.float8_e4m3fn).double() * ref.e8m0_value(f).repeat_interleave(32, -1)[:, :K] for q, f in zip(xq, xs)]
+    want, tol = ref.linear64(val, w, group)
+    keep = [i for i in range(M) if i not in nan]
+    assert out[nan].isnan().all()
+    ref.check(out[keep], want[keep], tol[keep] + 2.0 ** -133, "out")
