@@ -7,7 +7,12 @@
 //                                        +0.0, so an all -0.0 sum is +0.0)
 //   y = h * rsqrt(mean(h^2) + eps) * gamma
 //   per group of G columns: a = max|y|,  scale = a / 448 or a power of two,
-//   code = e4m3(y * (1 / scale))
+//   code = e4m3(y / scale)
+// With z = h * gamma, y / scale is z * 448 / max|z|: the code of the fp32 form
+// needs no inv, and two roundings (of 448 / max|z| and of the product, the
+// rounding error of z going in through an fma) decide it.  z is formed at the
+// size of y, h times the power of two below inv, so it leaves fp32's range only
+// where y does.
 // Backward (dy = sum_r dy_r the all-reduced output gradient, d_res the
 // gradient of the updated residual, inv = rsqrt(mean(h^2) + eps)):
 //   dh      = inv * dy * gamma - h * inv^3 * mean(dy * gamma * h) + d_res
@@ -156,14 +161,15 @@ __device__ __forceinline__ void produce(const Ring& g, const RowsParams& p) {
 template <bool ONE>
 __device__ __forceinline__ void sum_ranks(const uint8_t* at, int R, size_t step, float (&f)[8]) {
     unpack8(*reinterpret_cast<const uint4*>(at), f);
-    if (ONE) return;
+    if constexpr (!ONE) {
 #pragma unroll
-    for (int r = 1; r < kMaxRanks; ++r) {
-        if (r < R) {
-            float v[8];
-            unpack8(*reinterpret_cast<const uint4*>(at + r * step), v);
+        for (int r = 1; r < kMaxRanks; ++r) {
+            if (r < R) {
+                float v[8];
+                unpack8(*reinterpret_cast<const uint4*>(at + r * step), v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] += v[i];
+                for (int i = 0; i < 8; ++i) f[i] += v[i];
+            }
         }
     }
 }
@@ -180,27 +186,30 @@ __device__ __forceinline__ float red_total(const float* red, int nwarps) {
 }
 
 // ------------------------------------------------------------ quantised forward
-// Scale of a group whose largest |y| has the bit pattern `a` (finite), and the
-// factor that takes y to code range.
+// Scale of a group whose largest |z| is `top` and largest |y| = top * m is
+// finite (1 <= m < 2), and the factor that takes z to code range.
 struct GroupScale {
-    float inv;
+    float factor;
     uint32_t stored;  // fp32 bits, or the E8M0 byte
 };
 
 template <bool POW2>
-__device__ __forceinline__ GroupScale group_scale(uint32_t a) {
+__device__ __forceinline__ GroupScale group_scale(float top, float m) {
     GroupScale s;
+    const float a = top * m;
     if (POW2) {
         // the smallest power of two X with a / X <= 448 = 1.75 * 2^8, as a biased exponent >= 0
-        int e = (int)(a >> 23) - 8 + ((a & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-        e = a == 0 ? 127 : max(e, 0);
+        const uint32_t u = __float_as_uint(a);
+        int e = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+        e = u == 0 ? 127 : max(e, 0);
         s.stored = (uint32_t)e;
-        s.inv = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e), e <= 247
+        s.factor = m * __uint_as_float((uint32_t)(254 - e) << 23);  // m * 2^(127 - e), e <= 247: exact
     } else {
         // at least 2^-126, so that its reciprocal is finite
-        const float sc = a == 0 ? 1.f : fmaxf(__fdiv_rn(__uint_as_float(a), 448.f), 1.17549435e-38f);
-        s.stored = __float_as_uint(sc);
-        s.inv = __frcp_rn(sc);
+        const bool tiny = a < 448 * 1.17549435e-38f;
+        const float sc = tiny ? 1.17549435e-38f : __fdiv_rn(a, 448.f);
+        s.stored = __float_as_uint(a == 0.f ? 1.f : sc);
+        s.factor = tiny ? m * 8.50705917e37f : __fdiv_rn(448.f, top);
     }
     return s;
 }
@@ -267,7 +276,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
         ss = warp_sum(ss);
         if (lane == 0) red[w] = ss;
         consumer_bar(p.nt);
-        const float inv = rsqrtf(red_total(red, nwarps) * p.inv_n + p.eps);
+        // inv = two * m: a power of two (0 for 0, infinite for NaN) and 1 <= m < 2
+        const uint32_t inv = __float_as_uint(rsqrtf(red_total(red, nwarps) * p.inv_n + p.eps));
+        const float two = __uint_as_float(inv & 0x7F800000u), m = __uint_as_float((inv & 0x7FFFFFu) | 0x3F800000u);
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
             if (k < p.slices) {
@@ -281,13 +292,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
                     *reinterpret_cast<float4*>(&gk[0]) = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2);
                     *reinterpret_cast<float4*>(&gk[4]) = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2 + 1);
                 }
-                // largest |y| as a bit pattern: infinities and NaN sort above every finite value
+                // largest |z| as a bit pattern: infinities and NaN sort above every finite value
                 uint32_t a = 0;
                 if (in) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        h[k][i] = h[k][i] * inv * gk[i];
-                        a = max(a, __float_as_uint(h[k][i]) & 0x7FFFFFFFu);
+                        h[k][i] *= two;
+                        a = max(a, __float_as_uint(h[k][i] * gk[i]) & 0x7FFFFFFFu);
                     }
                 }
                 // a group is 4, 8 or 16 neighbouring lanes (p.nt is a multiple of 32)
@@ -295,14 +306,21 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
                 if (in) {
                     uint2 q;
                     uint32_t stored;
-                    if (a < 0x7F800000u) {
-                        const GroupScale gs = group_scale<POW2>(a);
+                    const float top = __uint_as_float(a);
+                    if (top * m <= 3.40282347e38f) {
+                        const GroupScale gs = group_scale<POW2>(top, m);
                         stored = gs.stored;
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float z = h[k][i] * gk[i];
+                            v[i] = fmaf(z, gs.factor, fmaf(h[k][i], gk[i], -z) * gs.factor);
+                        }
                         uint32_t c[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(
-                                make_float2(h[k][2 * i] * gs.inv, h[k][2 * i + 1] * gs.inv), __NV_SATFINITE, __NV_E4M3);
+                            c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]),
+                                                                      __NV_SATFINITE, __NV_E4M3);
                         q = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
                     } else {  // not finite: NaN codes under a NaN scale
                         stored = POW2 ? 0xFFu : 0x7FC00000u;

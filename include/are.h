@@ -469,12 +469,14 @@ typedef enum are_scale_format {
  *  out_scale    : [M, ceil(N / group)], fp32 or E8M0 bytes; aligned to its element
  *  Result       : y as in are_allreduce_rmsnorm (fp32, before its bf16
  *                 rounding); a = max |y| of the group;
- *                 ARE_SCALE_F32:  scale = a / 448, correctly rounded, at least 2^-126;
+ *                 ARE_SCALE_F32:  scale = a / 448, rounded to fp32, at least 2^-126;
  *                 ARE_SCALE_E8M0: scale = the smallest power of two, at least
  *                 2^-127, with a / scale <= 448;
  *                 1 for a group of zeros;
- *                 code = e4m3(y * (1 / scale)), the reciprocal and the product
- *                 rounded to fp32, then to nearest even, saturating to +-448.
+ *                 code = e4m3(y / scale), to nearest even, saturating to +-448;
+ *                 y / scale is formed in fp32, and for fp32 scales as
+ *                 h gamma * (448 / max |h gamma|), without the rounding of
+ *                 the stored scale.
  *                 A group that holds a value that is not finite has a NaN
  *                 scale and NaN codes.
  * Needs no capacity of the workspace but R <= R_max.
