@@ -38,6 +38,7 @@ struct are_ws {
     uint32_t* d_staging = nullptr;
     size_t staging_words = 0;
     QweightDevice qweight{};          // resident clusters of the 4-bit kernel
+    uint8_t* d_tokens = nullptr;      // staged tokens of the 4-bit kernel
     float* d_dgamma = nullptr;        // backward: the blocks' partial dgamma sums
     int ar_resident[kArMaxPpt + 1] = {0};
     uint64_t oneshot_max_bytes = 0;   // set at creation
@@ -97,6 +98,7 @@ void free_ws(are_ws* ws) {
     cudaFree(ws->d_pieces);
     cudaFree(ws->d_staging);
     cudaFree(ws->d_dgamma);
+    cudaFree(ws->d_tokens);
     cudaFree(ws->d_chunk_ctr);
     cudaFree(ws->d_cons);
     if (ws->h_chunk_gen) cudaFreeHost(ws->h_chunk_gen);
@@ -482,6 +484,7 @@ are_status are_workspace_create(are_ws** out, const are_caps* caps) {
         for (int ppt = 1; ppt <= kArMaxPpt; ++ppt) ws->ar_resident[ppt] = ar_rmsnorm_resident_blocks(ppt, ws->num_sms);
         if (e == cudaSuccess) e = ar_oneshot_prepare();
     }
+    if (e == cudaSuccess) e = cudaMalloc(&ws->d_tokens, caps->R_max * kQweightScratch);
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_dgamma, norm_backward_scratch_words(caps->N_max, ws->num_sms) * 4);
     if (e == cudaSuccess) e = rows_prepare();
     if (e == cudaSuccess) e = qweight_prepare(ws->qweight);
@@ -803,6 +806,8 @@ are_status qweight_call(const void* const x[], const void* const xscale[], int s
     p.M = (int)M;
     p.N = (int)N;
     p.K = (int)K;
+    p.status = ws->d_status;
+    p.timeout_ns = ws->timeout_ns;
     p.qx = qx;
     p.group_shift = log2_group(group);
     p.groups = (int)ceil_div(K, group);
@@ -812,7 +817,8 @@ are_status qweight_call(const void* const x[], const void* const xscale[], int s
         p.xpow2 = scale_format == ARE_SCALE_E8M0;
     }
     int grid = 0, variant = 0, cluster = 0;
-    const cudaError_t e = launch_qweight(p, ws->qweight, &grid, &variant, &cluster, s);
+    const cudaError_t e = launch_qweight(p, ws->qweight, ws->d_tokens, ws->caps.R_max * kQweightScratch, &grid, &variant,
+                                         &cluster, s);
     ws->last = are_launch_info{ARE_KERNEL_QWEIGHT, grid, 256, cluster, 0, variant, 0, 0};
     return from_cuda(e);
 }

@@ -138,7 +138,14 @@ struct QweightParams {
     int qx;                              // tokens in 8 bits
     int xgroup_shift, xgroups;           // of the token scales
     int xpow2;
+    DevStatus* status;
+    unsigned long long timeout_ns;
     // set by launch_qweight:
+    int kp;                              // K, up to whole 256
+    uint8_t* tokens;                     // staged tokens [R][tiles_m][kp / 32][tile]: fp16 operands
+    float* sums;                         // their sums [R][tiles_m][kp / shared group][tile]
+    float* scales;                       // their scales [R][tiles_m][kp / 256 or xgroup][tile]
+    uint32_t* flags;                     // [R][tiles_m][kp / 256]: tokens with a value that is not finite
     int cluster;                         // CTAs a cluster: R * splits
     int splits;                          // K splits of a rank
     int split_k;                         // K range of a split
@@ -154,9 +161,11 @@ struct QweightDevice {
 };
 
 cudaError_t qweight_prepare(QweightDevice& dev);
-// Chooses the launch shape and launches; `grid`, `variant` and `cluster` report it.
-cudaError_t launch_qweight(QweightParams& p, const QweightDevice& dev, int* grid, int* variant, int* cluster,
-                           cudaStream_t s);
+// Bytes of a rank's staged tokens: a tile of 32 of K = 28672 with groups of 32, or more of shorter rows.
+constexpr size_t kQweightScratch = 2u << 20;
+// Chooses the launch shape and launches (in parts, if `scratch` does not hold all tokens); `grid`, `variant` and `cluster` report it.
+cudaError_t launch_qweight(QweightParams& p, const QweightDevice& dev, uint8_t* scratch, size_t scratch_bytes, int* grid,
+                           int* variant, int* cluster, cudaStream_t s);
 
 // ------------------------------------------------------------------ GEMM + reduce
 constexpr int kBM = 128;

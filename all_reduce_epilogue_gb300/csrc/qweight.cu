@@ -41,6 +41,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "are_internal.h"
 #include "ptx.cuh"
 
@@ -64,7 +66,20 @@ struct Shape {
     static constexpr int SLOT = ROWS * PITCH;
     static constexpr int RING = kWarps * DEPTH * SLOT;
     static constexpr int LD = ROWS + 4;               // floats between a sum's tokens: 4 token pairs x 8 rows in 32 banks
-    static constexpr int UNITS = 8;                   // units of 8 k a thread stages of a K tile
+    static constexpr int UNITS = 8;                   // units of 8 k a thread stages of a K tile (TT = 1)
+};
+
+// Shared memory of the kernel for wide tiles, of each of its two buffers, and its K tile: 512 k where they fit.
+template <int TT, bool QX, int WSTEPS, int STEPS>
+struct Wide {
+    static constexpr int TILE = TT == 2 && WSTEPS >= 2 ? 512 : 256;
+    static constexpr int WROWS = kWarps * Shape<TT>::ROWS + 1;                 // odd: a row's groups fall into different banks
+    static constexpr int XS = 2 * Shape<TT>::TOK * TILE;                        // bytes
+    static constexpr int XSUM = TILE / (STEPS * 32) * Shape<TT>::TOK;           // words
+    static constexpr int XSC = QX ? XSUM : TILE / 256 * Shape<TT>::TOK;         // (a token group is STEPS * 32 or more)
+    static constexpr int WSC = TILE / (WSTEPS * 32) * WROWS;
+    static constexpr int SMEM = Shape<TT>::RING + 2 * XS + 8 * (XSUM + XSC + WSC) + 32;
+    static_assert(SMEM <= kMaxSmem && 8 * WSC % 16 == 0, "two CTAs an SM, barriers aligned");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -85,12 +100,12 @@ __device__ __forceinline__ void cp_wait() {
 // wait for the one before: 12 thousand cycles for 24 of them).
 __device__ __forceinline__ void ldg_if(uint4& v, const void* p, bool on) {
     asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
         : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
         : "l"(p), "r"((uint32_t)on));
 }
 __device__ __forceinline__ void ldg_if(uint2& v, const void* p, bool on) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.cg.v2.u32 {%0, %1}, [%2];\n\t}"
                  : "+r"(v.x), "+r"(v.y)
                  : "l"(p), "r"((uint32_t)on));
 }
@@ -100,7 +115,7 @@ __device__ __forceinline__ void ldg_u16_if(uint32_t& v, const void* p, bool on) 
                  : "l"(p), "r"((uint32_t)on));
 }
 __device__ __forceinline__ void ldg_u8_if(uint32_t& v, const void* p, bool on) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u8 %0, [%1];\n\t}"
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.cg.u8 %0, [%1];\n\t}"
                  : "+r"(v)
                  : "l"(p), "r"((uint32_t)on));
 }
@@ -111,6 +126,11 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(addr)
                  : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
@@ -126,6 +146,33 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Pairs of fp32, two of them an instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
     return v;
 }
 
@@ -187,16 +234,385 @@ __device__ __forceinline__ float unscale_of(uint32_t top) {
     return top == 0u ? 1.f : top < 15u ? __uint_as_float(0x00400000u) : __uint_as_float((top - 14u) << 23);
 }
 
-// TT: token tiles of 8.  QX: tokens in 8 bits with fp32 scales, which are applied
-// with the weights' (power-of-two scales go into the staged tokens, exactly).
+// Tokens m0 .. m0 + toks of rank r, k from t0 to kend, as a tile of `tile_k` k in the order of the tensor
+// instruction's operands, with their sums and scales; tokens up to `rows` are written, those that do
+// not exist as zeros.  A warp takes a token's 256 k at a time, a unit of 8 k a lane; its (at most UNITS)
+// loads are in flight together with those of `between`.
+//   xs   : [k / 32][TT][lane] units of 8 k in fp16
+//   xsum : [k / GRAIN][TOK] sum x * 2^-24
+//   xsc  : [k / 256, or k / xgroup with QX][TOK] the tokens' scales
+//   bad  : bit m: token m has a value that is not finite
+template <int TT, bool QX, bool WIDE, int GRAIN, int UNITS, typename Between>
+__device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int m0, int rows, int toks, int t0, int kend,
+                                             int tile_k, uint8_t* xs, float* xsum, float* xsc, uint32_t* bad,
+                                             Between between) {
+    constexpr int TOK = TT * 8;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
+    int tokp = 1, toksh = 0;
+    while (tokp < rows) tokp <<= 1, ++toksh;
+    const int todo = ((tile_k + 255) >> 8) * tokp;  // (256 k, token) rows, the token innermost
+    uint4 v[UNITS];
+#pragma unroll
+    for (int j = 0; j < UNITS; ++j) {
+        v[j] = make_uint4(0u, 0u, 0u, 0u);
+        const int i = warp + j * kWarps, m = i & (tokp - 1), k = t0 + (i >> toksh) * 256 + lane * 8;
+        const bool in = i < todo && m < toks && k < kend;
+        const int64_t at = (int64_t)(m0 + m) * p.K + k;
+        if (QX || p.qx) {
+            uint2 b = make_uint2(0u, 0u);
+            ldg_if(b, static_cast<const uint8_t*>(p.x[r]) + at, in);
+            v[j].x = b.x;
+            v[j].y = b.y;
+            if (!QX) ldg_u8_if(v[j].z, static_cast<const uint8_t*>(p.xscale[r]) + (int64_t)(m0 + m) * p.xgroups + (k >> p.xgroup_shift), in);
+        } else {
+            ldg_if(v[j], static_cast<const uint16_t*>(p.x[r]) + at, in);
+        }
+    }
+    between();
+    // two rows at a time, so that one's steps fill the waits of the other's
+    if (QX || !p.qx)
+#pragma unroll
+    for (int j0 = 0; j0 < UNITS; j0 += 2) {
+        if (warp + j0 * kWarps >= todo) break;
+        float x[2][8], sum[2];  // the even k, 0 2 4 6, times 1; and the odd
+        int m[2], k[2];         // k within the tile
+        bool in[2];
+        uint32_t top[2] = {0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = warp + (j0 + e) * kWarps;
+            m[e] = i & (tokp - 1);
+            k[e] = (i >> toksh) * 256 + lane * 8;
+            in[e] = i < todo && m[e] < rows && k[e] < tile_k;
+            uint4& w = v[j0 + e];
+            if (QX) {
+                const float2 f[4] = {fp8x2_to_float2(w.x), fp8x2_to_float2(w.x >> 16), fp8x2_to_float2(w.y), fp8x2_to_float2(w.y >> 16)};
+#pragma unroll
+                for (int i4 = 0; i4 < 4; ++i4) {
+                    x[e][i4] = f[i4].x;
+                    x[e][4 + i4] = f[i4].y;
+                }
+            } else {
+                top[e] = __vmaxu2(__vmaxu2(w.x & 0x7F807F80u, w.y & 0x7F807F80u), __vmaxu2(w.z & 0x7F807F80u, w.w & 0x7F807F80u));
+            }
+        }
+        if (!QX) {
+            // the largest exponents
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top[e] = __reduce_max_sync(0xFFFFFFFFu, max(top[e] >> 23, top[e] >> 7 & 0xFFu));
+            if (top[0] == 255u || top[1] == 255u) {
+                // values that are not finite: zeros here, and their tokens are noted
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (top[e] != 255u) continue;
+                    if (lane == 0) atomicOr(bad, 1u << m[e]);
+                    uint32_t* w = &v[j0 + e].x;
+                    uint32_t t = 0u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0x0000FFFFu;
+                        if ((w[i] & 0x00007F80u) == 0x00007F80u) w[i] &= 0xFFFF0000u;
+                        t = __vmaxu2(t, w[i] & 0x7F807F80u);
+                    }
+                    top[e] = __reduce_max_sync(0xFFFFFFFFu, max(t >> 23, t >> 7 & 0xFFu));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float mul = scale_of(top[e]);
+                const uint32_t w[4] = {v[j0 + e].x, v[j0 + e].y, v[j0 + e].z, v[j0 + e].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[e][i] = bf_lo(w[i]) * mul;
+                    x[e][4 + i] = bf_hi(w[i]) * mul;
+                }
+                // (a row's first lane is in the tile wherever the row has a lane in it)
+                if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = unscale_of(top[e]) * 0x1p12f;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            // step st = 32 k, or lane c's word st of 128 k
+            const int st = WIDE ? (k[e] >> 7) * 4 + (lane & 3) : k[e] >> 5, c4 = WIDE ? lane >> 2 & 3 : lane & 3;
+            const float(&y)[8] = x[e];
+            if (in[e])
+                *reinterpret_cast<uint4*>(xs + (((st * TT + (m[e] >> 3)) * 8 + (m[e] & 7)) * 4 + c4) * 16) =
+                    make_uint4(f16x2(y[0], y[2]), f16x2(y[4] * 0.0625f, y[6] * 0.0625f), f16x2(y[1], y[3]),
+                               f16x2(y[5] * 0.0625f, y[7] * 0.0625f));
+            sum[e] = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+        }
+        // sum x over each GRAIN of k, in the weights' unit
+#pragma unroll
+        for (int o = 1; o < GRAIN / 8; o <<= 1)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], o);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if ((lane & (GRAIN / 8 - 1)) == 0 && in[e]) xsum[k[e] / GRAIN * TOK + m[e]] = sum[e] * 0x1p-24f;
+    }
+    // FP8 codes under power-of-two scales: in fp16, times the scale over the row's largest and 2^6
+    if (!QX && p.qx)
+#pragma unroll
+    for (int j0 = 0; j0 < UNITS; j0 += 2) {
+        if (warp + j0 * kWarps >= todo) break;
+        float sum[2];
+        int m[2], k[2];
+        bool in[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = warp + (j0 + e) * kWarps;
+            m[e] = i & (tokp - 1);
+            k[e] = (i >> toksh) * 256 + lane * 8;
+            in[e] = i < todo && m[e] < rows && k[e] < tile_k;
+            const uint4 w = v[j0 + e];
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, w.z == 255u ? 0u : w.z);
+            // 2^(z - top + 6): below 2^-24 it is nothing; a NaN scale
+            const uint32_t d = top - w.z;
+            const uint32_t mul = w.z == 255u ? 0x7FFFu : d <= 20u ? (21u - d) << 10 : d <= 30u ? 0x400u >> (d - 20u) : 0u;
+            const __half2 mul2 = h2_of(mul * 0x10001u), odd2 = __hmul2(mul2, __float2half2_rn(0.0625f));
+            const uint32_t h[4] = {fp8x2_to_f16x2(w.x), fp8x2_to_f16x2(w.x >> 16), fp8x2_to_f16x2(w.y), fp8x2_to_f16x2(w.y >> 16)};
+            const __half2 y0 = __hmul2(h2_of(__byte_perm(h[0], h[2], 0x5410)), mul2), y1 = __hmul2(h2_of(__byte_perm(h[0], h[2], 0x7632)), odd2);
+            const __half2 y2 = __hmul2(h2_of(__byte_perm(h[1], h[3], 0x5410)), mul2), y3 = __hmul2(h2_of(__byte_perm(h[1], h[3], 0x7632)), odd2);
+            const int st = WIDE ? (k[e] >> 7) * 4 + (lane & 3) : k[e] >> 5, c4 = WIDE ? lane >> 2 & 3 : lane & 3;
+            if (in[e])
+                *reinterpret_cast<uint4*>(xs + (((st * TT + (m[e] >> 3)) * 8 + (m[e] & 7)) * 4 + c4) * 16) =
+                    make_uint4(h2_bits(y0), h2_bits(y1), h2_bits(y2), h2_bits(y3));
+            const float2 f0 = __half22float2(y0), f1 = __half22float2(y1), f2 = __half22float2(y2), f3 = __half22float2(y3);
+            sum[e] = ((f0.x + f0.y) + (f2.x + f2.y)) + ((f1.x + f1.y) + (f3.x + f3.y)) * 16.f;
+            // 2^(top - 127) / 2^6 * 2^12 (above 2^127: such tokens overflow fp32 themselves)
+            if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = e8m0_to_float(top) * 64.f;
+        }
+#pragma unroll
+        for (int o = 1; o < GRAIN / 8; o <<= 1)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], o);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if ((lane & (GRAIN / 8 - 1)) == 0 && in[e]) xsum[k[e] / GRAIN * TOK + m[e]] = sum[e] * 0x1p-24f;
+    }
+    if (QX) {
+        const int x0 = t0 >> p.xgroup_shift;
+        for (int u = threadIdx.x; u < (tile_k >> p.xgroup_shift) * TOK; u += kThreads) {
+            const int m = u % TOK, gi = u / TOK;
+            const bool in = m < toks && x0 + gi < p.xgroups;
+            xsc[u] = in ? __ldcg(static_cast<const float*>(p.xscale[r]) + (int64_t)(m0 + m) * p.xgroups + x0 + gi) : 0.f;
+        }
+    }
+}
+
+// The tokens of a launch, staged once for all CTAs that read them: CTA (rank, token tile, 256 k).
+template <int TT, bool QX, int STEPS>
+__global__ void __launch_bounds__(kThreads) qweight_tokens_kernel(const __grid_constant__ QweightParams p) {
+    constexpr int TOK = TT * 8, GRAIN = STEPS * 32;
+    __shared__ uint32_t bad;
+    if (threadIdx.x == 0) bad = 0u;
+    const int chunks = p.kp >> 8, chunk = (int)blockIdx.x % chunks, b = (int)blockIdx.x / chunks;
+    const int m0 = b % p.tiles_m * TOK, k0 = chunk * 256;
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
+    const int fshift = QX ? p.xgroup_shift : 8;
+    stage_tokens<TT, QX, STEPS == 4, GRAIN, TT>(
+        p, b / p.tiles_m, m0, TOK, min(TOK, p.M - m0), k0, p.K, 256, p.tokens + ((size_t)b * p.kp + k0) * (TOK * 2),
+        p.sums + ((size_t)b * p.kp + k0) / GRAIN * TOK, p.scales + (((size_t)b * p.kp + k0) >> fshift) * TOK, &bad,
+        [] { __syncthreads(); });
+    __syncthreads();
+    if (threadIdx.x == 0) p.flags[blockIdx.x] = bad;
+}
+
+// Bounded wait for a tile's copies; after a timeout every wait of the CTA returns at once.
+__device__ __forceinline__ void tile_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, const QweightParams& p) {
+    if (ptx::mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (*abort) return;
+        if (ptx::globaltimer() - t0 > p.timeout_ns) {
+            record_error(p.status, ARE_DEV_PIPE_TIMEOUT, blockIdx.x, -6, -1);
+            *abort = 1u;
+            return;
+        }
+    }
+}
+
+// A group's scale and zero point (0..255: exact in bf16), in a word.
+__device__ __forceinline__ uint32_t scale_word(uint32_t scale, uint32_t zero) {
+    return scale | (__float_as_uint((float)zero) & 0xFFFF0000u);
+}
+
+// 128 k of a warp's rows times the tokens.
+//   at    : the lane's codes of the first row tile (shared memory)
+//   xat   : the lane's token operands
+//   words : the lane's row's scale word, of the block's first group; a group's words are `wrows` apart
+//   sums, scales: the lane's token pair's, of the block's first row
+//   acc   : [row tile][token tile][row g, g + 8] of the token pair
+template <int TT, int WSTEPS, int STEPS>
+__device__ __forceinline__ void products(uint64_t (&acc)[Shape<TT>::RT][TT][2], uint32_t at, uint32_t xat, const uint32_t* words,
+                                         int wrows, const float* sums, const float* scales, int fshift) {
+    using S = Shape<TT>;
+    constexpr int TOK = S::TOK, RT = S::RT, PITCH = S::PITCH;
+    constexpr bool OWN = S::OWN;
+    constexpr bool WIDE = STEPS == 4;  // a lane reads its 32 codes of 128 at once: all of them share the scales
+    // Four token tiles take the 128 k in two parts, whose operands fit the registers; TB tiles at a time, CH chains
+    // of sums each: a dependent instruction waits for the one before it (OWN: two row tiles are two chains).
+    constexpr int PARTS = TT == 4 ? 2 : 1, SP = 4 / PARTS, TB = TT == 2 ? 2 : 1, CH = OWN ? 1 : 2;
+    constexpr bool KEEP = STEPS > SP;  // a group's sums outlive a part
+    float d[KEEP ? TT : TB][RT][CH][4];
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) {
+        const int s0 = part * SP;
+        uint32_t a[RT][SP][2][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            uint32_t lo[SP], hi[SP];
+            const uint32_t from = at + rt * 16 * PITCH;
+            if (WIDE && SP == 4) {
+                const uint4 l4 = ld_shared_v4(from), h4 = ld_shared_v4(from + 8 * PITCH);
+                lo[0] = l4.x; lo[1] = l4.y; lo[SP - 2] = l4.z; lo[SP - 1] = l4.w;
+                hi[0] = h4.x; hi[1] = h4.y; hi[SP - 2] = h4.z; hi[SP - 1] = h4.w;
+            } else if (WIDE) {
+                const uint2 l2 = ld_shared_v2(from + s0 * 4), h2 = ld_shared_v2(from + 8 * PITCH + s0 * 4);
+                lo[0] = l2.x; lo[1] = l2.y;
+                hi[0] = h2.x; hi[1] = h2.y;
+            } else {
+#pragma unroll
+                for (int st = 0; st < SP; ++st) {
+                    lo[st] = ld_shared(from + (s0 + st) * 16);
+                    hi[st] = ld_shared(from + 8 * PITCH + (s0 + st) * 16);
+                }
+            }
+#pragma unroll
+            for (int st = 0; st < SP; ++st) {
+                codes8<0>(lo[st], a[rt][st][0], a[rt][st][1]);
+                codes8<1>(hi[st], a[rt][st][0], a[rt][st][1]);
+            }
+        }
+        // the scales and negated zero points of the rows' groups that end in this part, once for all tokens, in pairs
+        constexpr int WG = SP / WSTEPS > 0 ? SP / WSTEPS : 1;
+        uint64_t ws[WG][RT][2], wz[WG][RT][2];
+        if ((s0 + SP) % WSTEPS == 0 || STEPS <= SP) {
+#pragma unroll
+            for (int i = 0; i < WG; ++i)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t word = words[(s0 / WSTEPS + i) * wrows + rt * 16 + half * 8];
+                        ws[i][rt][half] = pair(__uint_as_float(word << 16), __uint_as_float(word << 16));
+                        const float z = __uint_as_float((word & 0xFFFF0000u) ^ 0x80000000u);
+                        wz[i][rt][half] = pair(z, z);
+                    }
+        }
+#pragma unroll
+        for (int tb = 0; tb < TT; tb += TB) {
+            uint4 b[TB][SP];
+#pragma unroll
+            for (int st = 0; st < SP; ++st)
+#pragma unroll
+                for (int t = 0; t < TB; ++t) b[t][st] = ld_shared_v4(xat + ((s0 + st) * TT + tb + t) * 512);
+#pragma unroll
+            for (int st = 0; st < SP; ++st) {
+#pragma unroll
+                for (int t = 0; t < TB; ++t)
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        float(&to)[CH][4] = d[KEEP ? tb + t : t][rt];
+                        const bool first = (s0 + st) % STEPS == 0;
+                        if (first) mma<true>(to[0], a[rt][st][0], b[t][st].x, b[t][st].y);
+                        else mma<false>(to[0], a[rt][st][0], b[t][st].x, b[t][st].y);
+                        if (CH == 2 && first) mma<true>(to[CH - 1], a[rt][st][1], b[t][st].z, b[t][st].w);
+                        else mma<false>(to[CH - 1], a[rt][st][1], b[t][st].z, b[t][st].w);
+                    }
+                if ((s0 + st) % STEPS != STEPS - 1) continue;
+#pragma unroll
+                for (int t = 0; t < TB; ++t) {
+                    const int tok = (tb + t) * 8;
+                    const uint64_t sum = *reinterpret_cast<const uint64_t*>(sums + (s0 + st) / STEPS * TOK + tok);
+                    const uint64_t f = *reinterpret_cast<const uint64_t*>(scales + ((s0 + st) * 32 >> fshift) * TOK + tok);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint64_t sc = ws[st / WSTEPS][rt][half], z = wz[st / WSTEPS][rt][half];
+                            const float(&d2)[CH][4] = d[KEEP ? tb + t : t][rt];
+                            uint64_t y = pair(d2[0][half * 2], d2[0][half * 2 + 1]);
+                            if (CH == 2) y = add2(y, pair(d2[CH - 1][half * 2], d2[CH - 1][half * 2 + 1]));
+                            uint64_t& e = acc[rt][tb + t][half];
+                            e = fma2(mul2(sc, f), fma2(z, sum, y), e);
+                        }
+                }
+            }
+        }
+    }
+}
+
+// Adds the cluster's sums, r ascending, and writes the outputs.  red: [slot_of(group)][rtoks][LD]; bad: tokens
+// of this CTA's K range that hold a value that is not finite, whose products are added here.
+template <int TT, bool QX, typename Slot>
+__device__ __forceinline__ void combine(const QweightParams& p, int q, int m0, int toks, int group0, int groups,
+                                        const float* red, const uint32_t* bad, Slot slot_of) {
+    constexpr int ROWS = Shape<TT>::ROWS, LD = Shape<TT>::LD;
+    __syncwarp();
+    ptx::cluster_sync();
+    constexpr int PAIRS = ROWS / 2;  // pairs of rows of a group
+    const uint32_t base = ptx::smem_u32(red), bad_addr = ptx::smem_u32(bad);
+    uint32_t any = 0u;
+    if (!QX) {
+#pragma unroll
+        for (int j = 0; j < kMaxRanks; ++j)
+            if (j < p.cluster) any |= ld_cluster(ptx::mapa_shared(bad_addr, (uint32_t)j));
+    }
+    // the cluster's threads take the (token, group, pair) in turn
+    for (int u = q * kThreads + threadIdx.x; u < groups * PAIRS * toks; u += p.cluster * kThreads) {
+        const int pair = u % PAIRS, a = u / PAIRS % groups, m = u / PAIRS / groups;
+        const int n = (group0 + a) * ROWS + pair * 2;
+        if (n < p.N) {
+            const uint32_t addr = base + (uint32_t)((slot_of(a) * p.rtoks + m) * LD + pair * 2) * 4u;
+            float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < kMaxRanks; ++j) {
+                if (j < p.cluster) {
+                    const float2 v = ld_cluster_f2(ptx::mapa_shared(addr, (uint32_t)j));
+                    s.x += v.x;
+                    s.y += v.y;
+                }
+            }
+            if (!QX && (any >> m & 1u)) {  // products of values that are not finite
+                for (int j = 0; j < p.cluster; ++j) {
+                    const int rj = j / p.splits, k0 = j % p.splits * p.split_k, k1 = min(p.K, k0 + p.split_k);
+                    const int64_t row = (int64_t)(m0 + m) * p.K;
+                    for (int k = k0; k < k1; ++k) {
+                        const float xv = __uint_as_float((uint32_t)__ldcg(static_cast<const uint16_t*>(p.x[rj]) + row + k) << 16);
+                        if ((__float_as_uint(xv) & 0x7F800000u) != 0x7F800000u) continue;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int64_t at = (int64_t)(n + i) * p.groups + (k >> p.group_shift);
+                            const uint32_t byte = __ldg(p.codes[rj] + (((int64_t)(n + i) * p.K + k) >> 1));
+                            const int u = (int)(k & 1 ? byte >> 4 : byte & 15u), z = p.zero[rj] ? __ldg(p.zero[rj] + at) : 8;
+                            const float w = (float)(u - z) * __uint_as_float((uint32_t)__ldg(p.scale[rj] + at) << 16);
+                            (i ? s.y : s.x) += xv * w;
+                        }
+                    }
+                }
+            }
+            const __nv_bfloat162 o = __floats2bfloat162_rn(s.x, s.y);
+            for (int v = 0; v < p.nviews; ++v)
+                *reinterpret_cast<__nv_bfloat162*>(p.views[v] + (int64_t)(m0 + m) * p.N + n) = o;
+        }
+    }
+    __syncwarp();
+    ptx::cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+// Up to 8 tokens a tile.
+// QX: tokens in 8 bits with fp32 scales, which are applied with the weights'
+// (power-of-two scales go into the staged tokens, exactly).
 // WSTEPS: steps of 32 k in a weight group; STEPS: those that share both scales,
 // the smaller of the weight and the token group.
-template <int TT, bool QX, int WSTEPS, int STEPS>
-__global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_constant__ QweightParams p) {
+template <bool QX, int WSTEPS, int STEPS>
+__global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_constant__ QweightParams p) {
     extern __shared__ __align__(128) uint8_t qw_smem[];
+    constexpr int TT = 1;
     using S = Shape<TT>;
-    constexpr int TOK = S::TOK, RT = S::RT, ROWS = S::ROWS, ITEM = S::ITEM, PITCH = S::PITCH, LD = S::LD;
-    constexpr bool OWN = S::OWN;
+    constexpr int TOK = S::TOK, ROWS = S::ROWS, ITEM = S::ITEM, PITCH = S::PITCH, LD = S::LD;
     constexpr bool WIDE = STEPS == 4;       // a lane reads its 32 codes of 128 at once: all of them share the scales
     constexpr int SLOT = S::SLOT, DEPTH = S::DEPTH, UNITS = S::UNITS;
     constexpr int GRAIN = STEPS * 32;       // k that share both scales
@@ -209,23 +625,23 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
     const int groups = min(p.run, (p.N + ROWS - 1) / ROWS - group0);  // of ROWS rows
     const int r = q / p.splits;
     const int kbeg = q % p.splits * p.split_k, kend = min(p.K, kbeg + p.split_k);  // never empty
+    const int tiles = (kend - kbeg + p.tile_k - 1) / p.tile_k;
     const int toks = min(TOK, p.M - m0);
 
     const uint32_t ring = ptx::smem_u32(qw_smem) + warp * (DEPTH * SLOT);
-    uint8_t* xs = qw_smem + S::RING;                                 // [k / 32][TT][lane] units of 8 k
-    float* xsum = reinterpret_cast<float*>(xs + 2 * TOK * p.tile_k);         // [k / GRAIN][TOK]: sum x * 2^-24
-    float* xsc = xsum + p.tile_k / GRAIN * TOK;                              // [k >> fshift][TOK]: the tokens' scales
     const int fshift = QX ? p.xgroup_shift : 8, frows = QX ? p.tile_k >> fshift : (p.tile_k + 255) >> 8;
-    const int wrows = p.run * ROWS + 1;                                      // odd: a row's groups fall into different banks
-    uint32_t* wsc = reinterpret_cast<uint32_t*>(xsc + frows * TOK);          // [k >> group][wrows]: scale | zero point << 16, in bf16
-    uint32_t* bad = wsc + (((p.tile_k >> p.group_shift) * wrows + 3) & ~3);  // bit m: token m has a value that is not finite
-    // OWN: the ring's place, when the products are done.  Else [group + warp][rtoks][LD].
-    float* red = reinterpret_cast<float*>(OWN ? qw_smem : reinterpret_cast<uint8_t*>(bad + 4));
+    const int wrows = p.run * ROWS + 1;                              // odd: a row's groups fall into different banks
+    uint8_t* xs = qw_smem + S::RING;                                 // as stage_tokens writes them
+    float* xsum = reinterpret_cast<float*>(xs + 2 * TOK * p.tile_k);
+    float* xsc = xsum + p.tile_k / GRAIN * TOK;
+    uint32_t* wsc = reinterpret_cast<uint32_t*>(xsc + frows * TOK);  // [k >> group][wrows]: scale | zero point << 16, in bf16
+    uint32_t* bad = wsc + (((p.tile_k >> p.group_shift) * wrows + 3) & ~3);
+    float* red = reinterpret_cast<float*>(bad + 4);                       // [group + warp][rtoks][LD]
 
     // this warp's items of a K tile: [first, first + count), item = group * per + K index
     const int per = p.tile_k / ITEM, all = groups * per;
-    const int first = OWN ? warp * per : warp * all / kWarps;
-    const int count = OWN ? (warp < groups ? per : 0) : (warp + 1) * all / kWarps - first;
+    const int first = warp * all / kWarps;
+    const int count = (warp + 1) * all / kWarps - first;
 
     // ---- the stream of codes, DEPTH - 1 items ahead of their use, by asynchronous copies.  N is a
     // multiple of 8: 8 rows exist or not.
@@ -243,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
     };
     auto fetch = [&](uint32_t slot) {
         if (fleft == 0) {
-            if (count > 0 && ftl + 1 < p.tiles_k) {
+            if (count > 0 && ftl + 1 < tiles) {
                 ++ftl;
                 fleft = count;
                 fgl = first / per;
@@ -277,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
         }
     };
 
-    if (threadIdx.x < 2) bad[threadIdx.x] = 0u;
+    if (threadIdx.x == 0) *bad = 0u;
     if (toks < TOK) {  // tokens that do not exist: zeros, which no tile overwrites
         for (int u = threadIdx.x; u < TOK * p.tile_k / 8; u += kThreads)
             *reinterpret_cast<uint4*>(xs + u * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -289,13 +705,8 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
     fetch(ring);
     fetch(ring + SLOT);
 
-    // ---- a K tile's tokens and weight scales into shared memory.  A warp takes a token's 256 k at a time, a unit of 8 k a
-    // lane; its (at most UNITS) loads are in flight together.
-    int tokp = 1, toksh = 0;
-    while (tokp < toks) tokp <<= 1, ++toksh;
     // The rows' scales and zero points: neighbouring lanes take a row's neighbouring groups (lanes on rows
     // of their own would touch a sector each with every load); what does not exist weighs nothing.
-    constexpr int WUNITS = 16;
     const bool zeros = p.zero[r] != nullptr;
     const int tg = p.tile_k >> p.group_shift;
     int tsh = 0;
@@ -303,13 +714,15 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
     // a thread's group of the tile is fixed; its rows are wstep apart
     const int wgi = threadIdx.x & ((1 << tsh) - 1), wrow = threadIdx.x >> tsh, wstep = kThreads >> tsh;
     const int wleft = min(p.run * ROWS, p.N - group0 * ROWS);
-    const int64_t wat = (int64_t)(group0 * ROWS + wrow) * p.groups + wgi, wjump = (int64_t)wstep * p.groups;
+    const int64_t wbase = (int64_t)group0 * ROWS * p.groups;  // the same for the CTA; its rows' offsets fit 32 bits
+    const int wat = wrow * p.groups + wgi, wjump = wstep * p.groups;
+    constexpr int WUNITS = 16;  // of a round
     uint32_t sv[WUNITS], zv[WUNITS];
     auto load_scales = [&](int t0, int round) {
         const bool on = wgi < tg && (t0 >> p.group_shift) + wgi < p.groups;
-        const int64_t at = wat + (t0 >> p.group_shift) + round * WUNITS * wjump;
-        const uint16_t* sp = p.scale[r] + at;
-        const uint8_t* zp = p.zero[r] + at;
+        const int at = wat + (t0 >> p.group_shift) + round * WUNITS * wjump;
+        const uint16_t* sp = p.scale[r] + wbase + at;
+        const uint8_t* zp = p.zero[r] + wbase + at;
 #pragma unroll
         for (int j = 0; j < WUNITS; ++j) {
             const bool in = on && wrow + (round * WUNITS + j) * wstep < wleft;
@@ -321,179 +734,34 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
             zp += wjump;
         }
     };
-    auto stage = [&](int tl) {
-        const int t0 = kbeg + tl * p.tile_k;
-        const int todo = ((p.tile_k + 255) >> 8) * tokp;  // (256 k, token) rows, the token innermost
-        uint4 v[UNITS];
-#pragma unroll
-        for (int j = 0; j < UNITS; ++j) {
-            v[j] = make_uint4(0u, 0u, 0u, 0u);
-            const int i = warp + j * kWarps, m = i & (tokp - 1), k = t0 + (i >> toksh) * 256 + lane * 8;
-            const bool in = i < todo && m < toks && k < kend;
-            const int64_t at = (int64_t)(m0 + m) * p.K + k;
-            if (QX || p.qx) {
-                uint2 b = make_uint2(0u, 0u);
-                ldg_if(b, static_cast<const uint8_t*>(p.x[r]) + at, in);
-                v[j].x = b.x;
-                v[j].y = b.y;
-                if (!QX) ldg_u8_if(v[j].z, static_cast<const uint8_t*>(p.xscale[r]) + (int64_t)(m0 + m) * p.xgroups + (k >> p.xgroup_shift), in);
-            } else {
-                ldg_if(v[j], static_cast<const uint16_t*>(p.x[r]) + at, in);
-            }
-        }
-        load_scales(t0, 0);            // in flight with the tokens
-        __syncthreads();               // every warp is done with the tile before (first: with clearing)
-        // two rows at a time, so that one's steps fill the waits of the other's
-        if (QX || !p.qx)
-#pragma unroll
-        for (int j0 = 0; j0 < UNITS; j0 += 2) {
-            if (warp + j0 * kWarps >= todo) break;
-            float x[2][8], sum[2];  // the even k, 0 2 4 6, times 1; and the odd
-            int m[2], k[2];         // k within the tile
-            bool in[2];
-            uint32_t top[2] = {0u, 0u};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = warp + (j0 + e) * kWarps;
-                m[e] = i & (tokp - 1);
-                k[e] = (i >> toksh) * 256 + lane * 8;
-                in[e] = i < todo && m[e] < toks && k[e] < p.tile_k;
-                uint4& w = v[j0 + e];
-                if (QX) {
-                    const float2 f[4] = {fp8x2_to_float2(w.x), fp8x2_to_float2(w.x >> 16), fp8x2_to_float2(w.y), fp8x2_to_float2(w.y >> 16)};
-#pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4) {
-                        x[e][i4] = f[i4].x;
-                        x[e][4 + i4] = f[i4].y;
-                    }
-                } else {
-                    top[e] = __vmaxu2(__vmaxu2(w.x & 0x7F807F80u, w.y & 0x7F807F80u), __vmaxu2(w.z & 0x7F807F80u, w.w & 0x7F807F80u));
-                }
-            }
-            if (!QX) {
-                // the largest exponents
-#pragma unroll
-                for (int e = 0; e < 2; ++e) top[e] = __reduce_max_sync(0xFFFFFFFFu, max(top[e] >> 23, top[e] >> 7 & 0xFFu));
-                if (top[0] == 255u || top[1] == 255u) {
-                    // values that are not finite: zeros here, and their tokens are noted
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (top[e] != 255u) continue;
-                        if (lane == 0) atomicOr(&bad[m[e] >> 5], 1u << (m[e] & 31));
-                        uint32_t* w = &v[j0 + e].x;
-                        uint32_t t = 0u;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0x0000FFFFu;
-                            if ((w[i] & 0x00007F80u) == 0x00007F80u) w[i] &= 0xFFFF0000u;
-                            t = __vmaxu2(t, w[i] & 0x7F807F80u);
-                        }
-                        top[e] = __reduce_max_sync(0xFFFFFFFFu, max(t >> 23, t >> 7 & 0xFFu));
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float mul = scale_of(top[e]);
-                    const uint32_t w[4] = {v[j0 + e].x, v[j0 + e].y, v[j0 + e].z, v[j0 + e].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[e][i] = bf_lo(w[i]) * mul;
-                        x[e][4 + i] = bf_hi(w[i]) * mul;
-                    }
-                    // (a row's first lane is in the tile wherever the row has a lane in it)
-                    if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = unscale_of(top[e]) * 0x1p12f;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                // step st = 32 k, or lane c's word st of 128 k
-                const int st = WIDE ? (k[e] >> 7) * 4 + (lane & 3) : k[e] >> 5, c4 = WIDE ? lane >> 2 & 3 : lane & 3;
-                const float(&y)[8] = x[e];
-                if (in[e])
-                    *reinterpret_cast<uint4*>(xs + (((st * TT + (m[e] >> 3)) * 8 + (m[e] & 7)) * 4 + c4) * 16) =
-                        make_uint4(f16x2(y[0], y[2]), f16x2(y[4] * 0.0625f, y[6] * 0.0625f), f16x2(y[1], y[3]),
-                                   f16x2(y[5] * 0.0625f, y[7] * 0.0625f));
-                sum[e] = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
-            }
-            // sum x over each GRAIN of k, in the weights' unit
-#pragma unroll
-            for (int o = 1; o < GRAIN / 8; o <<= 1)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], o);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if ((lane & (GRAIN / 8 - 1)) == 0 && in[e]) xsum[k[e] / GRAIN * TOK + m[e]] = sum[e] * 0x1p-24f;
-        }
-        // FP8 codes under power-of-two scales: in fp16, times the scale over the row's largest and 2^6
-        if (!QX && p.qx)
-#pragma unroll
-        for (int j0 = 0; j0 < UNITS; j0 += 2) {
-            if (warp + j0 * kWarps >= todo) break;
-            float sum[2];
-            int m[2], k[2];
-            bool in[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = warp + (j0 + e) * kWarps;
-                m[e] = i & (tokp - 1);
-                k[e] = (i >> toksh) * 256 + lane * 8;
-                in[e] = i < todo && m[e] < toks && k[e] < p.tile_k;
-                const uint4 w = v[j0 + e];
-                const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, w.z == 255u ? 0u : w.z);
-                // 2^(z - top + 6): below 2^-24 it is nothing; a NaN scale
-                const uint32_t d = top - w.z;
-                const uint32_t mul = w.z == 255u ? 0x7FFFu : d <= 20u ? (21u - d) << 10 : d <= 30u ? 0x400u >> (d - 20u) : 0u;
-                const __half2 mul2 = h2_of(mul * 0x10001u), odd2 = __hmul2(mul2, __float2half2_rn(0.0625f));
-                const uint32_t h[4] = {fp8x2_to_f16x2(w.x), fp8x2_to_f16x2(w.x >> 16), fp8x2_to_f16x2(w.y), fp8x2_to_f16x2(w.y >> 16)};
-                const __half2 y0 = __hmul2(h2_of(__byte_perm(h[0], h[2], 0x5410)), mul2), y1 = __hmul2(h2_of(__byte_perm(h[0], h[2], 0x7632)), odd2);
-                const __half2 y2 = __hmul2(h2_of(__byte_perm(h[1], h[3], 0x5410)), mul2), y3 = __hmul2(h2_of(__byte_perm(h[1], h[3], 0x7632)), odd2);
-                const int st = WIDE ? (k[e] >> 7) * 4 + (lane & 3) : k[e] >> 5, c4 = WIDE ? lane >> 2 & 3 : lane & 3;
-                if (in[e])
-                    *reinterpret_cast<uint4*>(xs + (((st * TT + (m[e] >> 3)) * 8 + (m[e] & 7)) * 4 + c4) * 16) =
-                        make_uint4(h2_bits(y0), h2_bits(y1), h2_bits(y2), h2_bits(y3));
-                const float2 f0 = __half22float2(y0), f1 = __half22float2(y1), f2 = __half22float2(y2), f3 = __half22float2(y3);
-                sum[e] = ((f0.x + f0.y) + (f2.x + f2.y)) + ((f1.x + f1.y) + (f3.x + f3.y)) * 16.f;
-                // 2^(top - 127) / 2^6 * 2^12 (above 2^127: such tokens overflow fp32 themselves)
-                if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = e8m0_to_float(top) * 64.f;
-            }
-#pragma unroll
-            for (int o = 1; o < GRAIN / 8; o <<= 1)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], o);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if ((lane & (GRAIN / 8 - 1)) == 0 && in[e]) xsum[k[e] / GRAIN * TOK + m[e]] = sum[e] * 0x1p-24f;
-        }
-        if (QX) {
-            const int x0 = t0 >> p.xgroup_shift;
-            for (int u = threadIdx.x; u < frows * TOK; u += kThreads) {
-                const int m = u % TOK, gi = u / TOK;
-                const bool in = m < toks && x0 + gi < p.xgroups;
-                xsc[u] = in ? __ldg(static_cast<const float*>(p.xscale[r]) + (int64_t)(m0 + m) * p.xgroups + x0 + gi) : 0.f;
-            }
-        }
+    auto store_scales = [&](int t0) {
         for (int round = 0; round * WUNITS * wstep < p.run * ROWS; ++round) {
             if (round) load_scales(t0, round);
             uint32_t* to = wsc + wgi * wrows + wrow + round * WUNITS * wstep;
 #pragma unroll
             for (int j = 0; j < WUNITS; ++j)
-                if (wgi < tg && wrow + (round * WUNITS + j) * wstep < p.run * ROWS)
-                    to[j * wstep] = sv[j] | (__float_as_uint((float)zv[j]) & 0xFFFF0000u);  // 0..255: exact in bf16
+                if (wgi < tg && wrow + (round * WUNITS + j) * wstep < p.run * ROWS) to[j * wstep] = scale_word(sv[j], zv[j]);
         }
+    };
+    auto stage = [&](int tl) {
+        const int t0 = kbeg + tl * p.tile_k;
+        stage_tokens<TT, QX, WIDE, GRAIN, UNITS>(p, r, m0, toks, toks, t0, kend, p.tile_k, xs, xsum, xsc, bad, [&] {
+            load_scales(t0, 0);  // in flight with the tokens
+            __syncthreads();     // every warp is done with the tile before (first: with clearing)
+        });
+        store_scales(t0);
         __syncthreads();
     };
-    float acc[RT][TT][4];
+    uint64_t acc[1][TT][2];
 #pragma unroll
-    for (int a = 0; a < RT; ++a)
+    for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[a][t][j] = 0.f;
+        for (int j = 0; j < 2; ++j) acc[0][t][j] = 0ull;
     const uint32_t xs_addr = ptx::smem_u32(xs) + lane * 16u;
     uint32_t cur = ring;
     const uint32_t ring_end = ring + DEPTH * SLOT;
 #pragma unroll 1
-    for (int tl = 0; tl < p.tiles_k; ++tl) {
+    for (int tl = 0; tl < tiles; ++tl) {
         stage(tl);
         const int ktile = kbeg + tl * p.tile_k;
         int gl = first / per, kk = first % per;
@@ -509,99 +777,20 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
 #pragma unroll
                 for (int blk = 0; blk < ITEM / 128; ++blk) {
                     const int kt = kk * ITEM + blk * 128;  // within the tile
-                    // 128 k of the rows
-                    uint32_t a[RT][4][2][4];
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        uint32_t lo[4], hi[4];
-                        const uint32_t from = at + rt * 16 * PITCH + blk * 64;
-                        if (WIDE) {
-                            const uint4 l4 = ld_shared_v4(from), h4 = ld_shared_v4(from + 8 * PITCH);
-                            lo[0] = l4.x; lo[1] = l4.y; lo[2] = l4.z; lo[3] = l4.w;
-                            hi[0] = h4.x; hi[1] = h4.y; hi[2] = h4.z; hi[3] = h4.w;
-                        } else {
-#pragma unroll
-                            for (int st = 0; st < 4; ++st) {
-                                lo[st] = ld_shared(from + st * 16);
-                                hi[st] = ld_shared(from + 8 * PITCH + st * 16);
-                            }
-                        }
-#pragma unroll
-                        for (int st = 0; st < 4; ++st) {
-                            codes8<0>(lo[st], a[rt][st][0], a[rt][st][1]);
-                            codes8<1>(hi[st], a[rt][st][0], a[rt][st][1]);
-                        }
-                    }
-                    // the rows' scales and zero points, once for all tokens
-                    float ws[4 / WSTEPS][RT][2], wz[4 / WSTEPS][RT][2];
-                    const uint32_t* words = wsc + (kt >> p.group_shift) * wrows + gl * ROWS + g;
-#pragma unroll
-                    for (int i = 0; i < 4 / WSTEPS; ++i)
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const uint32_t word = words[i * wrows + rt * 16 + half * 8];
-                                ws[i][rt][half] = __uint_as_float(word << 16);
-                                wz[i][rt][half] = __uint_as_float(word & 0xFFFF0000u);
-                            }
-                    // TB token tiles at a time, CH chains of sums each: a dependent instruction waits for
-                    // the one before it
-                    constexpr int TB = TT == 2 ? 2 : 1, CH = OWN ? 1 : 2;  // OWN: its two row tiles are two chains
-#pragma unroll
-                    for (int tb = 0; tb < TT; tb += TB) {
-                        const uint32_t xat = xs_addr + (uint32_t)(((kt >> 5) * TT + tb) * 512);
-                        uint4 b[TB][4];
-#pragma unroll
-                        for (int st = 0; st < 4; ++st)
-#pragma unroll
-                            for (int t = 0; t < TB; ++t) b[t][st] = ld_shared_v4(xat + st * TT * 512 + t * 512);
-                        float d[TB][RT][CH][4];
-#pragma unroll
-                        for (int st = 0; st < 4; ++st) {
-#pragma unroll
-                            for (int t = 0; t < TB; ++t)
-#pragma unroll
-                                for (int rt = 0; rt < RT; ++rt) {
-                                    if (st % STEPS == 0) mma<true>(d[t][rt][0], a[rt][st][0], b[t][st].x, b[t][st].y);
-                                    else mma<false>(d[t][rt][0], a[rt][st][0], b[t][st].x, b[t][st].y);
-                                    if (CH == 2 && st % STEPS == 0) mma<true>(d[t][rt][CH - 1], a[rt][st][1], b[t][st].z, b[t][st].w);
-                                    else mma<false>(d[t][rt][CH - 1], a[rt][st][1], b[t][st].z, b[t][st].w);
-                                }
-                            if (st % STEPS != STEPS - 1) continue;
-#pragma unroll
-                            for (int t = 0; t < TB; ++t) {
-                                const int tok = (tb + t) * 8 + 2 * c;
-                                const float2 sum = *reinterpret_cast<const float2*>(xsum + ((kt + st * 32) / GRAIN) * TOK + tok);
-                                const float2 f = *reinterpret_cast<const float2*>(xsc + ((kt + st * 32) >> fshift) * TOK + tok);
-#pragma unroll
-                                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                                    for (int half = 0; half < 2; ++half) {
-                                        const float s = ws[st / WSTEPS][rt][half], z = wz[st / WSTEPS][rt][half];
-                                        const float(&d2)[CH][4] = d[t][rt];
-                                        float y0 = d2[0][half * 2], y1 = d2[0][half * 2 + 1];
-                                        if (CH == 2) {
-                                            y0 += d2[CH - 1][half * 2];
-                                            y1 += d2[CH - 1][half * 2 + 1];
-                                        }
-                                        float* e = &acc[rt][tb + t][half * 2];
-                                        e[0] = fmaf(s * f.x, fmaf(-z, sum.x, y0), e[0]);
-                                        e[1] = fmaf(s * f.y, fmaf(-z, sum.y, y1), e[1]);
-                                    }
-                            }
-                        }
-                    }
+                    products<TT, WSTEPS, STEPS>(acc, at + blk * 64, xs_addr + (uint32_t)((kt >> 5) * TT * 512),
+                                                wsc + (kt >> p.group_shift) * wrows + gl * ROWS + g, wrows,
+                                                xsum + kt / GRAIN * TOK + 2 * c, xsc + (kt >> fshift) * TOK + 2 * c, fshift);
                 }
             }
-            if (!OWN && (++kk == per || left == 1)) {
+            if (++kk == per || left == 1) {
                 // the warp leaves a group: its sums go to the slot of (group, warp), which no other
                 // warp touches; along a CTA's items either index grows, so group + warp is unique
                 float* to = red + (gl + warp) * p.rtoks * LD + g;
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
                     float* e = to + (t * 8 + 2 * c) * LD;
-                    float* v = acc[0][t];
+                    const float2 v01 = unpair(acc[0][t][0]), v23 = unpair(acc[0][t][1]);
+                    const float v[4] = {v01.x, v01.y, v23.x, v23.y};
                     if (t * 8 + 2 * c >= p.rtoks) {
                     } else if (tl == 0) {
                         e[0] = v[0] * UNIT; e[LD] = v[1] * UNIT; e[8] = v[2] * UNIT; e[LD + 8] = v[3] * UNIT;
@@ -609,12 +798,10 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
                         e[0] = fmaf(v[0], UNIT, e[0]); e[LD] = fmaf(v[1], UNIT, e[LD]);
                         e[8] = fmaf(v[2], UNIT, e[8]); e[LD + 8] = fmaf(v[3], UNIT, e[LD + 8]);
                     }
-                    v[0] = v[1] = v[2] = v[3] = 0.f;
+                    acc[0][t][0] = acc[0][t][1] = 0ull;
                 }
                 kk = 0;
                 ++gl;
-            } else if (OWN) {
-                ++kk;
             }
         }
     }
@@ -623,105 +810,250 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_kernel(const __grid_const
 
     // ---- the sums: of a group over the CTA's warps (into the slot of its first warp), then over the
     // cluster, r ascending.  Item i belongs to warp (8 (i + 1) - 1) / all.
-    auto slot_of = [&](int a) { return OWN ? a : a + (kWarps * (a * per + 1) - 1) / all; };
-    if (OWN) {
-        if (count > 0) {
-            float* to = red + warp * p.rtoks * LD + g;
-#pragma unroll
-            for (int t = 0; t < TT; ++t) {
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    if (t * 8 + 2 * c >= p.rtoks) break;
-                    float* e = to + (t * 8 + 2 * c) * LD + rt * 16;
-                    e[0] = acc[rt][t][0] * UNIT; e[LD] = acc[rt][t][1] * UNIT;
-                    e[8] = acc[rt][t][2] * UNIT; e[LD + 8] = acc[rt][t][3] * UNIT;
-                }
-            }
-        }
-    } else {
-        for (int a = warp; a < groups; a += kWarps) {
-            const int s0 = slot_of(a), w0 = s0 - a, w1 = (kWarps * (a * per + per) - 1) / all;
-            for (int w = w0 + 1; w <= w1; ++w) {
-                if ((w + 1) * all / kWarps == w * all / kWarps) continue;  // a warp without items
-                for (int m = lane >> 4; m < toks; m += 2)
-                    red[(s0 * p.rtoks + m) * LD + (lane & 15)] += red[((a + w) * p.rtoks + m) * LD + (lane & 15)];
-            }
+    auto slot_of = [&](int a) { return a + (kWarps * (a * per + 1) - 1) / all; };
+    for (int a = warp; a < groups; a += kWarps) {
+        const int s0 = slot_of(a), w0 = s0 - a, w1 = (kWarps * (a * per + per) - 1) / all;
+        for (int w = w0 + 1; w <= w1; ++w) {
+            if ((w + 1) * all / kWarps == w * all / kWarps) continue;  // a warp without items
+            for (int m = lane >> 4; m < toks; m += 2)
+                red[(s0 * p.rtoks + m) * LD + (lane & 15)] += red[((a + w) * p.rtoks + m) * LD + (lane & 15)];
         }
     }
-    __syncwarp();
-    ptx::cluster_sync();
-    constexpr int PAIRS = ROWS / 2;  // pairs of rows of a group
-    const uint32_t base = ptx::smem_u32(red), bad_addr = ptx::smem_u32(bad);
-    uint32_t any[2] = {0u, 0u};
+    combine<TT, QX>(p, q, m0, toks, group0, groups, red, bad, slot_of);
+}
+
+// Tiles of 16 or 32 tokens: a warp owns 32 rows.  The staged tokens come in tiles of K by bulk copies, the
+// weights' scales with plain loads spread over the items of the tile before, both a tile ahead.
+template <int TT, bool QX, int WSTEPS, int STEPS>
+__global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_constant__ QweightParams p) {
+    extern __shared__ __align__(128) uint8_t qw_smem[];
+    using S = Shape<TT>;
+    using W = Wide<TT, QX, WSTEPS, STEPS>;
+    constexpr int TOK = S::TOK, RT = S::RT, ROWS = S::ROWS, ITEM = S::ITEM, PITCH = S::PITCH, LD = S::LD;
+    constexpr int SLOT = S::SLOT, DEPTH = S::DEPTH, TILE = W::TILE, PER = TILE / ITEM, WROWS = W::WROWS;
+    constexpr int GRAIN = STEPS * 32;       // k that share both scales
+    constexpr float UNIT = QX ? 0x1p24f : 0x1p12f;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
+    const int g = lane >> 2, c = lane & 3;
+    const int q = (int)(blockIdx.x % p.cluster);
+    const int tile = (int)(blockIdx.x / p.cluster);
+    const int m0 = tile % p.tiles_m * TOK, group0 = tile / p.tiles_m * kWarps;
+    const int groups = min(kWarps, (p.N + ROWS - 1) / ROWS - group0);
+    const int r = q / p.splits;
+    const int kbeg = q % p.splits * p.split_k, kend = min(p.K, kbeg + p.split_k);  // never empty
+    const int tiles = (kend - kbeg + TILE - 1) / TILE;
+    const bool active = warp < groups;
+
+    const uint32_t ring = ptx::smem_u32(qw_smem) + warp * (DEPTH * SLOT);
+    const int fshift = QX ? p.xgroup_shift : 8;
+    uint8_t* xs = qw_smem + S::RING;                                      // [buffer] as stage_tokens writes them
+    float* xsum = reinterpret_cast<float*>(xs + 2 * W::XS);
+    float* xsc = xsum + 2 * W::XSUM;
+    uint32_t* wsc = reinterpret_cast<uint32_t*>(xsc + 2 * W::XSC);        // [buffer][group][WROWS]: scale | zero point << 16, in bf16
+    uint32_t* bad = wsc + 2 * W::WSC;
+    uint32_t* issued = bad + 1;                                           // tiles copied so far
+    volatile uint32_t* abort = bad + 2;                                   // a wait has run out
+    uint64_t* full = reinterpret_cast<uint64_t*>(bad + 4);                // a buffer's copies have landed
+    float* red = reinterpret_cast<float*>(qw_smem);                       // the ring's place, when the products are done
+
+    // the stream of codes, DEPTH - 1 items ahead of their use
+    constexpr int LPR = ITEM / 32, RPI = 32 / LPR, CP = ROWS / RPI;  // lanes a row of codes, rows an instruction, instructions
+    const int frow = (group0 + warp) * ROWS, fn = p.N - frow;
+    const int rstep = RPI * (p.K >> 1);                              // p.K <= 2^24: a warp's rows are within 2^31 of each other
+    int fk = kbeg;
+    const uint8_t* fcodes = p.codes[r] + (((int64_t)frow * p.K + kbeg) >> 1) + lane / LPR * (p.K >> 1) + lane % LPR * 16;
+    const uint32_t lane_to = (uint32_t)(lane / LPR * PITCH + lane % LPR * 16);
+    auto fetch = [&](uint32_t slot) {
+        if (active && fk < kend) {
+            const uint32_t to = slot + lane_to;
+            if (fn >= ROWS && fk + ITEM <= kend) {
+#pragma unroll
+                for (int j = 0; j < CP; ++j) cp_async16(to + j * RPI * PITCH, fcodes + (int64_t)j * rstep);
+            } else {  // rows (8 exist or not: N is a multiple of 8) or K that end within the item: zeros
+                const bool kin = fk + lane % LPR * 32 < kend;
+#pragma unroll
+                for (int j = 0; j < CP; ++j) {
+                    const bool in = kin && j * RPI < fn;
+                    cp_async16(to + j * RPI * PITCH, in ? fcodes + (int64_t)j * rstep : p.codes[r], in);
+                }
+            }
+            fk += ITEM;
+            fcodes += ITEM / 2;
+        }
+        cp_commit();
+    };
+
+    // a tile of the staged tokens, by one thread
+    const int b = r * p.tiles_m + tile % p.tiles_m;
+    auto copy_tile = [&](int tl) {
+        const int t0 = kbeg + tl * TILE, kl = min(TILE, min(kbeg + p.split_k, p.kp) - t0), buf = tl & 1;
+        const size_t at = (size_t)b * p.kp + t0;
+        const uint32_t nx = (uint32_t)kl * (TOK * 2), ns = (uint32_t)(kl / GRAIN) * (TOK * 4), nf = (uint32_t)(kl >> fshift) * (TOK * 4);
+        *issued = (uint32_t)tl + 1u;
+        ptx::mbar_arrive_expect_tx(&full[buf], nx + ns + nf);
+        ptx::bulk_load(xs + buf * W::XS, p.tokens + at * (TOK * 2), nx, &full[buf]);
+        ptx::bulk_load(xsum + buf * W::XSUM, p.sums + at / GRAIN * TOK, ns, &full[buf]);
+        ptx::bulk_load(xsc + buf * W::XSC, p.scales + (at >> fshift) * TOK, nf, &full[buf]);
+    };
+
+    // The rows' scales and zero points of a tile, STEP rows apart, NE of them with an item: neighbouring lanes
+    // take a row's neighbouring groups; what does not exist weighs nothing.
+    constexpr int TG = TILE / (WSTEPS * 32), STEP = kThreads / TG, NE = TG / PER;
+    static_assert(kWarps * ROWS == kThreads && NE * PER == TG, "an item's share of the scales");
+    const bool zeros = p.zero[r] != nullptr;
+    const int wgi = threadIdx.x % TG, wrow = threadIdx.x / TG, wleft = p.N - group0 * ROWS;
+    const int64_t wbase = (int64_t)group0 * ROWS * p.groups;  // the CTA's rows are within 2^31 of it
+    uint32_t sv[NE], zv[NE];
+    auto load_scales = [&](int tl, int kk) {
+        const int gi = (kbeg + tl * TILE) / (WSTEPS * 32) + wgi;
+#pragma unroll
+        for (int j = 0; j < NE; ++j) {
+            const int row = wrow + (kk * NE + j) * STEP;
+            const int64_t at = wbase + (row * p.groups + gi);
+            const bool in = gi < p.groups && row < wleft;
+            sv[j] = 0u;
+            zv[j] = 8u;
+            ldg_u16_if(sv[j], p.scale[r] + at, in);
+            ldg_u8_if(zv[j], p.zero[r] + at, in && zeros);
+        }
+    };
+    uint32_t* wto = wsc + wgi * WROWS + wrow;
+    auto store_scales = [&](int tl, int kk) {
+#pragma unroll
+        for (int j = 0; j < NE; ++j) wto[(tl & 1) * W::WSC + (kk * NE + j) * STEP] = scale_word(sv[j], zv[j]);
+    };
+
+    if (threadIdx.x == 0) {
+        *bad = 0u;
+        *abort = 0u;
+        ptx::mbar_init(&full[0], 1);
+        ptx::mbar_init(&full[1], 1);
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_shared();
+    }
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
+    fetch(ring);
+    fetch(ring + SLOT);
+    if (threadIdx.x == 0) {
+        ptx::fence_proxy_async_global();
+        copy_tile(0);
+    }
+    __syncthreads();  // the barriers and `bad`
+    for (int kk = 0; kk < PER; ++kk) {
+        load_scales(0, kk);
+        store_scales(0, kk);
+    }
     if (!QX) {
-#pragma unroll
-        for (int j = 0; j < kMaxRanks; ++j)
-            if (j < p.cluster) {
-                any[0] |= ld_cluster(ptx::mapa_shared(bad_addr, (uint32_t)j));
-                if (TOK > 32) any[1] |= ld_cluster(ptx::mapa_shared(bad_addr + 4u, (uint32_t)j));
-            }
-    }
-    // the cluster's threads take the (token, group, pair) in turn
-    for (int u = q * kThreads + threadIdx.x; u < groups * PAIRS * toks; u += p.cluster * kThreads) {
-        const int pair = u % PAIRS, a = u / PAIRS % groups, m = u / PAIRS / groups;
-        const int n = (group0 + a) * ROWS + pair * 2;
-        if (n < p.N) {
-            const uint32_t addr = base + (uint32_t)((slot_of(a) * p.rtoks + m) * LD + pair * 2) * 4u;
-            float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int j = 0; j < kMaxRanks; ++j) {
-                if (j < p.cluster) {
-                    const float2 v = ld_cluster_f2(ptx::mapa_shared(addr, (uint32_t)j));
-                    s.x += v.x;
-                    s.y += v.y;
-                }
-            }
-            if (!QX && (any[m >> 5] >> (m & 31) & 1u)) {  // products of values that are not finite
-                for (int j = 0; j < p.cluster; ++j) {
-                    const int rj = j / p.splits, k0 = j % p.splits * p.split_k, k1 = min(p.K, k0 + p.split_k);
-                    const int64_t row = (int64_t)(m0 + m) * p.K;
-                    for (int k = k0; k < k1; ++k) {
-                        const float xv = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p.x[rj]) + row + k) << 16);
-                        if ((__float_as_uint(xv) & 0x7F800000u) != 0x7F800000u) continue;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int64_t at = (int64_t)(n + i) * p.groups + (k >> p.group_shift);
-                            const uint32_t byte = __ldg(p.codes[rj] + (((int64_t)(n + i) * p.K + k) >> 1));
-                            const int u = (int)(k & 1 ? byte >> 4 : byte & 15u), z = p.zero[rj] ? __ldg(p.zero[rj] + at) : 8;
-                            const float w = (float)(u - z) * __uint_as_float((uint32_t)__ldg(p.scale[rj] + at) << 16);
-                            (i ? s.y : s.x) += xv * w;
-                        }
-                    }
-                }
-            }
-            const __nv_bfloat162 o = __floats2bfloat162_rn(s.x, s.y);
-            for (int v = 0; v < p.nviews; ++v)
-                *reinterpret_cast<__nv_bfloat162*>(p.views[v] + (int64_t)(m0 + m) * p.N + n) = o;
+        const int chunks = ((kend + 255) >> 8) - (kbeg >> 8);
+        for (int i = threadIdx.x; i < chunks; i += kThreads) {
+            const uint32_t v = __ldcg(p.flags + (size_t)b * (p.kp >> 8) + (kbeg >> 8) + i);
+            if (v) atomicOr(bad, v);
         }
     }
-    __syncwarp();
-    ptx::cluster_sync();  // no CTA leaves while another reads its sums
+
+    uint64_t acc[RT][TT][2];
+#pragma unroll
+    for (int a = 0; a < RT; ++a)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[a][t][j] = 0ull;
+    const uint32_t xs_addr = ptx::smem_u32(xs) + lane * 16u;
+    const uint32_t* words = wsc + warp * ROWS + g;
+    const float *sums = xsum + 2 * c, *scales = xsc + 2 * c;
+    uint32_t cur = ring;
+    const uint32_t ring_end = ring + DEPTH * SLOT;
+#pragma unroll 1
+    for (int tl = 0; tl < tiles; ++tl) {
+        const int buf = tl & 1;
+        tile_wait(&full[buf], (uint32_t)(tl >> 1) & 1u, abort, p);
+        __syncthreads();  // the weights' scales are there, and every warp is done with the tile before
+        const bool more = tl + 1 < tiles;
+        if (threadIdx.x == 0 && more && !*abort) copy_tile(tl + 1);
+#pragma unroll 1
+        for (int kk = 0; kk < PER; ++kk) {
+            if (more) load_scales(tl + 1, kk);
+            cp_wait<DEPTH - 2>();
+            __syncwarp();  // every lane's copies have landed, and every lane has left the slot refilled now
+            const uint32_t next = cur + SLOT == ring_end ? ring : cur + SLOT;
+            fetch(next + SLOT == ring_end ? ring : next + SLOT);
+            if (active && kbeg + tl * TILE + kk * ITEM < kend)
+                products<TT, WSTEPS, STEPS>(acc, cur + g * PITCH + c * (STEPS == 4 ? 16 : 4),
+                                            xs_addr + (uint32_t)(buf * W::XS + kk * (4 * TT * 512)),
+                                            words + buf * W::WSC + kk * (4 / WSTEPS * WROWS), WROWS,
+                                            sums + buf * W::XSUM + kk * (4 / STEPS * TOK),
+                                            scales + buf * W::XSC + (kk * ITEM >> fshift) * TOK, fshift);
+            cur = next;
+            if (more) store_scales(tl + 1, kk);
+        }
+    }
+    cp_wait<0>();
+    if (threadIdx.x == 0 && *abort) {  // the CTA must not end before its copies have landed
+        const int n = (int)*issued;
+        for (int tl = max(n - 2, 0); tl < n; ++tl) {
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(&full[tl & 1], (uint32_t)(tl >> 1) & 1u))
+                if (ptx::globaltimer() - t0 > p.timeout_ns) break;
+        }
+    }
+    __syncthreads();
+    if (active) {
+        float* to = red + warp * p.rtoks * LD + g;
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                if (t * 8 + 2 * c >= p.rtoks) break;
+                float* e = to + (t * 8 + 2 * c) * LD + rt * 16;
+                const float2 v01 = unpair(acc[rt][t][0]), v23 = unpair(acc[rt][t][1]);
+                e[0] = v01.x * UNIT; e[LD] = v01.y * UNIT;
+                e[8] = v23.x * UNIT; e[LD + 8] = v23.y * UNIT;
+            }
+        }
+    }
+    combine<TT, QX>(p, q, m0, min(TOK, p.M - m0), group0, groups, red, bad, [](int a) { return a; });
 }
 
 typedef void (*Kernel)(QweightParams);
 
+// A launch's kernel and the shared memory that it takes (0: by its sizes).
+struct Choice {
+    Kernel kernel;
+    size_t smem;
+};
+template <int TT, bool QX, int WSTEPS, int STEPS>
+Choice choice() {
+    if constexpr (TT == 1) return {qweight_few_kernel<QX, WSTEPS, STEPS>, 0};
+    else return {qweight_wide_kernel<TT, QX, WSTEPS, STEPS>, Wide<TT, QX, WSTEPS, STEPS>::SMEM};
+}
 template <int TT, bool QX, int WSTEPS>
-Kernel kernel_of(int steps) {
-    if constexpr (!QX || WSTEPS == 1) return qweight_kernel<TT, QX, WSTEPS, WSTEPS>;
-    else if constexpr (WSTEPS == 2) return steps == 1 ? qweight_kernel<TT, QX, 2, 1> : qweight_kernel<TT, QX, 2, 2>;
-    else return steps == 1 ? qweight_kernel<TT, QX, 4, 1> : steps == 2 ? qweight_kernel<TT, QX, 4, 2> : qweight_kernel<TT, QX, 4, 4>;
+Choice kernel_of(int steps) {
+    if constexpr (!QX || WSTEPS == 1) return choice<TT, QX, WSTEPS, WSTEPS>();
+    else if constexpr (WSTEPS == 2) return steps == 1 ? choice<TT, QX, 2, 1>() : choice<TT, QX, 2, 2>();
+    else return steps == 1 ? choice<TT, QX, 4, 1>() : steps == 2 ? choice<TT, QX, 4, 2>() : choice<TT, QX, 4, 4>();
 }
 template <int TT, bool QX>
-Kernel kernel_of(int wsteps, int steps) {
+Choice kernel_of(int wsteps, int steps) {
     return wsteps == 1 ? kernel_of<TT, QX, 1>(steps) : wsteps == 2 ? kernel_of<TT, QX, 2>(steps) : kernel_of<TT, QX, 4>(steps);
 }
 template <int TT>
-Kernel kernel_of(bool qx, int wsteps, int steps) {
+Choice kernel_of(bool qx, int wsteps, int steps) {
     return qx ? kernel_of<TT, true>(wsteps, steps) : kernel_of<TT, false>(wsteps, steps);
 }
 // The kernel of a token tile and of the groups' sizes in steps of 32; steps <= wsteps.
-Kernel kernel_of(int tt, bool qx, int wsteps, int steps) {
+Choice kernel_of(int tt, bool qx, int wsteps, int steps) {
     return tt == 1 ? kernel_of<1>(qx, wsteps, steps) : tt == 2 ? kernel_of<2>(qx, wsteps, steps) : kernel_of<4>(qx, wsteps, steps);
+}
+
+// The kernel that stages the tokens for it (TT >= 2).
+template <int TT, bool QX>
+Kernel tokens_kernel_of(int steps) {
+    return steps == 1 ? qweight_tokens_kernel<TT, QX, 1> : steps == 2 ? qweight_tokens_kernel<TT, QX, 2> : qweight_tokens_kernel<TT, QX, 4>;
+}
+Kernel tokens_kernel_of(int tt, bool qx, int steps) {
+    if (tt == 2) return qx ? tokens_kernel_of<2, true>(steps) : tokens_kernel_of<2, false>(steps);
+    return qx ? tokens_kernel_of<4, true>(steps) : tokens_kernel_of<4, false>(steps);
 }
 
 void cluster_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int cluster, size_t smem) {
@@ -756,7 +1088,7 @@ cudaError_t qweight_prepare(QweightDevice& dev) {
             for (int wsteps = 1; wsteps <= 4; wsteps *= 2)
                 for (int steps = 1; steps <= wsteps; steps *= 2)
                     if (e == cudaSuccess)
-                        e = cudaFuncSetAttribute(kernel_of(tt, qx != 0, wsteps, steps),
+                        e = cudaFuncSetAttribute(kernel_of(tt, qx != 0, wsteps, steps).kernel,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     // clusters of each size that are resident at once, at the largest shared memory a launch takes
     for (int c = 1; c <= kMaxRanks && e == cudaSuccess; ++c) {
@@ -765,34 +1097,31 @@ cudaError_t qweight_prepare(QweightDevice& dev) {
         cluster_config(cfg, attr, c, kMaxSmem);
         cfg.gridDim = dim3((unsigned)c);
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&dev.clusters[c], kernel_of(2, true, 1, 1), &cfg);
+        e = cudaOccupancyMaxActiveClusters(&dev.clusters[c], kernel_of(2, true, 1, 1).kernel, &cfg);
         if (e == cudaSuccess && dev.clusters[c] < 1) dev.clusters[c] = 1;
     }
     return e;
 }
 
-cudaError_t launch_qweight(QweightParams& p, const QweightDevice& dev, int* grid, int* variant, int* cluster,
-                           cudaStream_t s) {
-    // Up to 32 tokens a CTA; more are further tiles, whose weights come from L2 (64 tokens in one tile
-    // need 200 registers a thread: spilled to 128 they took 139 us at R = 8, N = 7168, K = 2048).
-    const int tt = p.M <= 8 ? 1 : p.M <= 16 ? 2 : 4;
+// One launch over p.M tokens with token tiles of 8 tt.
+static cudaError_t launch_tiles(QweightParams& p, const QweightDevice& dev, int tt, int* grid, int* cluster,
+                                cudaStream_t s) {
     const int tok = tt * 8, wsteps = 1 << (p.group_shift - 5);
     const HostShape shape = tt == 1 ? host_shape<1>() : tt == 2 ? host_shape<2>() : host_shape<4>();
     const int rows = shape.rows, item = shape.item, ring = shape.ring, ld = shape.ld;
     const bool own = tt >= 2;
     const bool qx = p.qx && !p.xpow2;
     const int shift = qx && p.xgroup_shift < p.group_shift ? p.xgroup_shift : p.group_shift;
-    p.tiles_m = (p.M + tok - 1) / tok;
     const int64_t groups = (p.N + rows - 1) / rows;
     p.rtoks = p.M < tok ? (p.M + 1) / 2 * 2 : tok;
     const int slot = own ? 0 : p.rtoks * ld * 4;                // bytes of a group's sums beside the ring
     const int most = own ? kWarps : 24;                         // groups a CTA has room for
-    // Splits of a rank's K: those that leave the busiest CTA the fewest items, where a CTA more in
-    // the cluster's sum counts as one, and its start and end as four.
-    const int items_k = (p.K + item - 1) / item;
+    // Splits of a rank's K (of whole 256 k): those that leave the busiest CTA the fewest items, where a
+    // CTA more in the cluster's sum counts as one, and its start and end as four.
+    const int whole = 256 / item, items_k = (p.K + item - 1) / item;
     int64_t best = 0;
     for (int sp = 1; sp * p.R <= kMaxRanks && sp <= items_k; ++sp) {
-        const int per = (items_k + sp - 1) / sp;
+        const int per = ((items_k + sp - 1) / sp + whole - 1) / whole * whole;
         if ((items_k + per - 1) / per != sp) continue;  // a split would be empty
         const int resident = dev.clusters[sp * p.R];
         int64_t run = own ? kWarps : (groups * p.tiles_m + resident - 1) / resident;
@@ -807,34 +1136,75 @@ cudaError_t launch_qweight(QweightParams& p, const QweightDevice& dev, int* grid
         }
     }
     p.cluster = p.R * p.splits;
-    // K tile: at most `units` units of 8 k a thread, and as long as the tokens fit what the rest
-    // leaves; a multiple of an item and of 128
-    // (an item of 128 k holds its groups' scales whole: 128 is the largest group)
-    const int xstep = item * tok * 2 + (item >> shift) * tok * 4 + (qx ? item >> p.xgroup_shift : (item + 255) / 256) * tok * 4 +
-                      (item >> p.group_shift) * (p.run * rows + 1) * 4;
-    const int fixed = ring + 32 + (own ? 0 : (p.run + kWarps) * slot);
-    int room = (kMaxSmem - fixed) / xstep;
-    if (room > shape.units * 8 * kThreads / (tok * item)) room = shape.units * 8 * kThreads / (tok * item);
-    if (room < 1) return cudaErrorInvalidValue;
-    const int split_items = p.split_k / item;
-    p.tiles_k = (split_items + room - 1) / room;
-    const int tile_items = (split_items + p.tiles_k - 1) / p.tiles_k;
-    p.tiles_k = (split_items + tile_items - 1) / tile_items;
-    p.tile_k = tile_items * item;
-    size_t smem = (size_t)fixed + (size_t)tile_items * xstep;
-    const size_t sums = own ? (size_t)kWarps * p.rtoks * ld * 4 : 0;
-    if (smem < sums) smem = sums;
+    const int steps = 1 << (shift - 5);
+    const Choice k = kernel_of(tt, qx, wsteps, steps);
+    size_t smem = k.smem;
+    if (!own) {
+        // K tile: at most `units` units of 8 k a thread, and as long as the tokens fit what the rest
+        // leaves; a multiple of an item and of 128
+        // (an item of 128 k holds its groups' scales whole: 128 is the largest group)
+        const int xstep = item * tok * 2 + (item >> shift) * tok * 4 + (qx ? item >> p.xgroup_shift : (item + 255) / 256) * tok * 4 +
+                          (item >> p.group_shift) * (p.run * rows + 1) * 4;
+        const int fixed = ring + 32 + (p.run + kWarps) * slot;
+        const int units = shape.units * 8 * kThreads / (tok * item), split_items = p.split_k / item;
+        const int room = std::min((kMaxSmem - fixed) / xstep, units);
+        if (room < 1) return cudaErrorInvalidValue;
+        p.tiles_k = (split_items + room - 1) / room;
+        const int tile_items = (split_items + p.tiles_k - 1) / p.tiles_k;
+        p.tiles_k = (split_items + tile_items - 1) / tile_items;
+        p.tile_k = tile_items * item;
+        smem = (size_t)fixed + (size_t)tile_items * xstep;
+    }
 
     const int64_t runs = (groups + p.run - 1) / p.run;
     *cluster = p.cluster;
     *grid = (int)(runs * p.tiles_m * p.cluster);
-    *variant = tt;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
+    cfg.stream = s;
+    if (own) {
+        cluster_config(cfg, attr, 1, 0);
+        cfg.gridDim = dim3((unsigned)(p.R * p.tiles_m * (p.kp >> 8)));
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, tokens_kernel_of(tt, qx, steps), p);
+        if (e != cudaSuccess) return e;
+    }
     cluster_config(cfg, attr, p.cluster, smem);
     cfg.gridDim = dim3((unsigned)*grid);
-    cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, kernel_of(tt, qx, wsteps, 1 << (shift - 5)), p);
+    return cudaLaunchKernelEx(&cfg, k.kernel, p);
+}
+
+cudaError_t launch_qweight(QweightParams& p, const QweightDevice& dev, uint8_t* scratch, size_t scratch_bytes, int* grid,
+                           int* variant, int* cluster, cudaStream_t s) {
+    // Up to 8 tokens a CTA stages its own; with more, tiles of 16 or 32 are staged by a kernel before (each
+    // CTA staging them again took 30 to 50 % of the time at 16 and 64 tokens), as many at once as the
+    // scratch holds.  Rows too long for a tile of them go by 8 tokens.  More than 32 tokens a tile
+    // need 200 registers a thread: spilled to 128 they took 139 us at R = 8, M = 64, N = 7168, K = 2048.
+    int tt = p.M <= 8 ? 1 : p.M <= 16 ? 2 : 4;
+    p.kp = (p.K + 255) / 256 * 256;
+    // of a token tile: fp16 tokens, sums and scales of at least 32 k, and a flag word per 256 k
+    auto tile_bytes = [&](int t) { return (size_t)p.R * p.kp / 32 * (t * 8 * (64 + 4 + 4) + 4); };
+    if (tt > 1 && tile_bytes(tt) > scratch_bytes) tt = 1;
+    const int tok = tt * 8, M = p.M;
+    const int all = (M + tok - 1) / tok, most = tt == 1 ? all : (int)std::min<size_t>(all, scratch_bytes / tile_bytes(tt));
+    *variant = tt;
+    for (int first = 0; first < all; first += most) {
+        const int rest = M - first * tok;
+        p.tiles_m = std::min(most, all - first);
+        p.M = std::min(rest, p.tiles_m * tok);
+        const size_t k = (size_t)p.R * p.tiles_m * p.kp;
+        p.tokens = scratch;
+        p.sums = reinterpret_cast<float*>(scratch + k * tok * 2);
+        p.scales = p.sums + k / 32 * tok;
+        p.flags = reinterpret_cast<uint32_t*>(p.scales + k / 32 * tok);
+        const cudaError_t e = launch_tiles(p, dev, tt, grid, cluster, s);
+        if (e != cudaSuccess) return e;
+        for (int r = 0; r < p.R; ++r) {
+            p.x[r] = static_cast<const uint8_t*>(p.x[r]) + (size_t)p.M * p.K * (p.qx ? 1 : 2);
+            if (p.qx) p.xscale[r] = static_cast<const uint8_t*>(p.xscale[r]) + (size_t)p.M * p.xgroups * (p.xpow2 ? 1 : 4);
+        }
+        for (int v = 0; v < p.nviews; ++v) p.views[v] += (size_t)p.M * p.N;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace are
