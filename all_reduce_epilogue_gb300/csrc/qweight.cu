@@ -176,6 +176,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return v;
 }
 
+// Adds one; what was read from shared memory before is not read later, by this thread or by who sees the sum.
+__device__ __forceinline__ uint32_t atom_add_acq_rel(uint32_t* p) {
+    uint32_t v;
+    asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(v) : "r"(ptx::smem_u32(p)) : "memory");
+    return v;
+}
+
 // d (+)= a (weights) * b (tokens).
 template <bool FIRST>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -408,8 +415,9 @@ __global__ void __launch_bounds__(kThreads) qweight_tokens_kernel(const __grid_c
     if (threadIdx.x == 0) bad = 0u;
     const int chunks = p.kp >> 8, chunk = (int)blockIdx.x % chunks, b = (int)blockIdx.x / chunks;
     const int m0 = b % p.tiles_m * TOK, k0 = chunk * 256;
-    ptx::grid_launch_dependents();
+    // in this order: the kernel that follows knows that all that ran before this one has ended
     ptx::grid_wait();
+    ptx::grid_launch_dependents();
     const int fshift = QX ? p.xgroup_shift : 8;
     stage_tokens<TT, QX, STEPS == 4, GRAIN, TT>(
         p, b / p.tiles_m, m0, TOK, min(TOK, p.M - m0), k0, p.K, 256, p.tokens + ((size_t)b * p.kp + k0) * (TOK * 2),
@@ -451,9 +459,9 @@ __device__ __forceinline__ void products(uint64_t (&acc)[Shape<TT>::RT][TT][2], 
     constexpr int TOK = S::TOK, RT = S::RT, PITCH = S::PITCH;
     constexpr bool OWN = S::OWN;
     constexpr bool WIDE = STEPS == 4;  // a lane reads its 32 codes of 128 at once: all of them share the scales
-    // Four token tiles take the 128 k in two parts, whose operands fit the registers; TB tiles at a time, CH chains
-    // of sums each: a dependent instruction waits for the one before it (OWN: two row tiles are two chains).
-    constexpr int PARTS = TT == 4 ? 2 : 1, SP = 4 / PARTS, TB = TT == 2 ? 2 : 1, CH = OWN ? 1 : 2;
+    // Two row tiles take the 128 k in two parts, whose operands fit the registers, and TB token tiles at a time; one
+    // takes CH chains of sums: a dependent instruction waits for the one before it.
+    constexpr int PARTS = OWN ? 2 : 1, SP = 4 / PARTS, TB = OWN ? 2 : 1, CH = OWN ? 1 : 2;
     constexpr bool KEEP = STEPS > SP;  // a group's sums outlive a part
     float d[KEEP ? TT : TB][RT][CH][4];
 #pragma unroll
@@ -851,8 +859,8 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
     float* xsc = xsum + 2 * W::XSUM;
     uint32_t* wsc = reinterpret_cast<uint32_t*>(xsc + 2 * W::XSC);        // [buffer][group][WROWS]: scale | zero point << 16, in bf16
     uint32_t* bad = wsc + 2 * W::WSC;
-    uint32_t* issued = bad + 1;                                           // tiles copied so far
-    volatile uint32_t* abort = bad + 2;                                   // a wait has run out
+    volatile uint32_t* abort = bad + 1;                                   // a wait has run out
+    uint32_t* left = bad + 2;                                             // by buffer: warps that have left a tile, of all so far
     uint64_t* full = reinterpret_cast<uint64_t*>(bad + 4);                // a buffer's copies have landed
     float* red = reinterpret_cast<float*>(qw_smem);                       // the ring's place, when the products are done
 
@@ -883,26 +891,26 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
         cp_commit();
     };
 
-    // a tile of the staged tokens, by one thread
+    // a tile of the staged tokens, by one thread: the first two at the start, then by the warp that is the last
+    // to leave the tile two before
     const int b = r * p.tiles_m + tile % p.tiles_m;
     auto copy_tile = [&](int tl) {
         const int t0 = kbeg + tl * TILE, kl = min(TILE, min(kbeg + p.split_k, p.kp) - t0), buf = tl & 1;
         const size_t at = (size_t)b * p.kp + t0;
         const uint32_t nx = (uint32_t)kl * (TOK * 2), ns = (uint32_t)(kl / GRAIN) * (TOK * 4), nf = (uint32_t)(kl >> fshift) * (TOK * 4);
-        *issued = (uint32_t)tl + 1u;
         ptx::mbar_arrive_expect_tx(&full[buf], nx + ns + nf);
         ptx::bulk_load(xs + buf * W::XS, p.tokens + at * (TOK * 2), nx, &full[buf]);
         ptx::bulk_load(xsum + buf * W::XSUM, p.sums + at / GRAIN * TOK, ns, &full[buf]);
         ptx::bulk_load(xsc + buf * W::XSC, p.scales + (at >> fshift) * TOK, nf, &full[buf]);
     };
 
-    // The rows' scales and zero points of a tile, STEP rows apart, NE of them with an item: neighbouring lanes
-    // take a row's neighbouring groups; what does not exist weighs nothing.
-    constexpr int TG = TILE / (WSTEPS * 32), STEP = kThreads / TG, NE = TG / PER;
-    static_assert(kWarps * ROWS == kThreads && NE * PER == TG, "an item's share of the scales");
+    // The scales and zero points of the warp's rows in a tile, STEP rows apart, NE of them with an item: neighbouring
+    // lanes take a row's neighbouring groups; what does not exist weighs nothing.
+    constexpr int TG = TILE / (WSTEPS * 32), STEP = 32 / TG, NE = TG / PER;
+    static_assert(ROWS == 32 && NE * PER == TG, "an item's share of the scales");
     const bool zeros = p.zero[r] != nullptr;
-    const int wgi = threadIdx.x % TG, wrow = threadIdx.x / TG, wleft = p.N - group0 * ROWS;
-    const int64_t wbase = (int64_t)group0 * ROWS * p.groups;  // the CTA's rows are within 2^31 of it
+    const int wgi = lane % TG, wrow = lane / TG;
+    const int64_t wbase = (int64_t)frow * p.groups;  // the warp's rows are within 2^31 of it
     uint32_t sv[NE], zv[NE];
     auto load_scales = [&](int tl, int kk) {
         const int gi = (kbeg + tl * TILE) / (WSTEPS * 32) + wgi;
@@ -910,14 +918,14 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
         for (int j = 0; j < NE; ++j) {
             const int row = wrow + (kk * NE + j) * STEP;
             const int64_t at = wbase + (row * p.groups + gi);
-            const bool in = gi < p.groups && row < wleft;
+            const bool in = gi < p.groups && row < fn;
             sv[j] = 0u;
             zv[j] = 8u;
             ldg_u16_if(sv[j], p.scale[r] + at, in);
             ldg_u8_if(zv[j], p.zero[r] + at, in && zeros);
         }
     };
-    uint32_t* wto = wsc + wgi * WROWS + wrow;
+    uint32_t* wto = wsc + wgi * WROWS + warp * ROWS + wrow;
     auto store_scales = [&](int tl, int kk) {
 #pragma unroll
         for (int j = 0; j < NE; ++j) wto[(tl & 1) * W::WSC + (kk * NE + j) * STEP] = scale_word(sv[j], zv[j]);
@@ -925,6 +933,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
 
     if (threadIdx.x == 0) {
         *bad = 0u;
+        left[0] = left[1] = 0u;
         *abort = 0u;
         ptx::mbar_init(&full[0], 1);
         ptx::mbar_init(&full[1], 1);
@@ -932,17 +941,20 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
         ptx::fence_proxy_async_shared();
     }
     ptx::grid_launch_dependents();
-    ptx::grid_wait();
+    // The kernel before is the one that stages the tokens, and lets this one start when all that ran before it has
+    // ended: the weights can be read, the tokens after the wait.
     fetch(ring);
     fetch(ring + SLOT);
-    if (threadIdx.x == 0) {
-        ptx::fence_proxy_async_global();
-        copy_tile(0);
-    }
-    __syncthreads();  // the barriers and `bad`
     for (int kk = 0; kk < PER; ++kk) {
         load_scales(0, kk);
         store_scales(0, kk);
+    }
+    ptx::grid_wait();
+    __syncthreads();  // the barriers and `bad`
+    if (threadIdx.x == 0) {
+        ptx::fence_proxy_async_global();
+        copy_tile(0);
+        if (tiles > 1) copy_tile(1);
     }
     if (!QX) {
         const int chunks = ((kend + 255) >> 8) - (kbeg >> 8);
@@ -968,14 +980,12 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
     for (int tl = 0; tl < tiles; ++tl) {
         const int buf = tl & 1;
         tile_wait(&full[buf], (uint32_t)(tl >> 1) & 1u, abort, p);
-        __syncthreads();  // the weights' scales are there, and every warp is done with the tile before
         const bool more = tl + 1 < tiles;
-        if (threadIdx.x == 0 && more && !*abort) copy_tile(tl + 1);
-#pragma unroll 1
+#pragma unroll(TT == 2 ? PER : 1)
         for (int kk = 0; kk < PER; ++kk) {
             if (more) load_scales(tl + 1, kk);
             cp_wait<DEPTH - 2>();
-            __syncwarp();  // every lane's copies have landed, and every lane has left the slot refilled now
+            __syncwarp();  // every lane's copies have landed, its scales are stored, and it has left the slot refilled now
             const uint32_t next = cur + SLOT == ring_end ? ring : cur + SLOT;
             fetch(next + SLOT == ring_end ? ring : next + SLOT);
             if (active && kbeg + tl * TILE + kk * ITEM < kend)
@@ -987,17 +997,21 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
             cur = next;
             if (more) store_scales(tl + 1, kk);
         }
+        // a warp is at most a tile ahead of another (its next tile's copies start when all have left this one), so
+        // the count of this tile is whole before one of the next but one begins
+        __syncwarp();
+        if (lane == 0 && tl + 2 < tiles && !*abort && atom_add_acq_rel(&left[buf]) % kWarps == kWarps - 1) copy_tile(tl + 2);
     }
     cp_wait<0>();
+    __syncthreads();
     if (threadIdx.x == 0 && *abort) {  // the CTA must not end before its copies have landed
-        const int n = (int)*issued;
+        const int n = min(tiles, (int)(left[0] / kWarps + left[1] / kWarps) + 2);
         for (int tl = max(n - 2, 0); tl < n; ++tl) {
             const uint64_t t0 = ptx::globaltimer();
             while (!ptx::mbar_try_wait(&full[tl & 1], (uint32_t)(tl >> 1) & 1u))
                 if (ptx::globaltimer() - t0 > p.timeout_ns) break;
         }
     }
-    __syncthreads();
     if (active) {
         float* to = red + warp * p.rtoks * LD + g;
 #pragma unroll
