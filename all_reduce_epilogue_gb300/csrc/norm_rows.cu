@@ -370,8 +370,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
     int s = 0, buf = 0;
     uint32_t ph = 0;
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, buf ^= 1) {
-        float dy[PPT][8];
-        uint4 hv[PPT], ev[PPT];
+        float dy[ONE ? 1 : PPT][8];
+        uint4 dv[ONE ? PPT : 1], hv[PPT], ev[PPT];  // one rank's dy stays packed
         float c1 = 0.f, c2 = 0.f;
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
@@ -380,7 +380,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
                 ring_wait(&g.full[s], ph, g, p);
                 const uint8_t* at = g.stage + (size_t)s * p.stage_bytes + t * 16;
                 if (pk < P) {
-                    sum_ranks<ONE>(at, p.R, step, dy[k]);
+                    float(&d)[8] = dy[ONE ? 0 : k];
+                    sum_ranks<ONE>(at, p.R, step, d);
+                    if (ONE) dv[k] = *reinterpret_cast<const uint4*>(at);
                     hv[k] = *reinterpret_cast<const uint4*>(at + p.R * step);
                     if (p.has_res) ev[k] = *reinterpret_cast<const uint4*>(at + (p.R + 1) * step);
                     float h[8], gk[8];
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         c1 = fmaf(h[i], h[i], c1);
-                        c2 = fmaf(dy[k][i] * gk[i], h[i], c2);
+                        c2 = fmaf(d[i] * gk[i], h[i], c2);
                     }
                 }
                 __syncwarp();
@@ -418,11 +420,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
                     *reinterpret_cast<float4*>(&gk[0]) = reinterpret_cast<const float4*>(g.gamma)[pk * 2];
                     *reinterpret_cast<float4*>(&gk[4]) = reinterpret_cast<const float4*>(g.gamma)[pk * 2 + 1];
                     if (p.has_res) unpack8(ev[k], e);
+                    float(&d)[8] = dy[ONE ? 0 : k];
+                    if (ONE) unpack8(dv[k], d);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float xh = h[i] * inv;
-                        o[i] = fmaf(dy[k][i] * gk[i], inv, fmaf(-xh, m, e[i]));
-                        dg[k][i] = fmaf(dy[k][i], xh, dg[k][i]);
+                        o[i] = fmaf(d[i] * gk[i], inv, fmaf(-xh, m, e[i]));
+                        dg[k][i] = fmaf(d[i], xh, dg[k][i]);
                     }
                     ptx::st_stream_v4(p.res_out + row * (int64_t)p.N + pk * 8, pack8(o));
                 }
@@ -481,12 +485,15 @@ __global__ void __launch_bounds__(256) dgamma_sum_kernel(const float* part, floa
 }
 
 // Packs a thread holds, of a row of P.  Forward: about 256 threads a block.
-// Backward, whose state is 24 registers a pack: up to 2 packs in blocks like
-// the forward's; 3 and 4 in blocks of at most 256 threads with the producer's,
-// so that two blocks of 128 registers a thread share an SM; rows too wide for
-// that take the SM for one block.
+// Backward, whose state is 24 registers a pack (20 with one rank): up to 256
+// threads, two blocks an SM; above, as few packs as 16 warps allow, which may
+// have 128 registers each (17 warps: 96) in one block an SM.  R = 3,
+// 1001 x 5000: two packs 16 us, three in two blocks an SM 17; R = 8,
+// 4096 x 7168: two packs 97 us, four in two blocks 102; R = 4, 2048 x 10240:
+// three packs 51 us, in 17 warps 71, eight 81; 2048 x 16384: five packs 106 us,
+// four in 17 warps 115, eight 132.
 int packs_per_thread(int P) { return P <= 256 ? 1 : P <= 512 ? 2 : P <= 2048 ? 4 : 8; }
-int backward_packs_per_thread(int P) { return P <= 256 ? 1 : P <= 512 ? 2 : P <= 672 ? 3 : P <= 1024 ? 4 : 8; }
+int backward_packs_per_thread(int P) { return P <= 256 ? 1 : P <= 960 ? 2 : P <= 1440 ? 3 : P <= 1920 ? 4 : 5; }
 
 // Launches on the programmatic dependency: the kernel comes up while the one
 // before it in the stream runs out, and waits for its end before it touches
@@ -520,7 +527,7 @@ RowsPlan rows_plan(RowsParams& p, int num_sms) {
     p.nt = ((P + plan.ppt - 1) / plan.ppt + 31) / 32 * 32;
     p.slices = (P + p.nt - 1) / p.nt;
     p.stage_bytes = p.nsrc * p.nt * 16;
-    const int blocks = p.nt <= (p.backward && plan.ppt > 2 ? 224 : 256) && p.M > num_sms ? 2 : 1;
+    const int blocks = p.nt <= 256 && p.M > num_sms ? 2 : 1;
     const size_t fixed = (p.backward ? (size_t)p.N * 4 : 0) + kRedWords * 4 + 2 * kMaxStages * 8 + 16;
     const size_t room = (blocks == 2 ? kRowsSmemPair : kRowsSmemLimit) - fixed;
     p.stages = (int)(room / p.stage_bytes);
@@ -546,10 +553,10 @@ template <bool ONE>
 void (*backward_kernel(int ppt, int threads))(RowsParams) {
     switch (ppt) {
         case 1: return norm_backward_rows_kernel<1, ONE, 288, 2>;
-        case 2: return norm_backward_rows_kernel<2, ONE, 288, 2>;
-        case 3: return norm_backward_rows_kernel<3, ONE, 256, 2>;
-        case 4: return threads <= 256 ? norm_backward_rows_kernel<4, ONE, 256, 2> : norm_backward_rows_kernel<4, ONE, 288, 1>;
-        default: return norm_backward_rows_kernel<8, ONE, 288, 1>;
+        case 2: return threads <= 288 ? norm_backward_rows_kernel<2, ONE, 288, 2> : norm_backward_rows_kernel<2, ONE, 512, 1>;
+        case 3: return norm_backward_rows_kernel<3, ONE, 512, 1>;
+        case 4: return norm_backward_rows_kernel<4, ONE, 512, 1>;
+        default: return norm_backward_rows_kernel<5, ONE, 512, 1>;
     }
 }
 
@@ -560,8 +567,8 @@ cudaError_t rows_prepare() {
             if (e == cudaSuccess) e = opt_in(quant_kernel<false>(ppt, threads));
             if (e == cudaSuccess) e = opt_in(quant_kernel<true>(ppt, threads));
         }
-    for (int ppt : {1, 2, 3, 4, 8})
-        for (int threads : {256, 288})
+    for (int ppt : {1, 2, 3, 4, 5})
+        for (int threads : {288, 512})
             for (bool one : {false, true})
                 if (e == cudaSuccess)
                     e = opt_in(one ? backward_kernel<true>(ppt, threads) : backward_kernel<false>(ppt, threads));
