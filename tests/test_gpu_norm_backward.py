@@ -36,7 +36,8 @@ def run(ws, dy, h, gamma, dres, dgamma=True, dh=None):
 @pytest.mark.parametrize("R,M,N,dres", [(1, 1, 8, True), (8, 1, 7168, True), (2, 2, 40, False), (3, 7, 264, True),
                                         (1, 151, 1024, True), (1, 1000, 2048, False), (5, 305, 2056, True),
                                         (4, 33, 4096, False), (8, 620, 4104, True), (3, 9, 5000, True), (8, 311, 7168, True),
-                                        (8, 2, 8192, False), (2, 160, 8200, True), (8, 157, 16384, True), (1, 2500, 64, True)])
+                                        (8, 2, 8192, False), (2, 160, 8200, True), (8, 157, 16384, True), (1, 2500, 64, True),
+                                        (1, 400, 7680, True), (3, 200, 7688, False), (4, 170, 11528, True), (1, 160, 15368, True)])
 def test_against_64_bits(ws, R, M, N, dres):
     dy, h, gamma, e = inputs(R, M, N, 100 * R + M + N, dres)
     if M > 4:

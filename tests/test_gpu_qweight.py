@@ -262,3 +262,109 @@ def test_power_of_two_scales_of_any_size(ws, M):
     keep = [i for i in range(M) if i not in nan]
     assert out[nan].isnan().all()
     ref.check(out[keep], want[keep], tol[keep] + 2.0 ** -133, "out")
+
+
+@pytest.mark.parametrize("M", [12, 40])
+def test_values_that_are_not_finite_in_wide_tiles(ws, M):
+    """NaN and infinities in the first, a middle and the last token and k of staged tiles."""
+    R, N, K = 3, 72, 832
+    w, g = weights(R, N, K, 64, False, 31 + M)
+    w[0][0].fill_(0x99)  # every weight of rank 0: 1 * scale
+    x = [torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(R)]
+    x[0][0, 0] = float("-inf")
+    x[2][M // 2, 255] = float("nan")
+    x[0][M - 1, K - 1] = float("inf")
+    x[0][M - 1, 256] = float("inf")
+    y, _ = run(ws, x, w, 64)
+    assert (y[0] == float("-inf")).all() and y[M // 2].isnan().all() and (y[M - 1] == float("inf")).all()
+    keep = [m for m in range(M) if m not in (0, M // 2, M - 1)]
+    want, tol = ref.linear64([t[keep] for t in x], w, 64)
+    ref.check(y[keep], want, tol, "out")
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 72, 4096), (20, 64, 32768), (9, 40, 40000), (70, 24, 20000)])
+@pytest.mark.parametrize("eight", [False, True])
+def test_more_tokens_than_the_staging_buffer_holds(M, N, K, eight):
+    """A workspace for one rank: tokens that go in several parts, and rows too long to be staged at all."""
+    need_gpu()
+    with are.Workspace(R_max=1, M_max=1, N_max=8) as small:
+        w, g = weights(1, N, K, 32, True, M + K)
+        x = [torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16)]
+        big = torch.full((M + 1, N), 5.0, dtype=torch.bfloat16, device="cuda")
+        _, vals = run(small, x, w, 32, 32 if eight else None, False, out=big[:M])
+        want, tol = ref.linear64(vals, w, 32)
+        ref.check(big[:M], want, tol, "out")
+        assert (big[M] == 5).all()
+
+
+def test_operands_written_just_before(ws):
+    """Weights, scales and tokens that the kernel before in the stream writes, call after call into the same buffers."""
+    for M in (2, 16, 40):
+        R, N, K = 4, 512, 1024
+        sets = [weights(R, N, K, 128, True, 50 + i)[0] for i in range(3)]
+        g = torch.Generator(device="cuda").manual_seed(M)
+        xs = [[torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(R)] for _ in range(3)]
+        w = [tuple(torch.zeros_like(t) for t in r) for r in sets[0]]
+        qw = [are.QWeight(*t, 128) for t in w]
+        x = [torch.zeros_like(t) for t in xs[0]]
+        outs = [torch.empty((M, N), dtype=torch.bfloat16, device="cuda") for _ in range(9)]
+
+        def step(i, out):
+            for r in range(R):
+                for to, of in zip(w[r], sets[i % 3][r]):
+                    to.copy_(of)
+                x[r].copy_(xs[i * 2 % 3][r])
+            are.gemm_ar_qweight(x, qw, out, ws)
+
+        for i in range(3):  # with time in between
+            step(i, outs[i])
+            torch.cuda.synchronize()
+        want = [o.clone() for o in outs[:3]]
+        for i in range(9):
+            step(i, outs[i])
+        torch.cuda.synchronize()
+        assert all(torch.equal(outs[i], want[i % 3]) for i in range(9))
+        for o in outs:
+            o.zero_()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            for i in range(9):
+                step(i, outs[i])
+        for _ in range(2):
+            gr.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(outs[i], want[i % 3]) for i in range(9))
+
+
+def test_calls_in_a_row_share_the_staging_buffer(ws):
+    """Different layers back to back, by themselves and as two captured graphs: each sees its own tokens."""
+    layers = []
+    for i, (R, M, N, K, group) in enumerate([(8, 16, 256, 512, 64), (2, 40, 520, 1056, 32), (8, 33, 72, 2048, 128),
+                                             (1, 10, 1024, 256, 128), (3, 5, 136, 160, 32)]):
+        w, g = weights(R, N, K, group, True, 70 + i)
+        x = [torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(R)]
+        out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+        layers.append(([are.QWeight(*t, group) for t in w], x, out, ref.linear64(x, w, group)))
+
+    def step(ls):
+        for qw, x, out, _ in ls:
+            are.gemm_ar_qweight(x, qw, out, ws)
+
+    def look():
+        torch.cuda.synchronize()
+        for _, _, out, (want, tol) in layers:
+            ref.check(out, want, tol, "out")
+            out.zero_()
+
+    for _ in range(3):
+        step(layers)
+    look()
+    graphs = []
+    for part in (layers[:3], layers[3:]):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            step(part)
+    for _ in range(3):
+        for gr in graphs:
+            gr.replay()
+    look()
