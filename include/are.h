@@ -49,6 +49,10 @@
  *    (tile masks at 0, staging words at -0.0) is restored inside those
  *    kernels, never by a host step, so every replay finds it as the capture
  *    did.  Workspace creation, reset and snapshots are not capturable.
+ *  - are_allreduce_rmsnorm_quant_groups, are_allreduce_rmsnorm_backward and the
+ *    4-bit linears launch with programmatic stream serialisation: their
+ *    kernels may come up while earlier work of the stream still runs, and
+ *    touch global memory only when all of it has ended.
  *  - Every argument is validated before anything is launched: on any error
  *    nothing is launched and nothing is written.
  *  - Device-side waits are bounded by the workspace's timeout.  A wait that
@@ -219,14 +223,15 @@ ARE_API const char* are_status_string(are_status s);
  *  GEMM_AR: 1 <= R <= 8; K % 8 == 0; N % 8 == 0.
  *  ALLREDUCE_RMSNORM: 1 <= R <= 8; N % 8 == 0 (16-byte packs); N <= 32768.
  *  ALLREDUCE_RMSNORM_BACKWARD: as ALLREDUCE_RMSNORM, with N <= 16384.
- *  GEMM_AR_QWEIGHT: 1 <= R <= 8; K % 32 == 0 (16-byte rows of codes); N % 8 == 0;
- *           ceil(M / 8) * ceil(N / 16) < 2^28.
+ *  GEMM_AR_QWEIGHT: 1 <= R <= 8; K % 32 == 0 (16-byte rows of codes) and
+ *           K <= 2^24; N % 8 == 0; ceil(M / 8) * ceil(N / 16) < 2^28.
  * K is ignored for the two ALLREDUCE_RMSNORM operations.  Pure host function: no device needed. */
 ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
 
 /* Create a workspace on the current CUDA device: tile masks, the per-rank
  * partial buffer, the Lamport staging buffer (filled with the sentinel, on a
- * private stream, synchronously) and the device status word.
+ * private stream, synchronously), partial sums of dgamma, 2 MiB a rank of
+ * staged tokens for the 4-bit linear, and the device status word.
  * ROCm/mori PR #662, review threads: every capacity is validated before the
  * first allocation; buffer offsets are sized from the capacities, never from
  * a call's M, so the layout does not move between calls; a set-up that fails
@@ -529,12 +534,21 @@ typedef struct are_qweight {
  *  group   : 32, 64 or 128 consecutive k; the last group may be shorter
  *  out[v]  : bf16 [M, N] for every rank view v < R, as in are_gemm_ar (views
  *            may alias; identical pointers are written once)
- *  Result  : out[v][m][n] = bf16( sum_r sum_k x[r][m][k] * w_r(n, k) ); the
- *            codes enter exactly, group sums, scales and the sum over k and
- *            over r = 0..R-1 are in fp32, and the result is rounded once
- *            (a rank's partial is not rounded, as in are_gemm_rs).
- * K == 0 writes zeros.  Any M is computed; it is made for few (up to 64 tokens
- * read the weights once).  Needs no capacity of the workspace but R <= R_max.
+ *  Result  : out[v][m][n] = bf16( sum_r sum_k x[r][m][k] * w_r(n, k) ), formed
+ *            per group as (sum_k u x - zero * sum_k x) * scale: codes, zero
+ *            points and scales enter exactly; the group's sums, their
+ *            difference (whose error is relative to sum |u x|), and the sums
+ *            over groups and over r = 0..R-1 are in fp32, and the result is
+ *            rounded once (a rank's partial is not rounded, as in are_gemm_rs).  Tokens enter the products in fp16,
+ *            scaled by a power of two per token and 256 of k: values down to
+ *            2^-27 times the largest of the 256 exactly, smaller ones to
+ *            2^-35 of it, which is below the fp32 sums' rounding.  A value that
+ *            is not finite makes that token's outputs what the products give.
+ * K == 0 writes zeros.  Any M is computed; it is made for few: tiles of 8, 16 or
+ * 32 tokens, each of which reads the weights, from memory once for those that
+ * run together.  With M > 8 the tokens are first laid out in a buffer of the
+ * workspace, in several parts if it does not hold them.  Needs no capacity of
+ * the workspace but R <= R_max.
  */
 ARE_API are_status are_gemm_ar_qweight(const are_bf16* const x[], const are_qweight w[], int group,
                                        are_bf16* const out[], int R, int64_t M, int64_t N, int64_t K, are_ws* ws,
@@ -547,8 +561,10 @@ ARE_API are_status are_gemm_ar_qweight(const are_bf16* const x[], const are_qwei
  *  xscale[r]   : [M, ceil(K / xgroup)], fp32 or E8M0 bytes; aligned to its element
  *  scale_format: are_scale_format
  *  xgroup      : 32, 64 or 128, independent of `group`
- * The other arguments and the arithmetic are as for are_gemm_ar_qweight; the
- * token scales are applied in fp32 to the group sums.
+ * The other arguments and the arithmetic are as for are_gemm_ar_qweight.  fp32
+ * token scales are applied in fp32 to the sums of each shared group of k; E8M0
+ * scales go into the fp16 tokens relative to the largest of each 256 of k: what
+ * is 2^-30 of it or less is off by at most 2^-34 of it.
  */
 ARE_API are_status are_gemm_ar_qweight_qx(const uint8_t* const xq[], const void* const xscale[], int scale_format,
                                           int xgroup, const are_qweight w[], int group, are_bf16* const out[], int R,
