@@ -1093,62 +1093,56 @@ HostShape host_shape() {
     return {S::ROWS, S::ITEM, S::RING, S::LD, S::UNITS};
 }
 
-}  // namespace
+HostShape host_shape(int tt) { return tt == 1 ? host_shape<1>() : tt == 2 ? host_shape<2>() : host_shape<4>(); }
 
-cudaError_t qweight_prepare(QweightDevice& dev) {
-    cudaError_t e = cudaSuccess;
-    for (int tt = 1; tt <= 4; tt *= 2)
-        for (int qx = 0; qx < 2; ++qx)
-            for (int wsteps = 1; wsteps <= 4; wsteps *= 2)
-                for (int steps = 1; steps <= wsteps; steps *= 2)
-                    if (e == cudaSuccess)
-                        e = cudaFuncSetAttribute(kernel_of(tt, qx != 0, wsteps, steps).kernel,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    // clusters of each size that are resident at once, at the largest shared memory a launch takes
-    for (int c = 1; c <= kMaxRanks && e == cudaSuccess; ++c) {
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[2];
-        cluster_config(cfg, attr, c, kMaxSmem);
-        cfg.gridDim = dim3((unsigned)c);
-        cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&dev.clusters[c], kernel_of(2, true, 1, 1).kernel, &cfg);
-        if (e == cudaSuccess && dev.clusters[c] < 1) dev.clusters[c] = 1;
+// How a launch over p.M tokens in tiles of 8 tt is cut, and what it is expected to cost, in items of 2 KB of codes.
+struct Cut {
+    int splits, split_k, run;
+    int64_t cost;
+};
+
+// Splits of a rank's K (of whole 256 k): of what the busiest CTA does one after the other, its items, its start and
+// end, and a little for each CTA more that the cluster adds up.
+//  * tt = 1: items of 16 rows x 256 k, the run's by all warps; staging a token's 256 k costs as half an item.
+//    (R = 1, 4096 x 4096, 8 tokens: 8.2 us in clusters of 8; 14.8 without a split, each CTA staging all of K.)
+//  * tt = 2, 4: items of 32 rows x 128 k, a warp each; one with 32 tokens takes 15/8 as long as with 16.
+//    (R = 8, 7168 x 2048: 23 us a launch of one wave with 16, 38 with 32.)
+Cut cut_of(const QweightParams& p, const QweightDevice& dev, int tt) {
+    const HostShape shape = host_shape(tt);
+    const bool own = tt >= 2;
+    const int64_t groups = (p.N + shape.rows - 1) / shape.rows, tiles_m = (p.M + tt * 8 - 1) / (tt * 8);
+    const int most = own ? kWarps : 24;  // groups a CTA has room for
+    const int whole = 256 / shape.item, items_k = (p.K + shape.item - 1) / shape.item;
+    Cut best{};
+    for (int sp = 1; sp * p.R <= kMaxRanks && sp <= items_k; ++sp) {
+        const int per = ((items_k + sp - 1) / sp + whole - 1) / whole * whole;
+        if ((items_k + per - 1) / per != sp) continue;  // a split would be empty
+        const int resident = dev.clusters[sp * p.R];
+        const int64_t run = own ? kWarps : std::min<int64_t>((groups * tiles_m + resident - 1) / resident, most);
+        const int64_t waves = ((groups + run - 1) / run * tiles_m + resident - 1) / resident;
+        const int64_t busiest = own ? (tt == 2 ? 8 * per + 4 : 15 * per + 8) : run * per + std::min(p.M, 8) * per / 2 + 20;
+        const int64_t cost = waves * busiest + (own ? 1 : 2) * sp;
+        if (best.cost == 0 || cost < best.cost) best = Cut{sp, per * shape.item, (int)run, cost};
     }
-    return e;
+    return best;
 }
 
 // One launch over p.M tokens with token tiles of 8 tt.
-static cudaError_t launch_tiles(QweightParams& p, const QweightDevice& dev, int tt, int* grid, int* cluster,
-                                cudaStream_t s) {
+cudaError_t launch_tiles(QweightParams& p, const QweightDevice& dev, int tt, int* grid, int* cluster, cudaStream_t s) {
     const int tok = tt * 8, wsteps = 1 << (p.group_shift - 5);
-    const HostShape shape = tt == 1 ? host_shape<1>() : tt == 2 ? host_shape<2>() : host_shape<4>();
+    const HostShape shape = host_shape(tt);
     const int rows = shape.rows, item = shape.item, ring = shape.ring, ld = shape.ld;
     const bool own = tt >= 2;
     const bool qx = p.qx && !p.xpow2;
     const int shift = qx && p.xgroup_shift < p.group_shift ? p.xgroup_shift : p.group_shift;
     const int64_t groups = (p.N + rows - 1) / rows;
+    p.tiles_m = (p.M + tok - 1) / tok;
     p.rtoks = p.M < tok ? (p.M + 1) / 2 * 2 : tok;
     const int slot = own ? 0 : p.rtoks * ld * 4;                // bytes of a group's sums beside the ring
-    const int most = own ? kWarps : 24;                         // groups a CTA has room for
-    // Splits of a rank's K (of whole 256 k): those that leave the busiest CTA the fewest items, where a
-    // CTA more in the cluster's sum counts as one, and its start and end as four.
-    const int whole = 256 / item, items_k = (p.K + item - 1) / item;
-    int64_t best = 0;
-    for (int sp = 1; sp * p.R <= kMaxRanks && sp <= items_k; ++sp) {
-        const int per = ((items_k + sp - 1) / sp + whole - 1) / whole * whole;
-        if ((items_k + per - 1) / per != sp) continue;  // a split would be empty
-        const int resident = dev.clusters[sp * p.R];
-        int64_t run = own ? kWarps : (groups * p.tiles_m + resident - 1) / resident;
-        if (run > most) run = most;
-        const int64_t waves = ((groups + run - 1) / run * p.tiles_m + resident - 1) / resident;
-        const int64_t cost = waves * (run * per + 4) + sp;
-        if (best == 0 || cost < best) {
-            best = cost;
-            p.splits = sp;
-            p.split_k = per * item;
-            p.run = (int)run;
-        }
-    }
+    const Cut cut = cut_of(p, dev, tt);
+    p.splits = cut.splits;
+    p.split_k = cut.split_k;
+    p.run = cut.run;
     p.cluster = p.R * p.splits;
     const int steps = 1 << (shift - 5);
     const Choice k = kernel_of(tt, qx, wsteps, steps);
@@ -1187,25 +1181,51 @@ static cudaError_t launch_tiles(QweightParams& p, const QweightDevice& dev, int 
     return cudaLaunchKernelEx(&cfg, k.kernel, p);
 }
 
+}  // namespace
+
+cudaError_t qweight_prepare(QweightDevice& dev) {
+    cudaError_t e = cudaSuccess;
+    for (int tt = 1; tt <= 4; tt *= 2)
+        for (int qx = 0; qx < 2; ++qx)
+            for (int wsteps = 1; wsteps <= 4; wsteps *= 2)
+                for (int steps = 1; steps <= wsteps; steps *= 2)
+                    if (e == cudaSuccess)
+                        e = cudaFuncSetAttribute(kernel_of(tt, qx != 0, wsteps, steps).kernel,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    // clusters of each size that are resident at once, at the largest shared memory a launch takes
+    for (int c = 1; c <= kMaxRanks && e == cudaSuccess; ++c) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        cluster_config(cfg, attr, c, kMaxSmem);
+        cfg.gridDim = dim3((unsigned)c);
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&dev.clusters[c], kernel_of(2, true, 1, 1).kernel, &cfg);
+        if (e == cudaSuccess && dev.clusters[c] < 1) dev.clusters[c] = 1;
+    }
+    return e;
+}
+
 cudaError_t launch_qweight(QweightParams& p, const QweightDevice& dev, uint8_t* scratch, size_t scratch_bytes, int* grid,
                            int* variant, int* cluster, cudaStream_t s) {
-    // Up to 8 tokens a CTA stages its own; with more, tiles of 16 or 32 are staged by a kernel before (each
-    // CTA staging them again took 30 to 50 % of the time at 16 and 64 tokens), as many at once as the
-    // scratch holds.  Rows too long for a tile of them go by 8 tokens.  More than 32 tokens a tile
-    // need 200 registers a thread: spilled to 128 they took 139 us at R = 8, M = 64, N = 7168, K = 2048.
-    int tt = p.M <= 8 ? 1 : p.M <= 16 ? 2 : 4;
+    // Up to 8 tokens a CTA stages its own (R = 8, 8 tokens, 7168 x 2048: 19.7 us, a staging kernel before 22.9; R = 2,
+    // 512 x 512: 5.1 us and 6.1).  With more, tiles of 16 or 32, whichever is expected to end first, are
+    // staged by a kernel before (each CTA staging them again took 30 to 50 % of the time at 16 and 64
+    // tokens), as many at once as the scratch holds.  Rows too long for a tile of them go by 8 tokens.
+    // More than 32 tokens a tile need 200 registers a thread: spilled to 128 they took 139 us at R = 8,
+    // M = 64, N = 7168, K = 2048, tiles of 32 take 75.
     p.kp = (p.K + 255) / 256 * 256;
     // of a token tile: fp16 tokens, sums and scales of at least 32 k, and a flag word per 256 k
     auto tile_bytes = [&](int t) { return (size_t)p.R * p.kp / 32 * (t * 8 * (64 + 4 + 4) + 4); };
-    if (tt > 1 && tile_bytes(tt) > scratch_bytes) tt = 1;
+    int tt = p.M <= 8 || tile_bytes(2) > scratch_bytes ? 1 : 2;
+    if (tt == 2 && p.M > 16 && tile_bytes(4) <= scratch_bytes && cut_of(p, dev, 4).cost <= cut_of(p, dev, 2).cost) tt = 4;
     const int tok = tt * 8, M = p.M;
     const int all = (M + tok - 1) / tok, most = tt == 1 ? all : (int)std::min<size_t>(all, scratch_bytes / tile_bytes(tt));
     *variant = tt;
     for (int first = 0; first < all; first += most) {
         const int rest = M - first * tok;
-        p.tiles_m = std::min(most, all - first);
-        p.M = std::min(rest, p.tiles_m * tok);
-        const size_t k = (size_t)p.R * p.tiles_m * p.kp;
+        const int tiles = std::min(most, all - first);
+        p.M = std::min(rest, tiles * tok);
+        const size_t k = (size_t)p.R * tiles * p.kp;
         p.tokens = scratch;
         p.sums = reinterpret_cast<float*>(scratch + k * tok * 2);
         p.scales = p.sums + k / 32 * tok;
