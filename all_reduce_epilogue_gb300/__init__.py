@@ -613,9 +613,9 @@ class QWeight:
 def _qweights(w: Sequence, R: int, M: int, K: int, out, dev: int):
     """The C arrays of the weights and of the output views, and the weights' N and group."""
     import torch
-    N, group = w[0].N, w[0].group
     if len(w) != R:
         raise ValueError(f"{R} ranks of tokens, {len(w)} of weights")
+    N, group = w[0].N, w[0].group
     if [q._key for q in w] != [(N, K, group, dev)] * R:
         raise ValueError(f"every rank's weights must be [{N}, {K}] in groups of {group} on CUDA device {dev}")
     if w[0].zero is not None and all([q.zero is not None for q in w]):

@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
     // the stream of codes, DEPTH - 1 items ahead of their use
     constexpr int LPR = ITEM / 32, RPI = 32 / LPR, CP = ROWS / RPI;  // lanes a row of codes, rows an instruction, instructions
     const int frow = (group0 + warp) * ROWS, fn = p.N - frow;
-    const int rstep = RPI * (p.K >> 1);                              // p.K <= 2^24: a warp's rows are within 2^31 of each other
+    const int rstep = RPI * (p.K >> 1);                              // p.K <= 2^20: a warp's rows are within 2^31 of each other
     int fk = kbeg;
     const uint8_t* fcodes = p.codes[r] + (((int64_t)frow * p.K + kbeg) >> 1) + lane / LPR * (p.K >> 1) + lane % LPR * 16;
     const uint32_t lane_to = (uint32_t)(lane / LPR * PITCH + lane % LPR * 16);

@@ -224,7 +224,7 @@ ARE_API const char* are_status_string(are_status s);
  *  ALLREDUCE_RMSNORM: 1 <= R <= 8; N % 8 == 0 (16-byte packs); N <= 32768.
  *  ALLREDUCE_RMSNORM_BACKWARD: as ALLREDUCE_RMSNORM, with N <= 16384.
  *  GEMM_AR_QWEIGHT: 1 <= R <= 8; K % 32 == 0 (16-byte rows of codes) and
- *           K <= 2^24; N % 8 == 0; ceil(M / 8) * ceil(N / 16) < 2^28.
+ *           K <= 2^20; N % 8 == 0; ceil(M / 8) * ceil(N / 16) < 2^28.
  * K is ignored for the two ALLREDUCE_RMSNORM operations.  Pure host function: no device needed. */
 ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
 
@@ -533,7 +533,8 @@ typedef struct are_qweight {
  *            copied before the call returns)
  *  group   : 32, 64 or 128 consecutive k; the last group may be shorter
  *  out[v]  : bf16 [M, N] for every rank view v < R, as in are_gemm_ar (views
- *            may alias; identical pointers are written once)
+ *            may alias; identical pointers are written once); must not overlap
+ *            the tokens or the weights
  *  Result  : out[v][m][n] = bf16( sum_r sum_k x[r][m][k] * w_r(n, k) ), formed
  *            per group as (sum_k u x - zero * sum_k x) * scale: codes, zero
  *            points and scales enter exactly; the group's sums, their

@@ -368,3 +368,14 @@ def test_calls_in_a_row_share_the_staging_buffer(ws):
         for gr in graphs:
             gr.replay()
     look()
+
+
+def test_refuses_ranks_without_weights(ws):
+    w, _ = weights(2, 16, 64, 32, False, 90)
+    x = [torch.zeros((2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    out = torch.full((2, 16), 3.0, dtype=torch.bfloat16, device="cuda")
+    for qw in ([], [are.QWeight(*w[0], 32)], [are.QWeight(*t, 32) for t in w + w[:1]]):
+        with pytest.raises(ValueError):
+            are.gemm_ar_qweight(x, qw, out, ws)
+    torch.cuda.synchronize()
+    assert (out == 3).all()

@@ -29,8 +29,8 @@ def lib():
     ((are.OP_GEMM_AR_QWEIGHT, 0, 1, 8, 64), False),
     ((are.OP_GEMM_AR_QWEIGHT, 1, 1 << 30, 1 << 20, 64), False),    # more CTAs than a grid holds
     ((are.OP_GEMM_AR_QWEIGHT, 1, -1, 8, 64), False),
-    ((are.OP_GEMM_AR_QWEIGHT, 1, 1, 8, 1 << 24), True),
-    ((are.OP_GEMM_AR_QWEIGHT, 1, 1, 8, (1 << 24) + 32), False),    # K too large
+    ((are.OP_GEMM_AR_QWEIGHT, 1, 1, 8, 1 << 20), True),
+    ((are.OP_GEMM_AR_QWEIGHT, 1, 1, 8, (1 << 20) + 32), False),    # K too large
 ])
 def test_supports(lib, args, ok):
     assert (lib.are_supports(*args) == are.OK) == ok
