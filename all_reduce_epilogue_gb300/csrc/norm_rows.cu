@@ -35,6 +35,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "are_internal.h"
 #include "ptx.cuh"
 
@@ -42,8 +44,9 @@ namespace are {
 namespace {
 
 constexpr int kMaxStages = 16;
-constexpr size_t kRowsSmemLimit = 227 * 1024;   // one block per SM
-constexpr size_t kRowsSmemPair = 113 * 1024;    // two blocks per SM
+constexpr size_t kRowsSmemLimit = 227 * 1024;   // a block
+constexpr size_t kRowsSmemSm = 228 * 1024;      // an SM, 1 KB of it for each block
+constexpr int kRowsThreads = 640;               // threads an SM at the 96 registers of blocks up to 288
 constexpr int kRedWords = 2 * 2 * 32;           // [buffer][statistic][warp]
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
@@ -531,9 +534,11 @@ RowsPlan rows_plan(RowsParams& p, int num_sms) {
     p.nt = ((P + plan.ppt - 1) / plan.ppt + 31) / 32 * 32;
     p.slices = (P + p.nt - 1) / p.nt;
     p.stage_bytes = p.nsrc * p.nt * 16;
-    const int blocks = p.nt <= 256 && p.M > num_sms ? 2 : 1;
+    const int fit = p.nt > 256 ? 1 : kRowsThreads / (p.nt + 32);  // blocks of an SM
+    const int64_t rounds = (p.M + num_sms - 1) / num_sms;
+    const int blocks = (int)(rounds < fit ? rounds : fit);
     const size_t fixed = (p.backward ? (size_t)p.N * 4 : 0) + kRedWords * 4 + 2 * kMaxStages * 8 + 16;
-    const size_t room = (blocks == 2 ? kRowsSmemPair : kRowsSmemLimit) - fixed;
+    const size_t room = (blocks == 1 ? kRowsSmemLimit : kRowsSmemSm / blocks - 1024) - fixed;
     p.stages = (int)(room / p.stage_bytes);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     plan.smem = fixed + (size_t)p.stages * p.stage_bytes;
@@ -596,7 +601,9 @@ cudaError_t launch_norm_backward_rows(RowsParams& p, const RowsPlan& plan, float
 }
 
 size_t norm_backward_scratch_words(int64_t n_max, int num_sms) {
-    return (size_t)(n_max < kBackwardMaxN ? n_max : kBackwardMaxN) * 2 * num_sms;
+    // rows of N from an SM's blocks: two, or of narrow rows as many as rows_plan fits, of at most nt * 8 columns
+    const int64_t n = n_max < kBackwardMaxN ? n_max : kBackwardMaxN;
+    return (size_t)std::max<int64_t>(2 * n, 8 * kRowsThreads) * num_sms;
 }
 
 }  // namespace are
