@@ -49,20 +49,44 @@ constexpr size_t kRowsSmemSm = 228 * 1024;      // an SM, 1 KB of it for each bl
 constexpr int kRowsThreads = 640;               // threads an SM at the 96 registers of blocks up to 288
 constexpr int kRedWords = 2 * 2 * 32;           // [buffer][statistic][warp]
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xFFFF0000u);
-    f[4] = __uint_as_float(v.z << 16); f[5] = __uint_as_float(v.z & 0xFFFF0000u);
-    f[6] = __uint_as_float(v.w << 16); f[7] = __uint_as_float(v.w & 0xFFFF0000u);
+using ptx::add2;
+using ptx::fma2;
+using ptx::mul2;
+using ptx::pair;
+using ptx::unpair;
+
+// A pack of 8 columns in fp32 is four pairs: their arithmetic is two columns an instruction.
+typedef uint64_t Pack[4];
+
+__device__ __forceinline__ void unpack8(const uint4& v, Pack& f) {
+    f[0] = pair(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+    f[1] = pair(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+    f[2] = pair(__uint_as_float(v.z << 16), __uint_as_float(v.z & 0xFFFF0000u));
+    f[3] = pair(__uint_as_float(v.w << 16), __uint_as_float(v.w & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+    const float2 f = unpair(v);
+    __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<uint32_t*>(&b);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const Pack& f) {
+    return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+}
+
+// 8 fp32 words, 16-byte aligned (shared or global memory).
+__device__ __forceinline__ void load8(const float* at, Pack& f) {
+    const float4 a = reinterpret_cast<const float4*>(at)[0], b = reinterpret_cast<const float4*>(at)[1];
+    f[0] = pair(a.x, a.y);
+    f[1] = pair(a.z, a.w);
+    f[2] = pair(b.x, b.y);
+    f[3] = pair(b.z, b.w);
+}
+
+__device__ __forceinline__ float both(uint64_t v) {
+    const float2 f = unpair(v);
+    return f.x + f.y;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -166,16 +190,16 @@ __device__ __forceinline__ void produce(const Ring& g, const RowsParams& p) {
 // Sum of the R partials of this thread's pack, r ascending from +0.0.  ONE: R is
 // 1, the common case of the backward pass, without the code of the other ranks.
 template <bool ONE>
-__device__ __forceinline__ void sum_ranks(const uint8_t* at, int R, size_t step, float (&f)[8]) {
+__device__ __forceinline__ void sum_ranks(const uint8_t* at, int R, size_t step, Pack& f) {
     unpack8(*reinterpret_cast<const uint4*>(at), f);
     if constexpr (!ONE) {
 #pragma unroll
         for (int r = 1; r < kMaxRanks; ++r) {
             if (r < R) {
-                float v[8];
+                Pack v;
                 unpack8(*reinterpret_cast<const uint4*>(at + r * step), v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] += v[i];
+                for (int i = 0; i < 4; ++i) f[i] = add2(f[i], v[i]);
             }
         }
     }
@@ -237,22 +261,19 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
     const int P = p.N >> 3;
     const size_t step = (size_t)p.nt * 16;
     constexpr bool kGammaRegs = PPT <= 4;
-    float gam[kGammaRegs ? PPT : 1][8];
+    Pack gam[kGammaRegs ? PPT : 1];
     if (kGammaRegs) {
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
             const int pk = t + k * p.nt;
-            if (pk < P) {
-                *reinterpret_cast<float4*>(&gam[k][0]) = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2);
-                *reinterpret_cast<float4*>(&gam[k][4]) = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2 + 1);
-            }
+            if (pk < P) load8(p.gamma + pk * 8, gam[k]);
         }
     }
     int s = 0, buf = 0;
     uint32_t ph = 0;
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, buf ^= 1) {
-        float h[PPT][8];
-        float ss = 0.f;
+        Pack h[PPT];
+        uint64_t ss2 = 0ull;
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
             if (k < p.slices) {
@@ -262,15 +283,15 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
                 if (pk < P) {
                     sum_ranks<false>(at, p.R, step, h[k]);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) h[k][i] += 0.f;  // a sum of -0.0 counts as +0.0
+                    for (int i = 0; i < 4; ++i) h[k][i] = add2(h[k][i], 0ull);  // a sum of -0.0 counts as +0.0
                     if (p.has_res) {
-                        float e[8];
+                        Pack e;
                         unpack8(*reinterpret_cast<const uint4*>(at + p.R * step), e);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) h[k][i] += e[i];
+                        for (int i = 0; i < 4; ++i) h[k][i] = add2(h[k][i], e[i]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) ss = fmaf(h[k][i], h[k][i], ss);
+                    for (int i = 0; i < 4; ++i) ss2 = fma2(h[k][i], h[k][i], ss2);
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&g.empty[s]);
@@ -280,32 +301,33 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
         }
         // one barrier a row: the next row's partial sums go to the other buffer
         float* red = g.red + buf * 64;
-        ss = warp_sum(ss);
+        const float ss = warp_sum(both(ss2));
         if (lane == 0) red[w] = ss;
         consumer_bar(p.nt);
         // inv = two * m: a power of two (0 for 0, infinite for NaN) and 1 <= m < 2
         const uint32_t inv = __float_as_uint(rsqrtf(red_total(red, nwarps) * p.inv_n + p.eps));
         const float two = __uint_as_float(inv & 0x7F800000u), m = __uint_as_float((inv & 0x7FFFFFu) | 0x3F800000u);
+        const uint64_t two2 = pair(two, two), minus = pair(-1.f, -1.f);
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
             if (k < p.slices) {
                 const int pk = t + k * p.nt;
                 const bool in = pk < P;
-                float gk[8];
+                Pack gk;
                 if (kGammaRegs) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) gk[i] = gam[kGammaRegs ? k : 0][i];
+                    for (int i = 0; i < 4; ++i) gk[i] = gam[kGammaRegs ? k : 0][i];
                 } else if (in) {
-                    *reinterpret_cast<float4*>(&gk[0]) = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2);
-                    *reinterpret_cast<float4*>(&gk[4]) = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2 + 1);
+                    load8(p.gamma + pk * 8, gk);
                 }
                 // largest |z| as a bit pattern: infinities and NaN sort above every finite value
                 uint32_t a = 0;
                 if (in) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        h[k][i] *= two;
-                        a = max(a, __float_as_uint(h[k][i] * gk[i]) & 0x7FFFFFFFu);
+                    for (int i = 0; i < 4; ++i) {
+                        h[k][i] = mul2(h[k][i], two2);
+                        const float2 z = unpair(mul2(h[k][i], gk[i]));
+                        a = max(a, max(__float_as_uint(z.x) & 0x7FFFFFFFu, __float_as_uint(z.y) & 0x7FFFFFFFu));
                     }
                 }
                 // a group is 4, 8 or 16 neighbouring lanes (p.nt is a multiple of 32)
@@ -317,17 +339,14 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
                     if (top * m <= 3.40282347e38f) {
                         const GroupScale gs = group_scale<POW2>(top, m);
                         stored = gs.stored;
-                        float v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float z = h[k][i] * gk[i];
-                            v[i] = fmaf(z, gs.factor, fmaf(h[k][i], gk[i], -z) * gs.factor);
-                        }
+                        const uint64_t factor = pair(gs.factor, gs.factor);
                         uint32_t c[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]),
+                        for (int i = 0; i < 4; ++i) {
+                            const uint64_t z = mul2(h[k][i], gk[i]), lost = fma2(h[k][i], gk[i], mul2(z, minus));
+                            c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(unpair(fma2(z, factor, mul2(lost, factor))),
                                                                       __NV_SATFINITE, __NV_E4M3);
+                        }
                         q = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
                     } else {  // not finite: NaN codes under a NaN scale
                         stored = POW2 ? 0xFFu : 0x7FC00000u;
@@ -369,17 +388,17 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
             reinterpret_cast<float4*>(g.gamma)[pk * 2 + 1] = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2 + 1);
         }
     }
-    float dg[PPT][8];
+    Pack dg[PPT];
 #pragma unroll
     for (int k = 0; k < PPT; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dg[k][i] = 0.f;
+        for (int i = 0; i < 4; ++i) dg[k][i] = 0ull;
     int s = 0, buf = 0;
     uint32_t ph = 0;
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, buf ^= 1) {
-        float dy[ONE ? 1 : PPT][8];
+        Pack dy[ONE ? 1 : PPT];
         uint4 dv[ONE ? PPT : 1], hv[PPT], ev[PPT];  // one rank's dy stays packed
-        float c1 = 0.f, c2 = 0.f;
+        uint64_t s1 = 0ull, s2 = 0ull;
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
             if (k < p.slices) {
@@ -387,19 +406,18 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
                 ring_wait(&g.full[s], ph, g, p);
                 const uint8_t* at = g.stage + (size_t)s * p.stage_bytes + t * 16;
                 if (pk < P) {
-                    float(&d)[8] = dy[ONE ? 0 : k];
+                    Pack& d = dy[ONE ? 0 : k];
                     sum_ranks<ONE>(at, p.R, step, d);
                     if (ONE) dv[k] = *reinterpret_cast<const uint4*>(at);
                     hv[k] = *reinterpret_cast<const uint4*>(at + p.R * step);
                     if (p.has_res) ev[k] = *reinterpret_cast<const uint4*>(at + (p.R + 1) * step);
-                    float h[8], gk[8];
+                    Pack h, gk;
                     unpack8(hv[k], h);
-                    *reinterpret_cast<float4*>(&gk[0]) = reinterpret_cast<const float4*>(g.gamma)[pk * 2];
-                    *reinterpret_cast<float4*>(&gk[4]) = reinterpret_cast<const float4*>(g.gamma)[pk * 2 + 1];
+                    load8(g.gamma + pk * 8, gk);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        c1 = fmaf(h[i], h[i], c1);
-                        c2 = fmaf(d[i] * gk[i], h[i], c2);
+                    for (int i = 0; i < 4; ++i) {
+                        s1 = fma2(h[i], h[i], s1);
+                        s2 = fma2(mul2(d[i], gk[i]), h[i], s2);
                     }
                 }
                 __syncwarp();
@@ -408,8 +426,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
             }
         }
         float* red = g.red + buf * 64;
-        c1 = warp_sum(c1);
-        c2 = warp_sum(c2);
+        const float c1 = warp_sum(both(s1)), c2 = warp_sum(both(s2));
         if (lane == 0) {
             red[w] = c1;
             red[32 + w] = c2;
@@ -417,23 +434,23 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
         consumer_bar(p.nt);
         const float inv = rsqrtf(red_total(red, nwarps) * p.inv_n + p.eps);
         const float m = inv * (red_total(red + 32, nwarps) * p.inv_n) * inv;  // inv^2 * mean(dy gamma h): dh = inv dy gamma - m (h inv) + d_res
+        const uint64_t inv2 = pair(inv, inv), m2 = pair(-m, -m);
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
             if (k < p.slices) {
                 const int pk = t + k * p.nt;
                 if (pk < P) {
-                    float h[8], gk[8], e[8] = {}, o[8];
+                    Pack h, gk, e = {}, o;
                     unpack8(hv[k], h);
-                    *reinterpret_cast<float4*>(&gk[0]) = reinterpret_cast<const float4*>(g.gamma)[pk * 2];
-                    *reinterpret_cast<float4*>(&gk[4]) = reinterpret_cast<const float4*>(g.gamma)[pk * 2 + 1];
+                    load8(g.gamma + pk * 8, gk);
                     if (p.has_res) unpack8(ev[k], e);
-                    float(&d)[8] = dy[ONE ? 0 : k];
+                    Pack& d = dy[ONE ? 0 : k];
                     if (ONE) unpack8(dv[k], d);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float xh = h[i] * inv;
-                        o[i] = fmaf(d[i] * gk[i], inv, fmaf(-xh, m, e[i]));
-                        dg[k][i] = fmaf(d[i], xh, dg[k][i]);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t xh = mul2(h[i], inv2);
+                        o[i] = fma2(mul2(d[i], gk[i]), inv2, fma2(xh, m2, e[i]));
+                        dg[k][i] = fma2(d[i], xh, dg[k][i]);
                     }
                     ptx::st_stream_v4(p.res_out + row * (int64_t)p.N + pk * 8, pack8(o));
                 }
@@ -446,8 +463,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
         for (int k = 0; k < PPT; ++k) {
             const int pk = t + k * p.nt;
             if (pk < P) {
-                *reinterpret_cast<float4*>(to + pk * 8) = *reinterpret_cast<const float4*>(&dg[k][0]);
-                *reinterpret_cast<float4*>(to + pk * 8 + 4) = *reinterpret_cast<const float4*>(&dg[k][4]);
+                const float2 a = unpair(dg[k][0]), b = unpair(dg[k][1]), c = unpair(dg[k][2]), d = unpair(dg[k][3]);
+                *reinterpret_cast<float4*>(to + pk * 8) = make_float4(a.x, a.y, b.x, b.y);
+                *reinterpret_cast<float4*>(to + pk * 8 + 4) = make_float4(c.x, c.y, d.x, d.y);
             }
         }
     }
