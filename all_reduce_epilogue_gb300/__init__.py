@@ -460,7 +460,7 @@ def _need(t, dtype, shape, dev: int, what: str):
 
 
 def _need_one_of(t, dtypes, shape, dev: int, what: str):
-    _need(t, t.dtype if t.dtype in dtypes else dtypes[0], shape, dev, what)
+    _need(t, t.dtype if t.dtype in dtypes else next(iter(dtypes)), shape, dev, what)
 
 
 def _need_all(tensors, dtype, shape, dev: int, what: str):
@@ -472,9 +472,15 @@ def _need_all(tensors, dtype, shape, dev: int, what: str):
             _need(t, dtype, shape, dev, what)
 
 
+_T = None
+
+
 def _tensor_type():
-    import torch
-    return torch.Tensor
+    global _T
+    if _T is None:
+        import torch
+        _T = torch.Tensor
+    return _T
 
 
 def _addresses(tensors) -> array:
@@ -549,7 +555,7 @@ def allreduce_rmsnorm_quant_groups(partials: Sequence, residual, gamma, eps: flo
     _need(gamma, torch.float32, (N,), dev, "gamma")
     _need_one_of(out_q, (torch.uint8, torch.float8_e4m3fn), shape, dev, "out_q")
     kinds = _scale_kinds()
-    _need_one_of(out_scale, tuple(kinds), (M, -(-N // _group_of(group, "group"))), dev, "out_scale")
+    _need_one_of(out_scale, kinds, (M, -(-N // _group_of(group, "group"))), dev, "out_scale")
     parts = _addresses(partials)
     rc = load_library().are_allreduce_rmsnorm_quant_groups(
         _at(parts), _address(residual), gamma.data_ptr(), eps, kinds[out_scale.dtype], group, out_q.data_ptr(),

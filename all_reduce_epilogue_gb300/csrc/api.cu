@@ -899,7 +899,9 @@ are_status are_allreduce_rmsnorm_backward(const are_bf16* const dy[], const are_
     }
     p.res_out = dh;
     p.backward = 1;
-    const RowsPlan plan = rows_plan(p, ws->num_sms);
+    RowsPlan plan = rows_plan(p, ws->num_sms);
+    // a row of partial sums a block
+    plan.grid = (int)std::min<int64_t>(plan.grid, (int64_t)norm_backward_scratch_words(ws->caps.N_max, ws->num_sms) / N);
     ws->last = are_launch_info{ARE_KERNEL_NORM_BACKWARD_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
     return from_cuda(launch_norm_backward_rows(p, plan, ws->d_dgamma, dgamma, s));
 }

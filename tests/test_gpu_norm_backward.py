@@ -168,3 +168,17 @@ def test_refusals(ws):
         with pytest.raises(are.AreError) as err:
             call(w=small)
         assert err.value.status == are.ECAPACITY
+
+
+@pytest.mark.parametrize("N", [8, 64, 264, 768, 1032, 2048, 2056, 2816, 3592, 4096, 7680])
+def test_workspaces_no_wider_than_the_row(N):
+    """The partial sums of dgamma fit a workspace made for just this width, with as many blocks as a call can have."""
+    need_gpu()
+    dy, h, gamma, e = inputs(1, 3300, N, N, True)
+    want, tol, want_g, tol_g = ref.backward64(dy, h, gamma, e)
+    with are.Workspace(R_max=1, M_max=1, N_max=N) as small:
+        dh, dg = run(small, dy, h, gamma, e)
+        grid = small.last_launch()["grid"]
+    ref.check(dh, want, tol, "dh")
+    ref.check(dg, want_g, tol_g, "dgamma")
+    assert grid >= 152 if N > 4096 else grid >= 304
