@@ -217,6 +217,25 @@ __device__ __forceinline__ float red_total(const float* red, int nwarps) {
 }
 
 // ------------------------------------------------------------ quantised forward
+// The larger magnitude, NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float v;
+    asm("{\n\t.reg .f32 x, y;\n\tabs.f32 x, %1;\n\tabs.f32 y, %2;\n\tmax.NaN.f32 %0, x, y;\n\t}" : "=f"(v) : "f"(a), "f"(b));
+    return v;
+}
+
+// n / d from an approximate reciprocal of d, corrected once by the remainder (Markstein 1990: the quotient's
+// remainder is exact in an fma): correctly rounded but for the last bit's rare ties.  No over- or underflow on the way.
+__device__ __forceinline__ float quotient(float n, float d, float rcp) {
+    const float q = n * rcp;
+    return fmaf(fmaf(-d, q, n), rcp, q);
+}
+__device__ __forceinline__ float approx_rcp(float d) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return r;
+}
+
 // Scale of a group whose largest |z| is `top` and largest |y| = top * m is
 // finite (1 <= m < 2), and the factor that takes z to code range.
 struct GroupScale {
@@ -238,9 +257,10 @@ __device__ __forceinline__ GroupScale group_scale(float top, float m) {
     } else {
         // at least 2^-126, so that its reciprocal is finite
         const bool tiny = a < 448 * 1.17549435e-38f;
-        const float sc = tiny ? 1.17549435e-38f : __fdiv_rn(a, 448.f);
+        const float sc = tiny ? 1.17549435e-38f : quotient(a, 448.f, 1.f / 448.f);
         s.stored = __float_as_uint(a == 0.f ? 1.f : sc);
-        s.factor = tiny ? m * 8.50705917e37f : __fdiv_rn(448.f, top);
+        // (the reciprocal of the largest magnitudes would be a denormal)
+        s.factor = tiny ? m * 8.50705917e37f : top < 0x1p120f ? quotient(448.f, top, approx_rcp(top)) : __fdiv_rn(448.f, top);
     }
     return s;
 }
@@ -320,22 +340,20 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
                 } else if (in) {
                     load8(p.gamma + pk * 8, gk);
                 }
-                // largest |z| as a bit pattern: infinities and NaN sort above every finite value
-                uint32_t a = 0;
+                float top = 0.f;  // largest |z|
                 if (in) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         h[k][i] = mul2(h[k][i], two2);
                         const float2 z = unpair(mul2(h[k][i], gk[i]));
-                        a = max(a, max(__float_as_uint(z.x) & 0x7FFFFFFFu, __float_as_uint(z.y) & 0x7FFFFFFFu));
+                        top = max_abs(top, max_abs(z.x, z.y));
                     }
                 }
                 // a group is 4, 8 or 16 neighbouring lanes (p.nt is a multiple of 32)
-                for (int o = 1; o < p.group_packs; o <<= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+                for (int o = 1; o < p.group_packs; o <<= 1) top = max_abs(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
                 if (in) {
                     uint2 q;
                     uint32_t stored;
-                    const float top = __uint_as_float(a);
                     if (top * m <= 3.40282347e38f) {
                         const GroupScale gs = group_scale<POW2>(top, m);
                         stored = gs.stored;

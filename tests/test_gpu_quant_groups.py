@@ -195,3 +195,20 @@ def test_refusals(ws):
     empty = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
     call([empty, empty], None, gamma, q[:0], s[:0])
     assert ws.last_launch()["kernel"] == "none"
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+def test_magnitudes_over_all_of_fp32(ws, pow2):
+    """Groups from below the smallest normal scale up to near fp32's largest value."""
+    M, N = 6, 2048
+    g = torch.Generator(device="cuda").manual_seed(17)
+    sign = torch.randint(0, 2, (M, N), generator=g, device="cuda") * 2 - 1
+    size = 2.0 ** -torch.randint(0, 3, (M, N), generator=g, device="cuda").double()
+    parts = [(sign * size).to(torch.bfloat16)]
+    e = torch.tensor([-140, -126, -118, -117, -116, -110, -60, -1, 0, 30, 100, 118, 119, 120, 121, 122, 123, 124, 125, 125,
+                      -149, -130, -125, -119, 60, 119, 120, 120, 126, 126, 10, 90], device="cuda").double()
+    gamma = (2.0 ** e * 0.9).repeat_interleave(64).float()
+    q, s, ro = run(ws, parts, None, gamma, 64, pow2)
+    _, _, y, tol = ref.norm64(parts, None, gamma)
+    assert y.abs().max() < 3.4e38
+    ref.check_quant(q, s, y, tol + 2.0 ** -149, 64, pow2)  # a denormal's step
