@@ -817,6 +817,10 @@ are_status qweight_call(const void* const x[], const void* const xscale[], int s
         p.xpow2 = scale_format == ARE_SCALE_E8M0;
     }
     int grid = 0, variant = 0, cluster = 0;
+    p.force_tile = ws->debug_flags & ARE_DEBUG_QWEIGHT_FEW                                                    ? 8
+                   : !(ws->debug_flags & ARE_DEBUG_QWEIGHT_STAGED)                                            ? 0
+                   : ws->debug_arg == 16 || ws->debug_arg == 32                                               ? (int)ws->debug_arg
+                                                                                                              : -1;
     const cudaError_t e = launch_qweight(p, ws->qweight, ws->d_tokens, ws->caps.R_max * kQweightScratch, &grid, &variant,
                                          &cluster, s);
     ws->last = are_launch_info{ARE_KERNEL_QWEIGHT, grid, 256, cluster, 0, variant, 0, 0};

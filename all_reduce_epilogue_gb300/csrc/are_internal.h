@@ -138,6 +138,7 @@ struct QweightParams {
     int qx;                              // tokens in 8 bits
     int xgroup_shift, xgroups;           // of the token scales
     int xpow2;
+    int force_tile;                      // 0: by size; 8, 16, 32: tokens a tile; -1: 16 or 32
     DevStatus* status;
     unsigned long long timeout_ns;
     // set by launch_qweight:

@@ -1194,17 +1194,22 @@ cudaError_t qweight_prepare(QweightDevice& dev) {
 
 cudaError_t launch_qweight(QweightParams& p, const QweightDevice& dev, uint8_t* scratch, size_t scratch_bytes, int* grid,
                            int* variant, int* cluster, cudaStream_t s) {
-    // Up to 8 tokens a CTA stages its own (R = 8, 8 tokens, 7168 x 2048: 19.7 us, a staging kernel before 22.9; R = 2,
-    // 512 x 512: 5.1 us and 6.1).  With more, tiles of 16 or 32, whichever is expected to end first, are
-    // staged by a kernel before (each CTA staging them again took 30 to 50 % of the time at 16 and 64
-    // tokens), as many at once as the scratch holds.  Rows too long for a tile of them go by 8 tokens.
-    // More than 32 tokens a tile need 200 registers a thread: spilled to 128 they took 139 us at R = 8,
-    // M = 64, N = 7168, K = 2048, tiles of 32 take 75.
+    // In tiles of 8 tokens a CTA stages its own; tiles of 16 or 32, whichever is expected to end first, are staged by
+    // a kernel before (each CTA staging them again took 30 to 50 % of the time at 16 and 64 tokens), as many at
+    // once as the scratch holds.  That kernel and its launch cost as much as 30 items:
+    //  * R = 8, 7168 x 2048: 8 tokens 19.7 us in a tile of 8, 22.9 in one of 16; 16 tokens 47 and 23; 64 tokens 75 in 32s;
+    //  * R = 4, 1024 x 2048: 12 tokens 8.3 and 11.0; 64 tokens 17.5 and 15.8;
+    //  * R = 2, 512 x 512: 8 tokens 5.1 and 6.1, 64 tokens 6.1 and 7.0.
+    // Rows too long for a staged tile go by 8 tokens.  More than 32 tokens a tile need 200 registers a thread:
+    // spilled to 128 they took 139 us at R = 8, M = 64, N = 7168, K = 2048.
     p.kp = (p.K + 255) / 256 * 256;
     // of a token tile: fp16 tokens, sums and scales of at least 32 k, and a flag word per 256 k
     auto tile_bytes = [&](int t) { return (size_t)p.R * p.kp / 32 * (t * 8 * (64 + 4 + 4) + 4); };
-    int tt = p.M <= 8 || tile_bytes(2) > scratch_bytes ? 1 : 2;
-    if (tt == 2 && p.M > 16 && tile_bytes(4) <= scratch_bytes && cut_of(p, dev, 4).cost <= cut_of(p, dev, 2).cost) tt = 4;
+    int tt = p.force_tile == 8 || (p.M <= 8 && p.force_tile == 0) || tile_bytes(2) > scratch_bytes ? 1 : 2;
+    if (tt == 2 && p.force_tile != 16 && tile_bytes(4) <= scratch_bytes &&
+        (p.force_tile == 32 || (p.M > 16 && cut_of(p, dev, 4).cost <= cut_of(p, dev, 2).cost)))
+        tt = 4;
+    if (p.force_tile == 0 && tt > 1 && cut_of(p, dev, 1).cost <= cut_of(p, dev, tt).cost + 30) tt = 1;
     const int tok = tt * 8, M = p.M;
     const int all = (M + tok - 1) / tok, most = tt == 1 ? all : (int)std::min<size_t>(all, scratch_bytes / tile_bytes(tt));
     *variant = tt;

@@ -136,8 +136,12 @@ enum {
                                      row, where the pair's second tile is absent, and below one wave) */
     ARE_DEBUG_RS_RING = 1024u,    /* GEMM+RS on the CTA-pair kernel: push the running sum along the ranks
                                      whatever the size (chunked calls always do) */
-    ARE_DEBUG_RS_SPLIT = 2048u    /* GEMM+RS on the CTA-pair kernel: every unit of a tile reduces its row slice
+    ARE_DEBUG_RS_SPLIT = 2048u,   /* GEMM+RS on the CTA-pair kernel: every unit of a tile reduces its row slice
                                      (two-shot) whatever the size; not with chunking */
+    ARE_DEBUG_QWEIGHT_FEW = 4096u,    /* 4-bit linear: tiles of 8 tokens whatever the size (its sums over k are
+                                         grouped otherwise than in wider tiles) */
+    ARE_DEBUG_QWEIGHT_STAGED = 8192u  /* 4-bit linear: tiles of 16 or 32 tokens whatever the size, `debug_arg` of
+                                         them if it is 16 or 32, where the workspace's buffer holds one */
 };
 
 /* Device status word, see are_get_device_status(). */
@@ -546,10 +550,11 @@ typedef struct are_qweight {
  *            2^-35 of it, which is below the fp32 sums' rounding.  A value that
  *            is not finite makes that token's outputs what the products give.
  * K == 0 writes zeros.  Any M is computed; it is made for few: tiles of 8, 16 or
- * 32 tokens, each of which reads the weights, from memory once for those that
- * run together.  With M > 8 the tokens are first laid out in a buffer of the
- * workspace, in several parts if it does not hold them.  Needs no capacity of
- * the workspace but R <= R_max.
+ * 32 tokens, by the size of the problem, each of which reads the weights, from
+ * memory once for those that run together.  For tiles of 16 and 32 the tokens
+ * are first laid out in a buffer of the workspace, in several parts if it does
+ * not hold them.  ARE_DEBUG_QWEIGHT_FEW / ARE_DEBUG_QWEIGHT_STAGED force the
+ * tile.  Needs no capacity of the workspace but R <= R_max.
  */
 ARE_API are_status are_gemm_ar_qweight(const are_bf16* const x[], const are_qweight w[], int group,
                                        are_bf16* const out[], int R, int64_t M, int64_t N, int64_t K, are_ws* ws,

@@ -379,3 +379,76 @@ def test_refuses_ranks_without_weights(ws):
             are.gemm_ar_qweight(x, qw, out, ws)
     torch.cuda.synchronize()
     assert (out == 3).all()
+
+
+@pytest.fixture(params=[8, 16, 32], ids=lambda t: f"tiles of {t}")
+def tiled(request):
+    """A workspace whose calls all take tiles of so many tokens."""
+    need_gpu()
+    with are.Workspace(R_max=8, M_max=1, N_max=8) as w:
+        w.set_debug(are.DEBUG_QWEIGHT_FEW if request.param == 8 else are.DEBUG_QWEIGHT_STAGED, request.param)
+        yield w, {8: 1, 16: 2, 32: 4}[request.param]
+
+
+TILED = [(1, 1, 8, 32), (2, 3, 256, 128), (5, 9, 264, 1056), (6, 16, 72, 800), (7, 17, 200, 288), (8, 33, 1000, 320),
+         (8, 64, 136, 2080), (1, 64, 4104, 96), (2, 65, 128, 608), (1, 100, 72, 352), (2, 20, 2048, 4128), (4, 31, 32, 64)]
+
+
+@pytest.mark.parametrize("R,M,N,K", TILED)
+def test_every_tile_against_64_bits(tiled, R, M, N, K):
+    w_, variant = tiled
+    for group in (32, 64, 128):
+        w, g = weights(R, N, K, group, group != 64, R + M + N + K + group)
+        x = [torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(R)]
+        for xgroup, pow2 in ((None, False), (32, True), (32, False), (64, False), (128, True), (128, False)):
+            y, vals = run(w_, x, w, group, xgroup, pow2)
+            want, tol = ref.linear64(vals, w, group)
+            ref.check(y, want, tol, f"group {group}, token group {xgroup}, {pow2}")
+        assert w_.last_launch()["variant"] == variant
+
+
+def test_every_tile_with_values_that_are_not_finite(tiled):
+    w_, _ = tiled
+    R, M, N, K = 3, 40, 72, 832
+    w, g = weights(R, N, K, 64, False, 71)
+    w[0][0].fill_(0x99)  # every weight of rank 0: 1 * scale
+    x = [torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(R)]
+    x[0][0, 0] = float("-inf")
+    x[2][M // 2, 255] = float("nan")
+    x[0][M - 1, K - 1] = float("inf")
+    y, _ = run(w_, x, w, 64)
+    assert (y[0] == float("-inf")).all() and y[M // 2].isnan().all() and (y[M - 1] == float("inf")).all()
+    keep = [m for m in range(M) if m not in (0, M // 2, M - 1)]
+    want, tol = ref.linear64([t[keep] for t in x], w, 64)
+    ref.check(y[keep], want, tol, "out")
+
+
+def test_every_tile_captured_with_operands_written_before(tiled):
+    w_, _ = tiled
+    R, M, N, K = 4, 40, 512, 1024
+    sets = [weights(R, N, K, 128, True, 80 + i) for i in range(2)]
+    xs = [[torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(R)] for _, g in sets]
+    w = [tuple(torch.zeros_like(t) for t in r) for r in sets[0][0]]
+    qw, x = [are.QWeight(*t, 128) for t in w], [torch.zeros_like(t) for t in xs[0]]
+    outs = [torch.empty((M, N), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+
+    def step(i):
+        for r in range(R):
+            for to, of in zip(w[r], sets[i % 2][0][r]):
+                to.copy_(of)
+            x[r].copy_(xs[i % 2][r])
+        are.gemm_ar_qweight(x, qw, outs[i], w_)
+
+    for i in range(4):
+        step(i)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        for i in range(4):
+            step(i)
+    for _ in range(2):
+        for i in range(4):
+            want, tol = ref.linear64(xs[i % 2], sets[i % 2][0], 128)
+            ref.check(outs[i], want, tol, f"call {i}")
+        for o in outs:
+            o.zero_()
+        gr.replay()
