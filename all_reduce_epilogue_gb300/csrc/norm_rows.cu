@@ -30,8 +30,11 @@
 // backward pass keep its dgamma sums in registers until the block ends; a
 // small kernel adds the blocks' rows of them (4 us).
 // Measured (a copy moves 6.78 TB/s): forward, R = 8, 4096 x 7168: 99 us,
-// 6.2 TB/s; backward, R = 8, 4096 x 7168: 96 us, 6.7 TB/s; R = 1, 16384 x 4096:
-// 90 us, 5.9 TB/s.  One row of 7168 at R = 8: 5.9 us, all latency.
+// 6.2 TB/s; backward, R = 8, 4096 x 7168: 97 us, 6.7 TB/s; R = 1, 16384 x 4096:
+// 90 us, 6.0 TB/s.  One row of 7168 at R = 8: 5.7 us, all latency.  Narrow rows
+// are bound by issue: R = 1, 16384 x 2048 backward 57 us, 4.7 TB/s, issue slots
+// 58 % used; so their arithmetic is in pairs of columns, and an SM takes as many
+// blocks as its registers hold (16384 x 1024: 34 us; two blocks 43).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

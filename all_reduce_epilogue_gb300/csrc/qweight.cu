@@ -34,13 +34,13 @@
 // small, part of a rank's) K range for all of them.  At the end the CTAs add
 // their fp32 sums over distributed shared memory, r ascending: no partial sum
 // goes through global memory and the order never varies.
-//  * Up to 8 tokens (qweight_few_kernel), a CTA stages its tokens itself, and
-//    the (group, K) items of a CTA are dealt to its warps in equal contiguous
+//  * In tiles of 8 tokens (qweight_few_kernel), a CTA stages its tokens itself,
+//    and the (group, K) items of a CTA are dealt to its warps in equal contiguous
 //    runs of 16-row groups.  R = 8, one token, 7168 x 2048: 17 us, 3.6 TB/s of
 //    codes; issue slots are 48 % used (about 70 % in the loop over the codes,
 //    which is 60 % of the time), DRAM 37 %.
-//  * With more (qweight_tokens_kernel, then qweight_wide_kernel), the tokens are
-//    staged once, in global memory, and come in tiles of K by bulk copies; a warp
+//  * In tiles of 16 or 32 (qweight_tokens_kernel, then qweight_wide_kernel), they
+//    are staged once, in global memory, and come in tiles of K by bulk copies; a warp
 //    owns 32 rows, which share the tokens' operands, and their sums stay in
 //    registers.  R = 8: 16 tokens, 8192 x 4096, groups of 64: 47 us (4 of them
 //    staging), 3.1 TB/s; 64 tokens, 7168 x 2048: 75 us, tensor pipes 44 %, issue
