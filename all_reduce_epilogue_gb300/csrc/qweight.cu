@@ -50,6 +50,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "are_internal.h"
 #include "ptx.cuh"
@@ -76,12 +77,19 @@ struct Shape {
     static constexpr int ROWS = RT * 16;
     static constexpr int ITEM = OWN ? 128 : 256;      // k of a slot
     static constexpr int DEPTH = 3;                   // ring slots of a warp
-    static constexpr int PITCH = ITEM / 2 + 16;       // bytes: reads of 8 rows start in 8 different bank quads
+    static constexpr int PITCH = ITEM / 2;            // bytes of a row's codes, in 16-byte pieces that swizzle() permutes
     static constexpr int SLOT = ROWS * PITCH;
     static constexpr int RING = kWarps * DEPTH * SLOT;
     static constexpr int LD = ROWS + 4;               // floats between a sum's tokens: 4 token pairs x 8 rows in 32 banks
     static constexpr int UNITS = 8;                   // units of 8 k a thread stages of a K tile (TT = 1)
 };
+
+// What the places of row g's 16-byte pieces are xored with (times 16), its bits reversed: then the 4-, 8- and 16-byte
+// reads of 4 lanes of each of 8 rows meet no bank twice, in rows of 64 bytes as of 128.
+template <int PITCH>
+__device__ __forceinline__ uint32_t swizzle(int g) {
+    return (uint32_t)((g & 1) << 2 | (g & 2) | (g >> 2 & 1)) % (PITCH / 16) * 16u;
+}
 
 // Shared memory of the kernel for wide tiles, of each of its two buffers, and its K tile: 512 k where they fit.
 template <int TT, bool QX, int WSTEPS, int STEPS>
@@ -236,7 +244,7 @@ __device__ __forceinline__ float unscale_of(uint32_t top) {
 //   xsum : [k / GRAIN][TOK] sum x * 2^-24
 //   xsc  : [k / 256, or k / xgroup with QX][TOK] the tokens' scales
 //   bad  : bit m: token m has a value that is not finite
-template <int TT, bool QX, bool WIDE, int GRAIN, int UNITS, typename Between>
+template <int TT, bool QX, int SPAN, int GRAIN, int UNITS, typename Between>
 __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int m0, int rows, int toks, int t0, int kend,
                                              int tile_k, uint8_t* xs, float* xsum, float* xsc, uint32_t* bad,
                                              Between between) {
@@ -326,8 +334,8 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            // step st = 32 k, or lane c's word st of 128 k
-            const int st = WIDE ? (k[e] >> 7) * 4 + (lane & 3) : k[e] >> 5, c4 = WIDE ? lane >> 2 & 3 : lane & 3;
+            // unit u of SPAN k is lane c4's, in step st
+            const int u = lane % (SPAN / 8), st = k[e] / SPAN * (SPAN / 32) + u % (SPAN / 32), c4 = u / (SPAN / 32);
             const float(&y)[8] = x[e];
             if (in[e])
                 *reinterpret_cast<uint4*>(xs + (((st * TT + (m[e] >> 3)) * 8 + (m[e] & 7)) * 4 + c4) * 16) =
@@ -367,7 +375,7 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
             const uint32_t h[4] = {fp8x2_to_f16x2(w.x), fp8x2_to_f16x2(w.x >> 16), fp8x2_to_f16x2(w.y), fp8x2_to_f16x2(w.y >> 16)};
             const __half2 y0 = __hmul2(h2_of(__byte_perm(h[0], h[2], 0x5410)), mul2), y1 = __hmul2(h2_of(__byte_perm(h[0], h[2], 0x7632)), odd2);
             const __half2 y2 = __hmul2(h2_of(__byte_perm(h[1], h[3], 0x5410)), mul2), y3 = __hmul2(h2_of(__byte_perm(h[1], h[3], 0x7632)), odd2);
-            const int st = WIDE ? (k[e] >> 7) * 4 + (lane & 3) : k[e] >> 5, c4 = WIDE ? lane >> 2 & 3 : lane & 3;
+            const int u = lane % (SPAN / 8), st = k[e] / SPAN * (SPAN / 32) + u % (SPAN / 32), c4 = u / (SPAN / 32);
             if (in[e])
                 *reinterpret_cast<uint4*>(xs + (((st * TT + (m[e] >> 3)) * 8 + (m[e] & 7)) * 4 + c4) * 16) =
                     make_uint4(h2_bits(y0), h2_bits(y1), h2_bits(y2), h2_bits(y3));
@@ -406,7 +414,7 @@ __global__ void __launch_bounds__(kThreads) qweight_tokens_kernel(const __grid_c
     ptx::grid_wait();
     ptx::grid_launch_dependents();
     const int fshift = QX ? p.xgroup_shift : 8;
-    stage_tokens<TT, QX, STEPS == 4, GRAIN, TT>(
+    stage_tokens<TT, QX, GRAIN < 64 ? 32 : 64, GRAIN, TT>(
         p, b / p.tiles_m, m0, TOK, min(TOK, p.M - m0), k0, p.K, 256, p.tokens + ((size_t)b * p.kp + k0) * (TOK * 2),
         p.sums + ((size_t)b * p.kp + k0) / GRAIN * TOK, p.scales + (((size_t)b * p.kp + k0) >> fshift) * TOK, &bad,
         [] { __syncthreads(); });
@@ -433,19 +441,19 @@ __device__ __forceinline__ uint32_t scale_word(uint32_t scale, uint32_t zero) {
     return scale | (__float_as_uint((float)zero) & 0xFFFF0000u);
 }
 
-// 128 k of a warp's rows times the tokens.
-//   at    : the lane's codes of the first row tile (shared memory)
+// 128 k of a warp's rows times the tokens.  A lane reads its codes of a step of 32 k, or of up to four steps that share
+// the scales at once, which permutes their k; the tokens are staged in the same order.
+//   at    : row g's codes of the first row tile (shared memory), sw its swizzle, BLK the 128 k of them
 //   xat   : the lane's token operands
 //   words : the lane's row's scale word, of the block's first group; a group's words are `wrows` apart
 //   sums, scales: the lane's token pair's, of the block's first row
 //   acc   : [row tile][token tile][row g, g + 8] of the token pair
-template <int TT, int WSTEPS, int STEPS>
-__device__ __forceinline__ void products(uint64_t (&acc)[Shape<TT>::RT][TT][2], uint32_t at, uint32_t xat, const uint32_t* words,
+template <int TT, int WSTEPS, int STEPS, int BLK>
+__device__ __forceinline__ void products(uint64_t (&acc)[Shape<TT>::RT][TT][2], uint32_t at, uint32_t sw, int c, uint32_t xat, const uint32_t* words,
                                          int wrows, const float* sums, const float* scales, int fshift) {
     using S = Shape<TT>;
     constexpr int TOK = S::TOK, RT = S::RT, PITCH = S::PITCH;
     constexpr bool OWN = S::OWN;
-    constexpr bool WIDE = STEPS == 4;  // a lane reads its 32 codes of 128 at once: all of them share the scales
     // Two row tiles take the 128 k in two parts, whose operands fit the registers, and TB token tiles at a time; one
     // takes CH chains of sums: a dependent instruction waits for the one before it.
     constexpr int PARTS = OWN ? 2 : 1, SP = 4 / PARTS, TB = OWN ? 2 : 1, CH = OWN ? 1 : 2;
@@ -459,19 +467,25 @@ __device__ __forceinline__ void products(uint64_t (&acc)[Shape<TT>::RT][TT][2], 
         for (int rt = 0; rt < RT; ++rt) {
             uint32_t lo[SP], hi[SP];
             const uint32_t from = at + rt * 16 * PITCH;
-            if (WIDE && SP == 4) {
-                const uint4 l4 = ld_shared_v4(from), h4 = ld_shared_v4(from + 8 * PITCH);
+            if (STEPS == 4 && SP == 4) {
+                const uint32_t o = ((uint32_t)c * 16u ^ sw) ^ (BLK * 64u);
+                const uint4 l4 = ld_shared_v4(from + o), h4 = ld_shared_v4(from + 8 * PITCH + o);
                 lo[0] = l4.x; lo[1] = l4.y; lo[SP - 2] = l4.z; lo[SP - 1] = l4.w;
                 hi[0] = h4.x; hi[1] = h4.y; hi[SP - 2] = h4.z; hi[SP - 1] = h4.w;
-            } else if (WIDE) {
-                const uint2 l2 = ld_shared_v2(from + s0 * 4), h2 = ld_shared_v2(from + 8 * PITCH + s0 * 4);
-                lo[0] = l2.x; lo[1] = l2.y;
-                hi[0] = h2.x; hi[1] = h2.y;
+            } else if (STEPS >= 2) {
+#pragma unroll
+                for (int st = 0; st < SP; st += 2) {
+                    const uint32_t o = (((uint32_t)c / 2u * 16u ^ sw) ^ (BLK * 64u + (s0 + st) / 2 * 32u)) + (uint32_t)c % 2u * 8u;
+                    const uint2 l2 = ld_shared_v2(from + o), h2 = ld_shared_v2(from + 8 * PITCH + o);
+                    lo[st] = l2.x; lo[st + 1] = l2.y;
+                    hi[st] = h2.x; hi[st + 1] = h2.y;
+                }
             } else {
 #pragma unroll
                 for (int st = 0; st < SP; ++st) {
-                    lo[st] = ld_shared(from + (s0 + st) * 16);
-                    hi[st] = ld_shared(from + 8 * PITCH + (s0 + st) * 16);
+                    const uint32_t o = (sw ^ (BLK * 64u + (s0 + st) * 16u)) + (uint32_t)c * 4u;
+                    lo[st] = ld_shared(from + o);
+                    hi[st] = ld_shared(from + 8 * PITCH + o);
                 }
             }
 #pragma unroll
@@ -608,7 +622,6 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_c
     constexpr int TT = 1;
     using S = Shape<TT>;
     constexpr int TOK = S::TOK, ROWS = S::ROWS, ITEM = S::ITEM, PITCH = S::PITCH, LD = S::LD;
-    constexpr bool WIDE = STEPS == 4;       // a lane reads its 32 codes of 128 at once: all of them share the scales
     constexpr int SLOT = S::SLOT, DEPTH = S::DEPTH, UNITS = S::UNITS;
     constexpr int GRAIN = STEPS * 32;       // k that share both scales
     constexpr float UNIT = QX ? 0x1p24f : 0x1p12f;  // what the sums lack (half of it is in the staged scales: none under- or overflows)
@@ -643,7 +656,8 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_c
     constexpr int LPR = ITEM / 32, RPI = 32 / LPR, CP = ROWS / RPI;  // lanes a row of codes, rows an instruction, instructions
     const int64_t rstep = (int64_t)RPI * (p.K >> 1);
     const int64_t lane_off = (int64_t)(lane / LPR) * (p.K >> 1) + lane % LPR * 16;
-    const uint32_t lane_to = (uint32_t)(lane / LPR * PITCH + lane % LPR * 16);
+    const uint32_t lane_to = (uint32_t)(lane / LPR * PITCH) + ((uint32_t)(lane % LPR * 16) ^ swizzle<PITCH>(lane / LPR));
+    static_assert(RPI == 4, "a row 4 further has the lowest bit of its swizzle the other way");
     const uint8_t* fcodes = nullptr;
     int ftl = -1, fleft = 0, fkk = 0, fgl = 0, fk = 0, fn = 0;
     auto seek = [&]() {  // group fgl, K index fkk of tile ftl
@@ -668,13 +682,13 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_c
         const uint32_t to = slot + lane_to;
         if (fn >= ROWS && fk + ITEM <= kend) {
 #pragma unroll
-            for (int j = 0; j < CP; ++j) cp_async16(to + j * RPI * PITCH, fcodes + j * rstep);
+            for (int j = 0; j < CP; ++j) cp_async16((to ^ (j & 1) * 16u) + j * RPI * PITCH, fcodes + j * rstep);
         } else {  // rows or K that end within the item: zeros
             const bool kin = fk + lane % LPR * 32 < kend;
 #pragma unroll
             for (int j = 0; j < CP; ++j) {
                 const bool in = kin && j * RPI < fn;
-                cp_async16(to + j * RPI * PITCH, in ? fcodes + j * rstep : p.codes[r], in);
+                cp_async16((to ^ (j & 1) * 16u) + j * RPI * PITCH, in ? fcodes + j * rstep : p.codes[r], in);
             }
         }
         cp_commit();
@@ -740,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_c
     };
     auto stage = [&](int tl) {
         const int t0 = kbeg + tl * p.tile_k;
-        stage_tokens<TT, QX, WIDE, GRAIN, UNITS>(p, r, m0, toks, toks, t0, kend, p.tile_k, xs, xsum, xsc, bad, [&] {
+        stage_tokens<TT, QX, GRAIN, GRAIN, UNITS>(p, r, m0, toks, toks, t0, kend, p.tile_k, xs, xsum, xsc, bad, [&] {
             load_scales(t0, 0);  // in flight with the tokens
             __syncthreads();     // every warp is done with the tile before (first: with clearing)
         });
@@ -752,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_c
     for (int t = 0; t < TT; ++t)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[0][t][j] = 0ull;
-    const uint32_t xs_addr = ptx::smem_u32(xs) + lane * 16u;
+    const uint32_t xs_addr = ptx::smem_u32(xs) + lane * 16u, sw = swizzle<PITCH>(g);
     uint32_t cur = ring;
     const uint32_t ring_end = ring + DEPTH * SLOT;
 #pragma unroll 1
@@ -766,16 +780,18 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_c
             __syncwarp();  // every lane's copies have landed, and every lane has left the slot refilled now
             const uint32_t next = cur + SLOT == ring_end ? ring : cur + SLOT;
             fetch(next + SLOT == ring_end ? ring : next + SLOT);
-            const uint32_t at = cur + g * PITCH + c * (WIDE ? 16 : 4);
+            const uint32_t at = cur + g * PITCH;
             cur = next;
             if (ktile + kk * ITEM < kend) {
-#pragma unroll
-                for (int blk = 0; blk < ITEM / 128; ++blk) {
-                    const int kt = kk * ITEM + blk * 128;  // within the tile
-                    products<TT, WSTEPS, STEPS>(acc, at + blk * 64, xs_addr + (uint32_t)((kt >> 5) * TT * 512),
-                                                wsc + (kt >> p.group_shift) * wrows + gl * ROWS + g, wrows,
-                                                xsum + kt / GRAIN * TOK + 2 * c, xsc + (kt >> fshift) * TOK + 2 * c, fshift);
-                }
+                auto block = [&](auto blk) {
+                    constexpr int BLK = decltype(blk)::value;
+                    const int kt = kk * ITEM + BLK * 128;  // within the tile
+                    products<TT, WSTEPS, STEPS, BLK>(acc, at, sw, c, xs_addr + (uint32_t)((kt >> 5) * TT * 512),
+                                                     wsc + (kt >> p.group_shift) * wrows + gl * ROWS + g, wrows,
+                                                     xsum + kt / GRAIN * TOK + 2 * c, xsc + (kt >> fshift) * TOK + 2 * c, fshift);
+                };
+                block(std::integral_constant<int, 0>());
+                block(std::integral_constant<int, 1>());
             }
             if (++kk == per || left == 1) {
                 // the warp leaves a group: its sums go to the slot of (group, warp), which no other
@@ -857,7 +873,8 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
     const int rstep = RPI * (p.K >> 1);                              // p.K <= 2^20: a warp's rows are within 2^31 of each other
     int fk = kbeg;
     const uint8_t* fcodes = p.codes[r] + (((int64_t)frow * p.K + kbeg) >> 1) + lane / LPR * (p.K >> 1) + lane % LPR * 16;
-    const uint32_t lane_to = (uint32_t)(lane / LPR * PITCH + lane % LPR * 16);
+    const uint32_t lane_to = (uint32_t)(lane / LPR * PITCH) + ((uint32_t)(lane % LPR * 16) ^ swizzle<PITCH>(lane / LPR));
+    static_assert(RPI == 8, "a row 8 further has the same swizzle");
     auto fetch = [&](uint32_t slot) {
         if (active && fk < kend) {
             const uint32_t to = slot + lane_to;
@@ -958,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
         for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int j = 0; j < 2; ++j) acc[a][t][j] = 0ull;
-    const uint32_t xs_addr = ptx::smem_u32(xs) + lane * 16u;
+    const uint32_t xs_addr = ptx::smem_u32(xs) + lane * 16u, sw = swizzle<PITCH>(g);
     const uint32_t* words = wsc + warp * ROWS + g;
     const float *sums = xsum + 2 * c, *scales = xsc + 2 * c;
     uint32_t cur = ring;
@@ -976,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
             const uint32_t next = cur + SLOT == ring_end ? ring : cur + SLOT;
             fetch(next + SLOT == ring_end ? ring : next + SLOT);
             if (active && kbeg + tl * TILE + kk * ITEM < kend)
-                products<TT, WSTEPS, STEPS>(acc, cur + g * PITCH + c * (STEPS == 4 ? 16 : 4),
+                products<TT, WSTEPS, STEPS, 0>(acc, cur + g * PITCH, sw, c,
                                             xs_addr + (uint32_t)(buf * W::XS + kk * (4 * TT * 512)),
                                             words + buf * W::WSC + kk * (4 / WSTEPS * WROWS), WROWS,
                                             sums + buf * W::XSUM + kk * (4 / STEPS * TOK),
