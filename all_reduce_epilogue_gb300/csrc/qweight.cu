@@ -711,8 +711,8 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_c
     }
     ptx::grid_launch_dependents();
     ptx::grid_wait();
-    fetch(ring);
-    fetch(ring + SLOT);
+#pragma unroll
+    for (int i = 0; i < DEPTH - 1; ++i) fetch(ring + i * SLOT);
 
     // The rows' scales and zero points: neighbouring lanes take a row's neighbouring groups (lanes on rows
     // of their own would touch a sector each with every load); what does not exist weighs nothing.
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_c
             cp_wait<DEPTH - 2>();
             __syncwarp();  // every lane's copies have landed, and every lane has left the slot refilled now
             const uint32_t next = cur + SLOT == ring_end ? ring : cur + SLOT;
-            fetch(next + SLOT == ring_end ? ring : next + SLOT);
+            fetch(cur == ring ? ring_end - SLOT : cur - SLOT);  // the slot before
             const uint32_t at = cur + g * PITCH;
             cur = next;
             if (ktile + kk * ITEM < kend) {
@@ -947,8 +947,8 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
     ptx::grid_launch_dependents();
     // The kernel before is the one that stages the tokens, and lets this one start when all that ran before it has
     // ended: the weights can be read, the tokens after the wait.
-    fetch(ring);
-    fetch(ring + SLOT);
+#pragma unroll
+    for (int i = 0; i < DEPTH - 1; ++i) fetch(ring + i * SLOT);
     for (int kk = 0; kk < PER; ++kk) {
         load_scales(0, kk);
         store_scales(0, kk);
@@ -991,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
             cp_wait<DEPTH - 2>();
             __syncwarp();  // every lane's copies have landed, its scales are stored, and it has left the slot refilled now
             const uint32_t next = cur + SLOT == ring_end ? ring : cur + SLOT;
-            fetch(next + SLOT == ring_end ? ring : next + SLOT);
+            fetch(cur == ring ? ring_end - SLOT : cur - SLOT);  // the slot before
             if (active && kbeg + tl * TILE + kk * ITEM < kend)
                 products<TT, WSTEPS, STEPS, 0>(acc, cur + g * PITCH, sw, c,
                                             xs_addr + (uint32_t)(buf * W::XS + kk * (4 * TT * 512)),
