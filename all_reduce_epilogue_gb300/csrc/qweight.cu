@@ -42,8 +42,8 @@
 //  * In tiles of 16 or 32 (qweight_tokens_kernel, then qweight_wide_kernel), they
 //    are staged once, in global memory, and come in tiles of K by bulk copies; a warp
 //    owns 32 rows, which share the tokens' operands, and their sums stay in
-//    registers.  R = 8: 16 tokens, 8192 x 4096, groups of 64: 47 us (4 of them
-//    staging), 3.1 TB/s; 64 tokens, 7168 x 2048: 75 us, tensor pipes 44 %, issue
+//    registers.  R = 8: 16 tokens, 8192 x 4096, groups of 64: 46 us (4 of them
+//    staging), 3.1 TB/s; 64 tokens, 7168 x 2048: 71 us, tensor pipes 44 %, issue
 //    41 %, at the four warps a scheduler that the registers allow.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1214,7 +1214,7 @@ cudaError_t launch_qweight(QweightParams& p, const QweightDevice& dev, uint8_t* 
     // In tiles of 8 tokens a CTA stages its own; tiles of 16 or 32, whichever is expected to end first, are staged by
     // a kernel before (each CTA staging them again took 30 to 50 % of the time at 16 and 64 tokens), as many at
     // once as the scratch holds.  That kernel and its launch cost as much as 30 items:
-    //  * R = 8, 7168 x 2048: 8 tokens 19.7 us in a tile of 8, 22.9 in one of 16; 16 tokens 47 and 23; 64 tokens 75 in 32s;
+    //  * R = 8, 7168 x 2048: 8 tokens 19.2 us in a tile of 8, 22.9 in one of 16; 16 tokens 47 and 21.7; 64 tokens 71 in 32s;
     //  * R = 4, 1024 x 2048: 12 tokens 8.3 and 11.0; 64 tokens 17.5 and 15.8;
     //  * R = 2, 512 x 512: 8 tokens 5.1 and 6.1, 64 tokens 6.1 and 7.0.
     // Rows too long for a staged tile go by 8 tokens.  More than 32 tokens a tile need 200 registers a thread:
