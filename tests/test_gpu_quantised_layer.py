@@ -86,3 +86,49 @@ def test_training_step():
     _, tol, _, tol_g = ref.backward64(dy, h, gamma, dres)
     ref.check(dh, x.grad, tol, "dh")
     ref.check(dgamma, gm.grad, tol_g, "dgamma")
+
+
+def test_two_streams_with_a_workspace_each():
+    """The same calls at once on two streams, each with its own workspace and tensors: the bits of either alone."""
+    need_gpu()
+    R, M, N, K = 4, 24, 512, 1024
+    sides = []
+    for i in range(2):
+        g = torch.Generator(device="cuda").manual_seed(200 + i)
+        rand = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+        parts, gamma = [rand(M, K) for _ in range(R)], torch.rand(K, generator=g, device="cuda") + 0.5
+        w = [are.QWeight(torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8),
+                         rand(N, K // 128) * 0.01, None, 128) for _ in range(R)]
+        out = [torch.empty((M, K), dtype=torch.uint8, device="cuda"), torch.empty((M, K // 128), device="cuda"),
+               torch.empty((M, N), dtype=torch.bfloat16, device="cuda"), torch.empty((M, K), dtype=torch.bfloat16, device="cuda"),
+               torch.empty(K, device="cuda")]
+        ws = are.Workspace(R_max=R, M_max=1, N_max=K)
+        ws.set_debug(are.DEBUG_QWEIGHT_STAGED, 16 * (i + 1))
+        sides.append((parts, gamma, w, out, ws, torch.cuda.Stream()))
+
+    def step(side, stream=None):
+        parts, gamma, w, (q, f, y, dh, dg), ws, _ = side
+        are.allreduce_rmsnorm_quant_groups(parts, None, gamma, 1e-6, q, f, ws, group=128, stream=stream)
+        are.gemm_ar_qweight_qx([q] * R, [f] * R, w, y, ws, xgroup=128, stream=stream)
+        are.allreduce_rmsnorm_backward(parts, parts[0], gamma, 1e-6, dh, dg, ws, stream=stream)
+
+    try:
+        want = []
+        for side in sides:
+            step(side)
+            torch.cuda.synchronize()
+            want.append([t.clone() for t in side[3]])
+            for t in side[3]:
+                t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(50):
+            for side in sides:
+                step(side, side[5])
+        torch.cuda.synchronize()
+        for side, expected in zip(sides, want):
+            assert side[4].device_status()["code"] == 0
+            for t, e in zip(side[3], expected):
+                assert torch.equal(t, e)
+    finally:
+        for side in sides:
+            side[4].close()
