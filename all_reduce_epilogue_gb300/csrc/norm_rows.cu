@@ -31,7 +31,7 @@
 // small kernel adds the blocks' rows of them (4 us).
 // Measured (a copy moves 6.78 TB/s): forward, R = 8, 4096 x 7168: 99 us,
 // 6.2 TB/s; backward, R = 8, 4096 x 7168: 97 us, 6.7 TB/s; R = 1, 16384 x 4096:
-// 90 us, 6.0 TB/s.  One row of 7168 at R = 8: 5.7 us, all latency.  Narrow rows
+// 90 us, 6.0 TB/s.  One row of 7168 at R = 8: 3.9 us, all latency.  Narrow rows
 // are bound by issue: R = 1, 16384 x 2048 backward 57 us, 4.7 TB/s, issue slots
 // 58 % used; so their arithmetic is in pairs of columns, and an SM takes as many
 // blocks as its registers hold (16384 x 1024: 34 us; two blocks 43).
@@ -562,7 +562,14 @@ __global__ void __launch_bounds__(256) dgamma_sum_kernel(const float* part, floa
 // 4096 x 7168: two packs 97 us, four in two blocks 102; R = 4, 2048 x 10240:
 // three packs 51 us, in 17 warps 71, eight 81; 2048 x 16384: five packs 106 us,
 // four in 17 warps 115, eight 132.
-int packs_per_thread(int P) { return P <= 256 ? 1 : P <= 512 ? 2 : P <= 2048 ? 4 : 8; }
+// With no more rows than SMs a block has its SM alone, and a forward row takes
+// up to 512 threads (R = 8, 7168 columns: one row 3.9 us, with 224 threads 5.4;
+// 152 rows 4.5 and 5.7.  Backward it costs: R = 4, 150 x 4096: 6.1 us, with 256
+// threads 5.4).
+int packs_per_thread(int P, bool alone) {
+    if (alone && P <= 1024) return P <= 512 ? 1 : 2;
+    return P <= 256 ? 1 : P <= 512 ? 2 : P <= 2048 ? 4 : 8;
+}
 int backward_packs_per_thread(int P) { return P <= 256 ? 1 : P <= 960 ? 2 : P <= 1440 ? 3 : P <= 1920 ? 4 : 5; }
 
 // Launches on the programmatic dependency: the kernel comes up while the one
@@ -593,7 +600,7 @@ cudaError_t opt_in(F f) {
 RowsPlan rows_plan(RowsParams& p, int num_sms) {
     RowsPlan plan;
     const int P = p.N / 8;
-    plan.ppt = p.backward ? backward_packs_per_thread(P) : packs_per_thread(P);
+    plan.ppt = p.backward ? backward_packs_per_thread(P) : packs_per_thread(P, p.M <= num_sms);
     p.nt = ((P + plan.ppt - 1) / plan.ppt + 31) / 32 * 32;
     p.slices = (P + p.nt - 1) / p.nt;
     p.stage_bytes = p.nsrc * p.nt * 16;
@@ -614,8 +621,8 @@ RowsPlan rows_plan(RowsParams& p, int num_sms) {
 template <bool POW2>
 void (*quant_kernel(int ppt, int threads))(RowsParams) {
     switch (ppt) {
-        case 1: return norm_quant_rows_kernel<1, POW2, 288, 2>;
-        case 2: return norm_quant_rows_kernel<2, POW2, 288, 2>;
+        case 1: return threads <= 288 ? norm_quant_rows_kernel<1, POW2, 288, 2> : norm_quant_rows_kernel<1, POW2, 544, 1>;
+        case 2: return threads <= 288 ? norm_quant_rows_kernel<2, POW2, 288, 2> : norm_quant_rows_kernel<2, POW2, 544, 1>;
         case 4: return threads <= 288 ? norm_quant_rows_kernel<4, POW2, 288, 2> : norm_quant_rows_kernel<4, POW2, 544, 1>;
         default: return norm_quant_rows_kernel<8, POW2, 544, 1>;
     }
