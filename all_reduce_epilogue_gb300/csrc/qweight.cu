@@ -36,15 +36,15 @@
 // goes through global memory and the order never varies.
 //  * In tiles of 8 tokens (qweight_few_kernel), a CTA stages its tokens itself,
 //    and the (group, K) items of a CTA are dealt to its warps in equal contiguous
-//    runs of 16-row groups.  R = 8, one token, 7168 x 2048: 17 us, 3.6 TB/s of
-//    codes; issue slots are 48 % used (about 70 % in the loop over the codes,
-//    which is 60 % of the time), DRAM 37 %.
+//    runs of 16-row groups.  R = 8, one token, 7168 x 2048: 17 us, 3.7 TB/s of
+//    codes; issue slots are 51 % used (about 70 % in the loop over the codes,
+//    which is 60 % of the time), DRAM 38 %.
 //  * In tiles of 16 or 32 (qweight_tokens_kernel, then qweight_wide_kernel), they
 //    are staged once, in global memory, and come in tiles of K by bulk copies; a warp
 //    owns 32 rows, which share the tokens' operands, and their sums stay in
 //    registers.  R = 8: 16 tokens, 8192 x 4096, groups of 64: 46 us (4 of them
-//    staging), 3.1 TB/s; 64 tokens, 7168 x 2048: 71 us, tensor pipes 44 %, issue
-//    41 %, at the four warps a scheduler that the registers allow.
+//    staging), 3.1 TB/s; 64 tokens, 7168 x 2048: 71 us, tensor pipes 47 %, issue
+//    44 %, at the four warps a scheduler that the registers allow.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
