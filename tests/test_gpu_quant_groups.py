@@ -41,7 +41,8 @@ def run(ws, parts, res, gamma, group, pow2, residual_out=True):
 
 # one token to several rows a block; one pack, a partial last group, every packs-per-thread variant, widest row
 SHAPES = [(1, 1, 8), (2, 3, 40), (8, 1, 7168), (3, 5, 264), (4, 37, 4104), (8, 310, 1024), (1, 700, 2056), (5, 2, 5000),
-          (8, 2, 8192), (2, 3, 10008), (7, 2, 16384), (8, 2, 32768), (1, 1300, 64)]
+          (8, 2, 8192), (2, 3, 10008), (7, 2, 16384), (8, 2, 32768), (1, 1300, 64), (6, 200, 7168), (2, 160, 4096),
+          (1, 152, 2064), (4, 153, 5000), (3, 400, 8192), (8, 320, 16384)]
 
 
 @pytest.mark.parametrize("pow2", [False, True])
