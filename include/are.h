@@ -52,7 +52,7 @@
  *  - are_allreduce_rmsnorm_quant_groups, are_allreduce_rmsnorm_backward and the
  *    4-bit linears launch with programmatic stream serialisation: their
  *    kernels may come up while earlier work of the stream still runs, and
- *    touch global memory only when all of it has ended.
+ *    read and write no memory of the caller's before all of it has ended.
  *  - Every argument is validated before anything is launched: on any error
  *    nothing is launched and nothing is written.
  *  - Device-side waits are bounded by the workspace's timeout.  A wait that
