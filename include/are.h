@@ -198,9 +198,10 @@ typedef struct are_launch_info {
     int32_t kernel;       /* are_kernel */
     int32_t grid;         /* CTAs launched */
     int32_t block;        /* threads per CTA */
-    int32_t cluster;      /* CTAs per cluster (1 or 2) */
+    int32_t cluster;      /* CTAs per cluster (1 or 2; 4-bit linear: R times the parts of K, up to 8) */
     int32_t rank_block;   /* GEMM pair kernel: tile pairs per rank block, 0 = a pair's R units consecutive */
-    int32_t variant;      /* AR kernels: 8-element packs per thread of a row (template variant); GEMM pair
+    int32_t variant;      /* AR kernels and the norm's backward pass: 8-element packs per thread of a row
+                             (template variant); 4-bit linear: tokens of a tile / 8 (1, 2, 4); GEMM pair
                              kernel: 1 = every unit reduces its row slice of the tile (two-shot), 0 = the
                              GEMM+RS running sum pushed along the ranks */
     int32_t rank_group;   /* GEMM pair kernel: ranks run together inside a rank block (R = ranks innermost) */
