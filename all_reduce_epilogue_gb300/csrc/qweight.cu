@@ -367,10 +367,11 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
             k[e] = (i >> toksh) * 256 + lane * 8;
             in[e] = i < todo && m[e] < rows && k[e] < tile_k;
             const uint4 w = v[j0 + e];
-            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, w.z == 255u ? 0u : w.z);
+            // (at most 248, so that the scale that undoes it is finite: what is above then leaves fp16 only where it leaves fp32)
+            const uint32_t top = min(__reduce_max_sync(0xFFFFFFFFu, w.z == 255u ? 0u : w.z), 248u);
             // 2^(z - top + 6): below 2^-24 it is nothing; a NaN scale
-            const uint32_t d = top - w.z;
-            const uint32_t mul = w.z == 255u ? 0x7FFFu : d <= 20u ? (21u - d) << 10 : d <= 30u ? 0x400u >> (d - 20u) : 0u;
+            const int d = (int)top - (int)w.z;
+            const uint32_t mul = w.z == 255u ? 0x7FFFu : d <= 20 ? (uint32_t)(21 - d) << 10 : d <= 30 ? 0x400u >> (d - 20) : 0u;
             const __half2 mul2 = h2_of(mul * 0x10001u), odd2 = __hmul2(mul2, __float2half2_rn(0.0625f));
             const uint32_t h[4] = {fp8x2_to_f16x2(w.x), fp8x2_to_f16x2(w.x >> 16), fp8x2_to_f16x2(w.y), fp8x2_to_f16x2(w.y >> 16)};
             const __half2 y0 = __hmul2(h2_of(__byte_perm(h[0], h[2], 0x5410)), mul2), y1 = __hmul2(h2_of(__byte_perm(h[0], h[2], 0x7632)), odd2);
@@ -381,7 +382,7 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
                     make_uint4(h2_bits(y0), h2_bits(y1), h2_bits(y2), h2_bits(y3));
             const float2 f0 = __half22float2(y0), f1 = __half22float2(y1), f2 = __half22float2(y2), f3 = __half22float2(y3);
             sum[e] = ((f0.x + f0.y) + (f2.x + f2.y)) + ((f1.x + f1.y) + (f3.x + f3.y)) * 16.f;
-            // 2^(top - 127) / 2^6 * 2^12 (above 2^127: such tokens overflow fp32 themselves)
+            // 2^(top - 127) / 2^6 * 2^12
             if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = e8m0_to_float(top) * 64.f;
         }
 #pragma unroll

@@ -1,0 +1,46 @@
+"""8-bit tokens of the 4-bit linear at the ends of their scales' ranges, in every token tile."""
+import pytest
+import torch
+
+import all_reduce_epilogue_gb300 as are
+from tests import ops_ref as ref
+from tests.test_gpu_qweight import tiled, weights  # noqa: F401 (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def value(xq, xs, xgroup):
+    """The tokens in 64 bits; xs: E8M0 bytes or fp32."""
+    f = ref.e8m0_value(xs) if xs.dtype == torch.uint8 else xs.double()
+    return xq.view(torch.float8_e4m3fn).double() * f.repeat_interleave(xgroup, -1)[:, :xq.shape[1]]
+
+
+def product(ws, xq, xs, w, group, xgroup):
+    out = torch.full((xq[0].shape[0], w[0][0].shape[0]), 7.0, dtype=torch.bfloat16, device="cuda")
+    are.gemm_ar_qweight_qx(xq, xs, [are.QWeight(*t, group) for t in w], out, ws, xgroup=xgroup)
+    assert ws.device_status()["code"] == 0
+    return out
+
+
+def random_codes(g, *shape):
+    q = torch.randint(0, 256, shape, generator=g, device="cuda", dtype=torch.uint8)
+    q[(q & 0x7F) == 0x7F] = 0x38
+    return q
+
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_largest_power_of_two_scales(tiled, M):  # noqa: F811
+    """Bytes 249 to 254: codes of zero, and codes of 1 under small weights, whose sums fp32 holds."""
+    ws, _ = tiled
+    R, N, K, group = 2, 40, 544, 128
+    w, g = weights(R, N, K, group, True, 300 + M)
+    for _, s, _ in w:
+        s.mul_(2.0 ** -100)
+    xq = [torch.zeros((M, K), dtype=torch.uint8, device="cuda") for _ in range(R)]
+    xs = [torch.randint(249, 255, (M, 17), generator=g, device="cuda", dtype=torch.uint8) for _ in range(R)]
+    xq[0][1:] = 0x38
+    xq[1][2::3] = 0xB8
+    out = product(ws, xq, xs, w, group, 32)
+    assert (out[0] == 0).all()
+    want, tol = ref.linear64([value(q, s, 32) for q, s in zip(xq, xs)], w, group)
+    ref.check(out, want, tol, "out")
