@@ -199,12 +199,6 @@ __device__ __forceinline__ float e8m0_to_float(uint32_t b) {
     return __uint_as_float(b == 255u ? 0x7FC00000u : b == 0u ? 0x00400000u : b << 23);
 }
 
-__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
-__device__ __forceinline__ __half2 h2_of(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
-__device__ __forceinline__ uint32_t fp8x2_to_f16x2(uint32_t v) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 // Two floats of tokens as fp16.
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -272,7 +266,6 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
     }
     between();
     // two rows at a time, so that one's steps fill the waits of the other's
-    if (QX || !p.qx)
 #pragma unroll
     for (int j0 = 0; j0 < UNITS; j0 += 2) {
         if (warp + j0 * kWarps >= todo) break;
@@ -286,19 +279,29 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
             m[e] = i & (tokp - 1);
             k[e] = (i >> toksh) * 256 + lane * 8;
             in[e] = i < todo && m[e] < rows && k[e] < tile_k;
-            uint4& w = v[j0 + e];
-            if (QX) {
+            const uint4& w = v[j0 + e];
+            if (QX || p.qx) {
                 const float2 f[4] = {fp8x2_to_float2(w.x), fp8x2_to_float2(w.x >> 16), fp8x2_to_float2(w.y), fp8x2_to_float2(w.y >> 16)};
 #pragma unroll
                 for (int i4 = 0; i4 < 4; ++i4) {
                     x[e][i4] = f[i4].x;
                     x[e][4 + i4] = f[i4].y;
                 }
-            } else {
+            }
+            if (!QX && p.qx) {
+                // codes under power-of-two scales: times the scale over the row's largest and 2^6, rounded to fp16 once
+                // (the largest at most 248, so that what undoes it is finite: what is above then leaves fp16 only where
+                // it leaves fp32)
+                const uint32_t largest = min(__reduce_max_sync(0xFFFFFFFFu, w.z == 255u ? 0u : w.z), 248u);
+                const float mul = __uint_as_float(w.z == 255u ? 0x7FC00000u : (uint32_t)max((int)w.z - (int)largest + 133, 0) << 23);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[e][i] *= mul;
+                if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = e8m0_to_float(largest) * 64.f;  // 2^(largest - 127) / 2^6 * 2^12
+            } else if (!QX) {
                 top[e] = __vmaxu2(__vmaxu2(w.x & 0x7F807F80u, w.y & 0x7F807F80u), __vmaxu2(w.z & 0x7F807F80u, w.w & 0x7F807F80u));
             }
         }
-        if (!QX) {
+        if (!QX && !p.qx) {
             // the largest exponents
 #pragma unroll
             for (int e = 0; e < 2; ++e) top[e] = __reduce_max_sync(0xFFFFFFFFu, max(top[e] >> 23, top[e] >> 7 & 0xFFu));
@@ -344,47 +347,6 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
             sum[e] = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
         }
         // sum x over each GRAIN of k, in the weights' unit
-#pragma unroll
-        for (int o = 1; o < GRAIN / 8; o <<= 1)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], o);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if ((lane & (GRAIN / 8 - 1)) == 0 && in[e]) xsum[k[e] / GRAIN * TOK + m[e]] = sum[e] * 0x1p-24f;
-    }
-    // FP8 codes under power-of-two scales: in fp16, times the scale over the row's largest and 2^6
-    if (!QX && p.qx)
-#pragma unroll
-    for (int j0 = 0; j0 < UNITS; j0 += 2) {
-        if (warp + j0 * kWarps >= todo) break;
-        float sum[2];
-        int m[2], k[2];
-        bool in[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = warp + (j0 + e) * kWarps;
-            m[e] = i & (tokp - 1);
-            k[e] = (i >> toksh) * 256 + lane * 8;
-            in[e] = i < todo && m[e] < rows && k[e] < tile_k;
-            const uint4 w = v[j0 + e];
-            // (at most 248, so that the scale that undoes it is finite: what is above then leaves fp16 only where it leaves fp32)
-            const uint32_t top = min(__reduce_max_sync(0xFFFFFFFFu, w.z == 255u ? 0u : w.z), 248u);
-            // 2^(z - top + 6): below 2^-24 it is nothing; a NaN scale
-            const int d = (int)top - (int)w.z;
-            const uint32_t mul = w.z == 255u ? 0x7FFFu : d <= 20 ? (uint32_t)(21 - d) << 10 : d <= 30 ? 0x400u >> (d - 20) : 0u;
-            const __half2 mul2 = h2_of(mul * 0x10001u), odd2 = __hmul2(mul2, __float2half2_rn(0.0625f));
-            const uint32_t h[4] = {fp8x2_to_f16x2(w.x), fp8x2_to_f16x2(w.x >> 16), fp8x2_to_f16x2(w.y), fp8x2_to_f16x2(w.y >> 16)};
-            const __half2 y0 = __hmul2(h2_of(__byte_perm(h[0], h[2], 0x5410)), mul2), y1 = __hmul2(h2_of(__byte_perm(h[0], h[2], 0x7632)), odd2);
-            const __half2 y2 = __hmul2(h2_of(__byte_perm(h[1], h[3], 0x5410)), mul2), y3 = __hmul2(h2_of(__byte_perm(h[1], h[3], 0x7632)), odd2);
-            const int u = lane % (SPAN / 8), st = k[e] / SPAN * (SPAN / 32) + u % (SPAN / 32), c4 = u / (SPAN / 32);
-            if (in[e])
-                *reinterpret_cast<uint4*>(xs + (((st * TT + (m[e] >> 3)) * 8 + (m[e] & 7)) * 4 + c4) * 16) =
-                    make_uint4(h2_bits(y0), h2_bits(y1), h2_bits(y2), h2_bits(y3));
-            const float2 f0 = __half22float2(y0), f1 = __half22float2(y1), f2 = __half22float2(y2), f3 = __half22float2(y3);
-            sum[e] = ((f0.x + f0.y) + (f2.x + f2.y)) + ((f1.x + f1.y) + (f3.x + f3.y)) * 16.f;
-            // 2^(top - 127) / 2^6 * 2^12
-            if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = e8m0_to_float(top) * 64.f;
-        }
 #pragma unroll
         for (int o = 1; o < GRAIN / 8; o <<= 1)
 #pragma unroll

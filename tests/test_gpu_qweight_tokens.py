@@ -44,3 +44,25 @@ def test_largest_power_of_two_scales(tiled, M):  # noqa: F811
     assert (out[0] == 0).all()
     want, tol = ref.linear64([value(q, s, 32) for q, s in zip(xq, xs)], w, group)
     ref.check(out, want, tol, "out")
+
+
+@pytest.mark.parametrize("odd", [0, 1])
+def test_small_values_beside_a_large_one(tiled, odd):  # noqa: F811
+    """One value of 448 * 2^-d, d = 18 to 34, at an even or an odd k, beside one of 448 whose weights are zero.  A token
+    is off by at most 2^-35 of the largest of its 256 k, and exact from 2^-31 of it up."""
+    ws, _ = tiled
+    N, K, group = 72, 256, 32
+    w, _ = weights(1, N, K, group, False, 310)
+    w[0][0][:, 0] = 0x88  # k = 0 and 1 weigh nothing
+    d = torch.arange(18, 35, device="cuda")
+    M = len(d)
+    xq = torch.zeros((M, K), dtype=torch.uint8, device="cuda")
+    xs = torch.full((M, 8), 127, dtype=torch.uint8, device="cuda")
+    xq[:, 0] = 0x7E
+    at = 32 + 2 * torch.arange(M, device="cuda") * 6 + odd  # in groups 1 to 7
+    xq[torch.arange(M, device="cuda"), at] = 0x7E
+    xs[torch.arange(M, device="cuda"), at // 32] = (127 - d).to(torch.uint8)
+    out = product(ws, [xq], [xs], w, group, 32)
+    want, tol = ref.linear64([value(xq, xs, 32)], w, group)
+    lost = torch.where(d > 31, 448 * 2.0 ** -35, 0.0).double()[:, None] * 15 * w[0][1].double()[:, at // 32].T
+    ref.check(out, want, tol + lost, "out")
