@@ -15,11 +15,10 @@
 //    (Codes made into integers in fp16 take 9 instructions a word and in bf16
 //    11; FP8 operands would take 3, but FP8 mma.sync is not native here: it
 //    measured 36 cycles a sub-core for 32 of k, fp16 8.2 for 16.)
-//  * FP8 tokens are exact in fp16, and so are FP8 ones times power-of-two
-//    scales relative to their 256 of k's largest (what is 2^-30 below it is
-//    off by at most 2^-34 of it).  bf16 tokens are scaled, per token and 256 of
-//    k, by the power of two that takes the largest to 2^14..2^15, which their
-//    scale in fp32 undoes: what is 2^-27 times the largest or more stays exact,
+//  * FP8 tokens are exact in fp16.  bf16 tokens, and FP8 ones times their
+//    power-of-two scales, are scaled, per token and 256 of k, by the power of
+//    two that takes the largest value to 2^14..2^15, which their scale in fp32
+//    undoes: what is 2^-27 (FP8: 2^-31) times the largest or more stays exact,
 //    what is smaller is off by at most 2^-35 of it, below the fp32 sums' own
 //    rounding.
 //  * The zero point leaves the sums: sum (u - z) x = sum u x - z sum x, with
@@ -195,10 +194,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t* a, uint32_t b
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float e8m0_to_float(uint32_t b) {
-    return __uint_as_float(b == 255u ? 0x7FC00000u : b == 0u ? 0x00400000u : b << 23);
-}
-
 // Two floats of tokens as fp16.
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -289,14 +284,20 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
                 }
             }
             if (!QX && p.qx) {
-                // codes under power-of-two scales: times the scale over the row's largest and 2^6, rounded to fp16 once
-                // (the largest at most 248, so that what undoes it is finite: what is above then leaves fp16 only where
-                // it leaves fp32)
-                const uint32_t largest = min(__reduce_max_sync(0xFFFFFFFFu, w.z == 255u ? 0u : w.z), 248u);
-                const float mul = __uint_as_float(w.z == 255u ? 0x7FC00000u : (uint32_t)max((int)w.z - (int)largest + 133, 0) << 23);
+                // Codes under power-of-two scales: their largest value to 2^14..2^15, as for bf16, whatever scales the
+                // codes of zero are under.  `largest`: of the lanes' scale bytes plus biased exponents; within what
+                // keeps the factor that undoes it, 2^(largest - 268) * 2^12, a normal number (2^129 and more, which
+                // fp32 does not hold, may leave fp16)
+                float a = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[e][i] *= mul;
-                if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = e8m0_to_float(largest) * 64.f;  // 2^(largest - 127) / 2^6 * 2^12
+                for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[e][i]));
+                const uint32_t own = a == 0.f || w.z == 255u ? 0u : w.z + (__float_as_uint(a) >> 23);
+                const int largest = min(max((int)__reduce_max_sync(0xFFFFFFFFu, own), 141), 383);
+                // 2^(z - 127) * 2^(268 - largest), biased (at most 150 where a code is not zero); a NaN scale
+                const int mul = max(min((int)w.z - largest + 268, 150), 0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[e][i] *= __uint_as_float(w.z == 255u ? 0x7FC00000u : (uint32_t)mul << 23);
+                if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = __uint_as_float((uint32_t)(largest - 129) << 23);
             } else if (!QX) {
                 top[e] = __vmaxu2(__vmaxu2(w.x & 0x7F807F80u, w.y & 0x7F807F80u), __vmaxu2(w.z & 0x7F807F80u, w.w & 0x7F807F80u));
             }

@@ -570,8 +570,9 @@ ARE_API are_status are_gemm_ar_qweight(const are_bf16* const x[], const are_qwei
  *  xgroup      : 32, 64 or 128, independent of `group`
  * The other arguments and the arithmetic are as for are_gemm_ar_qweight.  fp32
  * token scales are applied in fp32 to the sums of each shared group of k; E8M0
- * scales go into the fp16 tokens relative to the largest of each 256 of k: what
- * is 2^-30 of it or less is off by at most 2^-34 of it.
+ * scales go into the fp16 tokens, scaled by a power of two per token and 256 of
+ * k as bf16 tokens are: values down to 2^-31 times the largest of the 256
+ * exactly, smaller ones to 2^-35 of it.
  */
 ARE_API are_status are_gemm_ar_qweight_qx(const uint8_t* const xq[], const void* const xscale[], int scale_format,
                                           int xgroup, const are_qweight w[], int group, are_bf16* const out[], int R,

@@ -66,3 +66,28 @@ def test_small_values_beside_a_large_one(tiled, odd):  # noqa: F811
     want, tol = ref.linear64([value(xq, xs, 32)], w, group)
     lost = torch.where(d > 31, 448 * 2.0 ** -35, 0.0).double()[:, None] * 15 * w[0][1].double()[:, at // 32].T
     ref.check(out, want, tol + lost, "out")
+
+
+@pytest.mark.parametrize("K,xgroup", [(256, 32), (544, 32), (512, 128)])
+def test_groups_of_zeros_beside_small_ones(tiled, K, xgroup):  # noqa: F811
+    """In every 256 k a group of zeros, under the scale 1 that the quantised norm gives it or the largest there is; the
+    others' scales are 2^-20 to 2^-40, the same in a row, so that what a row loses shows in its own sums."""
+    ws, _ = tiled
+    R, M, N, group = 2, 41, 72, 128
+    w, g = weights(R, N, K, group, True, 320 + K)
+    G = -(-K // xgroup)
+    byte = 87 + torch.arange(M, device="cuda") // 2
+    xq, xs = [], []
+    for r in range(R):
+        q = random_codes(g, M, K)
+        s = byte[:, None].repeat(1, G).to(torch.uint8)
+        for a in range(r % 2, G, 256 // xgroup):
+            q[:, a * xgroup:(a + 1) * xgroup] = 0
+            s[0::2, a], s[1::2, a] = 127, 254
+        xq.append(q), xs.append(s)
+    xq[0][5], xq[1][5] = 0, 0  # and a token of zeros
+    out = product(ws, xq, xs, w, group, xgroup)
+    want, tol = ref.linear64([value(q, s, xgroup) for q, s in zip(xq, xs)], w, group)
+    lost = 448 * 2.0 ** (byte.double()[:, None] - 127 - 35) * 15 * xgroup * sum(-(-group // xgroup) * t[1].double().sum(1) for t in w)
+    ref.check(out, want, tol + lost, "out")
+    assert (out[5] == 0).all()
