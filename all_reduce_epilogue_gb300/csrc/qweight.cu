@@ -283,7 +283,10 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
                     x[e][4 + i4] = f[i4].y;
                 }
             }
-            if (!QX && p.qx) {
+            if (QX) {  // as far up as fp16 goes (448 * 2^7)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[e][i] *= 128.f;
+            } else if (p.qx) {
                 // Codes under power-of-two scales: their largest value to 2^14..2^15, as for bf16, whatever scales the
                 // codes of zero are under.  `largest`: of the lanes' scale bytes plus biased exponents; within what
                 // keeps the factor that undoes it, 2^(largest - 268) * 2^12, a normal number (2^129 and more, which
@@ -298,7 +301,7 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[e][i] *= __uint_as_float(w.z == 255u ? 0x7FC00000u : (uint32_t)mul << 23);
                 if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = __uint_as_float((uint32_t)(largest - 129) << 23);
-            } else if (!QX) {
+            } else {
                 top[e] = __vmaxu2(__vmaxu2(w.x & 0x7F807F80u, w.y & 0x7F807F80u), __vmaxu2(w.z & 0x7F807F80u, w.w & 0x7F807F80u));
             }
         }
@@ -588,7 +591,9 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_c
     constexpr int TOK = S::TOK, ROWS = S::ROWS, ITEM = S::ITEM, PITCH = S::PITCH, LD = S::LD;
     constexpr int SLOT = S::SLOT, DEPTH = S::DEPTH, UNITS = S::UNITS;
     constexpr int GRAIN = STEPS * 32;       // k that share both scales
-    constexpr float UNIT = QX ? 0x1p24f : 0x1p12f;  // what the sums lack (half of it is in the staged scales: none under- or overflows)
+    // What the sums lack of the codes' 2^24: 2^12 of it is in the staged scales, or 2^7 in the tokens.  So outputs down to
+    // bf16's smallest normal ones keep bits enough in fp32 sums.
+    constexpr float UNIT = QX ? 0x1p17f : 0x1p12f;
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     const int g = lane >> 2, c = lane & 3;
     const int q = (int)(blockIdx.x % p.cluster);
@@ -807,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
     constexpr int TOK = S::TOK, RT = S::RT, ROWS = S::ROWS, ITEM = S::ITEM, PITCH = S::PITCH, LD = S::LD;
     constexpr int SLOT = S::SLOT, DEPTH = S::DEPTH, TILE = W::TILE, PER = TILE / ITEM, WROWS = W::WROWS;
     constexpr int GRAIN = STEPS * 32;       // k that share both scales
-    constexpr float UNIT = QX ? 0x1p24f : 0x1p12f;
+    constexpr float UNIT = QX ? 0x1p17f : 0x1p12f;  // as in qweight_few_kernel
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     const int g = lane >> 2, c = lane & 3;
     const int q = (int)(blockIdx.x % p.cluster);

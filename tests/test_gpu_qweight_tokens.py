@@ -91,3 +91,20 @@ def test_groups_of_zeros_beside_small_ones(tiled, K, xgroup):  # noqa: F811
     lost = 448 * 2.0 ** (byte.double()[:, None] - 127 - 35) * 15 * xgroup * sum(-(-group // xgroup) * t[1].double().sum(1) for t in w)
     ref.check(out, want, tol + lost, "out")
     assert (out[5] == 0).all()
+
+
+@pytest.mark.parametrize("xgroup", [32, 128])
+def test_small_fp32_scales(tiled, xgroup):  # noqa: F811
+    """fp32 token scales from 2^-126 to 2^-90, a magnitude a token; outputs down to bf16's smallest.  The sums are kept
+    2^17 smaller than the output, where a step of fp32 is 2^-149 at least: half a step for a product with scales of
+    up to 7 (2^2.7, the sum it multiplies) and one for the sum, a group: 2^17 * 2^-150 * 8."""
+    ws, _ = tiled
+    R, M, N, K, group = 2, 37, 72, 544, 128
+    w, g = weights(R, N, K, group, True, 330 + xgroup)
+    G = -(-K // xgroup)
+    e = torch.arange(M, device="cuda") - 126.0
+    xq = [random_codes(g, M, K) for _ in range(R)]
+    xs = [torch.exp2(e)[:, None] * (1 + torch.rand((M, G), generator=g, device="cuda")) for _ in range(R)]
+    out = product(ws, xq, xs, w, group, xgroup)
+    want, tol = ref.linear64([value(q, s, xgroup) for q, s in zip(xq, xs)], w, group)
+    ref.check(out, want, tol + R * max(G, -(-K // group)) * 2.0 ** -130 + 2.0 ** -134, "out")
