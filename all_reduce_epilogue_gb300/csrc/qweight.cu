@@ -67,6 +67,9 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSmem = 113 * 1024;       // two CTAs an SM
 
+// What the tokens are: bf16, or FP8 codes with fp32 or with power-of-two scales.
+enum Tokens { kBf16, kFp8, kFp8Pow2 };
+
 // The shape of the kernel for TT token tiles of 8.  An item (a ring slot) is 2 KB of codes.
 template <int TT>
 struct Shape {
@@ -231,9 +234,9 @@ __device__ __forceinline__ float unscale_of(uint32_t top) {
 // loads are in flight together with those of `between`.
 //   xs   : [k / 32][TT][lane] units of 8 k in fp16
 //   xsum : [k / GRAIN][TOK] sum x * 2^-24
-//   xsc  : [k / 256, or k / xgroup with QX][TOK] the tokens' scales
+//   xsc  : [k / 256, or k / xgroup with kFp8][TOK] the tokens' scales
 //   bad  : bit m: token m has a value that is not finite
-template <int TT, bool QX, int SPAN, int GRAIN, int UNITS, typename Between>
+template <int TT, Tokens KIND, int SPAN, int GRAIN, int UNITS, typename Between>
 __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int m0, int rows, int toks, int t0, int kend,
                                              int tile_k, uint8_t* xs, float* xsum, float* xsc, uint32_t* bad,
                                              Between between) {
@@ -243,20 +246,23 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
     while (tokp < rows) tokp <<= 1, ++toksh;
     const int todo = ((tile_k + 255) >> 8) * tokp;  // (256 k, token) rows, the token innermost
     uint4 v[UNITS];
+    constexpr int BYTES = KIND == kBf16 ? 2 : 1;
+    const uint8_t* from = static_cast<const uint8_t*>(p.x[r]) + ((int64_t)m0 * p.K + t0 + lane * 8) * BYTES;  // (32 rows of K <= 2^20: within 2^31)
 #pragma unroll
     for (int j = 0; j < UNITS; ++j) {
         v[j] = make_uint4(0u, 0u, 0u, 0u);
-        const int i = warp + j * kWarps, m = i & (tokp - 1), k = t0 + (i >> toksh) * 256 + lane * 8;
-        const bool in = i < todo && m < toks && k < kend;
-        const int64_t at = (int64_t)(m0 + m) * p.K + k;
-        if (QX || p.qx) {
+        const int i = warp + j * kWarps, m = i & (tokp - 1), k = (i >> toksh) * 256;
+        const bool in = i < todo && m < toks && t0 + lane * 8 + k < kend;
+        const uint8_t* at = from + (m * p.K + k) * BYTES;
+        if constexpr (KIND == kBf16) {
+            ldg_if(v[j], at, in);
+        } else {
             uint2 b = make_uint2(0u, 0u);
-            ldg_if(b, static_cast<const uint8_t*>(p.x[r]) + at, in);
+            ldg_if(b, at, in);
             v[j].x = b.x;
             v[j].y = b.y;
-            if (!QX) ldg_u8_if(v[j].z, static_cast<const uint8_t*>(p.xscale[r]) + (int64_t)(m0 + m) * p.xgroups + (k >> p.xgroup_shift), in);
-        } else {
-            ldg_if(v[j], static_cast<const uint16_t*>(p.x[r]) + at, in);
+            if (KIND == kFp8Pow2)
+                ldg_u8_if(v[j].z, static_cast<const uint8_t*>(p.xscale[r]) + (int64_t)(m0 + m) * p.xgroups + ((t0 + lane * 8 + k) >> p.xgroup_shift), in);
         }
     }
     between();
@@ -274,8 +280,8 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
             m[e] = i & (tokp - 1);
             k[e] = (i >> toksh) * 256 + lane * 8;
             in[e] = i < todo && m[e] < rows && k[e] < tile_k;
-            const uint4& w = v[j0 + e];
-            if (QX || p.qx) {
+            uint4& w = v[j0 + e];
+            if constexpr (KIND != kBf16) {
                 const float2 f[4] = {fp8x2_to_float2(w.x), fp8x2_to_float2(w.x >> 16), fp8x2_to_float2(w.y), fp8x2_to_float2(w.y >> 16)};
 #pragma unroll
                 for (int i4 = 0; i4 < 4; ++i4) {
@@ -283,29 +289,28 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
                     x[e][4 + i4] = f[i4].y;
                 }
             }
-            if (QX) {  // as far up as fp16 goes (448 * 2^7)
+            if constexpr (KIND == kFp8) {  // as far up as fp16 goes (448 * 2^7)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[e][i] *= 128.f;
-            } else if (p.qx) {
-                // Codes under power-of-two scales: their largest value to 2^14..2^15, as for bf16, whatever scales the
-                // codes of zero are under.  `largest`: of the lanes' scale bytes plus biased exponents; within what
-                // keeps the factor that undoes it, 2^(largest - 268) * 2^12, a normal number (2^129 and more, which
-                // fp32 does not hold, may leave fp16)
+                for (int i8 = 0; i8 < 8; ++i8) x[e][i8] *= 128.f;
+            } else if constexpr (KIND == kFp8Pow2) {
+                // The largest value goes to 2^14..2^15, as for bf16, whatever scales the codes of zero are under.
+                // `largest`: of the lanes' scale bytes plus biased exponents; within what keeps the factor that undoes it,
+                // 2^(largest - 268) * 2^12, a normal number (2^129 and more, which fp32 does not hold, may leave fp16)
                 float a = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[e][i]));
+                for (int i8 = 0; i8 < 8; ++i8) a = fmaxf(a, fabsf(x[e][i8]));
                 const uint32_t own = a == 0.f || w.z == 255u ? 0u : w.z + (__float_as_uint(a) >> 23);
                 const int largest = min(max((int)__reduce_max_sync(0xFFFFFFFFu, own), 141), 383);
-                // 2^(z - 127) * 2^(268 - largest), biased (at most 150 where a code is not zero); a NaN scale
+                // 2^(w.z - 127) * 2^(268 - largest), biased (at most 150 where a code is not zero); a NaN scale
                 const int mul = max(min((int)w.z - largest + 268, 150), 0);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[e][i] *= __uint_as_float(w.z == 255u ? 0x7FC00000u : (uint32_t)mul << 23);
+                for (int i8 = 0; i8 < 8; ++i8) x[e][i8] *= __uint_as_float(w.z == 255u ? 0x7FC00000u : (uint32_t)mul << 23);
                 if (lane == 0 && in[e]) xsc[(k[e] >> 8) * TOK + m[e]] = __uint_as_float((uint32_t)(largest - 129) << 23);
             } else {
                 top[e] = __vmaxu2(__vmaxu2(w.x & 0x7F807F80u, w.y & 0x7F807F80u), __vmaxu2(w.z & 0x7F807F80u, w.w & 0x7F807F80u));
             }
         }
-        if (!QX && !p.qx) {
+        if constexpr (KIND == kBf16) {
             // the largest exponents
 #pragma unroll
             for (int e = 0; e < 2; ++e) top[e] = __reduce_max_sync(0xFFFFFFFFu, max(top[e] >> 23, top[e] >> 7 & 0xFFu));
@@ -359,7 +364,7 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
         for (int e = 0; e < 2; ++e)
             if ((lane & (GRAIN / 8 - 1)) == 0 && in[e]) xsum[k[e] / GRAIN * TOK + m[e]] = sum[e] * 0x1p-24f;
     }
-    if (QX) {
+    if constexpr (KIND == kFp8) {
         const int x0 = t0 >> p.xgroup_shift;
         for (int u = threadIdx.x; u < (tile_k >> p.xgroup_shift) * TOK; u += kThreads) {
             const int m = u % TOK, gi = u / TOK;
@@ -370,7 +375,7 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
 }
 
 // The tokens of a launch, staged once for all CTAs that read them: CTA (rank, token tile, 256 k).
-template <int TT, bool QX, int STEPS>
+template <int TT, Tokens KIND, int STEPS>
 __global__ void __launch_bounds__(kThreads) qweight_tokens_kernel(const __grid_constant__ QweightParams p) {
     constexpr int TOK = TT * 8, GRAIN = STEPS * 32;
     __shared__ uint32_t bad;
@@ -380,8 +385,8 @@ __global__ void __launch_bounds__(kThreads) qweight_tokens_kernel(const __grid_c
     // in this order: the kernel that follows knows that all that ran before this one has ended
     ptx::grid_wait();
     ptx::grid_launch_dependents();
-    const int fshift = QX ? p.xgroup_shift : 8;
-    stage_tokens<TT, QX, GRAIN < 64 ? 32 : 64, GRAIN, TT>(
+    const int fshift = KIND == kFp8 ? p.xgroup_shift : 8;
+    stage_tokens<TT, KIND, GRAIN < 64 ? 32 : 64, GRAIN, TT>(
         p, b / p.tiles_m, m0, TOK, min(TOK, p.M - m0), k0, p.K, 256, p.tokens + ((size_t)b * p.kp + k0) * (TOK * 2),
         p.sums + ((size_t)b * p.kp + k0) / GRAIN * TOK, p.scales + (((size_t)b * p.kp + k0) >> fshift) * TOK, &bad,
         [] { __syncthreads(); });
@@ -522,7 +527,7 @@ __device__ __forceinline__ void products(uint64_t (&acc)[Shape<TT>::RT][TT][2], 
 
 // Adds the cluster's sums, r ascending, and writes the outputs.  red: [slot_of(group)][rtoks][LD]; bad: tokens
 // of this CTA's K range that hold a value that is not finite, whose products are added here.
-template <int TT, bool QX, typename Slot>
+template <int TT, bool NOTED, typename Slot>
 __device__ __forceinline__ void combine(const QweightParams& p, int q, int m0, int toks, int group0, int groups,
                                         const float* red, const uint32_t* bad, Slot slot_of) {
     constexpr int ROWS = Shape<TT>::ROWS, LD = Shape<TT>::LD;
@@ -531,7 +536,7 @@ __device__ __forceinline__ void combine(const QweightParams& p, int q, int m0, i
     constexpr int PAIRS = ROWS / 2;  // pairs of rows of a group
     const uint32_t base = ptx::smem_u32(red), bad_addr = ptx::smem_u32(bad);
     uint32_t any = 0u;
-    if (!QX) {
+    if (NOTED) {
 #pragma unroll
         for (int j = 0; j < kMaxRanks; ++j)
             if (j < p.cluster) any |= ld_cluster(ptx::mapa_shared(bad_addr, (uint32_t)j));
@@ -551,7 +556,7 @@ __device__ __forceinline__ void combine(const QweightParams& p, int q, int m0, i
                     s.y += v.y;
                 }
             }
-            if (!QX && (any >> m & 1u)) {  // products of values that are not finite
+            if (NOTED && (any >> m & 1u)) {  // products of values that are not finite
                 for (int j = 0; j < p.cluster; ++j) {
                     const int rj = j / p.splits, k0 = j % p.splits * p.split_k, k1 = min(p.K, k0 + p.split_k);
                     const int64_t row = (int64_t)(m0 + m) * p.K;
@@ -579,14 +584,15 @@ __device__ __forceinline__ void combine(const QweightParams& p, int q, int m0, i
 }
 
 // Up to 8 tokens a tile.
-// QX: tokens in 8 bits with fp32 scales, which are applied with the weights'
-// (power-of-two scales go into the staged tokens, exactly).
+// fp32 token scales (QX) are applied with the weights'; power-of-two scales go
+// into the staged tokens.
 // WSTEPS: steps of 32 k in a weight group; STEPS: those that share both scales,
 // the smaller of the weight and the token group.
-template <bool QX, int WSTEPS, int STEPS>
+template <Tokens KIND, int WSTEPS, int STEPS>
 __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_constant__ QweightParams p) {
     extern __shared__ __align__(128) uint8_t qw_smem[];
     constexpr int TT = 1;
+    constexpr bool QX = KIND == kFp8;
     using S = Shape<TT>;
     constexpr int TOK = S::TOK, ROWS = S::ROWS, ITEM = S::ITEM, PITCH = S::PITCH, LD = S::LD;
     constexpr int SLOT = S::SLOT, DEPTH = S::DEPTH, UNITS = S::UNITS;
@@ -723,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_c
     };
     auto stage = [&](int tl) {
         const int t0 = kbeg + tl * p.tile_k;
-        stage_tokens<TT, QX, GRAIN, GRAIN, UNITS>(p, r, m0, toks, toks, t0, kend, p.tile_k, xs, xsum, xsc, bad, [&] {
+        stage_tokens<TT, KIND, GRAIN, GRAIN, UNITS>(p, r, m0, toks, toks, t0, kend, p.tile_k, xs, xsum, xsc, bad, [&] {
             load_scales(t0, 0);  // in flight with the tokens
             __syncthreads();     // every warp is done with the tile before (first: with clearing)
         });
@@ -799,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_c
                 red[(s0 * p.rtoks + m) * LD + (lane & 15)] += red[((a + w) * p.rtoks + m) * LD + (lane & 15)];
         }
     }
-    combine<TT, QX>(p, q, m0, toks, group0, groups, red, bad, slot_of);
+    combine<TT, KIND == kBf16>(p, q, m0, toks, group0, groups, red, bad, slot_of);
 }
 
 // Tiles of 16 or 32 tokens: a warp owns 32 rows.  The staged tokens come in tiles of K by bulk copies, the
@@ -999,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_wide_kernel(const __grid_
             }
         }
     }
-    combine<TT, QX>(p, q, m0, min(TOK, p.M - m0), group0, groups, red, bad, [](int a) { return a; });
+    combine<TT, !QX>(p, q, m0, min(TOK, p.M - m0), group0, groups, red, bad, [](int a) { return a; });
 }
 
 typedef void (*Kernel)(QweightParams);
@@ -1009,38 +1015,42 @@ struct Choice {
     Kernel kernel;
     size_t smem;
 };
-template <int TT, bool QX, int WSTEPS, int STEPS>
+template <int TT, Tokens KIND, int WSTEPS, int STEPS>
 Choice choice() {
-    if constexpr (TT == 1) return {qweight_few_kernel<QX, WSTEPS, STEPS>, 0};
+    constexpr bool QX = KIND == kFp8;  // (wide tiles: the staged bf16 and power-of-two tokens look alike)
+    if constexpr (TT == 1) return {qweight_few_kernel<KIND, WSTEPS, STEPS>, 0};
     else return {qweight_wide_kernel<TT, QX, WSTEPS, STEPS>, Wide<TT, QX, WSTEPS, STEPS>::SMEM};
 }
-template <int TT, bool QX, int WSTEPS>
+template <int TT, Tokens KIND, int WSTEPS>
 Choice kernel_of(int steps) {
-    if constexpr (!QX || WSTEPS == 1) return choice<TT, QX, WSTEPS, WSTEPS>();
-    else if constexpr (WSTEPS == 2) return steps == 1 ? choice<TT, QX, 2, 1>() : choice<TT, QX, 2, 2>();
-    else return steps == 1 ? choice<TT, QX, 4, 1>() : steps == 2 ? choice<TT, QX, 4, 2>() : choice<TT, QX, 4, 4>();
+    if constexpr (KIND != kFp8 || WSTEPS == 1) return choice<TT, KIND, WSTEPS, WSTEPS>();
+    else if constexpr (WSTEPS == 2) return steps == 1 ? choice<TT, KIND, 2, 1>() : choice<TT, KIND, 2, 2>();
+    else return steps == 1 ? choice<TT, KIND, 4, 1>() : steps == 2 ? choice<TT, KIND, 4, 2>() : choice<TT, KIND, 4, 4>();
 }
-template <int TT, bool QX>
+template <int TT, Tokens KIND>
 Choice kernel_of(int wsteps, int steps) {
-    return wsteps == 1 ? kernel_of<TT, QX, 1>(steps) : wsteps == 2 ? kernel_of<TT, QX, 2>(steps) : kernel_of<TT, QX, 4>(steps);
+    return wsteps == 1 ? kernel_of<TT, KIND, 1>(steps) : wsteps == 2 ? kernel_of<TT, KIND, 2>(steps) : kernel_of<TT, KIND, 4>(steps);
 }
 template <int TT>
-Choice kernel_of(bool qx, int wsteps, int steps) {
-    return qx ? kernel_of<TT, true>(wsteps, steps) : kernel_of<TT, false>(wsteps, steps);
+Choice kernel_of(Tokens kind, int wsteps, int steps) {
+    return kind == kBf16 ? kernel_of<TT, kBf16>(wsteps, steps) : kind == kFp8 ? kernel_of<TT, kFp8>(wsteps, steps) : kernel_of<TT, kFp8Pow2>(wsteps, steps);
 }
 // The kernel of a token tile and of the groups' sizes in steps of 32; steps <= wsteps.
-Choice kernel_of(int tt, bool qx, int wsteps, int steps) {
-    return tt == 1 ? kernel_of<1>(qx, wsteps, steps) : tt == 2 ? kernel_of<2>(qx, wsteps, steps) : kernel_of<4>(qx, wsteps, steps);
+Choice kernel_of(int tt, Tokens kind, int wsteps, int steps) {
+    return tt == 1 ? kernel_of<1>(kind, wsteps, steps) : tt == 2 ? kernel_of<2>(kind, wsteps, steps) : kernel_of<4>(kind, wsteps, steps);
 }
 
 // The kernel that stages the tokens for it (TT >= 2).
-template <int TT, bool QX>
+template <int TT, Tokens KIND>
 Kernel tokens_kernel_of(int steps) {
-    return steps == 1 ? qweight_tokens_kernel<TT, QX, 1> : steps == 2 ? qweight_tokens_kernel<TT, QX, 2> : qweight_tokens_kernel<TT, QX, 4>;
+    return steps == 1 ? qweight_tokens_kernel<TT, KIND, 1> : steps == 2 ? qweight_tokens_kernel<TT, KIND, 2> : qweight_tokens_kernel<TT, KIND, 4>;
 }
-Kernel tokens_kernel_of(int tt, bool qx, int steps) {
-    if (tt == 2) return qx ? tokens_kernel_of<2, true>(steps) : tokens_kernel_of<2, false>(steps);
-    return qx ? tokens_kernel_of<4, true>(steps) : tokens_kernel_of<4, false>(steps);
+template <int TT>
+Kernel tokens_kernel_of(Tokens kind, int steps) {
+    return kind == kBf16 ? tokens_kernel_of<TT, kBf16>(steps) : kind == kFp8 ? tokens_kernel_of<TT, kFp8>(steps) : tokens_kernel_of<TT, kFp8Pow2>(steps);
+}
+Kernel tokens_kernel_of(int tt, Tokens kind, int steps) {
+    return tt == 2 ? tokens_kernel_of<2>(kind, steps) : tokens_kernel_of<4>(kind, steps);
 }
 
 void cluster_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int cluster, size_t smem) {
@@ -1118,7 +1128,8 @@ cudaError_t launch_tiles(QweightParams& p, const QweightDevice& dev, int tt, int
     p.run = cut.run;
     p.cluster = p.R * p.splits;
     const int steps = 1 << (shift - 5);
-    const Choice k = kernel_of(tt, qx, wsteps, steps);
+    const Tokens kind = !p.qx ? kBf16 : p.xpow2 ? kFp8Pow2 : kFp8;
+    const Choice k = kernel_of(tt, kind, wsteps, steps);
     size_t smem = k.smem;
     if (!own) {
         // K tile: at most `units` units of 8 k a thread, and as long as the tokens fit what the rest
@@ -1146,7 +1157,7 @@ cudaError_t launch_tiles(QweightParams& p, const QweightDevice& dev, int tt, int
     if (own) {
         cluster_config(cfg, attr, 1, 0);
         cfg.gridDim = dim3((unsigned)(p.R * p.tiles_m * (p.kp >> 8)));
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, tokens_kernel_of(tt, qx, steps), p);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, tokens_kernel_of(tt, kind, steps), p);
         if (e != cudaSuccess) return e;
     }
     cluster_config(cfg, attr, p.cluster, smem);
@@ -1159,11 +1170,11 @@ cudaError_t launch_tiles(QweightParams& p, const QweightDevice& dev, int tt, int
 cudaError_t qweight_prepare(QweightDevice& dev) {
     cudaError_t e = cudaSuccess;
     for (int tt = 1; tt <= 4; tt *= 2)
-        for (int qx = 0; qx < 2; ++qx)
+        for (Tokens kind : {kBf16, kFp8, kFp8Pow2})
             for (int wsteps = 1; wsteps <= 4; wsteps *= 2)
                 for (int steps = 1; steps <= wsteps; steps *= 2)
                     if (e == cudaSuccess)
-                        e = cudaFuncSetAttribute(kernel_of(tt, qx != 0, wsteps, steps).kernel,
+                        e = cudaFuncSetAttribute(kernel_of(tt, kind, wsteps, steps).kernel,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     // clusters of each size that are resident at once, at the largest shared memory a launch takes
     for (int c = 1; c <= kMaxRanks && e == cudaSuccess; ++c) {
@@ -1172,7 +1183,7 @@ cudaError_t qweight_prepare(QweightDevice& dev) {
         cluster_config(cfg, attr, c, kMaxSmem);
         cfg.gridDim = dim3((unsigned)c);
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&dev.clusters[c], kernel_of(2, true, 1, 1).kernel, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&dev.clusters[c], kernel_of(2, kFp8, 1, 1).kernel, &cfg);
         if (e == cudaSuccess && dev.clusters[c] < 1) dev.clusters[c] = 1;
     }
     return e;
