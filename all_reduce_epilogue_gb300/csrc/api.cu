@@ -426,6 +426,8 @@ are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K) {
             return ARE_OK;
         case ARE_OP_GEMM_AR_QWEIGHT:
             if (K < 0 || K > (1 << 20) || K % 32 || N % 8) return ARE_EINVAL;
+            // the kernels count tokens and rows, up to whole tiles of them (at most 24 groups of 16 rows), in 32 bits
+            if (M > kLim - 512 || N > kLim - 512) return ARE_EINVAL;
             // CTAs of 16 rows x 8 tokens, the smallest tiles, count below 2^31
             if (ceil_div(M, 8) * ceil_div(N, 16) >= kLim / kMaxRanks) return ARE_EINVAL;
             return ARE_OK;

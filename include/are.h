@@ -229,7 +229,7 @@ ARE_API const char* are_status_string(are_status s);
  *  ALLREDUCE_RMSNORM: 1 <= R <= 8; N % 8 == 0 (16-byte packs); N <= 32768.
  *  ALLREDUCE_RMSNORM_BACKWARD: as ALLREDUCE_RMSNORM, with N <= 16384.
  *  GEMM_AR_QWEIGHT: 1 <= R <= 8; K % 32 == 0 (16-byte rows of codes) and
- *           K <= 2^20; N % 8 == 0; ceil(M / 8) * ceil(N / 16) < 2^28.
+ *           K <= 2^20; N % 8 == 0; M, N <= 2^31 - 512; ceil(M / 8) * ceil(N / 16) < 2^28.
  * K is ignored for the two ALLREDUCE_RMSNORM operations.  Pure host function: no device needed. */
 ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
 
