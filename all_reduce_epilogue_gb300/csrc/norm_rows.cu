@@ -424,13 +424,14 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
     const int t = threadIdx.x, lane = t & 31, w = t >> 5, nwarps = p.nt >> 5;
     const int P = p.N >> 3;
     const size_t step = (size_t)p.nt * 16;
-    // a thread reads only the gamma words that it writes here: no barrier
+    // a thread reads only the gamma words that it writes here: no barrier.  (Not by non-coherent loads: the kernel before
+    // may have been writing gamma when this one started, before grid_wait.)
 #pragma unroll
     for (int k = 0; k < PPT; ++k) {
         const int pk = t + k * p.nt;
         if (pk < P) {
-            reinterpret_cast<float4*>(g.gamma)[pk * 2] = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2);
-            reinterpret_cast<float4*>(g.gamma)[pk * 2 + 1] = __ldg(reinterpret_cast<const float4*>(p.gamma) + pk * 2 + 1);
+            reinterpret_cast<float4*>(g.gamma)[pk * 2] = reinterpret_cast<const float4*>(p.gamma)[pk * 2];
+            reinterpret_cast<float4*>(g.gamma)[pk * 2 + 1] = reinterpret_cast<const float4*>(p.gamma)[pk * 2 + 1];
         }
     }
     Pack dg[PPT];

@@ -119,6 +119,9 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// (No load here is a non-coherent one: the kernel may start while the one before it in the stream still writes what it
+// reads after grid_wait, and such loads want memory that nothing writes in the kernel's lifetime.)
+//
 // Loads under a predicate: a register keeps its value where it is false, and no
 // branch stands between one load and the next (a branch each had every load
 // wait for the one before: 12 thousand cycles for 24 of them).
@@ -134,7 +137,7 @@ __device__ __forceinline__ void ldg_if(uint2& v, const void* p, bool on) {
                  : "l"(p), "r"((uint32_t)on));
 }
 __device__ __forceinline__ void ldg_u16_if(uint32_t& v, const void* p, bool on) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u16 %0, [%1];\n\t}"
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.u16 %0, [%1];\n\t}"
                  : "+r"(v)
                  : "l"(p), "r"((uint32_t)on));
 }
@@ -566,9 +569,9 @@ __device__ __forceinline__ void combine(const QweightParams& p, int q, int m0, i
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const int64_t at = (int64_t)(n + i) * p.groups + (k >> p.group_shift);
-                            const uint32_t byte = __ldg(p.codes[rj] + (((int64_t)(n + i) * p.K + k) >> 1));
-                            const int u = (int)(k & 1 ? byte >> 4 : byte & 15u), z = p.zero[rj] ? __ldg(p.zero[rj] + at) : 8;
-                            const float w = (float)(u - z) * __uint_as_float((uint32_t)__ldg(p.scale[rj] + at) << 16);
+                            const uint32_t byte = p.codes[rj][((int64_t)(n + i) * p.K + k) >> 1];
+                            const int u = (int)(k & 1 ? byte >> 4 : byte & 15u), z = p.zero[rj] ? p.zero[rj][at] : 8;
+                            const float w = (float)(u - z) * __uint_as_float((uint32_t)p.scale[rj][at] << 16);
                             (i ? s.y : s.x) += xv * w;
                         }
                     }

@@ -1,4 +1,7 @@
-"""Limits of the 4-bit linear that a GPU is not needed for."""
+"""Limits of the quantised and backward operations that a GPU is not needed for."""
+import os
+import re
+
 import pytest
 
 import all_reduce_epilogue_gb300 as are
@@ -22,3 +25,13 @@ def lib():
 def test_sizes_next_to_31_bits(lib, M, N, ok):
     for R in (1, 8):
         assert (lib.are_supports(are.OP_GEMM_AR_QWEIGHT, R, M, N, 32) == are.OK) == ok
+
+
+@pytest.mark.parametrize("source", ["norm_rows.cu", "qweight.cu"])
+def test_no_non_coherent_loads_under_programmatic_launch(source):
+    """These kernels may start before the kernel that writes their operands has ended; a non-coherent load wants memory
+    that is read-only for the whole life of the kernel, which begins before the wait."""
+    path = os.path.join(os.path.dirname(are.__file__), "csrc", source)
+    code = re.sub(r"//[^\n]*", "", open(path).read())
+    assert "ProgrammaticStreamSerialization" in code
+    assert not re.findall(r"__ldg\b|ld\.global(?:\.\w+)*\.nc\b|__restrict__", code)
