@@ -554,7 +554,10 @@ typedef struct are_qweight {
  * 32 tokens, by the size of the problem, each of which reads the weights, from
  * memory once for those that run together.  For tiles of 16 and 32 the tokens
  * are first laid out in a buffer of the workspace, in several parts if it does
- * not hold them.  ARE_DEBUG_QWEIGHT_FEW / ARE_DEBUG_QWEIGHT_STAGED force the
+ * not hold them.  The tile and the parts of K, and with them the order of the
+ * fp32 sums, go by the sizes, the device and that buffer (2 MiB times R_max):
+ * workspaces of the same R_max give the same bits, others may differ in them
+ * above 8 tokens, within the arithmetic above.  ARE_DEBUG_QWEIGHT_FEW / ARE_DEBUG_QWEIGHT_STAGED force the
  * tile.  Needs no capacity of the workspace but R <= R_max.
  */
 ARE_API are_status are_gemm_ar_qweight(const are_bf16* const x[], const are_qweight w[], int group,
