@@ -37,6 +37,8 @@ struct are_ws {
     size_t piece_words = 0;
     uint32_t* d_staging = nullptr;
     size_t staging_words = 0;
+    bool rows_ready = false;          // the row kernels' first call has prepared them
+    bool qweight_ready = false;       // the same of the 4-bit kernels
     QweightDevice qweight{};          // resident clusters of the 4-bit kernel
     uint8_t* d_tokens = nullptr;      // staged tokens of the 4-bit kernel
     float* d_dgamma = nullptr;        // backward: the blocks' partial dgamma sums
@@ -488,8 +490,6 @@ are_status are_workspace_create(are_ws** out, const are_caps* caps) {
     }
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_tokens, caps->R_max * kQweightScratch);
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_dgamma, norm_backward_scratch_words(caps->N_max, ws->num_sms) * 4);
-    if (e == cudaSuccess) e = rows_prepare();
-    if (e == cudaSuccess) e = qweight_prepare(ws->qweight);
     if (e != cudaSuccess) {
         are_status st = from_cuda(e);
         free_ws(ws);
@@ -742,6 +742,22 @@ bool aligned_to(const void* p, uintptr_t bytes) { return p != nullptr && reinter
 
 int log2_group(int group) { return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : -1; }
 
+// Opts the kernels in to their shared memory, at a workspace's first call of them (a stream capture allows it: no work is
+// enqueued and nothing waited for): who never calls them pays neither for that nor for loading them.
+cudaError_t prepare_rows(are_ws* ws) {
+    if (ws->rows_ready) return cudaSuccess;
+    const cudaError_t e = rows_prepare();
+    ws->rows_ready = e == cudaSuccess;
+    return e;
+}
+
+cudaError_t prepare_qweight(are_ws* ws) {
+    if (ws->qweight_ready) return cudaSuccess;
+    const cudaError_t e = qweight_prepare(ws->qweight);
+    ws->qweight_ready = e == cudaSuccess;
+    return e;
+}
+
 bool scale_format_ok(int f) { return f == ARE_SCALE_F32 || f == ARE_SCALE_E8M0; }
 
 // A scale tensor has no alignment but its element's.
@@ -797,6 +813,8 @@ are_status qweight_call(const void* const x[], const void* const xscale[], int s
         }
         return ARE_OK;
     }
+    cudaError_t e = prepare_qweight(ws);
+    if (e != cudaSuccess) return from_cuda(e);
     for (int r = 0; r < R; ++r) {
         p.x[r] = x[r];
         p.xscale[r] = qx ? xscale[r] : nullptr;
@@ -823,8 +841,7 @@ are_status qweight_call(const void* const x[], const void* const xscale[], int s
                    : !(ws->debug_flags & ARE_DEBUG_QWEIGHT_STAGED)                                            ? 0
                    : ws->debug_arg == 16 || ws->debug_arg == 32                                               ? (int)ws->debug_arg
                                                                                                               : -1;
-    const cudaError_t e = launch_qweight(p, ws->qweight, ws->d_tokens, ws->caps.R_max * kQweightScratch, &grid, &variant,
-                                         &cluster, s);
+    e = launch_qweight(p, ws->qweight, ws->d_tokens, ws->caps.R_max * kQweightScratch, &grid, &variant, &cluster, s);
     ws->last = are_launch_info{ARE_KERNEL_QWEIGHT, grid, 256, cluster, 0, variant, 0, 0};
     return from_cuda(e);
 }
@@ -853,6 +870,8 @@ are_status are_allreduce_rmsnorm_quant_groups(const are_bf16* const partials[], 
     if (R > ws->caps.R_max) return ARE_ECAPACITY;
     ws->last = are_launch_info{};
     if (M == 0 || N == 0) return ARE_OK;
+    const cudaError_t e = prepare_rows(ws);
+    if (e != cudaSuccess) return from_cuda(e);
 
     RowsParams p;
     rows_common(p, ws, partials, gamma, eps, R, M, N);
@@ -895,6 +914,9 @@ are_status are_allreduce_rmsnorm_backward(const are_bf16* const dy[], const are_
         ws->last.kernel = ARE_KERNEL_MEMSET;
         return from_cuda(cudaMemsetAsync(dgamma, 0, (size_t)N * 4, s));
     }
+
+    const cudaError_t e = prepare_rows(ws);
+    if (e != cudaSuccess) return from_cuda(e);
 
     RowsParams p;
     rows_common(p, ws, dy, gamma, eps, R, M, N);

@@ -672,10 +672,11 @@ cudaError_t launch_norm_backward_rows(RowsParams& p, const RowsPlan& plan, float
 }
 
 size_t norm_backward_scratch_words(int64_t n_max, int num_sms) {
-    // rows of N from an SM's blocks.  rows_plan fits kRowsThreads / (nt + 32) of them: with a pack a thread, N <= 8 nt,
-    // less than 8 * kRowsThreads columns; with two, N > 2048 and nt >= 160, three blocks at most and less than twice that
+    // rows of N from an SM's blocks.  rows_plan fits kRowsThreads / (nt + 32) of them, ten at most: with a pack a thread,
+    // N <= 8 nt, less than 8 * kRowsThreads columns; with two, N > 2048 and nt >= 160, three blocks at most and less than
+    // twice that
     const int64_t n = n_max < kBackwardMaxN ? n_max : kBackwardMaxN, most = 8 * kRowsThreads;
-    return (size_t)std::max(std::max(2 * n, std::min(3 * n, 2 * most)), most) * num_sms;
+    return (size_t)std::max(std::max(2 * n, std::min(3 * n, 2 * most)), std::min(kRowsThreads / 64 * n, most)) * num_sms;
 }
 
 }  // namespace are
