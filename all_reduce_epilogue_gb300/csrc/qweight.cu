@@ -223,12 +223,13 @@ __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&a0)[4], uint32_t (
 }
 
 // A token's power of two, 2^(141 - top) with `top` the biased exponent of its
-// largest value (at most 2^127; 1 for zeros), and what undoes it.
+// largest value (at most 2^127, which is enough for subnormal ones; `top` is 0
+// for them and for zeros), and what undoes it.
 __device__ __forceinline__ float scale_of(uint32_t top) {
-    return top == 0u ? 1.f : __uint_as_float(min(268u - top, 254u) << 23);
+    return __uint_as_float(min(268u - top, 254u) << 23);
 }
 __device__ __forceinline__ float unscale_of(uint32_t top) {
-    return top == 0u ? 1.f : top < 15u ? __uint_as_float(0x00400000u) : __uint_as_float((top - 14u) << 23);
+    return top < 15u ? __uint_as_float(0x00400000u) : __uint_as_float((top - 14u) << 23);
 }
 
 // Tokens m0 .. m0 + toks of rank r, k from t0 to kend, as a tile of `tile_k` k in the order of the tensor

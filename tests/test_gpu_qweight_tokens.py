@@ -108,3 +108,24 @@ def test_small_fp32_scales(tiled, xgroup):  # noqa: F811
     out = product(ws, xq, xs, w, group, xgroup)
     want, tol = ref.linear64([value(q, s, xgroup) for q, s in zip(xq, xs)], w, group)
     ref.check(out, want, tol + R * max(G, -(-K // group)) * 2.0 ** -130 + 2.0 ** -134, "out")
+
+
+@pytest.mark.parametrize("M", [2, 40])
+def test_bf16_tokens_below_the_normal_ones(tiled, M):  # noqa: F811
+    """Tokens that are all subnormal, under weights large enough for normal outputs; and subnormal beside normal ones."""
+    ws, _ = tiled
+    R, N, K, group = 2, 72, 544, 64
+    w, g = weights(R, N, K, group, True, 350 + M)
+    for _, s, _ in w:
+        s.mul_(2.0 ** 30)
+    x = []
+    for _ in range(R):
+        bits = torch.randint(1, 128, (M, K), generator=g, device="cuda", dtype=torch.int16)
+        x.append(torch.where(torch.rand((M, K), generator=g, device="cuda") < 0.5, bits, bits - 32768).view(torch.bfloat16))
+    x[0][1, 300:] = (torch.randn(K - 300, generator=g, device="cuda") * 2.0 ** -120).to(torch.bfloat16)
+    x[1][0, :256] = 0
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    are.gemm_ar_qweight(x, [are.QWeight(*t, group) for t in w], out, ws)
+    assert ws.device_status()["code"] == 0
+    want, tol = ref.linear64(x, w, group)
+    ref.check(out, want, tol - 1e-38, "out")
