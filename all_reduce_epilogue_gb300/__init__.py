@@ -598,22 +598,36 @@ class QWeight:
     ``codes``: uint8 [N, K / 2], byte i of a row holds k = 2i in its lower and
     2i + 1 in its upper four bits; ``scale``: bf16 [N, ceil(K / group)];
     ``zero``: uint8 of the same shape, values 0..15, or None (8 everywhere);
-    ``group``: 32, 64 or 128."""
+    ``group``: 32, 64 or 128.  The tensors are checked here, once; it holds
+    tensors of its own over the same memory, none of which can be replaced, so
+    what a call uses is what was checked.  Their contents may change, and a
+    tensor given another memory (``t.data = ...``) needs another QWeight."""
 
     __slots__ = ("codes", "scale", "zero", "group", "N", "K", "_key")
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"QWeight.{name} cannot be replaced: make another QWeight")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"QWeight.{name} cannot be removed")
 
     def __init__(self, codes, scale, zero=None, group: int = 128):
         import torch
         dev = codes.get_device()
         N, half = _matrix(codes, "codes")
-        self.N, self.K, self.group = N, 2 * half, _group_of(group, "group")
+        K = 2 * half
         _need(codes, torch.uint8, (N, half), dev, "codes")
-        groups = (N, -(-self.K // group))
+        groups = (N, -(-K // _group_of(group, "group")))
         _need(scale, torch.bfloat16, groups, dev, "scale")
         if zero is not None:
             _need(zero, torch.uint8, groups, dev, "zero")
-        self.codes, self.scale, self.zero = codes, scale, zero
-        self._key = (N, self.K, group, dev)
+        own = dict(codes=codes.detach(), scale=scale.detach(), zero=None if zero is None else zero.detach(), group=group,
+                   N=N, K=K, _key=(N, K, group, dev))
+        for name, value in own.items():
+            object.__setattr__(self, name, value)
+
+    def __reduce__(self):  # copies and pickles are checked again
+        return QWeight, (self.codes, self.scale, self.zero, self.group)
 
 
 def _qweights(w: Sequence, R: int, M: int, K: int, out, dev: int):

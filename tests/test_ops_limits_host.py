@@ -1,5 +1,7 @@
 """Limits of the quantised and backward operations that a GPU is not needed for."""
+import copy
 import os
+import pickle
 import re
 
 import pytest
@@ -35,3 +37,25 @@ def test_no_non_coherent_loads_under_programmatic_launch(source):
     code = re.sub(r"//[^\n]*", "", open(path).read())
     assert "ProgrammaticStreamSerialization" in code
     assert not re.findall(r"__ldg\b|ld\.global(?:\.\w+)*\.nc\b|__restrict__", code)
+
+
+def test_qweight_holds_what_it_checked():
+    """A tensor put in place of a checked one would reach the kernel unchecked: another shape, type or device."""
+    import torch
+    codes, scale = torch.zeros((16, 64), dtype=torch.uint8), torch.ones((16, 1), dtype=torch.bfloat16)
+    w = are.QWeight(codes, scale)
+    for name, value in (("codes", codes[:8]), ("scale", scale.float()), ("zero", codes), ("group", 32), ("N", 32), ("K", 256),
+                        ("_key", None), ("other", 1)):
+        with pytest.raises(AttributeError):
+            setattr(w, name, value)
+    with pytest.raises(AttributeError):
+        del w.codes
+    assert w.codes.data_ptr() == codes.data_ptr() and w.zero is None and (w.N, w.K, w.group) == (16, 128, 128)
+    # a tensor that changes its memory or shape afterwards takes nothing from under it
+    at = codes.data_ptr()
+    scale.data = torch.ones((2, 1), dtype=torch.bfloat16)
+    codes.fill_(7)
+    codes.data = torch.zeros((4, 4), dtype=torch.uint8)
+    assert w.codes.shape == (16, 64) and w.codes.data_ptr() == at and (w.codes == 7).all() and w.scale.shape == (16, 1)
+    for v in (copy.copy(w), copy.deepcopy(w), pickle.loads(pickle.dumps(w))):
+        assert torch.equal(v.codes, w.codes) and torch.equal(v.scale, w.scale) and (v.N, v.K, v.group) == (16, 128, 128)
