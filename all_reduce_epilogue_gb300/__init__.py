@@ -640,8 +640,13 @@ def _qweights(w: Sequence, R: int, M: int, K: int, out, dev: int):
         raise ValueError(f"every rank's weights must be [{N}, {K}] in groups of {group} on CUDA device {dev}")
     if w[0].zero is not None and all([q.zero is not None for q in w]):
         weights = _addresses([t for q in w for t in (q.codes, q.scale, q.zero)])
+        missing = 0 in weights
     else:
-        weights = array("Q", [v or 0 for q in w for v in (q.codes.data_ptr(), q.scale.data_ptr(), _address(q.zero))])
+        found = [_address(t) for q in w for t in (q.codes, q.scale, q.zero)]
+        weights = array("Q", [v or 0 for v in found])  # no zero points: a null pointer
+        missing = 0 in found
+    if missing and N and K:
+        raise ValueError("weights whose memory has been given back (a storage resized to nothing)")
     if isinstance(out, (list, tuple)):
         if len(out) != R:
             raise ValueError(f"{R} ranks, {len(out)} output views")

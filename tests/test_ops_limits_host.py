@@ -59,3 +59,27 @@ def test_qweight_holds_what_it_checked():
     assert w.codes.shape == (16, 64) and w.codes.data_ptr() == at and (w.codes == 7).all() and w.scale.shape == (16, 1)
     for v in (copy.copy(w), copy.deepcopy(w), pickle.loads(pickle.dumps(w))):
         assert torch.equal(v.codes, w.codes) and torch.equal(v.scale, w.scale) and (v.N, v.K, v.group) == (16, 128, 128)
+
+
+@pytest.mark.parametrize("which", ["codes", "scale", "zero"])
+@pytest.mark.parametrize("both", [False, True])
+def test_weights_without_memory_are_refused(which, both):
+    """A storage resized to nothing has the address 0, which for zero points would mean that there are none."""
+    import torch
+
+    def make():
+        t = dict(codes=torch.zeros((16, 64), dtype=torch.uint8), scale=torch.ones((16, 1), dtype=torch.bfloat16),
+                 zero=torch.zeros((16, 1), dtype=torch.uint8))
+        return are.QWeight(**t), t
+
+    (a, _), (b, t) = make(), make()
+    if not both:
+        a = are.QWeight(a.codes, a.scale)
+    out = torch.zeros((2, 16), dtype=torch.bfloat16)
+    are._qweights([a, b], 2, 2, 128, out, -1)
+    t[which].untyped_storage().resize_(0)
+    with pytest.raises(ValueError):
+        are._qweights([a, b], 2, 2, 128, out, -1)
+    empty = are.QWeight(torch.empty((16, 0), dtype=torch.uint8), torch.empty((16, 0), dtype=torch.bfloat16),
+                        torch.empty((16, 0), dtype=torch.uint8))
+    are._qweights([empty], 1, 2, 0, out, -1)
