@@ -32,8 +32,10 @@
 // Measured (a copy moves 6.78 TB/s): forward, R = 8, 4096 x 7168: 99 us,
 // 6.2 TB/s; backward, R = 8, 4096 x 7168: 97 us, 6.7 TB/s; R = 1, 16384 x 4096:
 // 90 us, 6.0 TB/s.  One row of 7168 at R = 8: 3.9 us, all latency.  Narrow rows
-// are bound by issue: R = 1, 16384 x 2048 backward 57 us, 4.7 TB/s, issue slots
-// 58 % used; so their arithmetic is in pairs of columns, and an SM takes as many
+// are below both rates (R = 1, 16384 x 2048 backward 57 us, 4.7 TB/s, issue
+// slots 58 % used): what each row costs besides its bytes, a barrier of the
+// block, two sums over its warps and a turn of the ring, is for one or two packs
+// a thread.  So their arithmetic is in pairs of columns, and an SM takes as many
 // blocks as its registers hold (16384 x 1024: 34 us; two blocks 43).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -252,7 +254,9 @@ __device__ __forceinline__ float max_abs(float a, float b) {
 }
 
 // n / d from an approximate reciprocal of d, corrected once by the remainder (Markstein 1990: the quotient's
-// remainder is exact in an fma): correctly rounded but for the last bit's rare ties.  No over- or underflow on the way.
+// remainder is exact in an fma).  The reciprocal is off by 2^-23 of its value at most and n * rcp by less than 2^-22, so
+// the corrected quotient before its rounding is off by less than 2^-44: correctly rounded unless n / d is within that of
+// a tie.  No over- or underflow on the way.
 __device__ __forceinline__ float quotient(float n, float d, float rcp) {
     const float q = n * rcp;
     return fmaf(fmaf(-d, q, n), rcp, q);

@@ -37,7 +37,7 @@
 //    and the (group, K) items of a CTA are dealt to its warps in equal contiguous
 //    runs of 16-row groups.  R = 8, one token, 7168 x 2048: 17 us, 3.7 TB/s of
 //    codes; issue slots are 51 % used (about 70 % in the loop over the codes,
-//    which is 60 % of the time), DRAM 38 %.
+//    which is 60 % of the time), DRAM 37 %; the rest is start and cluster sum.
 //  * In tiles of 16 or 32 (qweight_tokens_kernel, then qweight_wide_kernel), they
 //    are staged once, in global memory, and come in tiles of K by bulk copies; a warp
 //    owns 32 rows, which share the tokens' operands, and their sums stay in
