@@ -143,7 +143,7 @@ struct QweightParams {
     unsigned long long timeout_ns;
     // set by launch_qweight:
     int kp;                              // K, up to whole 256
-    uint8_t* tokens;                     // staged tokens [R][tiles_m][kp / 32][tile]: fp16 operands
+    uint8_t* tokens;                     // staged tokens [R][tiles_m][kp / 32][tile]: bf16 operands
     float* sums;                         // their sums [R][tiles_m][kp / shared group][tile]
     float* scales;                       // their scales [R][tiles_m][kp / 256 or xgroup][tile]
     uint32_t* flags;                     // [R][tiles_m][kp / 256]: tokens with a value that is not finite

@@ -7,20 +7,28 @@
 // Bound by the weights' bytes: M tokens use each of them M times.  What
 // competes with the bytes is the integer work of unpacking the codes, so that
 // is made as small as it gets:
-//  * A code in bits 0..3 of an fp16 is the subnormal u * 2^-24, in bits 4..7
-//    u * 2^-20, exactly.  So a word of 8 codes becomes four operand registers
-//    of m16n8k16 tensor instructions (16 rows of weights, 16 of k, 8 tokens,
-//    fp32 sums) by four masks and a shift: the pairs (0, 4) (1, 5) (2, 6)
-//    (3, 7).  The tokens are staged in that order, the odd k times 2^-4.
-//    (Codes made into integers in fp16 take 9 instructions a word and in bf16
-//    11; FP8 operands would take 3, but FP8 mma.sync is not native here: it
-//    measured 36 cycles a sub-core for 32 of k, fp16 8.2 for 16.)
-//  * FP8 tokens are exact in fp16.  bf16 tokens, and FP8 ones times their
-//    power-of-two scales, are scaled, per token and 256 of k, by the power of
-//    two that takes the largest value to 2^14..2^15, which their scale in fp32
-//    undoes: what is 2^-27 (FP8: 2^-31) times the largest or more stays exact,
-//    what is smaller is off by at most 2^-35 of it, below the fp32 sums' own
-//    rounding.
+//  * A code in bits 0..3 of a bf16 is the subnormal u * 2^-133; in bits 4..7 it is
+//    u * 2^-129, as the first binade of normal numbers goes on in the same steps.
+//    So a word of 8 codes becomes four operand registers of m16n8k16 tensor
+//    instructions (16 rows of weights, 16 of k, 8 tokens, fp32 sums) by four
+//    masks and a shift: the pairs (0, 4) (1, 5) (2, 6) (3, 7).  The tokens are
+//    staged in that order, scaled up to match, the odd k by 2^-4 less.
+//    (Codes made into normal numbers take 7 to 11 instructions a word.  FP8
+//    operands would take 3, but FP8 mma.sync is not native here: it measured 36
+//    cycles a sub-core for 32 of k, 16-bit ones 8.2 for 16.)
+//  * Such an instruction adds its 16 products and the sum so far to 25 bits below
+//    the largest of their exponents, and counts a subnormal's as 2^-126: 7 bits
+//    above u = 1.  What it cuts of each is up to 2^-18 of the largest token whose
+//    code is not zero (in units of the code), 17 times 2^-18 in all.  In fp16, with
+//    3 bits of mantissa more to be subnormal in, that was 2^-15; normal numbers
+//    (from E4M3, which reads a code byte as u * 2^-9) have 2^-25 of u times the
+//    token, and measured 6 to 11 % slower (one token 18.5 us for 16.6, 64 75.5 for
+//    70.9; all codes in bits 4..7, 2^-22: 17.8 and 76).  The output's rounding to
+//    bf16 is 2^-9 of what is left after the ranks and groups have been added up.
+//  * The tokens enter exactly: bf16 as they are, FP8 codes times 2^7 or times their
+//    power-of-two scales, scaled per token and 256 of k by the power of two that
+//    takes the largest value to 2^14..2^15, which their scale in fp32 undoes, and
+//    all by 2^109.  What is 2^-112 of the largest or less may lose bits.
 //  * The zero point leaves the sums: sum (u - z) x = sum u x - z sum x, with
 //    sum x per token and group in fp32.  The scales are applied in fp32, once
 //    per group, to the tensor instruction's fp32 sums.  No weight is rounded.
@@ -188,22 +196,22 @@ template <bool FIRST>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
     if (FIRST)
         asm(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%10, %10, %10, %10};"
             : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
     else
         asm(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%0, %1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two floats of tokens as fp16.
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
+// Two floats of tokens as bf16.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
 }
 __device__ __forceinline__ float2 fp8x2_to_float2(uint32_t v) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
@@ -212,7 +220,7 @@ __device__ __forceinline__ float2 fp8x2_to_float2(uint32_t v) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// A word's codes: pairs (0, 4) and (2, 6) times 2^-24, (1, 5) and (3, 7) times 2^-20.
+// A word's codes: pairs (0, 4) and (2, 6) times 2^-133, (1, 5) and (3, 7) times 2^-129.
 template <int HALF>
 __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&a0)[4], uint32_t (&a1)[4]) {
     a0[HALF] = w & 0x000F000Fu;
@@ -236,7 +244,7 @@ __device__ __forceinline__ float unscale_of(uint32_t top) {
 // instruction's operands, with their sums and scales; tokens up to `rows` are written, those that do
 // not exist as zeros.  A warp takes a token's 256 k at a time, a unit of 8 k a lane; its (at most UNITS)
 // loads are in flight together with those of `between`.
-//   xs   : [k / 32][TT][lane] units of 8 k in fp16
+//   xs   : [k / 32][TT][lane] units of 8 k in bf16
 //   xsum : [k / GRAIN][TOK] sum x * 2^-24
 //   xsc  : [k / 256, or k / xgroup with kFp8][TOK] the tokens' scales
 //   bad  : bit m: token m has a value that is not finite
@@ -293,13 +301,13 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
                     x[e][4 + i4] = f[i4].y;
                 }
             }
-            if constexpr (KIND == kFp8) {  // as far up as fp16 goes (448 * 2^7)
+            if constexpr (KIND == kFp8) {  // for the sums' unit
 #pragma unroll
                 for (int i8 = 0; i8 < 8; ++i8) x[e][i8] *= 128.f;
             } else if constexpr (KIND == kFp8Pow2) {
                 // The largest value goes to 2^14..2^15, as for bf16, whatever scales the codes of zero are under.
                 // `largest`: of the lanes' scale bytes plus biased exponents; within what keeps the factor that undoes it,
-                // 2^(largest - 268) * 2^12, a normal number (2^129 and more, which fp32 does not hold, may leave fp16)
+                // 2^(largest - 268) * 2^12, a normal number (2^129 and more, which fp32 does not hold, may leave bf16)
                 float a = 0.f;
 #pragma unroll
                 for (int i8 = 0; i8 < 8; ++i8) a = fmaxf(a, fabsf(x[e][i8]));
@@ -355,8 +363,8 @@ __device__ __forceinline__ void stage_tokens(const QweightParams& p, int r, int 
             const float(&y)[8] = x[e];
             if (in[e])
                 *reinterpret_cast<uint4*>(xs + (((st * TT + (m[e] >> 3)) * 8 + (m[e] & 7)) * 4 + c4) * 16) =
-                    make_uint4(f16x2(y[0], y[2]), f16x2(y[4] * 0.0625f, y[6] * 0.0625f), f16x2(y[1], y[3]),
-                               f16x2(y[5] * 0.0625f, y[7] * 0.0625f));
+                    make_uint4(bf16x2(y[0] * 0x1p109f, y[2] * 0x1p109f), bf16x2(y[4] * 0x1p105f, y[6] * 0x1p105f),
+                               bf16x2(y[1] * 0x1p109f, y[3] * 0x1p109f), bf16x2(y[5] * 0x1p105f, y[7] * 0x1p105f));
             sum[e] = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
         }
         // sum x over each GRAIN of k, in the weights' unit
@@ -601,8 +609,8 @@ __global__ void __launch_bounds__(kThreads, 2) qweight_few_kernel(const __grid_c
     constexpr int TOK = S::TOK, ROWS = S::ROWS, ITEM = S::ITEM, PITCH = S::PITCH, LD = S::LD;
     constexpr int SLOT = S::SLOT, DEPTH = S::DEPTH, UNITS = S::UNITS;
     constexpr int GRAIN = STEPS * 32;       // k that share both scales
-    // What the sums lack of the codes' 2^24: 2^12 of it is in the staged scales, or 2^7 in the tokens.  So outputs down to
-    // bf16's smallest normal ones keep bits enough in fp32 sums.
+    // What the sums lack of 2^24 (the codes' 2^-133 times the tokens' 2^109): 2^12 of it is in the staged scales, or 2^7 in
+    // the tokens.  So outputs down to bf16's smallest normal ones keep bits enough in fp32 sums.
     constexpr float UNIT = QX ? 0x1p17f : 0x1p12f;
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     const int g = lane >> 2, c = lane & 3;
@@ -1204,7 +1212,7 @@ cudaError_t launch_qweight(QweightParams& p, const QweightDevice& dev, uint8_t* 
     // Rows too long for a staged tile go by 8 tokens.  More than 32 tokens a tile need 200 registers a thread:
     // spilled to 128 they took 139 us at R = 8, M = 64, N = 7168, K = 2048.
     p.kp = (p.K + 255) / 256 * 256;
-    // of a token tile: fp16 tokens, sums and scales of at least 32 k, and a flag word per 256 k
+    // of a token tile: bf16 tokens, sums and scales of at least 32 k, and a flag word per 256 k
     auto tile_bytes = [&](int t) { return (size_t)p.R * p.kp / 32 * (t * 8 * (64 + 4 + 4) + 4); };
     int tt = p.force_tile == 8 || (p.M <= 8 && p.force_tile == 0) || tile_bytes(2) > scratch_bytes ? 1 : 2;
     if (tt == 2 && p.force_tile != 16 && tile_bytes(4) <= scratch_bytes &&

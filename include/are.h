@@ -543,15 +543,15 @@ typedef struct are_qweight {
  *            may alias; identical pointers are written once); must not overlap
  *            the tokens or the weights
  *  Result  : out[v][m][n] = bf16( sum_r sum_k x[r][m][k] * w_r(n, k) ), formed
- *            per group as (sum_k u x - zero * sum_k x) * scale: codes, zero
- *            points and scales enter exactly; the group's sums, their
- *            difference (whose error is relative to sum |u x|), and the sums
- *            over groups and over r = 0..R-1 are in fp32, and the result is
- *            rounded once (a rank's partial is not rounded, as in are_gemm_rs).  Tokens enter the products in fp16,
- *            scaled by a power of two per token and 256 of k: values down to
- *            2^-27 times the largest of the 256 exactly, smaller ones to
- *            2^-35 of it, which is below the fp32 sums' rounding.  A value that
- *            is not finite makes that token's outputs what the products give.
+ *            per group as (sum_k u x - zero * sum_k x) * scale: tokens, codes,
+ *            zero points and scales enter exactly (tokens down to 2^-112 of the
+ *            largest of their 256 k).  sum_k u x comes from tensor instructions
+ *            of 16 k, each of which cuts what it adds at 2^-18 of its largest
+ *            token, 17 times at most; its difference from zero * sum_k x (off
+ *            relative to sum |u x|), and the sums over groups and over
+ *            r = 0..R-1, are in fp32, and the result is rounded once (a rank's
+ *            partial is not rounded, as in are_gemm_rs).  A value that is not
+ *            finite makes that token's outputs what the products give.
  *            A group's scale times the largest token of the 256 k must be finite
  *            in fp32, or outputs may be infinite or NaN where the products alone
  *            are not.
@@ -580,10 +580,8 @@ ARE_API are_status are_gemm_ar_qweight(const are_bf16* const x[], const are_qwei
  *  scale_format: are_scale_format
  *  xgroup      : 32, 64 or 128, independent of `group`
  * The other arguments and the arithmetic are as for are_gemm_ar_qweight.  fp32
- * token scales are applied in fp32 to the sums of each shared group of k; E8M0
- * scales go into the fp16 tokens, scaled by a power of two per token and 256 of
- * k as bf16 tokens are: values down to 2^-31 times the largest of the 256
- * exactly, smaller ones to 2^-35 of it.  (Tokens of 2^128 and more, which fp32
+ * token scales are applied in fp32 to the sums of each shared group of k, E8M0
+ * scales to the tokens, exactly.  (Tokens of 2^128 and more, which fp32
  * does not hold, may count as infinite.)  With fp32 token scales it is a group's
  * scale times that of the token's group that must be finite in fp32.
  */

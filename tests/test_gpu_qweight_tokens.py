@@ -48,24 +48,22 @@ def test_largest_power_of_two_scales(tiled, M):  # noqa: F811
 
 @pytest.mark.parametrize("odd", [0, 1])
 def test_small_values_beside_a_large_one(tiled, odd):  # noqa: F811
-    """One value of 448 * 2^-d, d = 18 to 34, at an even or an odd k, beside one of 448 whose weights are zero.  A token
-    is off by at most 2^-35 of the largest of its 256 k, and exact from 2^-31 of it up."""
+    """One value of 448 * 2^-d, d = 18 to 100, at an even or an odd k, beside one of 448 whose weights are zero: exact."""
     ws, _ = tiled
     N, K, group = 72, 256, 32
     w, _ = weights(1, N, K, group, False, 310)
     w[0][0][:, 0] = 0x88  # k = 0 and 1 weigh nothing
-    d = torch.arange(18, 35, device="cuda")
+    d = torch.cat((torch.arange(18, 36), torch.arange(40, 101, 10))).cuda()
     M = len(d)
     xq = torch.zeros((M, K), dtype=torch.uint8, device="cuda")
     xs = torch.full((M, 8), 127, dtype=torch.uint8, device="cuda")
     xq[:, 0] = 0x7E
-    at = 32 + 2 * torch.arange(M, device="cuda") * 6 + odd  # in groups 1 to 7
+    at = 32 + 2 * torch.arange(M, device="cuda") * 4 + odd  # in groups 1 to 7
     xq[torch.arange(M, device="cuda"), at] = 0x7E
     xs[torch.arange(M, device="cuda"), at // 32] = (127 - d).to(torch.uint8)
     out = product(ws, [xq], [xs], w, group, 32)
     want, tol = ref.linear64([value(xq, xs, 32)], w, group)
-    lost = torch.where(d > 31, 448 * 2.0 ** -35, 0.0).double()[:, None] * 15 * w[0][1].double()[:, at // 32].T
-    ref.check(out, want, tol + lost, "out")
+    ref.check(out, want, tol - 1e-38, "out")
 
 
 @pytest.mark.parametrize("K,xgroup", [(256, 32), (544, 32), (512, 128)])
@@ -88,16 +86,15 @@ def test_groups_of_zeros_beside_small_ones(tiled, K, xgroup):  # noqa: F811
     xq[0][5], xq[1][5] = 0, 0  # and a token of zeros
     out = product(ws, xq, xs, w, group, xgroup)
     want, tol = ref.linear64([value(q, s, xgroup) for q, s in zip(xq, xs)], w, group)
-    lost = 448 * 2.0 ** (byte.double()[:, None] - 127 - 35) * 15 * xgroup * sum(-(-group // xgroup) * t[1].double().sum(1) for t in w)
-    ref.check(out, want, tol + lost, "out")
+    ref.check(out, want, tol, "out")
     assert (out[5] == 0).all()
 
 
 @pytest.mark.parametrize("xgroup", [32, 128])
 def test_small_fp32_scales(tiled, xgroup):  # noqa: F811
     """fp32 token scales from 2^-126 to 2^-90, a magnitude a token; outputs down to bf16's smallest.  The sums are kept
-    2^17 smaller than the output, where a step of fp32 is 2^-149 at least: half a step for a product with scales of
-    up to 7 (2^2.7, the sum it multiplies) and one for the sum, a group: 2^17 * 2^-150 * 8."""
+    2^17 smaller than the output, where a step of fp32 is 2^-149 at least: half a step for a product of scales, times up
+    to 2^2.7 (the sum that it multiplies), and one for the sum, a group: 2^17 * 2^-150 * 8."""
     ws, _ = tiled
     R, M, N, K, group = 2, 37, 72, 544, 128
     w, g = weights(R, N, K, group, True, 330 + xgroup)
@@ -129,3 +126,30 @@ def test_bf16_tokens_below_the_normal_ones(tiled, M):  # noqa: F811
     assert ws.device_status()["code"] == 0
     want, tol = ref.linear64(x, w, group)
     ref.check(out, want, tol - 1e-38, "out")
+
+
+@pytest.mark.parametrize("K,group", [(32, 32), (128, 128)])
+def test_small_tokens_beside_one_that_weighs_nothing(tiled, K, group):  # noqa: F811
+    """A token of 1 under codes equal to their zero points, among ones of 2^-12.  What is cut of 16 products and the sum
+    so far: 2^-18 each in the one instruction that has the large token, and 2^-25 of the sum so far, below 2^4, in those
+    that go on from it.  The zero point's product and the difference are of magnitude 15 * (1 + K * 2^-12): a sum of
+    tokens takes up to 10 additions, the rest 2."""
+    ws, _ = tiled
+    M, N = max(K, 64), 64
+    g = torch.Generator(device="cuda").manual_seed(360 + K)
+    u = torch.randint(1, 16, (N, K), generator=g, device="cuda", dtype=torch.uint8)
+    zero = torch.randint(1, 16, (N, 1), generator=g, device="cuda", dtype=torch.uint8)
+    x = (2.0 ** -12 * (0.5 + 0.5 * torch.rand((M, K), generator=g, device="cuda"))).to(torch.bfloat16)
+    at = torch.arange(M, device="cuda") % K
+    x[torch.arange(M, device="cuda"), at] = 1
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    one = torch.ones((N, 1), dtype=torch.bfloat16, device="cuda")
+    for m in range(0, M, max(1, M // 16)):
+        v = u.clone()
+        v[:, at[m]] = zero[:, 0]
+        codes = (v[:, 0::2] | v[:, 1::2] << 4).contiguous()
+        are.gemm_ar_qweight([x], [are.QWeight(codes, one, zero, group)], out, ws)
+        want = x[m].double() @ (v.double() - zero.double()).T
+        magnitude = 15 * (1 + K * 2.0 ** -12)
+        tol = 17 * 2.0 ** -18 + (K // 16 - 1) * 17 * 2.0 ** -21 + 12 * ref.U * magnitude
+        ref.check(out[m], want, tol + ref.BF16 * (want.abs() + tol), f"token {m}")
