@@ -74,3 +74,27 @@ def test_parts_into_several_views(kind, R, M, N, K):
     for v in views:
         ref.check(v[:M], want, tol, "out")
         assert (v[M] == 5).all()
+
+
+def test_eight_bit_types_and_bytes_give_the_same():
+    """float8_e4m3fn and float8_e8m0fnu tensors, written by the norm and read by the linear, and bytes."""
+    need_gpu()
+    R, M, N, K = 2, 12, 72, 320
+    w, g = weights(R, N, K, 64, False, 430)
+    qw = [are.QWeight(*t, 64) for t in w]
+    parts = [torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(R)]
+    gamma = torch.rand(K, generator=g, device="cuda") + 0.5
+    outs = []
+    with are.Workspace(R_max=R, M_max=1, N_max=K) as ws:
+        for codes, scales in ((torch.uint8, torch.uint8), (torch.float8_e4m3fn, torch.float8_e8m0fnu)):
+            q = torch.empty((M, K), dtype=codes, device="cuda")
+            s = torch.empty((M, 10), dtype=scales, device="cuda")
+            out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+            are.allreduce_rmsnorm_quant_groups(parts, None, gamma, 1e-6, q, s, ws, group=32)
+            are.gemm_ar_qweight_qx((q,) * R, (s,) * R, qw, (out,) * R, ws, xgroup=32)
+            outs.append((q.view(torch.uint8), s.view(torch.uint8), out))
+        assert ws.device_status()["code"] == 0
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    val = outs[0][0].view(torch.float8_e4m3fn).double() * ref.e8m0_value(outs[0][1]).repeat_interleave(32, -1)
+    want, tol = ref.linear64([val] * R, w, 64)
+    ref.check(outs[0][2], want, tol, "out")
