@@ -514,6 +514,9 @@ ARE_API are_status are_allreduce_rmsnorm_quant_groups(const are_bf16* const part
  *  Result  : inv = rsqrt(mean_j(h_j^2) + eps), per row;
  *            dh = bf16( inv * dy * gamma - h * inv^3 * mean_j(dy_j gamma_j h_j) + dres ),
  *            the gradient of every partial and of the incoming residual alike;
+ *            (the sum of dy gamma h is formed in fp32 before inv enters: products
+ *            below 2^-126, which matter only where eps is far below h^2 and h
+ *            itself tiny, lose bits);
  *            dgamma_j = sum_i dy_ij * h_ij * inv_i, in fp32, in an order that
  *            depends on M, N and the device's SM count alone.
  * M == 0 writes dgamma = 0.  Uses a buffer of the workspace for partial sums of
