@@ -18,6 +18,9 @@ Operations (the same names as the C ABI, without the ``are_`` prefix):
   columns.
 * ``allreduce_rmsnorm_backward(dy, h, gamma, eps, dh, dgamma, ws)``  its
   backward pass.
+* ``allreduce_layernorm(partials, residual, gamma, beta, eps, out, ws)`` and
+  ``allreduce_layernorm_backward(dy, h, gamma, eps, dh, dgamma, dbeta, ws)``  the
+  same pair with LayerNorm.
 * ``gemm_ar_qweight(x, w, out, ws)``, ``gemm_ar_qweight_qx(xq, xscale, w, out,
   ws)``  the row-parallel linear of a few tokens with 4-bit weights
   (``QWeight``), all-reduced; tokens in bf16 or in FP8 codes with scales.
@@ -37,6 +40,7 @@ OK, EINVAL, ENOMEM, ECUDA, ETIMEOUT, EBUSY, ENODEV, ECAPACITY, ECAPTURE = range(
 # ops
 OP_GEMM_RS, OP_GEMM_AR, OP_ALLREDUCE_RMSNORM = 1, 2, 3
 OP_ALLREDUCE_RMSNORM_BACKWARD, OP_GEMM_AR_QWEIGHT = 4, 5
+OP_ALLREDUCE_LAYERNORM, OP_ALLREDUCE_LAYERNORM_BACKWARD = 6, 7
 # scale formats (are_scale_format)
 SCALE_F32, SCALE_E8M0 = 0, 1
 # debug flags
@@ -52,7 +56,7 @@ CHUNK_Q = 1 << 32       # counter advance per completed chunk
 # kernels (are_kernel), as reported by Workspace.last_launch()
 KERNEL_NAMES = {0: "none", 1: "memset", 2: "gemm_reduce_kernel", 3: "gemm_pair_kernel", 4: "ar_rmsnorm_kernel",
                 5: "ar_oneshot_kernel", 6: "norm_quant_rows_kernel", 7: "norm_backward_rows_kernel",
-                8: "qweight_kernel"}
+                8: "qweight_kernel", 9: "layernorm_rows_kernel", 10: "layernorm_backward_rows_kernel"}
 PIECE_WORDS = 64
 TILE_M, TILE_N = 128, 256
 
@@ -65,7 +69,7 @@ EXPORTS = [
     "are_gemm_rs", "are_gemm_ar", "are_allreduce_rmsnorm", "are_allreduce_add_rmsnorm", "are_allreduce_rmsnorm_quant",
     "are_allreduce_rmsnorm_noalloc", "are_noalloc_device_status",
     "are_allreduce_rmsnorm_quant_groups", "are_allreduce_rmsnorm_backward", "are_gemm_ar_qweight",
-    "are_gemm_ar_qweight_qx",
+    "are_gemm_ar_qweight_qx", "are_allreduce_layernorm", "are_allreduce_layernorm_backward",
 ]
 
 
@@ -161,6 +165,10 @@ def load_library(path: str = LIB_PATH):
     lib.are_gemm_ar_qweight.argtypes = [vp, vp, i32, vp, i32, i64, i64, i64, vp, vp]
     lib.are_gemm_ar_qweight_qx.restype = i32
     lib.are_gemm_ar_qweight_qx.argtypes = [vp, vp, i32, i32, vp, i32, vp, i32, i64, i64, i64, vp, vp]
+    lib.are_allreduce_layernorm.restype = i32
+    lib.are_allreduce_layernorm.argtypes = [vp, vp, vp, vp, f32, vp, vp, i32, i64, i64, vp, vp]
+    lib.are_allreduce_layernorm_backward.restype = i32
+    lib.are_allreduce_layernorm_backward.argtypes = [vp, vp, vp, f32, vp, vp, vp, vp, i32, i64, i64, vp, vp]
     _lib = lib
     return lib
 
@@ -589,6 +597,60 @@ def allreduce_rmsnorm_backward(dy: Sequence, h, gamma, eps: float, dh, dgamma, w
         _at(parts), h.data_ptr(), gamma.data_ptr(), eps, _address(dres), dh.data_ptr(), _address(dgamma), R, M, N,
         ws.handle, _on_stream(stream, dev))
     _check(rc, "are_allreduce_rmsnorm_backward")
+
+
+def allreduce_layernorm(partials: Sequence, residual, gamma, beta, eps: float, out, ws: Workspace, residual_out=None,
+                        stream=None):
+    """out = bf16(layernorm(sum_r partials[r] + residual) * gamma + beta).
+
+    ``gamma``, ``beta``: float32 [N], ``beta`` may be None.  ``residual_out``
+    (may be ``residual``): the bf16 sum, the residual that the next layer takes."""
+    import torch
+    dev, bf16 = ws.device_index, torch.bfloat16
+    R = _ranks(partials, "partials")
+    shape = _matrix(partials[0], "partials")
+    M, N = shape
+    _need_all(partials, bf16, shape, dev, "partials")
+    if residual is not None:
+        _need(residual, bf16, shape, dev, "residual")
+    if residual_out is not None:
+        _need(residual_out, bf16, shape, dev, "residual_out")
+    _need(gamma, torch.float32, (N,), dev, "gamma")
+    if beta is not None:
+        _need(beta, torch.float32, (N,), dev, "beta")
+    _need(out, bf16, shape, dev, "out")
+    parts = _addresses(partials)
+    rc = load_library().are_allreduce_layernorm(
+        _at(parts), _address(residual), gamma.data_ptr(), _address(beta), eps, out.data_ptr(), _address(residual_out), R, M,
+        N, ws.handle, _on_stream(stream, dev))
+    _check(rc, "are_allreduce_layernorm")
+
+
+def allreduce_layernorm_backward(dy: Sequence, h, gamma, eps: float, dh, dgamma, dbeta, ws: Workspace, dres=None,
+                                 stream=None):
+    """Backward pass of all-reduce + residual + LayerNorm.
+
+    As ``allreduce_rmsnorm_backward``; ``dgamma`` and ``dbeta``: float32 [N],
+    either may be None."""
+    import torch
+    dev, bf16 = ws.device_index, torch.bfloat16
+    R = _ranks(dy, "dy")
+    shape = _matrix(dy[0], "dy")
+    M, N = shape
+    _need_all(dy, bf16, shape, dev, "dy")
+    _need(h, bf16, shape, dev, "h")
+    _need(dh, bf16, shape, dev, "dh")
+    if dres is not None:
+        _need(dres, bf16, shape, dev, "dres")
+    _need(gamma, torch.float32, (N,), dev, "gamma")
+    for t, what in ((dgamma, "dgamma"), (dbeta, "dbeta")):
+        if t is not None:
+            _need(t, torch.float32, (N,), dev, what)
+    parts = _addresses(dy)
+    rc = load_library().are_allreduce_layernorm_backward(
+        _at(parts), h.data_ptr(), gamma.data_ptr(), eps, _address(dres), dh.data_ptr(), _address(dgamma), _address(dbeta),
+        R, M, N, ws.handle, _on_stream(stream, dev))
+    _check(rc, "are_allreduce_layernorm_backward")
 
 
 class QWeight:

@@ -16,8 +16,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libare.so")
-SOURCES = ["api.cu", "gemm_reduce.cu", "ar_rmsnorm.cu", "noalloc.cu", "norm_rows.cu", "qweight.cu"]
-HEADERS = ["are_internal.h", "ptx.cuh"]
+SOURCES = ["api.cu", "gemm_reduce.cu", "ar_rmsnorm.cu", "noalloc.cu", "norm_rows.cu", "qweight.cu",
+           "layernorm.cu"]
+HEADERS = ["are_internal.h", "ptx.cuh", "rows.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 NVCC = os.environ.get("NVCC", "nvcc")

@@ -38,6 +38,7 @@ struct are_ws {
     uint32_t* d_staging = nullptr;
     size_t staging_words = 0;
     bool rows_ready = false;          // the row kernels' first call has prepared them
+    bool layernorm_ready = false;     // the same of the LayerNorm kernels
     bool qweight_ready = false;       // the same of the 4-bit kernels
     QweightDevice qweight{};          // resident clusters of the 4-bit kernel
     uint8_t* d_tokens = nullptr;      // staged tokens of the 4-bit kernel
@@ -421,9 +422,11 @@ are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K) {
             if (ceil_div(M, kBM) * ceil_div(N, kBN) * R >= kLim) return ARE_EINVAL;
             return ARE_OK;
         case ARE_OP_ALLREDUCE_RMSNORM:
+        case ARE_OP_ALLREDUCE_LAYERNORM:
             if (N % 8 || N > 32768) return ARE_EINVAL;
             return ARE_OK;
         case ARE_OP_ALLREDUCE_RMSNORM_BACKWARD:
+        case ARE_OP_ALLREDUCE_LAYERNORM_BACKWARD:
             if (N % 8 || N > kBackwardMaxN) return ARE_EINVAL;
             return ARE_OK;
         case ARE_OP_GEMM_AR_QWEIGHT:
@@ -751,6 +754,13 @@ cudaError_t prepare_rows(are_ws* ws) {
     return e;
 }
 
+cudaError_t prepare_layernorm(are_ws* ws) {
+    if (ws->layernorm_ready) return cudaSuccess;
+    const cudaError_t e = layernorm_prepare();
+    ws->layernorm_ready = e == cudaSuccess;
+    return e;
+}
+
 cudaError_t prepare_qweight(are_ws* ws) {
     if (ws->qweight_ready) return cudaSuccess;
     const cudaError_t e = qweight_prepare(ws->qweight);
@@ -932,6 +942,88 @@ are_status are_allreduce_rmsnorm_backward(const are_bf16* const dy[], const are_
     plan.grid = (int)std::min<int64_t>(plan.grid, (int64_t)norm_backward_scratch_words(ws->caps.N_max, ws->num_sms) / N);
     ws->last = are_launch_info{ARE_KERNEL_NORM_BACKWARD_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
     return from_cuda(launch_norm_backward_rows(p, plan, ws->d_dgamma, dgamma, s));
+}
+
+are_status are_allreduce_layernorm(const are_bf16* const partials[], const are_bf16* residual, const float* gamma,
+                                   const float* beta, float eps, are_bf16* out, are_bf16* residual_out, int R, int64_t M,
+                                   int64_t N, are_ws* ws, void* stream) {
+    if (!ws || !partials) return ARE_EINVAL;
+    are_status st = are_supports(ARE_OP_ALLREDUCE_LAYERNORM, R, M, N, 0);
+    if (st != ARE_OK) return st;
+    for (int r = 0; r < R; ++r)
+        if (!ptr_ok(partials[r], M * N)) return ARE_EINVAL;
+    if ((residual && !aligned16(residual)) || (residual_out && !aligned16(residual_out)) || !ptr_ok(gamma, N) ||
+        (beta && !aligned16(beta)) || !ptr_ok(out, M * N))
+        return ARE_EINVAL;
+    if (!(eps > 0.f) || !std::isfinite(eps)) return ARE_EINVAL;
+    TryLock lk(ws->mu);
+    if (!lk.ok) return ARE_EBUSY;
+    if (!on_device(ws)) return ARE_EINVAL;
+    if (R > ws->caps.R_max) return ARE_ECAPACITY;
+    ws->last = are_launch_info{};
+    if (M == 0 || N == 0) return ARE_OK;
+    const cudaError_t e = prepare_layernorm(ws);
+    if (e != cudaSuccess) return from_cuda(e);
+
+    RowsParams p;
+    rows_common(p, ws, partials, gamma, eps, R, M, N);
+    if (residual) {
+        p.src[p.nsrc++] = residual;
+        p.has_res = 1;
+    }
+    p.beta = beta;
+    p.out = out;
+    p.res_out = residual_out;
+    const RowsPlan plan = layernorm_plan(p, ws->num_sms);
+    ws->last = are_launch_info{ARE_KERNEL_LAYERNORM_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
+    return from_cuda(launch_layernorm_rows(p, plan, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+are_status are_allreduce_layernorm_backward(const are_bf16* const dy[], const are_bf16* h, const float* gamma, float eps,
+                                            const are_bf16* dres, are_bf16* dh, float* dgamma, float* dbeta, int R,
+                                            int64_t M, int64_t N, are_ws* ws, void* stream) {
+    if (!ws || !dy) return ARE_EINVAL;
+    are_status st = are_supports(ARE_OP_ALLREDUCE_LAYERNORM_BACKWARD, R, M, N, 0);
+    if (st != ARE_OK) return st;
+    for (int r = 0; r < R; ++r)
+        if (!ptr_ok(dy[r], M * N)) return ARE_EINVAL;
+    if (!ptr_ok(h, M * N) || (dres && !aligned16(dres)) || !ptr_ok(dh, M * N) || !ptr_ok(gamma, N) ||
+        (dgamma && !aligned16(dgamma)) || (dbeta && !aligned16(dbeta)))
+        return ARE_EINVAL;
+    if (!(eps > 0.f) || !std::isfinite(eps)) return ARE_EINVAL;
+    TryLock lk(ws->mu);
+    if (!lk.ok) return ARE_EBUSY;
+    if (!on_device(ws)) return ARE_EINVAL;
+    if (R > ws->caps.R_max || N > ws->caps.N_max) return ARE_ECAPACITY;
+    ws->last = are_launch_info{};
+    if (N == 0) return ARE_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0) {  // sums over no rows
+        for (float* sums : {dgamma, dbeta}) {
+            if (!sums) continue;
+            ws->last.kernel = ARE_KERNEL_MEMSET;
+            const cudaError_t e = cudaMemsetAsync(sums, 0, (size_t)N * 4, s);
+            if (e != cudaSuccess) return from_cuda(e);
+        }
+        return ARE_OK;
+    }
+    const cudaError_t e = prepare_layernorm(ws);
+    if (e != cudaSuccess) return from_cuda(e);
+
+    RowsParams p;
+    rows_common(p, ws, dy, gamma, eps, R, M, N);
+    p.src[p.nsrc++] = h;
+    if (dres) {
+        p.src[p.nsrc++] = dres;
+        p.has_res = 1;
+    }
+    p.res_out = dh;
+    p.backward = 1;
+    RowsPlan plan = layernorm_plan(p, ws->num_sms);
+    // two rows of partial sums a block
+    plan.grid = (int)std::min<int64_t>(plan.grid, (int64_t)norm_backward_scratch_words(ws->caps.N_max, ws->num_sms) / (2 * N));
+    ws->last = are_launch_info{ARE_KERNEL_LAYERNORM_BACKWARD_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
+    return from_cuda(launch_layernorm_backward_rows(p, plan, ws->d_dgamma, dgamma, dbeta, s));
 }
 
 are_status are_gemm_ar_qweight(const are_bf16* const x[], const are_qweight w[], int group, are_bf16* const out[], int R,

@@ -86,10 +86,13 @@ constexpr int64_t kBackwardMaxN = 16384;  // widest row whose dgamma sums fit a 
 struct RowsParams {
     const uint16_t* src[kRowSources];  // bf16 [M, N] each: the R partials, then residual (forward) or h and d_res (backward)
     const float* gamma;                // fp32 [N]
+    const float* beta;                 // LayerNorm forward: fp32 [N] or nullptr
+    uint16_t* out;                     // LayerNorm forward: bf16 [M, N]
     uint16_t* res_out;                 // bf16 [M, N]: h or nullptr (forward); dh (backward)
     uint8_t* out_q;                    // forward: FP8 E4M3 codes [M, N]
     void* out_scale;                   // forward: [M, groups] fp32 or E8M0 bytes
     float* dgamma;                     // backward: partial sums [grid, N], or nullptr
+    float* dbeta;                      // LayerNorm backward: the same
     DevStatus* status;
     int64_t M;
     int R;
@@ -99,6 +102,8 @@ struct RowsParams {
     int groups;         // forward: scales a row
     int group_packs;    // forward: 8-column packs a group (4, 8, 16)
     int backward;       // the backward pass (gamma in shared memory, fewer threads)
+    int extra_words;    // fp32 words of shared memory of the kernel's own, a multiple of 4 (set by the plans)
+    int red_words;      // words that a block's sums are exchanged in, a multiple of 4 (set by the plans)
     int nt;             // consumer threads, a multiple of 32 (set by rows_plan)
     int slices;         // slices of nt packs a row (set by rows_plan)
     int stages;         // ring stages (set by rows_plan)
@@ -107,6 +112,9 @@ struct RowsParams {
     float inv_n;
     uint64_t timeout_ns;
 };
+
+// The attribute of a launch on the programmatic dependency (norm_rows.cu).
+cudaLaunchAttribute dependent_launch();
 
 struct RowsPlan {
     int ppt;      // packs of a row a thread owns at most (template variant)
@@ -123,6 +131,13 @@ cudaError_t launch_norm_quant_rows(const RowsParams& p, const RowsPlan& plan, bo
 cudaError_t launch_norm_backward_rows(RowsParams& p, const RowsPlan& plan, float* scratch, float* dgamma,
                                       cudaStream_t stream);
 size_t norm_backward_scratch_words(int64_t n_max, int num_sms);
+
+// LayerNorm on the same rows (layernorm.cu).
+RowsPlan layernorm_plan(RowsParams& p, int num_sms);
+cudaError_t layernorm_prepare();
+cudaError_t launch_layernorm_rows(const RowsParams& p, const RowsPlan& plan, cudaStream_t stream);
+cudaError_t launch_layernorm_backward_rows(RowsParams& p, const RowsPlan& plan, float* scratch, float* dgamma,
+                                           float* dbeta, cudaStream_t stream);
 
 // ------------------------------------------------------------------ 4-bit weights, few tokens
 struct QweightParams {

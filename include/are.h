@@ -42,15 +42,17 @@
  *    with the same workspace returns ARE_EBUSY.
  *  - are_gemm_rs, are_gemm_ar, are_allreduce_rmsnorm, are_allreduce_add_rmsnorm,
  *    are_allreduce_rmsnorm_quant, are_allreduce_rmsnorm_quant_groups,
- *    are_allreduce_rmsnorm_backward, are_gemm_ar_qweight and
+ *    are_allreduce_rmsnorm_backward, are_allreduce_layernorm,
+ *    are_allreduce_layernorm_backward, are_gemm_ar_qweight and
  *    are_gemm_ar_qweight_qx may be captured into a CUDA graph once
  *    their workspace exists: they only enqueue work on `stream` (kernels;
  *    memsets for an empty contraction), and the state they leave for the next call
  *    (tile masks at 0, staging words at -0.0) is restored inside those
  *    kernels, never by a host step, so every replay finds it as the capture
  *    did.  Workspace creation, reset and snapshots are not capturable.
- *  - are_allreduce_rmsnorm_quant_groups, are_allreduce_rmsnorm_backward and the
- *    4-bit linears launch with programmatic stream serialisation: their
+ *  - are_allreduce_rmsnorm_quant_groups, are_allreduce_rmsnorm_backward, the
+ *    LayerNorm calls and the 4-bit linears launch with programmatic stream
+ *    serialisation: their
  *    kernels may come up while earlier work of the stream still runs, and
  *    read and write no memory of the caller's before all of it has ended.
  *    They wait for nothing but their own copies, so a status word that holds
@@ -107,7 +109,9 @@ typedef enum are_op {
     ARE_OP_GEMM_AR = 2,
     ARE_OP_ALLREDUCE_RMSNORM = 3,
     ARE_OP_ALLREDUCE_RMSNORM_BACKWARD = 4,
-    ARE_OP_GEMM_AR_QWEIGHT = 5
+    ARE_OP_GEMM_AR_QWEIGHT = 5,
+    ARE_OP_ALLREDUCE_LAYERNORM = 6,
+    ARE_OP_ALLREDUCE_LAYERNORM_BACKWARD = 7
 } are_op;
 
 /* Workspace capacities.  Buffers are sized from these once, at creation, so
@@ -193,7 +197,9 @@ typedef enum are_kernel {
     ARE_KERNEL_AR_ONESHOT = 5,    /* AR+RMSNorm, one-shot (no staging) */
     ARE_KERNEL_NORM_QUANT_ROWS = 6,    /* AR+RMSNorm with scales per group of columns */
     ARE_KERNEL_NORM_BACKWARD_ROWS = 7, /* AR+RMSNorm backward */
-    ARE_KERNEL_QWEIGHT = 8             /* 4-bit weights, few tokens */
+    ARE_KERNEL_QWEIGHT = 8,            /* 4-bit weights, few tokens */
+    ARE_KERNEL_LAYERNORM_ROWS = 9,     /* AR+LayerNorm */
+    ARE_KERNEL_LAYERNORM_BACKWARD_ROWS = 10 /* AR+LayerNorm backward */
 } are_kernel;
 
 typedef struct are_launch_info {
@@ -230,9 +236,11 @@ ARE_API const char* are_status_string(are_status s);
  *  GEMM_AR: 1 <= R <= 8; K % 8 == 0; N % 8 == 0.
  *  ALLREDUCE_RMSNORM: 1 <= R <= 8; N % 8 == 0 (16-byte packs); N <= 32768.
  *  ALLREDUCE_RMSNORM_BACKWARD: as ALLREDUCE_RMSNORM, with N <= 16384.
+ *  ALLREDUCE_LAYERNORM: as ALLREDUCE_RMSNORM.
+ *  ALLREDUCE_LAYERNORM_BACKWARD: as ALLREDUCE_RMSNORM_BACKWARD.
  *  GEMM_AR_QWEIGHT: 1 <= R <= 8; K % 32 == 0 (16-byte rows of codes) and
  *           K <= 2^20; N % 8 == 0; M, N <= 2^31 - 512; ceil(M / 8) * ceil(N / 16) < 2^28.
- * K is ignored for the two ALLREDUCE_RMSNORM operations.  Pure host function: no device needed. */
+ * K is ignored for the ALLREDUCE operations.  Pure host function: no device needed. */
 ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
 
 /* Create a workspace on the current CUDA device: tile masks, the per-rank
@@ -525,6 +533,44 @@ ARE_API are_status are_allreduce_rmsnorm_quant_groups(const are_bf16* const part
 ARE_API are_status are_allreduce_rmsnorm_backward(const are_bf16* const dy[], const are_bf16* h, const float* gamma,
                                                   float eps, const are_bf16* dres, are_bf16* dh, float* dgamma, int R,
                                                   int64_t M, int64_t N, are_ws* ws, void* stream);
+
+/*
+ * All-reduce + residual add + LayerNorm (one kernel; the pages' norm is the
+ * RMSNorm, and models with the other norm place it at the same point).
+ *  partials, residual, eps: as in are_allreduce_add_rmsnorm
+ *  gamma       : fp32 [N]
+ *  beta        : fp32 [N] or NULL (a norm without bias)
+ *  out         : bf16 [M, N]
+ *  residual_out: bf16 [M, N] or NULL; receives bf16(h); may be the same buffer
+ *                as `residual` (in place).  It must not alias a partial or `out`.
+ *  Result      : h = sum_{r=0..R-1} f32(partials[r]), in that order (a sum of
+ *                -0.0 counts as +0.0), + f32(residual);
+ *                out = bf16( (h - mean) * rsqrt(var + eps) * gamma + beta ),
+ *                mean = mean_j(h_j), var = mean_j((h_j - mean)^2), in fp32, the
+ *                squares summed around the mean.
+ * A row with a value that is not finite has NaN outputs; other rows do not
+ * notice.  Needs no capacity of the workspace but R <= R_max.
+ */
+ARE_API are_status are_allreduce_layernorm(const are_bf16* const partials[], const are_bf16* residual,
+                                           const float* gamma, const float* beta, float eps, are_bf16* out,
+                                           are_bf16* residual_out, int R, int64_t M, int64_t N, are_ws* ws, void* stream);
+
+/*
+ * Backward pass of all-reduce + residual add + LayerNorm.  Arguments as in
+ * are_allreduce_rmsnorm_backward (dres in place of dh allowed), and
+ *  dgamma, dbeta: fp32 [N], either may be NULL (frozen, or no bias); overwritten
+ *  Result  : dy = sum_{r=0..R-1} f32(dy[r]) in that order, g = dy * gamma,
+ *            inv = rsqrt(var + eps), xhat = (h - mean) * inv, per row of h;
+ *            dh = bf16( inv * (g - mean_j(g_j) - xhat * mean_j(g_j xhat_j)) + dres );
+ *            dgamma_j = sum_i dy_ij * xhat_ij, dbeta_j = sum_i dy_ij, in fp32, in
+ *            an order that depends on M, N and the device's SM count alone.
+ * beta does not enter.  M == 0 writes zeros to dgamma and dbeta.  Uses a buffer
+ * of the workspace for partial sums: N must not exceed N_max (ARE_ECAPACITY), R
+ * not R_max.
+ */
+ARE_API are_status are_allreduce_layernorm_backward(const are_bf16* const dy[], const are_bf16* h, const float* gamma,
+                                                    float eps, const are_bf16* dres, are_bf16* dh, float* dgamma,
+                                                    float* dbeta, int R, int64_t M, int64_t N, are_ws* ws, void* stream);
 
 /* 4-bit weights of one rank, output row by output row: weight (n, k) is
  * (u - zero[n][k / group]) * scale[n][k / group], u its 4-bit code. */

@@ -1,0 +1,57 @@
+"""Refusals of LayerNorm that need no GPU: the predicate, and the
+entry points' argument checks before any device access."""
+import ctypes
+import os
+import re
+
+import pytest
+
+import all_reduce_epilogue_gb300 as are
+from tests.test_ops_host import FakeWorkspace
+
+vp = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from all_reduce_epilogue_gb300 import build
+    build.build()
+    return are.load_library()
+
+
+@pytest.mark.parametrize("args,ok", [
+    ((are.OP_ALLREDUCE_LAYERNORM, 8, 4096, 7168, 0), True),
+    ((are.OP_ALLREDUCE_LAYERNORM, 1, 1, 32776, 0), False),
+    ((are.OP_ALLREDUCE_LAYERNORM, 1, 1, 12, 0), False),
+    ((are.OP_ALLREDUCE_LAYERNORM, 0, 1, 64, 0), False),
+    ((are.OP_ALLREDUCE_LAYERNORM_BACKWARD, 8, 0, 16384, 0), True),
+    ((are.OP_ALLREDUCE_LAYERNORM_BACKWARD, 1, 1, 16392, 0), False),
+    ((are.OP_ALLREDUCE_LAYERNORM_BACKWARD, 1, -1, 64, 0), False),
+])
+def test_supports(lib, args, ok):
+    assert (lib.are_supports(*args) == are.OK) == ok
+
+
+def test_null_workspace(lib):
+    A, f = (vp * 2)(16, 32), ctypes.c_float(1e-6)
+    assert lib.are_allreduce_layernorm(A, None, 16, None, f, 16, None, 2, 4, 64, None, None) == are.EINVAL
+    assert lib.are_allreduce_layernorm_backward(A, 16, 16, f, None, 16, 16, 16, 2, 4, 64, None, None) == are.EINVAL
+
+
+def test_binding_refuses_host_tensors(lib):
+    import torch
+    ws = FakeWorkspace()
+    x, g = torch.zeros((2, 64), dtype=torch.bfloat16), torch.ones(64)
+    with pytest.raises(ValueError):
+        are.allreduce_layernorm([x], None, g, g, 1e-6, x, ws)
+    with pytest.raises(ValueError):
+        are.allreduce_layernorm_backward([x], x, g, 1e-6, x, g, g, ws)
+
+
+@pytest.mark.parametrize("source", ["rows.cuh", "layernorm.cu"])
+def test_no_non_coherent_loads_under_programmatic_launch(source):
+    """These kernels may start before the kernel that writes their operands has ended; a non-coherent load wants memory
+    that is read-only for the whole life of the kernel, which begins before the wait."""
+    code = re.sub(r"//[^\n]*", "", open(os.path.join(os.path.dirname(are.__file__), "csrc", source)).read())
+    assert "launch_dependent(" in code
+    assert not re.findall(r"__ldg\b|ld\.global(?:\.\w+)*\.nc\b|__restrict__", code)
