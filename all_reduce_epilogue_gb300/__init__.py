@@ -21,6 +21,10 @@ Operations (the same names as the C ABI, without the ``are_`` prefix):
 * ``allreduce_layernorm(partials, residual, gamma, beta, eps, out, ws)`` and
   ``allreduce_layernorm_backward(dy, h, gamma, eps, dh, dgamma, dbeta, ws)``  the
   same pair with LayerNorm.
+* ``gemm_cross_entropy(h, w, targets, loss, lse, ws)`` and
+  ``gemm_cross_entropy_backward(h, w, targets, lse, dloss, dh, dw, ws)``  softmax
+  cross entropy of an output layer split over the ranks, without its logits, and
+  its gradients.
 * ``gemm_ar_qweight(x, w, out, ws)``, ``gemm_ar_qweight_qx(xq, xscale, w, out,
   ws)``  the row-parallel linear of a few tokens with 4-bit weights
   (``QWeight``), all-reduced; tokens in bf16 or in FP8 codes with scales.
@@ -41,6 +45,9 @@ OK, EINVAL, ENOMEM, ECUDA, ETIMEOUT, EBUSY, ENODEV, ECAPACITY, ECAPTURE = range(
 OP_GEMM_RS, OP_GEMM_AR, OP_ALLREDUCE_RMSNORM = 1, 2, 3
 OP_ALLREDUCE_RMSNORM_BACKWARD, OP_GEMM_AR_QWEIGHT = 4, 5
 OP_ALLREDUCE_LAYERNORM, OP_ALLREDUCE_LAYERNORM_BACKWARD = 6, 7
+OP_GEMM_CROSS_ENTROPY = 8
+# index formats (are_index_format)
+INDEX_I32, INDEX_I64 = 0, 1
 # scale formats (are_scale_format)
 SCALE_F32, SCALE_E8M0 = 0, 1
 # debug flags
@@ -56,7 +63,8 @@ CHUNK_Q = 1 << 32       # counter advance per completed chunk
 # kernels (are_kernel), as reported by Workspace.last_launch()
 KERNEL_NAMES = {0: "none", 1: "memset", 2: "gemm_reduce_kernel", 3: "gemm_pair_kernel", 4: "ar_rmsnorm_kernel",
                 5: "ar_oneshot_kernel", 6: "norm_quant_rows_kernel", 7: "norm_backward_rows_kernel",
-                8: "qweight_kernel", 9: "layernorm_rows_kernel", 10: "layernorm_backward_rows_kernel"}
+                8: "qweight_kernel", 9: "layernorm_rows_kernel", 10: "layernorm_backward_rows_kernel",
+                11: "xent_kernel<LogSum>", 12: "xent_kernel<DLogits>"}
 PIECE_WORDS = 64
 TILE_M, TILE_N = 128, 256
 
@@ -70,6 +78,7 @@ EXPORTS = [
     "are_allreduce_rmsnorm_noalloc", "are_noalloc_device_status",
     "are_allreduce_rmsnorm_quant_groups", "are_allreduce_rmsnorm_backward", "are_gemm_ar_qweight",
     "are_gemm_ar_qweight_qx", "are_allreduce_layernorm", "are_allreduce_layernorm_backward",
+    "are_gemm_cross_entropy", "are_gemm_cross_entropy_backward",
 ]
 
 
@@ -86,7 +95,7 @@ class AreLibraryMissing(RuntimeError):
 class _Caps(ctypes.Structure):
     _fields_ = [("R_max", ctypes.c_int32), ("M_max", ctypes.c_int64), ("N_max", ctypes.c_int64),
                 ("K_max", ctypes.c_int64), ("timeout_ns", ctypes.c_uint64), ("debug_flags", ctypes.c_uint32),
-                ("reserved", ctypes.c_uint32)]
+                ("vocab_piece", ctypes.c_uint32)]
 
 
 class _DevStatus(ctypes.Structure):
@@ -169,6 +178,10 @@ def load_library(path: str = LIB_PATH):
     lib.are_allreduce_layernorm.argtypes = [vp, vp, vp, vp, f32, vp, vp, i32, i64, i64, vp, vp]
     lib.are_allreduce_layernorm_backward.restype = i32
     lib.are_allreduce_layernorm_backward.argtypes = [vp, vp, vp, f32, vp, vp, vp, vp, i32, i64, i64, vp, vp]
+    lib.are_gemm_cross_entropy.restype = i32
+    lib.are_gemm_cross_entropy.argtypes = [vp, vp, vp, i32, i64, vp, vp, i32, i64, i64, i64, vp, vp]
+    lib.are_gemm_cross_entropy_backward.restype = i32
+    lib.are_gemm_cross_entropy_backward.argtypes = [vp, vp, vp, i32, i64, vp, vp, vp, vp, i32, i64, i64, i64, vp, vp]
     _lib = lib
     return lib
 
@@ -218,12 +231,14 @@ def _check_bf16(t, what: str):
 class Workspace:
     """Device workspace (tile masks, partial buffer, armed staging, status word).
 
-    Sized once from the capacities; use one workspace per stream."""
+    Sized once from the capacities; use one workspace per stream.
+    ``vocab_piece``: columns of the vocabulary whose gradient the cross entropy
+    holds at a time (8192, say); 0 for a workspace without its buffers."""
 
     def __init__(self, R_max: int, M_max: int, N_max: int, K_max: int = 0, timeout_ns: int = 0,
-                 debug_flags: int = 0):
+                 debug_flags: int = 0, vocab_piece: int = 0):
         lib = load_library()
-        caps = _Caps(R_max, M_max, N_max, K_max, timeout_ns, debug_flags, 0)
+        caps = _Caps(R_max, M_max, N_max, K_max, timeout_ns, debug_flags, vocab_piece)
         h = ctypes.c_void_p()
         self.device_index = _current_device()
         _check(lib.are_workspace_create(ctypes.byref(h), ctypes.byref(caps)), "are_workspace_create")
@@ -651,6 +666,73 @@ def allreduce_layernorm_backward(dy: Sequence, h, gamma, eps: float, dh, dgamma,
         _at(parts), h.data_ptr(), gamma.data_ptr(), eps, _address(dres), dh.data_ptr(), _address(dgamma), _address(dbeta),
         R, M, N, ws.handle, _on_stream(stream, dev))
     _check(rc, "are_allreduce_layernorm_backward")
+
+
+def _index_format(t, M: int, dev: int, what: str) -> int:
+    import torch
+    _need_one_of(t, (torch.int64, torch.int32), (M,), dev, what)
+    return INDEX_I64 if t.dtype is torch.int64 else INDEX_I32
+
+
+def _output_layer(h, w: Sequence, targets, vocab, dev: int):
+    """Checks that both directions of the cross entropy share; (R, M, N, K, vocab, index format)."""
+    import torch
+    M, K = _matrix(h, "h")
+    _need(h, torch.bfloat16, (M, K), dev, "h")
+    R = _ranks(w, "w")
+    N = _matrix(w[0], "w")[0]
+    _need_all(w, torch.bfloat16, (N, K), dev, "w")
+    vocab = R * N if vocab is None else vocab
+    if not 1 <= vocab <= R * N:
+        raise ValueError(f"vocab must be 1 to {R * N}, got {vocab}")
+    return R, M, N, K, vocab, _index_format(targets, M, dev, "targets")
+
+
+def gemm_cross_entropy(h, w: Sequence, targets, loss, lse, ws: Workspace, vocab: Optional[int] = None, stream=None):
+    """loss[i] = lse[i] - z[i, targets[i]], lse[i] = log sum_v exp z[i, v], with
+    the logits z = h @ cat(w).T never stored.
+
+    ``h``: bf16 [M, K]; ``w``: R bf16 [N, K] tensors, rank r's holds the
+    vocabulary from r * N on; ``targets``: int64 or int32 [M], outside the
+    vocabulary (-100, say): loss 0; ``loss``, ``lse``: float32 [M]; ``vocab``:
+    indices that count (R * N), the rows of ``w`` behind are padding.  The
+    workspace needs ``vocab_piece`` > 0, ``M_max`` >= M and ``K_max`` >= K."""
+    import torch
+    dev = ws.device_index
+    R, M, N, K, vocab, fmt = _output_layer(h, w, targets, vocab, dev)
+    _need(loss, torch.float32, (M,), dev, "loss")
+    _need(lse, torch.float32, (M,), dev, "lse")
+    weights = _addresses(w)
+    rc = load_library().are_gemm_cross_entropy(h.data_ptr(), _at(weights), targets.data_ptr(), fmt, vocab, loss.data_ptr(),
+                                               lse.data_ptr(), R, M, N, K, ws.handle, _on_stream(stream, dev))
+    _check(rc, "are_gemm_cross_entropy")
+
+
+def gemm_cross_entropy_backward(h, w: Sequence, targets, lse, dloss, dh, dw, ws: Workspace, vocab: Optional[int] = None,
+                                stream=None):
+    """Gradients of ``gemm_cross_entropy``: ``dloss`` (float32 [M]) is the
+    gradient of ``loss``, ``lse`` what the forward call wrote.
+
+    Writes ``dh`` (bf16 [M, K], summed over the ranks, or None) and ``dw`` (R
+    bf16 [N, K] tensors, or None)."""
+    import torch
+    dev = ws.device_index
+    R, M, N, K, vocab, fmt = _output_layer(h, w, targets, vocab, dev)
+    _need(lse, torch.float32, (M,), dev, "lse")
+    _need(dloss, torch.float32, (M,), dev, "dloss")
+    if dh is not None:
+        _need(dh, torch.bfloat16, (M, K), dev, "dh")
+    grads = None
+    if dw is not None:
+        if len(dw) != R:
+            raise ValueError(f"{R} ranks of weights, {len(dw)} of gradients")
+        _need_all(dw, torch.bfloat16, (N, K), dev, "dw")
+        grads = _addresses(dw)
+    weights = _addresses(w)
+    rc = load_library().are_gemm_cross_entropy_backward(
+        h.data_ptr(), _at(weights), targets.data_ptr(), fmt, vocab, lse.data_ptr(), dloss.data_ptr(), _address(dh),
+        None if grads is None else _at(grads), R, M, N, K, ws.handle, _on_stream(stream, dev))
+    _check(rc, "are_gemm_cross_entropy_backward")
 
 
 class QWeight:

@@ -39,6 +39,9 @@ struct are_ws {
     size_t staging_words = 0;
     bool rows_ready = false;          // the row kernels' first call has prepared them
     bool layernorm_ready = false;     // the same of the LayerNorm kernels
+    void* d_xent = nullptr;           // cross entropy: one allocation, see xent_buffers
+    XentSizes xent{};
+    int xent_clusters = 0;            // resident CTA pairs of its kernels, 0 before the first call
     bool qweight_ready = false;       // the same of the 4-bit kernels
     QweightDevice qweight{};          // resident clusters of the 4-bit kernel
     uint8_t* d_tokens = nullptr;      // staged tokens of the 4-bit kernel
@@ -104,6 +107,7 @@ void free_ws(are_ws* ws) {
     cudaFree(ws->d_tokens);
     cudaFree(ws->d_chunk_ctr);
     cudaFree(ws->d_cons);
+    cudaFree(ws->d_xent);
     if (ws->h_chunk_gen) cudaFreeHost(ws->h_chunk_gen);
     delete ws;
 }
@@ -429,6 +433,13 @@ are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K) {
         case ARE_OP_ALLREDUCE_LAYERNORM_BACKWARD:
             if (N % 8 || N > kBackwardMaxN) return ARE_EINVAL;
             return ARE_OK;
+        case ARE_OP_GEMM_CROSS_ENTROPY: {
+            if (K < 8 || K >= kLim || K % 8 || N < 1) return ARE_EINVAL;
+            // tiles are counted in 32 bits
+            const int64_t vt = R * ceil_div(N, 256), mt = ceil_div(M, 256), kt = ceil_div(K, 256), most = 1 << 30;
+            if (vt >= (1 << 21) || mt * vt >= most || kt * std::max(mt, vt) >= most) return ARE_EINVAL;
+            return ARE_OK;
+        }
         case ARE_OP_GEMM_AR_QWEIGHT:
             if (K < 0 || K > (1 << 20) || K % 32 || N % 8) return ARE_EINVAL;
             // the kernels count tokens and rows, up to whole tiles of them (at most 24 groups of 16 rows), in 32 bits
@@ -444,7 +455,8 @@ are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K) {
 are_status are_workspace_create(are_ws** out, const are_caps* caps) {
     if (!out || !caps) return ARE_EINVAL;
     *out = nullptr;
-    if (!ranks_ok(caps->R_max) || caps->M_max < 1 || caps->N_max < 8 || caps->N_max % 8 || caps->K_max < 0)
+    if (!ranks_ok(caps->R_max) || caps->M_max < 1 || caps->N_max < 8 || caps->N_max % 8 || caps->K_max < 0 ||
+        (caps->vocab_piece > 0 && caps->K_max == 0) || caps->vocab_piece > (1u << 28))
         return ARE_EINVAL;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -493,6 +505,10 @@ are_status are_workspace_create(are_ws** out, const are_caps* caps) {
     }
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_tokens, caps->R_max * kQweightScratch);
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_dgamma, norm_backward_scratch_words(caps->N_max, ws->num_sms) * 4);
+    if (e == cudaSuccess && caps->vocab_piece > 0) {
+        ws->xent = xent_sizes(caps->M_max, caps->K_max, caps->vocab_piece);
+        e = cudaMalloc(&ws->d_xent, ws->xent.d_bytes + ws->xent.sum_bytes + ws->xent.row_bytes);
+    }
     if (e != cudaSuccess) {
         are_status st = from_cuda(e);
         free_ws(ws);
@@ -788,6 +804,55 @@ void rows_common(RowsParams& p, const are_ws* ws, const are_bf16* const parts[],
     p.timeout_ns = ws->timeout_ns;
 }
 
+bool index_format_ok(int f) { return f == ARE_INDEX_I32 || f == ARE_INDEX_I64; }
+bool index_ptr_ok(const void* p, int format, int64_t n) {
+    return n == 0 || aligned_to(p, format == ARE_INDEX_I64 ? 8 : 4);
+}
+
+// What both directions of the cross entropy check and set.
+are_status xent_call(XentCall& c, XentBuffers& b, const are_bf16* h, const are_bf16* const w[], const void* targets,
+                     int index_format, int64_t vocab, int R, int64_t M, int64_t N, int64_t K, are_ws* ws) {
+    if (!on_device(ws)) return ARE_EINVAL;
+    if (!ws->d_xent || R > ws->caps.R_max || M > ws->caps.M_max || K > ws->caps.K_max) return ARE_ECAPACITY;
+    if (ws->xent_clusters == 0) {
+        // at the first call, which a stream capture allows: no work is enqueued and nothing waited for
+        const cudaError_t e = xent_prepare(&ws->xent_clusters);
+        if (e != cudaSuccess || ws->xent_clusters < 1) {
+            ws->xent_clusters = 0;
+            return e == cudaSuccess ? ARE_ECUDA : from_cuda(e);
+        }
+    }
+    c.h = h;
+    for (int r = 0; r < R; ++r) c.w[r] = w[r];
+    c.targets = targets;
+    c.wide = index_format == ARE_INDEX_I64;
+    c.R = R;
+    c.M = M;
+    c.Vs = N;
+    c.K = K;
+    c.vocab = vocab;
+    uint8_t* at = static_cast<uint8_t*>(ws->d_xent);
+    b.d = at;
+    b.sums = at + ws->xent.d_bytes;
+    b.rows = at + ws->xent.d_bytes + ws->xent.sum_bytes;
+    b.sizes = ws->xent;
+    b.clusters = ws->xent_clusters;
+    b.status = ws->d_status;
+    b.timeout_ns = ws->timeout_ns;
+    return ARE_OK;
+}
+
+// Arguments of both directions that need no workspace.
+bool xent_args_ok(const are_bf16* h, const are_bf16* const w[], const void* targets, int index_format, int64_t vocab, int R,
+                  int64_t M, int64_t N, int64_t K) {
+    if (!w || !index_format_ok(index_format) || vocab < 1 || vocab > R * N || !ptr_ok(h, M * K) ||
+        !index_ptr_ok(targets, index_format, M))
+        return false;
+    for (int r = 0; r < R; ++r)
+        if (!aligned16(w[r])) return false;
+    return true;
+}
+
 are_status qweight_call(const void* const x[], const void* const xscale[], int scale_format, int xgroup, bool qx,
                         const are_qweight w[], int group, are_bf16* const out[], int R, int64_t M, int64_t N, int64_t K,
                         are_ws* ws, void* stream) {
@@ -1024,6 +1089,71 @@ are_status are_allreduce_layernorm_backward(const are_bf16* const dy[], const ar
     plan.grid = (int)std::min<int64_t>(plan.grid, (int64_t)norm_backward_scratch_words(ws->caps.N_max, ws->num_sms) / (2 * N));
     ws->last = are_launch_info{ARE_KERNEL_LAYERNORM_BACKWARD_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
     return from_cuda(launch_layernorm_backward_rows(p, plan, ws->d_dgamma, dgamma, dbeta, s));
+}
+
+are_status are_gemm_cross_entropy(const are_bf16* h, const are_bf16* const w[], const void* targets, int index_format,
+                                  int64_t vocab, float* loss, float* lse, int R, int64_t M, int64_t N, int64_t K,
+                                  are_ws* ws, void* stream) {
+    if (!ws) return ARE_EINVAL;
+    are_status st = are_supports(ARE_OP_GEMM_CROSS_ENTROPY, R, M, N, K);
+    if (st != ARE_OK) return st;
+    if (!xent_args_ok(h, w, targets, index_format, vocab, R, M, N, K)) return ARE_EINVAL;
+    if (M > 0 && (!aligned_to(loss, 4) || !aligned_to(lse, 4))) return ARE_EINVAL;
+    TryLock lk(ws->mu);
+    if (!lk.ok) return ARE_EBUSY;
+    XentCall c{};
+    XentBuffers b{};
+    st = xent_call(c, b, h, w, targets, index_format, vocab, R, M, N, K, ws);
+    if (st != ARE_OK) return st;
+    ws->last = are_launch_info{};
+    if (M == 0) return ARE_OK;
+    c.loss = loss;
+    c.lse = lse;
+    int grid = 0;
+    const cudaError_t e = launch_xent_forward(c, b, reinterpret_cast<cudaStream_t>(stream), &grid);
+    ws->last = are_launch_info{ARE_KERNEL_CROSS_ENTROPY, grid, 256, 2, 0, 0, 0, 0};
+    return from_cuda(e);
+}
+
+are_status are_gemm_cross_entropy_backward(const are_bf16* h, const are_bf16* const w[], const void* targets,
+                                           int index_format, int64_t vocab, const float* lse, const float* dloss,
+                                           are_bf16* dh, are_bf16* const dw[], int R, int64_t M, int64_t N, int64_t K,
+                                           are_ws* ws, void* stream) {
+    if (!ws) return ARE_EINVAL;
+    are_status st = are_supports(ARE_OP_GEMM_CROSS_ENTROPY, R, M, N, K);
+    if (st != ARE_OK) return st;
+    if (!xent_args_ok(h, w, targets, index_format, vocab, R, M, N, K)) return ARE_EINVAL;
+    if (M > 0 && (!aligned_to(lse, 4) || !aligned_to(dloss, 4))) return ARE_EINVAL;
+    if (dh && !aligned16(dh)) return ARE_EINVAL;
+    if (dw)
+        for (int r = 0; r < R; ++r)
+            if (!aligned16(dw[r])) return ARE_EINVAL;
+    TryLock lk(ws->mu);
+    if (!lk.ok) return ARE_EBUSY;
+    XentCall c{};
+    XentBuffers b{};
+    st = xent_call(c, b, h, w, targets, index_format, vocab, R, M, N, K, ws);
+    if (st != ARE_OK) return st;
+    ws->last = are_launch_info{};
+    if ((!dh && !dw) || (M == 0 && !dw)) return ARE_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0) {  // sums over no rows
+        ws->last.kernel = ARE_KERNEL_MEMSET;
+        for (int r = 0; r < R; ++r) {
+            const cudaError_t e = cudaMemsetAsync(dw[r], 0, (size_t)N * K * 2, s);
+            if (e != cudaSuccess) return from_cuda(e);
+        }
+        return ARE_OK;
+    }
+    c.lse = const_cast<float*>(lse);
+    c.dloss = dloss;
+    c.dh = dh;
+    c.has_dw = dw != nullptr;
+    for (int r = 0; r < R && dw; ++r) c.dw[r] = dw[r];
+    int grid = 0;
+    const cudaError_t e = launch_xent_backward(c, b, s, &grid);
+    ws->last = are_launch_info{ARE_KERNEL_CROSS_ENTROPY_BACKWARD, grid, 256, 2, 0, 0, 0, 0};
+    return from_cuda(e);
 }
 
 are_status are_gemm_ar_qweight(const are_bf16* const x[], const are_qweight w[], int group, are_bf16* const out[], int R,

@@ -240,11 +240,72 @@ struct GemmParams {
     uint64_t timeout_ns;
 };
 
+// ------------------------------------------------------------------ cross entropy (cross_entropy.cu)
+enum XentPass : int { kXentLogSum = 0, kXentDLogits = 1, kXentDH = 2, kXentDW = 3 };
+
+struct XentParams {
+    CUtensorMap tmA, tmB;         // A; B of kXentDW (h)
+    CUtensorMap tmW[kMaxRanks];   // B of the others: the ranks' weights
+    CUtensorMap tmOut[kMaxRanks]; // d, dh or its sums, or the ranks' dW
+    const void* targets;
+    const float* lse;
+    const float* dloss;
+    float2* stats;                // kXentLogSum: [M, tiles_n] (maximum, sum of exp) pairs
+    float* target_logit;          // [M]
+    DevStatus* status;
+    int64_t vocab;                // columns of all ranks that count
+    int M, K, Vs;
+    int wide;                     // targets of 64 bits
+    int rank_tiles, tile0;        // vocabulary tiles of a rank; the piece's first
+    int tiles_m, tiles_n, splits, num_kb;
+    int group;                    // rows of tiles taken together
+    int units;                    // (set at the launch)
+    int sums, add;                // kXentDH: fp32 sums, added to what is there
+    uint64_t timeout_ns;
+};
+
+struct XentCall {
+    const are_bf16* h;
+    const are_bf16* w[kMaxRanks];
+    const void* targets;
+    int wide;
+    int R;
+    int64_t M, Vs, K, vocab;
+    float* loss;                  // forward
+    float* lse;                   // forward: written; backward: read
+    const float* dloss;           // backward
+    are_bf16* dh;                 // backward, or nullptr
+    are_bf16* dw[kMaxRanks];      // backward
+    bool has_dw;
+};
+
+struct XentSizes {
+    size_t d_bytes;    // d of a piece [M, piece], or the forward pass's pairs
+    size_t sum_bytes;  // fp32 sums of dh
+    size_t row_bytes;  // a running pair and a logit a row
+};
+
+struct XentBuffers {
+    void *d, *sums, *rows;
+    XentSizes sizes;
+    int clusters;
+    DevStatus* status;
+    uint64_t timeout_ns;
+};
+
+XentSizes xent_sizes(int64_t M_max, int64_t K_max, int64_t piece);
+cudaError_t xent_prepare(int* clusters);
+cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStream_t stream, int* grid);
+cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaStream_t stream, int* grid);
+
 size_t gemm_smem_bytes();
 cudaError_t gemm_prepare_kernels();
 // bf16 [outer, inner] row-major tensor map, 128B-swizzled boxes of box_inner x box_outer.
 cudaError_t make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
                            uint32_t box_outer);
+// fp32 [d2, d1, d0] map (d0 contiguous), 128B-swizzled boxes of box0 x box1 x 1.
+cudaError_t make_tmap_f32_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0,
+                             uint32_t box1);
 // The pair kernel's partial slots for T tiles and R ranks as a 5-D map (see GemmParams::tmPart).
 cudaError_t make_tmap_part(CUtensorMap* m, const void* part, uint64_t T, uint64_t R);
 cudaError_t launch_gemm_reduce(const GemmParams& p, int mode, int grid, cudaStream_t stream);

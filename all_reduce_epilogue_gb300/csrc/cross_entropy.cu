@@ -1,0 +1,668 @@
+// Softmax cross entropy of an output layer whose vocabulary is split over R ranks, and
+// its gradients, without the logits in memory.
+//
+// With z = h W^T (W: the ranks' weights W_r [Vs, K], one below the other), target t_i:
+//   lse_i  = log sum_v exp z_iv                    loss_i = lse_i - z_{i, t_i}
+//   d_iv   = dloss_i * (exp(z_iv - lse_i) - [v = t_i])
+//   dh     = d W                                   dW_r = d_r^T h
+//
+// Four products on the tensor cores, which are what bounds it (2 M V K operations
+// forward, three times that backward, the logits being formed a second time):
+//   kLogSum   z, whose epilogue leaves the maximum of a row's 256 columns and the sum of
+//             exp(z - maximum): 8 bytes for what would be 1 KB of logits.  A small
+//             kernel joins the tiles' pairs; pieces of the vocabulary as large as the
+//             buffer holds pairs for.
+//   kDLogits  z again, whose epilogue leaves d for one piece of the vocabulary, in bf16;
+//   kDH       d W, in fp32 sums over the pieces;
+//   kDW       d^T h, rounded to bf16 once.
+// d is rounded to bf16 because that is what the tensor cores multiply at their rate: half
+// a step, 2^-8 of a term, at random in sums of many terms, which is below the rounding of
+// the bf16 results; fp32's substitute tf32 runs at half the rate.  Maxima, sums, lse and all sums
+// of products are fp32.
+//
+// One kernel body for the four, the CTA-pair scheme of the GEMM kernels: 256x256 tiles,
+// each CTA staging its 128 rows of A and 128 columns of B by TMA (six stages of 32 KB),
+// the leader issuing cta_group::2 products into two accumulators of 256 TMEM columns, so
+// the epilogue of one tile runs under the products of the next.  What differs is which
+// tensor lies along the contraction: h and W_r in kLogSum and kDLogits and d in kDH do,
+// W_r in kDH, d and h in kDW lie across it, which the tensor cores read as it is
+// (MN-major operands), so nothing is transposed in memory.  Nothing waits on another
+// pair: a grid of any size is right, and it is persistent only for its two accumulators.
+// Tiles are taken in groups of rows whose operand stays in L2 while the other one
+// streams past.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "are_internal.h"
+#include "ptx.cuh"
+
+namespace are {
+namespace {
+
+constexpr int kThreads = 256;  // TMA producer, MMA issuer, TMEM allocator, idle, four epilogue warps
+constexpr int kTile = 256;     // rows and columns of a pair's tile
+constexpr int kStagesX = 6;
+constexpr uint32_t kHalf = 128 * 64 * 2;  // a CTA's part of an operand: 128 rows or columns, 64 of the contraction
+constexpr uint32_t kStageBytes = 2 * kHalf;
+constexpr uint32_t kBox = 4096;           // an epilogue warp's staging buffer: 32 rows of 128 bytes; two a warp
+constexpr int kBars = 2 * kStagesX + 4 + 1;
+constexpr size_t kSmem = 1024 + (size_t)kStagesX * kStageBytes + 8 * (size_t)kBox + kBars * 8 + 16;
+static_assert(kSmem <= 232448, "shared memory budget");
+constexpr float kLog2e = 1.4426950408889634f;
+
+__host__ __device__ constexpr bool a_across(int pass) { return pass == kXentDW; }
+__host__ __device__ constexpr bool b_across(int pass) { return pass == kXentDH || pass == kXentDW; }
+
+// Instruction descriptor: D fp32, A and B bf16, which of them lie across the contraction, N = 256, M = 256 (pair).
+__host__ __device__ constexpr uint32_t idesc(int pass) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_across(pass) ? 1u : 0u) << 15) | ((b_across(pass) ? 1u : 0u) << 16) |
+           ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor: 128B swizzle, tcgen05 version bit.
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Bounded wait on an mbarrier phase: after a timeout the CTA's roles give up one after the other.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag, const XentParams& p,
+                                       int id, int unit) {
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (ptx::globaltimer() - t0 > p.timeout_ns) {
+            record_error(p.status, ARE_DEV_PIPE_TIMEOUT, blockIdx.x, id, unit);
+            *abort_flag = 1u;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag, const XentParams& p,
+                                     int id, int unit) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    return wait_slow(bar, parity, abort_flag, p, id, unit);
+}
+// Wait for a copy or product that was issued (it completes by itself), whatever the abort flag says.
+__device__ __noinline__ void drain(uint64_t* bar, uint32_t parity, const XentParams& p) {
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait(bar, parity))
+        if (ptx::globaltimer() - t0 > p.timeout_ns) break;
+}
+
+struct Tile {
+    int tm, tn, split;
+    int kb0, kb1;  // its part of the contraction, in blocks of 64
+};
+
+// Order of the tiles: a split's tiles together; inside, groups of p.group rows of tiles, column by column.
+__device__ __forceinline__ Tile tile_of(const XentParams& p, int u) {
+    Tile t;
+    const int per = p.tiles_m * p.tiles_n;
+    t.split = u / per;
+    u -= t.split * per;
+    const int per_group = p.group * p.tiles_n, g = u / per_group, first = g * p.group;
+    const int rows = min(p.tiles_m - first, p.group);
+    u -= g * per_group;
+    t.tm = first + u % rows;
+    t.tn = u / rows;
+    t.kb0 = (int)((int64_t)p.num_kb * t.split / p.splits);
+    t.kb1 = (int)((int64_t)p.num_kb * (t.split + 1) / p.splits);
+    return t;
+}
+
+// A vocabulary tile (256 columns of one rank) of the piece: the rank, and its first column there.
+struct Place {
+    int rank, col;
+};
+__device__ __forceinline__ Place place_of(const XentParams& p, int tile) {
+    const int v = p.tile0 + tile, r = v / p.rank_tiles;
+    return Place{r, (v - r * p.rank_tiles) * kTile};
+}
+// Columns of the tile that are in the vocabulary, 0..256.
+__device__ __forceinline__ int columns_of(const XentParams& p, const Place& at) {
+    const int64_t left = min((int64_t)p.Vs - at.col, p.vocab - ((int64_t)at.rank * p.Vs + at.col));
+    return left < 0 ? 0 : left > kTile ? kTile : (int)left;
+}
+
+__device__ __forceinline__ int64_t target_of(const XentParams& p, int row) {
+    const int64_t t = p.wide ? static_cast<const int64_t*>(p.targets)[row] : static_cast<const int32_t*>(p.targets)[row];
+    return t >= 0 && t < p.vocab ? t : -1;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// 16-byte chunk c of a 128B-swizzled staging row.
+__device__ __forceinline__ uint4* chunk_at(uint8_t* base, int row, int c) {
+    return reinterpret_cast<uint4*>(base + row * 128 + ((c ^ (row & 7)) << 4));
+}
+
+// Two staging buffers a warp, each free again once the store before the last has read it.
+struct Stager {
+    uint8_t* base;
+    int n;
+    __device__ __forceinline__ uint8_t* next() {
+        uint8_t* b = base + (n++ & 1) * kBox;
+        if ((threadIdx.x & 31) == 0) ptx::bulk_wait_read1();
+        __syncwarp();
+        return b;
+    }
+};
+
+template <int PASS>
+__global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant__ XentParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = sA + kStagesX * kHalf;
+    uint8_t* sOut = sB + kStagesX * kHalf;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 8 * kBox);
+    uint64_t* empty = full + kStagesX;
+    uint64_t* tfull = empty + kStagesX;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* mma_done = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int q = (int)ptx::cluster_ctarank();  // 0 = leader
+    const int first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStagesX; ++s) { ptx::mbar_init(&full[s], 1); ptx::mbar_init(&empty[s], 1); }
+        for (int s = 0; s < 2; ++s) { ptx::mbar_init(&tfull[s], 1); ptx::mbar_init(&tempty[s], 8); }
+        ptx::mbar_init(mma_done, 1);
+        *abort_flag = 0u;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_shared();
+    }
+    if (warp == 2) {
+        ptx::tmem_alloc_pair(tmem_slot, 512);
+        ptx::tmem_relinquish_pair();
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer (both CTAs)
+        const bool issuer = ptx::elect_one();
+        const uint64_t pol = ptx::policy_evict_normal();
+        int stage = 0;
+        uint32_t ph = 0, issued = 0, issued_ph = 0;
+        bool aborted = false;
+        for (int u = first; u < p.units && !aborted; u += pairs) {
+            const Tile t = tile_of(p, u);
+            const Place at = place_of(p, PASS == kXentDW ? t.tm : t.tn);
+            const int a0 = t.tm * kTile + q * 128, b0 = t.tn * kTile + q * 128;
+            for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                const bool ok = wait(&empty[stage], ph ^ 1u, abort_flag, p, 30, u);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    aborted = true;
+                    break;
+                }
+                if (issuer) {
+                    // both CTAs' copies complete on the leader's barrier
+                    const uint32_t fb = ptx::mapa_shared(ptx::smem_u32(&full[stage]), 0);
+                    if (q == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+                    uint8_t *a = sA + stage * kHalf, *b = sB + stage * kHalf;
+                    const int k = kb * 64;
+                    if (PASS == kXentLogSum || PASS == kXentDLogits) {
+                        ptx::tma_load_2d_pair(a, &p.tmA, fb, k, a0, pol);
+                        ptx::tma_load_2d_pair(b, &p.tmW[at.rank], fb, k, at.col + q * 128, pol);
+                    } else if (PASS == kXentDH) {
+                        ptx::tma_load_2d_pair(a, &p.tmA, fb, k, a0, pol);
+                        const Place w = place_of(p, kb >> 2);
+                        const int v = w.col + (kb & 3) * 64;
+                        for (int i = 0; i < 2; ++i)
+                            ptx::tma_load_2d_pair(b + i * 8192, &p.tmW[w.rank], fb, b0 + i * 64, v, pol);
+                    } else {
+                        for (int i = 0; i < 2; ++i) {
+                            ptx::tma_load_2d_pair(a + i * 8192, &p.tmA, fb, a0 + i * 64, k, pol);
+                            ptx::tma_load_2d_pair(b + i * 8192, &p.tmB, fb, b0 + i * 64, k, pol);
+                        }
+                    }
+                }
+                __syncwarp();
+                issued |= 1u << stage;
+                issued_ph = (issued_ph & ~(1u << stage)) | (ph << stage);
+                if (++stage == kStagesX) { stage = 0; ph ^= 1u; }
+            }
+        }
+        if (q == 0) {
+            for (int s = 0; s < kStagesX; ++s)
+                if (issued & (1u << s)) drain(&full[s], (issued_ph >> s) & 1u, p);
+        } else if (aborted) {
+            // this CTA's copies land on the leader's barriers: give them time to land
+            const uint64_t t0 = ptx::globaltimer();
+            while (ptx::globaltimer() - t0 < 50000) {}
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (leader only)
+        if (q == 0) {
+            const bool issuer = ptx::elect_one();
+            int stage = 0, it = 0;
+            uint32_t ph = 0;
+            // along the contraction: rows of 128 bytes, 32 of them a step; across: two groups of 64 columns, 16 rows a step
+            const uint64_t adesc = sdesc(ptx::smem_u32(sA), a_across(PASS) ? 8192 : 16, 1024);
+            const uint64_t bdesc = sdesc(ptx::smem_u32(sB), b_across(PASS) ? 8192 : 16, 1024);
+            constexpr int kStepA = a_across(PASS) ? 128 : 2, kStepB = b_across(PASS) ? 128 : 2;
+            bool ok = true;
+            for (int u = first; u < p.units && ok; u += pairs, ++it) {
+                const Tile t = tile_of(p, u);
+                const int buf = it & 1;
+                ok = __all_sync(0xFFFFFFFFu, wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, p, 31, u));
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint32_t d = tmem_base + buf * kTile;
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    ok = __all_sync(0xFFFFFFFFu, wait(&full[stage], ph, abort_flag, p, 32, u));
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    if (issuer) {
+                        const uint64_t ad = adesc + (uint64_t)(stage * (kHalf >> 4)), bd = bdesc + (uint64_t)(stage * (kHalf >> 4));
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            ptx::umma_bf16_pair(d, ad + (uint64_t)(kk * kStepA), bd + (uint64_t)(kk * kStepB), idesc(PASS),
+                                                kb != t.kb0 || kk != 0);
+                        ptx::umma_commit_pair_multicast(&empty[stage], 0x3);
+                        if (kb == t.kb1 - 1) ptx::umma_commit_pair_multicast(&tfull[buf], 0x3);
+                    }
+                    __syncwarp();
+                    if (++stage == kStagesX) { stage = 0; ph ^= 1u; }
+                }
+            }
+            if (issuer) ptx::umma_commit_pair(mma_done);
+            __syncwarp();
+            drain(mma_done, 0, p);
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ epilogue: a thread owns a row of the CTA's half
+        const int w = warp - 4;
+        Stager out{sOut + w * 2 * kBox, 0};
+        int it = 0;
+        for (int u = first; u < p.units; u += pairs, ++it) {
+            const Tile t = tile_of(p, u);
+            const int buf = it & 1;
+            if (!__all_sync(0xFFFFFFFFu, wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, abort_flag, p, 33, u))) break;
+            ptx::tc_fence_after();
+            const uint32_t acc = tmem_base + ((uint32_t)(w * 32) << 16) + buf * kTile;
+            const int m0 = t.tm * kTile + q * 128 + w * 32, m = m0 + lane;  // the warp's rows of the tile, the thread's
+
+            if (PASS == kXentLogSum) {
+                const Place at = place_of(p, t.tn);
+                const int cols = columns_of(p, at);
+                const bool in = m < p.M;
+                const int64_t tgt = in ? target_of(p, m) : -1;
+                const int64_t mine = tgt < 0 ? -1 : tgt - ((int64_t)at.rank * p.Vs + at.col);  // the target's column, if in 0..cols-1
+                float top = -INFINITY, sum = 0.f;
+                for (int c = 0; c < cols; c += 32) {
+                    uint32_t v[32];
+                    ptx::tmem_ld32(acc + c, v);
+                    if (c + 32 > cols) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i >= cols) v[i] = 0xFF800000u;  // -inf: not in the vocabulary
+                    }
+                    float hi = top;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) hi = fmaxf(hi, __uint_as_float(v[i]));
+                    // the difference is formed before the scaling: a row's largest logit has exactly exp 1
+                    const uint64_t minus = ptx::pair(-hi, -hi), scale = ptx::pair(kLog2e, kLog2e);
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 e = ptx::unpair(ptx::mul2(
+                            ptx::add2(ptx::pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), minus), scale));
+                        part[(2 * i) & 3] += ex2(e.x);
+                        part[(2 * i + 1) & 3] += ex2(e.y);
+                    }
+                    sum = fmaf(sum, ex2((top - hi) * kLog2e), (part[0] + part[1]) + (part[2] + part[3]));
+                    top = hi;
+                    if (mine >= c && mine < c + 32 && mine < cols) {
+                        const int at_i = (int)mine - c;
+                        float z = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) z = i == at_i ? __uint_as_float(v[i]) : z;
+                        p.target_logit[m] = z;
+                    }
+                    __syncwarp();
+                }
+                if (in) p.stats[(size_t)m * p.tiles_n + t.tn] = make_float2(top, sum);
+            } else if (PASS == kXentDLogits) {
+                const Place at = place_of(p, t.tn);
+                const int cols = columns_of(p, at);
+                const int64_t tgt = m < p.M ? target_of(p, m) : -1;
+                const bool on = tgt >= 0;  // a row without a target has no gradient, whatever its logits
+                const int64_t mine = on ? tgt - ((int64_t)at.rank * p.Vs + at.col) : -1;
+                const float lse = on ? p.lse[m] : 0.f, g = on ? p.dloss[m] : 0.f;
+                const uint64_t minus = ptx::pair(-lse, -lse), scale = ptx::pair(kLog2e, kLog2e), g2 = ptx::pair(g, g);
+                for (int c = 0; c < kTile; c += 64) {
+                    uint8_t* box = out.next();
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int c0 = c + half * 32;
+                        uint32_t v[32], d[16];
+                        ptx::tmem_ld32(acc + c0, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 e = ptx::unpair(ptx::mul2(
+                                ptx::add2(ptx::pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), minus), scale));
+                            const float2 x = ptx::unpair(ptx::mul2(ptx::pair(ex2(e.x), ex2(e.y)), g2));
+                            d[i] = on ? bf16x2(x.x, x.y) : 0u;
+                        }
+                        if (c0 + 32 > cols) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                if (c0 + 2 * i >= cols) d[i] = 0u;
+                                else if (c0 + 2 * i + 1 >= cols) d[i] &= 0xFFFFu;
+                            }
+                        }
+                        if (mine >= c0 && mine < c0 + 32 && mine < cols) {
+                            // g (p - 1): the difference before the rounding, and without cancellation where p is near 1
+                            const int at_i = (int)mine - c0;
+                            float z = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) z = i == at_i ? __uint_as_float(v[i]) : z;
+                            const uint32_t own = bf16x2(g * expm1f(z - lse), 0.f);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                if (2 * i == at_i) d[i] = (d[i] & 0xFFFF0000u) | own;
+                                if (2 * i + 1 == at_i) d[i] = (d[i] & 0xFFFFu) | (own << 16);
+                            }
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *chunk_at(box, lane, half * 4 + i) = make_uint4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+                    }
+                    ptx::fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (m0 < p.M) ptx::tma_store_2d(&p.tmOut[0], box, t.tn * kTile + c, m0);
+                        ptx::bulk_commit();
+                    }
+                    __syncwarp();
+                }
+            } else if (PASS == kXentDH && p.sums) {
+                // fp32 sums of this split, over the pieces
+                for (int c = 0; c < kTile && t.tn * kTile + c < p.K; c += 32) {
+                    uint32_t v[32];
+                    ptx::tmem_ld32(acc + c, v);
+                    uint8_t* box = out.next();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *chunk_at(box, lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    ptx::fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (m0 < p.M) {
+                            if (p.add) ptx::tma_add_3d(&p.tmOut[0], box, t.tn * kTile + c, m0, t.split);
+                            else ptx::tma_store_3d(&p.tmOut[0], box, t.tn * kTile + c, m0, t.split);
+                        }
+                        ptx::bulk_commit();
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // bf16 results: rows of dh, or of a rank's dW
+                const Place at = place_of(p, PASS == kXentDW ? t.tm : 0);
+                const int r0 = PASS == kXentDW ? at.col + q * 128 + w * 32 : m0;
+                const bool store = r0 < (PASS == kXentDW ? p.Vs : p.M);
+                const CUtensorMap* map = &p.tmOut[PASS == kXentDW ? at.rank : 0];
+                for (int c = 0; c < kTile && t.tn * kTile + c < p.K; c += 64) {
+                    uint8_t* box = out.next();
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t v[32];
+                        ptx::tmem_ld32(acc + c + half * 32, v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t d[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                d[j] = bf16x2(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
+                            *chunk_at(box, lane, half * 4 + i) = make_uint4(d[0], d[1], d[2], d[3]);
+                        }
+                    }
+                    ptx::fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (store) ptx::tma_store_2d(map, box, t.tn * kTile + c, r0);
+                        ptx::bulk_commit();
+                    }
+                    __syncwarp();
+                }
+            }
+            // the accumulator goes back to the leader's MMA warp
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), 0));
+        }
+        if (lane == 0) ptx::bulk_wait0();
+    }
+
+    __syncwarp();
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    if (warp == 2) {
+        __syncwarp();
+        ptx::tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// Joins the tiles' (maximum, sum) pairs of a row, and the pieces' before; after the last
+// piece lse = max + log(sum) and loss = (max - z_t) + log(sum), which for a token that is
+// foreseen has no large terms.  A warp a row.
+__global__ void __launch_bounds__(256) xent_join_kernel(const float2* stats, float2* carry, const float* target_logit,
+                                                        const void* targets, int wide, int64_t vocab, float* loss, float* lse,
+                                                        int M, int tiles, int first, int last) {
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= M) return;
+    const float2* at = stats + (size_t)row * tiles;
+    float top = -INFINITY, sum = 0.f;
+    if (!first && lane == 0) {
+        const float2 c = carry[row];
+        top = c.x;
+        sum = c.y;
+    }
+    for (int i = lane; i < tiles; i += 32) {
+        const float2 v = at[i];
+        const float hi = fmaxf(top, v.x);
+        // (a tile outside the vocabulary has maximum -inf and sum 0)
+        sum = (hi == top ? sum : sum * ex2((top - hi) * kLog2e)) + (hi == v.x ? v.y : v.y * ex2((v.x - hi) * kLog2e));
+        top = hi;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float x = __shfl_xor_sync(0xFFFFFFFFu, top, o), y = __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const float hi = fmaxf(top, x);
+        const float a = hi == top ? sum : sum * ex2((top - hi) * kLog2e), b = hi == x ? y : y * ex2((x - hi) * kLog2e);
+        sum = a + b;  // the same in both lanes: a sum does not depend on the order of two terms
+        top = hi;
+    }
+    if (lane) return;
+    if (!last) {
+        carry[row] = make_float2(top, sum);
+        return;
+    }
+    const float rest = logf(sum);
+    lse[row] = top + rest;
+    const int64_t t = wide ? static_cast<const int64_t*>(targets)[row] : static_cast<const int32_t*>(targets)[row];
+    loss[row] = t >= 0 && t < vocab ? (top - target_logit[row]) + rest : 0.f;
+}
+
+// dh = the splits' fp32 sums, in their order, rounded to bf16 once.
+__global__ void __launch_bounds__(256) xent_dh_kernel(const float4* sums, uint2* dh, int64_t quads, int splits) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
+        float4 a = sums[i];
+        for (int s = 1; s < splits; ++s) {
+            const float4 b = sums[s * quads + i];
+            a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+        }
+        dh[i] = make_uint2(bf16x2(a.x, a.y), bf16x2(a.z, a.w));
+    }
+}
+
+template <int PASS>
+cudaError_t launch(XentParams& p, int clusters, cudaStream_t s) {
+    p.units = p.tiles_m * p.tiles_n * p.splits;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)std::min(p.units, clusters));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, xent_kernel<PASS>, p);
+}
+
+constexpr int kGroup = 16;  // rows of tiles whose operand stays in L2: 4096 rows
+
+int ceil256(int64_t n) { return (int)((n + kTile - 1) / kTile); }
+
+}  // namespace
+
+cudaError_t xent_prepare(int* clusters) {
+    cudaError_t e = cudaSuccess;
+    for (auto* f : {xent_kernel<kXentLogSum>, xent_kernel<kXentDLogits>, xent_kernel<kXentDH>, xent_kernel<kXentDW>})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2048);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(clusters, xent_kernel<kXentLogSum>, &cfg);
+}
+
+XentSizes xent_sizes(int64_t M_max, int64_t K_max, int64_t piece) {
+    XentSizes z;
+    z.d_bytes = (size_t)M_max * ceil256(piece) * kTile * 2;
+    // one set of sums for the longest call, or several for calls of few tiles that split the vocabulary over the pairs
+    z.sum_bytes = (size_t)M_max * K_max * 4 + (size_t)std::min<int64_t>(M_max, kTile) * kTile * 4 * 80;
+    z.row_bytes = (size_t)M_max * 12;
+    return z;
+}
+
+static void common(XentParams& p, const XentCall& c, const XentBuffers& b) {
+    p.M = (int)c.M;
+    p.K = (int)c.K;
+    p.Vs = (int)c.Vs;
+    p.vocab = c.vocab;
+    p.rank_tiles = ceil256(c.Vs);
+    p.targets = c.targets;
+    p.wide = c.wide;
+    p.status = b.status;
+    p.timeout_ns = b.timeout_ns;
+    p.splits = 1;
+    p.group = kGroup;
+}
+
+cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStream_t s, int* grid) {
+    XentParams p{};
+    common(p, c, b);
+    cudaError_t e = make_tmap_bf16(&p.tmA, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, 128);
+    for (int r = 0; r < c.R && e == cudaSuccess; ++r)
+        e = make_tmap_bf16(&p.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 128);
+    if (e != cudaSuccess) return e;
+    const int total = c.R * p.rank_tiles;
+    const int fit = (int)std::min<int64_t>(total, (int64_t)(b.sizes.d_bytes / ((size_t)c.M * 8)));
+    p.stats = static_cast<float2*>(b.d);
+    float2* carry = static_cast<float2*>(b.rows);
+    p.target_logit = reinterpret_cast<float*>(carry + c.M);
+    p.tiles_m = ceil256(c.M);
+    p.num_kb = (int)((c.K + 63) / 64);
+    for (p.tile0 = 0; p.tile0 < total && e == cudaSuccess; p.tile0 += p.tiles_n) {
+        p.tiles_n = std::min(fit, total - p.tile0);
+        e = launch<kXentLogSum>(p, b.clusters, s);
+        if (p.tile0 == 0) *grid = 2 * std::min(p.units, b.clusters);
+        if (e != cudaSuccess) return e;
+        xent_join_kernel<<<(unsigned)((c.M + 7) / 8), 256, 0, s>>>(p.stats, carry, p.target_logit, c.targets, c.wide, c.vocab,
+                                                                  c.loss, c.lse, (int)c.M, p.tiles_n, p.tile0 == 0,
+                                                                  p.tile0 + p.tiles_n == total);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaStream_t s, int* grid) {
+    XentParams z{};  // the logits and their gradient
+    common(z, c, b);
+    z.lse = c.lse;
+    z.dloss = c.dloss;
+    z.tiles_m = ceil256(c.M);
+    z.num_kb = (int)((c.K + 63) / 64);
+    XentParams dh = z, dw = z;
+    const int total = c.R * z.rank_tiles, tiles_k = ceil256(c.K);
+    const int most = (int)std::min<int64_t>(total, (int64_t)(b.sizes.d_bytes / ((size_t)c.M * kTile * 2)));
+    const int even = (total + most - 1) / most, piece = (total + even - 1) / even;
+    const int pieces = (total + piece - 1) / piece, left = total - (pieces - 1) * piece;  // the last piece's tiles, 1..piece
+    cudaError_t e = make_tmap_bf16(&z.tmA, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, 128);
+    for (int r = 0; r < c.R && e == cudaSuccess; ++r) {
+        e = make_tmap_bf16(&z.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 128);
+        if (e == cudaSuccess && c.dh) e = make_tmap_bf16(&dh.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 64);
+        if (e == cudaSuccess && c.has_dw) e = make_tmap_bf16(&dw.tmOut[r], c.dw[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 32);
+    }
+    if (e == cudaSuccess && c.has_dw) e = make_tmap_bf16(&dw.tmB, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, 64);
+    // dh of few tokens has few tiles: the vocabulary is split over the pairs that would have none
+    const size_t set = (size_t)c.M * c.K * 4;
+    dh.tiles_n = tiles_k;
+    dh.splits = std::max(1, std::min({b.clusters / (dh.tiles_m * tiles_k), (int)(b.sizes.sum_bytes / set), piece / 2, 4 * left}));
+    dh.sums = pieces > 1 || dh.splits > 1;
+    if (e == cudaSuccess && c.dh)
+        e = dh.sums ? make_tmap_f32_3d(&dh.tmOut[0], b.sums, (uint64_t)c.K, (uint64_t)c.M, (uint64_t)dh.splits, 32, 32)
+                    : make_tmap_bf16(&dh.tmOut[0], c.dh, (uint64_t)c.K, (uint64_t)c.M, 64, 32);
+    dw.tiles_n = tiles_k;
+    dw.num_kb = (int)((c.M + 63) / 64);
+    for (int t0 = 0; t0 < total && e == cudaSuccess; t0 += piece) {
+        const int n = std::min(piece, total - t0);
+        z.tile0 = dh.tile0 = dw.tile0 = t0;
+        z.tiles_n = dw.tiles_m = n;
+        dh.num_kb = 4 * n;
+        const uint64_t cols = (uint64_t)n * kTile;
+        if (t0 == 0 || n != piece) {  // the piece's d [M, cols]: as an output, along and across the contraction
+            e = make_tmap_bf16(&z.tmOut[0], b.d, cols, (uint64_t)c.M, 64, 32);
+            if (e == cudaSuccess) e = make_tmap_bf16(&dh.tmA, b.d, cols, (uint64_t)c.M, 64, 128);
+            if (e == cudaSuccess) e = make_tmap_bf16(&dw.tmA, b.d, cols, (uint64_t)c.M, 64, 64);
+        }
+        if (e == cudaSuccess) e = launch<kXentDLogits>(z, b.clusters, s);
+        if (t0 == 0) *grid = 2 * std::min(z.units, b.clusters);
+        dh.add = t0 > 0;
+        if (e == cudaSuccess && c.dh) e = launch<kXentDH>(dh, b.clusters, s);
+        if (e == cudaSuccess && c.has_dw) e = launch<kXentDW>(dw, b.clusters, s);
+    }
+    if (e == cudaSuccess && c.dh && dh.sums) {
+        const int64_t quads = c.M * c.K / 4;
+        xent_dh_kernel<<<(unsigned)std::min<int64_t>((quads + 255) / 256, 152 * 8), 256, 0, s>>>(
+            static_cast<const float4*>(b.sums), reinterpret_cast<uint2*>(c.dh), quads, dh.splits);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace are

@@ -43,7 +43,8 @@
  *  - are_gemm_rs, are_gemm_ar, are_allreduce_rmsnorm, are_allreduce_add_rmsnorm,
  *    are_allreduce_rmsnorm_quant, are_allreduce_rmsnorm_quant_groups,
  *    are_allreduce_rmsnorm_backward, are_allreduce_layernorm,
- *    are_allreduce_layernorm_backward, are_gemm_ar_qweight and
+ *    are_allreduce_layernorm_backward, are_gemm_cross_entropy,
+ *    are_gemm_cross_entropy_backward, are_gemm_ar_qweight and
  *    are_gemm_ar_qweight_qx may be captured into a CUDA graph once
  *    their workspace exists: they only enqueue work on `stream` (kernels;
  *    memsets for an empty contraction), and the state they leave for the next call
@@ -111,7 +112,8 @@ typedef enum are_op {
     ARE_OP_ALLREDUCE_RMSNORM_BACKWARD = 4,
     ARE_OP_GEMM_AR_QWEIGHT = 5,
     ARE_OP_ALLREDUCE_LAYERNORM = 6,
-    ARE_OP_ALLREDUCE_LAYERNORM_BACKWARD = 7
+    ARE_OP_ALLREDUCE_LAYERNORM_BACKWARD = 7,
+    ARE_OP_GEMM_CROSS_ENTROPY = 8
 } are_op;
 
 /* Workspace capacities.  Buffers are sized from these once, at creation, so
@@ -123,7 +125,8 @@ typedef struct are_caps {
     int64_t K_max;       /* largest K; 0 = no GEMM buffers (AR+RMSNorm only) */
     uint64_t timeout_ns; /* bound of every device-side wait; 0 = 200 ms */
     uint32_t debug_flags;/* ARE_DEBUG_* */
-    uint32_t reserved;
+    uint32_t vocab_piece;/* cross entropy: columns of the vocabulary whose gradient is held at a time (rounded up to
+                            256); 0 = no buffers for it */
 } are_caps;
 
 /* Debug switches (default off; they change bookkeeping, never the arithmetic). */
@@ -199,7 +202,9 @@ typedef enum are_kernel {
     ARE_KERNEL_NORM_BACKWARD_ROWS = 7, /* AR+RMSNorm backward */
     ARE_KERNEL_QWEIGHT = 8,            /* 4-bit weights, few tokens */
     ARE_KERNEL_LAYERNORM_ROWS = 9,     /* AR+LayerNorm */
-    ARE_KERNEL_LAYERNORM_BACKWARD_ROWS = 10 /* AR+LayerNorm backward */
+    ARE_KERNEL_LAYERNORM_BACKWARD_ROWS = 10, /* AR+LayerNorm backward */
+    ARE_KERNEL_CROSS_ENTROPY = 11,           /* cross entropy: the first of its kernels */
+    ARE_KERNEL_CROSS_ENTROPY_BACKWARD = 12
 } are_kernel;
 
 typedef struct are_launch_info {
@@ -240,13 +245,19 @@ ARE_API const char* are_status_string(are_status s);
  *  ALLREDUCE_LAYERNORM_BACKWARD: as ALLREDUCE_RMSNORM_BACKWARD.
  *  GEMM_AR_QWEIGHT: 1 <= R <= 8; K % 32 == 0 (16-byte rows of codes) and
  *           K <= 2^20; N % 8 == 0; M, N <= 2^31 - 512; ceil(M / 8) * ceil(N / 16) < 2^28.
+ *  GEMM_CROSS_ENTROPY (N: rows of one rank's weights, K: width of the hidden
+ *           states): 1 <= R <= 8; K >= 8, K % 8 == 0; N >= 1;
+ *           R * ceil(N / 256) < 2^21, ceil(M / 256) * R * ceil(N / 256) and
+ *           ceil(K / 256) * max(ceil(M / 256), R * ceil(N / 256)) < 2^30.
  * K is ignored for the ALLREDUCE operations.  Pure host function: no device needed. */
 ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
 
 /* Create a workspace on the current CUDA device: tile masks, the per-rank
  * partial buffer, the Lamport staging buffer (filled with the sentinel, on a
  * private stream, synchronously), partial sums of dgamma, 2 MiB a rank of
- * staged tokens for the 4-bit linear, and the device status word.
+ * staged tokens for the 4-bit linear, with vocab_piece > 0 the cross entropy's
+ * buffers (M_max * (2 * vocab_piece + 4 * K_max + 12) bytes and up to 20 MB), and
+ * the device status word.
  * ROCm/mori PR #662, review threads: every capacity is validated before the
  * first allocation; buffer offsets are sized from the capacities, never from
  * a call's M, so the layout does not move between calls; a set-up that fails
@@ -255,7 +266,8 @@ ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
  * commits: the staging region is private to this library and is armed here,
  * outside any stream capture, on a stream of its own (an arming captured into
  * a graph would re-arm on every replay, under the kernel's feet).
- *  caps : R_max 1..8, M_max >= 1, N_max >= 8 and N_max % 8 == 0, K_max >= 0.
+ *  caps : R_max 1..8, M_max >= 1, N_max >= 8 and N_max % 8 == 0, K_max >= 0;
+ *         vocab_piece > 0 needs K_max > 0.
  *  ws   : receives the handle; *ws is NULL on any failure.
  * Returns ARE_EINVAL for bad capacities, ARE_ENODEV if the current device is
  * not sm_103, ARE_ENOMEM / ARE_ECUDA if an allocation or the arming fails.
@@ -571,6 +583,56 @@ ARE_API are_status are_allreduce_layernorm(const are_bf16* const partials[], con
 ARE_API are_status are_allreduce_layernorm_backward(const are_bf16* const dy[], const are_bf16* h, const float* gamma,
                                                     float eps, const are_bf16* dres, are_bf16* dh, float* dgamma,
                                                     float* dbeta, int R, int64_t M, int64_t N, are_ws* ws, void* stream);
+
+/* How a tensor of token indices is stored. */
+typedef enum are_index_format {
+    ARE_INDEX_I32 = 0,
+    ARE_INDEX_I64 = 1
+} are_index_format;
+
+/*
+ * Softmax cross entropy of an output layer whose vocabulary is split over the
+ * ranks (column-parallel: the pages' row-parallel layers end in an all-reduce of
+ * partial sums, this one in an all-reduce of each row's maximum and sum).  The
+ * logits are never stored.
+ *  h       : bf16 [M, K], the hidden states (every rank has them)
+ *  w[r]    : bf16 [N, K], rank r's rows of the output layer: vocabulary index
+ *            r * N + n
+ *  vocab   : indices that count, 1 <= vocab <= R * N; weights behind are padding
+ *            and take no part
+ *  targets : [M] indices, are_index_format, aligned to its element.  A target
+ *            outside 0..vocab-1 (-100, say) has loss 0 and no gradient.
+ *  loss    : fp32 [M], 4-byte aligned
+ *  lse     : fp32 [M], 4-byte aligned; for the backward call
+ *  Result  : z_iv = sum_k h_ik w_vk (fp32), lse_i = log sum_{v < vocab} exp(z_iv),
+ *            loss_i = lse_i - z_{i, target_i}.  Rows do not depend on one another; a
+ *            row with a NaN or infinite logit has NaN or infinite results.
+ * Needs a workspace with vocab_piece > 0, M <= M_max, K <= K_max, R <= R_max.
+ */
+ARE_API are_status are_gemm_cross_entropy(const are_bf16* h, const are_bf16* const w[], const void* targets,
+                                          int index_format, int64_t vocab, float* loss, float* lse, int R, int64_t M,
+                                          int64_t N, int64_t K, are_ws* ws, void* stream);
+
+/*
+ * Its gradients.  h, w, targets, vocab: as in the forward call; lse: what it wrote.
+ *  dloss   : fp32 [M], 4-byte aligned: the gradient of loss
+ *  dh      : bf16 [M, K] or NULL, the sum over the ranks
+ *  dw      : NULL (frozen), or dw[r]: bf16 [N, K] for every rank; overwritten, rows
+ *            behind vocab with zeros
+ *  Result  : d_iv = dloss_i * (exp(z_iv - lse_i) - [v == target_i]), 0 in rows
+ *            without a target;  dh = bf16(d w), dw_r = bf16(d_r^T h).
+ *            d is rounded to bf16 before the products (half a step, 2^-8 of each
+ *            term), the products' sums are fp32 and rounded once.  A row without a
+ *            target has dh 0; its h enters dw times 0, so it must be finite.
+ * The vocabulary is taken in pieces of at most vocab_piece columns (more if M is
+ * below M_max), and for few tokens dh's sums are split; both go by the sizes,
+ * the capacities and the device, so workspaces of the same capacities give the
+ * same bits.  Outputs must not overlap inputs.  M == 0 writes zeros to dw.
+ */
+ARE_API are_status are_gemm_cross_entropy_backward(const are_bf16* h, const are_bf16* const w[], const void* targets,
+                                                   int index_format, int64_t vocab, const float* lse, const float* dloss,
+                                                   are_bf16* dh, are_bf16* const dw[], int R, int64_t M, int64_t N,
+                                                   int64_t K, are_ws* ws, void* stream);
 
 /* 4-bit weights of one rank, output row by output row: weight (n, k) is
  * (u - zero[n][k / group]) * scale[n][k / group], u its 4-bit code. */

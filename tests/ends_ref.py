@@ -65,3 +65,44 @@ def layernorm_backward64(dys, h, gamma, dres):
     m = (len(dys) + M + 64) * U
     dgamma, dbeta = (dy * xhat).sum(0), dy.sum(0)
     return (dh, tol, dgamma, m * (mag * xhat.abs()).sum(0) + (mag * tol_x).sum(0) + 1e-38, dbeta, m * mag.sum(0) + 1e-38)
+
+
+def cross_entropy64(h, ws, targets, vocab, dloss=None):
+    """loss, lse, dh, dw in 64 bits, each with its bound.
+
+    A logit's products are summed by tensor instructions of 16 terms that truncate: (K / 16 + 64) steps of
+    sum |h w|, as for the 4-bit linear.  lse is off by no more than the worst logit of its row, by 2^-20 for exp and
+    log (ex2 2^-22, 2^-21 for sums of up to 256 columns and joins) and by its rounding; d by its logit's error, lse's and
+    2^-20, relative to exp(z - lse), and by bf16's half step."""
+    M, K = h.shape
+    N = ws[0].shape[0]
+    w = torch.cat([t.double() for t in ws])
+    x = h.double()
+    z = x @ w[:vocab].T
+    err = (K / 16 + 64) * 2 * U * (x.abs() @ w[:vocab].abs().T)
+    lse = torch.logsumexp(z, 1)
+    worst = err.max(1).values if M else lse
+    tol_lse = worst + 2.0 ** -20 + 2 * U * lse.abs()
+    t = targets.long()
+    on = (t >= 0) & (t < vocab)
+    at = t.clamp(0, vocab - 1)[:, None]
+    loss = torch.where(on, lse - z.gather(1, at)[:, 0], 0.0)
+    tol_loss = torch.where(on, 2 * worst + 2.0 ** -20 + 2 * U * loss.abs(), 0.0)
+    out = [(loss, tol_loss), (lse, tol_lse)]
+    if dloss is None:
+        return out
+    g = torch.where(on, dloss.double(), 0.0)[:, None]
+    p = torch.exp(z - lse[:, None])
+    hot = torch.zeros_like(p).scatter_(1, at, 1.0) * on[:, None]
+    d = (p - hot) * g
+    e = p * g.abs() * (err + tol_lse[:, None] + 2.0 ** -20) * 1.1
+    e = e + BF16 * (d.abs() + e) + 1e-38
+    dh, mag = d @ w[:vocab], d.abs() @ w[:vocab].abs()
+    tol = e @ w[:vocab].abs() + (vocab / 16 + 64) * 2 * U * mag
+    out.append((dh, tol + BF16 * (dh.abs() + tol) + 1e-38))
+    dw = torch.zeros_like(w)
+    tol = torch.zeros_like(w)
+    dw[:vocab] = d.T @ x
+    tol[:vocab] = e.T @ x.abs() + (M / 16 + 64) * 2 * U * (d.abs().T @ x.abs())
+    tol[:vocab] += BF16 * (dw[:vocab].abs() + tol[:vocab]) + 1e-38
+    return out + [(dw.view(len(ws), N, K), tol.view(len(ws), N, K))]
