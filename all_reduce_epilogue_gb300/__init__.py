@@ -21,6 +21,9 @@ Operations (the same names as the C ABI, without the ``are_`` prefix):
 * ``allreduce_layernorm(partials, residual, gamma, beta, eps, out, ws)`` and
   ``allreduce_layernorm_backward(dy, h, gamma, eps, dh, dgamma, dbeta, ws)``  the
   same pair with LayerNorm.
+* ``embedding_ar(ids, tables, out, ws)`` and ``embedding_ar_backward(ids, dy,
+  dtables, ws)``  lookup in a table split over the ranks, and its gradient by
+  sorted tokens.
 * ``gemm_cross_entropy(h, w, targets, loss, lse, ws)`` and
   ``gemm_cross_entropy_backward(h, w, targets, lse, dloss, dh, dw, ws)``  softmax
   cross entropy of an output layer split over the ranks, without its logits, and
@@ -45,7 +48,7 @@ OK, EINVAL, ENOMEM, ECUDA, ETIMEOUT, EBUSY, ENODEV, ECAPACITY, ECAPTURE = range(
 OP_GEMM_RS, OP_GEMM_AR, OP_ALLREDUCE_RMSNORM = 1, 2, 3
 OP_ALLREDUCE_RMSNORM_BACKWARD, OP_GEMM_AR_QWEIGHT = 4, 5
 OP_ALLREDUCE_LAYERNORM, OP_ALLREDUCE_LAYERNORM_BACKWARD = 6, 7
-OP_GEMM_CROSS_ENTROPY = 8
+OP_GEMM_CROSS_ENTROPY, OP_EMBEDDING_AR, OP_EMBEDDING_AR_BACKWARD = 8, 9, 10
 # index formats (are_index_format)
 INDEX_I32, INDEX_I64 = 0, 1
 # scale formats (are_scale_format)
@@ -64,7 +67,7 @@ CHUNK_Q = 1 << 32       # counter advance per completed chunk
 KERNEL_NAMES = {0: "none", 1: "memset", 2: "gemm_reduce_kernel", 3: "gemm_pair_kernel", 4: "ar_rmsnorm_kernel",
                 5: "ar_oneshot_kernel", 6: "norm_quant_rows_kernel", 7: "norm_backward_rows_kernel",
                 8: "qweight_kernel", 9: "layernorm_rows_kernel", 10: "layernorm_backward_rows_kernel",
-                11: "xent_kernel<LogSum>", 12: "xent_kernel<DLogits>"}
+                11: "xent_kernel<LogSum>", 12: "xent_kernel<DLogits>", 13: "embed_kernel", 14: "embed_sort_kernel"}
 PIECE_WORDS = 64
 TILE_M, TILE_N = 128, 256
 
@@ -79,6 +82,7 @@ EXPORTS = [
     "are_allreduce_rmsnorm_quant_groups", "are_allreduce_rmsnorm_backward", "are_gemm_ar_qweight",
     "are_gemm_ar_qweight_qx", "are_allreduce_layernorm", "are_allreduce_layernorm_backward",
     "are_gemm_cross_entropy", "are_gemm_cross_entropy_backward",
+    "are_embedding_ar", "are_embedding_ar_backward",
 ]
 
 
@@ -182,6 +186,10 @@ def load_library(path: str = LIB_PATH):
     lib.are_gemm_cross_entropy.argtypes = [vp, vp, vp, i32, i64, vp, vp, i32, i64, i64, i64, vp, vp]
     lib.are_gemm_cross_entropy_backward.restype = i32
     lib.are_gemm_cross_entropy_backward.argtypes = [vp, vp, vp, i32, i64, vp, vp, vp, vp, i32, i64, i64, i64, vp, vp]
+    lib.are_embedding_ar.restype = i32
+    lib.are_embedding_ar.argtypes = [vp, i32, vp, f32, vp, i32, i64, i64, i64, vp, vp]
+    lib.are_embedding_ar_backward.restype = i32
+    lib.are_embedding_ar_backward.argtypes = [vp, i32, vp, f32, i32, vp, i32, i64, i64, i64, vp, vp]
     _lib = lib
     return lib
 
@@ -672,6 +680,47 @@ def _index_format(t, M: int, dev: int, what: str) -> int:
     import torch
     _need_one_of(t, (torch.int64, torch.int32), (M,), dev, what)
     return INDEX_I64 if t.dtype is torch.int64 else INDEX_I32
+
+
+def _tables(ids, rows, tables: Sequence, dev: int, what: str, rows_what: str):
+    """Checks that both directions of the embedding share; (R, M, N, V, index format)."""
+    import torch
+    M, N = _matrix(rows, rows_what)
+    _need(rows, torch.bfloat16, (M, N), dev, rows_what)
+    R = _ranks(tables, what)
+    V = _matrix(tables[0], what)[0]
+    _need_all(tables, torch.bfloat16, (V, N), dev, what)
+    return R, M, N, V, _index_format(ids, M, dev, "ids")
+
+
+def embedding_ar(ids, tables: Sequence, out, ws: Workspace, scale: float = 1.0, stream=None):
+    """out[i] = bf16(scale * row ids[i] of cat(tables)); zeros where ids[i] is
+    outside the vocabulary.
+
+    ``ids``: int64 or int32 [M]; ``tables``: R bf16 [V, N] tensors, rank r's
+    holds the vocabulary from r * V on; ``out``: bf16 [M, N]."""
+    dev = ws.device_index
+    R, M, N, V, fmt = _tables(ids, out, tables, dev, "tables", "out")
+    rows = _addresses(tables)
+    rc = load_library().are_embedding_ar(ids.data_ptr(), fmt, _at(rows), scale, out.data_ptr(), R, M, N, V, ws.handle,
+                                         _on_stream(stream, dev))
+    _check(rc, "are_embedding_ar")
+
+
+def embedding_ar_backward(ids, dy, dtables: Sequence, ws: Workspace, scale: float = 1.0, accumulate: bool = False,
+                          stream=None):
+    """The gradient of ``embedding_ar`` for every rank's table: row v of
+    cat(dtables) = bf16(scale * the fp32 sum of the dy[i] with ids[i] = v).
+
+    ``dy``: bf16 [M, N].  Every row is written, or, with ``accumulate``, the
+    rows that tokens have are added to and the others left alone.  The
+    workspace needs ``M_max`` >= M and ``N_max`` >= N."""
+    dev = ws.device_index
+    R, M, N, V, fmt = _tables(ids, dy, dtables, dev, "dtables", "dy")
+    rows = _addresses(dtables)
+    rc = load_library().are_embedding_ar_backward(ids.data_ptr(), fmt, dy.data_ptr(), scale, int(bool(accumulate)), _at(rows), R,
+                                                  M, N, V, ws.handle, _on_stream(stream, dev))
+    _check(rc, "are_embedding_ar_backward")
 
 
 def _output_layer(h, w: Sequence, targets, vocab, dev: int):

@@ -39,6 +39,8 @@ struct are_ws {
     size_t staging_words = 0;
     bool rows_ready = false;          // the row kernels' first call has prepared them
     bool layernorm_ready = false;     // the same of the LayerNorm kernels
+    bool embed_ready = false;         // the same of the embedding's gradient
+    void* d_sort = nullptr;           // embedding's gradient: sorted tokens
     void* d_xent = nullptr;           // cross entropy: one allocation, see xent_buffers
     XentSizes xent{};
     int xent_clusters = 0;            // resident CTA pairs of its kernels, 0 before the first call
@@ -108,6 +110,7 @@ void free_ws(are_ws* ws) {
     cudaFree(ws->d_chunk_ctr);
     cudaFree(ws->d_cons);
     cudaFree(ws->d_xent);
+    cudaFree(ws->d_sort);
     if (ws->h_chunk_gen) cudaFreeHost(ws->h_chunk_gen);
     delete ws;
 }
@@ -433,6 +436,10 @@ are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K) {
         case ARE_OP_ALLREDUCE_LAYERNORM_BACKWARD:
             if (N % 8 || N > kBackwardMaxN) return ARE_EINVAL;
             return ARE_OK;
+        case ARE_OP_EMBEDDING_AR:
+        case ARE_OP_EMBEDDING_AR_BACKWARD:
+            if (N % 8 || N > 32768 || K < 1 || K >= kLim || R * K >= kLim || M > (1 << 30)) return ARE_EINVAL;
+            return ARE_OK;
         case ARE_OP_GEMM_CROSS_ENTROPY: {
             if (K < 8 || K >= kLim || K % 8 || N < 1) return ARE_EINVAL;
             // tiles are counted in 32 bits
@@ -505,6 +512,7 @@ are_status are_workspace_create(are_ws** out, const are_caps* caps) {
     }
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_tokens, caps->R_max * kQweightScratch);
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_dgamma, norm_backward_scratch_words(caps->N_max, ws->num_sms) * 4);
+    if (e == cudaSuccess) e = cudaMalloc(&ws->d_sort, embed_sort_bytes(caps->M_max));
     if (e == cudaSuccess && caps->vocab_piece > 0) {
         ws->xent = xent_sizes(caps->M_max, caps->K_max, caps->vocab_piece);
         e = cudaMalloc(&ws->d_xent, ws->xent.d_bytes + ws->xent.sum_bytes + ws->xent.row_bytes);
@@ -809,6 +817,19 @@ bool index_ptr_ok(const void* p, int format, int64_t n) {
     return n == 0 || aligned_to(p, format == ARE_INDEX_I64 ? 8 : 4);
 }
 
+void embed_common(EmbedParams& p, const void* ids, int index_format, float scale, const are_bf16* const tables[], int R,
+                  int64_t M, int64_t N, int64_t V) {
+    for (int r = 0; r < R; ++r) p.tables[r] = const_cast<are_bf16*>(tables[r]);
+    p.ids = ids;
+    p.M = M;
+    p.N = (int)N;
+    p.R = R;
+    p.Vs = (uint32_t)V;
+    p.V = (uint32_t)(R * V);
+    p.wide = index_format == ARE_INDEX_I64;
+    p.scale = scale;
+}
+
 // What both directions of the cross entropy check and set.
 are_status xent_call(XentCall& c, XentBuffers& b, const are_bf16* h, const are_bf16* const w[], const void* targets,
                      int index_format, int64_t vocab, int R, int64_t M, int64_t N, int64_t K, are_ws* ws) {
@@ -1089,6 +1110,62 @@ are_status are_allreduce_layernorm_backward(const are_bf16* const dy[], const ar
     plan.grid = (int)std::min<int64_t>(plan.grid, (int64_t)norm_backward_scratch_words(ws->caps.N_max, ws->num_sms) / (2 * N));
     ws->last = are_launch_info{ARE_KERNEL_LAYERNORM_BACKWARD_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
     return from_cuda(launch_layernorm_backward_rows(p, plan, ws->d_dgamma, dgamma, dbeta, s));
+}
+
+are_status are_embedding_ar(const void* ids, int index_format, const are_bf16* const table[], float scale, are_bf16* out,
+                            int R, int64_t M, int64_t N, int64_t V, are_ws* ws, void* stream) {
+    if (!ws || !table) return ARE_EINVAL;
+    are_status st = are_supports(ARE_OP_EMBEDDING_AR, R, M, N, V);
+    if (st != ARE_OK) return st;
+    if (!index_format_ok(index_format) || !index_ptr_ok(ids, index_format, M) || !std::isfinite(scale) || !ptr_ok(out, M * N))
+        return ARE_EINVAL;
+    for (int r = 0; r < R; ++r)
+        if (!ptr_ok(table[r], V * N)) return ARE_EINVAL;
+    TryLock lk(ws->mu);
+    if (!lk.ok) return ARE_EBUSY;
+    if (!on_device(ws)) return ARE_EINVAL;
+    if (R > ws->caps.R_max) return ARE_ECAPACITY;
+    ws->last = are_launch_info{};
+    if (M == 0 || N == 0) return ARE_OK;
+    EmbedParams p{};
+    embed_common(p, ids, index_format, scale, table, R, M, N, V);
+    p.out = out;
+    int grid = 0;
+    const cudaError_t e = launch_embedding(p, &grid, reinterpret_cast<cudaStream_t>(stream));
+    ws->last = are_launch_info{ARE_KERNEL_EMBEDDING, grid, 128, 1, 0, 0, 0, 0};
+    return from_cuda(e);
+}
+
+are_status are_embedding_ar_backward(const void* ids, int index_format, const are_bf16* dy, float scale, int accumulate,
+                                     are_bf16* const dtable[], int R, int64_t M, int64_t N, int64_t V, are_ws* ws,
+                                     void* stream) {
+    if (!ws || !dtable) return ARE_EINVAL;
+    are_status st = are_supports(ARE_OP_EMBEDDING_AR_BACKWARD, R, M, N, V);
+    if (st != ARE_OK) return st;
+    if (!index_format_ok(index_format) || !index_ptr_ok(ids, index_format, M) || !std::isfinite(scale) || !ptr_ok(dy, M * N))
+        return ARE_EINVAL;
+    for (int r = 0; r < R; ++r)
+        if (!ptr_ok(dtable[r], V * N)) return ARE_EINVAL;
+    TryLock lk(ws->mu);
+    if (!lk.ok) return ARE_EBUSY;
+    if (!on_device(ws)) return ARE_EINVAL;
+    if (R > ws->caps.R_max || M > ws->caps.M_max || N > ws->caps.N_max) return ARE_ECAPACITY;
+    ws->last = are_launch_info{};
+    if (N == 0 || (M == 0 && accumulate)) return ARE_OK;
+    if (!ws->embed_ready) {  // as prepare_rows
+        const cudaError_t e = embed_prepare();
+        if (e != cudaSuccess) return from_cuda(e);
+        ws->embed_ready = true;
+    }
+    EmbedParams p{};
+    embed_common(p, ids, index_format, scale, dtable, R, M, N, V);
+    p.dy = dy;
+    p.accumulate = accumulate != 0;
+    int grid = 0;
+    const cudaError_t e = launch_embedding_backward(p, ws->d_sort, ws->d_dgamma, ws->num_sms, &grid,
+                                                    reinterpret_cast<cudaStream_t>(stream));
+    ws->last = are_launch_info{ARE_KERNEL_EMBEDDING_BACKWARD, grid, 1024, 1, 0, 0, 0, 0};
+    return from_cuda(e);
 }
 
 are_status are_gemm_cross_entropy(const are_bf16* h, const are_bf16* const w[], const void* targets, int index_format,

@@ -240,6 +240,35 @@ struct GemmParams {
     uint64_t timeout_ns;
 };
 
+// ------------------------------------------------------------------ embedding (embedding.cu)
+struct EmbedParams {
+    uint16_t* tables[kMaxRanks];  // bf16 [Vs, N]: the tables (forward, read only) or their gradients
+    const void* ids;              // [M]
+    const uint16_t* dy;           // backward: bf16 [M, N]
+    uint16_t* out;                // forward: bf16 [M, N]
+    int64_t M;
+    int N, R;
+    uint32_t Vs, V;               // rows of a rank, of all ranks
+    int wide;                     // ids of 64 bits
+    int accumulate;
+    float scale;
+    // backward, set at the launch
+    uint32_t* keys[2];            // ids, and the tokens' positions, between the passes of the sort
+    uint32_t* idx[2];
+    const uint32_t* sorted;       // after the last pass
+    const uint32_t* order;
+    int passes, digit_bits;
+    int64_t chunk, chunks;        // sorted tokens of a chunk
+    int width, block_chunks;      // 8-column packs of a row that a block takes; chunks it takes
+    float* part;                  // [2 chunks, N]
+};
+
+cudaError_t embed_prepare();
+size_t embed_sort_bytes(int64_t M_max);
+cudaError_t launch_embedding(const EmbedParams& p, int* grid, cudaStream_t stream);
+// sort: embed_sort_bytes(M); scratch: norm_backward_scratch_words(N, num_sms) floats.
+cudaError_t launch_embedding_backward(EmbedParams& p, void* sort, float* scratch, int num_sms, int* grid, cudaStream_t stream);
+
 // ------------------------------------------------------------------ cross entropy (cross_entropy.cu)
 enum XentPass : int { kXentLogSum = 0, kXentDLogits = 1, kXentDH = 2, kXentDW = 3 };
 

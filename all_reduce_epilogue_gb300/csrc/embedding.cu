@@ -1,0 +1,381 @@
+// Lookup in an embedding table whose vocabulary is split over R ranks, and its gradient.
+//
+//   out_i    = scale * table[id_i]                      (0 where id_i is outside the vocabulary)
+//   dtable_v = scale * sum_{i : id_i = v} dy_i          (every row of every rank is written)
+//
+// In a tensor-parallel model each rank looks up the tokens of its own rows, has zeros for the
+// others, and the all-reduce adds R partials of which one is not zero: on one GPU that sum is
+// the row itself, read from the rank that has it.
+//
+// Both are bound by memory: forward 4 bytes an output element, backward 2 for dy and 2 for
+// each element of the tables, most of which are zeros.  The gradient's sums go by the tokens
+// sorted by (id, position): a token's rows meet in fp32 in the order of their positions, whatever
+// the hardware's order is.
+//   1. One block sorts the ids, stable, 9 or 10 bits a pass (a warp ranks its own run of tokens
+//      by matching digits, counters per warp and digit keep the order), in shared memory for up
+//      to 16384 tokens, in runs of that for more; all other blocks write the tables' zeros
+//      meanwhile, which takes longer.
+//   2. The sorted tokens are cut into chunks of equal length, whatever the ids: a token that makes
+//      up a tenth of a batch is then work for a tenth of the chunks.  A chunk's sums that do not
+//      reach its ends are results; the others are partial rows.
+//   3. The partial rows of an id are added in order.
+// Rows that tokens touch are written twice, first with zeros: knowing them in step 1 would mean
+// that the zeros wait for the sort.
+#include <algorithm>
+
+#include "rows.cuh"
+
+namespace are {
+namespace {
+
+constexpr int kSortThreads = 1024, kSortWarps = 32;
+constexpr int kRun = 16384;           // tokens sorted at once
+constexpr int kItems = kRun / kSortThreads;
+constexpr int kMaxBins = 1024;
+constexpr size_t kSortSmem = (size_t)kRun * 8 + (size_t)kSortWarps * kMaxBins * 2 + 2 * kMaxBins * 4 + 64 * 4;
+static_assert(kSortSmem <= kRowsSmemLimit, "shared memory budget");
+constexpr int kThreads = 128;
+
+__device__ __forceinline__ uint32_t id_of(const EmbedParams& p, int64_t i) {
+    const int64_t v = p.wide ? static_cast<const int64_t*>(p.ids)[i] : static_cast<const int32_t*>(p.ids)[i];
+    return v >= 0 && v < p.V ? (uint32_t)v : p.V;  // V: none
+}
+
+__device__ __forceinline__ uint16_t* row_of(uint16_t* const* tables, uint32_t id, const EmbedParams& p) {
+    const uint32_t r = id / p.Vs;
+    return tables[r] + (size_t)(id - r * p.Vs) * p.N;
+}
+
+// ---------------------------------------------------------------------- forward
+// A thread takes up to four packs of 8 columns, a block's threads consecutive ones of one or more rows.
+__global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__ EmbedParams p) {
+    const int P = p.N >> 3;
+    const int64_t at = (int64_t)blockIdx.x * (kThreads * 4), row0 = at / P;
+    const int in0 = (int)(at - row0 * P);
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
+    uint4 v[4];
+    int64_t row[4];
+    int col[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t i = (uint32_t)in0 + j * kThreads + threadIdx.x, r = i / (uint32_t)P;
+        row[j] = row0 + r;
+        col[j] = (int)(i - r * P) * 8;
+        v[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (row[j] < p.M) {
+            const uint32_t id = id_of(p, row[j]);
+            if (id < p.V) v[j] = *reinterpret_cast<const uint4*>(row_of(p.tables, id, p) + col[j]);
+        }
+    }
+    const uint64_t scale = pair(p.scale, p.scale);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (row[j] < p.M) {
+            if (p.scale != 1.f) {
+                Pack f;
+                unpack8(v[j], f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], scale);
+                v[j] = pack8(f);
+            }
+            *reinterpret_cast<uint4*>(p.out + row[j] * p.N + col[j]) = v[j];
+        }
+    }
+}
+
+// ------------------------------------------------------------------------- sort
+// Exclusive sum over the block's threads; `warps` holds 32 words.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warps) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // (the words' last readers are done)
+    if (lane == 31) warps[w] = x;
+    __syncthreads();
+    if (w == 0) {
+        uint32_t s = warps[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+            if (lane >= o) s += y;
+        }
+        warps[lane] = s;
+    }
+    __syncthreads();
+    return x - v + (w ? warps[w - 1] : 0u);
+}
+
+__device__ __forceinline__ void sort_tokens(const EmbedParams& p, uint8_t* smem) {
+    uint32_t* skey = reinterpret_cast<uint32_t*>(smem);
+    uint32_t* sidx = skey + kRun;
+    uint16_t* count = reinterpret_cast<uint16_t*>(sidx + kRun);          // [warp][bin]
+    uint32_t* local = reinterpret_cast<uint32_t*>(count + kSortWarps * kMaxBins);  // a bin's first place in the run
+    uint32_t* global = local + kMaxBins;                                 // and in the whole order
+    uint32_t* scan = global + kMaxBins;
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    const int M = (int)p.M, bins = 1 << p.digit_bits;
+    const bool one = M <= kRun;
+    uint16_t* mine = count + w * bins;
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * p.digit_bits;
+        const uint32_t mask = bins - 1;
+        const uint32_t *from_key = p.keys[(pass & 1) ^ 1], *from_idx = p.idx[(pass & 1) ^ 1];
+        uint32_t *to_key = p.keys[pass & 1], *to_idx = p.idx[pass & 1];
+        if (!one) {
+            for (int b = t; b < bins; b += kSortThreads) global[b] = 0;
+            __syncthreads();
+            for (int i = t; i < M; i += kSortThreads)
+                atomicAdd(&global[((pass == 0 ? id_of(p, i) : from_key[i]) >> shift) & mask], 1u);
+            __syncthreads();
+            const uint32_t n = t < bins ? global[t] : 0u, first = block_scan(n, scan);
+            if (t < bins) global[t] = first;
+        }
+        for (int c0 = 0; c0 < M; c0 += kRun) {
+            const int n = min(kRun, M - c0), per = (n + kSortThreads - 1) / kSortThreads;  // items of a thread
+            for (int i = t; i < kSortWarps * bins / 2; i += kSortThreads) reinterpret_cast<uint32_t*>(count)[i] = 0;
+            __syncthreads();
+            // a warp has a run of per * 32 items, in their order; an item's place among the warp's of its digit
+            uint32_t key[kItems], idx[kItems], place[kItems / 2];
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) {
+                if (j < per) {
+                    const int i = w * per * 32 + j * 32 + lane;
+                    const bool in = i < n;
+                    key[j] = !in ? 0u : pass == 0 ? id_of(p, c0 + i) : one ? skey[i] : from_key[c0 + i];
+                    idx[j] = !in ? 0u : pass == 0 ? (uint32_t)(c0 + i) : one ? sidx[i] : from_idx[c0 + i];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) {
+                if (j < per) {
+                    const bool in = w * per * 32 + j * 32 + lane < n;
+                    const uint32_t d = in ? (key[j] >> shift) & mask : 0xFFFFFFFFu;
+                    const uint32_t same = __match_any_sync(0xFFFFFFFFu, d);
+                    const int leader = __ffs(same) - 1;
+                    uint32_t before = 0;
+                    if (lane == leader && in) {
+                        before = mine[d];
+                        mine[d] = (uint16_t)(before + __popc(same));
+                    }
+                    before = __shfl_sync(0xFFFFFFFFu, before, leader) + __popc(same & ((1u << lane) - 1u));
+                    if (j & 1) place[j / 2] |= before << 16;
+                    else place[j / 2] = before;
+                    __syncwarp();
+                }
+            }
+            __syncthreads();
+            uint32_t total = 0;
+            if (t < bins) {
+#pragma unroll 8
+                for (int v = 0; v < kSortWarps; ++v) {
+                    const uint32_t x = count[v * bins + t];
+                    count[v * bins + t] = (uint16_t)total;
+                    total += x;
+                }
+            }
+            const uint32_t first = block_scan(total, scan);
+            if (t < bins) local[t] = first;
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) {
+                if (j < per && w * per * 32 + j * 32 + lane < n) {
+                    const uint32_t d = (key[j] >> shift) & mask;
+                    const uint32_t to = local[d] + mine[d] + ((place[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
+                    skey[to] = key[j];
+                    sidx[to] = idx[j];
+                }
+            }
+            __syncthreads();
+            if (!one || pass == p.passes - 1) {
+                for (int i = t; i < n; i += kSortThreads) {
+                    const uint32_t k = skey[i], d = (k >> shift) & mask;
+                    const uint32_t to = one ? (uint32_t)i : global[d] + (i - local[d]);
+                    to_key[to] = k;
+                    to_idx[to] = sidx[i];
+                }
+                __syncthreads();
+                if (!one && t < bins) global[t] += total;
+            }
+        }
+        __syncthreads();  // global memory of this pass, too, is the next pass's input
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __grid_constant__ EmbedParams p) {
+    extern __shared__ __align__(128) uint8_t sort_smem[];
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
+    if (blockIdx.x == 0 && p.M > 0) {
+        sort_tokens(p, sort_smem);
+        return;
+    }
+    const int skip = p.M > 0 ? 1 : 0;
+    const int64_t packs = (int64_t)p.Vs * (p.N >> 3), step = (int64_t)(gridDim.x - skip) * kSortThreads;
+    const int64_t i0 = (int64_t)(blockIdx.x - skip) * kSortThreads + threadIdx.x;
+    for (int r = 0; r < p.R; ++r) {
+        uint4* to = reinterpret_cast<uint4*>(p.tables[r]);
+        for (int64_t i = i0; i < packs; i += step) to[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// ------------------------------------------------------------------------- sums
+// A thread's place: which chunk, which 8 columns.  Rows narrower than the block leave room for several chunks.
+struct Where {
+    int64_t chunk;
+    int pack;
+};
+__device__ __forceinline__ Where where(const EmbedParams& p) {
+    const int sub = threadIdx.x / p.width;
+    Where x{(int64_t)blockIdx.x * p.block_chunks + sub, (int)(blockIdx.y * p.width + threadIdx.x - sub * p.width)};
+    if (sub >= p.block_chunks || x.chunk >= p.chunks || x.pack >= p.N >> 3) x.pack = -1;
+    return x;
+}
+
+__device__ __forceinline__ void store_row(const EmbedParams& p, uint32_t id, int pack, const Pack& sum) {
+    uint4* to = reinterpret_cast<uint4*>(row_of(p.tables, id, p)) + pack;
+    const uint64_t scale = pair(p.scale, p.scale);
+    Pack f = {};
+    if (p.accumulate) unpack8(*to, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = fma2(sum[i], scale, f[i]);
+    *to = pack8(f);
+}
+
+__device__ __forceinline__ void store_part(const EmbedParams& p, int64_t row, int pack, const Pack& sum) {
+    uint64_t* to = reinterpret_cast<uint64_t*>(p.part + row * p.N + pack * 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = sum[i];
+}
+
+// Partial rows: 2c, the sum that goes on from the chunk before c; 2c + 1, the one that starts in c and goes on behind.
+__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_constant__ EmbedParams p) {
+    const Where x = where(p);
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
+    if (x.pack < 0) return;
+    constexpr int U = 8;  // rows in flight
+    const int first = (int)(x.chunk * p.chunk), end = (int)min((int64_t)first + p.chunk, p.M);
+    const uint32_t prev = first > 0 ? p.sorted[first - 1] : p.V, next = end < p.M ? p.sorted[end] : p.V;
+    Pack sum = {};
+    uint32_t cur = p.V;
+    bool started = false;  // the current sum starts in this chunk
+    for (int i0 = first; i0 < end; i0 += U) {
+        uint32_t key[U];
+        uint4 v[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) key[j] = i0 + j < end ? p.sorted[i0 + j] : p.V;
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (key[j] < p.V) v[j] = ptx::ld_stream_v4(p.dy + (size_t)p.order[i0 + j] * p.N + x.pack * 8);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (key[j] >= p.V) continue;
+            if (key[j] != cur) {
+                if (cur < p.V) {
+                    if (started) store_row(p, cur, x.pack, sum);
+                    else store_part(p, 2 * x.chunk, x.pack, sum);
+                }
+                started = i0 + j > first || key[j] != prev;
+                cur = key[j];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = 0ull;
+            }
+            Pack f;
+            unpack8(v[j], f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = add2(sum[i], f[i]);
+        }
+    }
+    if (cur < p.V) {
+        if (!started) store_part(p, 2 * x.chunk, x.pack, sum);
+        else if (cur == next) store_part(p, 2 * x.chunk + 1, x.pack, sum);
+        else store_row(p, cur, x.pack, sum);
+    }
+}
+
+// An id that crosses chunks: its sum starts in the chunk that this thread has, and goes on through the next ones.
+__global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ EmbedParams p) {
+    const Where x = where(p);
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
+    if (x.pack < 0) return;
+    const int64_t first = x.chunk * p.chunk, end = first + p.chunk;
+    if (end >= p.M) return;
+    const uint32_t id = p.sorted[end - 1];
+    if (id >= p.V || p.sorted[end] != id || (first > 0 && p.sorted[first - 1] == id)) return;
+    Pack sum;
+    load8(p.part + (2 * x.chunk + 1) * p.N + x.pack * 8, sum);
+    constexpr int U = 4;
+    bool more = true;
+    for (int64_t c = x.chunk + 1; more; c += U) {
+        Pack v[U];
+        bool in[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            in[j] = (c + j) * p.chunk < p.M && p.sorted[(c + j) * p.chunk] == id;
+            if (in[j]) load8(p.part + 2 * (c + j) * p.N + x.pack * 8, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (!in[j]) {
+                more = false;
+                break;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = add2(sum[i], v[j][i]);
+        }
+    }
+    store_row(p, id, x.pack, sum);
+}
+
+}  // namespace
+
+cudaError_t embed_prepare() { return cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem); }
+
+size_t embed_sort_bytes(int64_t M_max) { return (size_t)M_max * 16; }
+
+cudaError_t launch_embedding(const EmbedParams& p, int* grid, cudaStream_t s) {
+    const int64_t packs = p.M * (p.N / 8), blocks = (packs + kThreads * 4 - 1) / (kThreads * 4);
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    *grid = (int)blocks;
+    return launch_dependent(embed_kernel, dim3((unsigned)blocks), kThreads, 0, s, p);
+}
+
+cudaError_t launch_embedding_backward(EmbedParams& p, void* sort, float* scratch, int num_sms, int* grid, cudaStream_t s) {
+    // passes of equal length, of 10 bits at most; V itself stands for "no id"
+    int bits = 1;
+    while (bits < 32 && (p.V >> bits)) ++bits;
+    p.passes = (bits + 9) / 10;
+    p.digit_bits = (bits + p.passes - 1) / p.passes;
+    uint32_t* words = static_cast<uint32_t*>(sort);
+    for (int i = 0; i < 2; ++i) {
+        p.keys[i] = words + (2 * i) * p.M;
+        p.idx[i] = words + (2 * i + 1) * p.M;
+    }
+    p.sorted = p.keys[(p.passes - 1) & 1];
+    p.order = p.idx[(p.passes - 1) & 1];
+    p.part = scratch;
+    // two partial rows a chunk; what a workspace of this width has, so that the order of the sums goes by the sizes alone
+    const int64_t rows = (int64_t)norm_backward_scratch_words(p.N, num_sms) / p.N;
+    p.chunk = std::max<int64_t>(8, (p.M + rows / 2 - 1) / (rows / 2));
+    p.chunks = (p.M + p.chunk - 1) / p.chunk;
+    *grid = p.accumulate ? 1 : num_sms;
+    cudaError_t e = launch_dependent(embed_sort_kernel, dim3((unsigned)*grid), kSortThreads, kSortSmem, s, p);
+    if (e != cudaSuccess || p.M == 0) return e;
+    // a row's packs over blocks of equal width, or several chunks in a block
+    const int P = p.N / 8, slabs = (P + kThreads - 1) / kThreads;
+    p.width = (P + slabs - 1) / slabs;
+    p.block_chunks = kThreads / p.width;
+    const int threads = (p.width * p.block_chunks + 31) / 32 * 32;
+    const dim3 blocks((unsigned)((p.chunks + p.block_chunks - 1) / p.block_chunks), (unsigned)slabs);
+    e = launch_dependent(embed_sum_kernel, blocks, threads, 0, s, p);
+    if (e == cudaSuccess && p.chunks > 1) e = launch_dependent(embed_join_kernel, blocks, threads, 0, s, p);
+    return e;
+}
+
+}  // namespace are

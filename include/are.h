@@ -44,7 +44,8 @@
  *    are_allreduce_rmsnorm_quant, are_allreduce_rmsnorm_quant_groups,
  *    are_allreduce_rmsnorm_backward, are_allreduce_layernorm,
  *    are_allreduce_layernorm_backward, are_gemm_cross_entropy,
- *    are_gemm_cross_entropy_backward, are_gemm_ar_qweight and
+ *    are_gemm_cross_entropy_backward, are_embedding_ar,
+ *    are_embedding_ar_backward, are_gemm_ar_qweight and
  *    are_gemm_ar_qweight_qx may be captured into a CUDA graph once
  *    their workspace exists: they only enqueue work on `stream` (kernels;
  *    memsets for an empty contraction), and the state they leave for the next call
@@ -52,7 +53,7 @@
  *    kernels, never by a host step, so every replay finds it as the capture
  *    did.  Workspace creation, reset and snapshots are not capturable.
  *  - are_allreduce_rmsnorm_quant_groups, are_allreduce_rmsnorm_backward, the
- *    LayerNorm calls and the 4-bit linears launch with programmatic stream
+ *    LayerNorm and embedding calls and the 4-bit linears launch with programmatic stream
  *    serialisation: their
  *    kernels may come up while earlier work of the stream still runs, and
  *    read and write no memory of the caller's before all of it has ended.
@@ -113,7 +114,9 @@ typedef enum are_op {
     ARE_OP_GEMM_AR_QWEIGHT = 5,
     ARE_OP_ALLREDUCE_LAYERNORM = 6,
     ARE_OP_ALLREDUCE_LAYERNORM_BACKWARD = 7,
-    ARE_OP_GEMM_CROSS_ENTROPY = 8
+    ARE_OP_GEMM_CROSS_ENTROPY = 8,
+    ARE_OP_EMBEDDING_AR = 9,
+    ARE_OP_EMBEDDING_AR_BACKWARD = 10
 } are_op;
 
 /* Workspace capacities.  Buffers are sized from these once, at creation, so
@@ -204,7 +207,9 @@ typedef enum are_kernel {
     ARE_KERNEL_LAYERNORM_ROWS = 9,     /* AR+LayerNorm */
     ARE_KERNEL_LAYERNORM_BACKWARD_ROWS = 10, /* AR+LayerNorm backward */
     ARE_KERNEL_CROSS_ENTROPY = 11,           /* cross entropy: the first of its kernels */
-    ARE_KERNEL_CROSS_ENTROPY_BACKWARD = 12
+    ARE_KERNEL_CROSS_ENTROPY_BACKWARD = 12,
+    ARE_KERNEL_EMBEDDING = 13,
+    ARE_KERNEL_EMBEDDING_BACKWARD = 14       /* the first of its kernels */
 } are_kernel;
 
 typedef struct are_launch_info {
@@ -249,13 +254,16 @@ ARE_API const char* are_status_string(are_status s);
  *           states): 1 <= R <= 8; K >= 8, K % 8 == 0; N >= 1;
  *           R * ceil(N / 256) < 2^21, ceil(M / 256) * R * ceil(N / 256) and
  *           ceil(K / 256) * max(ceil(M / 256), R * ceil(N / 256)) < 2^30.
+ *  EMBEDDING_AR, EMBEDDING_AR_BACKWARD (N: width of a row, K: rows of one rank's
+ *           table): 1 <= R <= 8; N % 8 == 0 and N <= 32768; K >= 1, R * K < 2^31;
+ *           M <= 2^30.
  * K is ignored for the ALLREDUCE operations.  Pure host function: no device needed. */
 ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
 
 /* Create a workspace on the current CUDA device: tile masks, the per-rank
  * partial buffer, the Lamport staging buffer (filled with the sentinel, on a
  * private stream, synchronously), partial sums of dgamma, 2 MiB a rank of
- * staged tokens for the 4-bit linear, with vocab_piece > 0 the cross entropy's
+ * staged tokens for the 4-bit linear, 16 * M_max bytes of sorted tokens, with vocab_piece > 0 the cross entropy's
  * buffers (M_max * (2 * vocab_piece + 4 * K_max + 12) bytes and up to 20 MB), and
  * the device status word.
  * ROCm/mori PR #662, review threads: every capacity is validated before the
@@ -589,6 +597,38 @@ typedef enum are_index_format {
     ARE_INDEX_I32 = 0,
     ARE_INDEX_I64 = 1
 } are_index_format;
+
+/*
+ * Lookup in an embedding table whose vocabulary is split over the ranks,
+ * all-reduced: a rank contributes the rows that it has, and zeros (the pages'
+ * layers start behind it).
+ *  ids     : [M] indices, are_index_format, aligned to its element; an index
+ *            outside 0..R*V-1 (a padded position's -1, say) has a row of zeros
+ *  table[r]: bf16 [V, N], rank r's rows: index r * V + v
+ *  scale   : finite
+ *  out     : bf16 [M, N]
+ *  Result  : out_i = bf16( f32(row of ids_i) * scale ).
+ * Needs no capacity of the workspace but R <= R_max.
+ */
+ARE_API are_status are_embedding_ar(const void* ids, int index_format, const are_bf16* const table[], float scale,
+                                    are_bf16* out, int R, int64_t M, int64_t N, int64_t V, are_ws* ws, void* stream);
+
+/*
+ * Its gradient, by sorted tokens.
+ *  dy       : bf16 [M, N], the gradient of out
+ *  dtable[r]: bf16 [V, N] for every rank
+ *  accumulate: 0: every row is written, with zeros where no token has it; 1: the
+ *             rows that tokens have are added to, the others are left alone (a
+ *             table tied to an output layer whose gradient dtable holds already)
+ *  Result   : s_v = sum over the i with ids_i = v of f32(dy_i), in fp32, in an
+ *             order that depends on the ids, M, N and the device's SM count alone;
+ *             dtable_v = bf16( s_v * scale ), accumulating bf16( s_v * scale + f32(dtable_v) ).
+ * The tables must not overlap one another, dy or ids.  Needs M <= M_max,
+ * N <= N_max, R <= R_max.
+ */
+ARE_API are_status are_embedding_ar_backward(const void* ids, int index_format, const are_bf16* dy, float scale,
+                                             int accumulate, are_bf16* const dtable[], int R, int64_t M, int64_t N,
+                                             int64_t V, are_ws* ws, void* stream);
 
 /*
  * Softmax cross entropy of an output layer whose vocabulary is split over the

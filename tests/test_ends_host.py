@@ -1,4 +1,4 @@
-"""Refusals of LayerNorm that need no GPU: the predicate, and the
+"""Refusals of LayerNorm, the embedding and the cross entropy that need no GPU: the predicate, and the
 entry points' argument checks before any device access."""
 import ctypes
 import os
@@ -27,6 +27,21 @@ def lib():
     ((are.OP_ALLREDUCE_LAYERNORM_BACKWARD, 8, 0, 16384, 0), True),
     ((are.OP_ALLREDUCE_LAYERNORM_BACKWARD, 1, 1, 16392, 0), False),
     ((are.OP_ALLREDUCE_LAYERNORM_BACKWARD, 1, -1, 64, 0), False),
+    ((are.OP_GEMM_CROSS_ENTROPY, 8, 4096, 8191, 4096), True),
+    ((are.OP_GEMM_CROSS_ENTROPY, 1, 0, 1, 8), True),
+    ((are.OP_GEMM_CROSS_ENTROPY, 1, 1, 0, 8), False),               # an empty vocabulary
+    ((are.OP_GEMM_CROSS_ENTROPY, 1, 1, 8, 0), False),
+    ((are.OP_GEMM_CROSS_ENTROPY, 1, 1, 8, 12), False),              # K % 8
+    ((are.OP_GEMM_CROSS_ENTROPY, 9, 1, 8, 8), False),
+    ((are.OP_GEMM_CROSS_ENTROPY, 8, 1, 1 << 26, 8), False),         # 2^21 tiles of the vocabulary
+    ((are.OP_GEMM_CROSS_ENTROPY, 1, 1 << 30, 1 << 18, 8), False),   # tiles past 2^30
+    ((are.OP_EMBEDDING_AR, 8, 0, 32768, 1), True),
+    ((are.OP_EMBEDDING_AR, 1, 1, 32776, 1), False),
+    ((are.OP_EMBEDDING_AR, 1, 1, 12, 1), False),
+    ((are.OP_EMBEDDING_AR, 1, 1, 64, 0), False),
+    ((are.OP_EMBEDDING_AR, 8, 1, 64, 1 << 28), False),              # R * V past 31 bits
+    ((are.OP_EMBEDDING_AR_BACKWARD, 8, 1 << 30, 64, (1 << 28) - 1), True),
+    ((are.OP_EMBEDDING_AR_BACKWARD, 1, (1 << 30) + 1, 64, 1), False),
 ])
 def test_supports(lib, args, ok):
     assert (lib.are_supports(*args) == are.OK) == ok
@@ -36,6 +51,10 @@ def test_null_workspace(lib):
     A, f = (vp * 2)(16, 32), ctypes.c_float(1e-6)
     assert lib.are_allreduce_layernorm(A, None, 16, None, f, 16, None, 2, 4, 64, None, None) == are.EINVAL
     assert lib.are_allreduce_layernorm_backward(A, 16, 16, f, None, 16, 16, 16, 2, 4, 64, None, None) == are.EINVAL
+    assert lib.are_gemm_cross_entropy(16, A, 16, 0, 8, 16, 16, 2, 4, 8, 64, None, None) == are.EINVAL
+    assert lib.are_gemm_cross_entropy_backward(16, A, 16, 0, 8, 16, 16, 16, A, 2, 4, 8, 64, None, None) == are.EINVAL
+    assert lib.are_embedding_ar(16, 0, A, f, 16, 2, 4, 64, 8, None, None) == are.EINVAL
+    assert lib.are_embedding_ar_backward(16, 0, 16, f, 0, A, 2, 4, 64, 8, None, None) == are.EINVAL
 
 
 def test_binding_refuses_host_tensors(lib):
@@ -46,9 +65,18 @@ def test_binding_refuses_host_tensors(lib):
         are.allreduce_layernorm([x], None, g, g, 1e-6, x, ws)
     with pytest.raises(ValueError):
         are.allreduce_layernorm_backward([x], x, g, 1e-6, x, g, g, ws)
+    ids, f = torch.zeros(2, dtype=torch.int64), torch.zeros(2)
+    with pytest.raises(ValueError):
+        are.gemm_cross_entropy(x, [x], ids, f, f, ws)
+    with pytest.raises(ValueError):
+        are.gemm_cross_entropy_backward(x, [x], ids, f, f, x, [x], ws)
+    with pytest.raises(ValueError):
+        are.embedding_ar(ids, [x], x, ws)
+    with pytest.raises(ValueError):
+        are.embedding_ar_backward(ids, x, [x], ws)
 
 
-@pytest.mark.parametrize("source", ["rows.cuh", "layernorm.cu"])
+@pytest.mark.parametrize("source", ["rows.cuh", "layernorm.cu", "embedding.cu"])
 def test_no_non_coherent_loads_under_programmatic_launch(source):
     """These kernels may start before the kernel that writes their operands has ended; a non-coherent load wants memory
     that is read-only for the whole life of the kernel, which begins before the wait."""
