@@ -287,6 +287,7 @@ struct XentParams {
     int wide;                     // targets of 64 bits
     int rank_tiles, tile0;        // vocabulary tiles of a rank; the piece's first
     int tiles_m, tiles_n, splits, num_kb;
+    int a_rows;                   // rows of A that a copy takes: 128, fewer if M is less
     int group;                    // rows of tiles taken together
     int units;                    // (set at the launch)
     int sums, add;                // kXentDH: fp32 sums, added to what is there

@@ -209,6 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
             const Tile t = tile_of(p, u);
             const Place at = place_of(p, PASS == kXentDW ? t.tm : t.tn);
             const int a0 = t.tm * kTile + q * 128, b0 = t.tn * kTile + q * 128;
+            // rows of A behind the last one are not loaded: whatever the buffers hold, it enters no other row's sums
+            const bool has_a = a_across(PASS) || a0 < p.M, both_a = a_across(PASS) || t.tm * kTile + 128 < p.M;
+            const uint32_t a_bytes = a_across(PASS) ? kHalf : (uint32_t)p.a_rows * 128;
             for (int kb = t.kb0; kb < t.kb1; ++kb) {
                 const bool ok = wait(&empty[stage], ph ^ 1u, abort_flag, p, 30, u);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -218,14 +221,14 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                 if (issuer) {
                     // both CTAs' copies complete on the leader's barrier
                     const uint32_t fb = ptx::mapa_shared(ptx::smem_u32(&full[stage]), 0);
-                    if (q == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+                    if (q == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kHalf + (both_a ? 2 * a_bytes : a_bytes));
                     uint8_t *a = sA + stage * kHalf, *b = sB + stage * kHalf;
                     const int k = kb * 64;
                     if (PASS == kXentLogSum || PASS == kXentDLogits) {
-                        ptx::tma_load_2d_pair(a, &p.tmA, fb, k, a0, pol);
+                        if (has_a) ptx::tma_load_2d_pair(a, &p.tmA, fb, k, a0, pol);
                         ptx::tma_load_2d_pair(b, &p.tmW[at.rank], fb, k, at.col + q * 128, pol);
                     } else if (PASS == kXentDH) {
-                        ptx::tma_load_2d_pair(a, &p.tmA, fb, k, a0, pol);
+                        if (has_a) ptx::tma_load_2d_pair(a, &p.tmA, fb, k, a0, pol);
                         const Place w = place_of(p, kb >> 2);
                         const int v = w.col + (kb & 3) * 64;
                         for (int i = 0; i < 2; ++i)
@@ -581,12 +584,14 @@ static void common(XentParams& p, const XentCall& c, const XentBuffers& b) {
     p.timeout_ns = b.timeout_ns;
     p.splits = 1;
     p.group = kGroup;
+    p.a_rows = 8;
+    while (p.a_rows < 128 && p.a_rows < c.M) p.a_rows *= 2;
 }
 
 cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStream_t s, int* grid) {
     XentParams p{};
     common(p, c, b);
-    cudaError_t e = make_tmap_bf16(&p.tmA, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, 128);
+    cudaError_t e = make_tmap_bf16(&p.tmA, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, p.a_rows);
     for (int r = 0; r < c.R && e == cudaSuccess; ++r)
         e = make_tmap_bf16(&p.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 128);
     if (e != cudaSuccess) return e;
@@ -622,7 +627,7 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
     const int most = (int)std::min<int64_t>(total, (int64_t)(b.sizes.d_bytes / ((size_t)c.M * kTile * 2)));
     const int even = (total + most - 1) / most, piece = (total + even - 1) / even;
     const int pieces = (total + piece - 1) / piece, left = total - (pieces - 1) * piece;  // the last piece's tiles, 1..piece
-    cudaError_t e = make_tmap_bf16(&z.tmA, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, 128);
+    cudaError_t e = make_tmap_bf16(&z.tmA, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, z.a_rows);
     for (int r = 0; r < c.R && e == cudaSuccess; ++r) {
         e = make_tmap_bf16(&z.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 128);
         if (e == cudaSuccess && c.dh) e = make_tmap_bf16(&dh.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 64);
@@ -647,7 +652,7 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
         const uint64_t cols = (uint64_t)n * kTile;
         if (t0 == 0 || n != piece) {  // the piece's d [M, cols]: as an output, along and across the contraction
             e = make_tmap_bf16(&z.tmOut[0], b.d, cols, (uint64_t)c.M, 64, 32);
-            if (e == cudaSuccess) e = make_tmap_bf16(&dh.tmA, b.d, cols, (uint64_t)c.M, 64, 128);
+            if (e == cudaSuccess) e = make_tmap_bf16(&dh.tmA, b.d, cols, (uint64_t)c.M, 64, dh.a_rows);
             if (e == cudaSuccess) e = make_tmap_bf16(&dw.tmA, b.d, cols, (uint64_t)c.M, 64, 64);
         }
         if (e == cudaSuccess) e = launch<kXentDLogits>(z, b.clusters, s);
