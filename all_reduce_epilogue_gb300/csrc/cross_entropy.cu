@@ -35,8 +35,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "are_internal.h"
-#include "ptx.cuh"
+#include "rows.cuh"
 
 namespace are {
 namespace {
@@ -197,6 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
     ptx::cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();  // nothing of the caller's or of the buffers is touched before
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer (both CTAs)
@@ -476,6 +477,8 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2* stats, flo
                                                         const void* targets, int wide, int64_t vocab, float* loss, float* lse,
                                                         int M, int tiles, int first, int last) {
     const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
     if (row >= M) return;
     const float2* at = stats + (size_t)row * tiles;
     float top = -INFINITY, sum = 0.f;
@@ -512,11 +515,19 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2* stats, flo
 
 // dh = the splits' fp32 sums, in their order, rounded to bf16 once.
 __global__ void __launch_bounds__(256) xent_dh_kernel(const float4* sums, uint2* dh, int64_t quads, int splits) {
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
         float4 a = sums[i];
-        for (int s = 1; s < splits; ++s) {
-            const float4 b = sums[s * quads + i];
-            a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+        constexpr int U = 8;  // sets in flight
+        for (int s0 = 1; s0 < splits; s0 += U) {
+            float4 b[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (s0 + j < splits) b[j] = sums[(s0 + j) * quads + i];
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (s0 + j < splits) { a.x += b[j].x; a.y += b[j].y; a.z += b[j].z; a.w += b[j].w; }
         }
         dh[i] = make_uint2(bf16x2(a.x, a.y), bf16x2(a.z, a.w));
     }
@@ -525,17 +536,18 @@ __global__ void __launch_bounds__(256) xent_dh_kernel(const float4* sums, uint2*
 template <int PASS>
 cudaError_t launch(XentParams& p, int clusters, cudaStream_t s) {
     p.units = p.tiles_m * p.tiles_n * p.splits;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1] = dependent_launch();  // a CTA comes up on an SM that the kernel before has left
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)std::min(p.units, clusters));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, xent_kernel<PASS>, p);
 }
 
@@ -570,6 +582,18 @@ XentSizes xent_sizes(int64_t M_max, int64_t K_max, int64_t piece) {
     z.sum_bytes = (size_t)M_max * K_max * 4 + (size_t)std::min<int64_t>(M_max, kTile) * kTile * 4 * 80;
     z.row_bytes = (size_t)M_max * 12;
     return z;
+}
+
+// Sets of sums that dh's contraction over the vocabulary is split into, at most `most`.  Few tokens have few tiles, and
+// the pairs that would have none take parts of the contraction; with a few waves of tiles, two to four parts make the
+// last wave shorter (4096 tokens, K = 4096: 256 tiles are 3.4 waves of 76; in two parts 6.7: 170 -> 150 us a piece).
+static int dh_splits(int tiles, int clusters, int most) {
+    int best = std::max(1, std::min(clusters / tiles, most));
+    auto filled = [&](int s) { return (double)tiles * s / (((int64_t)tiles * s + clusters - 1) / clusters * clusters); };
+    if (tiles > clusters)
+        for (int s = 2; s <= std::min(4, most); ++s)
+            if (filled(s) > filled(best) + 0.04) best = s;
+    return best;
 }
 
 static void common(XentParams& p, const XentCall& c, const XentBuffers& b) {
@@ -607,10 +631,9 @@ cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStr
         e = launch<kXentLogSum>(p, b.clusters, s);
         if (p.tile0 == 0) *grid = 2 * std::min(p.units, b.clusters);
         if (e != cudaSuccess) return e;
-        xent_join_kernel<<<(unsigned)((c.M + 7) / 8), 256, 0, s>>>(p.stats, carry, p.target_logit, c.targets, c.wide, c.vocab,
-                                                                  c.loss, c.lse, (int)c.M, p.tiles_n, p.tile0 == 0,
-                                                                  p.tile0 + p.tiles_n == total);
-        e = cudaGetLastError();
+        e = launch_dependent(xent_join_kernel, dim3((unsigned)((c.M + 7) / 8)), 256, 0, s, p.stats, carry, p.target_logit,
+                             c.targets, c.wide, c.vocab, c.loss, c.lse, (int)c.M, p.tiles_n, p.tile0 == 0,
+                             p.tile0 + p.tiles_n == total);
     }
     return e;
 }
@@ -634,10 +657,9 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
         if (e == cudaSuccess && c.has_dw) e = make_tmap_bf16(&dw.tmOut[r], c.dw[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 32);
     }
     if (e == cudaSuccess && c.has_dw) e = make_tmap_bf16(&dw.tmB, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, 64);
-    // dh of few tokens has few tiles: the vocabulary is split over the pairs that would have none
-    const size_t set = (size_t)c.M * c.K * 4;
     dh.tiles_n = tiles_k;
-    dh.splits = std::max(1, std::min({b.clusters / (dh.tiles_m * tiles_k), (int)(b.sizes.sum_bytes / set), piece / 2, 4 * left}));
+    dh.splits = dh_splits(dh.tiles_m * tiles_k, b.clusters,
+                          (int)std::min({(int64_t)(b.sizes.sum_bytes / ((size_t)c.M * c.K * 4)), (int64_t)piece / 2, (int64_t)4 * left}));
     dh.sums = pieces > 1 || dh.splits > 1;
     if (e == cudaSuccess && c.dh)
         e = dh.sums ? make_tmap_f32_3d(&dh.tmOut[0], b.sums, (uint64_t)c.K, (uint64_t)c.M, (uint64_t)dh.splits, 32, 32)
@@ -663,9 +685,8 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
     }
     if (e == cudaSuccess && c.dh && dh.sums) {
         const int64_t quads = c.M * c.K / 4;
-        xent_dh_kernel<<<(unsigned)std::min<int64_t>((quads + 255) / 256, 152 * 8), 256, 0, s>>>(
-            static_cast<const float4*>(b.sums), reinterpret_cast<uint2*>(c.dh), quads, dh.splits);
-        e = cudaGetLastError();
+        e = launch_dependent(xent_dh_kernel, dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 16 * b.clusters)), 256, 0, s,
+                             static_cast<const float4*>(b.sums), reinterpret_cast<uint2*>(c.dh), quads, dh.splits);
     }
     return e;
 }

@@ -32,6 +32,7 @@ constexpr int kSortThreads = 1024, kSortWarps = 32;
 constexpr int kRun = 16384;           // tokens sorted at once
 constexpr int kItems = kRun / kSortThreads;
 constexpr int kMaxBins = 1024;
+constexpr int kRankMax = 512;         // tokens that are ranked by comparison
 constexpr size_t kSortSmem = (size_t)kRun * 8 + (size_t)kSortWarps * kMaxBins * 2 + 2 * kMaxBins * 4 + 64 * 4;
 static_assert(kSortSmem <= kRowsSmemLimit, "shared memory budget");
 constexpr int kThreads = 128;
@@ -206,12 +207,44 @@ __device__ __forceinline__ void sort_tokens(const EmbedParams& p, uint8_t* smem)
     }
 }
 
+// Few tokens: a token's place is the number of tokens before it in (id, position) order, counted over all of them by as
+// many threads a token as there are.
+__device__ __forceinline__ void rank_tokens(const EmbedParams& p, uint8_t* smem) {
+    uint32_t* key = reinterpret_cast<uint32_t*>(smem);
+    uint32_t* rank = key + kRankMax + 4;
+    const int t = threadIdx.x, M = (int)p.M, M4 = (M + 3) & ~3;
+    if (t < M4) {
+        key[t] = t < M ? id_of(p, t) : 0xFFFFFFFFu;
+        rank[t] = 0;
+    }
+    __syncthreads();
+    const int parts = kSortThreads / M, part = t / M, i = t - part * M;
+    if (part < parts) {
+        const int per = (M4 / 4 + parts - 1) / parts * 4, j0 = part * per, j1 = min(j0 + per, M4);
+        const uint32_t k = key[i];
+        uint32_t n = 0;
+        for (int j = j0; j < j1; j += 4) {
+            const uint4 o = *reinterpret_cast<const uint4*>(key + j);
+            n += (o.x < k || (o.x == k && j < i)) + (o.y < k || (o.y == k && j + 1 < i)) + (o.z < k || (o.z == k && j + 2 < i)) +
+                 (o.w < k || (o.w == k && j + 3 < i));
+        }
+        if (n) atomicAdd(&rank[i], n);
+    }
+    __syncthreads();
+    if (t < M) {
+        const uint32_t to = rank[t];
+        p.keys[0][to] = key[t];
+        p.idx[0][to] = t;
+    }
+}
+
 __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __grid_constant__ EmbedParams p) {
     extern __shared__ __align__(128) uint8_t sort_smem[];
     ptx::grid_launch_dependents();
     ptx::grid_wait();
     if (blockIdx.x == 0 && p.M > 0) {
-        sort_tokens(p, sort_smem);
+        if (p.passes == 0) rank_tokens(p, sort_smem);
+        else sort_tokens(p, sort_smem);
         return;
     }
     const int skip = p.M > 0 ? 1 : 0;
@@ -253,42 +286,59 @@ __device__ __forceinline__ void store_part(const EmbedParams& p, int64_t row, in
 }
 
 // Partial rows: 2c, the sum that goes on from the chunk before c; 2c + 1, the one that starts in c and goes on behind.
+// A block's tokens come through shared memory, 512 at a time, so that a thread's loads of dy wait for no other.
 __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_constant__ EmbedParams p) {
+    constexpr int kTokens = 512, U = 8;  // U: rows in flight
+    __shared__ uint32_t keys[kTokens], order[kTokens];
     const Where x = where(p);
+    const int t = threadIdx.x, sub = t / p.width;
+    const int tile = min((int)p.chunk, kTokens / p.block_chunks);  // tokens of a chunk at a time
+    const int64_t block0 = (int64_t)blockIdx.x * p.block_chunks;
     ptx::grid_launch_dependents();
     ptx::grid_wait();
-    if (x.pack < 0) return;
-    constexpr int U = 8;  // rows in flight
-    const int first = (int)(x.chunk * p.chunk), end = (int)min((int64_t)first + p.chunk, p.M);
-    const uint32_t prev = first > 0 ? p.sorted[first - 1] : p.V, next = end < p.M ? p.sorted[end] : p.V;
+    const int64_t first = x.chunk * p.chunk;
+    const int n = x.pack < 0 ? 0 : (int)min(p.chunk, p.M - first);
+    const uint32_t prev = n && first > 0 ? p.sorted[first - 1] : p.V, next = n && first + n < p.M ? p.sorted[first + n] : p.V;
     Pack sum = {};
     uint32_t cur = p.V;
     bool started = false;  // the current sum starts in this chunk
-    for (int i0 = first; i0 < end; i0 += U) {
-        uint32_t key[U];
-        uint4 v[U];
+    for (int at = 0; at < (int)p.chunk; at += tile) {
+        __syncthreads();
+        for (int i = t; i < tile * p.block_chunks; i += blockDim.x) {
+            const int c = i / tile, j = at + i - c * tile;
+            const int64_t from = (block0 + c) * p.chunk + j;
+            const bool in = j < (int)p.chunk && from < p.M;
+            keys[i] = in ? p.sorted[from] : p.V;
+            order[i] = in ? p.order[from] : 0u;
+        }
+        __syncthreads();
+        const int end = min(tile, n - at);
+        for (int i0 = 0; i0 < end; i0 += U) {
+            uint32_t key[U];
+            uint4 v[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) key[j] = i0 + j < end ? p.sorted[i0 + j] : p.V;
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (key[j] < p.V) v[j] = ptx::ld_stream_v4(p.dy + (size_t)p.order[i0 + j] * p.N + x.pack * 8);
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (key[j] >= p.V) continue;
-            if (key[j] != cur) {
-                if (cur < p.V) {
-                    if (started) store_row(p, cur, x.pack, sum);
-                    else store_part(p, 2 * x.chunk, x.pack, sum);
-                }
-                started = i0 + j > first || key[j] != prev;
-                cur = key[j];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sum[i] = 0ull;
+            for (int j = 0; j < U; ++j) {
+                key[j] = i0 + j < end ? keys[sub * tile + i0 + j] : p.V;
+                if (key[j] < p.V) v[j] = ptx::ld_stream_v4(p.dy + (size_t)order[sub * tile + i0 + j] * p.N + x.pack * 8);
             }
-            Pack f;
-            unpack8(v[j], f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] = add2(sum[i], f[i]);
+            for (int j = 0; j < U; ++j) {
+                if (key[j] >= p.V) continue;
+                if (key[j] != cur) {
+                    if (cur < p.V) {
+                        if (started) store_row(p, cur, x.pack, sum);
+                        else store_part(p, 2 * x.chunk, x.pack, sum);
+                    }
+                    started = at + i0 + j > 0 || key[j] != prev;
+                    cur = key[j];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[i] = 0ull;
+                }
+                Pack f;
+                unpack8(v[j], f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = add2(sum[i], f[i]);
+            }
         }
     }
     if (cur < p.V) {
@@ -310,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
     if (id >= p.V || p.sorted[end] != id || (first > 0 && p.sorted[first - 1] == id)) return;
     Pack sum;
     load8(p.part + (2 * x.chunk + 1) * p.N + x.pack * 8, sum);
-    constexpr int U = 4;
+    constexpr int U = 8;
     bool more = true;
     for (int64_t c = x.chunk + 1; more; c += U) {
         Pack v[U];
@@ -357,8 +407,10 @@ cudaError_t launch_embedding_backward(EmbedParams& p, void* sort, float* scratch
         p.keys[i] = words + (2 * i) * p.M;
         p.idx[i] = words + (2 * i + 1) * p.M;
     }
-    p.sorted = p.keys[(p.passes - 1) & 1];
-    p.order = p.idx[(p.passes - 1) & 1];
+    if (p.M <= kRankMax) p.passes = 0;
+    const int last = p.passes ? (p.passes - 1) & 1 : 0;
+    p.sorted = p.keys[last];
+    p.order = p.idx[last];
     p.part = scratch;
     // two partial rows a chunk; what a workspace of this width has, so that the order of the sums goes by the sizes alone
     const int64_t rows = (int64_t)norm_backward_scratch_words(p.N, num_sms) / p.N;

@@ -23,63 +23,41 @@
 namespace are {
 namespace {
 
-constexpr int kStat = 32;                     // words of one statistic: one a warp
-constexpr int kRedSet = 4 * kStat;            // words of one exchange
-constexpr int kRedAll = 2 * kRedSet + 2 * kStat;  // two exchanges in turn, the warps' columns and their reciprocals
+constexpr int kRedWarps = 32;
+constexpr int kRedAll = 2 * kRedWarps * 4;  // two exchanges in turn: a warp's four sums together
 
-// Columns that warp w owns.
-__device__ __forceinline__ int warp_columns(int w, const RowsParams& p) {
-    const int P = p.N >> 3;
+// The join is spread over a warp's lanes: lane l has the sums of warp l modulo `ways`, the
+// power of two that holds the block's warps, so sums over `ways` neighbouring lanes are
+// the block's, in every lane.  (A thread that ran through all the warps' sums by itself took
+// 28 % of the backward kernel's instructions at 4096 columns.)
+struct Join {
+    int ways;
+    float n, inv_n;    // this lane's warp's columns, 0 behind the last warp
+    float own_inv_n;   // the reciprocal of the thread's own warp's
+};
+
+__device__ __forceinline__ Join make_join(const RowsParams& p) {
+    const int lane = threadIdx.x & 31, nwarps = p.nt >> 5, P = p.N >> 3;
+    Join j;
+    j.ways = 1;
+    while (j.ways < nwarps) j.ways <<= 1;
+    const int w = lane & (j.ways - 1);
     int n = 0;
-    for (int k = 0; k < p.slices; ++k) {
-        const int left = P - (w * 32 + k * p.nt);
-        n += left < 0 ? 0 : left > 32 ? 32 : left;
+    if (w < nwarps) {
+        for (int k = 0; k < p.slices; ++k) {
+            const int left = P - (w * 32 + k * p.nt);
+            n += left < 0 ? 0 : left > 32 ? 32 : left;
+        }
     }
-    return n * 8;
+    j.n = (float)(n * 8);
+    j.inv_n = n ? 1.f / j.n : 0.f;
+    j.own_inv_n = __shfl_sync(0xFFFFFFFFu, j.inv_n, threadIdx.x >> 5);
+    return j;
 }
 
-// Words behind the last warp stay zero, so the joins may run over whole float4s.
-__device__ __forceinline__ void init_columns(const Ring& g, const RowsParams& p) {
-    if (threadIdx.x < (unsigned)(p.nt >> 5)) {
-        const float n = (float)warp_columns(threadIdx.x, p);
-        g.red[2 * kRedSet + threadIdx.x] = n;
-        g.red[2 * kRedSet + kStat + threadIdx.x] = 1.f / n;
-    }
-    __syncthreads();
-}
-
-__device__ __forceinline__ float quad(const float4& v) { return (v.x + v.y) + (v.z + v.w); }
-
-// The row's mean from the warps' sums.
-__device__ __forceinline__ float join_mean(const float* red, int nwarps, float inv_n) {
-    float t = 0.f;
-    for (int w = 0; w < nwarps; w += 4) t += quad(*reinterpret_cast<const float4*>(red + w));
-    return t * inv_n;
-}
-
-__device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-
-// sum (h - mean)^2 from the warps' sums S, squares Q around their own means, and columns n (1/n).
-__device__ __forceinline__ float join_squares(const float* S, const float* Q, const float* n, int nwarps, float mean) {
-    float t = 0.f;
-    for (int w = 0; w < nwarps; w += 4) {
-        const float4 s = at4(S + w), q = at4(Q + w), c = at4(n + w), r = at4(n + kStat + w);
-        const float a = fmaf(s.x, r.x, -mean), b = fmaf(s.y, r.y, -mean), d = fmaf(s.z, r.z, -mean), e = fmaf(s.w, r.w, -mean);
-        t += (fmaf(c.x * a, a, q.x) + fmaf(c.y * b, b, q.y)) + (fmaf(c.z * d, d, q.z) + fmaf(c.w * e, e, q.w));
-    }
-    return t;
-}
-
-// sum g (h - mean) from the warps' G = sum g and C = sum g (h - m_w).
-__device__ __forceinline__ float join_products(const float* S, const float* G, const float* C, const float* n, int nwarps,
-                                               float mean) {
-    float t = 0.f;
-    for (int w = 0; w < nwarps; w += 4) {
-        const float4 s = at4(S + w), g = at4(G + w), c = at4(C + w), r = at4(n + kStat + w);
-        t += (fmaf(g.x, fmaf(s.x, r.x, -mean), c.x) + fmaf(g.y, fmaf(s.y, r.y, -mean), c.y)) +
-             (fmaf(g.z, fmaf(s.z, r.z, -mean), c.z) + fmaf(g.w, fmaf(s.w, r.w, -mean), c.w));
-    }
-    return t;
+__device__ __forceinline__ float join_sum(float v, int ways) {
+    for (int o = 1; o < ways; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
 }
 
 // ---------------------------------------------------------------------- forward
@@ -90,19 +68,17 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_rows_kernel(const _
     extern __shared__ __align__(128) uint8_t rows_smem[];
     const Ring g = carve(rows_smem, p);
     ring_init(g, p);
-    init_columns(g, p);
     ptx::grid_launch_dependents();
     ptx::grid_wait();
     if (threadIdx.x >= p.nt) {
         produce(g, p);
         return;
     }
-    const int t = threadIdx.x, lane = t & 31, w = t >> 5, nwarps = p.nt >> 5;
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     const int P = p.N >> 3;
     const size_t step = (size_t)p.nt * 16;
     constexpr bool kGammaRegs = PPT <= 4, kBetaRegs = PPT <= 2, kBetaShared = PPT == 4;
-    const float* cols = g.red + 2 * kRedSet;
-    const float inv_cols = cols[kStat + w];
+    const Join join = make_join(p);
     Pack gam[kGammaRegs ? PPT : 1], bet[kBetaRegs ? PPT : 1];
 #pragma unroll
     for (int k = 0; k < PPT; ++k) {
@@ -151,9 +127,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_rows_kernel(const _
                 if (p.res_out && pk < P) ptx::st_stream_v4(p.res_out + row * (int64_t)p.N + pk * 8, pack8(h[k]));
             }
         }
-        float* red = g.red + buf * kRedSet;
+        float4* red = reinterpret_cast<float4*>(g.red) + buf * kRedWarps;
         const float S = warp_sum(both(sum2));
-        const float own = S * inv_cols;  // the warp's mean
+        const float own = S * join.own_inv_n;  // the warp's mean
         const uint64_t own2 = pair(-own, -own);
         uint64_t q2 = 0ull;
 #pragma unroll
@@ -167,13 +143,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_rows_kernel(const _
             }
         }
         const float Q = warp_sum(both(q2));
-        if (lane == 0) {
-            red[w] = S;
-            red[kStat + w] = Q;
-        }
+        if (lane == 0) *reinterpret_cast<float2*>(red + w) = make_float2(S, Q);
         consumer_bar(p.nt);
-        const float mean = join_mean(red, nwarps, p.inv_n);
-        const float inv = rsqrtf(join_squares(red, red + kStat, cols, nwarps, mean) * p.inv_n + p.eps);
+        const float2 v = *reinterpret_cast<const float2*>(red + (lane & (join.ways - 1)));
+        const float mean = join_sum(v.x, join.ways) * p.inv_n;
+        const float off = fmaf(v.x, join.inv_n, -mean);
+        const float inv = rsqrtf(join_sum(fmaf(join.n * off, off, v.y), join.ways) * p.inv_n + p.eps);
         const uint64_t mean2 = pair(-mean, -mean), inv2 = pair(inv, inv);
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
@@ -214,19 +189,17 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_backward_rows_kerne
     extern __shared__ __align__(128) uint8_t rows_smem[];
     const Ring g = carve(rows_smem, p);
     ring_init(g, p);
-    init_columns(g, p);
     ptx::grid_launch_dependents();
     ptx::grid_wait();
     if (threadIdx.x >= p.nt) {
         produce(g, p);
         return;
     }
-    const int t = threadIdx.x, lane = t & 31, w = t >> 5, nwarps = p.nt >> 5;
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     const int P = p.N >> 3;
     const size_t step = (size_t)p.nt * 16;
     constexpr bool kRegs = PPT <= 2;
-    const float* cols = g.red + 2 * kRedSet;
-    const float inv_cols = cols[kStat + w];
+    const Join join = make_join(p);
     float* const beta_sums = g.extra + p.N;
     // a thread reads only the words that it writes here: no barrier
     Pack dg[PPT], db[kRegs ? PPT : 1];
@@ -275,48 +248,58 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_backward_rows_kerne
                 if (++s == p.stages) { s = 0; ph ^= 1u; }
             }
         }
-        float* red = g.red + buf * kRedSet;
+        float4* red = reinterpret_cast<float4*>(g.red) + buf * kRedWarps;
         const float S = warp_sum(both(sum2));
-        const float own = S * inv_cols;  // the warp's mean
+        const float own = S * join.own_inv_n;  // the warp's mean
         const uint64_t own2 = pair(-own, -own);
         uint64_t q2 = 0ull, g2 = 0ull, c2 = 0ull;
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
             if (k < p.slices && t + k * p.nt < P) {
-                Pack h, gk;
+                Pack gk, h;
                 unpack8(hv[k], h);
                 load8(g.extra + (t + k * p.nt) * 8, gk);
                 Pack& d = dy[ONE ? 0 : k];
                 if (ONE) unpack8(dv[k], d);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint64_t c = add2(h[i], own2), gi = mul2(d[i], gk[i]);
-                    q2 = fma2(c, c, q2);
+                    const uint64_t gi = mul2(d[i], gk[i]);
+                    h[i] = add2(h[i], own2);
+                    q2 = fma2(h[i], h[i], q2);
                     g2 = add2(gi, g2);
-                    c2 = fma2(gi, c, c2);
+                    c2 = fma2(gi, h[i], c2);
                 }
             }
         }
-        const float Q = warp_sum(both(q2)), G = warp_sum(both(g2)), C = warp_sum(both(c2));
-        if (lane == 0) {
-            red[w] = S;
-            red[kStat + w] = Q;
-            red[2 * kStat + w] = G;
-            red[3 * kStat + w] = C;
+        // Q, G and C over the warp at once: with a step, lanes keep fewer of them
+        float Q = both(q2), G = both(g2), C = both(c2);
+        {
+            const bool hi = lane & 16, mid = lane & 8;
+            float v = (hi ? C : Q) + __shfl_xor_sync(0xFFFFFFFFu, hi ? Q : C, 16);
+            G += __shfl_xor_sync(0xFFFFFFFFu, G, 16);
+            v = (mid ? G : v) + __shfl_xor_sync(0xFFFFFFFFu, mid ? v : G, 8);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            // lane 0: Q, lane 8: G, lane 16: C
+            float* to = reinterpret_cast<float*>(red + w);
+            if (lane == 0) *reinterpret_cast<float2*>(to) = make_float2(S, v);
+            if (lane == 8) to[2] = v;
+            if (lane == 16) to[3] = v;
         }
         consumer_bar(p.nt);
-        const float mean = join_mean(red, nwarps, p.inv_n);
-        const float inv = rsqrtf(join_squares(red, red + kStat, cols, nwarps, mean) * p.inv_n + p.eps);
-        const float a = join_mean(red + 2 * kStat, nwarps, p.inv_n);  // mean(g)
-        const float b = join_products(red, red + 2 * kStat, red + 3 * kStat, cols, nwarps, mean) * p.inv_n * inv;  // mean(g xhat)
-        const uint64_t mean2 = pair(-mean, -mean), inv2 = pair(inv, inv), b2 = pair(-inv * b, -inv * b),
-                       a2 = pair(-a, -a);
+        const float4 v = red[lane & (join.ways - 1)];
+        const float mean = join_sum(v.x, join.ways) * p.inv_n;
+        const float off = fmaf(v.x, join.inv_n, -mean);
+        const float inv = rsqrtf(join_sum(fmaf(join.n * off, off, v.y), join.ways) * p.inv_n + p.eps);
+        const float a = join_sum(v.z, join.ways) * p.inv_n;                          // mean(g)
+        const float b = join_sum(fmaf(v.z, off, v.w), join.ways) * p.inv_n * inv;    // mean(g xhat)
+        const uint64_t mean2 = pair(-mean, -mean), inv2 = pair(inv, inv), b2 = pair(-inv * b, -inv * b), a2 = pair(-a, -a);
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
             if (k < p.slices) {
                 const int pk = t + k * p.nt;
                 if (pk < P) {
-                    Pack h, gk, e = {}, o;
+                    Pack gk, e = {}, o, h;
                     unpack8(hv[k], h);
                     load8(g.extra + pk * 8, gk);
                     if (p.has_res) unpack8(ev[k], e);
@@ -360,6 +343,230 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_backward_rows_kerne
     }
 }
 
+// Rows of up to 4096 columns: a block takes ROWS of them at a time, whose sums share one
+// exchange and whose latencies run side by side (one row at a time, 16384 x 4096 took 138 us
+// for a floor of 79: neither memory nor the issue slots were busy, but every row went through
+// 25 shuffles, a barrier and the join one after the other).  It has no producer warp, which
+// leaves 128 registers a thread: behind the barrier everyone has read the rows, so warp 0
+// sends the ring's next copies from there.
+constexpr int kSmallThreads = 512;  // threads an SM, at 128 registers
+
+template <int N>
+struct Reduced {
+    // Sums of N (a power of two) values over the warp; lane l ends up with the sum of value l / (32 / N).
+    // With each of the first steps a lane sends half of what it has and keeps the other half.
+    static __device__ __forceinline__ float run(float (&v)[N]) {
+        const int lane = threadIdx.x & 31;
+        int o = 16;
+#pragma unroll
+        for (int n = N; n > 1; n >>= 1, o >>= 1) {
+            const bool upper = lane & o;
+#pragma unroll
+            for (int i = 0; i < n / 2; ++i)
+                v[i] = (upper ? v[i + n / 2] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[i] : v[i + n / 2], o);
+        }
+        float t = v[0];
+        for (; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+        return t;
+    }
+};
+
+template <int PPT, int ROWS, bool ONE>
+__global__ void __launch_bounds__(256, 2) layernorm_backward_small_kernel(const __grid_constant__ RowsParams p) {
+    extern __shared__ __align__(128) uint8_t rows_smem[];
+    Ring g;  // (for ring_wait)
+    g.stage = rows_smem;
+    g.extra = reinterpret_cast<float*>(rows_smem + (size_t)p.stages * p.stage_bytes);
+    g.red = g.extra + p.extra_words;
+    g.full = reinterpret_cast<uint64_t*>(g.red + p.red_words);
+    g.abort = reinterpret_cast<volatile uint32_t*>(g.full + kMaxStages);
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5, nwarps = p.nt >> 5, P = p.N >> 3, S = p.stages;
+    if (t == 0) {
+        for (int s = 0; s < S; ++s) ptx::mbar_init(&g.full[s], 1);
+        *g.abort = 0u;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_shared();
+    }
+    for (int i = t; i < p.red_words; i += p.nt) g.red[i] = 0.f;
+    __syncthreads();
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
+
+    // this block's k-th row (M and more: none)
+    auto row_at = [&](int64_t k) { return (blockIdx.x + k / ROWS * gridDim.x) * ROWS + k % ROWS; };
+    const uint32_t bytes = (uint32_t)p.N * 2u;
+    const uint64_t pol = ptx::policy_evict_first();
+    auto send = [&](int64_t k) {  // warp 0
+        const int64_t row = row_at(k);
+        if (row >= p.M) return;
+        const int s = (int)(k % S);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&g.full[s], bytes * (uint32_t)p.nsrc);
+        __syncwarp();
+        if (lane < p.nsrc)
+            ptx::bulk_load_hint(g.stage + (size_t)s * p.stage_bytes + (size_t)lane * bytes, p.src[lane] + row * (int64_t)p.N, bytes,
+                                &g.full[s], pol);
+    };
+    if (w == 0)
+        for (int k = 0; k < S; ++k) send(k);
+
+    // a thread reads only the gamma words that it writes here
+#pragma unroll
+    for (int k = 0; k < PPT; ++k) {
+        const int pk = t + k * p.nt;
+        if (pk < P) {
+            reinterpret_cast<float4*>(g.extra)[pk * 2] = reinterpret_cast<const float4*>(p.gamma)[pk * 2];
+            reinterpret_cast<float4*>(g.extra)[pk * 2 + 1] = reinterpret_cast<const float4*>(p.gamma)[pk * 2 + 1];
+        }
+    }
+    const Join join = make_join(p);
+    Pack dg[PPT], db[PPT];
+#pragma unroll
+    for (int k = 0; k < PPT; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dg[k][i] = db[k][i] = 0ull;
+    int s = 0, buf = 0;
+    uint32_t ph = 0;
+    int64_t k0 = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < p.M; row0 += (int64_t)gridDim.x * ROWS, k0 += ROWS, buf ^= 1) {
+        Pack dy[ONE ? 1 : ROWS][ONE ? 1 : PPT];
+        uint4 dv[ONE ? ROWS : 1][ONE ? PPT : 1], hv[ROWS][PPT], ev[ROWS][PPT];
+        float sums[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const bool there = row0 + r < p.M;
+            if (there) ring_wait(&g.full[s], ph, g, p);
+            const uint8_t* at = g.stage + (size_t)s * p.stage_bytes;
+            uint64_t sum2 = 0ull;
+#pragma unroll
+            for (int k = 0; k < PPT; ++k) {
+                const int pk = t + k * p.nt;
+                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                const bool in = there && pk < P;
+                const uint8_t* a = at + (size_t)pk * 16;
+                hv[r][k] = in ? *reinterpret_cast<const uint4*>(a + p.R * bytes) : zero;
+                ev[r][k] = in && p.has_res ? *reinterpret_cast<const uint4*>(a + (p.R + 1) * bytes) : zero;
+                if (ONE) {
+                    dv[ONE ? r : 0][ONE ? k : 0] = in ? *reinterpret_cast<const uint4*>(a) : zero;
+                } else if (in) {
+                    sum_ranks<false>(a, p.R, bytes, dy[ONE ? 0 : r][ONE ? 0 : k]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dy[ONE ? 0 : r][ONE ? 0 : k][i] = 0ull;
+                }
+                Pack h;
+                unpack8(hv[r][k], h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum2 = add2(h[i], sum2);
+            }
+            sums[r] = both(sum2);
+            if (++s == S) { s = 0; ph ^= 1u; }
+        }
+        const float mine = Reduced<ROWS>::run(sums);  // lane l: row l / (32 / ROWS)
+        float own[ROWS], v[4 * ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            own[r] = __shfl_sync(0xFFFFFFFFu, mine, r * (32 / ROWS));  // the warp's sum of the row
+            const float mean = own[r] * join.own_inv_n;
+            const uint64_t own2 = pair(-mean, -mean);
+            uint64_t q2 = 0ull, g2 = 0ull, c2 = 0ull;
+#pragma unroll
+            for (int k = 0; k < PPT; ++k) {
+                if (t + k * p.nt < P) {
+                    Pack h, gk, d1;
+                    unpack8(hv[r][k], h);
+                    load8(g.extra + (t + k * p.nt) * 8, gk);
+                    if (ONE) unpack8(dv[ONE ? r : 0][ONE ? k : 0], d1);
+                    const Pack& d = ONE ? d1 : dy[ONE ? 0 : r][ONE ? 0 : k];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t c = add2(h[i], own2), gi = mul2(d[i], gk[i]);
+                        q2 = fma2(c, c, q2);
+                        g2 = add2(gi, g2);
+                        c2 = fma2(gi, c, c2);
+                    }
+                }
+            }
+            v[r] = both(q2);
+            v[ROWS + r] = both(g2);
+            v[2 * ROWS + r] = both(c2);
+            v[3 * ROWS + r] = 0.f;
+        }
+        // lane l: value l / (8 / ROWS) of Q, G, C of the rows; its rows' sums are known to every lane
+        const float part = Reduced<4 * ROWS>::run(v);
+        float* red = g.red + buf * (ROWS * 4 * 8);  // [statistic][row][warp]
+        constexpr int kPer = 8 / ROWS;
+        if (lane % kPer == 0 && lane / kPer < 3 * ROWS) red[(lane / kPer) * 8 + w] = part;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+            if (lane == 31) red[(3 * ROWS + r) * 8 + w] = own[r];
+        __syncthreads();
+        if (w == 0) {
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) send(k0 + S + r);
+        }
+        // the join: eight lanes a row, a warp's sums in each
+        const int jr = (lane >> 3) & (ROWS - 1), jw = lane & 7;
+        const bool counts = jw < nwarps;
+        const float Q = red[jr * 8 + jw], G = red[(ROWS + jr) * 8 + jw], C = red[(2 * ROWS + jr) * 8 + jw],
+                    H = red[(3 * ROWS + jr) * 8 + jw];
+        const float n = counts ? join.n : 0.f, inv_n = counts ? join.inv_n : 0.f;
+        const float mean = join_sum(H, 8) * p.inv_n;
+        const float off = fmaf(H, inv_n, -mean);
+        const float inv = rsqrtf(join_sum(fmaf(n * off, off, Q), 8) * p.inv_n + p.eps);
+        const float a = join_sum(G, 8) * p.inv_n;                          // mean(g)
+        const float b = join_sum(fmaf(G, off, C), 8) * p.inv_n * inv;      // mean(g xhat)
+        const float neg = -inv * b;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const float rm = -__shfl_sync(0xFFFFFFFFu, mean, r * 8), ri = __shfl_sync(0xFFFFFFFFu, inv, r * 8),
+                        ra = -__shfl_sync(0xFFFFFFFFu, a, r * 8), rb = __shfl_sync(0xFFFFFFFFu, neg, r * 8);
+            if (row0 + r >= p.M) continue;
+            const uint64_t mean2 = pair(rm, rm), inv2 = pair(ri, ri), a2 = pair(ra, ra), b2 = pair(rb, rb);
+#pragma unroll
+            for (int k = 0; k < PPT; ++k) {
+                const int pk = t + k * p.nt;
+                if (pk < P) {
+                    Pack h, gk, e, o, d1;
+                    unpack8(hv[r][k], h);
+                    unpack8(ev[r][k], e);
+                    load8(g.extra + pk * 8, gk);
+                    if (ONE) unpack8(dv[ONE ? r : 0][ONE ? k : 0], d1);
+                    const Pack& d = ONE ? d1 : dy[ONE ? 0 : r][ONE ? 0 : k];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t xh = mul2(add2(h[i], mean2), inv2);
+                        o[i] = fma2(fma2(d[i], gk[i], a2), inv2, fma2(xh, b2, e[i]));
+                        dg[k][i] = fma2(d[i], xh, dg[k][i]);
+                        db[k][i] = add2(db[k][i], d[i]);
+                    }
+                    ptx::st_stream_v4(p.res_out + (row0 + r) * (int64_t)p.N + pk * 8, pack8(o));
+                }
+            }
+        }
+    }
+    if (w == 0 && *g.abort) {
+        // the block must not end before its copies have landed (they have, unless a wait ran out)
+        for (int64_t k = k0 > S ? k0 - S : 0; k < k0 + S; ++k) {
+            if (row_at(k) >= p.M) break;
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(&g.full[k % S], (uint32_t)(k / S) & 1u))
+                if (ptx::globaltimer() - t0 > p.timeout_ns) break;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < PPT; ++k) {
+        const int pk = t + k * p.nt;
+        if (pk < P) {
+            const size_t at = (size_t)blockIdx.x * p.N + pk * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (p.dgamma) reinterpret_cast<uint64_t*>(p.dgamma + at)[i] = dg[k][i];
+                if (p.dbeta) reinterpret_cast<uint64_t*>(p.dbeta + at)[i] = db[k][i];
+            }
+        }
+    }
+}
+
 // Packs a thread holds, of a row of P: as the RMSNorm's kernels, whose registers these have.
 int packs_per_thread(int P, bool alone) {
     if (alone && P <= 1024) return P <= 512 ? 1 : 2;
@@ -378,7 +585,9 @@ void (*forward_kernel(int ppt, int threads))(RowsParams) {
 }
 
 template <bool ONE>
-void (*backward_kernel(int ppt, int threads))(RowsParams) {
+void (*backward_kernel(int ppt, int threads, int rows))(RowsParams) {
+    if (rows == 4) return layernorm_backward_small_kernel<1, 4, ONE>;
+    if (rows == 2) return layernorm_backward_small_kernel<2, 2, ONE>;
     switch (ppt) {
         case 1: return layernorm_backward_rows_kernel<1, ONE, 288, 2>;
         case 2:
@@ -394,6 +603,30 @@ void (*backward_kernel(int ppt, int threads))(RowsParams) {
 RowsPlan layernorm_plan(RowsParams& p, int num_sms) {
     const int P = p.N / 8;
     const int ppt = p.backward ? backward_packs_per_thread(P) : packs_per_thread(P, p.M <= num_sms);
+    p.rows = 1;
+    const int one_nt = ((P + ppt - 1) / ppt + 31) / 32 * 32;
+    if (p.backward && ppt <= 2 && P <= 512 && p.M > (int64_t)num_sms * (kRowsThreads / (one_nt + 32))) {
+        // several rows at a time, where there is more than a round of single ones and the ring holds that many for every
+        // block that an SM's registers hold
+        RowsPlan plan;
+        plan.ppt = ppt;
+        p.rows = ppt == 1 ? 4 : 2;
+        p.nt = one_nt;
+        p.slices = ppt;
+        p.extra_words = p.N;
+        p.red_words = 2 * p.rows * 4 * 8;
+        p.stage_bytes = p.nsrc * p.N * 2;
+        const int64_t items = (p.M + p.rows - 1) / p.rows, rounds = (items + num_sms - 1) / num_sms;
+        const int blocks = (int)std::min<int64_t>(rounds, std::min(kSmallThreads / p.nt, 10));
+        const size_t fixed = (size_t)(p.extra_words + p.red_words) * 4 + kMaxStages * 8 + 16;
+        const size_t room = (blocks == 1 ? kRowsSmemLimit : kRowsSmemSm / blocks - 1024) - fixed;
+        p.stages = (int)std::min<size_t>(room / p.stage_bytes, kMaxStages);
+        plan.smem = fixed + (size_t)p.stages * p.stage_bytes;
+        plan.threads = p.nt;
+        plan.grid = (int)std::min<int64_t>(items, (int64_t)blocks * num_sms);
+        if (p.stages >= p.rows) return plan;
+        p.rows = 1;
+    }
     p.extra_words = p.backward ? (ppt <= 2 ? p.N : 2 * p.N) : ppt == 4 ? p.N : 0;
     p.red_words = kRedAll;
     return rows_shape(p, ppt, num_sms);
@@ -408,7 +641,10 @@ cudaError_t layernorm_prepare() {
         for (int threads : {288, 512})
             for (bool one : {false, true})
                 if (e == cudaSuccess)
-                    e = opt_in(one ? backward_kernel<true>(ppt, threads) : backward_kernel<false>(ppt, threads));
+                    e = opt_in(one ? backward_kernel<true>(ppt, threads, 1) : backward_kernel<false>(ppt, threads, 1));
+    for (int rows : {2, 4})
+        for (bool one : {false, true})
+            if (e == cudaSuccess) e = opt_in(one ? backward_kernel<true>(0, 0, rows) : backward_kernel<false>(0, 0, rows));
     return e;
 }
 
@@ -423,7 +659,8 @@ cudaError_t launch_layernorm_backward_rows(RowsParams& p, const RowsPlan& plan, 
     float* const second = scratch + (dgamma ? (size_t)plan.grid * p.N : 0);
     p.dgamma = dgamma == nullptr ? nullptr : one ? dgamma : scratch;
     p.dbeta = dbeta == nullptr ? nullptr : one ? dbeta : second;
-    auto* kernel = p.R == 1 ? backward_kernel<true>(plan.ppt, plan.threads) : backward_kernel<false>(plan.ppt, plan.threads);
+    auto* kernel = p.R == 1 ? backward_kernel<true>(plan.ppt, plan.threads, p.rows)
+                            : backward_kernel<false>(plan.ppt, plan.threads, p.rows);
     cudaError_t e = launch_dependent(kernel, plan.grid, plan.threads, plan.smem, s, p);
     if (e == cudaSuccess && !one && (dgamma || dbeta))
         e = launch_dependent(dgamma_sum_kernel, dim3((p.N + 15) / 16, dgamma && dbeta ? 2 : 1), 256, 0, s, scratch,

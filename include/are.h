@@ -53,7 +53,8 @@
  *    kernels, never by a host step, so every replay finds it as the capture
  *    did.  Workspace creation, reset and snapshots are not capturable.
  *  - are_allreduce_rmsnorm_quant_groups, are_allreduce_rmsnorm_backward, the
- *    LayerNorm and embedding calls and the 4-bit linears launch with programmatic stream
+ *    LayerNorm, embedding and cross entropy calls and the 4-bit linears launch
+ *    with programmatic stream
  *    serialisation: their
  *    kernels may come up while earlier work of the stream still runs, and
  *    read and write no memory of the caller's before all of it has ended.
@@ -583,7 +584,8 @@ ARE_API are_status are_allreduce_layernorm(const are_bf16* const partials[], con
  *            inv = rsqrt(var + eps), xhat = (h - mean) * inv, per row of h;
  *            dh = bf16( inv * (g - mean_j(g_j) - xhat * mean_j(g_j xhat_j)) + dres );
  *            dgamma_j = sum_i dy_ij * xhat_ij, dbeta_j = sum_i dy_ij, in fp32, in
- *            an order that depends on M, N and the device's SM count alone.
+ *            an order that depends on M, N, R, whether dres is given and the
+ *            device's SM count alone.
  * beta does not enter.  M == 0 writes zeros to dgamma and dbeta.  Uses a buffer
  * of the workspace for partial sums: N must not exceed N_max (ARE_ECAPACITY), R
  * not R_max.
