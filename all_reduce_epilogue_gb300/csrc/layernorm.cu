@@ -8,12 +8,11 @@
 //   dh     = inv * (g - mean(g) - xhat * mean(g * xhat)) + d_res
 //   dgamma = sum_i dy_i * xhat_i,  dbeta = sum_i dy_i
 //
-// The variance is a sum of squares around the mean, not mean(h^2) - mean^2, which
-// loses a row whose mean is large against its spread.  It takes one exchange over the
-// block all the same: a warp sums its columns, takes the squares (and the products
-// with g) around its own mean m_w, and the block joins the warps' sums,
-//   sum (h - mean)^2 = sum_w Q_w + n_w (m_w - mean)^2,
-//   sum g (h - mean) = sum_w C_w + G_w (m_w - mean)
+// The forward pass's variance is a sum of squares around the mean, not mean(h^2) -
+// mean^2, which loses a row whose mean is large against its spread.  It takes one
+// exchange over the block all the same: a warp sums its columns, takes the squares
+// around its own mean m_w, and the block joins the warps' sums,
+//   sum (h - mean)^2 = sum_w Q_w + n_w (m_w - mean)^2
 // (Chan, Golub and LeVeque 1979): shuffles within the warp instead of a second
 // barrier of the block.
 #include <algorithm>
@@ -24,7 +23,9 @@ namespace are {
 namespace {
 
 constexpr int kRedWarps = 32;
-constexpr int kRedAll = 2 * kRedWarps * 4;  // two exchanges in turn: a warp's four sums together
+constexpr int kWarps = 16;                  // backward: warps of a block, at most
+constexpr int kRedAll = 2 * kRedWarps * 4;  // two exchanges in turn: forward two sums a warp, backward up to six
+static_assert(2 * 6 * kWarps <= kRedAll, "words of an exchange");
 
 // The join is spread over a warp's lanes: lane l has the sums of warp l modulo `ways`, the
 // power of two that holds the block's warps, so sums over `ways` neighbouring lanes are
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_rows_kernel(const _
                 if (p.res_out && pk < P) ptx::st_stream_v4(p.res_out + row * (int64_t)p.N + pk * 8, pack8(h[k]));
             }
         }
-        float4* red = reinterpret_cast<float4*>(g.red) + buf * kRedWarps;
+        float2* red = reinterpret_cast<float2*>(g.red) + buf * kRedWarps;
         const float S = warp_sum(both(sum2));
         const float own = S * join.own_inv_n;  // the warp's mean
         const uint64_t own2 = pair(-own, -own);
@@ -143,9 +144,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_rows_kernel(const _
             }
         }
         const float Q = warp_sum(both(q2));
-        if (lane == 0) *reinterpret_cast<float2*>(red + w) = make_float2(S, Q);
+        if (lane == 0) red[w] = make_float2(S, Q);
         consumer_bar(p.nt);
-        const float2 v = *reinterpret_cast<const float2*>(red + (lane & (join.ways - 1)));
+        const float2 v = red[lane & (join.ways - 1)];
         const float mean = join_sum(v.x, join.ways) * p.inv_n;
         const float off = fmaf(v.x, join.inv_n, -mean);
         const float inv = rsqrtf(join_sum(fmaf(join.n * off, off, v.y), join.ways) * p.inv_n + p.eps);
@@ -182,6 +183,90 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_rows_kernel(const _
 }
 
 // --------------------------------------------------------------------- backward
+// The backward pass needs four sums a row, and takes them in one pass: H = sum h,
+// Q = sum h^2, G = sum g, C = sum g h, from which mean = H / N, var = Q / N - mean^2 and
+// sum g (h - mean) = C - mean G.  Where the mean is large against the spread these
+// differences lose what the terms have: a row with mean^2 > 4 var takes Q and C again,
+// around the mean, from the registers that still hold it (one more exchange; the same row
+// always does, whatever its neighbours are).  Elsewhere the differences cost at most a factor
+// of 5 of the sums' relative error, 2^-21 or so.
+constexpr float kSpread = 4.f;
+
+template <int N>
+struct Reduced {
+    // Sums of N (a power of two) values over the warp; lane l ends up with the sum of value l / (32 / N).
+    // With each of the first steps a lane sends half of what it has and keeps the other half.
+    static __device__ __forceinline__ float run(float (&v)[N]) {
+        const int lane = threadIdx.x & 31;
+        int o = 16;
+#pragma unroll
+        for (int n = N; n > 1; n >>= 1, o >>= 1) {
+            const bool upper = lane & o;
+#pragma unroll
+            for (int i = 0; i < n / 2; ++i)
+                v[i] = (upper ? v[i + n / 2] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[i] : v[i + n / 2], o);
+        }
+        float t = v[0];
+        for (; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+        return t;
+    }
+};
+
+// The block's sums of a row, in every thread, from what its warps left: `at[s * step + w]`, statistic s of warp w,
+// zero behind the last warp; eight lanes add up each statistic.
+struct RowSums {
+    float Q, G, C, H;
+};
+__device__ __forceinline__ RowSums block_sums(const float* at, int step, int nwarps) {
+    const int lane = threadIdx.x & 31;
+    const float* mine = at + (lane >> 3) * step + (lane & 7);
+    float v = mine[0];
+    if (nwarps > 8) v += mine[8];
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return RowSums{__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 8), __shfl_sync(0xFFFFFFFFu, v, 16),
+                   __shfl_sync(0xFFFFFFFFu, v, 24)};
+}
+
+// What a row's outputs need: dh = inv * (g - a) - (h - mean) * inv * b + d_res, as pairs.
+struct RowCoefs {
+    uint64_t mean2, inv2, a2, b2;
+};
+__device__ __forceinline__ RowCoefs row_coefs(float mean, float var, float a, float products, const RowsParams& p) {
+    const float inv = rsqrtf(var + p.eps), b = -inv * (products * p.inv_n * inv);
+    return RowCoefs{pair(-mean, -mean), pair(inv, inv), pair(-a, -a), pair(b, b)};
+}
+
+// The four sums' terms of one pack, and Q's and C's around the mean.
+__device__ __forceinline__ void add_terms(const Pack& h, const Pack& d, const Pack& g, uint64_t& Q, uint64_t& G, uint64_t& C,
+                                          uint64_t& H) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t gi = mul2(d[i], g[i]);
+        H = add2(h[i], H);
+        Q = fma2(h[i], h[i], Q);
+        G = add2(gi, G);
+        C = fma2(gi, h[i], C);
+    }
+}
+__device__ __forceinline__ void add_centred(const Pack& h, const Pack& d, const Pack& g, uint64_t mean2, uint64_t& Q, uint64_t& C) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t c = add2(h[i], mean2);
+        Q = fma2(c, c, Q);
+        C = fma2(mul2(d[i], g[i]), c, C);
+    }
+}
+__device__ __forceinline__ void outputs(const Pack& h, const Pack& d, const Pack& g, const Pack& e, const RowCoefs& c, Pack& o,
+                                        Pack& dg) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t xh = mul2(add2(h[i], c.mean2), c.inv2);
+        o[i] = fma2(fma2(d[i], g[i], c.a2), c.inv2, fma2(xh, c.b2, e[i]));
+        dg[i] = fma2(d[i], xh, dg[i]);
+    }
+}
+
 // dbeta's sums: in registers up to two packs a thread, above in the thread's own words
 // of shared memory (with dgamma's they would not fit the 128 registers of 16 warps).
 template <int PPT, bool ONE, int THREADS, int BLOCKS>
@@ -195,11 +280,10 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_backward_rows_kerne
         produce(g, p);
         return;
     }
-    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5, nwarps = p.nt >> 5;
     const int P = p.N >> 3;
     const size_t step = (size_t)p.nt * 16;
     constexpr bool kRegs = PPT <= 2;
-    const Join join = make_join(p);
     float* const beta_sums = g.extra + p.N;
     // a thread reads only the words that it writes here: no barrier
     Pack dg[PPT], db[kRegs ? PPT : 1];
@@ -226,7 +310,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_backward_rows_kerne
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, buf ^= 1) {
         Pack dy[ONE ? 1 : PPT];
         uint4 dv[ONE ? PPT : 1], hv[PPT], ev[PPT];  // one rank's dy stays packed
-        uint64_t sum2 = 0ull;
+        uint64_t Q = 0ull, G = 0ull, C = 0ull, H = 0ull;
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
             if (k < p.slices) {
@@ -234,66 +318,53 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_backward_rows_kerne
                 ring_wait(&g.full[s], ph, g, p);
                 const uint8_t* at = g.stage + (size_t)s * p.stage_bytes + t * 16;
                 if (pk < P) {
+                    Pack h, gk;
+                    Pack& d = dy[ONE ? 0 : k];
+                    sum_ranks<ONE>(at, p.R, step, d);
                     if (ONE) dv[k] = *reinterpret_cast<const uint4*>(at);
-                    else sum_ranks<false>(at, p.R, step, dy[ONE ? 0 : k]);
                     hv[k] = *reinterpret_cast<const uint4*>(at + p.R * step);
                     if (p.has_res) ev[k] = *reinterpret_cast<const uint4*>(at + (p.R + 1) * step);
-                    Pack h;
                     unpack8(hv[k], h);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sum2 = add2(h[i], sum2);
+                    load8(g.extra + pk * 8, gk);
+                    add_terms(h, d, gk, Q, G, C, H);
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&g.empty[s]);
                 if (++s == p.stages) { s = 0; ph ^= 1u; }
             }
         }
-        float4* red = reinterpret_cast<float4*>(g.red) + buf * kRedWarps;
-        const float S = warp_sum(both(sum2));
-        const float own = S * join.own_inv_n;  // the warp's mean
-        const uint64_t own2 = pair(-own, -own);
-        uint64_t q2 = 0ull, g2 = 0ull, c2 = 0ull;
+        float* red = g.red + buf * (6 * kWarps);  // [Q, G, C, H, and Q, C around the mean][warp]
+        float v[4] = {both(Q), both(G), both(C), both(H)};
+        const float part = Reduced<4>::run(v);
+        if ((lane & 7) == 0) red[(lane >> 3) * kWarps + w] = part;
+        consumer_bar(p.nt);
+        const RowSums sums = block_sums(red, kWarps, nwarps);
+        const float mean = sums.H * p.inv_n;
+        float var = fmaf(sums.Q, p.inv_n, -mean * mean), products = fmaf(-mean, sums.G, sums.C);
+        if (!(mean * mean <= kSpread * var)) {
+            uint64_t cq = 0ull, cc = 0ull;
+            const uint64_t mean2 = pair(-mean, -mean);
 #pragma unroll
-        for (int k = 0; k < PPT; ++k) {
-            if (k < p.slices && t + k * p.nt < P) {
-                Pack gk, h;
-                unpack8(hv[k], h);
-                load8(g.extra + (t + k * p.nt) * 8, gk);
-                Pack& d = dy[ONE ? 0 : k];
-                if (ONE) unpack8(dv[k], d);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint64_t gi = mul2(d[i], gk[i]);
-                    h[i] = add2(h[i], own2);
-                    q2 = fma2(h[i], h[i], q2);
-                    g2 = add2(gi, g2);
-                    c2 = fma2(gi, h[i], c2);
+            for (int k = 0; k < PPT; ++k) {
+                if (k < p.slices && t + k * p.nt < P) {
+                    Pack h, gk;
+                    unpack8(hv[k], h);
+                    load8(g.extra + (t + k * p.nt) * 8, gk);
+                    Pack& d = dy[ONE ? 0 : k];
+                    if (ONE) unpack8(dv[k], d);
+                    add_centred(h, d, gk, mean2, cq, cc);
                 }
             }
+            const float q = warp_sum(both(cq)), c = warp_sum(both(cc));
+            if (lane == 0) {
+                red[4 * kWarps + w] = q;
+                red[5 * kWarps + w] = c;
+            }
+            consumer_bar(p.nt);
+            var = red_total(red + 4 * kWarps, nwarps) * p.inv_n;
+            products = red_total(red + 5 * kWarps, nwarps);
         }
-        // Q, G and C over the warp at once: with a step, lanes keep fewer of them
-        float Q = both(q2), G = both(g2), C = both(c2);
-        {
-            const bool hi = lane & 16, mid = lane & 8;
-            float v = (hi ? C : Q) + __shfl_xor_sync(0xFFFFFFFFu, hi ? Q : C, 16);
-            G += __shfl_xor_sync(0xFFFFFFFFu, G, 16);
-            v = (mid ? G : v) + __shfl_xor_sync(0xFFFFFFFFu, mid ? v : G, 8);
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            // lane 0: Q, lane 8: G, lane 16: C
-            float* to = reinterpret_cast<float*>(red + w);
-            if (lane == 0) *reinterpret_cast<float2*>(to) = make_float2(S, v);
-            if (lane == 8) to[2] = v;
-            if (lane == 16) to[3] = v;
-        }
-        consumer_bar(p.nt);
-        const float4 v = red[lane & (join.ways - 1)];
-        const float mean = join_sum(v.x, join.ways) * p.inv_n;
-        const float off = fmaf(v.x, join.inv_n, -mean);
-        const float inv = rsqrtf(join_sum(fmaf(join.n * off, off, v.y), join.ways) * p.inv_n + p.eps);
-        const float a = join_sum(v.z, join.ways) * p.inv_n;                          // mean(g)
-        const float b = join_sum(fmaf(v.z, off, v.w), join.ways) * p.inv_n * inv;    // mean(g xhat)
-        const uint64_t mean2 = pair(-mean, -mean), inv2 = pair(inv, inv), b2 = pair(-inv * b, -inv * b), a2 = pair(-a, -a);
+        const RowCoefs coefs = row_coefs(mean, var, sums.G * p.inv_n, products, p);
 #pragma unroll
         for (int k = 0; k < PPT; ++k) {
             if (k < p.slices) {
@@ -305,20 +376,16 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_backward_rows_kerne
                     if (p.has_res) unpack8(ev[k], e);
                     Pack& d = dy[ONE ? 0 : k];
                     if (ONE) unpack8(dv[k], d);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint64_t xh = mul2(add2(h[i], mean2), inv2);
-                        o[i] = fma2(fma2(d[i], gk[i], a2), inv2, fma2(xh, b2, e[i]));
-                        dg[k][i] = fma2(d[i], xh, dg[k][i]);
-                        if (kRegs) db[kRegs ? k : 0][i] = add2(db[kRegs ? k : 0][i], d[i]);
-                    }
+                    outputs(h, d, gk, e, coefs, o, dg[k]);
                     ptx::st_stream_v4(p.res_out + row * (int64_t)p.N + pk * 8, pack8(o));
-                    if (!kRegs && p.dbeta) {
-                        Pack v;
-                        load8(beta_sums + pk * 8, v);
+                    if (kRegs) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            reinterpret_cast<uint64_t*>(beta_sums + pk * 8)[i] = add2(v[i], d[i]);
+                        for (int i = 0; i < 4; ++i) db[kRegs ? k : 0][i] = add2(db[kRegs ? k : 0][i], d[i]);
+                    } else if (p.dbeta) {
+                        Pack b;
+                        load8(beta_sums + pk * 8, b);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) reinterpret_cast<uint64_t*>(beta_sums + pk * 8)[i] = add2(b[i], d[i]);
                     }
                 }
             }
@@ -350,26 +417,6 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_backward_rows_kerne
 // leaves 128 registers a thread: behind the barrier everyone has read the rows, so warp 0
 // sends the ring's next copies from there.
 constexpr int kSmallThreads = 512;  // threads an SM, at 128 registers
-
-template <int N>
-struct Reduced {
-    // Sums of N (a power of two) values over the warp; lane l ends up with the sum of value l / (32 / N).
-    // With each of the first steps a lane sends half of what it has and keeps the other half.
-    static __device__ __forceinline__ float run(float (&v)[N]) {
-        const int lane = threadIdx.x & 31;
-        int o = 16;
-#pragma unroll
-        for (int n = N; n > 1; n >>= 1, o >>= 1) {
-            const bool upper = lane & o;
-#pragma unroll
-            for (int i = 0; i < n / 2; ++i)
-                v[i] = (upper ? v[i + n / 2] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[i] : v[i + n / 2], o);
-        }
-        float t = v[0];
-        for (; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-        return t;
-    }
-};
 
 template <int PPT, int ROWS, bool ONE>
 __global__ void __launch_bounds__(256, 2) layernorm_backward_small_kernel(const __grid_constant__ RowsParams p) {
@@ -418,7 +465,6 @@ __global__ void __launch_bounds__(256, 2) layernorm_backward_small_kernel(const 
             reinterpret_cast<float4*>(g.extra)[pk * 2 + 1] = reinterpret_cast<const float4*>(p.gamma)[pk * 2 + 1];
         }
     }
-    const Join join = make_join(p);
     Pack dg[PPT], db[PPT];
 #pragma unroll
     for (int k = 0; k < PPT; ++k)
@@ -430,115 +476,104 @@ __global__ void __launch_bounds__(256, 2) layernorm_backward_small_kernel(const 
     for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < p.M; row0 += (int64_t)gridDim.x * ROWS, k0 += ROWS, buf ^= 1) {
         Pack dy[ONE ? 1 : ROWS][ONE ? 1 : PPT];
         uint4 dv[ONE ? ROWS : 1][ONE ? PPT : 1], hv[ROWS][PPT], ev[ROWS][PPT];
-        float sums[ROWS];
+        float v[4 * ROWS];  // Q, G, C, H of each row
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            const bool there = row0 + r < p.M;
-            if (there) ring_wait(&g.full[s], ph, g, p);
-            const uint8_t* at = g.stage + (size_t)s * p.stage_bytes;
-            uint64_t sum2 = 0ull;
+            uint64_t Q = 0ull, G = 0ull, C = 0ull, H = 0ull;
+            if (row0 + r < p.M) {
+                ring_wait(&g.full[s], ph, g, p);
+                const uint8_t* at = g.stage + (size_t)s * p.stage_bytes + t * 16;
 #pragma unroll
-            for (int k = 0; k < PPT; ++k) {
-                const int pk = t + k * p.nt;
-                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                const bool in = there && pk < P;
-                const uint8_t* a = at + (size_t)pk * 16;
-                hv[r][k] = in ? *reinterpret_cast<const uint4*>(a + p.R * bytes) : zero;
-                ev[r][k] = in && p.has_res ? *reinterpret_cast<const uint4*>(a + (p.R + 1) * bytes) : zero;
-                if (ONE) {
-                    dv[ONE ? r : 0][ONE ? k : 0] = in ? *reinterpret_cast<const uint4*>(a) : zero;
-                } else if (in) {
-                    sum_ranks<false>(a, p.R, bytes, dy[ONE ? 0 : r][ONE ? 0 : k]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) dy[ONE ? 0 : r][ONE ? 0 : k][i] = 0ull;
-                }
-                Pack h;
-                unpack8(hv[r][k], h);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sum2 = add2(h[i], sum2);
-            }
-            sums[r] = both(sum2);
-            if (++s == S) { s = 0; ph ^= 1u; }
-        }
-        const float mine = Reduced<ROWS>::run(sums);  // lane l: row l / (32 / ROWS)
-        float own[ROWS], v[4 * ROWS];
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            own[r] = __shfl_sync(0xFFFFFFFFu, mine, r * (32 / ROWS));  // the warp's sum of the row
-            const float mean = own[r] * join.own_inv_n;
-            const uint64_t own2 = pair(-mean, -mean);
-            uint64_t q2 = 0ull, g2 = 0ull, c2 = 0ull;
-#pragma unroll
-            for (int k = 0; k < PPT; ++k) {
-                if (t + k * p.nt < P) {
-                    Pack h, gk, d1;
-                    unpack8(hv[r][k], h);
-                    load8(g.extra + (t + k * p.nt) * 8, gk);
-                    if (ONE) unpack8(dv[ONE ? r : 0][ONE ? k : 0], d1);
-                    const Pack& d = ONE ? d1 : dy[ONE ? 0 : r][ONE ? 0 : k];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint64_t c = add2(h[i], own2), gi = mul2(d[i], gk[i]);
-                        q2 = fma2(c, c, q2);
-                        g2 = add2(gi, g2);
-                        c2 = fma2(gi, c, c2);
+                for (int k = 0; k < PPT; ++k, at += p.nt * 16) {
+                    const int pk = t + k * p.nt;
+                    if (pk < P) {
+                        Pack h, gk, d1;
+                        Pack& d = ONE ? d1 : dy[ONE ? 0 : r][ONE ? 0 : k];
+                        if (ONE) dv[ONE ? r : 0][ONE ? k : 0] = *reinterpret_cast<const uint4*>(at);
+                        hv[r][k] = *reinterpret_cast<const uint4*>(at + p.R * bytes);
+                        if (p.has_res) ev[r][k] = *reinterpret_cast<const uint4*>(at + (p.R + 1) * bytes);
+                        if (ONE) unpack8(dv[ONE ? r : 0][ONE ? k : 0], d);
+                        else sum_ranks<false>(at, p.R, bytes, d);
+                        unpack8(hv[r][k], h);
+                        load8(g.extra + pk * 8, gk);
+                        add_terms(h, d, gk, Q, G, C, H);
                     }
                 }
             }
-            v[r] = both(q2);
-            v[ROWS + r] = both(g2);
-            v[2 * ROWS + r] = both(c2);
-            v[3 * ROWS + r] = 0.f;
+            v[r] = both(Q);
+            v[ROWS + r] = both(G);
+            v[2 * ROWS + r] = both(C);
+            v[3 * ROWS + r] = both(H);
+            if (++s == S) { s = 0; ph ^= 1u; }
         }
-        // lane l: value l / (8 / ROWS) of Q, G, C of the rows; its rows' sums are known to every lane
-        const float part = Reduced<4 * ROWS>::run(v);
-        float* red = g.red + buf * (ROWS * 4 * 8);  // [statistic][row][warp]
+        const float part = Reduced<4 * ROWS>::run(v);  // lane l: value l / (8 / ROWS)
+        float* red = g.red + buf * (ROWS * 6 * 8);  // [statistic][row][warp]
         constexpr int kPer = 8 / ROWS;
-        if (lane % kPer == 0 && lane / kPer < 3 * ROWS) red[(lane / kPer) * 8 + w] = part;
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r)
-            if (lane == 31) red[(3 * ROWS + r) * 8 + w] = own[r];
+        if (lane % kPer == 0) red[(lane / kPer) * 8 + w] = part;
         __syncthreads();
         if (w == 0) {
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) send(k0 + S + r);
         }
-        // the join: eight lanes a row, a warp's sums in each
-        const int jr = (lane >> 3) & (ROWS - 1), jw = lane & 7;
-        const bool counts = jw < nwarps;
-        const float Q = red[jr * 8 + jw], G = red[(ROWS + jr) * 8 + jw], C = red[(2 * ROWS + jr) * 8 + jw],
-                    H = red[(3 * ROWS + jr) * 8 + jw];
-        const float n = counts ? join.n : 0.f, inv_n = counts ? join.inv_n : 0.f;
-        const float mean = join_sum(H, 8) * p.inv_n;
-        const float off = fmaf(H, inv_n, -mean);
-        const float inv = rsqrtf(join_sum(fmaf(n * off, off, Q), 8) * p.inv_n + p.eps);
-        const float a = join_sum(G, 8) * p.inv_n;                          // mean(g)
-        const float b = join_sum(fmaf(G, off, C), 8) * p.inv_n * inv;      // mean(g xhat)
-        const float neg = -inv * b;
+        float mean[ROWS], var[ROWS], a[ROWS], products[ROWS];
+        bool far = false;  // the same in every thread of the block
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            const float rm = -__shfl_sync(0xFFFFFFFFu, mean, r * 8), ri = __shfl_sync(0xFFFFFFFFu, inv, r * 8),
-                        ra = -__shfl_sync(0xFFFFFFFFu, a, r * 8), rb = __shfl_sync(0xFFFFFFFFu, neg, r * 8);
+            const RowSums sums = block_sums(red + r * 8, ROWS * 8, nwarps);
+            mean[r] = sums.H * p.inv_n;
+            var[r] = fmaf(sums.Q, p.inv_n, -mean[r] * mean[r]);
+            a[r] = sums.G * p.inv_n;
+            products[r] = fmaf(-mean[r], sums.G, sums.C);
+            far |= !(mean[r] * mean[r] <= kSpread * var[r]);
+        }
+        if (far) {
+            float* again = red + 4 * ROWS * 8;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                uint64_t cq = 0ull, cc = 0ull;
+                const uint64_t mean2 = pair(-mean[r], -mean[r]);
+#pragma unroll
+                for (int k = 0; k < PPT; ++k) {
+                    if (row0 + r < p.M && t + k * p.nt < P) {
+                        Pack h, gk, d1;
+                        unpack8(hv[r][k], h);
+                        load8(g.extra + (t + k * p.nt) * 8, gk);
+                        if (ONE) unpack8(dv[ONE ? r : 0][ONE ? k : 0], d1);
+                        add_centred(h, ONE ? d1 : dy[ONE ? 0 : r][ONE ? 0 : k], gk, mean2, cq, cc);
+                    }
+                }
+                const float q = warp_sum(both(cq)), c = warp_sum(both(cc));
+                if (lane == 0) {
+                    again[r * 8 + w] = q;
+                    again[(ROWS + r) * 8 + w] = c;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                if (!(mean[r] * mean[r] <= kSpread * var[r])) {
+                    var[r] = red_total(again + r * 8, nwarps) * p.inv_n;
+                    products[r] = red_total(again + (ROWS + r) * 8, nwarps);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
             if (row0 + r >= p.M) continue;
-            const uint64_t mean2 = pair(rm, rm), inv2 = pair(ri, ri), a2 = pair(ra, ra), b2 = pair(rb, rb);
+            const RowCoefs coefs = row_coefs(mean[r], var[r], a[r], products[r], p);
 #pragma unroll
             for (int k = 0; k < PPT; ++k) {
                 const int pk = t + k * p.nt;
                 if (pk < P) {
-                    Pack h, gk, e, o, d1;
+                    Pack h, gk, e = {}, o, d1;
                     unpack8(hv[r][k], h);
-                    unpack8(ev[r][k], e);
+                    if (p.has_res) unpack8(ev[r][k], e);
                     load8(g.extra + pk * 8, gk);
                     if (ONE) unpack8(dv[ONE ? r : 0][ONE ? k : 0], d1);
                     const Pack& d = ONE ? d1 : dy[ONE ? 0 : r][ONE ? 0 : k];
+                    outputs(h, d, gk, e, coefs, o, dg[k]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint64_t xh = mul2(add2(h[i], mean2), inv2);
-                        o[i] = fma2(fma2(d[i], gk[i], a2), inv2, fma2(xh, b2, e[i]));
-                        dg[k][i] = fma2(d[i], xh, dg[k][i]);
-                        db[k][i] = add2(db[k][i], d[i]);
-                    }
+                    for (int i = 0; i < 4; ++i) db[k][i] = add2(db[k][i], d[i]);
                     ptx::st_stream_v4(p.res_out + (row0 + r) * (int64_t)p.N + pk * 8, pack8(o));
                 }
             }
@@ -614,7 +649,7 @@ RowsPlan layernorm_plan(RowsParams& p, int num_sms) {
         p.nt = one_nt;
         p.slices = ppt;
         p.extra_words = p.N;
-        p.red_words = 2 * p.rows * 4 * 8;
+        p.red_words = 2 * p.rows * 6 * 8;
         p.stage_bytes = p.nsrc * p.N * 2;
         const int64_t items = (p.M + p.rows - 1) / p.rows, rounds = (items + num_sms - 1) / num_sms;
         const int blocks = (int)std::min<int64_t>(rounds, std::min(kSmallThreads / p.nt, 10));

@@ -49,13 +49,20 @@ def layernorm_backward64(dys, h, gamma, dres):
     dy, mag = x.sum(0), x.abs().sum(0)
     h, gm = h.double(), gamma.double()
     M = h.shape[0]
-    _, inv, rel, xhat, tol_x = stats64(h, h.abs())
+    mean, inv, rel, xhat, tol_x = stats64(h, h.abs())
     g, gmag = dy * gm, mag * gm.abs()
+    # a row with mean^2 <= 4 var has var = mean(h^2) - mean^2 and the products' sum less mean * sum g: the sums' errors are
+    # relative to terms up to 5 var; mean(h^2) is off by 64 U of it, mean^2 by 2 |mean| * 64 U mean|h| and a rounding
+    near = mean * mean <= 4.1 * (1 / (inv * inv) - EPS)
+    lost = torch.where(near, 193 * U * (h * h).mean(1, keepdim=True) * inv * inv, 0.0)
+    rel, tol_x = rel + lost, tol_x + lost * xhat.abs()
     a, b = g.mean(1, keepdim=True), (g * xhat).mean(1, keepdim=True)
     dh = inv * (g - a - xhat * b)
     n = (len(dys) + 64) * U
     tol_a = n * gmag.mean(1, keepdim=True)
     tol_b = n * (gmag * xhat.abs()).mean(1, keepdim=True) + (gmag * tol_x).mean(1, keepdim=True) + rel * b.abs()
+    tol_b = tol_b + torch.where(near, inv * (n * (gmag * h.abs()).mean(1, keepdim=True) + n * mean.abs() * gmag.mean(1, keepdim=True)
+                                             + 66 * U * a.abs() * h.abs().mean(1, keepdim=True)), 0.0)
     tol = inv * (n * gmag + tol_a + xhat.abs() * tol_b + tol_x * b.abs()) + (rel + 8 * U) * inv * (
         gmag + a.abs() + xhat.abs() * b.abs())
     if dres is not None:

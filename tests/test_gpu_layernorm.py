@@ -152,6 +152,25 @@ def test_backward_against_64_bits(ws, R, M, N, dres):
     assert torch.equal(backward(ws, dy, h, gamma, e, False, False)[0], got[0])
 
 
+@pytest.mark.parametrize("R", [1, 3])
+@pytest.mark.parametrize("N", [64, 1000, 2056, 4096, 7168, 16384])
+def test_backward_of_means_large_against_the_spread(ws, N, R):
+    """Rows of 1000 +- 4 between rows of 3 +- 3 (next to the border of the two formulas) and 0 +- 3: the first kind is summed
+    again around its mean, and neither kind changes its bits with what its neighbours are."""
+    M = 1500
+    dy, h, gamma, e = backward_inputs(R, M, N, 3 * N + R)
+    x = h.float() / 3
+    kind = torch.arange(M, device="cuda") % 3
+    near = torch.where(kind[:, None] == 0, x * 3 + 6, x * 3).to(torch.bfloat16)
+    h = torch.where(kind[:, None] == 2, (x * 4 + 1000).to(torch.bfloat16), near)
+    got = backward(ws, dy, h, gamma, e)
+    want = ref.layernorm_backward64(dy, h, gamma, e)
+    for g, w, tol, what in zip(got, want[::2], want[1::2], ("dh", "dgamma", "dbeta")):
+        ref.check(g, w, tol, what)
+    alone = backward(ws, dy, near, gamma, e)[0]
+    assert torch.equal(alone[kind != 2], got[0][kind != 2])
+
+
 def test_backward_against_differences(ws):
     """The gradient of L = sum(dy * y) + sum(dres * h) by central differences of the forward formula in 64 bits."""
     dy, h, gamma, e = backward_inputs(3, 4, 96, 77)
