@@ -271,12 +271,20 @@ cudaError_t launch_embedding(const EmbedParams& p, int* grid, cudaStream_t strea
 cudaError_t launch_embedding_backward(EmbedParams& p, void* sort, float* scratch, int num_sms, int* grid, cudaStream_t stream);
 
 // ------------------------------------------------------------------ cross entropy (cross_entropy.cu)
-enum XentPass : int { kXentLogSum = 0, kXentDLogits = 1, kXentDH = 2, kXentDW = 3 };
+enum XentPass : int { kXentLogSum = 0, kXentDLogits = 1, kXentDH = 2, kXentDW = 3, kXentGrads = 4 };
+
+struct XentGrid {
+    int tiles_m, tiles_n;  // 256 x 256
+    int splits;            // parts of the contraction
+    int num_kb;            // its blocks of 64
+    int units;             // tiles_m * tiles_n * splits (set at the launch)
+};
 
 struct XentParams {
-    CUtensorMap tmA, tmB;         // A; B of kXentDW (h)
+    CUtensorMap tmA, tmA2, tmB;   // A; kXentDW's A (d) and B (h)
     CUtensorMap tmW[kMaxRanks];   // B of the others: the ranks' weights
-    CUtensorMap tmOut[kMaxRanks]; // d, dh or its sums, or the ranks' dW
+    CUtensorMap tmOut[kMaxRanks]; // d, or the ranks' dW
+    CUtensorMap tmDH;             // dh or its sums
     const void* targets;
     const float* lse;
     const float* dloss;
@@ -284,10 +292,10 @@ struct XentParams {
     float* target_logit;          // [M]
     DevStatus* status;
     int64_t vocab;                // columns of all ranks that count
-    int M, K, Vs;
+    int M, K, Vs, R;
     int wide;                     // targets of 64 bits
     int rank_tiles, tile0;        // vocabulary tiles of a rank; the piece's first
-    int tiles_m, tiles_n, splits, num_kb;
+    XentGrid grid[2];             // the second: kXentDW's in kXentGrads
     int a_rows;                   // rows of A that a copy takes: 128, fewer if M is less
     int group;                    // rows of tiles taken together
     int units;                    // (set at the launch)

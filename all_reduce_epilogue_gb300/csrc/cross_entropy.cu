@@ -14,7 +14,8 @@
 //             buffer holds pairs for.
 //   kDLogits  z again, whose epilogue leaves d for one piece of the vocabulary, in bf16;
 //   kDH       d W, in fp32 sums over the pieces;
-//   kDW       d^T h, rounded to bf16 once.
+//   kDW       d^T h, rounded to bf16 once; the tiles of both in one launch (kGrads), the
+//             long ones of kDH first.
 // d is rounded to bf16 because that is what the tensor cores multiply at their rate: half
 // a step, 2^-8 of a term, at random in sums of many terms, which is below the rounding of
 // the bf16 results; fp32's substitute tf32 runs at half the rate.  Maxima, sums, lse and all sums
@@ -51,12 +52,9 @@ constexpr size_t kSmem = 1024 + (size_t)kStagesX * kStageBytes + 8 * (size_t)kBo
 static_assert(kSmem <= 232448, "shared memory budget");
 constexpr float kLog2e = 1.4426950408889634f;
 
-__host__ __device__ constexpr bool a_across(int pass) { return pass == kXentDW; }
-__host__ __device__ constexpr bool b_across(int pass) { return pass == kXentDH || pass == kXentDW; }
-
 // Instruction descriptor: D fp32, A and B bf16, which of them lie across the contraction, N = 256, M = 256 (pair).
-__host__ __device__ constexpr uint32_t idesc(int pass) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_across(pass) ? 1u : 0u) << 15) | ((b_across(pass) ? 1u : 0u) << 16) |
+__device__ __forceinline__ uint32_t idesc(bool a_across, bool b_across) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_across << 15) | ((uint32_t)b_across << 16) |
            ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
 }
 
@@ -93,23 +91,31 @@ __device__ __noinline__ void drain(uint64_t* bar, uint32_t parity, const XentPar
 }
 
 struct Tile {
+    int kind;      // which product: kXentLogSum, kXentDLogits, kXentDH, kXentDW
     int tm, tn, split;
     int kb0, kb1;  // its part of the contraction, in blocks of 64
 };
 
-// Order of the tiles: a split's tiles together; inside, groups of p.group rows of tiles, column by column.
+// Order of the tiles: the first grid's, then the second's; in a grid a split's tiles together; inside, groups of p.group
+// rows of tiles, column by column.
+template <int PASS>
 __device__ __forceinline__ Tile tile_of(const XentParams& p, int u) {
     Tile t;
-    const int per = p.tiles_m * p.tiles_n;
+    t.kind = PASS;
+    if (PASS == kXentGrads) t.kind = u < p.grid[0].units ? kXentDH : kXentDW;
+    const bool second = PASS == kXentGrads && u >= p.grid[0].units;
+    const XentGrid& g = p.grid[second ? 1 : 0];
+    if (second) u -= p.grid[0].units;
+    const int per = g.tiles_m * g.tiles_n;
     t.split = u / per;
     u -= t.split * per;
-    const int per_group = p.group * p.tiles_n, g = u / per_group, first = g * p.group;
-    const int rows = min(p.tiles_m - first, p.group);
-    u -= g * per_group;
+    const int per_group = p.group * g.tiles_n, n = u / per_group, first = n * p.group;
+    const int rows = min(g.tiles_m - first, p.group);
+    u -= n * per_group;
     t.tm = first + u % rows;
     t.tn = u / rows;
-    t.kb0 = (int)((int64_t)p.num_kb * t.split / p.splits);
-    t.kb1 = (int)((int64_t)p.num_kb * (t.split + 1) / p.splits);
+    t.kb0 = (int)((int64_t)g.num_kb * t.split / g.splits);
+    t.kb1 = (int)((int64_t)g.num_kb * (t.split + 1) / g.splits);
     return t;
 }
 
@@ -191,6 +197,14 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
         ptx::tmem_alloc_pair(tmem_slot, 512);
         ptx::tmem_relinquish_pair();
     }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tmap(&p.tmA);
+        for (int r = 0; r < p.R; ++r) ptx::prefetch_tmap(&p.tmW[r]);
+        if (PASS == kXentGrads) {
+            ptx::prefetch_tmap(&p.tmA2);
+            ptx::prefetch_tmap(&p.tmB);
+        }
+    }
     __syncwarp();
     ptx::tc_fence_before();
     ptx::cluster_sync();
@@ -207,12 +221,13 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
         uint32_t ph = 0, issued = 0, issued_ph = 0;
         bool aborted = false;
         for (int u = first; u < p.units && !aborted; u += pairs) {
-            const Tile t = tile_of(p, u);
-            const Place at = place_of(p, PASS == kXentDW ? t.tm : t.tn);
+            const Tile t = tile_of<PASS>(p, u);
+            const bool dh = PASS == kXentGrads && t.kind == kXentDH, dw = PASS == kXentGrads && !dh;
+            const Place at = place_of(p, PASS == kXentGrads ? 0 : t.tn);
             const int a0 = t.tm * kTile + q * 128, b0 = t.tn * kTile + q * 128;
             // rows of A behind the last one are not loaded: whatever the buffers hold, it enters no other row's sums
-            const bool has_a = a_across(PASS) || a0 < p.M, both_a = a_across(PASS) || t.tm * kTile + 128 < p.M;
-            const uint32_t a_bytes = a_across(PASS) ? kHalf : (uint32_t)p.a_rows * 128;
+            const bool has_a = dw || a0 < p.M, both_a = dw || t.tm * kTile + 128 < p.M;
+            const uint32_t a_bytes = dw ? kHalf : (uint32_t)p.a_rows * 128;
             for (int kb = t.kb0; kb < t.kb1; ++kb) {
                 const bool ok = wait(&empty[stage], ph ^ 1u, abort_flag, p, 30, u);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -225,19 +240,20 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                     if (q == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kHalf + (both_a ? 2 * a_bytes : a_bytes));
                     uint8_t *a = sA + stage * kHalf, *b = sB + stage * kHalf;
                     const int k = kb * 64;
-                    if (PASS == kXentLogSum || PASS == kXentDLogits) {
-                        if (has_a) ptx::tma_load_2d_pair(a, &p.tmA, fb, k, a0, pol);
-                        ptx::tma_load_2d_pair(b, &p.tmW[at.rank], fb, k, at.col + q * 128, pol);
-                    } else if (PASS == kXentDH) {
-                        if (has_a) ptx::tma_load_2d_pair(a, &p.tmA, fb, k, a0, pol);
-                        const Place w = place_of(p, kb >> 2);
-                        const int v = w.col + (kb & 3) * 64;
-                        for (int i = 0; i < 2; ++i)
-                            ptx::tma_load_2d_pair(b + i * 8192, &p.tmW[w.rank], fb, b0 + i * 64, v, pol);
-                    } else {
+                    if (dw) {
                         for (int i = 0; i < 2; ++i) {
-                            ptx::tma_load_2d_pair(a + i * 8192, &p.tmA, fb, a0 + i * 64, k, pol);
+                            ptx::tma_load_2d_pair(a + i * 8192, &p.tmA2, fb, a0 + i * 64, k, pol);
                             ptx::tma_load_2d_pair(b + i * 8192, &p.tmB, fb, b0 + i * 64, k, pol);
+                        }
+                    } else {
+                        if (has_a) ptx::tma_load_2d_pair(a, &p.tmA, fb, k, a0, pol);
+                        if (dh) {
+                            const Place w = place_of(p, kb >> 2);
+                            const int v = w.col + (kb & 3) * 64;
+                            for (int i = 0; i < 2; ++i)
+                                ptx::tma_load_2d_pair(b + i * 8192, &p.tmW[w.rank], fb, b0 + i * 64, v, pol);
+                        } else {
+                            ptx::tma_load_2d_pair(b, &p.tmW[at.rank], fb, k, at.col + q * 128, pol);
                         }
                     }
                 }
@@ -261,13 +277,16 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
             const bool issuer = ptx::elect_one();
             int stage = 0, it = 0;
             uint32_t ph = 0;
-            // along the contraction: rows of 128 bytes, 32 of them a step; across: two groups of 64 columns, 16 rows a step
-            const uint64_t adesc = sdesc(ptx::smem_u32(sA), a_across(PASS) ? 8192 : 16, 1024);
-            const uint64_t bdesc = sdesc(ptx::smem_u32(sB), b_across(PASS) ? 8192 : 16, 1024);
-            constexpr int kStepA = a_across(PASS) ? 128 : 2, kStepB = b_across(PASS) ? 128 : 2;
+            constexpr bool kAcrossB = PASS == kXentGrads;
             bool ok = true;
             for (int u = first; u < p.units && ok; u += pairs, ++it) {
-                const Tile t = tile_of(p, u);
+                const Tile t = tile_of<PASS>(p, u);
+                // along the contraction: rows of 128 bytes, 32 of them a step; across: two groups of 64 columns, 16 rows a step
+                const bool across_a = PASS == kXentGrads && t.kind == kXentDW;
+                const uint64_t adesc = sdesc(ptx::smem_u32(sA), across_a ? 8192 : 16, 1024);
+                const uint64_t bdesc = sdesc(ptx::smem_u32(sB), kAcrossB ? 8192 : 16, 1024);
+                const int step_a = across_a ? 128 : 2, step_b = kAcrossB ? 128 : 2;
+                const uint32_t id = idesc(across_a, kAcrossB);
                 const int buf = it & 1;
                 ok = __all_sync(0xFFFFFFFFu, wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, p, 31, u));
                 if (!ok) break;
@@ -281,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                         const uint64_t ad = adesc + (uint64_t)(stage * (kHalf >> 4)), bd = bdesc + (uint64_t)(stage * (kHalf >> 4));
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            ptx::umma_bf16_pair(d, ad + (uint64_t)(kk * kStepA), bd + (uint64_t)(kk * kStepB), idesc(PASS),
+                            ptx::umma_bf16_pair(d, ad + (uint64_t)(kk * step_a), bd + (uint64_t)(kk * step_b), id,
                                                 kb != t.kb0 || kk != 0);
                         ptx::umma_commit_pair_multicast(&empty[stage], 0x3);
                         if (kb == t.kb1 - 1) ptx::umma_commit_pair_multicast(&tfull[buf], 0x3);
@@ -300,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
         Stager out{sOut + w * 2 * kBox, 0};
         int it = 0;
         for (int u = first; u < p.units; u += pairs, ++it) {
-            const Tile t = tile_of(p, u);
+            const Tile t = tile_of<PASS>(p, u);
             const int buf = it & 1;
             if (!__all_sync(0xFFFFFFFFu, wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, abort_flag, p, 33, u))) break;
             ptx::tc_fence_after();
@@ -346,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                     }
                     __syncwarp();
                 }
-                if (in) p.stats[(size_t)m * p.tiles_n + t.tn] = make_float2(top, sum);
+                if (in) p.stats[(size_t)m * p.grid[0].tiles_n + t.tn] = make_float2(top, sum);
             } else if (PASS == kXentDLogits) {
                 const Place at = place_of(p, t.tn);
                 const int cols = columns_of(p, at);
@@ -402,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                     }
                     __syncwarp();
                 }
-            } else if (PASS == kXentDH && p.sums) {
+            } else if (t.kind == kXentDH && p.sums) {
                 // fp32 sums of this split, over the pieces
                 for (int c = 0; c < kTile && t.tn * kTile + c < p.K; c += 32) {
                     uint32_t v[32];
@@ -415,8 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                     __syncwarp();
                     if (lane == 0) {
                         if (m0 < p.M) {
-                            if (p.add) ptx::tma_add_3d(&p.tmOut[0], box, t.tn * kTile + c, m0, t.split);
-                            else ptx::tma_store_3d(&p.tmOut[0], box, t.tn * kTile + c, m0, t.split);
+                            if (p.add) ptx::tma_add_3d(&p.tmDH, box, t.tn * kTile + c, m0, t.split);
+                            else ptx::tma_store_3d(&p.tmDH, box, t.tn * kTile + c, m0, t.split);
                         }
                         ptx::bulk_commit();
                     }
@@ -424,10 +443,11 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                 }
             } else {
                 // bf16 results: rows of dh, or of a rank's dW
-                const Place at = place_of(p, PASS == kXentDW ? t.tm : 0);
-                const int r0 = PASS == kXentDW ? at.col + q * 128 + w * 32 : m0;
-                const bool store = r0 < (PASS == kXentDW ? p.Vs : p.M);
-                const CUtensorMap* map = &p.tmOut[PASS == kXentDW ? at.rank : 0];
+                const bool dw = t.kind == kXentDW;
+                const Place at = place_of(p, dw ? t.tm : 0);
+                const int r0 = dw ? at.col + q * 128 + w * 32 : m0;
+                const bool store = r0 < (dw ? p.Vs : p.M);
+                const CUtensorMap* map = dw ? &p.tmOut[at.rank] : &p.tmDH;
                 for (int c = 0; c < kTile && t.tn * kTile + c < p.K; c += 64) {
                     uint8_t* box = out.next();
 #pragma unroll
@@ -535,7 +555,8 @@ __global__ void __launch_bounds__(256) xent_dh_kernel(const float4* sums, uint2*
 
 template <int PASS>
 cudaError_t launch(XentParams& p, int clusters, cudaStream_t s) {
-    p.units = p.tiles_m * p.tiles_n * p.splits;
+    p.units = 0;
+    for (XentGrid& g : p.grid) p.units += g.units = g.tiles_m * g.tiles_n * g.splits;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -559,7 +580,7 @@ int ceil256(int64_t n) { return (int)((n + kTile - 1) / kTile); }
 
 cudaError_t xent_prepare(int* clusters) {
     cudaError_t e = cudaSuccess;
-    for (auto* f : {xent_kernel<kXentLogSum>, xent_kernel<kXentDLogits>, xent_kernel<kXentDH>, xent_kernel<kXentDW>})
+    for (auto* f : {xent_kernel<kXentLogSum>, xent_kernel<kXentDLogits>, xent_kernel<kXentGrads>})
         if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
@@ -606,7 +627,7 @@ static void common(XentParams& p, const XentCall& c, const XentBuffers& b) {
     p.wide = c.wide;
     p.status = b.status;
     p.timeout_ns = b.timeout_ns;
-    p.splits = 1;
+    p.R = c.R;
     p.group = kGroup;
     p.a_rows = 8;
     while (p.a_rows < 128 && p.a_rows < c.M) p.a_rows *= 2;
@@ -624,16 +645,16 @@ cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStr
     p.stats = static_cast<float2*>(b.d);
     float2* carry = static_cast<float2*>(b.rows);
     p.target_logit = reinterpret_cast<float*>(carry + c.M);
-    p.tiles_m = ceil256(c.M);
-    p.num_kb = (int)((c.K + 63) / 64);
-    for (p.tile0 = 0; p.tile0 < total && e == cudaSuccess; p.tile0 += p.tiles_n) {
-        p.tiles_n = std::min(fit, total - p.tile0);
+    XentGrid& g = p.grid[0];
+    g = XentGrid{ceil256(c.M), 0, 1, (int)((c.K + 63) / 64), 0};
+    for (p.tile0 = 0; p.tile0 < total && e == cudaSuccess; p.tile0 += g.tiles_n) {
+        g.tiles_n = std::min(fit, total - p.tile0);
         e = launch<kXentLogSum>(p, b.clusters, s);
         if (p.tile0 == 0) *grid = 2 * std::min(p.units, b.clusters);
         if (e != cudaSuccess) return e;
         e = launch_dependent(xent_join_kernel, dim3((unsigned)((c.M + 7) / 8)), 256, 0, s, p.stats, carry, p.target_logit,
-                             c.targets, c.wide, c.vocab, c.loss, c.lse, (int)c.M, p.tiles_n, p.tile0 == 0,
-                             p.tile0 + p.tiles_n == total);
+                             c.targets, c.wide, c.vocab, c.loss, c.lse, (int)c.M, g.tiles_n, p.tile0 == 0,
+                             p.tile0 + g.tiles_n == total);
     }
     return e;
 }
@@ -643,50 +664,45 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
     common(z, c, b);
     z.lse = c.lse;
     z.dloss = c.dloss;
-    z.tiles_m = ceil256(c.M);
-    z.num_kb = (int)((c.K + 63) / 64);
-    XentParams dh = z, dw = z;
-    const int total = c.R * z.rank_tiles, tiles_k = ceil256(c.K);
+    XentParams d = z;  // the products with it
+    const int total = c.R * z.rank_tiles, tiles_m = ceil256(c.M), tiles_k = ceil256(c.K);
     const int most = (int)std::min<int64_t>(total, (int64_t)(b.sizes.d_bytes / ((size_t)c.M * kTile * 2)));
     const int even = (total + most - 1) / most, piece = (total + even - 1) / even;
     const int pieces = (total + piece - 1) / piece, left = total - (pieces - 1) * piece;  // the last piece's tiles, 1..piece
     cudaError_t e = make_tmap_bf16(&z.tmA, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, z.a_rows);
     for (int r = 0; r < c.R && e == cudaSuccess; ++r) {
         e = make_tmap_bf16(&z.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 128);
-        if (e == cudaSuccess && c.dh) e = make_tmap_bf16(&dh.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 64);
-        if (e == cudaSuccess && c.has_dw) e = make_tmap_bf16(&dw.tmOut[r], c.dw[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 32);
+        if (e == cudaSuccess) e = make_tmap_bf16(&d.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 64);
+        if (e == cudaSuccess && c.has_dw) e = make_tmap_bf16(&d.tmOut[r], c.dw[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 32);
     }
-    if (e == cudaSuccess && c.has_dw) e = make_tmap_bf16(&dw.tmB, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, 64);
-    dh.tiles_n = tiles_k;
-    dh.splits = dh_splits(dh.tiles_m * tiles_k, b.clusters,
-                          (int)std::min({(int64_t)(b.sizes.sum_bytes / ((size_t)c.M * c.K * 4)), (int64_t)piece / 2, (int64_t)4 * left}));
-    dh.sums = pieces > 1 || dh.splits > 1;
+    if (e == cudaSuccess) e = make_tmap_bf16(&d.tmB, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, 64);
+    const int splits = dh_splits(tiles_m * tiles_k, b.clusters,
+                                 (int)std::min({(int64_t)(b.sizes.sum_bytes / ((size_t)c.M * c.K * 4)), (int64_t)piece / 2, (int64_t)4 * left}));
+    d.sums = pieces > 1 || splits > 1;
     if (e == cudaSuccess && c.dh)
-        e = dh.sums ? make_tmap_f32_3d(&dh.tmOut[0], b.sums, (uint64_t)c.K, (uint64_t)c.M, (uint64_t)dh.splits, 32, 32)
-                    : make_tmap_bf16(&dh.tmOut[0], c.dh, (uint64_t)c.K, (uint64_t)c.M, 64, 32);
-    dw.tiles_n = tiles_k;
-    dw.num_kb = (int)((c.M + 63) / 64);
+        e = d.sums ? make_tmap_f32_3d(&d.tmDH, b.sums, (uint64_t)c.K, (uint64_t)c.M, (uint64_t)splits, 32, 32)
+                   : make_tmap_bf16(&d.tmDH, c.dh, (uint64_t)c.K, (uint64_t)c.M, 64, 32);
     for (int t0 = 0; t0 < total && e == cudaSuccess; t0 += piece) {
         const int n = std::min(piece, total - t0);
-        z.tile0 = dh.tile0 = dw.tile0 = t0;
-        z.tiles_n = dw.tiles_m = n;
-        dh.num_kb = 4 * n;
+        z.tile0 = d.tile0 = t0;
+        z.grid[0] = XentGrid{tiles_m, n, 1, (int)((c.K + 63) / 64), 0};
+        if (c.dh) d.grid[0] = XentGrid{tiles_m, tiles_k, splits, 4 * n, 0};
+        if (c.has_dw) d.grid[1] = XentGrid{n, tiles_k, 1, (int)((c.M + 63) / 64), 0};
         const uint64_t cols = (uint64_t)n * kTile;
         if (t0 == 0 || n != piece) {  // the piece's d [M, cols]: as an output, along and across the contraction
             e = make_tmap_bf16(&z.tmOut[0], b.d, cols, (uint64_t)c.M, 64, 32);
-            if (e == cudaSuccess) e = make_tmap_bf16(&dh.tmA, b.d, cols, (uint64_t)c.M, 64, dh.a_rows);
-            if (e == cudaSuccess) e = make_tmap_bf16(&dw.tmA, b.d, cols, (uint64_t)c.M, 64, 64);
+            if (e == cudaSuccess) e = make_tmap_bf16(&d.tmA, b.d, cols, (uint64_t)c.M, 64, d.a_rows);
+            if (e == cudaSuccess) e = make_tmap_bf16(&d.tmA2, b.d, cols, (uint64_t)c.M, 64, 64);
         }
         if (e == cudaSuccess) e = launch<kXentDLogits>(z, b.clusters, s);
         if (t0 == 0) *grid = 2 * std::min(z.units, b.clusters);
-        dh.add = t0 > 0;
-        if (e == cudaSuccess && c.dh) e = launch<kXentDH>(dh, b.clusters, s);
-        if (e == cudaSuccess && c.has_dw) e = launch<kXentDW>(dw, b.clusters, s);
+        d.add = t0 > 0;
+        if (e == cudaSuccess) e = launch<kXentGrads>(d, b.clusters, s);
     }
-    if (e == cudaSuccess && c.dh && dh.sums) {
+    if (e == cudaSuccess && c.dh && d.sums) {
         const int64_t quads = c.M * c.K / 4;
         e = launch_dependent(xent_dh_kernel, dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 16 * b.clusters)), 256, 0, s,
-                             static_cast<const float4*>(b.sums), reinterpret_cast<uint2*>(c.dh), quads, dh.splits);
+                             static_cast<const float4*>(b.sums), reinterpret_cast<uint2*>(c.dh), quads, splits);
     }
     return e;
 }
