@@ -294,6 +294,7 @@ struct XentParams {
     int64_t vocab;                // columns of all ranks that count
     int M, K, Vs, R;
     int wide;                     // targets of 64 bits
+    int tile;                     // columns of a vocabulary tile: 256, or 128 of one CTA
     int rank_tiles, tile0;        // vocabulary tiles of a rank; the piece's first
     XentGrid grid[2];             // the second: kXentDW's in kXentGrads
     int a_rows;                   // rows of A that a copy takes: 128, fewer if M is less

@@ -52,10 +52,10 @@ constexpr size_t kSmem = 1024 + (size_t)kStagesX * kStageBytes + 8 * (size_t)kBo
 static_assert(kSmem <= 232448, "shared memory budget");
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Instruction descriptor: D fp32, A and B bf16, which of them lie across the contraction, N = 256, M = 256 (pair).
-__device__ __forceinline__ uint32_t idesc(bool a_across, bool b_across) {
+// Instruction descriptor: D fp32, A and B bf16, which of them lie across the contraction, `side` rows and columns.
+__device__ __forceinline__ uint32_t idesc(bool a_across, bool b_across, int side) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_across << 15) | ((uint32_t)b_across << 16) |
-           ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+           ((uint32_t)(side >> 3) << 17) | ((uint32_t)(side >> 4) << 24);
 }
 
 // Shared-memory matrix descriptor: 128B swizzle, tcgen05 version bit.
@@ -119,18 +119,18 @@ __device__ __forceinline__ Tile tile_of(const XentParams& p, int u) {
     return t;
 }
 
-// A vocabulary tile (256 columns of one rank) of the piece: the rank, and its first column there.
+// A vocabulary tile (p.tile columns of one rank) of the piece: the rank, and its first column there.
 struct Place {
     int rank, col;
 };
 __device__ __forceinline__ Place place_of(const XentParams& p, int tile) {
     const int v = p.tile0 + tile, r = v / p.rank_tiles;
-    return Place{r, (v - r * p.rank_tiles) * kTile};
+    return Place{r, (v - r * p.rank_tiles) * p.tile};
 }
-// Columns of the tile that are in the vocabulary, 0..256.
-__device__ __forceinline__ int columns_of(const XentParams& p, const Place& at) {
+// Columns of the tile that are in the vocabulary, 0..side.
+__device__ __forceinline__ int columns_of(const XentParams& p, const Place& at, int side) {
     const int64_t left = min((int64_t)p.Vs - at.col, p.vocab - ((int64_t)at.rank * p.Vs + at.col));
-    return left < 0 ? 0 : left > kTile ? kTile : (int)left;
+    return left < 0 ? 0 : left > side ? side : (int)left;
 }
 
 __device__ __forceinline__ int64_t target_of(const XentParams& p, int row) {
@@ -166,7 +166,7 @@ struct Stager {
     }
 };
 
-template <int PASS>
+template <int PASS, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant__ XentParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -182,20 +182,26 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int q = (int)ptx::cluster_ctarank();  // 0 = leader
-    const int first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    constexpr int kSide = PAIR ? 256 : 128;  // rows and columns of a tile
+    const int q = PAIR ? (int)ptx::cluster_ctarank() : 0;  // 0 = leader
+    const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, pairs = PAIR ? gridDim.x >> 1 : gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStagesX; ++s) { ptx::mbar_init(&full[s], 1); ptx::mbar_init(&empty[s], 1); }
-        for (int s = 0; s < 2; ++s) { ptx::mbar_init(&tfull[s], 1); ptx::mbar_init(&tempty[s], 8); }
+        for (int s = 0; s < 2; ++s) { ptx::mbar_init(&tfull[s], 1); ptx::mbar_init(&tempty[s], PAIR ? 8 : 4); }
         ptx::mbar_init(mma_done, 1);
         *abort_flag = 0u;
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_shared();
     }
     if (warp == 2) {
-        ptx::tmem_alloc_pair(tmem_slot, 512);
-        ptx::tmem_relinquish_pair();
+        if (PAIR) {
+            ptx::tmem_alloc_pair(tmem_slot, 2 * kSide);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(tmem_slot, 2 * kSide);
+            ptx::tmem_relinquish();
+        }
     }
     if (warp == 0 && lane == 0) {
         ptx::prefetch_tmap(&p.tmA);
@@ -207,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
     }
     __syncwarp();
     ptx::tc_fence_before();
-    ptx::cluster_sync();
+    if (PAIR) ptx::cluster_sync();
+    else __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     ptx::grid_launch_dependents();
@@ -224,9 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
             const Tile t = tile_of<PASS>(p, u);
             const bool dh = PASS == kXentGrads && t.kind == kXentDH, dw = PASS == kXentGrads && !dh;
             const Place at = place_of(p, PASS == kXentGrads ? 0 : t.tn);
-            const int a0 = t.tm * kTile + q * 128, b0 = t.tn * kTile + q * 128;
+            const int a0 = t.tm * kSide + q * 128, b0 = t.tn * kSide + q * 128;
             // rows of A behind the last one are not loaded: whatever the buffers hold, it enters no other row's sums
-            const bool has_a = dw || a0 < p.M, both_a = dw || t.tm * kTile + 128 < p.M;
+            const bool has_a = dw || a0 < p.M, both_a = dw || t.tm * kSide + 128 < p.M;
             const uint32_t a_bytes = dw ? kHalf : (uint32_t)p.a_rows * 128;
             for (int kb = t.kb0; kb < t.kb1; ++kb) {
                 const bool ok = wait(&empty[stage], ph ^ 1u, abort_flag, p, 30, u);
@@ -236,11 +243,17 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                 }
                 if (issuer) {
                     // both CTAs' copies complete on the leader's barrier
-                    const uint32_t fb = ptx::mapa_shared(ptx::smem_u32(&full[stage]), 0);
-                    if (q == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kHalf + (both_a ? 2 * a_bytes : a_bytes));
                     uint8_t *a = sA + stage * kHalf, *b = sB + stage * kHalf;
                     const int k = kb * 64;
-                    if (dw) {
+                    if (!PAIR) {
+                        ptx::mbar_arrive_expect_tx(&full[stage], kHalf + a_bytes);
+                        ptx::tma_load_2d(a, &p.tmA, &full[stage], k, a0, pol);
+                        ptx::tma_load_2d(b, &p.tmW[at.rank], &full[stage], k, at.col, pol);
+                    }
+                    const uint32_t fb = PAIR ? ptx::mapa_shared(ptx::smem_u32(&full[stage]), 0) : 0;
+                    if (PAIR && q == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kHalf + (both_a ? 2 * a_bytes : a_bytes));
+                    if (!PAIR) {
+                    } else if (dw) {
                         for (int i = 0; i < 2; ++i) {
                             ptx::tma_load_2d_pair(a + i * 8192, &p.tmA2, fb, a0 + i * 64, k, pol);
                             ptx::tma_load_2d_pair(b + i * 8192, &p.tmB, fb, b0 + i * 64, k, pol);
@@ -286,12 +299,12 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                 const uint64_t adesc = sdesc(ptx::smem_u32(sA), across_a ? 8192 : 16, 1024);
                 const uint64_t bdesc = sdesc(ptx::smem_u32(sB), kAcrossB ? 8192 : 16, 1024);
                 const int step_a = across_a ? 128 : 2, step_b = kAcrossB ? 128 : 2;
-                const uint32_t id = idesc(across_a, kAcrossB);
+                const uint32_t id = idesc(across_a, kAcrossB, kSide);
                 const int buf = it & 1;
                 ok = __all_sync(0xFFFFFFFFu, wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, p, 31, u));
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const uint32_t d = tmem_base + buf * kTile;
+                const uint32_t d = tmem_base + buf * kSide;
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
                     ok = __all_sync(0xFFFFFFFFu, wait(&full[stage], ph, abort_flag, p, 32, u));
                     if (!ok) break;
@@ -299,17 +312,26 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                     if (issuer) {
                         const uint64_t ad = adesc + (uint64_t)(stage * (kHalf >> 4)), bd = bdesc + (uint64_t)(stage * (kHalf >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            ptx::umma_bf16_pair(d, ad + (uint64_t)(kk * step_a), bd + (uint64_t)(kk * step_b), id,
-                                                kb != t.kb0 || kk != 0);
-                        ptx::umma_commit_pair_multicast(&empty[stage], 0x3);
-                        if (kb == t.kb1 - 1) ptx::umma_commit_pair_multicast(&tfull[buf], 0x3);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint64_t ak = ad + (uint64_t)(kk * step_a), bk = bd + (uint64_t)(kk * step_b);
+                            if (PAIR) ptx::umma_bf16_pair(d, ak, bk, id, kb != t.kb0 || kk != 0);
+                            else ptx::umma_bf16(d, ak, bk, id, kb != t.kb0 || kk != 0);
+                        }
+                        if (PAIR) ptx::umma_commit_pair_multicast(&empty[stage], 0x3);
+                        else ptx::umma_commit(&empty[stage]);
+                        if (kb == t.kb1 - 1) {
+                            if (PAIR) ptx::umma_commit_pair_multicast(&tfull[buf], 0x3);
+                            else ptx::umma_commit(&tfull[buf]);
+                        }
                     }
                     __syncwarp();
                     if (++stage == kStagesX) { stage = 0; ph ^= 1u; }
                 }
             }
-            if (issuer) ptx::umma_commit_pair(mma_done);
+            if (issuer) {
+                if (PAIR) ptx::umma_commit_pair(mma_done);
+                else ptx::umma_commit(mma_done);
+            }
             __syncwarp();
             drain(mma_done, 0, p);
         }
@@ -323,12 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
             const int buf = it & 1;
             if (!__all_sync(0xFFFFFFFFu, wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, abort_flag, p, 33, u))) break;
             ptx::tc_fence_after();
-            const uint32_t acc = tmem_base + ((uint32_t)(w * 32) << 16) + buf * kTile;
-            const int m0 = t.tm * kTile + q * 128 + w * 32, m = m0 + lane;  // the warp's rows of the tile, the thread's
+            const uint32_t acc = tmem_base + ((uint32_t)(w * 32) << 16) + buf * kSide;
+            const int m0 = t.tm * kSide + q * 128 + w * 32, m = m0 + lane;  // the warp's rows of the tile, the thread's
 
             if (PASS == kXentLogSum) {
                 const Place at = place_of(p, t.tn);
-                const int cols = columns_of(p, at);
+                const int cols = columns_of(p, at, kSide);
                 const bool in = m < p.M;
                 const int64_t tgt = in ? target_of(p, m) : -1;
                 const int64_t mine = tgt < 0 ? -1 : tgt - ((int64_t)at.rank * p.Vs + at.col);  // the target's column, if in 0..cols-1
@@ -368,13 +390,13 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                 if (in) p.stats[(size_t)m * p.grid[0].tiles_n + t.tn] = make_float2(top, sum);
             } else if (PASS == kXentDLogits) {
                 const Place at = place_of(p, t.tn);
-                const int cols = columns_of(p, at);
+                const int cols = columns_of(p, at, kSide);
                 const int64_t tgt = m < p.M ? target_of(p, m) : -1;
                 const bool on = tgt >= 0;  // a row without a target has no gradient, whatever its logits
                 const int64_t mine = on ? tgt - ((int64_t)at.rank * p.Vs + at.col) : -1;
                 const float lse = on ? p.lse[m] : 0.f, g = on ? p.dloss[m] : 0.f;
                 const uint64_t minus = ptx::pair(-lse, -lse), scale = ptx::pair(kLog2e, kLog2e), g2 = ptx::pair(g, g);
-                for (int c = 0; c < kTile; c += 64) {
+                for (int c = 0; c < kSide; c += 64) {
                     uint8_t* box = out.next();
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -416,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                     ptx::fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        if (m0 < p.M) ptx::tma_store_2d(&p.tmOut[0], box, t.tn * kTile + c, m0);
+                        if (m0 < p.M) ptx::tma_store_2d(&p.tmOut[0], box, t.tn * kSide + c, m0);
                         ptx::bulk_commit();
                     }
                     __syncwarp();
@@ -475,18 +497,23 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
             // the accumulator goes back to the leader's MMA warp
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), 0));
+            if (lane == 0) {
+                if (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), 0));
+                else ptx::mbar_arrive(&tempty[buf]);
+            }
         }
         if (lane == 0) ptx::bulk_wait0();
     }
 
     __syncwarp();
     ptx::tc_fence_before();
-    ptx::cluster_sync();
+    if (PAIR) ptx::cluster_sync();
+    else __syncthreads();
     ptx::tc_fence_after();
     if (warp == 2) {
         __syncwarp();
-        ptx::tmem_dealloc_pair(tmem_base, 512);
+        if (PAIR) ptx::tmem_dealloc_pair(tmem_base, 2 * kSide);
+        else ptx::tmem_dealloc(tmem_base, 2 * kSide);
     }
 }
 
@@ -507,12 +534,18 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2* stats, flo
         top = c.x;
         sum = c.y;
     }
-    for (int i = lane; i < tiles; i += 32) {
-        const float2 v = at[i];
-        const float hi = fmaxf(top, v.x);
-        // (a tile outside the vocabulary has maximum -inf and sum 0)
-        sum = (hi == top ? sum : sum * ex2((top - hi) * kLog2e)) + (hi == v.x ? v.y : v.y * ex2((v.x - hi) * kLog2e));
-        top = hi;
+    constexpr int U = 8;  // pairs in flight
+    for (int i0 = lane; i0 < tiles; i0 += 32 * U) {
+        float2 v[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) v[j] = i0 + 32 * j < tiles ? at[i0 + 32 * j] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const float hi = fmaxf(top, v[j].x);
+            // (a tile outside the vocabulary has maximum -inf and sum 0)
+            sum = (hi == top ? sum : sum * ex2((top - hi) * kLog2e)) + (hi == v[j].x ? v[j].y : v[j].y * ex2((v[j].x - hi) * kLog2e));
+            top = hi;
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -553,25 +586,28 @@ __global__ void __launch_bounds__(256) xent_dh_kernel(const float4* sums, uint2*
     }
 }
 
-template <int PASS>
+template <int PASS, bool PAIR = true>
 cudaError_t launch(XentParams& p, int clusters, cudaStream_t s) {
     p.units = 0;
     for (XentGrid& g : p.grid) p.units += g.units = g.tiles_m * g.tiles_n * g.splits;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = PAIR ? 2 : 1;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1] = dependent_launch();  // a CTA comes up on an SM that the kernel before has left
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (unsigned)std::min(p.units, clusters));
+    cfg.gridDim = dim3((unsigned)(PAIR ? 2 * std::min(p.units, clusters) : std::min(p.units, 2 * clusters)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, xent_kernel<PASS>, p);
+    return cudaLaunchKernelEx(&cfg, xent_kernel<PASS, PAIR>, p);
 }
 
+// Up to 128 tokens the logits' tiles are 128 x 128, each of one CTA: of a pair's 256 rows half would be empty, and its
+// product of 256 x 256 x 64 takes 0.27 us whatever it holds, as long as the copies do.
+constexpr int kFewTokens = 128;
 constexpr int kGroup = 16;  // rows of tiles whose operand stays in L2: 4096 rows
 
 int ceil256(int64_t n) { return (int)((n + kTile - 1) / kTile); }
@@ -580,7 +616,8 @@ int ceil256(int64_t n) { return (int)((n + kTile - 1) / kTile); }
 
 cudaError_t xent_prepare(int* clusters) {
     cudaError_t e = cudaSuccess;
-    for (auto* f : {xent_kernel<kXentLogSum>, xent_kernel<kXentDLogits>, xent_kernel<kXentGrads>})
+    for (auto* f : {xent_kernel<kXentLogSum, true>, xent_kernel<kXentLogSum, false>, xent_kernel<kXentDLogits, true>,
+                    xent_kernel<kXentDLogits, false>, xent_kernel<kXentGrads, true>})
         if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
@@ -593,7 +630,7 @@ cudaError_t xent_prepare(int* clusters) {
     cfg.dynamicSmemBytes = kSmem;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(clusters, xent_kernel<kXentLogSum>, &cfg);
+    return cudaOccupancyMaxActiveClusters(clusters, xent_kernel<kXentLogSum, true>, &cfg);
 }
 
 XentSizes xent_sizes(int64_t M_max, int64_t K_max, int64_t piece) {
@@ -622,6 +659,7 @@ static void common(XentParams& p, const XentCall& c, const XentBuffers& b) {
     p.K = (int)c.K;
     p.Vs = (int)c.Vs;
     p.vocab = c.vocab;
+    p.tile = kTile;
     p.rank_tiles = ceil256(c.Vs);
     p.targets = c.targets;
     p.wide = c.wide;
@@ -629,8 +667,7 @@ static void common(XentParams& p, const XentCall& c, const XentBuffers& b) {
     p.timeout_ns = b.timeout_ns;
     p.R = c.R;
     p.group = kGroup;
-    p.a_rows = 8;
-    while (p.a_rows < 128 && p.a_rows < c.M) p.a_rows *= 2;
+    p.a_rows = (int)std::min<int64_t>((c.M + 7) / 8 * 8, 128);
 }
 
 cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStream_t s, int* grid) {
@@ -640,6 +677,11 @@ cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStr
     for (int r = 0; r < c.R && e == cudaSuccess; ++r)
         e = make_tmap_bf16(&p.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 128);
     if (e != cudaSuccess) return e;
+    const bool few = c.M <= kFewTokens;
+    if (few) {
+        p.tile = 128;
+        p.rank_tiles = (int)((c.Vs + 127) / 128);
+    }
     const int total = c.R * p.rank_tiles;
     const int fit = (int)std::min<int64_t>(total, (int64_t)(b.sizes.d_bytes / ((size_t)c.M * 8)));
     p.stats = static_cast<float2*>(b.d);
@@ -649,7 +691,7 @@ cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStr
     g = XentGrid{ceil256(c.M), 0, 1, (int)((c.K + 63) / 64), 0};
     for (p.tile0 = 0; p.tile0 < total && e == cudaSuccess; p.tile0 += g.tiles_n) {
         g.tiles_n = std::min(fit, total - p.tile0);
-        e = launch<kXentLogSum>(p, b.clusters, s);
+        e = few ? launch<kXentLogSum, false>(p, b.clusters, s) : launch<kXentLogSum>(p, b.clusters, s);
         if (p.tile0 == 0) *grid = 2 * std::min(p.units, b.clusters);
         if (e != cudaSuccess) return e;
         e = launch_dependent(xent_join_kernel, dim3((unsigned)((c.M + 7) / 8)), 256, 0, s, p.stats, carry, p.target_logit,
@@ -665,7 +707,12 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
     z.lse = c.lse;
     z.dloss = c.dloss;
     XentParams d = z;  // the products with it
-    const int total = c.R * z.rank_tiles, tiles_m = ceil256(c.M), tiles_k = ceil256(c.K);
+    const bool few = c.M <= kFewTokens;
+    if (few) {
+        z.tile = 128;
+        z.rank_tiles *= 2;  // halves of the tiles that the products take
+    }
+    const int total = c.R * d.rank_tiles, tiles_m = ceil256(c.M), tiles_k = ceil256(c.K);
     const int most = (int)std::min<int64_t>(total, (int64_t)(b.sizes.d_bytes / ((size_t)c.M * kTile * 2)));
     const int even = (total + most - 1) / most, piece = (total + even - 1) / even;
     const int pieces = (total + piece - 1) / piece, left = total - (pieces - 1) * piece;  // the last piece's tiles, 1..piece
@@ -685,7 +732,8 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
     for (int t0 = 0; t0 < total && e == cudaSuccess; t0 += piece) {
         const int n = std::min(piece, total - t0);
         z.tile0 = d.tile0 = t0;
-        z.grid[0] = XentGrid{tiles_m, n, 1, (int)((c.K + 63) / 64), 0};
+        z.grid[0] = XentGrid{tiles_m, few ? 2 * n : n, 1, (int)((c.K + 63) / 64), 0};
+        if (few) z.tile0 = 2 * t0;
         if (c.dh) d.grid[0] = XentGrid{tiles_m, tiles_k, splits, 4 * n, 0};
         if (c.has_dw) d.grid[1] = XentGrid{n, tiles_k, 1, (int)((c.M + 63) / 64), 0};
         const uint64_t cols = (uint64_t)n * kTile;
@@ -694,7 +742,7 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
             if (e == cudaSuccess) e = make_tmap_bf16(&d.tmA, b.d, cols, (uint64_t)c.M, 64, d.a_rows);
             if (e == cudaSuccess) e = make_tmap_bf16(&d.tmA2, b.d, cols, (uint64_t)c.M, 64, 64);
         }
-        if (e == cudaSuccess) e = launch<kXentDLogits>(z, b.clusters, s);
+        if (e == cudaSuccess) e = few ? launch<kXentDLogits, false>(z, b.clusters, s) : launch<kXentDLogits>(z, b.clusters, s);
         if (t0 == 0) *grid = 2 * std::min(z.units, b.clusters);
         d.add = t0 > 0;
         if (e == cudaSuccess) e = launch<kXentGrads>(d, b.clusters, s);

@@ -51,7 +51,9 @@ def compare(got, want):
 # tile; K below, at and past a block of 64; several pieces (1024 columns at 1100 rows); split sums (few rows)
 SHAPES = [(1, 1, 1, 8), (1, 1, 256, 64), (1, 128, 256, 64), (2, 5, 100, 72), (1, 256, 256, 256), (3, 77, 367, 200),
           (8, 1, 333, 1024), (1, 300, 1000, 136), (4, 129, 511, 520), (1, 1, 30000, 64), (2, 64, 5000, 256), (8, 257, 40, 1000),
-          (1, 1100, 5000, 128), (3, 1025, 1537, 264), (5, 600, 1300, 1024), (1, 20, 70000, 512)]
+          (1, 1100, 5000, 128), (3, 1025, 1537, 264), (5, 600, 1300, 1024), (1, 20, 70000, 512),
+          (1, 8, 3000, 64), (2, 9, 700, 72), (3, 16, 240, 128), (2, 17, 1000, 136), (1, 31, 241, 64), (4, 33, 600, 200),
+          (1, 96, 40000, 64), (7, 127, 321, 96), (2, 128, 2000, 1024), (1, 3, 111000, 8)]
 
 
 @pytest.mark.parametrize("R,M,N,K", SHAPES)
