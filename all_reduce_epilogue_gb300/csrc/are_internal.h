@@ -260,6 +260,7 @@ struct EmbedParams {
     const uint32_t* order;
     int passes, digit_bits;
     int64_t chunk, chunks;        // sorted tokens of a chunk
+    uint32_t* crossing;           // how many chunks have an id that starts in them and goes on behind, and which
     int width, block_chunks;      // 8-column packs of a row that a block takes; chunks it takes
     float* part;                  // [2 chunks, N]
 };

@@ -11,10 +11,10 @@
 // each element of the tables, most of which are zeros.  The gradient's sums go by the tokens
 // sorted by (id, position): a token's rows meet in fp32 in the order of their positions, whatever
 // the hardware's order is.
-//   1. One block sorts the ids, stable, 9 or 10 bits a pass (a warp ranks its own run of tokens
-//      by matching digits, counters per warp and digit keep the order), in shared memory for up
-//      to 16384 tokens, in runs of that for more; all other blocks write the tables' zeros
-//      meanwhile, which takes longer.
+//   1. One block sorts the ids, stable, up to 10 bits a pass (a warp ranks its own run of tokens
+//      by matching digits, counters per warp and digit keep the order), in shared memory for
+//      up to 16384 tokens, in runs of that for more; all other blocks write the tables' zeros
+//      meanwhile, which mostly takes longer.
 //   2. The sorted tokens are cut into chunks of equal length, whatever the ids: a token that makes
 //      up a tenth of a batch is then work for a tenth of the chunks.  A chunk's sums that do not
 //      reach its ends are results; the others are partial rows.
@@ -36,10 +36,16 @@ constexpr int kRankMax = 512;         // tokens that are ranked by comparison
 constexpr size_t kSortSmem = (size_t)kRun * 8 + (size_t)kSortWarps * kMaxBins * 2 + 2 * kMaxBins * 4 + 64 * 4;
 static_assert(kSortSmem <= kRowsSmemLimit, "shared memory budget");
 constexpr int kThreads = 128;
+constexpr int kShort = 16;            // chunks behind its first one through which one warp adds up an id's sum
+constexpr int kSumBlocks = 6;         // blocks of the sums on an SM
 
-__device__ __forceinline__ uint32_t id_of(const EmbedParams& p, int64_t i) {
-    const int64_t v = p.wide ? static_cast<const int64_t*>(p.ids)[i] : static_cast<const int32_t*>(p.ids)[i];
+template <typename T>
+__device__ __forceinline__ uint32_t id_as(const EmbedParams& p, int64_t i) {
+    const int64_t v = static_cast<const T*>(p.ids)[i];
     return v >= 0 && v < p.V ? (uint32_t)v : p.V;  // V: none
+}
+__device__ __forceinline__ uint32_t id_of(const EmbedParams& p, int64_t i) {
+    return p.wide ? id_as<int64_t>(p, i) : id_as<int32_t>(p, i);
 }
 
 __device__ __forceinline__ uint16_t* row_of(uint16_t* const* tables, uint32_t id, const EmbedParams& p) {
@@ -142,15 +148,17 @@ __device__ __forceinline__ void sort_tokens(const EmbedParams& p, uint8_t* smem)
             __syncthreads();
             // a warp has a run of per * 32 items, in their order; an item's place among the warp's of its digit
             uint32_t key[kItems], idx[kItems], place[kItems / 2];
+            const int i0 = w * per * 32 + lane;
+            // one kind of source a loop, so that its loads run side by side
+            auto items = [&](auto load) {
 #pragma unroll
-            for (int j = 0; j < kItems; ++j) {
-                if (j < per) {
-                    const int i = w * per * 32 + j * 32 + lane;
-                    const bool in = i < n;
-                    key[j] = !in ? 0u : pass == 0 ? id_of(p, c0 + i) : one ? skey[i] : from_key[c0 + i];
-                    idx[j] = !in ? 0u : pass == 0 ? (uint32_t)(c0 + i) : one ? sidx[i] : from_idx[c0 + i];
-                }
-            }
+                for (int j = 0; j < kItems; ++j)
+                    if (j < per && i0 + j * 32 < n) load(j, i0 + j * 32);
+            };
+            if (pass > 0 && one) items([&](int j, int i) { key[j] = skey[i]; idx[j] = sidx[i]; });
+            else if (pass > 0) items([&](int j, int i) { key[j] = from_key[c0 + i]; idx[j] = from_idx[c0 + i]; });
+            else if (p.wide) items([&](int j, int i) { key[j] = id_as<int64_t>(p, c0 + i); idx[j] = c0 + i; });
+            else items([&](int j, int i) { key[j] = id_as<int32_t>(p, c0 + i); idx[j] = c0 + i; });
 #pragma unroll
             for (int j = 0; j < kItems; ++j) {
                 if (j < per) {
@@ -243,6 +251,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
     ptx::grid_launch_dependents();
     ptx::grid_wait();
     if (blockIdx.x == 0 && p.M > 0) {
+        if (threadIdx.x < 2) p.crossing[threadIdx.x] = 0;
         if (p.passes == 0) rank_tokens(p, sort_smem);
         else sort_tokens(p, sort_smem);
         return;
@@ -287,7 +296,7 @@ __device__ __forceinline__ void store_part(const EmbedParams& p, int64_t row, in
 
 // Partial rows: 2c, the sum that goes on from the chunk before c; 2c + 1, the one that starts in c and goes on behind.
 // A block's tokens come through shared memory, 512 at a time, so that a thread's loads of dy wait for no other.
-__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_constant__ EmbedParams p) {
+__global__ void __launch_bounds__(kThreads, kSumBlocks) embed_sum_kernel(const __grid_constant__ EmbedParams p) {
     constexpr int kTokens = 512, U = 8;  // U: rows in flight
     __shared__ uint32_t keys[kTokens], order[kTokens];
     const Where x = where(p);
@@ -343,51 +352,98 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_consta
     }
     if (cur < p.V) {
         if (!started) store_part(p, 2 * x.chunk, x.pack, sum);
-        else if (cur == next) store_part(p, 2 * x.chunk + 1, x.pack, sum);
-        else store_row(p, cur, x.pack, sum);
+        else if (cur == next) {
+            store_part(p, 2 * x.chunk + 1, x.pack, sum);
+            if (x.pack == 0) {  // listed, in any order: those that go on for long from the front, the others from the end
+                const int64_t far = (x.chunk + 1 + kShort) * p.chunk;
+                if (far < p.M && p.sorted[far] == cur) p.crossing[2 + atomicAdd(p.crossing, 1u)] = (uint32_t)x.chunk;
+                else p.crossing[1 + p.chunks - atomicAdd(p.crossing + 1, 1u)] = (uint32_t)x.chunk;
+            }
+        } else {
+            store_row(p, cur, x.pack, sum);
+        }
     }
 }
 
-// An id that crosses chunks: its sum starts in the chunk that this thread has, and goes on through the next ones.
-__global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ EmbedParams p) {
-    const Where x = where(p);
-    ptx::grid_launch_dependents();
-    ptx::grid_wait();
-    if (x.pack < 0) return;
-    const int64_t first = x.chunk * p.chunk, end = first + p.chunk;
-    if (end >= p.M) return;
-    const uint32_t id = p.sorted[end - 1];
-    if (id >= p.V || p.sorted[end] != id || (first > 0 && p.sorted[first - 1] == id)) return;
-    Pack sum;
-    load8(p.part + (2 * x.chunk + 1) * p.N + x.pack * 8, sum);
-    constexpr int U = 8;
-    bool more = true;
-    for (int64_t c = x.chunk + 1; more; c += U) {
+// Ids that cross chunks: a sum starts in a listed chunk and goes on through the next ones, up to kShort of them, which one
+// warp adds up, or more, of which a block's warps take equal runs, in order, and add the runs' sums in order.  (An id that
+// makes up much of a batch has hundreds: 16384 tokens of 64 ids, 512 columns, a thread alone: 75 us.)
+constexpr int kJoinWarps = 8;
+
+// sum += the partial rows 2c of the chunks c0 .. c1 - 1
+__device__ __forceinline__ void add_parts(const EmbedParams& p, int64_t c0, int64_t c1, int pack, Pack& sum) {
+    constexpr int U = 4;  // rows in flight
+    for (int64_t c = c0; c < c1; c += U) {
         Pack v[U];
-        bool in[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (c + j < c1) load8(p.part + 2 * (c + j) * p.N + pack * 8, v[j]);
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            in[j] = (c + j) * p.chunk < p.M && p.sorted[(c + j) * p.chunk] == id;
-            if (in[j]) load8(p.part + 2 * (c + j) * p.N + x.pack * 8, v[j]);
-        }
+            if (c + j < c1) {
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (!in[j]) {
-                more = false;
-                break;
+                for (int i = 0; i < 4; ++i) sum[i] = add2(sum[i], v[j][i]);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] = add2(sum[i], v[j][i]);
         }
     }
-    store_row(p, id, x.pack, sum);
+}
+
+__global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const __grid_constant__ EmbedParams p) {
+    __shared__ uint64_t runs[kJoinWarps][4][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, P = p.N >> 3, slabs = (P + 31) / 32;
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
+    const int64_t longs = (int64_t)p.crossing[0] * slabs, shorts = (int64_t)p.crossing[1] * slabs;
+    for (int64_t i = blockIdx.x; i < longs; i += gridDim.x) {
+        const int64_t chunk = p.crossing[2 + i / slabs];
+        const int pack = (int)(i % slabs) * 32 + lane;
+        const uint32_t id = p.sorted[(chunk + 1) * p.chunk];
+        // the last chunk that begins with this id: 32 places at a time
+        int64_t lo = chunk + 1, hi = p.chunks;  // lo does, hi does not
+        while (hi - lo > 1) {
+            const int64_t step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+            const int far = __popc(__ballot_sync(0xFFFFFFFFu, at < hi && p.sorted[at * p.chunk] == id));  // (lanes that have it come first)
+            hi = min(hi, lo + (far + 1) * step);
+            lo += far * step;
+        }
+        const int64_t n = lo - chunk;
+        Pack sum = {};
+        if (pack < P) {
+            if (w == 0) load8(p.part + (2 * chunk + 1) * p.N + pack * 8, sum);
+            add_parts(p, chunk + 1 + n * w / kJoinWarps, chunk + 1 + n * (w + 1) / kJoinWarps, pack, sum);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) runs[w][k][lane] = sum[k];
+        __syncthreads();
+        if (w == 0 && pack < P) {
+            for (int r = 1; r < kJoinWarps; ++r)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum[k] = add2(sum[k], runs[r][k][lane]);
+            store_row(p, id, pack, sum);
+        }
+        __syncthreads();
+    }
+    for (int64_t i = (int64_t)(gridDim.x - 1 - blockIdx.x) * kJoinWarps + w; i < shorts; i += (int64_t)gridDim.x * kJoinWarps) {
+        const int64_t chunk = p.crossing[1 + p.chunks - i / slabs];
+        const int pack = (int)(i % slabs) * 32 + lane;
+        const int64_t at = chunk + 1 + lane;
+        const uint32_t key = lane < kShort && at < p.chunks ? p.sorted[at * p.chunk] : p.V;
+        const uint32_t id = __shfl_sync(0xFFFFFFFFu, key, 0);
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, key == id));
+        if (pack >= P) continue;
+        Pack sum;
+        load8(p.part + (2 * chunk + 1) * p.N + pack * 8, sum);
+        add_parts(p, chunk + 1, chunk + 1 + n, pack, sum);
+        store_row(p, id, pack, sum);
+    }
 }
 
 }  // namespace
 
 cudaError_t embed_prepare() { return cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem); }
 
-size_t embed_sort_bytes(int64_t M_max) { return (size_t)M_max * 16; }
+// Keys and positions twice, and the list of chunks (of 8 tokens or more) in which an id starts that goes on behind.
+size_t embed_sort_bytes(int64_t M_max) { return (size_t)M_max * 16 + (size_t)(M_max / 8 + 4) * 4; }
 
 cudaError_t launch_embedding(const EmbedParams& p, int* grid, cudaStream_t s) {
     const int64_t packs = p.M * (p.N / 8), blocks = (packs + kThreads * 4 - 1) / (kThreads * 4);
@@ -407,26 +463,32 @@ cudaError_t launch_embedding_backward(EmbedParams& p, void* sort, float* scratch
         p.keys[i] = words + (2 * i) * p.M;
         p.idx[i] = words + (2 * i + 1) * p.M;
     }
+    p.crossing = words + 4 * p.M;
     if (p.M <= kRankMax) p.passes = 0;
     const int last = p.passes ? (p.passes - 1) & 1 : 0;
     p.sorted = p.keys[last];
     p.order = p.idx[last];
     p.part = scratch;
-    // two partial rows a chunk; what a workspace of this width has, so that the order of the sums goes by the sizes alone
-    const int64_t rows = (int64_t)norm_backward_scratch_words(p.N, num_sms) / p.N;
-    p.chunk = std::max<int64_t>(8, (p.M + rows / 2 - 1) / (rows / 2));
-    p.chunks = (p.M + p.chunk - 1) / p.chunk;
-    *grid = p.accumulate ? 1 : num_sms;
-    cudaError_t e = launch_dependent(embed_sort_kernel, dim3((unsigned)*grid), kSortThreads, kSortSmem, s, p);
-    if (e != cudaSuccess || p.M == 0) return e;
     // a row's packs over blocks of equal width, or several chunks in a block
     const int P = p.N / 8, slabs = (P + kThreads - 1) / kThreads;
     p.width = (P + slabs - 1) / slabs;
     p.block_chunks = kThreads / p.width;
+    // as many chunks as run at once (16384 x 4096: 222 of 74 tokens, 32 us; 373 of 44, which take a second round, 36),
+    // two partial rows each, of those that a workspace of this width has, so that the order of the sums goes by the
+    // sizes alone
+    const int64_t rows = (int64_t)norm_backward_scratch_words(p.N, num_sms) / p.N;
+    const int64_t most = std::min<int64_t>(rows / 2, (int64_t)num_sms * kSumBlocks / slabs * p.block_chunks);
+    p.chunk = std::max<int64_t>(8, (p.M + most - 1) / most);
+    p.chunks = (p.M + p.chunk - 1) / p.chunk;
+    *grid = p.accumulate ? 1 : num_sms;
+    cudaError_t e = launch_dependent(embed_sort_kernel, dim3((unsigned)*grid), kSortThreads, kSortSmem, s, p);
+    if (e != cudaSuccess || p.M == 0) return e;
     const int threads = (p.width * p.block_chunks + 31) / 32 * 32;
     const dim3 blocks((unsigned)((p.chunks + p.block_chunks - 1) / p.block_chunks), (unsigned)slabs);
     e = launch_dependent(embed_sum_kernel, blocks, threads, 0, s, p);
-    if (e == cudaSuccess && p.chunks > 1) e = launch_dependent(embed_join_kernel, blocks, threads, 0, s, p);
+    if (e == cudaSuccess && p.chunks > 1)
+        e = launch_dependent(embed_join_kernel, dim3((unsigned)std::min<int64_t>(3 * num_sms, p.chunks * ((P + 31) / 32))),
+                             kJoinWarps * 32, 0, s, p);
     return e;
 }
 
