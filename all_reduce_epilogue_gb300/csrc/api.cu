@@ -812,6 +812,29 @@ void rows_common(RowsParams& p, const are_ws* ws, const are_bf16* const parts[],
     p.timeout_ns = ws->timeout_ns;
 }
 
+// Memory that a call writes: no two of its pieces may overlap, nor one of them what the call reads.
+struct Extents {
+    struct Piece {
+        uintptr_t at, end;
+    };
+    Piece written[2 * kMaxRanks + 4];
+    int n = 0;
+    bool ok = true;
+    bool meets(const void* p, size_t bytes) const {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        for (int i = 0; i < n; ++i)
+            if (p && bytes && at < written[i].end && written[i].at < at + bytes) return true;
+        return false;
+    }
+    void write(const void* p, size_t bytes) {
+        ok = ok && !meets(p, bytes);
+        if (p && bytes) written[n++] = Piece{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes};
+    }
+    void read(const void* p, size_t bytes) { ok = ok && !meets(p, bytes); }
+};
+
+size_t index_bytes(int format, int64_t n) { return (size_t)n * (format == ARE_INDEX_I64 ? 8 : 4); }
+
 bool index_format_ok(int f) { return f == ARE_INDEX_I32 || f == ARE_INDEX_I64; }
 bool index_ptr_ok(const void* p, int format, int64_t n) {
     return n == 0 || aligned_to(p, format == ARE_INDEX_I64 ? 8 : 4);
@@ -861,6 +884,13 @@ are_status xent_call(XentCall& c, XentBuffers& b, const are_bf16* h, const are_b
     b.status = ws->d_status;
     b.timeout_ns = ws->timeout_ns;
     return ARE_OK;
+}
+
+void xent_reads(Extents& mem, const are_bf16* h, const are_bf16* const w[], const void* targets, int index_format, int R,
+                int64_t M, int64_t N, int64_t K) {
+    mem.read(h, (size_t)M * K * 2);
+    for (int r = 0; r < R; ++r) mem.read(w[r], (size_t)N * K * 2);
+    mem.read(targets, index_bytes(index_format, M));
 }
 
 // Arguments of both directions that need no workspace.
@@ -1119,8 +1149,14 @@ are_status are_embedding_ar(const void* ids, int index_format, const are_bf16* c
     if (st != ARE_OK) return st;
     if (!index_format_ok(index_format) || !index_ptr_ok(ids, index_format, M) || !std::isfinite(scale) || !ptr_ok(out, M * N))
         return ARE_EINVAL;
-    for (int r = 0; r < R; ++r)
+    Extents mem;
+    mem.write(out, (size_t)M * N * 2);
+    mem.read(ids, index_bytes(index_format, M));
+    for (int r = 0; r < R; ++r) {
         if (!ptr_ok(table[r], V * N)) return ARE_EINVAL;
+        mem.read(table[r], (size_t)V * N * 2);
+    }
+    if (!mem.ok) return ARE_EINVAL;
     TryLock lk(ws->mu);
     if (!lk.ok) return ARE_EBUSY;
     if (!on_device(ws)) return ARE_EINVAL;
@@ -1144,8 +1180,14 @@ are_status are_embedding_ar_backward(const void* ids, int index_format, const ar
     if (st != ARE_OK) return st;
     if (!index_format_ok(index_format) || !index_ptr_ok(ids, index_format, M) || !std::isfinite(scale) || !ptr_ok(dy, M * N))
         return ARE_EINVAL;
-    for (int r = 0; r < R; ++r)
+    Extents mem;
+    for (int r = 0; r < R; ++r) {
         if (!ptr_ok(dtable[r], V * N)) return ARE_EINVAL;
+        mem.write(dtable[r], (size_t)V * N * 2);
+    }
+    mem.read(ids, index_bytes(index_format, M));
+    mem.read(dy, (size_t)M * N * 2);
+    if (!mem.ok) return ARE_EINVAL;
     TryLock lk(ws->mu);
     if (!lk.ok) return ARE_EBUSY;
     if (!on_device(ws)) return ARE_EINVAL;
@@ -1176,6 +1218,11 @@ are_status are_gemm_cross_entropy(const are_bf16* h, const are_bf16* const w[], 
     if (st != ARE_OK) return st;
     if (!xent_args_ok(h, w, targets, index_format, vocab, R, M, N, K)) return ARE_EINVAL;
     if (M > 0 && (!aligned_to(loss, 4) || !aligned_to(lse, 4))) return ARE_EINVAL;
+    Extents mem;
+    mem.write(loss, (size_t)M * 4);
+    mem.write(lse, (size_t)M * 4);
+    xent_reads(mem, h, w, targets, index_format, R, M, N, K);
+    if (!mem.ok) return ARE_EINVAL;
     TryLock lk(ws->mu);
     if (!lk.ok) return ARE_EBUSY;
     XentCall c{};
@@ -1202,9 +1249,16 @@ are_status are_gemm_cross_entropy_backward(const are_bf16* h, const are_bf16* co
     if (!xent_args_ok(h, w, targets, index_format, vocab, R, M, N, K)) return ARE_EINVAL;
     if (M > 0 && (!aligned_to(lse, 4) || !aligned_to(dloss, 4))) return ARE_EINVAL;
     if (dh && !aligned16(dh)) return ARE_EINVAL;
-    if (dw)
-        for (int r = 0; r < R; ++r)
-            if (!aligned16(dw[r])) return ARE_EINVAL;
+    Extents mem;
+    mem.write(dh, (size_t)M * K * 2);
+    for (int r = 0; r < R && dw; ++r) {
+        if (!aligned16(dw[r])) return ARE_EINVAL;
+        mem.write(dw[r], (size_t)N * K * 2);
+    }
+    xent_reads(mem, h, w, targets, index_format, R, M, N, K);
+    mem.read(lse, (size_t)M * 4);
+    mem.read(dloss, (size_t)M * 4);
+    if (!mem.ok) return ARE_EINVAL;
     TryLock lk(ws->mu);
     if (!lk.ok) return ARE_EBUSY;
     XentCall c{};

@@ -654,6 +654,16 @@ static int dh_splits(int tiles, int clusters, int most) {
     return best;
 }
 
+// Rows of rank r's weights that are in the vocabulary.  Those behind are not read, and count as zeros where a tile has them:
+// whatever they hold, infinities and NaN too, enters nothing.
+static int64_t rows_in(const XentCall& c, int r) { return std::max<int64_t>(0, std::min(c.Vs, c.vocab - r * c.Vs)); }
+static int last_rank(const XentCall& c) { return (int)((c.vocab - 1) / c.Vs); }
+// Vocabulary tiles, up to the last that holds some of the vocabulary.
+static int tiles_in(const XentCall& c, int tile, int rank_tiles) {
+    const int r = last_rank(c);
+    return r * rank_tiles + (int)((rows_in(c, r) + tile - 1) / tile);
+}
+
 static void common(XentParams& p, const XentCall& c, const XentBuffers& b) {
     p.M = (int)c.M;
     p.K = (int)c.K;
@@ -665,7 +675,7 @@ static void common(XentParams& p, const XentCall& c, const XentBuffers& b) {
     p.wide = c.wide;
     p.status = b.status;
     p.timeout_ns = b.timeout_ns;
-    p.R = c.R;
+    p.R = last_rank(c) + 1;  // ranks behind have none of the vocabulary
     p.group = kGroup;
     p.a_rows = (int)std::min<int64_t>((c.M + 7) / 8 * 8, 128);
 }
@@ -674,15 +684,15 @@ cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStr
     XentParams p{};
     common(p, c, b);
     cudaError_t e = make_tmap_bf16(&p.tmA, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, p.a_rows);
-    for (int r = 0; r < c.R && e == cudaSuccess; ++r)
-        e = make_tmap_bf16(&p.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 128);
+    for (int r = 0; r < p.R && e == cudaSuccess; ++r)
+        e = make_tmap_bf16(&p.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)rows_in(c, r), 64, 128);
     if (e != cudaSuccess) return e;
     const bool few = c.M <= kFewTokens;
     if (few) {
         p.tile = 128;
         p.rank_tiles = (int)((c.Vs + 127) / 128);
     }
-    const int total = c.R * p.rank_tiles;
+    const int total = tiles_in(c, p.tile, p.rank_tiles);
     const int fit = (int)std::min<int64_t>(total, (int64_t)(b.sizes.d_bytes / ((size_t)c.M * 8)));
     p.stats = static_cast<float2*>(b.d);
     float2* carry = static_cast<float2*>(b.rows);
@@ -712,14 +722,19 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
         z.tile = 128;
         z.rank_tiles *= 2;  // halves of the tiles that the products take
     }
-    const int total = c.R * d.rank_tiles, tiles_m = ceil256(c.M), tiles_k = ceil256(c.K);
+    const int total = tiles_in(c, kTile, d.rank_tiles), tiles_m = ceil256(c.M), tiles_k = ceil256(c.K);
     const int most = (int)std::min<int64_t>(total, (int64_t)(b.sizes.d_bytes / ((size_t)c.M * kTile * 2)));
     const int even = (total + most - 1) / most, piece = (total + even - 1) / even;
     const int pieces = (total + piece - 1) / piece, left = total - (pieces - 1) * piece;  // the last piece's tiles, 1..piece
     cudaError_t e = make_tmap_bf16(&z.tmA, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, z.a_rows);
-    for (int r = 0; r < c.R && e == cudaSuccess; ++r) {
-        e = make_tmap_bf16(&z.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 128);
-        if (e == cudaSuccess) e = make_tmap_bf16(&d.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 64);
+    for (int r = 0; r < c.R && c.has_dw && e == cudaSuccess; ++r) {
+        // rows of dW that no tile has
+        const int64_t from = r < z.R - 1 ? c.Vs : r >= z.R ? 0 : std::min<int64_t>(c.Vs, (int64_t)ceil256(rows_in(c, r)) * kTile);
+        if (from < c.Vs) e = cudaMemsetAsync(c.dw[r] + from * c.K, 0, (size_t)(c.Vs - from) * c.K * 2, s);
+    }
+    for (int r = 0; r < z.R && e == cudaSuccess; ++r) {
+        e = make_tmap_bf16(&z.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)rows_in(c, r), 64, 128);
+        if (e == cudaSuccess) e = make_tmap_bf16(&d.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)rows_in(c, r), 64, 64);
         if (e == cudaSuccess && c.has_dw) e = make_tmap_bf16(&d.tmOut[r], c.dw[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 32);
     }
     if (e == cudaSuccess) e = make_tmap_bf16(&d.tmB, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, 64);

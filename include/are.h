@@ -625,8 +625,8 @@ ARE_API are_status are_embedding_ar(const void* ids, int index_format, const are
  *  Result   : s_v = sum over the i with ids_i = v of f32(dy_i), in fp32, in an
  *             order that depends on the ids, M, N and the device's SM count alone;
  *             dtable_v = bf16( s_v * scale ), accumulating bf16( s_v * scale + f32(dtable_v) ).
- * The tables must not overlap one another, dy or ids.  Needs M <= M_max,
- * N <= N_max, R <= R_max.
+ * Tables that overlap one another, dy or ids are refused (ARE_EINVAL).  Needs
+ * M <= M_max, N <= N_max, R <= R_max.
  */
 ARE_API are_status are_embedding_ar_backward(const void* ids, int index_format, const are_bf16* dy, float scale,
                                              int accumulate, are_bf16* const dtable[], int R, int64_t M, int64_t N,
@@ -640,8 +640,8 @@ ARE_API are_status are_embedding_ar_backward(const void* ids, int index_format, 
  *  h       : bf16 [M, K], the hidden states (every rank has them)
  *  w[r]    : bf16 [N, K], rank r's rows of the output layer: vocabulary index
  *            r * N + n
- *  vocab   : indices that count, 1 <= vocab <= R * N; weights behind are padding
- *            and take no part
+ *  vocab   : indices that count, 1 <= vocab <= R * N; weights behind are padding:
+ *            they are not read
  *  targets : [M] indices, are_index_format, aligned to its element.  A target
  *            outside 0..vocab-1 (-100, say) has loss 0 and no gradient.
  *  loss    : fp32 [M], 4-byte aligned
@@ -669,7 +669,8 @@ ARE_API are_status are_gemm_cross_entropy(const are_bf16* h, const are_bf16* con
  * The vocabulary is taken in pieces of at most vocab_piece columns (more if M is
  * below M_max), and for few tokens dh's sums are split; both go by the sizes,
  * the capacities and the device, so workspaces of the same capacities give the
- * same bits.  Outputs must not overlap inputs.  M == 0 writes zeros to dw.
+ * same bits.  Outputs that overlap one another or an input are refused
+ * (ARE_EINVAL), here and in the forward call.  M == 0 writes zeros to dw.
  */
 ARE_API are_status are_gemm_cross_entropy_backward(const are_bf16* h, const are_bf16* const w[], const void* targets,
                                                    int index_format, int64_t vocab, const float* lse, const float* dloss,

@@ -84,6 +84,7 @@ def cross_entropy64(h, ws, targets, vocab, dloss=None):
     M, K = h.shape
     N = ws[0].shape[0]
     w = torch.cat([t.double() for t in ws])
+    w[vocab:] = 0   # padding, whatever it holds
     x = h.double()
     z = x @ w[:vocab].T
     err = (K / 16 + 64) * 2 * U * (x.abs() @ w[:vocab].abs().T)

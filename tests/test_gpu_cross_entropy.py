@@ -67,16 +67,20 @@ def test_against_64_bits(ws, R, M, N, K):
     assert torch.equal(run(ws, h, w, t, dloss, dh=False)[3], got[3])
 
 
-@pytest.mark.parametrize("R,N,vocab", [(3, 367, 1100), (4, 256, 769), (2, 300, 300), (8, 100, 150), (1, 512, 1), (3, 400, 401)])
+@pytest.mark.parametrize("R,N,vocab", [(3, 367, 1100), (4, 256, 769), (2, 300, 300), (8, 100, 150), (1, 512, 1), (3, 400, 401),
+                                       (4, 1000, 1200), (2, 700, 1)])
 def test_padded_vocabulary(ws, R, N, vocab):
     """Weights behind the vocabulary take no part, whatever they hold; their gradients are zero."""
-    h, w, t, dloss = inputs(R, 70, N, 96, vocab, vocab=vocab)
-    full = torch.cat(w)
-    full[vocab:] = 1e30
-    w = list(full.view(R, N, -1).clone())
-    got = run(ws, h, w, t, dloss, vocab=vocab)
-    compare(got, ref.cross_entropy64(h, w, t, vocab, dloss))
-    assert (got[3].flatten(0, 1)[vocab:] == 0).all()
+    for M in (70, 300):
+        h, w, t, dloss = inputs(R, M, N, 96, vocab, vocab=vocab)
+        full = torch.cat(w)
+        full[vocab:] = float("nan")
+        full[vocab + 1::2] = float("inf")
+        w = list(full.view(R, N, -1).clone())
+        got = run(ws, h, w, t, dloss, vocab=vocab)
+        compare(got, ref.cross_entropy64(h, w, t, vocab, dloss))
+        assert (got[3].flatten(0, 1)[vocab:] == 0).all()
+        assert torch.equal(run(ws, h, w, t, dloss, vocab=vocab, dh=False)[3], got[3])
 
 
 def test_foreseen_tokens_and_large_logits(ws):
@@ -227,6 +231,14 @@ def test_refusals(ws):
         a.update(kw)
         with pytest.raises(ValueError):
             are.gemm_cross_entropy_backward(h, w, t, lse, a["dloss"], a["dh"], a["dw"], ws)
+    for kw in (dict(dw=[dw[0], dw[0]]), dict(dw=[dw[0], w[1]]), dict(dh=h), dict(dh=dw[1][:6])):   # overlapping outputs
+        a = dict(dh=dh, dw=dw)
+        a.update(kw)
+        with pytest.raises(are.AreError) as e:
+            are.gemm_cross_entropy_backward(h, w, t, lse, dloss, a["dh"], a["dw"], ws)
+        assert e.value.status == are.EINVAL
+    with pytest.raises(are.AreError):
+        are.gemm_cross_entropy(h, w, t, loss, loss, ws)
     odd = torch.empty((6, 60), dtype=torch.bfloat16, device="cuda")
     with pytest.raises(are.AreError):
         are.gemm_cross_entropy(odd, [odd], t, loss, lse, ws)      # K % 8

@@ -232,9 +232,16 @@ def test_refusals(ws):
             are.embedding_ar(ids, d, out, ws, scale=scale)
         with pytest.raises(are.AreError):
             are.embedding_ar_backward(ids, dy, d, ws, scale=scale)
+    both = r(11, 64)
+    for tables, grad in (([d[0], d[0]], dy), ([both[:5], both[4:9]], dy), ([both[:5], both[5:10]], both[4:10])):   # overlapping
+        with pytest.raises(are.AreError) as e:
+            are.embedding_ar_backward(ids, grad, tables, ws)
+        assert e.value.status == are.EINVAL
+    with pytest.raises(are.AreError):
+        are.embedding_ar(ids, [both[:5], both[5:10]], both[4:10], ws)
     odd = torch.empty((6, 60), dtype=torch.bfloat16, device="cuda")
     with pytest.raises(are.AreError):
-        are.embedding_ar(ids, [odd], odd, ws)
+        are.embedding_ar(ids, [odd], torch.empty_like(odd), ws)
     for caps in (dict(R_max=1), dict(M_max=5), dict(N_max=32)):
         c = dict(R_max=2, M_max=6, N_max=64)
         c.update(caps)
