@@ -289,7 +289,7 @@ struct XentParams {
     const void* targets;
     const float* lse;
     const float* dloss;
-    float2* stats;                // kXentLogSum: [M, tiles_n] (maximum, sum of exp) pairs
+    float2* stats;                // kXentLogSum: [M, tiles_n, groups of columns] (maximum, sum of exp) pairs
     float* target_logit;          // [M]
     DevStatus* status;
     int64_t vocab;                // columns of all ranks that count

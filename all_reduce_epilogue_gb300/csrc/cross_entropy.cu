@@ -8,8 +8,8 @@
 //
 // Four products on the tensor cores, which are what bounds it (2 M V K operations
 // forward, three times that backward, the logits being formed a second time):
-//   kLogSum   z, whose epilogue leaves the maximum of a row's 256 columns and the sum of
-//             exp(z - maximum): 8 bytes for what would be 1 KB of logits.  A small
+//   kLogSum   z, whose epilogue leaves the maximum of 64 or 128 columns of a row and the
+//             sum of exp(z - maximum): 8 bytes for what would be 256 and more.  A small
 //             kernel joins the tiles' pairs; pieces of the vocabulary as large as the
 //             buffer holds pairs for.
 //   kDLogits  z again, whose epilogue leaves d for one piece of the vocabulary, in bf16;
@@ -41,15 +41,28 @@
 namespace are {
 namespace {
 
-constexpr int kThreads = 256;  // TMA producer, MMA issuer, TMEM allocator, idle, four epilogue warps
 constexpr int kTile = 256;     // rows and columns of a pair's tile
-constexpr int kStagesX = 6;
 constexpr uint32_t kHalf = 128 * 64 * 2;  // a CTA's part of an operand: 128 rows or columns, 64 of the contraction
 constexpr uint32_t kStageBytes = 2 * kHalf;
 constexpr uint32_t kBox = 4096;           // an epilogue warp's staging buffer: 32 rows of 128 bytes; two a warp
-constexpr int kBars = 2 * kStagesX + 4 + 1;
-constexpr size_t kSmem = 1024 + (size_t)kStagesX * kStageBytes + 8 * (size_t)kBox + kBars * 8 + 16;
-static_assert(kSmem <= 232448, "shared memory budget");
+// Blocks of 64 of the contraction that the tensor cores add up before the logits' sums go on in registers.  Their fp32 sums
+// are cut, not rounded, at every step of 16: over the whole of K = 2048 a foreseen token's logit of 10 came out 4e-5 too
+// small, and a loss of such logits had five digits (1.8e-5 off).  With rounded sums of parts of 512 the losses of 4096
+// tokens are 1.7e-7 off (an fp32 product 3e-7), of 256 0.9e-7, and take 1132 and 1348 us where sums in one piece take 1060:
+// reading an accumulator holds the products up.  One CTA's tiles, of few tokens, wait for memory anyway: 256.
+constexpr int kPartPair = 8, kPartOne = 4;
+
+template <int PASS, bool PAIR>
+struct Shape {
+    // four epilogue warps; sixteen for the logits, whose columns are in registers: 64 a thread, and the 128 of one CTA's tile
+    static constexpr int kEpi = PASS == kXentGrads || !PAIR ? 4 : 16;
+    static constexpr int kThreads = 128 + 32 * kEpi;  // and a TMA producer, an MMA issuer, a TMEM allocator, an idle warp
+    static constexpr int kBoxes = PASS == kXentLogSum ? 0 : PASS == kXentDLogits && PAIR ? 16 : 8;  // staging buffers
+    static constexpr int kStages = kBoxes == 16 ? 5 : 6;
+    static constexpr int kBars = 2 * kStages + 4 + 1;
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + (size_t)kBoxes * kBox + kBars * 8 + 16;
+    static_assert(kSmem <= 232448, "shared memory budget");
+};
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Instruction descriptor: D fp32, A and B bf16, which of them lie across the contraction, `side` rows and columns.
@@ -154,7 +167,7 @@ __device__ __forceinline__ uint4* chunk_at(uint8_t* base, int row, int c) {
     return reinterpret_cast<uint4*>(base + row * 128 + ((c ^ (row & 7)) << 4));
 }
 
-// Two staging buffers a warp, each free again once the store before the last has read it.
+// Two staging buffers a warp (kXentGrads), each free again once the store before the last has read it.
 struct Stager {
     uint8_t* base;
     int n;
@@ -167,15 +180,16 @@ struct Stager {
 };
 
 template <int PASS, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant__ XentParams p) {
+__global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(const __grid_constant__ XentParams p) {
+    constexpr int kStages = Shape<PASS, PAIR>::kStages, kEpi = Shape<PASS, PAIR>::kEpi, kPart = PAIR ? kPartPair : kPartOne;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
-    uint8_t* sB = sA + kStagesX * kHalf;
-    uint8_t* sOut = sB + kStagesX * kHalf;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 8 * kBox);
-    uint64_t* empty = full + kStagesX;
-    uint64_t* tfull = empty + kStagesX;
+    uint8_t* sB = sA + kStages * kHalf;
+    uint8_t* sOut = sB + kStages * kHalf;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sOut + Shape<PASS, PAIR>::kBoxes * kBox);
+    uint64_t* empty = full + kStages;
+    uint64_t* tfull = empty + kStages;
     uint64_t* tempty = tfull + 2;
     uint64_t* mma_done = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -187,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
     const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, pairs = PAIR ? gridDim.x >> 1 : gridDim.x;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStagesX; ++s) { ptx::mbar_init(&full[s], 1); ptx::mbar_init(&empty[s], 1); }
-        for (int s = 0; s < 2; ++s) { ptx::mbar_init(&tfull[s], 1); ptx::mbar_init(&tempty[s], PAIR ? 8 : 4); }
+        for (int s = 0; s < kStages; ++s) { ptx::mbar_init(&full[s], 1); ptx::mbar_init(&empty[s], 1); }
+        for (int s = 0; s < 2; ++s) { ptx::mbar_init(&tfull[s], 1); ptx::mbar_init(&tempty[s], PAIR ? 2 * kEpi : kEpi); }
         ptx::mbar_init(mma_done, 1);
         *abort_flag = 0u;
         ptx::fence_mbar_init();
@@ -273,11 +287,11 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                 __syncwarp();
                 issued |= 1u << stage;
                 issued_ph = (issued_ph & ~(1u << stage)) | (ph << stage);
-                if (++stage == kStagesX) { stage = 0; ph ^= 1u; }
+                if (++stage == kStages) { stage = 0; ph ^= 1u; }
             }
         }
         if (q == 0) {
-            for (int s = 0; s < kStagesX; ++s)
+            for (int s = 0; s < kStages; ++s)
                 if (issued & (1u << s)) drain(&full[s], (issued_ph >> s) & 1u, p);
         } else if (aborted) {
             // this CTA's copies land on the leader's barriers: give them time to land
@@ -292,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
             uint32_t ph = 0;
             constexpr bool kAcrossB = PASS == kXentGrads;
             bool ok = true;
-            for (int u = first; u < p.units && ok; u += pairs, ++it) {
+            for (int u = first; u < p.units && ok; u += pairs) {
                 const Tile t = tile_of<PASS>(p, u);
                 // along the contraction: rows of 128 bytes, 32 of them a step; across: two groups of 64 columns, 16 rows a step
                 const bool across_a = PASS == kXentGrads && t.kind == kXentDW;
@@ -300,32 +314,38 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                 const uint64_t bdesc = sdesc(ptx::smem_u32(sB), kAcrossB ? 8192 : 16, 1024);
                 const int step_a = across_a ? 128 : 2, step_b = kAcrossB ? 128 : 2;
                 const uint32_t id = idesc(across_a, kAcrossB, kSide);
-                const int buf = it & 1;
-                ok = __all_sync(0xFFFFFFFFu, wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, p, 31, u));
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint32_t d = tmem_base + buf * kSide;
+                // an accumulator holds the whole sum, or a part of it (kPart blocks)
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    const int in_part = PASS == kXentGrads ? kb - t.kb0 : (kb - t.kb0) % kPart;
+                    const bool last = kb == t.kb1 - 1 || (PASS != kXentGrads && in_part == kPart - 1);
+                    const int buf = it & 1;
+                    if (in_part == 0) {
+                        ok = __all_sync(0xFFFFFFFFu, wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, p, 31, u));
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                    }
                     ok = __all_sync(0xFFFFFFFFu, wait(&full[stage], ph, abort_flag, p, 32, u));
                     if (!ok) break;
                     ptx::tc_fence_after();
                     if (issuer) {
+                        const uint32_t d = tmem_base + buf * kSide;
                         const uint64_t ad = adesc + (uint64_t)(stage * (kHalf >> 4)), bd = bdesc + (uint64_t)(stage * (kHalf >> 4));
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             const uint64_t ak = ad + (uint64_t)(kk * step_a), bk = bd + (uint64_t)(kk * step_b);
-                            if (PAIR) ptx::umma_bf16_pair(d, ak, bk, id, kb != t.kb0 || kk != 0);
-                            else ptx::umma_bf16(d, ak, bk, id, kb != t.kb0 || kk != 0);
+                            if (PAIR) ptx::umma_bf16_pair(d, ak, bk, id, in_part != 0 || kk != 0);
+                            else ptx::umma_bf16(d, ak, bk, id, in_part != 0 || kk != 0);
                         }
                         if (PAIR) ptx::umma_commit_pair_multicast(&empty[stage], 0x3);
                         else ptx::umma_commit(&empty[stage]);
-                        if (kb == t.kb1 - 1) {
+                        if (last) {
                             if (PAIR) ptx::umma_commit_pair_multicast(&tfull[buf], 0x3);
                             else ptx::umma_commit(&tfull[buf]);
                         }
                     }
                     __syncwarp();
-                    if (++stage == kStagesX) { stage = 0; ph ^= 1u; }
+                    if (++stage == kStages) { stage = 0; ph ^= 1u; }
+                    if (last) ++it;
                 }
             }
             if (issuer) {
@@ -335,6 +355,126 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
             __syncwarp();
             drain(mma_done, 0, p);
         }
+    } else if (warp >= 4 && PASS != kXentGrads) {
+        // ------------------------------------------------------------ the logits: a thread owns a group of a row's columns
+        constexpr int kGroups = kEpi / 4, kCols = kSide / kGroups;
+        const int w = warp & 3, group = (warp - 4) >> 2;
+        uint8_t* const box = sOut + (warp - 4) * (kCols / 64) * kBox;
+        const uint64_t scale = ptx::pair(kLog2e, kLog2e);
+        int part = 0;
+        bool ok = true;
+        for (int u = first; u < p.units; u += pairs) {
+            const Tile t = tile_of<PASS>(p, u);
+            uint64_t z[kCols / 2];  // pairs of columns
+#pragma unroll
+            for (int i = 0; i < kCols / 2; ++i) z[i] = 0ull;
+            for (int kb = t.kb0; kb < t.kb1; kb += kPart, ++part) {
+                const int buf = part & 1;
+                ok = __all_sync(0xFFFFFFFFu, wait(&tfull[buf], (uint32_t)(part >> 1) & 1u, abort_flag, p, 33, u));
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint32_t acc = tmem_base + ((uint32_t)(w * 32) << 16) + buf * kSide + group * kCols;
+#pragma unroll
+                for (int j = 0; j < kCols; j += 16) {
+                    uint32_t v[16];
+                    ptx::tmem_ld16(acc + j, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        z[j / 2 + i] = ptx::add2(z[j / 2 + i], ptx::pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])));
+                }
+                // the accumulator goes back to the leader's MMA warp
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), 0));
+                    else ptx::mbar_arrive(&tempty[buf]);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            const Place at = place_of(p, t.tn);
+            const int cols = max(0, min(kCols, columns_of(p, at, kSide) - group * kCols));  // of the group, in the vocabulary
+            const int m0 = t.tm * kSide + q * 128 + w * 32, m = m0 + lane;                  // the warp's rows, the thread's
+            const int64_t tgt = m < p.M ? target_of(p, m) : -1;
+            const int64_t column = tgt - ((int64_t)at.rank * p.Vs + at.col + group * kCols);
+            const int mine = tgt >= 0 && column >= 0 && column < cols ? (int)column : -1;  // the target's column, if it is here
+            float target = 0.f;
+            if (mine >= 0) {
+#pragma unroll
+                for (int i = 0; i < kCols / 2; ++i) {
+                    const float2 e = ptx::unpair(z[i]);
+                    target = 2 * i == mine ? e.x : 2 * i + 1 == mine ? e.y : target;
+                }
+            }
+            if (PASS == kXentLogSum) {
+                if (mine >= 0) p.target_logit[m] = target;
+                float top = -INFINITY, sum[4] = {0.f, 0.f, 0.f, 0.f};
+                if (cols > 0) {
+                    if (cols < kCols) {
+#pragma unroll
+                        for (int i = 0; i < kCols / 2; ++i) {
+                            const float2 e = ptx::unpair(z[i]);
+                            z[i] = ptx::pair(2 * i < cols ? e.x : -INFINITY, 2 * i + 1 < cols ? e.y : -INFINITY);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kCols / 2; ++i) {
+                        const float2 e = ptx::unpair(z[i]);
+                        top = fmaxf(top, fmaxf(e.x, e.y));
+                    }
+                    // the difference is formed before the scaling: a row's largest logit has exactly exp 1
+                    const uint64_t minus = ptx::pair(-top, -top);
+#pragma unroll
+                    for (int i = 0; i < kCols / 2; ++i) {
+                        const float2 e = ptx::unpair(ptx::mul2(ptx::add2(z[i], minus), scale));
+                        sum[(2 * i) & 3] += ex2(e.x);
+                        sum[(2 * i + 1) & 3] += ex2(e.y);
+                    }
+                }
+                if (m < p.M)
+                    p.stats[((size_t)m * p.grid[0].tiles_n + t.tn) * kGroups + group] = make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+            } else {
+                const bool on = tgt >= 0;  // a row without a target has no gradient, whatever its logits
+                const float lse = on ? p.lse[m] : 0.f, g = on ? p.dloss[m] : 0.f;
+                const uint64_t minus = ptx::pair(-lse, -lse), g2 = ptx::pair(g, g);
+                // g (p - 1): the difference before the rounding, and without cancellation where p is near 1
+                uint32_t d[kCols / 2];
+#pragma unroll
+                for (int i = 0; i < kCols / 2; ++i) {
+                    const float2 e = ptx::unpair(ptx::mul2(ptx::add2(z[i], minus), scale));
+                    const float2 x = ptx::unpair(ptx::mul2(ptx::pair(ex2(e.x), ex2(e.y)), g2));
+                    d[i] = on ? bf16x2(x.x, x.y) : 0u;
+                }
+                if (cols < kCols) {
+#pragma unroll
+                    for (int i = 0; i < kCols / 2; ++i) d[i] = 2 * i >= cols ? 0u : 2 * i + 1 >= cols ? d[i] & 0xFFFFu : d[i];
+                }
+                if (mine >= 0) {
+                    const uint32_t own = bf16x2(g * expm1f(target - lse), 0.f);
+#pragma unroll
+                    for (int i = 0; i < kCols / 2; ++i) {
+                        if (2 * i == mine) d[i] = (d[i] & 0xFFFF0000u) | own;
+                        if (2 * i + 1 == mine) d[i] = (d[i] & 0xFFFFu) | (own << 16);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::bulk_wait_read0();
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kCols / 8; ++i)
+                    *chunk_at(box + (i / 8) * kBox, lane, i % 8) = make_uint4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+                ptx::fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    if (m0 < p.M)
+                        for (int i = 0; i < kCols / 64; ++i)
+                            ptx::tma_store_2d(&p.tmOut[0], box + i * kBox, t.tn * kSide + group * kCols + i * 64, m0);
+                    ptx::bulk_commit();
+                }
+            }
+            __syncwarp();
+        }
+        if (lane == 0) ptx::bulk_wait0();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ epilogue: a thread owns a row of the CTA's half
         const int w = warp - 4;
@@ -348,102 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
             const uint32_t acc = tmem_base + ((uint32_t)(w * 32) << 16) + buf * kSide;
             const int m0 = t.tm * kSide + q * 128 + w * 32, m = m0 + lane;  // the warp's rows of the tile, the thread's
 
-            if (PASS == kXentLogSum) {
-                const Place at = place_of(p, t.tn);
-                const int cols = columns_of(p, at, kSide);
-                const bool in = m < p.M;
-                const int64_t tgt = in ? target_of(p, m) : -1;
-                const int64_t mine = tgt < 0 ? -1 : tgt - ((int64_t)at.rank * p.Vs + at.col);  // the target's column, if in 0..cols-1
-                float top = -INFINITY, sum = 0.f;
-                for (int c = 0; c < cols; c += 32) {
-                    uint32_t v[32];
-                    ptx::tmem_ld32(acc + c, v);
-                    if (c + 32 > cols) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i >= cols) v[i] = 0xFF800000u;  // -inf: not in the vocabulary
-                    }
-                    float hi = top;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) hi = fmaxf(hi, __uint_as_float(v[i]));
-                    // the difference is formed before the scaling: a row's largest logit has exactly exp 1
-                    const uint64_t minus = ptx::pair(-hi, -hi), scale = ptx::pair(kLog2e, kLog2e);
-                    float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 e = ptx::unpair(ptx::mul2(
-                            ptx::add2(ptx::pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), minus), scale));
-                        part[(2 * i) & 3] += ex2(e.x);
-                        part[(2 * i + 1) & 3] += ex2(e.y);
-                    }
-                    sum = fmaf(sum, ex2((top - hi) * kLog2e), (part[0] + part[1]) + (part[2] + part[3]));
-                    top = hi;
-                    if (mine >= c && mine < c + 32 && mine < cols) {
-                        const int at_i = (int)mine - c;
-                        float z = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) z = i == at_i ? __uint_as_float(v[i]) : z;
-                        p.target_logit[m] = z;
-                    }
-                    __syncwarp();
-                }
-                if (in) p.stats[(size_t)m * p.grid[0].tiles_n + t.tn] = make_float2(top, sum);
-            } else if (PASS == kXentDLogits) {
-                const Place at = place_of(p, t.tn);
-                const int cols = columns_of(p, at, kSide);
-                const int64_t tgt = m < p.M ? target_of(p, m) : -1;
-                const bool on = tgt >= 0;  // a row without a target has no gradient, whatever its logits
-                const int64_t mine = on ? tgt - ((int64_t)at.rank * p.Vs + at.col) : -1;
-                const float lse = on ? p.lse[m] : 0.f, g = on ? p.dloss[m] : 0.f;
-                const uint64_t minus = ptx::pair(-lse, -lse), scale = ptx::pair(kLog2e, kLog2e), g2 = ptx::pair(g, g);
-                for (int c = 0; c < kSide; c += 64) {
-                    uint8_t* box = out.next();
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int c0 = c + half * 32;
-                        uint32_t v[32], d[16];
-                        ptx::tmem_ld32(acc + c0, v);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 e = ptx::unpair(ptx::mul2(
-                                ptx::add2(ptx::pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), minus), scale));
-                            const float2 x = ptx::unpair(ptx::mul2(ptx::pair(ex2(e.x), ex2(e.y)), g2));
-                            d[i] = on ? bf16x2(x.x, x.y) : 0u;
-                        }
-                        if (c0 + 32 > cols) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                if (c0 + 2 * i >= cols) d[i] = 0u;
-                                else if (c0 + 2 * i + 1 >= cols) d[i] &= 0xFFFFu;
-                            }
-                        }
-                        if (mine >= c0 && mine < c0 + 32 && mine < cols) {
-                            // g (p - 1): the difference before the rounding, and without cancellation where p is near 1
-                            const int at_i = (int)mine - c0;
-                            float z = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) z = i == at_i ? __uint_as_float(v[i]) : z;
-                            const uint32_t own = bf16x2(g * expm1f(z - lse), 0.f);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                if (2 * i == at_i) d[i] = (d[i] & 0xFFFF0000u) | own;
-                                if (2 * i + 1 == at_i) d[i] = (d[i] & 0xFFFFu) | (own << 16);
-                            }
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *chunk_at(box, lane, half * 4 + i) = make_uint4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
-                    }
-                    ptx::fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (m0 < p.M) ptx::tma_store_2d(&p.tmOut[0], box, t.tn * kSide + c, m0);
-                        ptx::bulk_commit();
-                    }
-                    __syncwarp();
-                }
-            } else if (t.kind == kXentDH && p.sums) {
+            if (t.kind == kXentDH && p.sums) {
                 // fp32 sums of this split, over the pieces
                 for (int c = 0; c < kTile && t.tn * kTile + c < p.K; c += 32) {
                     uint32_t v[32];
@@ -597,8 +642,8 @@ cudaError_t launch(XentParams& p, int clusters, cudaStream_t s) {
     attr[1] = dependent_launch();  // a CTA comes up on an SM that the kernel before has left
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(PAIR ? 2 * std::min(p.units, clusters) : std::min(p.units, 2 * clusters)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.blockDim = dim3(Shape<PASS, PAIR>::kThreads);
+    cfg.dynamicSmemBytes = Shape<PASS, PAIR>::kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -608,34 +653,38 @@ cudaError_t launch(XentParams& p, int clusters, cudaStream_t s) {
 // Up to 128 tokens the logits' tiles are 128 x 128, each of one CTA: of a pair's 256 rows half would be empty, and its
 // product of 256 x 256 x 64 takes 0.27 us whatever it holds, as long as the copies do.
 constexpr int kFewTokens = 128;
+constexpr size_t kMinPairs = 4u << 20;  // bytes for d or the forward pass's pairs, whatever M_max is: few pieces for few tokens
 constexpr int kGroup = 16;  // rows of tiles whose operand stays in L2: 4096 rows
 
 int ceil256(int64_t n) { return (int)((n + kTile - 1) / kTile); }
 
 }  // namespace
 
+template <int PASS, bool PAIR>
+static cudaError_t opt_in_xent() {
+    return cudaFuncSetAttribute(xent_kernel<PASS, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<PASS, PAIR>::kSmem);
+}
+
 cudaError_t xent_prepare(int* clusters) {
-    cudaError_t e = cudaSuccess;
-    for (auto* f : {xent_kernel<kXentLogSum, true>, xent_kernel<kXentLogSum, false>, xent_kernel<kXentDLogits, true>,
-                    xent_kernel<kXentDLogits, false>, xent_kernel<kXentGrads, true>})
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    if (e != cudaSuccess) return e;
+    for (cudaError_t e : {opt_in_xent<kXentLogSum, true>(), opt_in_xent<kXentLogSum, false>(), opt_in_xent<kXentDLogits, true>(),
+                          opt_in_xent<kXentDLogits, false>(), opt_in_xent<kXentGrads, true>()})
+        if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2048);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.blockDim = dim3(Shape<kXentLogSum, true>::kThreads);
+    cfg.dynamicSmemBytes = Shape<kXentDLogits, true>::kSmem;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(clusters, xent_kernel<kXentLogSum, true>, &cfg);
+    return cudaOccupancyMaxActiveClusters(clusters, xent_kernel<kXentDLogits, true>, &cfg);
 }
 
 XentSizes xent_sizes(int64_t M_max, int64_t K_max, int64_t piece) {
     XentSizes z;
-    z.d_bytes = (size_t)M_max * ceil256(piece) * kTile * 2;
+    z.d_bytes = std::max<size_t>((size_t)M_max * ceil256(piece) * kTile * 2, kMinPairs);
     // one set of sums for the longest call, or several for calls of few tiles that split the vocabulary over the pairs
     z.sum_bytes = (size_t)M_max * K_max * 4 + (size_t)std::min<int64_t>(M_max, kTile) * kTile * 4 * 80;
     z.row_bytes = (size_t)M_max * 12;
@@ -692,8 +741,8 @@ cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStr
         p.tile = 128;
         p.rank_tiles = (int)((c.Vs + 127) / 128);
     }
-    const int total = tiles_in(c, p.tile, p.rank_tiles);
-    const int fit = (int)std::min<int64_t>(total, (int64_t)(b.sizes.d_bytes / ((size_t)c.M * 8)));
+    const int total = tiles_in(c, p.tile, p.rank_tiles), each = few ? 1 : 4;  // pairs of a row that a tile leaves
+    const int fit = (int)std::min<int64_t>(total, (int64_t)(b.sizes.d_bytes / ((size_t)c.M * 8 * each)));
     p.stats = static_cast<float2*>(b.d);
     float2* carry = static_cast<float2*>(b.rows);
     p.target_logit = reinterpret_cast<float*>(carry + c.M);
@@ -705,7 +754,7 @@ cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStr
         if (p.tile0 == 0) *grid = 2 * std::min(p.units, b.clusters);
         if (e != cudaSuccess) return e;
         e = launch_dependent(xent_join_kernel, dim3((unsigned)((c.M + 7) / 8)), 256, 0, s, p.stats, carry, p.target_logit,
-                             c.targets, c.wide, c.vocab, c.loss, c.lse, (int)c.M, g.tiles_n, p.tile0 == 0,
+                             c.targets, c.wide, c.vocab, c.loss, c.lse, (int)c.M, each * g.tiles_n, p.tile0 == 0,
                              p.tile0 + g.tiles_n == total);
     }
     return e;

@@ -265,7 +265,7 @@ ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
  * partial buffer, the Lamport staging buffer (filled with the sentinel, on a
  * private stream, synchronously), partial sums of dgamma, 2 MiB a rank of
  * staged tokens for the 4-bit linear, 17 * M_max bytes of sorted tokens, with vocab_piece > 0 the cross entropy's
- * buffers (M_max * (2 * vocab_piece + 4 * K_max + 12) bytes and up to 20 MB), and
+ * buffers (M_max * (2 * vocab_piece + 4 * K_max + 12) bytes and up to 24 MB), and
  * the device status word.
  * ROCm/mori PR #662, review threads: every capacity is validated before the
  * first allocation; buffer offsets are sized from the capacities, never from
