@@ -1206,7 +1206,9 @@ are_status are_embedding_ar_backward(const void* ids, int index_format, const ar
     int grid = 0;
     const cudaError_t e = launch_embedding_backward(p, ws->d_sort, ws->d_dgamma, ws->num_sms, &grid,
                                                     reinterpret_cast<cudaStream_t>(stream));
-    ws->last = are_launch_info{ARE_KERNEL_EMBEDDING_BACKWARD, grid, 1024, 1, 0, 0, 0, 0};
+    const bool few = M > 0 && M <= kEmbedFew;
+    ws->last = are_launch_info{few ? ARE_KERNEL_EMBEDDING_BACKWARD_FEW : ARE_KERNEL_EMBEDDING_BACKWARD, grid, few ? 256 : 1024,
+                               1, 0, 0, 0, 0};
     return from_cuda(e);
 }
 

@@ -265,6 +265,7 @@ struct EmbedParams {
     float* part;                  // [2 chunks, N]
 };
 
+constexpr int kEmbedFew = 512;  // tokens whose gradient is one launch
 cudaError_t embed_prepare();
 size_t embed_sort_bytes(int64_t M_max);
 cudaError_t launch_embedding(const EmbedParams& p, int* grid, cudaStream_t stream);

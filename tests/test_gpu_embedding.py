@@ -69,10 +69,11 @@ def gradient64(ids, dy, V, scale, base=None):
     return s, tol + BF16 * (s.abs() + tol) + 1e-38, n > 0
 
 
-# one token; fewer tokens than a chunk; runs of ids over chunk ends; 16384 tokens and one more than the sort takes at
+# one token; up to 512 tokens, in one launch; one more; runs of ids over chunk ends; 16384 tokens and one more than the sort takes at
 # once, several of its runs; one to three passes of digits; narrow rows (chunks share a block), rows of several slabs
 @pytest.mark.parametrize("kind", ["text", "uniform", "one", "runs"])
-@pytest.mark.parametrize("R,M,N,V", [(1, 1, 8, 1), (2, 7, 72, 3), (3, 300, 1032, 367), (8, 1000, 64, 50), (4, 1025, 2056, 700),
+@pytest.mark.parametrize("R,M,N,V", [(1, 1, 8, 1), (2, 7, 72, 3), (3, 300, 1032, 367), (1, 512, 520, 90), (2, 511, 40, 3000000),
+                                     (1, 513, 4104, 77), (8, 1000, 64, 50), (4, 1025, 2056, 700),
                                      (2, 5000, 136, 40000), (1, 16384, 264, 65536), (5, 16385, 64, 8192), (2, 40000, 128, 600000),
                                      (8, 3000, 4096, 100), (1, 70000, 8, 5), (1, 33000, 40, 1100000)])
 def test_gradient(ws, R, M, N, V, kind):
@@ -81,7 +82,8 @@ def test_gradient(ws, R, M, N, V, kind):
     buf = torch.full((R, V + 1, N), 3.0, dtype=torch.bfloat16, device="cuda")
     d = [b[:V] for b in buf]
     are.embedding_ar_backward(ids, dy, d, ws, scale=1.7)
-    assert ws.device_status()["code"] == 0 and ws.last_launch()["kernel"] == "embed_sort_kernel"
+    assert ws.device_status()["code"] == 0
+    assert ws.last_launch()["kernel"] == ("embed_few_kernel" if M <= 512 else "embed_sort_kernel")
     scale = torch.tensor(1.7).item()
     want, tol, there = gradient64(ids, dy, R * V, scale)
     check(torch.cat(d), want, tol, "dtable")
