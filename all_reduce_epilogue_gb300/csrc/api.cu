@@ -515,7 +515,7 @@ are_status are_workspace_create(are_ws** out, const are_caps* caps) {
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_sort, embed_sort_bytes(caps->M_max));
     if (e == cudaSuccess && caps->vocab_piece > 0) {
         ws->xent = xent_sizes(caps->M_max, caps->K_max, caps->vocab_piece);
-        e = cudaMalloc(&ws->d_xent, ws->xent.d_bytes + ws->xent.sum_bytes + ws->xent.row_bytes);
+        e = cudaMalloc(&ws->d_xent, ws->xent.d_bytes + ws->xent.sum_bytes + ws->xent.h_bytes + ws->xent.row_bytes);
     }
     if (e != cudaSuccess) {
         are_status st = from_cuda(e);
@@ -878,7 +878,8 @@ are_status xent_call(XentCall& c, XentBuffers& b, const are_bf16* h, const are_b
     uint8_t* at = static_cast<uint8_t*>(ws->d_xent);
     b.d = at;
     b.sums = at + ws->xent.d_bytes;
-    b.rows = at + ws->xent.d_bytes + ws->xent.sum_bytes;
+    b.h = at + ws->xent.d_bytes + ws->xent.sum_bytes;
+    b.rows = static_cast<uint8_t*>(b.h) + ws->xent.h_bytes;
     b.sizes = ws->xent;
     b.clusters = ws->xent_clusters;
     b.status = ws->d_status;
@@ -1235,10 +1236,7 @@ are_status are_gemm_cross_entropy(const are_bf16* h, const are_bf16* const w[], 
     if (M == 0) return ARE_OK;
     c.loss = loss;
     c.lse = lse;
-    int grid = 0;
-    const cudaError_t e = launch_xent_forward(c, b, reinterpret_cast<cudaStream_t>(stream), &grid);
-    ws->last = are_launch_info{ARE_KERNEL_CROSS_ENTROPY, grid, 256, 2, 0, 0, 0, 0};
-    return from_cuda(e);
+    return from_cuda(launch_xent_forward(c, b, reinterpret_cast<cudaStream_t>(stream), &ws->last));
 }
 
 are_status are_gemm_cross_entropy_backward(const are_bf16* h, const are_bf16* const w[], const void* targets,
@@ -1283,10 +1281,7 @@ are_status are_gemm_cross_entropy_backward(const are_bf16* h, const are_bf16* co
     c.dh = dh;
     c.has_dw = dw != nullptr;
     for (int r = 0; r < R && dw; ++r) c.dw[r] = dw[r];
-    int grid = 0;
-    const cudaError_t e = launch_xent_backward(c, b, s, &grid);
-    ws->last = are_launch_info{ARE_KERNEL_CROSS_ENTROPY_BACKWARD, grid, 256, 2, 0, 0, 0, 0};
-    return from_cuda(e);
+    return from_cuda(launch_xent_backward(c, b, s, &ws->last));
 }
 
 are_status are_gemm_ar_qweight(const are_bf16* const x[], const are_qweight w[], int group, are_bf16* const out[], int R,

@@ -324,11 +324,12 @@ struct XentCall {
 struct XentSizes {
     size_t d_bytes;    // d of a piece [M, piece], or the forward pass's pairs
     size_t sum_bytes;  // fp32 sums of dh
+    size_t h_bytes;    // the hidden states of rows with a target
     size_t row_bytes;  // a running pair and a logit a row
 };
 
 struct XentBuffers {
-    void *d, *sums, *rows;
+    void *d, *sums, *h, *rows;
     XentSizes sizes;
     int clusters;
     DevStatus* status;
@@ -337,8 +338,8 @@ struct XentBuffers {
 
 XentSizes xent_sizes(int64_t M_max, int64_t K_max, int64_t piece);
 cudaError_t xent_prepare(int* clusters);
-cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStream_t stream, int* grid);
-cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaStream_t stream, int* grid);
+cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStream_t stream, are_launch_info* info);
+cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaStream_t stream, are_launch_info* info);
 
 size_t gemm_smem_bytes();
 cudaError_t gemm_prepare_kernels();

@@ -638,6 +638,32 @@ __global__ void __launch_bounds__(256) xent_dh_kernel(const float4* sums, uint2*
     }
 }
 
+// The hidden states with zeros in the rows that have no target: d is 0 there, but 0 times an infinity or a NaN, which padding
+// may hold, is none.  A copy is 64 MB to move at 4096 x 4096, 10 us of a step of 5 ms; the products read it in h's place.
+__global__ void __launch_bounds__(256) xent_rows_kernel(const uint4* h, const void* targets, int wide, int64_t vocab, uint4* out,
+                                                        int64_t packs, int row_packs) {
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
+    constexpr int U = 4;  // packs in flight
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < packs; i0 += U * step) {
+        uint4 v[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t i = i0 + j * step;
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < packs) {
+                const int64_t row = i / row_packs;
+                const int64_t t = wide ? static_cast<const int64_t*>(targets)[row] : static_cast<const int32_t*>(targets)[row];
+                if (t >= 0 && t < vocab) v[j] = h[i];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (i0 + j * step < packs) out[i0 + j * step] = v[j];
+    }
+}
+
 template <int PASS, bool PAIR = true>
 cudaError_t launch(XentParams& p, int clusters, cudaStream_t s) {
     p.units = 0;
@@ -667,6 +693,12 @@ int ceil256(int64_t n) { return (int)((n + kTile - 1) / kTile); }
 
 }  // namespace
 
+template <int PASS>
+static are_launch_info launched(int kernel, const XentParams& p, bool few, int clusters) {
+    return few ? are_launch_info{kernel, std::min(p.units, 2 * clusters), Shape<PASS, false>::kThreads, 1, 0, 0, 0, p.group}
+               : are_launch_info{kernel, 2 * std::min(p.units, clusters), Shape<PASS, true>::kThreads, 2, 0, 0, 0, p.group};
+}
+
 template <int PASS, bool PAIR>
 static cudaError_t opt_in_xent() {
     return cudaFuncSetAttribute(xent_kernel<PASS, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<PASS, PAIR>::kSmem);
@@ -694,6 +726,7 @@ XentSizes xent_sizes(int64_t M_max, int64_t K_max, int64_t piece) {
     z.d_bytes = std::max<size_t>((size_t)M_max * ceil256(piece) * kTile * 2, kMinPairs);
     // one set of sums for the longest call, or several for calls of few tiles that split the vocabulary over the pairs
     z.sum_bytes = (size_t)M_max * K_max * 4 + (size_t)std::min<int64_t>(M_max, kTile) * kTile * 4 * 80;
+    z.h_bytes = (size_t)M_max * K_max * 2;
     z.row_bytes = (size_t)M_max * 12;
     return z;
 }
@@ -736,7 +769,7 @@ static void common(XentParams& p, const XentCall& c, const XentBuffers& b) {
     p.a_rows = (int)std::min<int64_t>((c.M + 7) / 8 * 8, 128);
 }
 
-cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStream_t s, int* grid) {
+cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStream_t s, are_launch_info* info) {
     XentParams p{};
     common(p, c, b);
     cudaError_t e = make_tmap_bf16(&p.tmA, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, p.a_rows);
@@ -758,7 +791,7 @@ cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStr
     for (p.tile0 = 0; p.tile0 < total && e == cudaSuccess; p.tile0 += g.tiles_n) {
         g.tiles_n = std::min(fit, total - p.tile0);
         e = few ? launch<kXentLogSum, false>(p, b.clusters, s) : launch<kXentLogSum>(p, b.clusters, s);
-        if (p.tile0 == 0) *grid = 2 * std::min(p.units, b.clusters);
+        if (p.tile0 == 0) *info = launched<kXentLogSum>(ARE_KERNEL_CROSS_ENTROPY, p, few, b.clusters);
         if (e != cudaSuccess) return e;
         e = launch_dependent(xent_join_kernel, dim3((unsigned)((c.M + 7) / 8)), 256, 0, s, p.stats, carry, p.target_logit,
                              c.targets, c.wide, c.vocab, c.loss, c.lse, (int)c.M, each * g.tiles_n, p.tile0 == 0,
@@ -767,7 +800,7 @@ cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStr
     return e;
 }
 
-cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaStream_t s, int* grid) {
+cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaStream_t s, are_launch_info* info) {
     XentParams z{};  // the logits and their gradient
     common(z, c, b);
     z.lse = c.lse;
@@ -793,13 +826,19 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
         if (e == cudaSuccess) e = make_tmap_bf16(&d.tmW[r], c.w[r], (uint64_t)c.K, (uint64_t)rows_in(c, r), 64, 64);
         if (e == cudaSuccess && c.has_dw) e = make_tmap_bf16(&d.tmOut[r], c.dw[r], (uint64_t)c.K, (uint64_t)c.Vs, 64, 32);
     }
-    if (e == cudaSuccess) e = make_tmap_bf16(&d.tmB, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, 64);
+    if (e == cudaSuccess) e = make_tmap_bf16(&d.tmB, b.h, (uint64_t)c.K, (uint64_t)c.M, 64, 64);
     const int splits = dh_splits(tiles_m * tiles_k, b.clusters,
                                  (int)std::min({(int64_t)(b.sizes.sum_bytes / ((size_t)c.M * c.K * 4)), (int64_t)piece / 2, (int64_t)4 * left}));
     d.sums = pieces > 1 || splits > 1;
     if (e == cudaSuccess && c.dh)
         e = d.sums ? make_tmap_f32_3d(&d.tmDH, b.sums, (uint64_t)c.K, (uint64_t)c.M, (uint64_t)splits, 32, 32)
                    : make_tmap_bf16(&d.tmDH, c.dh, (uint64_t)c.K, (uint64_t)c.M, 64, 32);
+    if (e == cudaSuccess && c.has_dw) {
+        const int64_t packs = c.M * c.K / 8;
+        e = launch_dependent(xent_rows_kernel, dim3((unsigned)std::min<int64_t>((packs + 255) / 256, 16 * b.clusters)), 256, 0, s,
+                             reinterpret_cast<const uint4*>(c.h), c.targets, c.wide, c.vocab, static_cast<uint4*>(b.h), packs,
+                             (int)(c.K / 8));
+    }
     for (int t0 = 0; t0 < total && e == cudaSuccess; t0 += piece) {
         const int n = std::min(piece, total - t0);
         z.tile0 = d.tile0 = t0;
@@ -814,7 +853,7 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
             if (e == cudaSuccess) e = make_tmap_bf16(&d.tmA2, b.d, cols, (uint64_t)c.M, 64, 64);
         }
         if (e == cudaSuccess) e = few ? launch<kXentDLogits, false>(z, b.clusters, s) : launch<kXentDLogits>(z, b.clusters, s);
-        if (t0 == 0) *grid = 2 * std::min(z.units, b.clusters);
+        if (t0 == 0) *info = launched<kXentDLogits>(ARE_KERNEL_CROSS_ENTROPY_BACKWARD, z, few, b.clusters);
         d.add = t0 > 0;
         if (e == cudaSuccess) e = launch<kXentGrads>(d, b.clusters, s);
     }

@@ -266,7 +266,7 @@ ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
  * partial buffer, the Lamport staging buffer (filled with the sentinel, on a
  * private stream, synchronously), partial sums of dgamma, 2 MiB a rank of
  * staged tokens for the 4-bit linear, 17 * M_max bytes of sorted tokens, with vocab_piece > 0 the cross entropy's
- * buffers (M_max * (2 * vocab_piece + 4 * K_max + 12) bytes and up to 24 MB), and
+ * buffers (M_max * (2 * vocab_piece + 6 * K_max + 12) bytes and up to 24 MB), and
  * the device status word.
  * ROCm/mori PR #662, review threads: every capacity is validated before the
  * first allocation; buffer offsets are sized from the capacities, never from
@@ -666,7 +666,7 @@ ARE_API are_status are_gemm_cross_entropy(const are_bf16* h, const are_bf16* con
  *            without a target;  dh = bf16(d w), dw_r = bf16(d_r^T h).
  *            d is rounded to bf16 before the products (half a step, 2^-8 of each
  *            term), the products' sums are fp32 and rounded once.  A row without a
- *            target has dh 0; its h enters dw times 0, so it must be finite.
+ *            target has dh 0 and takes no part in dw, whatever its h holds.
  * The vocabulary is taken in pieces of at most vocab_piece columns (more if M is
  * below M_max), and for few tokens dh's sums are split; both go by the sizes,
  * the capacities and the device, so workspaces of the same capacities give the

@@ -61,6 +61,8 @@ def test_against_64_bits(ws, R, M, N, K):
     h, w, t, dloss = inputs(R, M, N, K, R + M + N + K)
     got = run(ws, h, w, t, dloss)
     compare(got, ref.cross_entropy64(h, w, t, R * N, dloss))
+    last = ws.last_launch()
+    assert last["kernel"] == "xent_kernel<DLogits>" and (last["cluster"], last["block"]) == ((1, 256) if M <= 128 else (2, 640))
     for a, b in zip(got, run(ws, h, w, t.int(), dloss)):   # the same bits again, and from 32-bit targets
         assert torch.equal(a, b)
     assert torch.equal(run(ws, h, w, t, dloss, dw=False)[2], got[2])
@@ -117,6 +119,15 @@ def test_rows_without_a_target_and_nan(ws):
     compare([g[keep] if g is not None else None for g in got[:3]], want[:3])
     assert got[1][3].isnan() and not got[0][6].isfinite() and not got[1][6].isfinite() and (got[2][3] == 0).all()
     assert got[0][3] == 0
+    # rows without a target (1 and 3) take no part in dw, whatever they hold
+    for M in (9, 200):
+        h2, w2, t2, g2 = inputs(2, M, 300, 128, 13)
+        wild = h2.clone()
+        wild[3], wild[1, ::2] = float("nan"), float("inf")
+        _, _, dh, dw = run(ws, wild, w2, t2, g2)
+        want = ref.cross_entropy64(h2, w2, t2, 600, g2)
+        ref.check(dh, *want[2], "dh")
+        ref.check(dw, *want[3], "dw")
     # no row has a target
     none = torch.full((9,), -100, device="cuda")
     loss, _, dh, dw = run(ws, h, w, none, dloss)
