@@ -133,6 +133,9 @@ cudaError_t launch_norm_backward_rows(RowsParams& p, const RowsPlan& plan, float
                                       cudaStream_t stream);
 size_t norm_backward_scratch_words(int64_t n_max, int num_sms);
 
+// The columns' sums over `rows` partial rows [rows, N], and with `second` over as many right behind them.
+cudaError_t launch_row_sums(const float* part, float* first, float* second, int rows, int N, cudaStream_t stream);
+
 // LayerNorm on the same rows (layernorm.cu).
 RowsPlan layernorm_plan(RowsParams& p, int num_sms);
 cudaError_t layernorm_prepare();

@@ -32,11 +32,11 @@
 // Tiles are taken in groups of rows whose operand stays in L2 while the other one
 // streams past (16 rows of tiles: forward 1055 us, 8: 1076).
 //
-// Measured, 4096 tokens, K = 4096, vocabulary 65536 over 8 ranks: forward 1.12 ms, 1.97
+// Measured, 4096 tokens, K = 4096, vocabulary 65536 over 8 ranks: forward 1.07 ms, 2.05
 // PFLOP/s; forward and backward 5.2 ms, 1.69 PFLOP/s, the rate that the power limit leaves a
 // library's product (5.5 ms in a long run).  One token, K = 2048, vocabulary 32000: 28 us,
 // 4.7 TB/s, of which 7 are the two kernels' starts and ends.  77 tokens, K = 1000,
-// vocabulary 11001, both directions: 45 us, the latencies of five kernels (35 at K = 1024,
+// vocabulary 11001, both directions: 46 us, the latencies of six kernels (37 at K = 1024,
 // whose rows are whole lines).
 #include <cuda_bf16.h>
 
@@ -53,11 +53,12 @@ constexpr uint32_t kHalf = 128 * 64 * 2;  // a CTA's part of an operand: 128 row
 constexpr uint32_t kStageBytes = 2 * kHalf;
 constexpr uint32_t kBox = 4096;           // an epilogue warp's staging buffer: 32 rows of 128 bytes; two a warp
 // Blocks of 64 of the contraction that the tensor cores add up before the logits' sums go on in registers.  Their fp32 sums
-// are cut, not rounded, at every step of 16: over the whole of K = 2048 a foreseen token's logit of 10 came out 4e-5 too
-// small, and a loss of such logits had five digits (1.8e-5 off).  With rounded sums of parts of 512 the losses of 4096
-// tokens are 1.7e-7 off (an fp32 product 3e-7), of 256 0.9e-7, and take 1132 and 1348 us where sums in one piece take 1060:
-// reading an accumulator holds the products up.  One CTA's tiles, of few tokens, wait for memory anyway: 256.
-constexpr int kPartPair = 8, kPartOne = 4;
+// are cut, not rounded, at every step of 16: over the whole of K = 4096 the losses of 4096 tokens were 1.5e-6 off, and the
+// loss of one foreseen token at K = 2048, whose logit of 10 came out 4e-5 too small, 1.8e-5.  With rounded sums of parts of
+// 1024 the 4096 losses are 3.6e-7 off, as far as a product in fp32 (3.1e-7); of 512 1.7e-7, of 256 0.9e-7; reading the
+// accumulators holds the products up: 1070, 1115 and 1348 us, in one piece 1060.  One CTA's tiles, of few tokens, wait for
+// memory anyway: 256.
+constexpr int kPartPair = 16, kPartOne = 4;
 
 template <int PASS, bool PAIR>
 struct Shape {
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(co
             if (!__all_sync(0xFFFFFFFFu, wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, abort_flag, p, 33, u))) break;
             ptx::tc_fence_after();
             const uint32_t acc = tmem_base + ((uint32_t)(w * 32) << 16) + buf * kSide;
-            const int m0 = t.tm * kSide + q * 128 + w * 32, m = m0 + lane;  // the warp's rows of the tile, the thread's
+            const int m0 = t.tm * kSide + q * 128 + w * 32;  // the warp's rows of the tile
 
             if (t.kind == kXentDH && p.sums) {
                 // fp32 sums of this split, over the pieces
@@ -732,12 +733,12 @@ XentSizes xent_sizes(int64_t M_max, int64_t K_max, int64_t piece) {
 }
 
 // Sets of sums that dh's contraction over the vocabulary is split into, at most `most`.  Few tokens have few tiles, and
-// the pairs that would have none take parts of the contraction; with a few waves of tiles, two to four parts make the
-// last wave shorter (4096 tokens, K = 4096: 256 tiles are 3.4 waves of 76; in two parts 6.7: 170 -> 150 us a piece).
+// the pairs that would have none take parts of the contraction; from half a wave of tiles on, two to four parts make the
+// last wave fuller (4096 tokens, K = 4096: 256 tiles are 3.4 waves of 76; in two parts 6.7: 170 -> 150 us a piece).
 static int dh_splits(int tiles, int clusters, int most) {
     int best = std::max(1, std::min(clusters / tiles, most));
     auto filled = [&](int s) { return (double)tiles * s / (((int64_t)tiles * s + clusters - 1) / clusters * clusters); };
-    if (tiles > clusters)
+    if (best == 1)
         for (int s = 2; s <= std::min(4, most); ++s)
             if (filled(s) > filled(best) + 0.04) best = s;
     return best;

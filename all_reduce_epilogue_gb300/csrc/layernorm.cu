@@ -706,8 +706,7 @@ cudaError_t launch_layernorm_backward_rows(RowsParams& p, const RowsPlan& plan, 
                             : backward_kernel<false>(plan.ppt, plan.threads, p.rows);
     cudaError_t e = launch_dependent(kernel, plan.grid, plan.threads, plan.smem, s, p);
     if (e == cudaSuccess && !one && (dgamma || dbeta))
-        e = launch_dependent(dgamma_sum_kernel, dim3((p.N + 15) / 16, dgamma && dbeta ? 2 : 1), 256, 0, s, scratch,
-                             dgamma ? dgamma : dbeta, dbeta, plan.grid, p.N);
+        e = launch_row_sums(scratch, dgamma ? dgamma : dbeta, dgamma ? dbeta : nullptr, plan.grid, p.N, s);
     return e;
 }
 

@@ -322,6 +322,49 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_rows_kernel(con
     }
 }
 
+// dgamma[j] = sum over the blocks' partial rows, in an order that the number of
+// rows alone decides: 64 strands of every 64th row, then the strands.
+// blockIdx.y: a second set of partial rows right behind the first (the LayerNorm's dbeta).
+__global__ void __launch_bounds__(256) dgamma_sum_kernel(const float* part, float* dgamma, float* second, int rows, int N) {
+    if (blockIdx.y) {
+        part += (size_t)rows * N;
+        dgamma = second;
+    }
+    __shared__ float4 sum[8][4];
+    const int c = threadIdx.x & 3, strand = threadIdx.x >> 2;
+    const int col = (blockIdx.x * 4 + c) * 4;
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < N) {
+        float4 v[5];
+        for (int r0 = strand; r0 < rows; r0 += 5 * 64) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+                v[i] = r0 + i * 64 < rows ? __ldcg(reinterpret_cast<const float4*>(part + (size_t)(r0 + i * 64) * N + col))
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                a.x += v[i].x; a.y += v[i].y; a.z += v[i].z; a.w += v[i].w;
+            }
+        }
+    }
+    for (int o = 4; o < 32; o <<= 1) {  // the 8 strands of a warp
+        a.x += __shfl_xor_sync(0xFFFFFFFFu, a.x, o);
+        a.y += __shfl_xor_sync(0xFFFFFFFFu, a.y, o);
+        a.z += __shfl_xor_sync(0xFFFFFFFFu, a.z, o);
+        a.w += __shfl_xor_sync(0xFFFFFFFFu, a.w, o);
+    }
+    if ((threadIdx.x & 31) < 4) sum[threadIdx.x >> 5][c] = a;
+    __syncthreads();
+    if (threadIdx.x < 16) {
+        const int out = blockIdx.x * 16 + threadIdx.x;
+        float t = 0.f;
+        for (int w = 0; w < 8; ++w) t += reinterpret_cast<const float*>(sum[w])[threadIdx.x];
+        if (out < N) dgamma[out] = t;
+    }
+}
+
 // Packs a thread holds, of a row of P.  Forward: about 256 threads a block.
 // Backward, whose state is 24 registers a pack (20 with one rank): up to 256
 // threads, two blocks an SM; above, as few packs as 16 warps allow, which may
@@ -398,6 +441,10 @@ cudaError_t launch_norm_quant_rows(const RowsParams& p, const RowsPlan& plan, bo
     return launch_dependent(kernel, plan.grid, plan.threads, plan.smem, s, p);
 }
 
+cudaError_t launch_row_sums(const float* part, float* first, float* second, int rows, int N, cudaStream_t s) {
+    return launch_dependent(dgamma_sum_kernel, dim3((N + 15) / 16, second ? 2 : 1), 256, 0, s, part, first, second, rows, N);
+}
+
 cudaError_t launch_norm_backward_rows(RowsParams& p, const RowsPlan& plan, float* scratch, float* dgamma,
                                       cudaStream_t s) {
     // a single block's sums are the result
@@ -405,7 +452,7 @@ cudaError_t launch_norm_backward_rows(RowsParams& p, const RowsPlan& plan, float
     auto* kernel = p.R == 1 ? backward_kernel<true>(plan.ppt, plan.threads) : backward_kernel<false>(plan.ppt, plan.threads);
     cudaError_t e = launch_dependent(kernel, plan.grid, plan.threads, plan.smem, s, p);
     if (e == cudaSuccess && dgamma != nullptr && plan.grid > 1)
-        e = launch_dependent(dgamma_sum_kernel, (p.N + 15) / 16, 256, 0, s, scratch, dgamma, nullptr, plan.grid, p.N);
+        e = launch_row_sums(scratch, dgamma, nullptr, plan.grid, p.N, s);
     return e;
 }
 

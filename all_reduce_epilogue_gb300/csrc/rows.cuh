@@ -1,6 +1,6 @@
 // What the row-streaming kernels share: the ring of stages that a producer warp fills
 // with slices of a row's sources, fp32 arithmetic in pairs of columns, sums over a
-// block's warps, the sum of the blocks' partial rows, and their launch.
+// block's warps, and their launch.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -204,49 +204,6 @@ __device__ __forceinline__ float red_total(const float* red, int nwarps) {
         t += (v.x + v.y) + (v.z + v.w);
     }
     return t;
-}
-
-// dgamma[j] = sum over the blocks' partial rows, in an order that the number of
-// rows alone decides: 64 strands of every 64th row, then the strands.
-// blockIdx.y: a second set of partial rows right behind the first (the LayerNorm's dbeta).
-__global__ void __launch_bounds__(256) dgamma_sum_kernel(const float* part, float* dgamma, float* second, int rows, int N) {
-    if (blockIdx.y) {
-        part += (size_t)rows * N;
-        dgamma = second;
-    }
-    __shared__ float4 sum[8][4];
-    const int c = threadIdx.x & 3, strand = threadIdx.x >> 2;
-    const int col = (blockIdx.x * 4 + c) * 4;
-    ptx::grid_launch_dependents();
-    ptx::grid_wait();
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (col < N) {
-        float4 v[5];
-        for (int r0 = strand; r0 < rows; r0 += 5 * 64) {
-#pragma unroll
-            for (int i = 0; i < 5; ++i)
-                v[i] = r0 + i * 64 < rows ? __ldcg(reinterpret_cast<const float4*>(part + (size_t)(r0 + i * 64) * N + col))
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-                a.x += v[i].x; a.y += v[i].y; a.z += v[i].z; a.w += v[i].w;
-            }
-        }
-    }
-    for (int o = 4; o < 32; o <<= 1) {  // the 8 strands of a warp
-        a.x += __shfl_xor_sync(0xFFFFFFFFu, a.x, o);
-        a.y += __shfl_xor_sync(0xFFFFFFFFu, a.y, o);
-        a.z += __shfl_xor_sync(0xFFFFFFFFu, a.z, o);
-        a.w += __shfl_xor_sync(0xFFFFFFFFu, a.w, o);
-    }
-    if ((threadIdx.x & 31) < 4) sum[threadIdx.x >> 5][c] = a;
-    __syncthreads();
-    if (threadIdx.x < 16) {
-        const int out = blockIdx.x * 16 + threadIdx.x;
-        float t = 0.f;
-        for (int w = 0; w < 8; ++w) t += reinterpret_cast<const float*>(sum[w])[threadIdx.x];
-        if (out < N) dgamma[out] = t;
-    }
 }
 
 // Launches on the programmatic dependency: the kernel comes up while the one

@@ -77,7 +77,7 @@ def layernorm_backward64(dys, h, gamma, dres):
 def cross_entropy64(h, ws, targets, vocab, dloss=None):
     """loss, lse, dh, dw in 64 bits, each with its bound.
 
-    A logit's products are summed by tensor instructions of 16 terms that cut their sums at one step, 32 of them at most
+    A logit's products are summed by tensor instructions of 16 terms that cut their sums at one step, 64 of them at most
     before the sum goes on in rounded steps of half that, K / 256 at most; 16 more steps for what an instruction cuts from its
     terms: all relative to sum |h w|.  lse is off by no more than the worst logit of its row, by 2^-20 for exp and
     log (ex2 2^-22, 2^-21 for sums of up to 256 columns and joins) and by its rounding; d by its logit's error, lse's and
@@ -88,7 +88,7 @@ def cross_entropy64(h, ws, targets, vocab, dloss=None):
     w[vocab:] = 0   # padding, whatever it holds
     x = h.double()
     z = x @ w[:vocab].T
-    err = (min(K / 16, 32) + K / 512 + 16) * 2 * U * (x.abs() @ w[:vocab].abs().T)
+    err = (min(K / 16, 64) + K / 512 + 16) * 2 * U * (x.abs() @ w[:vocab].abs().T)
     lse = torch.logsumexp(z, 1)
     worst = err.max(1).values if M else lse
     tol_lse = worst + 2.0 ** -20 + 2 * U * lse.abs()

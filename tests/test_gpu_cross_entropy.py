@@ -155,11 +155,13 @@ def test_against_differences(ws):
 
 
 def test_pieces_give_the_same_loss_and_close_gradients(ws):
-    """The smallest workspace (pieces of one tile, forward in several pieces too) against the bound."""
-    h, w, t, dloss = inputs(3, 50, 9000, 64, 8)
-    with are.Workspace(R_max=3, M_max=50, N_max=8, K_max=64, vocab_piece=1) as small:
-        got = run(small, h, w, t, dloss)
-    compare(got, ref.cross_entropy64(h, w, t, 27000, dloss))
+    """The smallest workspace, whose buffer holds 8 tiles of d backward, 131 tiles' pairs forward (few tokens: 163 and 10485):
+    several pieces both ways, the last one short."""
+    for M, N, K in ((1000, 12001, 64), (50, 23100, 8), (128, 181000, 8)):
+        h, w, t, dloss = inputs(3, M, N, K, 8)
+        with are.Workspace(R_max=3, M_max=M, N_max=8, K_max=K, vocab_piece=1) as small:
+            got = run(small, h, w, t, dloss)
+        compare(got, ref.cross_entropy64(h, w, t, 3 * N, dloss))
 
 
 def test_guards_stream_and_no_rows(ws):
