@@ -1092,7 +1092,7 @@ are_status are_allreduce_layernorm(const are_bf16* const partials[], const are_b
     p.out = out;
     p.res_out = residual_out;
     const RowsPlan plan = layernorm_plan(p, ws->num_sms);
-    ws->last = are_launch_info{ARE_KERNEL_LAYERNORM_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
+    ws->last = are_launch_info{p.lanes ? ARE_KERNEL_LAYERNORM_NARROW : ARE_KERNEL_LAYERNORM_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
     return from_cuda(launch_layernorm_rows(p, plan, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -18,7 +18,7 @@
 //
 // Bound by HBM, as the RMSNorm's: every input once, every output once.  Measured (a
 // copy moves 6.78 TB/s): forward, R = 8, 4096 x 7168: 99 us, 6.5 TB/s; R = 1,
-// 16384 x 4096: 89 us, 6.0 TB/s, x 768: 24 us, 4.3 TB/s; one row of 7168, R = 8:
+// 16384 x 4096: 89 us, 6.0 TB/s, x 768: 21 us, 4.8 TB/s, x 64: 3.2 us; one row of 7168, R = 8:
 // 4.1 us, all latency.  Backward, R = 1, 16384 x 7168: 153 us, 6.1 TB/s, x 4096:
 // 93 us, 5.8 TB/s, x 768: 34 us, 3.0 TB/s (a row's exchange and joins for one pack a
 // thread); R = 3, 1001 x 5000: 16.8 us, 6.6 rows an SM and 4 us for the sums of the
@@ -184,6 +184,99 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_rows_kernel(const _
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[i] = fma2(mul2(add2(h[k][i], mean2), inv2), gk[i], bk[i]);
                     ptx::st_stream_v4(p.out + row * (int64_t)p.N + pk * 8, pack8(o));
+                }
+            }
+        }
+    }
+}
+
+// Rows of up to 1024 columns, many of them (see narrow()): 8, 16 or 32 lanes take a row each, so a row costs no barrier and no
+// turn of a ring, and an SM has up to 128 rows in flight.
+constexpr int kNarrowWarps = 8;
+
+template <int PPT>
+__global__ void __launch_bounds__(kNarrowWarps * 32, PPT <= 2 ? 4 : 3) layernorm_narrow_kernel(const __grid_constant__ RowsParams p) {
+    const int lane = threadIdx.x & 31, G = p.lanes, l = lane & (G - 1), P = p.N >> 3, per_warp = 32 / G;
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
+    const int64_t warps = (int64_t)gridDim.x * kNarrowWarps;
+    for (int64_t w = (int64_t)blockIdx.x * kNarrowWarps + (threadIdx.x >> 5); w * per_warp < p.M; w += warps) {
+        const int64_t row = w * per_warp + lane / G;
+        const bool there = row < p.M;  // (all lanes stay for the exchanges)
+        Pack h[PPT];
+        uint64_t sum2 = 0ull;
+        const int64_t at = row * p.N + l * 8;
+        auto load = [&](const uint16_t* from, int k) {
+            return there && l + k * G < P ? ptx::ld_stream_v4(from + at + k * G * 8) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        {
+            uint4 v[PPT];
+#pragma unroll
+            for (int k = 0; k < PPT; ++k) v[k] = load(p.src[0], k);
+            // the ranks in turn, a rank's loads under the additions of the one before
+            for (int r = 1; r < p.nsrc; ++r) {
+                uint4 next[PPT];
+#pragma unroll
+                for (int k = 0; k < PPT; ++k) next[k] = load(p.src[r], k);
+#pragma unroll
+                for (int k = 0; k < PPT; ++k) {
+                    Pack f;
+                    unpack8(v[k], f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) h[k][i] = r == 1 ? f[i] : add2(h[k][i], f[i]);
+                    if (p.has_res && r == p.nsrc - 1) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) h[k][i] = add2(h[k][i], 0ull);  // a sum of -0.0 counts as +0.0
+                    }
+                    v[k] = next[k];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < PPT; ++k) {
+                Pack f;
+                unpack8(v[k], f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[k][i] = p.nsrc == 1 ? f[i] : add2(h[k][i], f[i]);
+                    if (!p.has_res) h[k][i] = add2(h[k][i], 0ull);
+                    sum2 = add2(h[k][i], sum2);
+                }
+            }
+        }
+        if (p.res_out && there) {
+#pragma unroll
+            for (int k = 0; k < PPT; ++k)
+                if (l + k * G < P) ptx::st_stream_v4(p.res_out + at + k * G * 8, pack8(h[k]));
+        }
+        float sum = both(sum2);
+        for (int o = 1; o < G; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const float mean = sum * p.inv_n;
+        const uint64_t mean2 = pair(-mean, -mean);
+        uint64_t q2 = 0ull;
+#pragma unroll
+        for (int k = 0; k < PPT; ++k) {
+            if (l + k * G < P) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[k][i] = add2(h[k][i], mean2);
+                    q2 = fma2(h[k][i], h[k][i], q2);
+                }
+            }
+        }
+        float q = both(q2);
+        for (int o = 1; o < G; o <<= 1) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
+        const float inv = rsqrtf(q * p.inv_n + p.eps);
+        const uint64_t inv2 = pair(inv, inv);
+        if (there) {
+#pragma unroll
+            for (int k = 0; k < PPT; ++k) {
+                if (l + k * G < P) {
+                    Pack g, b = {}, o;
+                    load8(p.gamma + (l + k * G) * 8, g);
+                    if (p.beta) load8(p.beta + (l + k * G) * 8, b);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = fma2(mul2(h[k][i], inv2), g[i], b[i]);
+                    ptx::st_stream_v4(p.out + at + k * G * 8, pack8(o));
                 }
             }
         }
@@ -610,6 +703,13 @@ __global__ void __launch_bounds__(256, 2) layernorm_backward_small_kernel(const 
     }
 }
 
+// Lanes a row rather than a block: where a row is hardly more than its exchange (R = 8, 16384 x 64: 4.0 us, a block 15.5), and
+// with few sources where there are many rows (R = 1, 16384 x 264: 10.7 us for 16.7, x 1024 26.5 for 29.5; 4000 x 1024 8.9 for
+// 8.0; with eight, whose loads the ring keeps further ahead, 16384 x 264 26.9 for 22.1).
+bool narrow(int P, int sources, int64_t M, int num_sms) {
+    return P <= 16 ? M > 4 * (int64_t)num_sms : P <= 128 && sources <= 3 && M > 32 * (int64_t)num_sms;
+}
+
 // Packs a thread holds, of a row of P: as the RMSNorm's kernels, whose registers these have.
 int packs_per_thread(int P, bool alone) {
     if (alone && P <= 1024) return P <= 512 ? 1 : 2;
@@ -645,6 +745,17 @@ void (*backward_kernel(int ppt, int threads, int rows))(RowsParams) {
 
 RowsPlan layernorm_plan(RowsParams& p, int num_sms) {
     const int P = p.N / 8;
+    p.lanes = 0;
+    if (!p.backward && narrow(P, p.nsrc, p.M, num_sms)) {
+        RowsPlan plan;
+        p.lanes = P <= 8 ? 8 : P <= 16 ? 16 : 32;
+        plan.ppt = (P + p.lanes - 1) / p.lanes;
+        plan.threads = kNarrowWarps * 32;
+        plan.smem = 0;
+        const int64_t rows = kNarrowWarps * (32 / p.lanes), blocks = (p.M + rows - 1) / rows;
+        plan.grid = (int)std::min<int64_t>(blocks, (int64_t)num_sms * (plan.ppt <= 2 ? 4 : 3));
+        return plan;
+    }
     const int ppt = p.backward ? backward_packs_per_thread(P) : packs_per_thread(P, p.M <= num_sms);
     p.rows = 1;
     const int one_nt = ((P + ppt - 1) / ppt + 31) / 32 * 32;
@@ -692,7 +803,12 @@ cudaError_t layernorm_prepare() {
 }
 
 cudaError_t launch_layernorm_rows(const RowsParams& p, const RowsPlan& plan, cudaStream_t s) {
-    return launch_dependent(forward_kernel(plan.ppt, plan.threads), plan.grid, plan.threads, plan.smem, s, p);
+    auto* kernel = p.lanes == 0   ? forward_kernel(plan.ppt, plan.threads)
+                   : plan.ppt == 1 ? layernorm_narrow_kernel<1>
+                   : plan.ppt == 2 ? layernorm_narrow_kernel<2>
+                   : plan.ppt == 3 ? layernorm_narrow_kernel<3>
+                                   : layernorm_narrow_kernel<4>;
+    return launch_dependent(kernel, plan.grid, plan.threads, plan.smem, s, p);
 }
 
 cudaError_t launch_layernorm_backward_rows(RowsParams& p, const RowsPlan& plan, float* scratch, float* dgamma, float* dbeta,

@@ -40,7 +40,10 @@ def run(ws, parts, res, gamma, beta, residual_out=True, out=None):
 # one token to several rows a block; one pack, a partial last warp, every packs-per-thread variant, the widest row
 SHAPES = [(1, 1, 8), (2, 3, 40), (8, 1, 7168), (3, 5, 264), (4, 37, 4104), (8, 310, 1024), (1, 700, 2056), (5, 2, 5000),
           (8, 2, 8192), (2, 3, 10008), (7, 2, 16384), (8, 2, 32768), (1, 1300, 64), (6, 200, 7168), (2, 160, 4096),
-          (1, 152, 2064), (4, 153, 5000), (3, 400, 8192), (8, 320, 16384), (1, 400, 24000), (8, 170, 32768), (1, 4000, 768)]
+          (1, 152, 2064), (4, 153, 5000), (3, 400, 8192), (8, 320, 16384), (1, 400, 24000), (8, 170, 32768), (1, 4000, 768),
+          # lanes a row: 1 to 16 packs with any number of ranks, up to 128 with few, a last warp with rows missing
+          (1, 700, 8), (8, 1111, 64), (3, 611, 72), (5, 701, 128), (1, 5001, 136), (2, 5003, 264), (1, 5000, 520), (2, 4871, 768),
+          (1, 6001, 1000), (1, 5000, 1024)]
 
 
 @pytest.mark.parametrize("R,M,N", SHAPES)
@@ -54,7 +57,7 @@ def test_forward_against_64_bits(ws, R, M, N):
     want, tol, h, tol_h = ref.layernorm64(parts, res, gamma, beta)
     ref.check(y, want, tol, "y")
     ref.check(ro, h, tol_h, "residual_out")
-    assert ws.last_launch()["kernel"] == "layernorm_rows_kernel"
+    assert ws.last_launch()["kernel"] in ("layernorm_rows_kernel", "layernorm_narrow_kernel")
     # without the optional tensors; in place of the residual
     y2, _ = run(ws, parts, res, gamma, beta, residual_out=False)
     assert torch.equal(y2, y)
