@@ -68,7 +68,8 @@ KERNEL_NAMES = {0: "none", 1: "memset", 2: "gemm_reduce_kernel", 3: "gemm_pair_k
                 5: "ar_oneshot_kernel", 6: "norm_quant_rows_kernel", 7: "norm_backward_rows_kernel",
                 8: "qweight_kernel", 9: "layernorm_rows_kernel", 10: "layernorm_backward_rows_kernel",
                 11: "xent_kernel<LogSum>", 12: "xent_kernel<DLogits>", 13: "embed_kernel", 14: "embed_sort_kernel",
-                15: "embed_few_kernel", 16: "layernorm_narrow_kernel"}
+                15: "embed_few_kernel", 16: "layernorm_narrow_kernel",
+                17: "layernorm_backward_narrow_kernel"}
 PIECE_WORDS = 64
 TILE_M, TILE_N = 128, 256
 

@@ -1139,7 +1139,7 @@ are_status are_allreduce_layernorm_backward(const are_bf16* const dy[], const ar
     RowsPlan plan = layernorm_plan(p, ws->num_sms);
     // two rows of partial sums a block
     plan.grid = (int)std::min<int64_t>(plan.grid, (int64_t)norm_backward_scratch_words(ws->caps.N_max, ws->num_sms) / (2 * N));
-    ws->last = are_launch_info{ARE_KERNEL_LAYERNORM_BACKWARD_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
+    ws->last = are_launch_info{p.lanes ? ARE_KERNEL_LAYERNORM_BACKWARD_NARROW : ARE_KERNEL_LAYERNORM_BACKWARD_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
     return from_cuda(launch_layernorm_backward_rows(p, plan, ws->d_dgamma, dgamma, dbeta, s));
 }
 

@@ -104,7 +104,7 @@ struct RowsParams {
     int backward;       // the backward pass (gamma in shared memory, fewer threads)
     int extra_words;    // fp32 words of shared memory of the kernel's own, a multiple of 4 (set by the plans)
     int red_words;      // words that a block's sums are exchanged in, a multiple of 4 (set by the plans)
-    int lanes;          // LayerNorm forward: lanes that take a row (8, 16, 32), 0: a block does (set by layernorm_plan)
+    int lanes;          // LayerNorm: lanes that take a row (8, 16, 32), 0: a block does (set by layernorm_plan)
     int rows;           // LayerNorm backward: rows that a block takes at a time (set by layernorm_plan)
     int nt;             // consumer threads, a multiple of 32 (set by rows_plan)
     int slices;         // slices of nt packs a row (set by rows_plan)

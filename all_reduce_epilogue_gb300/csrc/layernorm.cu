@@ -21,7 +21,7 @@
 // 16384 x 4096: 89 us, 6.0 TB/s, x 768: 21 us, 4.8 TB/s, x 64: 3.2 us; one row of 7168, R = 8:
 // 4.1 us, all latency.  Backward, R = 1, 16384 x 7168: 153 us, 6.1 TB/s, x 4096:
 // 93 us, 5.8 TB/s, x 768: 34 us, 3.0 TB/s (a row's exchange and joins for one pack a
-// thread); R = 3, 1001 x 5000: 16.8 us, 6.6 rows an SM and 4 us for the sums of the
+// thread), x 264: 18 us, x 64: 9.4; R = 3, 1001 x 5000: 16.8 us, 6.6 rows an SM and 4 us for the sums of the
 // blocks' partial rows.
 #include <algorithm>
 
@@ -703,11 +703,150 @@ __global__ void __launch_bounds__(256, 2) layernorm_backward_small_kernel(const 
     }
 }
 
+// The same rows by lanes, backward: a lane has the same columns in every row that it takes, and a block joins its lanes' and
+// warps' sums in a fixed order at its end.
+constexpr int kNarrowBackWarps = 4;
+
+template <int PPT, bool ONE>
+__global__ void __launch_bounds__(kNarrowBackWarps * 32, PPT == 1 ? 6 : 5)
+    layernorm_backward_narrow_kernel(const __grid_constant__ RowsParams p) {
+    __shared__ float sums[2][512];
+    const int lane = threadIdx.x & 31, wb = threadIdx.x >> 5, G = p.lanes, l = lane & (G - 1), P = p.N >> 3, per_warp = 32 / G;
+    ptx::grid_launch_dependents();
+    ptx::grid_wait();
+    Pack dg[PPT], db[PPT];
+#pragma unroll
+    for (int k = 0; k < PPT; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dg[k][i] = db[k][i] = 0ull;
+    const int64_t warps = (int64_t)gridDim.x * kNarrowBackWarps;
+    for (int64_t w = (int64_t)blockIdx.x * kNarrowBackWarps + wb; w * per_warp < p.M; w += warps) {
+        const int64_t row = w * per_warp + lane / G;
+        const bool there = row < p.M;  // (all lanes stay for the exchanges; a row that is not there is zeros)
+        const int64_t at = row * p.N + l * 8;
+        auto load = [&](const uint16_t* from, int k) {
+            return there && l + k * G < P ? ptx::ld_stream_v4(from + at + k * G * 8) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        Pack dy[ONE ? 1 : PPT];
+        uint4 dv[PPT], hv[PPT], ev[PPT];
+#pragma unroll
+        for (int k = 0; k < PPT; ++k) dv[k] = load(p.src[0], k);
+#pragma unroll
+        for (int k = 0; k < PPT; ++k) hv[k] = load(p.src[p.R], k);
+        if (p.has_res) {
+#pragma unroll
+            for (int k = 0; k < PPT; ++k) ev[k] = load(p.src[p.R + 1], k);
+        }
+        if (!ONE) {
+#pragma unroll
+            for (int k = 0; k < PPT; ++k) unpack8(dv[k], dy[ONE ? 0 : k]);
+            for (int r = 1; r < p.R; ++r) {
+#pragma unroll
+                for (int k = 0; k < PPT; ++k) dv[k] = load(p.src[r], k);
+#pragma unroll
+                for (int k = 0; k < PPT; ++k) {
+                    Pack f;
+                    unpack8(dv[k], f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dy[ONE ? 0 : k][i] = add2(dy[ONE ? 0 : k][i], f[i]);
+                }
+            }
+        }
+        uint64_t sum2 = 0ull;
+#pragma unroll
+        for (int k = 0; k < PPT; ++k) {
+            Pack h;
+            unpack8(hv[k], h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum2 = add2(h[i], sum2);
+        }
+        float H = both(sum2);
+        for (int o = 1; o < G; o <<= 1) H += __shfl_xor_sync(0xFFFFFFFFu, H, o);
+        const float mean = H * p.inv_n;
+        const uint64_t mean2 = pair(-mean, -mean);
+        uint64_t q2 = 0ull, g2 = 0ull, c2 = 0ull;
+#pragma unroll
+        for (int k = 0; k < PPT; ++k) {
+            if (l + k * G < P) {
+                Pack h, gk, d1;
+                unpack8(hv[k], h);
+                load8(p.gamma + (l + k * G) * 8, gk);
+                if (ONE) unpack8(dv[k], d1);
+                const Pack& d = ONE ? d1 : dy[ONE ? 0 : k];
+                add_centred(h, d, gk, mean2, q2, c2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) g2 = fma2(d[i], gk[i], g2);
+            }
+        }
+        float Q = both(q2), A = both(g2), C = both(c2);
+        for (int o = 1; o < G; o <<= 1) {
+            Q += __shfl_xor_sync(0xFFFFFFFFu, Q, o);
+            A += __shfl_xor_sync(0xFFFFFFFFu, A, o);
+            C += __shfl_xor_sync(0xFFFFFFFFu, C, o);
+        }
+        const RowCoefs coefs = row_coefs(mean, Q * p.inv_n, A * p.inv_n, C, p);
+        if (there) {
+#pragma unroll
+            for (int k = 0; k < PPT; ++k) {
+                if (l + k * G < P) {
+                    Pack h, gk, e = {}, o, d1;
+                    unpack8(hv[k], h);
+                    if (p.has_res) unpack8(ev[k], e);
+                    load8(p.gamma + (l + k * G) * 8, gk);
+                    if (ONE) unpack8(dv[k], d1);
+                    const Pack& d = ONE ? d1 : dy[ONE ? 0 : k];
+                    outputs(h, d, gk, e, coefs, o, dg[k]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) db[k][i] = add2(db[k][i], d[i]);
+                    ptx::st_stream_v4(p.res_out + at + k * G * 8, pack8(o));
+                }
+            }
+        }
+    }
+    // the lanes of a warp that have the same columns, then the warps in turn
+    for (int w = 0; w < kNarrowBackWarps; ++w) {
+        if (wb == w) {
+#pragma unroll
+            for (int k = 0; k < PPT; ++k) {
+                const int pk = l + k * G;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float2 a = unpair(dg[k][i]), b = unpair(db[k][i]);
+                    for (int o = G; o < 32; o <<= 1) {
+                        a.x += __shfl_xor_sync(0xFFFFFFFFu, a.x, o);
+                        a.y += __shfl_xor_sync(0xFFFFFFFFu, a.y, o);
+                        b.x += __shfl_xor_sync(0xFFFFFFFFu, b.x, o);
+                        b.y += __shfl_xor_sync(0xFFFFFFFFu, b.y, o);
+                    }
+                    if (lane < G && pk < P) {
+                        float2* const g = reinterpret_cast<float2*>(sums[0] + pk * 8) + i;
+                        float2* const t = reinterpret_cast<float2*>(sums[1] + pk * 8) + i;
+                        const float2 x = w ? *g : make_float2(0.f, 0.f), y = w ? *t : make_float2(0.f, 0.f);
+                        *g = make_float2(x.x + a.x, x.y + a.y);
+                        *t = make_float2(y.x + b.x, y.y + b.y);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+    for (int j = threadIdx.x; j < p.N; j += kNarrowBackWarps * 32) {
+        if (p.dgamma) p.dgamma[(size_t)blockIdx.x * p.N + j] = sums[0][j];
+        if (p.dbeta) p.dbeta[(size_t)blockIdx.x * p.N + j] = sums[1][j];
+    }
+}
+
 // Lanes a row rather than a block: where a row is hardly more than its exchange (R = 8, 16384 x 64: 4.0 us, a block 15.5), and
 // with few sources where there are many rows (R = 1, 16384 x 264: 10.7 us for 16.7, x 1024 26.5 for 29.5; 4000 x 1024 8.9 for
 // 8.0; with eight, whose loads the ring keeps further ahead, 16384 x 264 26.9 for 22.1).
 bool narrow(int P, int sources, int64_t M, int num_sms) {
     return P <= 16 ? M > 4 * (int64_t)num_sms : P <= 128 && sources <= 3 && M > 32 * (int64_t)num_sms;
+}
+
+// Backward, where a block already takes four such rows at a time: R = 1, 16384 x 64: 9.4 us for 17.2, x 264 17.9 for 25.9, 4000
+// x 264 10.0 for 12.0, 1500 x 64 5.9 for 7.2; R = 4, 16384 x 64 10.3 for 20.2, but 4000 x 264 12.4 for 10.5.
+bool narrow_backward(int P, int sources, int64_t M, int num_sms) {
+    return (P <= 16 || (P <= 64 && sources <= 3)) && M > 8 * (int64_t)num_sms;
 }
 
 // Packs a thread holds, of a row of P: as the RMSNorm's kernels, whose registers these have.
@@ -728,7 +867,8 @@ void (*forward_kernel(int ppt, int threads))(RowsParams) {
 }
 
 template <bool ONE>
-void (*backward_kernel(int ppt, int threads, int rows))(RowsParams) {
+void (*backward_kernel(int ppt, int threads, int rows, int lanes))(RowsParams) {
+    if (lanes) return ppt == 1 ? layernorm_backward_narrow_kernel<1, ONE> : layernorm_backward_narrow_kernel<2, ONE>;
     if (rows == 4) return layernorm_backward_small_kernel<1, 4, ONE>;
     if (rows == 2) return layernorm_backward_small_kernel<2, 2, ONE>;
     switch (ppt) {
@@ -746,18 +886,20 @@ void (*backward_kernel(int ppt, int threads, int rows))(RowsParams) {
 RowsPlan layernorm_plan(RowsParams& p, int num_sms) {
     const int P = p.N / 8;
     p.lanes = 0;
-    if (!p.backward && narrow(P, p.nsrc, p.M, num_sms)) {
+    p.rows = 1;
+    if (p.backward ? narrow_backward(P, p.nsrc, p.M, num_sms) : narrow(P, p.nsrc, p.M, num_sms)) {
         RowsPlan plan;
         p.lanes = P <= 8 ? 8 : P <= 16 ? 16 : 32;
         plan.ppt = (P + p.lanes - 1) / p.lanes;
-        plan.threads = kNarrowWarps * 32;
+        const int warps = p.backward ? kNarrowBackWarps : kNarrowWarps;
+        const int resident = p.backward ? (plan.ppt == 1 ? 6 : 5) : plan.ppt <= 2 ? 4 : 3;
+        plan.threads = warps * 32;
         plan.smem = 0;
-        const int64_t rows = kNarrowWarps * (32 / p.lanes), blocks = (p.M + rows - 1) / rows;
-        plan.grid = (int)std::min<int64_t>(blocks, (int64_t)num_sms * (plan.ppt <= 2 ? 4 : 3));
+        const int64_t rows = warps * (32 / p.lanes), blocks = (p.M + rows - 1) / rows;
+        plan.grid = (int)std::min<int64_t>(blocks, (int64_t)num_sms * resident);
         return plan;
     }
     const int ppt = p.backward ? backward_packs_per_thread(P) : packs_per_thread(P, p.M <= num_sms);
-    p.rows = 1;
     const int one_nt = ((P + ppt - 1) / ppt + 31) / 32 * 32;
     if (p.backward && ppt <= 2 && P <= 512 && p.M > (int64_t)num_sms * (kRowsThreads / (one_nt + 32))) {
         // several rows at a time, where there is more than a round of single ones and the ring holds that many for every
@@ -795,10 +937,10 @@ cudaError_t layernorm_prepare() {
         for (int threads : {288, 512})
             for (bool one : {false, true})
                 if (e == cudaSuccess)
-                    e = opt_in(one ? backward_kernel<true>(ppt, threads, 1) : backward_kernel<false>(ppt, threads, 1));
+                    e = opt_in(one ? backward_kernel<true>(ppt, threads, 1, 0) : backward_kernel<false>(ppt, threads, 1, 0));
     for (int rows : {2, 4})
         for (bool one : {false, true})
-            if (e == cudaSuccess) e = opt_in(one ? backward_kernel<true>(0, 0, rows) : backward_kernel<false>(0, 0, rows));
+            if (e == cudaSuccess) e = opt_in(one ? backward_kernel<true>(0, 0, rows, 0) : backward_kernel<false>(0, 0, rows, 0));
     return e;
 }
 
@@ -818,8 +960,8 @@ cudaError_t launch_layernorm_backward_rows(RowsParams& p, const RowsPlan& plan, 
     float* const second = scratch + (dgamma ? (size_t)plan.grid * p.N : 0);
     p.dgamma = dgamma == nullptr ? nullptr : one ? dgamma : scratch;
     p.dbeta = dbeta == nullptr ? nullptr : one ? dbeta : second;
-    auto* kernel = p.R == 1 ? backward_kernel<true>(plan.ppt, plan.threads, p.rows)
-                            : backward_kernel<false>(plan.ppt, plan.threads, p.rows);
+    auto* kernel = p.R == 1 ? backward_kernel<true>(plan.ppt, plan.threads, p.rows, p.lanes)
+                            : backward_kernel<false>(plan.ppt, plan.threads, p.rows, p.lanes);
     cudaError_t e = launch_dependent(kernel, plan.grid, plan.threads, plan.smem, s, p);
     if (e == cudaSuccess && !one && (dgamma || dbeta))
         e = launch_row_sums(scratch, dgamma ? dgamma : dbeta, dgamma ? dbeta : nullptr, plan.grid, p.N, s);

@@ -212,7 +212,8 @@ typedef enum are_kernel {
     ARE_KERNEL_EMBEDDING = 13,
     ARE_KERNEL_EMBEDDING_BACKWARD = 14,      /* the first of its kernels */
     ARE_KERNEL_EMBEDDING_BACKWARD_FEW = 15,  /* up to 512 tokens */
-    ARE_KERNEL_LAYERNORM_NARROW = 16         /* AR+LayerNorm, lanes a row */
+    ARE_KERNEL_LAYERNORM_NARROW = 16,        /* AR+LayerNorm, lanes a row */
+    ARE_KERNEL_LAYERNORM_BACKWARD_NARROW = 17 /* its backward pass */
 } are_kernel;
 
 typedef struct are_launch_info {
