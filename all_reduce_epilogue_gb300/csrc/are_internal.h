@@ -350,9 +350,6 @@ cudaError_t gemm_prepare_kernels();
 // bf16 [outer, inner] row-major tensor map, 128B-swizzled boxes of box_inner x box_outer.
 cudaError_t make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
                            uint32_t box_outer);
-// fp32 [d2, d1, d0] map (d0 contiguous), 128B-swizzled boxes of box0 x box1 x 1.
-cudaError_t make_tmap_f32_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0,
-                             uint32_t box1);
 // The pair kernel's partial slots for T tiles and R ranks as a 5-D map (see GemmParams::tmPart).
 cudaError_t make_tmap_part(CUtensorMap* m, const void* part, uint64_t T, uint64_t R);
 cudaError_t launch_gemm_reduce(const GemmParams& p, int mode, int grid, cudaStream_t stream);

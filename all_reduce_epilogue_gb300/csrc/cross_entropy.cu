@@ -39,6 +39,7 @@
 // vocabulary 11001, both directions: 46 us, the latencies of six kernels (37 at K = 1024,
 // whose rows are whole lines).
 #include <cuda_bf16.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cmath>
@@ -690,6 +691,20 @@ constexpr int kFewTokens = 128;
 constexpr size_t kMinPairs = 4u << 20;  // bytes for d or the forward pass's pairs, whatever M_max is: few pieces for few tokens
 constexpr int kGroup = 16;  // rows of tiles whose operand stays in L2: 4096 rows
 
+// dh's sums as a map [splits, M, K] of fp32, 128B-swizzled boxes of 32 columns x 32 rows.
+cudaError_t make_tmap_sums(CUtensorMap* m, const void* base, uint64_t K, uint64_t M, uint64_t splits) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {K, M, splits}, strides[2] = {K * 4, K * M * 4};
+    const cuuint32_t box[3] = {32, 32, 1}, each[3] = {1, 1, 1};
+    const CUresult r = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
+        m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 int ceil256(int64_t n) { return (int)((n + kTile - 1) / kTile); }
 
 }  // namespace
@@ -832,7 +847,7 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
                                  (int)std::min({(int64_t)(b.sizes.sum_bytes / ((size_t)c.M * c.K * 4)), (int64_t)piece / 2, (int64_t)4 * left}));
     d.sums = pieces > 1 || splits > 1;
     if (e == cudaSuccess && c.dh)
-        e = d.sums ? make_tmap_f32_3d(&d.tmDH, b.sums, (uint64_t)c.K, (uint64_t)c.M, (uint64_t)splits, 32, 32)
+        e = d.sums ? make_tmap_sums(&d.tmDH, b.sums, (uint64_t)c.K, (uint64_t)c.M, (uint64_t)splits)
                    : make_tmap_bf16(&d.tmDH, c.dh, (uint64_t)c.K, (uint64_t)c.M, 64, 32);
     if (e == cudaSuccess && c.has_dw) {
         const int64_t packs = c.M * c.K / 8;
