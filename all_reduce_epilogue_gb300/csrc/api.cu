@@ -1073,6 +1073,17 @@ are_status are_allreduce_layernorm(const are_bf16* const partials[], const are_b
         (beta && !aligned16(beta)) || !ptr_ok(out, M * N))
         return ARE_EINVAL;
     if (!(eps > 0.f) || !std::isfinite(eps)) return ARE_EINVAL;
+    // a row is read before it is written, so `out` may be one of the inputs itself, residual_out the residual
+    const size_t bytes = (size_t)M * N * 2;
+    Extents mem;
+    mem.write(residual_out, bytes);
+    mem.write(out, bytes);
+    for (int r = 0; r < R; ++r)
+        if (partials[r] != out) mem.read(partials[r], bytes);
+    if (residual != out && residual != residual_out) mem.read(residual, bytes);
+    mem.read(gamma, (size_t)N * 4);
+    mem.read(beta, (size_t)N * 4);
+    if (!mem.ok) return ARE_EINVAL;
     TryLock lk(ws->mu);
     if (!lk.ok) return ARE_EBUSY;
     if (!on_device(ws)) return ARE_EINVAL;
@@ -1108,6 +1119,15 @@ are_status are_allreduce_layernorm_backward(const are_bf16* const dy[], const ar
         (dgamma && !aligned16(dgamma)) || (dbeta && !aligned16(dbeta)))
         return ARE_EINVAL;
     if (!(eps > 0.f) || !std::isfinite(eps)) return ARE_EINVAL;
+    Extents mem;
+    mem.write(dh, (size_t)M * N * 2);
+    mem.write(dgamma, (size_t)N * 4);
+    mem.write(dbeta, (size_t)N * 4);
+    for (int r = 0; r < R; ++r) mem.read(dy[r], (size_t)M * N * 2);
+    mem.read(h, (size_t)M * N * 2);
+    if (dres != dh) mem.read(dres, (size_t)M * N * 2);
+    mem.read(gamma, (size_t)N * 4);
+    if (!mem.ok) return ARE_EINVAL;
     TryLock lk(ws->mu);
     if (!lk.ok) return ARE_EBUSY;
     if (!on_device(ws)) return ARE_EINVAL;

@@ -564,16 +564,17 @@ ARE_API are_status are_allreduce_rmsnorm_backward(const are_bf16* const dy[], co
  *  partials, residual, eps: as in are_allreduce_add_rmsnorm
  *  gamma       : fp32 [N]
  *  beta        : fp32 [N] or NULL (a norm without bias)
- *  out         : bf16 [M, N]
+ *  out         : bf16 [M, N]; may be the same buffer as a partial or `residual`
  *  residual_out: bf16 [M, N] or NULL; receives bf16(h); may be the same buffer
- *                as `residual` (in place).  It must not alias a partial or `out`.
+ *                as `residual` (in place)
  *  Result      : h = sum_{r=0..R-1} f32(partials[r]), in that order (a sum of
  *                -0.0 counts as +0.0), + f32(residual);
  *                out = bf16( (h - mean) * rsqrt(var + eps) * gamma + beta ),
  *                mean = mean_j(h_j), var = mean_j((h_j - mean)^2), in fp32, the
  *                squares summed around the mean.
  * A row with a value that is not finite has NaN outputs; other rows do not
- * notice.  Needs no capacity of the workspace but R <= R_max.
+ * notice.  Outputs that overlap one another or an input in any other way are
+ * refused (ARE_EINVAL).  Needs no capacity of the workspace but R <= R_max.
  */
 ARE_API are_status are_allreduce_layernorm(const are_bf16* const partials[], const are_bf16* residual,
                                            const float* gamma, const float* beta, float eps, are_bf16* out,
@@ -581,7 +582,8 @@ ARE_API are_status are_allreduce_layernorm(const are_bf16* const partials[], con
 
 /*
  * Backward pass of all-reduce + residual add + LayerNorm.  Arguments as in
- * are_allreduce_rmsnorm_backward (dres in place of dh allowed), and
+ * are_allreduce_rmsnorm_backward (dres in place of dh allowed; any other overlap
+ * of an output is refused, ARE_EINVAL), and
  *  dgamma, dbeta: fp32 [N], either may be NULL (frozen, or no bias); overwritten
  *  Result  : dy = sum_{r=0..R-1} f32(dy[r]) in that order, g = dy * gamma,
  *            inv = rsqrt(var + eps), xhat = (h - mean) * inv, per row of h;

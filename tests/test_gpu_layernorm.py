@@ -301,3 +301,46 @@ def test_refusals(ws):
             are.allreduce_layernorm(parts, res, gamma, beta, ref.EPS, out, small)   # R
         with pytest.raises(are.AreError):
             are.allreduce_layernorm_backward(parts[:1], res, gamma, ref.EPS, out, dg, None, small)  # N
+
+
+@pytest.mark.parametrize("R,M,N", [(2, 700, 64), (1, 5001, 264), (3, 37, 4104), (1, 153, 24000)])
+def test_in_place_of_an_input(ws, R, M, N):
+    """`out` may be a partial or the residual itself: a row is read before it is written."""
+    parts, res, gamma, beta = inputs(R, M, N, R + M + N)
+    y, ro = run(ws, parts, res, gamma, beta)
+    into = res.clone()
+    run(ws, parts, into, gamma, beta, out=into)
+    assert torch.equal(into, y)
+    first = parts[0].clone()
+    _, h = run(ws, [first] + parts[1:], res, gamma, beta, out=first)
+    assert torch.equal(first, y) and torch.equal(h, ro)
+
+
+def test_overlaps_are_refused(ws):
+    """Memory that a call writes next to what it reads: every other overlap than an input in place."""
+    M, N = 6, 64
+    buf = torch.zeros(4 * M * N, dtype=torch.bfloat16, device="cuda")
+    at = lambda k: buf[k:k + M * N].view(M, N)
+    x, shifted, free = at(0), at(8), at(2 * M * N)
+    sums = torch.zeros(3 * N, device="cuda")
+    gamma, a, b = sums[:N], sums[N:2 * N], sums[2 * N:]
+
+    def forward(parts, res, out, ro, beta=a, weight=gamma):
+        are.allreduce_layernorm(parts, res, weight, beta, ref.EPS, out, ws, residual_out=ro)
+
+    def back(dy, h, dh, dgamma=a, dbeta=b, dres=None):
+        are.allreduce_layernorm_backward(dy, h, gamma, ref.EPS, dh, dgamma, dbeta, ws, dres=dres)
+
+    other = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    words = buf.view(torch.float32)[:N]   # in x
+    for call in (lambda: forward([x], None, shifted, None), lambda: forward([x], shifted, other, x),
+                 lambda: forward([x], other, free, shifted), lambda: forward([x], None, free, free),
+                 lambda: forward([other], x, other, shifted), lambda: forward([other], None, x, None, beta=words),
+                 lambda: forward([other], None, other, x, weight=words),
+                 lambda: back([x], other, x), lambda: back([x], other, shifted), lambda: back([other], x, x),
+                 lambda: back([other], x, free, dres=at(2 * M * N + 8)), lambda: back([x], other, free, dgamma=a, dbeta=a),
+                 lambda: back([x], other, free, dgamma=gamma), lambda: back([x], other, free, dbeta=words)):
+        with pytest.raises(are.AreError):
+            call()
+    back([x], other, free, dres=free)
+    torch.cuda.synchronize()
