@@ -279,11 +279,25 @@ cudaError_t launch_embedding_backward(EmbedParams& p, void* sort, float* scratch
 // ------------------------------------------------------------------ cross entropy (cross_entropy.cu)
 enum XentPass : int { kXentLogSum = 0, kXentDLogits = 1, kXentDH = 2, kXentDW = 3, kXentGrads = 4 };
 
+// n / d for n < 2^31 as a product and a shift (Granlund and Montgomery 1994): with s = ceil(log2 d) and mul = floor(2^(31+s) / d)
+// + 1 the product is less than n 2^-(31+s) <= 1/d too large.
+struct Divisor {
+    uint32_t mul = 0, shift = 0;
+    Divisor() = default;
+    explicit Divisor(uint32_t d) {
+        uint32_t s = 0;
+        while ((1ull << s) < d) ++s;
+        mul = (uint32_t)((1ull << (31 + s)) / d + 1);
+        shift = 31 + s;
+    }
+};
+
 struct XentGrid {
     int tiles_m, tiles_n;  // 256 x 256
     int splits;            // parts of the contraction
     int num_kb;            // its blocks of 64
-    int units;             // tiles_m * tiles_n * splits (set at the launch)
+    int units;             // tiles_m * tiles_n * splits (set at the launch, as what follows)
+    Divisor per_split, per_group, rows, last_rows, parts;  // tiles of a split, of a group; rows of a group, of the last one; splits
 };
 
 struct XentParams {
@@ -302,6 +316,7 @@ struct XentParams {
     int wide;                     // targets of 64 bits
     int tile;                     // columns of a vocabulary tile: 256, or 128 of one CTA
     int rank_tiles, tile0;        // vocabulary tiles of a rank; the piece's first
+    Divisor per_rank;             // rank_tiles (set at the launch)
     XentGrid grid[2];             // the second: kXentDW's in kXentGrads
     int a_rows;                   // rows of A that a copy takes: 128, fewer if M is less
     int group;                    // rows of tiles taken together

@@ -112,6 +112,8 @@ __device__ __noinline__ void drain(uint64_t* bar, uint32_t parity, const XentPar
         if (ptx::globaltimer() - t0 > p.timeout_ns) break;
 }
 
+__device__ __forceinline__ int quotient(int n, const Divisor& d) { return (int)(((uint64_t)(uint32_t)n * d.mul) >> d.shift); }
+
 struct Tile {
     int kind;      // which product: kXentLogSum, kXentDLogits, kXentDH, kXentDW
     int tm, tn, split;
@@ -128,16 +130,15 @@ __device__ __forceinline__ Tile tile_of(const XentParams& p, int u) {
     const bool second = PASS == kXentGrads && u >= p.grid[0].units;
     const XentGrid& g = p.grid[second ? 1 : 0];
     if (second) u -= p.grid[0].units;
-    const int per = g.tiles_m * g.tiles_n;
-    t.split = u / per;
-    u -= t.split * per;
-    const int per_group = p.group * g.tiles_n, n = u / per_group, first = n * p.group;
-    const int rows = min(g.tiles_m - first, p.group);
-    u -= n * per_group;
-    t.tm = first + u % rows;
-    t.tn = u / rows;
-    t.kb0 = (int)((int64_t)g.num_kb * t.split / g.splits);
-    t.kb1 = (int)((int64_t)g.num_kb * (t.split + 1) / g.splits);
+    t.split = quotient(u, g.per_split);
+    u -= t.split * (g.tiles_m * g.tiles_n);
+    const int n = quotient(u, g.per_group), first = n * p.group, left = g.tiles_m - first;
+    const bool whole = left >= p.group;
+    u -= n * (p.group * g.tiles_n);
+    t.tn = quotient(u, whole ? g.rows : g.last_rows);
+    t.tm = first + (u - t.tn * (whole ? p.group : left));
+    t.kb0 = quotient(g.num_kb * t.split, g.parts);
+    t.kb1 = quotient(g.num_kb * (t.split + 1), g.parts);
     return t;
 }
 
@@ -146,7 +147,7 @@ struct Place {
     int rank, col;
 };
 __device__ __forceinline__ Place place_of(const XentParams& p, int tile) {
-    const int v = p.tile0 + tile, r = v / p.rank_tiles;
+    const int v = p.tile0 + tile, r = quotient(v, p.per_rank);
     return Place{r, (v - r * p.rank_tiles) * p.tile};
 }
 // Columns of the tile that are in the vocabulary, 0..side.
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(co
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), 0));
+                    if (PAIR) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), 0));
                     else ptx::mbar_arrive(&tempty[buf]);
                 }
                 __syncwarp();
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(co
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), 0));
+                if (PAIR) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&tempty[buf]), 0));
                 else ptx::mbar_arrive(&tempty[buf]);
             }
         }
@@ -669,7 +670,16 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const uint4* h, const vo
 template <int PASS, bool PAIR = true>
 cudaError_t launch(XentParams& p, int clusters, cudaStream_t s) {
     p.units = 0;
-    for (XentGrid& g : p.grid) p.units += g.units = g.tiles_m * g.tiles_n * g.splits;
+    p.per_rank = Divisor(p.rank_tiles);
+    for (XentGrid& g : p.grid) {
+        p.units += g.units = g.tiles_m * g.tiles_n * g.splits;
+        if (g.units == 0) continue;
+        g.per_split = Divisor(g.tiles_m * g.tiles_n);
+        g.per_group = Divisor(p.group * g.tiles_n);
+        g.rows = Divisor(p.group);
+        g.last_rows = Divisor((g.tiles_m - 1) % p.group + 1);
+        g.parts = Divisor(g.splits);
+    }
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = PAIR ? 2 : 1;
