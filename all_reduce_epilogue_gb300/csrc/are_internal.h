@@ -322,6 +322,8 @@ struct XentParams {
     int group;                    // rows of tiles taken together
     int units;                    // (set at the launch)
     int sums, add;                // kXentDH: fp32 sums, added to what is there
+    const uint4* rows_from;       // kXentDLogits: h, or nullptr
+    uint4* rows_to;               // and its copy with zeros in the rows that have no target
     uint64_t timeout_ns;
 };
 

@@ -189,6 +189,27 @@ struct Stager {
     }
 };
 
+// The hidden states with zeros in the rows that have no target: d is 0 there, but 0 times an infinity or a NaN, which padding
+// may hold, is none.  dW's product reads the copy in h's place.  kXentDLogits' epilogue warps make it before their first tile,
+// under its products (a launch of its own took 10 us of 5 ms at 4096 x 4096, 2 of 40 at 77 x 1000).
+__device__ __forceinline__ void copy_rows(const XentParams& p, int warp, int warps) {
+    const int lane = threadIdx.x & 31, packs = p.K >> 3;
+    for (int64_t row = warp; row < p.M; row += warps) {
+        const bool on = target_of(p, (int)row) >= 0;
+        const uint4* from = p.rows_from + row * packs;
+        uint4* to = p.rows_to + row * packs;
+        constexpr int U = 4;  // packs in flight
+        for (int i0 = lane; i0 < packs; i0 += 32 * U) {
+            uint4 v[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) v[j] = on && i0 + 32 * j < packs ? from[i0 + 32 * j] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (i0 + 32 * j < packs) to[i0 + 32 * j] = v[j];
+        }
+    }
+}
+
 template <int PASS, bool PAIR>
 __global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(const __grid_constant__ XentParams p) {
     constexpr int kStages = Shape<PASS, PAIR>::kStages, kEpi = Shape<PASS, PAIR>::kEpi, kPart = PAIR ? kPartPair : kPartOne;
@@ -373,6 +394,7 @@ __global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(co
         const uint64_t scale = ptx::pair(kLog2e, kLog2e);
         int part = 0;
         bool ok = true;
+        if (PASS == kXentDLogits && p.rows_from) copy_rows(p, blockIdx.x * kEpi + warp - 4, gridDim.x * kEpi);
         for (int u = first; u < p.units; u += pairs) {
             const Tile t = tile_of<PASS>(p, u);
             uint64_t z[kCols / 2];  // pairs of columns
@@ -641,32 +663,6 @@ __global__ void __launch_bounds__(256) xent_dh_kernel(const float4* sums, uint2*
     }
 }
 
-// The hidden states with zeros in the rows that have no target: d is 0 there, but 0 times an infinity or a NaN, which padding
-// may hold, is none.  A copy is 64 MB to move at 4096 x 4096, 10 us of a step of 5 ms; the products read it in h's place.
-__global__ void __launch_bounds__(256) xent_rows_kernel(const uint4* h, const void* targets, int wide, int64_t vocab, uint4* out,
-                                                        int64_t packs, int row_packs) {
-    ptx::grid_launch_dependents();
-    ptx::grid_wait();
-    constexpr int U = 4;  // packs in flight
-    const int64_t step = (int64_t)gridDim.x * 256;
-    for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < packs; i0 += U * step) {
-        uint4 v[U];
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int64_t i = i0 + j * step;
-            v[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < packs) {
-                const int64_t row = i / row_packs;
-                const int64_t t = wide ? static_cast<const int64_t*>(targets)[row] : static_cast<const int32_t*>(targets)[row];
-                if (t >= 0 && t < vocab) v[j] = h[i];
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (i0 + j * step < packs) out[i0 + j * step] = v[j];
-    }
-}
-
 template <int PASS, bool PAIR = true>
 cudaError_t launch(XentParams& p, int clusters, cudaStream_t s) {
     p.units = 0;
@@ -859,11 +855,9 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
     if (e == cudaSuccess && c.dh)
         e = d.sums ? make_tmap_sums(&d.tmDH, b.sums, (uint64_t)c.K, (uint64_t)c.M, (uint64_t)splits)
                    : make_tmap_bf16(&d.tmDH, c.dh, (uint64_t)c.K, (uint64_t)c.M, 64, 32);
-    if (e == cudaSuccess && c.has_dw) {
-        const int64_t packs = c.M * c.K / 8;
-        e = launch_dependent(xent_rows_kernel, dim3((unsigned)std::min<int64_t>((packs + 255) / 256, 16 * b.clusters)), 256, 0, s,
-                             reinterpret_cast<const uint4*>(c.h), c.targets, c.wide, c.vocab, static_cast<uint4*>(b.h), packs,
-                             (int)(c.K / 8));
+    if (c.has_dw) {
+        z.rows_from = reinterpret_cast<const uint4*>(c.h);
+        z.rows_to = static_cast<uint4*>(b.h);
     }
     for (int t0 = 0; t0 < total && e == cudaSuccess; t0 += piece) {
         const int n = std::min(piece, total - t0);
@@ -880,6 +874,7 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
         }
         if (e == cudaSuccess) e = few ? launch<kXentDLogits, false>(z, b.clusters, s) : launch<kXentDLogits>(z, b.clusters, s);
         if (t0 == 0) *info = launched<kXentDLogits>(ARE_KERNEL_CROSS_ENTROPY_BACKWARD, z, few, b.clusters);
+        z.rows_from = nullptr;
         d.add = t0 > 0;
         if (e == cudaSuccess) e = launch<kXentGrads>(d, b.clusters, s);
     }
