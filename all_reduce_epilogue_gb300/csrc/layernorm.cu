@@ -854,7 +854,15 @@ int packs_per_thread(int P, bool alone) {
     if (alone && P <= 1024) return P <= 512 ? 1 : 2;
     return P <= 256 ? 1 : P <= 512 ? 2 : P <= 2048 ? 4 : 8;
 }
-int backward_packs_per_thread(int P) { return P <= 256 ? 1 : P <= 960 ? 2 : P <= 1440 ? 3 : P <= 1920 ? 4 : 5; }
+// Backward, three packs for a little more than two blocks of two hold: two blocks an SM have two rows' latencies side by side,
+// but need more rows to pay for their partial sums (R = 3: 16384 x 4104 119 us for 150 with one block, 4096 x 5120 41 for 46,
+// 1001 x 5120 17.3 for 16.7; R = 1: 16384 x 4104 113 for 121, 4096 x 5120 41 for 40).  Two packs with 16 warps and a
+// producer leave 96 registers a thread, enough for one rank's dy, which stays packed (R = 1: 16384 x 8192 182 us for 219 with
+// three packs; R = 3: 241 for 219).
+int backward_packs_per_thread(int P, int R, int sources, int64_t M, int num_sms) {
+    if (P > 512 && P <= 672 && M * sources > 100 * (int64_t)num_sms) return 3;
+    return P <= 256 ? 1 : P <= (R == 1 ? 1024 : 960) ? 2 : P <= 1440 ? 3 : P <= 1920 ? 4 : 5;
+}
 
 // The kernel of a plan: blocks of up to 288 threads leave room for two on an SM.
 void (*forward_kernel(int ppt, int threads))(RowsParams) {
@@ -874,6 +882,7 @@ void (*backward_kernel(int ppt, int threads, int rows, int lanes))(RowsParams) {
     switch (ppt) {
         case 1: return layernorm_backward_rows_kernel<1, ONE, 288, 2>;
         case 2:
+            if (ONE && threads > 512) return layernorm_backward_rows_kernel<2, true, 544, 1>;
             return threads <= 288 ? layernorm_backward_rows_kernel<2, ONE, 288, 2> : layernorm_backward_rows_kernel<2, ONE, 512, 1>;
         case 3: return layernorm_backward_rows_kernel<3, ONE, 512, 1>;
         case 4: return layernorm_backward_rows_kernel<4, ONE, 512, 1>;
@@ -899,7 +908,7 @@ RowsPlan layernorm_plan(RowsParams& p, int num_sms) {
         plan.grid = (int)std::min<int64_t>(blocks, (int64_t)num_sms * resident);
         return plan;
     }
-    const int ppt = p.backward ? backward_packs_per_thread(P) : packs_per_thread(P, p.M <= num_sms);
+    const int ppt = p.backward ? backward_packs_per_thread(P, p.R, p.nsrc, p.M, num_sms) : packs_per_thread(P, p.M <= num_sms);
     const int one_nt = ((P + ppt - 1) / ppt + 31) / 32 * 32;
     if (p.backward && ppt <= 2 && P <= 512 && p.M > (int64_t)num_sms * (kRowsThreads / (one_nt + 32))) {
         // several rows at a time, where there is more than a round of single ones and the ring holds that many for every
@@ -934,7 +943,7 @@ cudaError_t layernorm_prepare() {
         for (int threads : {288, 544})
             if (e == cudaSuccess) e = opt_in(forward_kernel(ppt, threads));
     for (int ppt : {1, 2, 3, 4, 5})
-        for (int threads : {288, 512})
+        for (int threads : {288, 512, 544})
             for (bool one : {false, true})
                 if (e == cudaSuccess)
                     e = opt_in(one ? backward_kernel<true>(ppt, threads, 1, 0) : backward_kernel<false>(ppt, threads, 1, 0));

@@ -344,3 +344,10 @@ def test_overlaps_are_refused(ws):
             call()
     back([x], other, free, dres=free)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("R,M,N,dres", [(3, 3100, 4104, True), (1, 5100, 5376, False), (8, 1700, 4608, True), (1, 155, 8192, True),
+                                        (1, 500, 7688, False), (2, 155, 8192, True), (1, 153, 8200, True)])
+def test_backward_of_wide_rows_against_64_bits(ws, R, M, N, dres):
+    """Three packs a thread and two blocks an SM, where there are many rows; two packs and 16 warps with one rank."""
+    test_backward_against_64_bits(ws, R, M, N, dres)
