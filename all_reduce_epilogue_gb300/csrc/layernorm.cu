@@ -17,7 +17,7 @@
 // barrier of the block.
 //
 // Bound by HBM, as the RMSNorm's: every input once, every output once.  Measured (a
-// copy moves 6.78 TB/s): forward, R = 8, 4096 x 7168: 99 us, 6.5 TB/s; R = 1,
+// copy moves 6.78 TB/s): forward, R = 8, 4096 x 7168: 98 us, 6.6 TB/s; R = 1,
 // 16384 x 4096: 89 us, 6.0 TB/s, x 768: 21 us, 4.8 TB/s, x 64: 3.2 us; one row of 7168, R = 8:
 // 4.1 us, all latency.  Backward, R = 1, 16384 x 7168: 153 us, 6.1 TB/s, x 4096:
 // 93 us, 5.8 TB/s, x 768: 34 us, 3.0 TB/s (a row's exchange and joins for one pack a
@@ -71,7 +71,7 @@ __device__ __forceinline__ float join_sum(float v, int ways) {
 
 // ---------------------------------------------------------------------- forward
 // Where gamma and beta come from: registers (up to two packs a thread), gamma from
-// registers and beta from shared memory (four), both from the caches (eight).
+// registers and beta from shared memory (three, four), both from the caches (eight).
 template <int PPT, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_rows_kernel(const __grid_constant__ RowsParams p) {
     extern __shared__ __align__(128) uint8_t rows_smem[];
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) layernorm_rows_kernel(const _
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     const int P = p.N >> 3;
     const size_t step = (size_t)p.nt * 16;
-    constexpr bool kGammaRegs = PPT <= 4, kBetaRegs = PPT <= 2, kBetaShared = PPT == 4;
+    constexpr bool kGammaRegs = PPT <= 4, kBetaRegs = PPT <= 2, kBetaShared = PPT == 3 || PPT == 4;
     const Join join = make_join(p);
     Pack gam[kGammaRegs ? PPT : 1], bet[kBetaRegs ? PPT : 1];
 #pragma unroll
@@ -849,10 +849,15 @@ bool narrow_backward(int P, int sources, int64_t M, int num_sms) {
     return (P <= 16 || (P <= 64 && sources <= 3)) && M > 8 * (int64_t)num_sms;
 }
 
-// Packs a thread holds, of a row of P: as the RMSNorm's kernels, whose registers these have.
-int packs_per_thread(int P, bool alone) {
-    if (alone && P <= 1024) return P <= 512 ? 1 : 2;
-    return P <= 256 ? 1 : P <= 512 ? 2 : P <= 2048 ? 4 : 8;
+// Packs a thread holds, of a row of P.  A row alone takes as many warps as it fills.  Up to 512 packs several blocks of an SM
+// hide one another's latencies (R = 1, 16384 x 2048, in us: one pack a thread and two blocks 55, two packs and four 51; 4096 x
+// 1536 15.0 and 10.6), above one block of up to 16 warps has the shortest row (R = 1, 16384 x 10000: four packs 289, three 225;
+// R = 8, 1001 x 7168: 28.1, two 24.6, though 16384 rows of it take 387 for 382).  Up to 640 four packs leave room for three
+// blocks, which many rows use (R = 1, 16384 x 5120: two packs 150, four 117; R = 8, 1001 rows: 19.6 and 22.6).
+int packs_per_thread(int P, int64_t M, int num_sms) {
+    if (M <= num_sms && P <= 1024) return P <= 512 ? 1 : 2;
+    if (P > 512 && P <= 640 && M > 16 * (int64_t)num_sms) return 4;
+    return P <= 128 ? 1 : P <= 1024 ? 2 : P <= 1536 ? 3 : P <= 2048 ? 4 : 8;
 }
 // Backward, three packs for a little more than two blocks of two hold: two blocks an SM have two rows' latencies side by side,
 // but need more rows to pay for their partial sums (R = 3: 16384 x 4104 119 us for 150 with one block, 4096 x 5120 41 for 46,
@@ -869,6 +874,7 @@ void (*forward_kernel(int ppt, int threads))(RowsParams) {
     switch (ppt) {
         case 1: return threads <= 288 ? layernorm_rows_kernel<1, 288, 2> : layernorm_rows_kernel<1, 544, 1>;
         case 2: return threads <= 288 ? layernorm_rows_kernel<2, 288, 2> : layernorm_rows_kernel<2, 544, 1>;
+        case 3: return layernorm_rows_kernel<3, 544, 1>;
         case 4: return threads <= 288 ? layernorm_rows_kernel<4, 288, 2> : layernorm_rows_kernel<4, 544, 1>;
         default: return layernorm_rows_kernel<8, 544, 1>;
     }
@@ -908,7 +914,7 @@ RowsPlan layernorm_plan(RowsParams& p, int num_sms) {
         plan.grid = (int)std::min<int64_t>(blocks, (int64_t)num_sms * resident);
         return plan;
     }
-    const int ppt = p.backward ? backward_packs_per_thread(P, p.R, p.nsrc, p.M, num_sms) : packs_per_thread(P, p.M <= num_sms);
+    const int ppt = p.backward ? backward_packs_per_thread(P, p.R, p.nsrc, p.M, num_sms) : packs_per_thread(P, p.M, num_sms);
     const int one_nt = ((P + ppt - 1) / ppt + 31) / 32 * 32;
     if (p.backward && ppt <= 2 && P <= 512 && p.M > (int64_t)num_sms * (kRowsThreads / (one_nt + 32))) {
         // several rows at a time, where there is more than a round of single ones and the ring holds that many for every
@@ -932,14 +938,14 @@ RowsPlan layernorm_plan(RowsParams& p, int num_sms) {
         if (p.stages >= p.rows) return plan;
         p.rows = 1;
     }
-    p.extra_words = p.backward ? (ppt <= 2 ? p.N : 2 * p.N) : ppt == 4 ? p.N : 0;
+    p.extra_words = p.backward ? (ppt <= 2 ? p.N : 2 * p.N) : ppt == 3 || ppt == 4 ? p.N : 0;
     p.red_words = kRedAll;
     return rows_shape(p, ppt, num_sms);
 }
 
 cudaError_t layernorm_prepare() {
     cudaError_t e = cudaSuccess;
-    for (int ppt : {1, 2, 4, 8})
+    for (int ppt : {1, 2, 3, 4, 8})
         for (int threads : {288, 544})
             if (e == cudaSuccess) e = opt_in(forward_kernel(ppt, threads));
     for (int ppt : {1, 2, 3, 4, 5})

@@ -351,3 +351,10 @@ def test_overlaps_are_refused(ws):
 def test_backward_of_wide_rows_against_64_bits(ws, R, M, N, dres):
     """Three packs a thread and two blocks an SM, where there are many rows; two packs and 16 warps with one rank."""
     test_backward_against_64_bits(ws, R, M, N, dres)
+
+
+@pytest.mark.parametrize("R,M,N", [(2, 400, 8200), (1, 310, 12288), (8, 155, 10000), (1, 2500, 5000), (3, 600, 5000), (1, 600, 1032),
+                                   (3, 310, 2048), (2, 160, 12296), (1, 309, 8192), (4, 311, 6144)])
+def test_forward_of_every_split_of_a_row(ws, R, M, N):
+    """Two to four packs a thread, one to four blocks an SM."""
+    test_forward_against_64_bits(ws, R, M, N)
