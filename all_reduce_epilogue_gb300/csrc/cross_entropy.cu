@@ -32,11 +32,11 @@
 // Tiles are taken in groups of rows whose operand stays in L2 while the other one
 // streams past (16 rows of tiles: forward 1055 us, 8: 1076).
 //
-// Measured, 4096 tokens, K = 4096, vocabulary 65536 over 8 ranks: forward 1.07 ms, 2.05
-// PFLOP/s; forward and backward 5.2 ms, 1.69 PFLOP/s, the rate that the power limit leaves a
-// library's product (5.5 ms in a long run).  One token, K = 2048, vocabulary 32000: 28 us,
-// 4.7 TB/s, of which 7 are the two kernels' starts and ends.  77 tokens, K = 1000,
-// vocabulary 11001, both directions: 46 us, the latencies of six kernels (37 at K = 1024,
+// Measured, 4096 tokens, K = 4096, vocabulary 65536 over 8 ranks: forward 1.04 to 1.09 ms, 2.0
+// to 2.1 PFLOP/s; forward and backward 5.1 to 5.3 ms, 1.7 PFLOP/s, the rate that the power limit
+// leaves a library's product (5.4 ms in a long run).  One token, K = 2048, vocabulary 32000: 27 us,
+// 4.8 TB/s, of which 7 are the two kernels' starts and ends.  77 tokens, K = 1000,
+// vocabulary 11001, both directions: 41 us, the latencies of five kernels (33 at K = 1024,
 // whose rows are whole lines).
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -414,7 +414,8 @@ __global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(co
                     for (int i = 0; i < 8; ++i)
                         z[j / 2 + i] = ptx::add2(z[j / 2 + i], ptx::pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])));
                 }
-                // the accumulator goes back to the leader's MMA warp
+                // the accumulator goes back to the leader's MMA warp (with a release it went 2000 cycles later, when the
+                // stores in flight had ended: forward 1053 us for 1047, 128 tokens' gradients 185 for 157)
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
