@@ -32,9 +32,9 @@
 // Tiles are taken in groups of rows whose operand stays in L2 while the other one
 // streams past (16 rows of tiles: forward 1055 us, 8: 1076).
 //
-// Measured, 4096 tokens, K = 4096, vocabulary 65536 over 8 ranks: forward 1.04 to 1.09 ms, 2.0
+// Measured, 4096 tokens, K = 4096, vocabulary 65536 over 8 ranks: forward 1.05 to 1.09 ms, 2.0
 // to 2.1 PFLOP/s; forward and backward 5.1 to 5.3 ms, 1.7 PFLOP/s, the rate that the power limit
-// leaves a library's product (5.4 ms in a long run).  One token, K = 2048, vocabulary 32000: 27 us,
+// leaves a library's product (5.5 ms in a long run).  One token, K = 2048, vocabulary 32000: 27 us,
 // 4.8 TB/s, of which 7 are the two kernels' starts and ends.  77 tokens, K = 1000,
 // vocabulary 11001, both directions: 41 us, the latencies of five kernels (33 at K = 1024,
 // whose rows are whole lines).
@@ -56,10 +56,9 @@ constexpr uint32_t kBox = 4096;           // an epilogue warp's staging buffer: 
 // Blocks of 64 of the contraction that the tensor cores add up before the logits' sums go on in registers.  Their fp32 sums
 // are cut, not rounded, at every step of 16: over the whole of K = 4096 the losses of 4096 tokens were 1.5e-6 off, and the
 // loss of one foreseen token at K = 2048, whose logit of 10 came out 4e-5 too small, 1.8e-5.  With rounded sums of parts of
-// 1024 the 4096 losses are 3.6e-7 off, as far as a product in fp32 (3.1e-7); of 512 1.7e-7, of 256 0.9e-7; reading the
-// accumulators holds the products up: 1070, 1115 and 1348 us, in one piece 1060.  One CTA's tiles, of few tokens, wait for
-// memory anyway: 256.
-constexpr int kPartPair = 16, kPartOne = 4;
+// 512 the 4096 losses are 1.7e-7 off (a product in fp32 3.1e-7), of 1024 3.6e-7, of 256 0.9e-7; reading the accumulators holds
+// the products up: 1077, 1070 and 1102 us in a forward pass.  One CTA's tiles, of few tokens, wait for memory anyway: 256.
+constexpr int kPartPair = 8, kPartOne = 4;
 
 template <int PASS, bool PAIR>
 struct Shape {
