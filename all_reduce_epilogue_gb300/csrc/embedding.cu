@@ -11,10 +11,10 @@
 // each element of the tables, most of which are zeros.  The gradient's sums go by the tokens
 // sorted by (id, position): a token's rows meet in fp32 in the order of their positions, whatever
 // the hardware's order is.
-//   1. One block sorts the ids, stable, up to 10 bits a pass (a warp ranks its own run of tokens
-//      by matching digits, counters per warp and digit keep the order), in shared memory for
-//      up to 16384 tokens, in runs of that for more; all other blocks write the tables' zeros
-//      meanwhile, which mostly takes longer.
+//   1. A cluster of eight CTAs sorts the ids, stable, up to 10 bits a pass (a warp ranks its own run of
+//      tokens by matching digits, counters per warp and digit keep the order), in shared memory for up to
+//      131072 tokens, in runs of that for more; up to 2048 tokens one CTA does.  Beside it, on the other
+//      SMs, a second kernel writes the tables' zeros, which mostly takes longer.
 //   2. The sorted tokens are cut into chunks of equal length, whatever the ids: a token that makes
 //      up a tenth of a batch is then work for a tenth of the chunks.  A chunk's sums that do not
 //      reach its ends are results; the others are partial rows.
@@ -24,8 +24,9 @@
 // Up to 512 tokens a kernel of its own does all of it.
 //
 // Measured, 16384 x 4096, vocabulary 65536 over 8 ranks: lookup 31 us, 8.6 TB/s (rows that come
-// again are in L2); gradient 127 us, 5.3 TB/s of the bytes it cannot do without: zeros 82 us, the
-// sort below them, sums 33, join 8.  300 x 1032, vocabulary 11001: 8.7 us.
+// again are in L2); gradient 123 us, 5.5 TB/s of the bytes it cannot do without: zeros 82 us, the
+// sort below them, sums 33, join 8; added to tables that are there 95 us (with one CTA's sort 132).
+// 300 x 1032, vocabulary 11001: 8.7 us; 16384 x 1032: 34 (one CTA's sort 63).
 #include <algorithm>
 
 #include "rows.cuh"
@@ -34,11 +35,13 @@ namespace are {
 namespace {
 
 constexpr int kSortThreads = 1024, kSortWarps = 32;
-constexpr int kRun = 16384;           // tokens sorted at once
-constexpr int kItems = kRun / kSortThreads;
+constexpr int kSortCluster = 8;       // CTAs
+constexpr int kSortOne = 2048;        // tokens that one CTA sorts: 16.2 us with sums and join at 1024 x 1032, a cluster 17.5; at 4096 24.0 and 20.7
 constexpr int kMaxBins = 1024;
-constexpr size_t kSortSmem = (size_t)kRun * 8 + (size_t)kSortWarps * kMaxBins * 2 + 2 * kMaxBins * 4 + 64 * 4;
-static_assert(kSortSmem <= kRowsSmemLimit, "shared memory budget");
+template <int ITEMS>  // of a thread
+constexpr size_t kSortSmem = (size_t)ITEMS * kSortThreads * 8 + (size_t)kSortWarps * kMaxBins * 2 + 4 * kMaxBins * 4 + 64 * 4;
+static_assert(kSortSmem<16> <= kRowsSmemLimit, "shared memory budget");
+constexpr int kZeroThreads = 512, kZeroBlocks = 2;  // of an SM
 constexpr int kThreads = 128;
 constexpr int kShort = 16;            // chunks behind its first one through which one warp adds up an id's sum
 constexpr int kSumBlocks = 6;         // blocks of the sums on an SM
@@ -121,52 +124,85 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warps) {
     return x - v + (w ? warps[w - 1] : 0u);
 }
 
-__device__ __forceinline__ void sort_tokens(const EmbedParams& p, uint8_t* smem) {
+// The CTAs of a cluster sort as one: each ranks a part of the tokens, in their order, and writes its items to the places that
+// all parts' counts give them, in whichever CTA's shared memory that is.
+template <bool CLUSTER, int ITEMS>
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __grid_constant__ EmbedParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
     uint32_t* skey = reinterpret_cast<uint32_t*>(smem);
-    uint32_t* sidx = skey + kRun;
-    uint16_t* count = reinterpret_cast<uint16_t*>(sidx + kRun);          // [warp][bin]
-    uint32_t* local = reinterpret_cast<uint32_t*>(count + kSortWarps * kMaxBins);  // a bin's first place in the run
-    uint32_t* global = local + kMaxBins;                                 // and in the whole order
-    uint32_t* scan = global + kMaxBins;
+    uint32_t* sidx = skey + ITEMS * kSortThreads;
+    uint16_t* count = reinterpret_cast<uint16_t*>(sidx + ITEMS * kSortThreads);   // [warp][bin]
+    uint32_t* local = reinterpret_cast<uint32_t*>(count + kSortWarps * kMaxBins);  // where this CTA's items of a bin begin in the run
+    uint32_t* first = local + kMaxBins;                                            // where the bin does
+    uint32_t* global = first + kMaxBins;                                           // and where its next items go in the whole order
+    uint32_t* totals = global + kMaxBins;                                          // this CTA's items of a bin
+    uint32_t* scan = totals + kMaxBins;
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    const int M = (int)p.M, bins = 1 << p.digit_bits;
-    const bool one = M <= kRun;
+    constexpr int C = CLUSTER ? kSortCluster : 1;
+    const int q = CLUSTER ? (int)ptx::cluster_ctarank() : 0;
+    const int M = (int)p.M, bins = 1 << p.digit_bits, run = C * ITEMS * kSortThreads;
+    const bool one = M <= run;
+    const uint32_t mask = bins - 1;
     uint16_t* mine = count + w * bins;
+    auto sync = [] {
+        __syncwarp();
+        if (CLUSTER) ptx::cluster_sync();
+        else __syncthreads();
+    };
+    // the sum over the CTAs of a bin's total, and over those before this one
+    auto joined = [&](int bin, uint32_t& before) {
+        uint32_t all = 0;
+        before = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const uint32_t x = CLUSTER ? ptx::ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(totals + bin), c)) : totals[bin];
+            before += c < q ? x : 0u;
+            all += x;
+        }
+        return all;
+    };
+    if (p.accumulate) ptx::grid_launch_dependents();
+    ptx::grid_wait();
+    if (q == 0 && t < 2) p.crossing[t] = 0;
     for (int pass = 0; pass < p.passes; ++pass) {
         const int shift = pass * p.digit_bits;
-        const uint32_t mask = bins - 1;
         const uint32_t *from_key = p.keys[(pass & 1) ^ 1], *from_idx = p.idx[(pass & 1) ^ 1];
         uint32_t *to_key = p.keys[pass & 1], *to_idx = p.idx[pass & 1];
         if (!one) {
-            for (int b = t; b < bins; b += kSortThreads) global[b] = 0;
+            for (int b = t; b < bins; b += kSortThreads) totals[b] = 0;
             __syncthreads();
-            for (int i = t; i < M; i += kSortThreads)
-                atomicAdd(&global[((pass == 0 ? id_of(p, i) : from_key[i]) >> shift) & mask], 1u);
-            __syncthreads();
-            const uint32_t n = t < bins ? global[t] : 0u, first = block_scan(n, scan);
-            if (t < bins) global[t] = first;
+            for (int i = q * kSortThreads + t; i < M; i += C * kSortThreads)
+                atomicAdd(&totals[((pass == 0 ? id_of(p, i) : from_key[i]) >> shift) & mask], 1u);
+            sync();
+            uint32_t before, n = t < bins ? joined(t, before) : 0u;
+            const uint32_t at = block_scan(n, scan);
+            if (t < bins) global[t] = at;
+            sync();  // the totals have been read
         }
-        for (int c0 = 0; c0 < M; c0 += kRun) {
-            const int n = min(kRun, M - c0), per = (n + kSortThreads - 1) / kSortThreads;  // items of a thread
+        for (int c0 = 0; c0 < M; c0 += run) {
+            const int n = min(run, M - c0), per = (n + C * kSortThreads - 1) / (C * kSortThreads);  // items of a thread
+            const int part = per * kSortThreads;                                                    // of a CTA
             for (int i = t; i < kSortWarps * bins / 2; i += kSortThreads) reinterpret_cast<uint32_t*>(count)[i] = 0;
             __syncthreads();
             // a warp has a run of per * 32 items, in their order; an item's place among the warp's of its digit
-            uint32_t key[kItems], idx[kItems], place[kItems / 2];
-            const int i0 = w * per * 32 + lane;
+            uint32_t key[ITEMS], idx[ITEMS], place[ITEMS / 2];
+            const int s0 = w * per * 32 + lane, i0 = q * part + s0;  // its first item in the CTA's part, in the run
             // one kind of source a loop, so that its loads run side by side
             auto items = [&](auto load) {
 #pragma unroll
-                for (int j = 0; j < kItems; ++j)
-                    if (j < per && i0 + j * 32 < n) load(j, i0 + j * 32);
+                for (int j = 0; j < ITEMS; ++j)
+                    if (j < per && i0 + j * 32 < n) load(j, j * 32);
             };
-            if (pass > 0 && one) items([&](int j, int i) { key[j] = skey[i]; idx[j] = sidx[i]; });
-            else if (pass > 0) items([&](int j, int i) { key[j] = from_key[c0 + i]; idx[j] = from_idx[c0 + i]; });
-            else if (p.wide) items([&](int j, int i) { key[j] = id_as<int64_t>(p, c0 + i); idx[j] = c0 + i; });
-            else items([&](int j, int i) { key[j] = id_as<int32_t>(p, c0 + i); idx[j] = c0 + i; });
+            if (pass > 0 && one) items([&](int j, int k) { key[j] = skey[s0 + k]; idx[j] = sidx[s0 + k]; });
+            else if (pass > 0) items([&](int j, int k) { key[j] = from_key[c0 + i0 + k]; idx[j] = from_idx[c0 + i0 + k]; });
+            else if (p.wide) items([&](int j, int k) { key[j] = id_as<int64_t>(p, c0 + i0 + k); idx[j] = c0 + i0 + k; });
+            else items([&](int j, int k) { key[j] = id_as<int32_t>(p, c0 + i0 + k); idx[j] = c0 + i0 + k; });
+            // the zeros' kernel may begin: the loads of the ids, which would wait behind its stores, are on their way
+            if (pass == 0 && c0 == 0) ptx::grid_launch_dependents();
 #pragma unroll
-            for (int j = 0; j < kItems; ++j) {
+            for (int j = 0; j < ITEMS; ++j) {
                 if (j < per) {
-                    const bool in = w * per * 32 + j * 32 + lane < n;
+                    const bool in = i0 + j * 32 < n;
                     const uint32_t d = in ? (key[j] >> shift) & mask : 0xFFFFFFFFu;
                     const uint32_t same = __match_any_sync(0xFFFFFFFFu, d);
                     const int leader = __ffs(same) - 1;
@@ -182,59 +218,68 @@ __device__ __forceinline__ void sort_tokens(const EmbedParams& p, uint8_t* smem)
                 }
             }
             __syncthreads();
-            uint32_t total = 0;
             if (t < bins) {
+                uint32_t total = 0;
 #pragma unroll 8
                 for (int v = 0; v < kSortWarps; ++v) {
                     const uint32_t x = count[v * bins + t];
                     count[v * bins + t] = (uint16_t)total;
                     total += x;
                 }
+                totals[t] = total;
             }
-            const uint32_t first = block_scan(total, scan);
-            if (t < bins) local[t] = first;
+            sync();  // the CTAs' totals are there, and their items in registers
+            uint32_t before = 0;
+            const uint32_t all = t < bins ? joined(t, before) : 0u, at = block_scan(all, scan);
+            if (t < bins) {
+                first[t] = at;
+                local[t] = at + before;
+            }
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < kItems; ++j) {
-                if (j < per && w * per * 32 + j * 32 + lane < n) {
+            for (int j = 0; j < ITEMS; ++j) {
+                if (j < per && i0 + j * 32 < n) {
                     const uint32_t d = (key[j] >> shift) & mask;
                     const uint32_t to = local[d] + mine[d] + ((place[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
-                    skey[to] = key[j];
-                    sidx[to] = idx[j];
+                    if (CLUSTER) {
+                        const uint32_t c = to / part, in = to - c * part;
+                        ptx::st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(skey + in), c), key[j]);
+                        ptx::st_cluster_u32(ptx::mapa_shared(ptx::smem_u32(sidx + in), c), idx[j]);
+                    } else {
+                        skey[to] = key[j];
+                        sidx[to] = idx[j];
+                    }
                 }
             }
-            __syncthreads();
+            sync();
             if (!one || pass == p.passes - 1) {
-                for (int i = t; i < n; i += kSortThreads) {
-                    const uint32_t k = skey[i], d = (k >> shift) & mask;
-                    const uint32_t to = one ? (uint32_t)i : global[d] + (i - local[d]);
+                for (int i = t; i < part && q * part + i < n; i += kSortThreads) {
+                    const uint32_t k = skey[i], d = (k >> shift) & mask, i_run = q * part + i;
+                    const uint32_t to = one ? i_run : global[d] + (i_run - first[d]);
                     to_key[to] = k;
                     to_idx[to] = sidx[i];
                 }
-                __syncthreads();
-                if (!one && t < bins) global[t] += total;
+                if (!one) {
+                    __syncthreads();
+                    if (t < bins) global[t] += all;
+                    sync();  // the items have left; global memory of this pass, too, is the next pass's input
+                }
             }
         }
-        __syncthreads();  // global memory of this pass, too, is the next pass's input
     }
 }
 
-__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __grid_constant__ EmbedParams p) {
-    extern __shared__ __align__(128) uint8_t sort_smem[];
+// Zeros in the tables.  Behind the sort it begins when all of the sort's CTAs have passed their wait, so what came before them
+// has ended; it ends after the sort, so that who waits for it waits for both.
+__global__ void __launch_bounds__(kZeroThreads) embed_zero_kernel(const __grid_constant__ EmbedParams p) {
+    if (p.M == 0) ptx::grid_wait();
     ptx::grid_launch_dependents();
-    ptx::grid_wait();
-    if (blockIdx.x == 0 && p.M > 0) {
-        if (threadIdx.x < 2) p.crossing[threadIdx.x] = 0;
-        sort_tokens(p, sort_smem);
-        return;
-    }
-    const int skip = p.M > 0 ? 1 : 0;
-    const int64_t packs = (int64_t)p.Vs * (p.N >> 3), step = (int64_t)(gridDim.x - skip) * kSortThreads;
-    const int64_t i0 = (int64_t)(blockIdx.x - skip) * kSortThreads + threadIdx.x;
+    const int64_t packs = (int64_t)p.Vs * (p.N >> 3), step = (int64_t)gridDim.x * kZeroThreads;
     for (int r = 0; r < p.R; ++r) {
         uint4* to = reinterpret_cast<uint4*>(p.tables[r]);
-        for (int64_t i = i0; i < packs; i += step) to[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int64_t i = (int64_t)blockIdx.x * kZeroThreads + threadIdx.x; i < packs; i += step) to[i] = make_uint4(0u, 0u, 0u, 0u);
     }
+    ptx::grid_wait();
 }
 
 // ------------------------------------------------------------------------- sums
@@ -415,7 +460,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const __gri
 // id's first token sums all of its rows, or, if there are many, the block's warps sum equal runs of them, in order.  (A
 // warp's neighbours have the next tokens, so an id's columns lie in different blocks.)  Other blocks write zeros to the rows
 // that no token has, which a table of the ids tells.  (300 x 1032, vocabulary 11001: 8.7 us, sort, sums and join 12.8, a
-// block instead of a warp for each token 11.3; 513 tokens, which the sort takes, 15.4 us, 512 10.9.)
+// block instead of a warp for each token 11.3; 513 tokens, which the sort takes, 13.5 us, 512 10.9.)
 constexpr int kFew = kEmbedFew, kFewWarps = 8, kFewThreads = 32 * kFewWarps, kSlots = 1024;
 constexpr int kHot = 32;  // rows that one warp sums
 static_assert(kHot * kFewWarps <= kFew, "a list for each warp");
@@ -532,7 +577,32 @@ __global__ void __launch_bounds__(kFewThreads) embed_few_kernel(const __grid_con
 
 }  // namespace
 
-cudaError_t embed_prepare() { return cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem); }
+template <bool CLUSTER, int ITEMS>
+static cudaError_t opt_in_sort() {
+    return cudaFuncSetAttribute(embed_sort_kernel<CLUSTER, ITEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem<ITEMS>);
+}
+cudaError_t embed_prepare() {
+    for (cudaError_t e : {opt_in_sort<false, 4>(), opt_in_sort<true, 4>(), opt_in_sort<true, 16>()})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
+}
+
+template <bool CLUSTER, int ITEMS>
+static cudaError_t launch_sort(const EmbedParams& p, cudaStream_t s) {
+    cudaLaunchAttribute attr[2];
+    attr[0] = dependent_launch();
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kSortCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CLUSTER ? kSortCluster : 1);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = kSortSmem<ITEMS>;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = CLUSTER ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, embed_sort_kernel<CLUSTER, ITEMS>, p);
+}
 
 // Keys and positions twice, and the list of chunks (of 8 tokens or more) in which an id starts that goes on behind.
 size_t embed_sort_bytes(int64_t M_max) { return (size_t)M_max * 16 + (size_t)(M_max / 8 + 4) * 4; }
@@ -576,8 +646,16 @@ cudaError_t launch_embedding_backward(EmbedParams& p, void* sort, float* scratch
     const int64_t most = std::min<int64_t>(rows / 2, (int64_t)num_sms * kSumBlocks / slabs * p.block_chunks);
     p.chunk = std::max<int64_t>(8, (p.M + most - 1) / most);
     p.chunks = (p.M + p.chunk - 1) / p.chunk;
-    *grid = p.accumulate ? 1 : num_sms;
-    cudaError_t e = launch_dependent(embed_sort_kernel, dim3((unsigned)*grid), kSortThreads, kSortSmem, s, p);
+    const bool cluster = p.M > kSortOne;
+    *grid = p.M == 0 ? 0 : cluster ? kSortCluster : 1;
+    cudaError_t e = cudaSuccess;
+    // (four items a thread need no spilled registers: 16384 x 1032 34 us, with room for 16 38)
+    if (p.M > 0)
+        e = !cluster                                 ? launch_sort<false, 4>(p, s)
+            : p.M <= 4 * kSortCluster * kSortThreads ? launch_sort<true, 4>(p, s)
+                                                     : launch_sort<true, 16>(p, s);
+    // zeros on the SMs that the sort leaves: with a share for its own they would end late
+    if (e == cudaSuccess && !p.accumulate) e = launch_dependent(embed_zero_kernel, dim3((unsigned)(kZeroBlocks * (num_sms - *grid))), kZeroThreads, 0, s, p);
     if (e != cudaSuccess || p.M == 0) return e;
     const int threads = (p.width * p.block_chunks + 31) / 32 * 32;
     const dim3 blocks((unsigned)((p.chunks + p.block_chunks - 1) / p.block_chunks), (unsigned)slabs);

@@ -251,3 +251,36 @@ def test_refusals(ws):
             with pytest.raises(are.AreError) as e:
                 are.embedding_ar_backward(ids, dy, d, other)
             assert e.value.status == are.ECAPACITY
+
+
+# one CTA's most tokens and a cluster's first; a part with no token; four items a thread and more; all that a cluster sorts at once, one
+# more, several runs; one to three passes
+@pytest.mark.parametrize("kind", ["text", "uniform", "one", "runs"])
+@pytest.mark.parametrize("R,M,N,V", [(2, 2048, 64, 900), (2, 2049, 64, 900), (1, 7169, 40, 1), (3, 32768, 64, 5000), (1, 32769, 64, 70000),
+                                     (4, 131072, 16, 300), (1, 131073, 8, 1100000), (2, 300000, 8, 9000)])
+def test_gradient_by_a_cluster_s_sort(R, M, N, V, kind):
+    need_gpu()
+    with are.Workspace(R_max=R, M_max=M, N_max=N) as ws:
+        test_gradient(ws, R, M, N, V, kind)
+
+
+def test_gradients_back_to_back(ws):
+    """Calls in a row, whose kernels overlap at their ends, on tables that the call before wrote and read: zeros of the next
+    call come after the sums of this one."""
+    r, g = rand(11)
+    M, N, V = 6000, 1032, 3000
+    d = [torch.empty(V, N, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    calls = []
+    for k in range(6):
+        ids, dy = tokens("text" if k % 2 else "uniform", M, 2 * V, g), r(M, N)
+        calls.append((ids, dy, torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")))
+    torch.cuda.synchronize()
+    for ids, dy, out in calls:
+        are.embedding_ar_backward(ids, dy, d, ws)
+        are.embedding_ar(ids, d, out, ws)
+    torch.cuda.synchronize()
+    for ids, dy, out in calls:
+        want, tol, _ = gradient64(ids, dy, 2 * V, 1.0)
+        here = (ids >= 0) & (ids < 2 * V)
+        at = ids.clamp(0, 2 * V - 1)
+        check(out, want[at] * here[:, None], torch.where(here[:, None], tol[at], 1e-38), "rows read back")
