@@ -284,3 +284,25 @@ def test_gradients_back_to_back(ws):
         here = (ids >= 0) & (ids < 2 * V)
         at = ids.clamp(0, 2 * V - 1)
         check(out, want[at] * here[:, None], torch.where(here[:, None], tol[at], 1e-38), "rows read back")
+
+
+def test_gradient_of_a_vocabulary_past_30_bits():
+    """Four passes of digits in several runs: a pass reads what other CTAs wrote where the pass before the last had read."""
+    need_gpu()
+    R, V, M, N = 8, 140_000_000, 140_000, 8
+    r, g = rand(17)
+    ids = torch.randint(0, R * V, (M,), generator=g, device="cuda")
+    ids[::7] = ids[3]
+    dy = r(M, N)
+    d = [torch.full((V, N), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(R)]
+    with are.Workspace(R_max=R, M_max=M, N_max=N) as ws:
+        are.embedding_ar_backward(ids, dy, d, ws)
+        assert ws.device_status()["code"] == 0
+    there, at = torch.unique(ids, return_inverse=True)
+    want, tol, _ = gradient64(at, dy, len(there), 1.0)
+    got = torch.stack([t[(there - k * V).clamp(0, V - 1)] for k, t in enumerate(d)])
+    rank = torch.div(there, V, rounding_mode="floor")
+    check(got[rank, torch.arange(len(there), device="cuda")], want, tol, "dtable")
+    for k, t in enumerate(d):   # and nothing else
+        rows = t.view(torch.int64).view(V, 2)
+        assert int((rows != 0).any(1).sum()) <= int((rank == k).sum())
