@@ -18,7 +18,7 @@ LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libare.so")
 SOURCES = ["api.cu", "gemm_reduce.cu", "ar_rmsnorm.cu", "noalloc.cu", "norm_rows.cu", "qweight.cu",
            "layernorm.cu", "cross_entropy.cu", "embedding.cu"]
-HEADERS = ["are_internal.h", "ptx.cuh", "rows.cuh"]
+HEADERS = ["are_internal.h", "ptx.cuh", "rows.cuh", "xent_sizes.h"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 NVCC = os.environ.get("NVCC", "nvcc")

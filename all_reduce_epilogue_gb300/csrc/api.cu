@@ -514,8 +514,8 @@ are_status are_workspace_create(are_ws** out, const are_caps* caps) {
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_dgamma, norm_backward_scratch_words(caps->N_max, ws->num_sms) * 4);
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_sort, embed_sort_bytes(caps->M_max));
     if (e == cudaSuccess && caps->vocab_piece > 0) {
-        ws->xent = xent_sizes(caps->M_max, caps->K_max, caps->vocab_piece);
-        e = cudaMalloc(&ws->d_xent, ws->xent.d_bytes + ws->xent.sum_bytes + ws->xent.h_bytes + ws->xent.row_bytes);
+        e = xent_sizes(caps->M_max, caps->K_max, caps->vocab_piece, ws->xent) ? cudaMalloc(&ws->d_xent, ws->xent.total())
+                                                                              : cudaErrorMemoryAllocation;
     }
     if (e != cudaSuccess) {
         are_status st = from_cuda(e);
@@ -877,9 +877,9 @@ are_status xent_call(XentCall& c, XentBuffers& b, const are_bf16* h, const are_b
     c.vocab = vocab;
     uint8_t* at = static_cast<uint8_t*>(ws->d_xent);
     b.d = at;
-    b.sums = at + ws->xent.d_bytes;
-    b.h = at + ws->xent.d_bytes + ws->xent.sum_bytes;
-    b.rows = static_cast<uint8_t*>(b.h) + ws->xent.h_bytes;
+    b.sums = at + ws->xent.sums_at();
+    b.h = at + ws->xent.h_at();
+    b.rows = at + ws->xent.rows_at();
     b.sizes = ws->xent;
     b.clusters = ws->xent_clusters;
     b.status = ws->d_status;

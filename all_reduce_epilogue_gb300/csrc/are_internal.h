@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/are.h"
+#include "xent_sizes.h"
 
 namespace are {
 
@@ -342,13 +343,6 @@ struct XentCall {
     bool has_dw;
 };
 
-struct XentSizes {
-    size_t d_bytes;    // d of a piece [M, piece], or the forward pass's pairs
-    size_t sum_bytes;  // fp32 sums of dh
-    size_t h_bytes;    // the hidden states of rows with a target
-    size_t row_bytes;  // a running pair and a logit a row
-};
-
 struct XentBuffers {
     void *d, *sums, *h, *rows;
     XentSizes sizes;
@@ -357,7 +351,6 @@ struct XentBuffers {
     uint64_t timeout_ns;
 };
 
-XentSizes xent_sizes(int64_t M_max, int64_t K_max, int64_t piece);
 cudaError_t xent_prepare(int* clusters);
 cudaError_t launch_xent_forward(const XentCall& c, const XentBuffers& b, cudaStream_t stream, are_launch_info* info);
 cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaStream_t stream, are_launch_info* info);

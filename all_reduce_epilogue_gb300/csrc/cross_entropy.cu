@@ -49,7 +49,7 @@
 namespace are {
 namespace {
 
-constexpr int kTile = 256;     // rows and columns of a pair's tile
+constexpr int kTile = kXentTile;  // rows and columns of a pair's tile
 constexpr uint32_t kHalf = 128 * 64 * 2;  // a CTA's part of an operand: 128 rows or columns, 64 of the contraction
 constexpr uint32_t kStageBytes = 2 * kHalf;
 constexpr uint32_t kBox = 4096;           // an epilogue warp's staging buffer: 32 rows of 128 bytes; two a warp
@@ -694,7 +694,6 @@ cudaError_t launch(XentParams& p, int clusters, cudaStream_t s) {
 // Up to 128 tokens the logits' tiles are 128 x 128, each of one CTA: of a pair's 256 rows half would be empty, and its
 // product of 256 x 256 x 64 takes 0.27 us whatever it holds, as long as the copies do.
 constexpr int kFewTokens = 128;
-constexpr size_t kMinPairs = 4u << 20;  // bytes for d or the forward pass's pairs, whatever M_max is: few pieces for few tokens
 constexpr int kGroup = 16;  // rows of tiles whose operand stays in L2: 4096 rows
 
 // dh's sums as a map [splits, M, K] of fp32, 128B-swizzled boxes of 32 columns x 32 rows.
@@ -741,16 +740,6 @@ cudaError_t xent_prepare(int* clusters) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaOccupancyMaxActiveClusters(clusters, xent_kernel<kXentDLogits, true>, &cfg);
-}
-
-XentSizes xent_sizes(int64_t M_max, int64_t K_max, int64_t piece) {
-    XentSizes z;
-    z.d_bytes = std::max<size_t>((size_t)M_max * ceil256(piece) * kTile * 2, kMinPairs);
-    // one set of sums for the longest call, or several for calls of few tiles that split the vocabulary over the pairs
-    z.sum_bytes = (size_t)M_max * K_max * 4 + (size_t)std::min<int64_t>(M_max, kTile) * kTile * 4 * 80;
-    z.h_bytes = (size_t)M_max * K_max * 2;
-    z.row_bytes = (size_t)M_max * 12;
-    return z;
 }
 
 // Sets of sums that dh's contraction over the vocabulary is split into, at most `most`.  Few tokens have few tiles, and

@@ -3,6 +3,7 @@ entry points' argument checks before any device access."""
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -83,3 +84,41 @@ def test_no_non_coherent_loads_under_programmatic_launch(source):
     code = re.sub(r"//[^\n]*", "", open(os.path.join(os.path.dirname(are.__file__), "csrc", source)).read())
     assert "launch_dependent(" in code
     assert not re.findall(r"__ldg\b|ld\.global(?:\.\w+)*\.nc\b|__restrict__", code)
+
+
+SIZES_PROGRAM = r"""
+#include <cstdio>
+#include <cstdlib>
+
+#include "xent_sizes.h"
+
+int main(int argc, char** argv) {
+    for (int i = 1; i + 2 < argc; i += 3) {
+        are::XentSizes z{};
+        const bool ok = are::xent_sizes(atoll(argv[i]), atoll(argv[i + 1]), atoll(argv[i + 2]), z);
+        printf("%d %zu %zu %zu %zu\n", ok, z.sums_at(), z.h_at(), z.rows_at(), z.total());
+    }
+}
+"""
+
+
+def _sizes(tmp_path, caps):
+    src, exe = tmp_path / "sizes.cpp", tmp_path / "sizes"
+    src.write_text(SIZES_PROGRAM)
+    csrc = os.path.join(os.path.dirname(are.__file__), "csrc")
+    subprocess.run([os.environ.get("CXX", "g++"), "-std=c++17", "-I", csrc, str(src), "-o", str(exe)], check=True)
+    lines = subprocess.run([str(exe), *[str(v) for c in caps for v in c]], check=True, capture_output=True, text=True).stdout
+    return [[int(v) for v in line.split()] for line in lines.splitlines()]
+
+
+def test_cross_entropy_buffers(tmp_path):
+    """The cross entropy's buffers begin on 256 bytes and hold what a call of the capacities needs, whatever M_max and K_max
+    are (workspaces take any K_max; calls have K % 8 == 0)."""
+    caps = [(m, k, v) for m in (1, 2, 3, 5, 77, 129, 4096) for k in (1, 2, 7, 8, 1000, 1001, 1002, 1004, 4096)
+            for v in (1, 256, 257, 8192)]
+    for (m, k, v), (ok, sums, h, rows, total) in zip(caps, _sizes(tmp_path, caps), strict=True):
+        assert ok and not sums % 256 and not h % 256 and not rows % 256, (m, k, v)
+        assert sums >= m * -(-v // 256) * 256 * 2 and h - sums >= m * k * 4 and rows - h >= m * k * 2 and total - rows >= m * 12
+    # capacities whose products pass 64 bits are refused, not wrapped
+    for ok, *_ in _sizes(tmp_path, [(1, (1 << 63) - 8, 256), (1 << 62, 8, 256), (1 << 31, 1 << 31, 1), (1 << 40, 8, 1 << 28)]):
+        assert not ok

@@ -264,3 +264,23 @@ def test_refusals(ws):
             assert e.value.status == are.ECAPACITY
     with pytest.raises(are.AreError):
         are.Workspace(R_max=1, M_max=1, N_max=8, vocab_piece=256)   # K_max missing
+
+
+@pytest.mark.parametrize("M,K_max", [(77, 1001), (1, 1001), (5, 1002), (131, 1004)])
+def test_capacities_that_are_no_multiple_of_8(M, K_max):
+    """Workspaces take any K_max: both directions, in several pieces of the smallest buffer."""
+    need_gpu()
+    R, N, K = 3, 14000 if M > 5 else 12, 1000
+    h, w, t, dloss = inputs(R, M, N, K, K_max)
+    want = ref.cross_entropy64(h, w, t, R * N, dloss)
+    with are.Workspace(R_max=R, M_max=M, N_max=8, K_max=K_max, vocab_piece=1) as ws:
+        got = run(ws, h, w, t, dloss)
+        compare(got, want)
+        assert torch.equal(run(ws, h, w, t, dloss, dw=False)[2], got[2])
+
+
+def test_capacities_that_no_device_holds():
+    need_gpu()
+    with pytest.raises(are.AreError) as e:
+        are.Workspace(R_max=1, M_max=1, N_max=8, K_max=(1 << 63) - 8, vocab_piece=256)
+    assert e.value.status == are.ENOMEM
