@@ -78,6 +78,7 @@ EXPORTS = [
     "are_version", "are_status_string", "are_supports", "are_workspace_create", "are_workspace_destroy",
     "are_workspace_reset", "are_workspace_set_debug", "are_workspace_set_oneshot_max_bytes",
     "are_workspace_set_gemm_order", "are_workspace_set_chunks", "are_chunk_generation", "are_chunk_wait",
+    "are_workspace_set_logit_gradient",
     "are_get_device_status", "are_debug_snapshot", "are_debug_last_launch",
     "are_gemm_rs", "are_gemm_ar", "are_allreduce_rmsnorm", "are_allreduce_add_rmsnorm", "are_allreduce_rmsnorm_quant",
     "are_allreduce_rmsnorm_noalloc", "are_noalloc_device_status",
@@ -145,6 +146,8 @@ def load_library(path: str = LIB_PATH):
     lib.are_workspace_set_oneshot_max_bytes.argtypes = [vp, u64]
     lib.are_workspace_set_gemm_order.restype = i32
     lib.are_workspace_set_gemm_order.argtypes = [vp, i32, i32, i32]
+    lib.are_workspace_set_logit_gradient.restype = i32
+    lib.are_workspace_set_logit_gradient.argtypes = [vp, i32]
     lib.are_workspace_set_chunks.restype = i32
     lib.are_workspace_set_chunks.argtypes = [vp, i32, i32]
     lib.are_chunk_generation.restype = i32
@@ -312,6 +315,12 @@ class Workspace:
         not depend on it."""
         _check(load_library().are_workspace_set_gemm_order(self.handle, group_m, block_pairs, rank_group),
                "are_workspace_set_gemm_order")
+
+    def set_logit_gradient(self, parts: int):
+        """bf16 parts of the logits' gradient in the cross entropy's backward
+        products: 2 (the default), as near as fp32, or 1, rounded once to bf16, in
+        half the products' time."""
+        _check(load_library().are_workspace_set_logit_gradient(self.handle, parts), "are_workspace_set_logit_gradient")
 
     def set_chunks(self, chunks: int, stripe: int = 0):
         """GEMM+RS chunked owner-segment completion: `chunks` per segment (0 =

@@ -44,6 +44,7 @@ struct are_ws {
     void* d_xent = nullptr;           // cross entropy: one allocation, see xent_buffers
     XentSizes xent{};
     int xent_clusters = 0;            // resident CTA pairs of its kernels, 0 before the first call
+    int xent_parts = 2;               // bf16 parts of the logits' gradient
     bool qweight_ready = false;       // the same of the 4-bit kernels
     QweightDevice qweight{};          // resident clusters of the 4-bit kernel
     uint8_t* d_tokens = nullptr;      // staged tokens of the 4-bit kernel
@@ -556,6 +557,14 @@ are_status are_workspace_set_debug(are_ws* ws, uint32_t flags, int64_t arg) {
     return ARE_OK;
 }
 
+are_status are_workspace_set_logit_gradient(are_ws* ws, int parts) {
+    if (!ws || parts < 1 || parts > 2) return ARE_EINVAL;
+    TryLock lk(ws->mu);
+    if (!lk.ok) return ARE_EBUSY;
+    ws->xent_parts = parts;
+    return ARE_OK;
+}
+
 are_status are_workspace_set_gemm_order(are_ws* ws, int group_m, int block_pairs, int rank_group) {
     if (!ws || group_m < 0 || rank_group < 0 || rank_group > kMaxRanks) return ARE_EINVAL;
     TryLock lk(ws->mu);
@@ -881,6 +890,7 @@ are_status xent_call(XentCall& c, XentBuffers& b, const are_bf16* h, const are_b
     b.h = at + ws->xent.h_at();
     b.rows = at + ws->xent.rows_at();
     b.sizes = ws->xent;
+    b.parts = ws->xent_parts;
     b.clusters = ws->xent_clusters;
     b.status = ws->d_status;
     b.timeout_ns = ws->timeout_ns;

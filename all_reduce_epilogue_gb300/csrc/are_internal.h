@@ -323,6 +323,7 @@ struct XentParams {
     int group;                    // rows of tiles taken together
     int units;                    // (set at the launch)
     int sums, add;                // kXentDH: fp32 sums, added to what is there
+    int second, columns;          // d has a second bf16 part (1) or not (0), which lies `columns` behind the first
     const uint4* rows_from;       // kXentDLogits: h, or nullptr
     uint4* rows_to;               // and its copy with zeros in the rows that have no target
     uint64_t timeout_ns;
@@ -346,6 +347,7 @@ struct XentCall {
 struct XentBuffers {
     void *d, *sums, *h, *rows;
     XentSizes sizes;
+    int parts;                    // bf16 parts of d: 2, or 1
     int clusters;
     DevStatus* status;
     uint64_t timeout_ns;

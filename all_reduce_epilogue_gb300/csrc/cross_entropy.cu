@@ -12,14 +12,14 @@
 //             sum of exp(z - maximum): 8 bytes for what would be 256 and more.  A small
 //             kernel joins the tiles' pairs; pieces of the vocabulary as large as the
 //             buffer holds pairs for.
-//   kDLogits  z again, whose epilogue leaves d for one piece of the vocabulary, in bf16;
+//   kDLogits  z again, whose epilogue leaves d for one piece of the vocabulary, in two bf16 parts;
 //   kDH       d W, in fp32 sums over the pieces;
 //   kDW       d^T h, rounded to bf16 once; the tiles of both in one launch (kGrads), the
 //             long ones of kDH first.
-// d is rounded to bf16 because that is what the tensor cores multiply at their rate: half
-// a step, 2^-8 of a term, at random in sums of many terms, which is below the rounding of
-// the bf16 results; fp32's substitute tf32 runs at half the rate.  Maxima, sums, lse and all sums
-// of products are fp32.
+// The tensor cores multiply bf16, and d has more bits: bf16(d) and bf16(d - bf16(d)), one behind
+// the other along the contraction, are d to 2^-16 of a term.  With the first alone, which a caller
+// may choose, dh and dw are as far from 64 bits as two roundings, 2.4e-3, instead of one, 1.7e-3.
+// (tf32 has the rate of the two parts and 2^-11.)  Maxima, sums, lse and all sums of products are fp32.
 //
 // One kernel body for the four, the CTA-pair scheme of the GEMM kernels: 256x256 tiles,
 // each CTA staging its 128 rows of A and 128 columns of B by TMA (six stages of 32 KB),
@@ -298,15 +298,18 @@ __global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(co
                     if (PAIR && q == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kHalf + (both_a ? 2 * a_bytes : a_bytes));
                     if (!PAIR) {
                     } else if (dw) {
+                        // d's first and second part in turn, with the same block of h
+                        const int part = (kb & p.second) * p.columns, row = (kb >> p.second) * 64;
                         for (int i = 0; i < 2; ++i) {
-                            ptx::tma_load_2d_pair(a + i * 8192, &p.tmA2, fb, a0 + i * 64, k, pol);
-                            ptx::tma_load_2d_pair(b + i * 8192, &p.tmB, fb, b0 + i * 64, k, pol);
+                            ptx::tma_load_2d_pair(a + i * 8192, &p.tmA2, fb, part + a0 + i * 64, row, pol);
+                            ptx::tma_load_2d_pair(b + i * 8192, &p.tmB, fb, b0 + i * 64, row, pol);
                         }
                     } else {
-                        if (has_a) ptx::tma_load_2d_pair(a, &p.tmA, fb, k, a0, pol);
+                        if (has_a) ptx::tma_load_2d_pair(a, &p.tmA, fb, dh ? (kb & p.second) * p.columns + (kb >> p.second) * 64 : k, a0, pol);
                         if (dh) {
-                            const Place w = place_of(p, kb >> 2);
-                            const int v = w.col + (kb & 3) * 64;
+                            const int block = kb >> p.second;
+                            const Place w = place_of(p, block >> 2);
+                            const int v = w.col + (block & 3) * 64;
                             for (int i = 0; i < 2; ++i)
                                 ptx::tma_load_2d_pair(b + i * 8192, &p.tmW[w.rank], fb, b0 + i * 64, v, pol);
                         } else {
@@ -469,39 +472,40 @@ __global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(co
                 const bool on = tgt >= 0;  // a row without a target has no gradient, whatever its logits
                 const float lse = on ? p.lse[m] : 0.f, g = on ? p.dloss[m] : 0.f;
                 const uint64_t minus = ptx::pair(-lse, -lse), g2 = ptx::pair(g, g);
-                // g (p - 1): the difference before the rounding, and without cancellation where p is near 1
-                uint32_t d[kCols / 2];
+                // g (p - 1) for the target: the difference before the rounding, and without cancellation where p is near 1
+                const float own = mine >= 0 ? g * expm1f(target - lse) : 0.f;
 #pragma unroll
                 for (int i = 0; i < kCols / 2; ++i) {
                     const float2 e = ptx::unpair(ptx::mul2(ptx::add2(z[i], minus), scale));
-                    const float2 x = ptx::unpair(ptx::mul2(ptx::pair(ex2(e.x), ex2(e.y)), g2));
-                    d[i] = on ? bf16x2(x.x, x.y) : 0u;
+                    float2 x = ptx::unpair(ptx::mul2(ptx::pair(ex2(e.x), ex2(e.y)), g2));
+                    x.x = !on || 2 * i >= cols ? 0.f : 2 * i == mine ? own : x.x;
+                    x.y = !on || 2 * i + 1 >= cols ? 0.f : 2 * i + 1 == mine ? own : x.y;
+                    z[i] = ptx::pair(x.x, x.y);
                 }
-                if (cols < kCols) {
+                // d rounded to bf16, and what that rounding left, which is rounded in its turn
+                for (int part = 0; part <= p.second; ++part) {
+                    __syncwarp();
+                    if (lane == 0) ptx::bulk_wait_read0();
+                    __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < kCols / 2; ++i) d[i] = 2 * i >= cols ? 0u : 2 * i + 1 >= cols ? d[i] & 0xFFFFu : d[i];
-                }
-                if (mine >= 0) {
-                    const uint32_t own = bf16x2(g * expm1f(target - lse), 0.f);
+                    for (int i = 0; i < kCols / 8; ++i) {
+                        uint32_t d[4];
 #pragma unroll
-                    for (int i = 0; i < kCols / 2; ++i) {
-                        if (2 * i == mine) d[i] = (d[i] & 0xFFFF0000u) | own;
-                        if (2 * i + 1 == mine) d[i] = (d[i] & 0xFFFFu) | (own << 16);
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 x = ptx::unpair(z[4 * i + j]);
+                            d[j] = bf16x2(x.x, x.y);
+                            z[4 * i + j] = ptx::pair(x.x - __uint_as_float(d[j] << 16), x.y - __uint_as_float(d[j] & 0xFFFF0000u));
+                        }
+                        *chunk_at(box + (i / 8) * kBox, lane, i % 8) = make_uint4(d[0], d[1], d[2], d[3]);
                     }
-                }
-                __syncwarp();
-                if (lane == 0) ptx::bulk_wait_read0();
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < kCols / 8; ++i)
-                    *chunk_at(box + (i / 8) * kBox, lane, i % 8) = make_uint4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
-                ptx::fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    if (m0 < p.M)
-                        for (int i = 0; i < kCols / 64; ++i)
-                            ptx::tma_store_2d(&p.tmOut[0], box + i * kBox, t.tn * kSide + group * kCols + i * 64, m0);
-                    ptx::bulk_commit();
+                    ptx::fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (m0 < p.M)
+                            for (int i = 0; i < kCols / 64; ++i)
+                                ptx::tma_store_2d(&p.tmOut[0], box + i * kBox, part * p.columns + t.tn * kSide + group * kCols + i * 64, m0);
+                        ptx::bulk_commit();
+                    }
                 }
             }
             __syncwarp();
@@ -824,6 +828,7 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
     }
     const int total = tiles_in(c, kTile, d.rank_tiles), tiles_m = ceil256(c.M), tiles_k = ceil256(c.K);
     const int most = (int)std::min<int64_t>(total, (int64_t)(b.sizes.d_bytes / ((size_t)c.M * kTile * 2)));
+    z.second = d.second = b.parts - 1;
     const int even = (total + most - 1) / most, piece = (total + even - 1) / even;
     const int pieces = (total + piece - 1) / piece, left = total - (pieces - 1) * piece;  // the last piece's tiles, 1..piece
     cudaError_t e = make_tmap_bf16(&z.tmA, c.h, (uint64_t)c.K, (uint64_t)c.M, 64, z.a_rows);
@@ -853,10 +858,11 @@ cudaError_t launch_xent_backward(const XentCall& c, const XentBuffers& b, cudaSt
         z.tile0 = d.tile0 = t0;
         z.grid[0] = XentGrid{tiles_m, few ? 2 * n : n, 1, (int)((c.K + 63) / 64), 0};
         if (few) z.tile0 = 2 * t0;
-        if (c.dh) d.grid[0] = XentGrid{tiles_m, tiles_k, splits, 4 * n, 0};
-        if (c.has_dw) d.grid[1] = XentGrid{n, tiles_k, 1, (int)((c.M + 63) / 64), 0};
-        const uint64_t cols = (uint64_t)n * kTile;
-        if (t0 == 0 || n != piece) {  // the piece's d [M, cols]: as an output, along and across the contraction
+        if (c.dh) d.grid[0] = XentGrid{tiles_m, tiles_k, splits, 4 * n * b.parts, 0};
+        if (c.has_dw) d.grid[1] = XentGrid{n, tiles_k, 1, (int)((c.M + 63) / 64) * b.parts, 0};
+        z.columns = d.columns = n * kTile;
+        const uint64_t cols = (uint64_t)n * kTile * b.parts;
+        if (t0 == 0 || n != piece) {  // the piece's d [M, parts, columns]: as an output, along and across the contraction
             e = make_tmap_bf16(&z.tmOut[0], b.d, cols, (uint64_t)c.M, 64, 32);
             if (e == cudaSuccess) e = make_tmap_bf16(&d.tmA, b.d, cols, (uint64_t)c.M, 64, d.a_rows);
             if (e == cudaSuccess) e = make_tmap_bf16(&d.tmA2, b.d, cols, (uint64_t)c.M, 64, 64);

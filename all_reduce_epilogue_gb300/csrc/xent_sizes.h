@@ -7,18 +7,18 @@
 namespace are {
 
 constexpr int kXentTile = 256;              // rows and columns of a tile
-constexpr size_t kXentMinPairs = 4u << 20;  // bytes for d or the forward pass's pairs, whatever M_max is: few pieces for few tokens
+constexpr size_t kXentMinPairs = 4u << 20;  // bytes for a part of d or the forward pass's pairs, whatever M_max is: few pieces for few tokens
 
 // Each a multiple of 256 bytes, so that every buffer begins where a tensor map, a copy or a vector access may.
 struct XentSizes {
-    size_t d_bytes;    // d of a piece [M, piece], or the forward pass's pairs
+    size_t d_bytes;    // one of the two parts of a piece's d [M, piece], or the forward pass's pairs
     size_t sum_bytes;  // fp32 sums of dh
     size_t h_bytes;    // the hidden states of rows with a target
     size_t row_bytes;  // a running pair and a logit a row
-    size_t sums_at() const { return d_bytes; }
-    size_t h_at() const { return d_bytes + sum_bytes; }
-    size_t rows_at() const { return d_bytes + sum_bytes + h_bytes; }
-    size_t total() const { return d_bytes + sum_bytes + h_bytes + row_bytes; }
+    size_t sums_at() const { return 2 * d_bytes; }
+    size_t h_at() const { return sums_at() + sum_bytes; }
+    size_t rows_at() const { return h_at() + h_bytes; }
+    size_t total() const { return rows_at() + row_bytes; }
 };
 
 // False for capacities whose buffers no device holds (the sizes stay below 2^48, and so do their products).

@@ -268,7 +268,7 @@ ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
  * partial buffer, the Lamport staging buffer (filled with the sentinel, on a
  * private stream, synchronously), partial sums of dgamma, 2 MiB a rank of
  * staged tokens for the 4-bit linear, 17 * M_max bytes of sorted tokens, with vocab_piece > 0 the cross entropy's
- * buffers (M_max * (2 * vocab_piece + 6 * K_max + 12) bytes and up to 24 MB), and
+ * buffers (M_max * (4 * vocab_piece + 6 * K_max + 12) bytes and up to 28 MB), and
  * the device status word.
  * ROCm/mori PR #662, review threads: every capacity is validated before the
  * first allocation; buffer offsets are sized from the capacities, never from
@@ -311,6 +311,17 @@ ARE_API are_status are_workspace_set_debug(are_ws* ws, uint32_t flags, int64_t a
  * single-GPU caller may raise it.  Returns ARE_EINVAL for a NULL workspace,
  * ARE_EBUSY if the workspace is in use by another thread. */
 ARE_API are_status are_workspace_set_oneshot_max_bytes(are_ws* ws, uint64_t bytes);
+
+/* How are_gemm_cross_entropy_backward hands the logits' gradient d to its two
+ * products on the bf16 tensor cores, for later calls.
+ *  parts : 2 (the default): as bf16(d) and bf16(d - bf16(d)); dh and dw are as near the
+ *          exact values as fp32 products rounded once to bf16.
+ *          1: as bf16(d), off by up to 2^-8 of each term, for callers who train with
+ *          a bf16 gradient of the logits: dh and dw are about 1.4 times as far off,
+ *          and the two products take half the time.
+ * Returns ARE_EINVAL for a NULL workspace or other parts, ARE_EBUSY if the workspace is
+ * in use by another thread. */
+ARE_API are_status are_workspace_set_logit_gradient(are_ws* ws, int parts);
 
 /* Order of the CTA-pair GEMM kernel's work units (tuning; the results do not
  * depend on it: every tile is still summed in the order r = 0..R-1).  A unit is
@@ -668,8 +679,9 @@ ARE_API are_status are_gemm_cross_entropy(const are_bf16* h, const are_bf16* con
  *            behind vocab with zeros
  *  Result  : d_iv = dloss_i * (exp(z_iv - lse_i) - [v == target_i]), 0 in rows
  *            without a target;  dh = bf16(d w), dw_r = bf16(d_r^T h).
- *            d is rounded to bf16 before the products (half a step, 2^-8 of each
- *            term), the products' sums are fp32 and rounded once.  A row without a
+ *            d enters the products as two bf16 parts, whose sum is off by 2^-16 of
+ *            each term (are_workspace_set_logit_gradient), the products' sums are
+ *            fp32 and rounded once.  A row without a
  *            target has dh 0 and takes no part in dw, whatever its h holds.
  * The vocabulary is taken in pieces of at most vocab_piece columns (more if M is
  * below M_max), and for few tokens dh's sums are split; both go by the sizes,

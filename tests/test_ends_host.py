@@ -118,7 +118,7 @@ def test_cross_entropy_buffers(tmp_path):
             for v in (1, 256, 257, 8192)]
     for (m, k, v), (ok, sums, h, rows, total) in zip(caps, _sizes(tmp_path, caps), strict=True):
         assert ok and not sums % 256 and not h % 256 and not rows % 256, (m, k, v)
-        assert sums >= m * -(-v // 256) * 256 * 2 and h - sums >= m * k * 4 and rows - h >= m * k * 2 and total - rows >= m * 12
+        assert sums >= 2 * m * -(-v // 256) * 256 * 2 and h - sums >= m * k * 4 and rows - h >= m * k * 2 and total - rows >= m * 12
     # capacities whose products pass 64 bits are refused, not wrapped
     for ok, *_ in _sizes(tmp_path, [(1, (1 << 63) - 8, 256), (1 << 62, 8, 256), (1 << 31, 1 << 31, 1), (1 << 40, 8, 1 << 28)]):
         assert not ok

@@ -284,3 +284,63 @@ def test_capacities_that_no_device_holds():
     with pytest.raises(are.AreError) as e:
         are.Workspace(R_max=1, M_max=1, N_max=8, K_max=(1 << 63) - 8, vocab_piece=256)
     assert e.value.status == are.ENOMEM
+
+
+def half_step(v):
+    """Half a step of bf16 at |v|."""
+    return torch.ldexp(torch.ones_like(v), torch.frexp(v.abs())[1] - 9)
+
+
+def gradient_bounds(h, w, t, vocab, dloss):
+    """dh, dw in 64 bits, each with the bound of products of an fp32 d, rounded to bf16 once: as ref.cross_entropy64, with
+    2^-16 for d's two bf16 parts (half a step of bf16 of what half a step of bf16 left) in place of a half step, twice the
+    terms for the two parts, and the result's own half step."""
+    K, x, y = h.shape[1], h.double(), torch.cat([v.double() for v in w])[:vocab]
+    U = 2.0 ** -24
+    z = x @ y.T
+    err = (min(K / 16, 64) + K / 512 + 16) * 2 * U * (x.abs() @ y.abs().T)
+    lse = torch.logsumexp(z, 1, keepdim=True)
+    tol_lse = err.max(1, keepdim=True).values + 2.0 ** -20 + 2 * U * lse.abs()
+    on = ((t >= 0) & (t < vocab))[:, None]
+    g = torch.where(on, dloss.double()[:, None], 0.0)
+    p = torch.exp(z - lse)
+    d = (p - torch.zeros_like(p).scatter_(1, t.long().clamp(0, vocab - 1)[:, None], 1.0)) * g
+    e = p * g * (err + tol_lse + 2.0 ** -20) * 1.1
+    e = e + 2.0 ** -16 * (d.abs() + e)
+    out = []
+    for a, ea, b, n in ((d, e, y, vocab), (d.T, e.T, x, len(h))):
+        want = a @ b
+        tol = ea @ b.abs() + (n / 8 + 64) * 2 * U * (a.abs() @ b.abs())
+        out.append((want, tol + half_step(want.abs() + tol) + 1e-30))
+    return out
+
+
+@pytest.mark.parametrize("R,M,N,K", [(2, 40, 90, 64), (1, 128, 300, 64), (3, 200, 70, 64), (1, 600, 500, 72), (2, 3, 700, 8)])
+def test_gradients_are_as_near_as_fp32_products(ws, R, M, N, K):
+    h, w, t, dloss = inputs(R, M, N, K, 7 * M + K)
+    want = gradient_bounds(h, w, t, R * N, dloss)
+    _, _, dh, dw = run(ws, h, w, t, dloss)
+    ref.check(dh, *want[0], "dh")
+    ref.check(dw.flatten(0, 1), *want[1], "dw")
+
+
+def test_one_part_of_the_logits_gradient(ws):
+    """A caller may have the logits' gradient rounded to bf16 once: within a half step of each term, and not within 2^-16."""
+    for M in (40, 300):
+        h, w, t, dloss = inputs(2, M, 500, 64, M)
+        loss, lse, dh, dw = run(ws, h, w, t, dloss)
+        ws.set_logit_gradient(1)
+        try:
+            got = run(ws, h, w, t, dloss)
+            again = run(ws, h, w, t, dloss, dw=False)[2]
+        finally:
+            ws.set_logit_gradient(2)
+        compare(got, ref.cross_entropy64(h, w, t, 1000, dloss))
+        assert torch.equal(got[0], loss) and torch.equal(got[1], lse) and torch.equal(again, got[2])
+        far = [((g.double().view_as(v) - v).abs() > tol).any() for g, (v, tol) in zip(got[2:], gradient_bounds(h, w, t, 1000, dloss))]
+        assert all(far)
+        back = run(ws, h, w, t, dloss)
+        assert torch.equal(back[2], dh) and torch.equal(back[3], dw)
+    for parts in (0, 3, -1):
+        with pytest.raises(are.AreError):
+            ws.set_logit_gradient(parts)
