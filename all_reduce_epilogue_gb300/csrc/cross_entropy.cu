@@ -57,8 +57,10 @@ constexpr uint32_t kBox = 4096;           // an epilogue warp's staging buffer: 
 // are cut, not rounded, at every step of 16: over the whole of K = 4096 the losses of 4096 tokens were 1.5e-6 off, and the
 // loss of one foreseen token at K = 2048, whose logit of 10 came out 4e-5 too small, 1.8e-5.  With rounded sums of parts of
 // 512 the 4096 losses are 1.7e-7 off (a product in fp32 3.1e-7), of 1024 3.6e-7, of 256 0.9e-7; reading the accumulators holds
-// the products up: 1077, 1070 and 1102 us in a forward pass.  One CTA's tiles, of few tokens, wait for memory anyway: 256.
-constexpr int kPartPair = 8, kPartOne = 4;
+// the products up: 1077, 1070 and 1102 us in a forward pass.  One CTA's tiles, of few tokens, mostly wait for memory: with parts
+// of 256 one token's loss is 3.4e-7 off (K = 2048, vocabulary 32000, the mean of 40), of 128 2.1e-7, as a product in fp32 is, of 64
+// 1.7e-7, in 27.8, 28.3 and 29.1 us.
+constexpr int kPartPair = 8, kPartOne = 2;
 
 template <int PASS, bool PAIR>
 struct Shape {
