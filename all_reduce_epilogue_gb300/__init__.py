@@ -78,7 +78,7 @@ EXPORTS = [
     "are_version", "are_status_string", "are_supports", "are_workspace_create", "are_workspace_destroy",
     "are_workspace_reset", "are_workspace_set_debug", "are_workspace_set_oneshot_max_bytes",
     "are_workspace_set_gemm_order", "are_workspace_set_chunks", "are_chunk_generation", "are_chunk_wait",
-    "are_workspace_set_logit_gradient",
+    "are_workspace_set_vocab_piece", "are_workspace_set_logit_gradient",
     "are_get_device_status", "are_debug_snapshot", "are_debug_last_launch",
     "are_gemm_rs", "are_gemm_ar", "are_allreduce_rmsnorm", "are_allreduce_add_rmsnorm", "are_allreduce_rmsnorm_quant",
     "are_allreduce_rmsnorm_noalloc", "are_noalloc_device_status",
@@ -102,7 +102,7 @@ class AreLibraryMissing(RuntimeError):
 class _Caps(ctypes.Structure):
     _fields_ = [("R_max", ctypes.c_int32), ("M_max", ctypes.c_int64), ("N_max", ctypes.c_int64),
                 ("K_max", ctypes.c_int64), ("timeout_ns", ctypes.c_uint64), ("debug_flags", ctypes.c_uint32),
-                ("vocab_piece", ctypes.c_uint32)]
+                ("reserved", ctypes.c_uint32)]
 
 
 class _DevStatus(ctypes.Structure):
@@ -146,6 +146,8 @@ def load_library(path: str = LIB_PATH):
     lib.are_workspace_set_oneshot_max_bytes.argtypes = [vp, u64]
     lib.are_workspace_set_gemm_order.restype = i32
     lib.are_workspace_set_gemm_order.argtypes = [vp, i32, i32, i32]
+    lib.are_workspace_set_vocab_piece.restype = i32
+    lib.are_workspace_set_vocab_piece.argtypes = [vp, i64]
     lib.are_workspace_set_logit_gradient.restype = i32
     lib.are_workspace_set_logit_gradient.argtypes = [vp, i32]
     lib.are_workspace_set_chunks.restype = i32
@@ -251,12 +253,18 @@ class Workspace:
     def __init__(self, R_max: int, M_max: int, N_max: int, K_max: int = 0, timeout_ns: int = 0,
                  debug_flags: int = 0, vocab_piece: int = 0):
         lib = load_library()
-        caps = _Caps(R_max, M_max, N_max, K_max, timeout_ns, debug_flags, vocab_piece)
+        caps = _Caps(R_max, M_max, N_max, K_max, timeout_ns, debug_flags, 0)
         h = ctypes.c_void_p()
         self.device_index = _current_device()
         _check(lib.are_workspace_create(ctypes.byref(h), ctypes.byref(caps)), "are_workspace_create")
         self._h = h
         self.caps = dict(R_max=R_max, M_max=M_max, N_max=N_max, K_max=K_max)
+        if vocab_piece:
+            try:
+                self.set_vocab_piece(vocab_piece)
+            except AreError:
+                self.close()
+                raise
 
     @property
     def handle(self):
@@ -315,6 +323,12 @@ class Workspace:
         not depend on it."""
         _check(load_library().are_workspace_set_gemm_order(self.handle, group_m, block_pairs, rank_group),
                "are_workspace_set_gemm_order")
+
+    def set_vocab_piece(self, columns: int):
+        """Allocate the cross entropy's buffers, for a gradient of so many columns of
+        the vocabulary at a time, in place of those that are there; 0 releases them.
+        Synchronises."""
+        _check(load_library().are_workspace_set_vocab_piece(self.handle, columns), "are_workspace_set_vocab_piece")
 
     def set_logit_gradient(self, parts: int):
         """bf16 parts of the logits' gradient in the cross entropy's backward

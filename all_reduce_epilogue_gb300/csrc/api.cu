@@ -41,7 +41,7 @@ struct are_ws {
     bool layernorm_ready = false;     // the same of the LayerNorm kernels
     bool embed_ready = false;         // the same of the embedding's gradient
     void* d_sort = nullptr;           // embedding's gradient: sorted tokens
-    void* d_xent = nullptr;           // cross entropy: one allocation, see xent_buffers
+    void* d_xent = nullptr;           // cross entropy: one allocation (xent_sizes.h), or none
     XentSizes xent{};
     int xent_clusters = 0;            // resident CTA pairs of its kernels, 0 before the first call
     int xent_parts = 2;               // bf16 parts of the logits' gradient
@@ -463,8 +463,7 @@ are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K) {
 are_status are_workspace_create(are_ws** out, const are_caps* caps) {
     if (!out || !caps) return ARE_EINVAL;
     *out = nullptr;
-    if (!ranks_ok(caps->R_max) || caps->M_max < 1 || caps->N_max < 8 || caps->N_max % 8 || caps->K_max < 0 ||
-        (caps->vocab_piece > 0 && caps->K_max == 0) || caps->vocab_piece > (1u << 28))
+    if (!ranks_ok(caps->R_max) || caps->M_max < 1 || caps->N_max < 8 || caps->N_max % 8 || caps->K_max < 0)
         return ARE_EINVAL;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -514,10 +513,6 @@ are_status are_workspace_create(are_ws** out, const are_caps* caps) {
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_tokens, caps->R_max * kQweightScratch);
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_dgamma, norm_backward_scratch_words(caps->N_max, ws->num_sms) * 4);
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_sort, embed_sort_bytes(caps->M_max));
-    if (e == cudaSuccess && caps->vocab_piece > 0) {
-        e = xent_sizes(caps->M_max, caps->K_max, caps->vocab_piece, ws->xent) ? cudaMalloc(&ws->d_xent, ws->xent.total())
-                                                                              : cudaErrorMemoryAllocation;
-    }
     if (e != cudaSuccess) {
         are_status st = from_cuda(e);
         free_ws(ws);
@@ -554,6 +549,27 @@ are_status are_workspace_set_debug(are_ws* ws, uint32_t flags, int64_t arg) {
     if (!lk.ok) return ARE_EBUSY;
     ws->debug_flags = flags;
     ws->debug_arg = arg;
+    return ARE_OK;
+}
+
+are_status are_workspace_set_vocab_piece(are_ws* ws, int64_t columns) {
+    if (!ws || columns < 0 || columns > (1 << 28)) return ARE_EINVAL;
+    TryLock lk(ws->mu);
+    if (!lk.ok) return ARE_EBUSY;
+    int dev = -1;
+    if ((columns > 0 && ws->caps.K_max == 0) || cudaGetDevice(&dev) != cudaSuccess || dev != ws->device) return ARE_EINVAL;
+    XentSizes sizes{};
+    if (columns > 0 && !xent_sizes(ws->caps.M_max, ws->caps.K_max, columns, sizes)) return ARE_ENOMEM;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return from_cuda(e);
+    cudaFree(ws->d_xent);
+    ws->d_xent = nullptr;
+    if (columns == 0) return ARE_OK;
+    void* at = nullptr;
+    e = cudaMalloc(&at, sizes.total());
+    if (e != cudaSuccess) return from_cuda(e);
+    ws->d_xent = at;
+    ws->xent = sizes;
     return ARE_OK;
 }
 

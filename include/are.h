@@ -129,8 +129,7 @@ typedef struct are_caps {
     int64_t K_max;       /* largest K; 0 = no GEMM buffers (AR+RMSNorm only) */
     uint64_t timeout_ns; /* bound of every device-side wait; 0 = 200 ms */
     uint32_t debug_flags;/* ARE_DEBUG_* */
-    uint32_t vocab_piece;/* cross entropy: columns of the vocabulary whose gradient is held at a time (rounded up to
-                            256); 0 = no buffers for it */
+    uint32_t reserved;   /* not read */
 } are_caps;
 
 /* Debug switches (default off; they change bookkeeping, never the arithmetic). */
@@ -267,8 +266,7 @@ ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
 /* Create a workspace on the current CUDA device: tile masks, the per-rank
  * partial buffer, the Lamport staging buffer (filled with the sentinel, on a
  * private stream, synchronously), partial sums of dgamma, 2 MiB a rank of
- * staged tokens for the 4-bit linear, 17 * M_max bytes of sorted tokens, with vocab_piece > 0 the cross entropy's
- * buffers (M_max * (4 * vocab_piece + 6 * K_max + 12) bytes and up to 28 MB), and
+ * staged tokens for the 4-bit linear, 17 * M_max bytes of sorted tokens, and
  * the device status word.
  * ROCm/mori PR #662, review threads: every capacity is validated before the
  * first allocation; buffer offsets are sized from the capacities, never from
@@ -278,8 +276,7 @@ ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
  * commits: the staging region is private to this library and is armed here,
  * outside any stream capture, on a stream of its own (an arming captured into
  * a graph would re-arm on every replay, under the kernel's feet).
- *  caps : R_max 1..8, M_max >= 1, N_max >= 8 and N_max % 8 == 0, K_max >= 0;
- *         vocab_piece > 0 needs K_max > 0.
+ *  caps : R_max 1..8, M_max >= 1, N_max >= 8 and N_max % 8 == 0, K_max >= 0.
  *  ws   : receives the handle; *ws is NULL on any failure.
  * Returns ARE_EINVAL for bad capacities, ARE_ENODEV if the current device is
  * not sm_103, ARE_ENOMEM / ARE_ECUDA if an allocation or the arming fails.
@@ -311,6 +308,18 @@ ARE_API are_status are_workspace_set_debug(are_ws* ws, uint32_t flags, int64_t a
  * single-GPU caller may raise it.  Returns ARE_EINVAL for a NULL workspace,
  * ARE_EBUSY if the workspace is in use by another thread. */
 ARE_API are_status are_workspace_set_oneshot_max_bytes(are_ws* ws, uint64_t bytes);
+
+/* Allocate the cross entropy's buffers, which a workspace does not have from its
+ * creation (M_max * (4 * columns + 6 * K_max + 12) bytes and up to 28 MB), or
+ * release them.
+ *  columns : columns of the vocabulary whose gradient is held at a time, rounded up
+ *            to 256 (8192, say), at most 2^28; 0 releases the buffers.
+ * Buffers that are there are released first, after a synchronisation of the
+ * device; graphs captured with them must not be replayed any more.
+ * Returns ARE_EINVAL for a NULL workspace, columns out of range, K_max == 0 or
+ * another current device, ARE_ENOMEM if the buffers do not fit (there are none
+ * then), ARE_EBUSY if the workspace is in use by another thread.  Not capturable. */
+ARE_API are_status are_workspace_set_vocab_piece(are_ws* ws, int64_t columns);
 
 /* How are_gemm_cross_entropy_backward hands the logits' gradient d to its two
  * products on the bf16 tensor cores, for later calls.
@@ -665,7 +674,7 @@ ARE_API are_status are_embedding_ar_backward(const void* ids, int index_format, 
  *  Result  : z_iv = sum_k h_ik w_vk (fp32), lse_i = log sum_{v < vocab} exp(z_iv),
  *            loss_i = lse_i - z_{i, target_i}.  Rows do not depend on one another; a
  *            row with a NaN or infinite logit has NaN or infinite results.
- * Needs a workspace with vocab_piece > 0, M <= M_max, K <= K_max, R <= R_max.
+ * Needs a workspace with are_workspace_set_vocab_piece, M <= M_max, K <= K_max, R <= R_max.
  */
 ARE_API are_status are_gemm_cross_entropy(const are_bf16* h, const are_bf16* const w[], const void* targets,
                                           int index_format, int64_t vocab, float* loss, float* lse, int R, int64_t M,
@@ -683,7 +692,7 @@ ARE_API are_status are_gemm_cross_entropy(const are_bf16* h, const are_bf16* con
  *            each term (are_workspace_set_logit_gradient), the products' sums are
  *            fp32 and rounded once.  A row without a
  *            target has dh 0 and takes no part in dw, whatever its h holds.
- * The vocabulary is taken in pieces of at most vocab_piece columns (more if M is
+ * The vocabulary is taken in pieces of at most are_workspace_set_vocab_piece's columns (more if M is
  * below M_max), and for few tokens dh's sums are split; both go by the sizes,
  * the capacities and the device, so workspaces of the same capacities give the
  * same bits.  Outputs that overlap one another or an input are refused

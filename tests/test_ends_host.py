@@ -122,3 +122,8 @@ def test_cross_entropy_buffers(tmp_path):
     # capacities whose products pass 64 bits are refused, not wrapped
     for ok, *_ in _sizes(tmp_path, [(1, (1 << 63) - 8, 256), (1 << 62, 8, 256), (1 << 31, 1 << 31, 1), (1 << 40, 8, 1 << 28)]):
         assert not ok
+
+
+def test_setters_refuse_null_workspaces(lib):
+    assert lib.are_workspace_set_vocab_piece(None, 256) == are.EINVAL
+    assert lib.are_workspace_set_logit_gradient(None, 2) == are.EINVAL

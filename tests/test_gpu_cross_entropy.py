@@ -1,4 +1,6 @@
 """Softmax cross entropy of an output layer split over the ranks, and its gradients."""
+import ctypes
+
 import pytest
 import torch
 
@@ -344,3 +346,42 @@ def test_one_part_of_the_logits_gradient(ws):
     for parts in (0, 3, -1):
         with pytest.raises(are.AreError):
             ws.set_logit_gradient(parts)
+
+
+def test_the_reserved_word_of_the_capacities_is_not_read():
+    """A caller from before the cross entropy may have left it unset: the workspace is made, without the cross entropy's
+    buffers."""
+    need_gpu()
+    lib = are.load_library()
+    free = []
+    for word in (0, 0xDEADBEEF, 4096, 1 << 28):
+        for K_max in (0, 512):
+            caps, ws = are._Caps(2, 65536, 64, K_max, 0, 0, word), ctypes.c_void_p()
+            assert lib.are_workspace_create(ctypes.byref(ws), ctypes.byref(caps)) == are.OK
+            if K_max:
+                free.append(torch.cuda.mem_get_info()[0])
+            assert lib.are_workspace_destroy(ws) == are.OK
+    assert max(free) - min(free) < 1 << 26   # (4096 columns of 65536 rows are 2^30 bytes)
+
+
+def test_buffers_made_changed_and_released():
+    need_gpu()
+    h, w, t, dloss = inputs(2, 60, 3000, 64, 1)
+    want = ref.cross_entropy64(h, w, t, 6000, dloss)
+    with are.Workspace(R_max=2, M_max=60, N_max=8, K_max=64) as ws:
+        for columns in (0, 256, 5000, 256, 0):
+            ws.set_vocab_piece(columns)
+            if columns:
+                compare(run(ws, h, w, t, dloss), want)
+            else:
+                with pytest.raises(are.AreError) as e:
+                    run(ws, h, w, t, dloss)
+                assert e.value.status == are.ECAPACITY
+        ws.set_vocab_piece(256)
+        for columns in (-1, (1 << 28) + 1):
+            with pytest.raises(are.AreError) as e:
+                ws.set_vocab_piece(columns)
+            assert e.value.status == are.EINVAL
+        compare(run(ws, h, w, t, dloss), want)
+    with are.Workspace(R_max=2, M_max=60, N_max=8) as ws, pytest.raises(are.AreError):
+        ws.set_vocab_piece(256)   # K_max missing
