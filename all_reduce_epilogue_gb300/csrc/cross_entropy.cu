@@ -521,10 +521,15 @@ __global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(co
         for (int u = first; u < p.units; u += pairs, ++it) {
             const Tile t = tile_of<PASS>(p, u);
             const int buf = it & 1;
+            const bool dw = t.kind == kXentDW;
+            const Place at = place_of(p, dw ? t.tm : 0);
+            const int m0 = t.tm * kSide + q * 128 + w * 32;        // the warp's rows of the tile
+            const int r0 = dw ? at.col + q * 128 + w * 32 : m0;   // and of dh, or of a rank's dW
+            // a row without a target, or behind the vocabulary, is zeros: its d is, but 0 times an infinity or a NaN is none
+            const bool on = dw ? r0 + lane - at.col < columns_of(p, at, kSide) : m0 + lane < p.M && target_of(p, m0 + lane) >= 0;
             if (!__all_sync(0xFFFFFFFFu, wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, abort_flag, p, 33, u))) break;
             ptx::tc_fence_after();
             const uint32_t acc = tmem_base + ((uint32_t)(w * 32) << 16) + buf * kSide;
-            const int m0 = t.tm * kSide + q * 128 + w * 32;  // the warp's rows of the tile
 
             if (t.kind == kXentDH && p.sums) {
                 // fp32 sums of this split, over the pieces
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(co
                     uint8_t* box = out.next();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        *chunk_at(box, lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        *chunk_at(box, lane, i) = on ? make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]) : make_uint4(0u, 0u, 0u, 0u);
                     ptx::fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
@@ -548,9 +553,6 @@ __global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(co
                 }
             } else {
                 // bf16 results: rows of dh, or of a rank's dW
-                const bool dw = t.kind == kXentDW;
-                const Place at = place_of(p, dw ? t.tm : 0);
-                const int r0 = dw ? at.col + q * 128 + w * 32 : m0;
                 const bool store = r0 < (dw ? p.Vs : p.M);
                 const CUtensorMap* map = dw ? &p.tmOut[at.rank] : &p.tmDH;
                 for (int c = 0; c < kTile && t.tn * kTile + c < p.K; c += 64) {
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(Shape<PASS, PAIR>::kThreads, 1) xent_kernel(co
                             uint32_t d[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                d[j] = bf16x2(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
+                                d[j] = on ? bf16x2(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1])) : 0u;
                             *chunk_at(box, lane, half * 4 + i) = make_uint4(d[0], d[1], d[2], d[3]);
                         }
                     }

@@ -691,7 +691,7 @@ ARE_API are_status are_gemm_cross_entropy(const are_bf16* h, const are_bf16* con
  *            d enters the products as two bf16 parts, whose sum is off by 2^-16 of
  *            each term (are_workspace_set_logit_gradient), the products' sums are
  *            fp32 and rounded once.  A row without a
- *            target has dh 0 and takes no part in dw, whatever its h holds.
+ *            target has dh 0 and takes no part in dw, whatever its row of h and w hold.
  * The vocabulary is taken in pieces of at most are_workspace_set_vocab_piece's columns (more if M is
  * below M_max), and for few tokens dh's sums are split; both go by the sizes,
  * the capacities and the device, so workspaces of the same capacities give the

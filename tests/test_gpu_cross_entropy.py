@@ -385,3 +385,22 @@ def test_buffers_made_changed_and_released():
         compare(run(ws, h, w, t, dloss), want)
     with are.Workspace(R_max=2, M_max=60, N_max=8) as ws, pytest.raises(are.AreError):
         ws.set_vocab_piece(256)   # K_max missing
+
+
+@pytest.mark.parametrize("M", [9, 200, 1000])
+def test_zeros_whatever_the_other_operand_holds(ws, M):
+    """Rows without a target have dh 0 whatever the weights hold, padding has dw 0 whatever the hidden states do."""
+    R, N, K, vocab = 3, 401, 96, 1100
+    h, w, t, dloss = inputs(R, M, N, K, M, vocab=vocab)
+    none = (t < 0) | (t >= vocab)
+    bad = [v.clone() for v in w]
+    bad[0][5, 3], bad[1][400, 7] = float("inf"), float("nan")
+    dh = run(ws, h, bad, t, dloss, vocab=vocab)[2]
+    assert none.any() and (dh[none] == 0).all() and dh[~none].isnan().any()
+    wild = h.clone()
+    wild[5, 3], wild[6, 9] = float("inf"), float("nan")    # both have a target
+    _, _, dh, dw = run(ws, wild, w, t, dloss, vocab=vocab)
+    dw = dw.flatten(0, 1)
+    assert (dw[vocab:] == 0).all() and dw[:vocab].isnan().any() and (dh[none] == 0).all()
+    with are.Workspace(R_max=R, M_max=M, N_max=8, K_max=K, vocab_piece=1) as small:   # (1000 rows: fp32 sums over pieces)
+        assert (run(small, h, bad, t, dloss, vocab=vocab)[2][none] == 0).all()
