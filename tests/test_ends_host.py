@@ -127,3 +127,12 @@ def test_cross_entropy_buffers(tmp_path):
 def test_setters_refuse_null_workspaces(lib):
     assert lib.are_workspace_set_vocab_piece(None, 256) == are.EINVAL
     assert lib.are_workspace_set_logit_gradient(None, 2) == are.EINVAL
+
+
+@pytest.mark.parametrize("source", ["cross_entropy.cu", "ptx.cuh", "norm_rows.cu", "qweight.cu"])
+def test_no_non_coherent_loads_in_the_other_kernels_under_programmatic_launch(source):
+    """The same of the cross entropy, of the wrappers that all of them load through, and of the earlier kernels."""
+    code = re.sub(r"//[^\n]*", "", open(os.path.join(os.path.dirname(are.__file__), "csrc", source)).read())
+    assert not re.findall(r"__ldg\b|ld\.global(?:\.\w+)*\.nc\b|__restrict__", code)
+    if source == "ptx.cuh":
+        assert re.findall(r"ld_stream_v4", code)
