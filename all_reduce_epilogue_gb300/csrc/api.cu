@@ -40,7 +40,8 @@ struct are_ws {
     bool rows_ready = false;          // the row kernels' first call has prepared them
     bool layernorm_ready = false;     // the same of the LayerNorm kernels
     bool embed_ready = false;         // the same of the embedding's gradient
-    void* d_sort = nullptr;           // embedding's gradient: sorted tokens
+    void* d_sort = nullptr;           // embedding's gradient: sorted tokens (its first call allocates them)
+    void* d_two_sums = nullptr;       // the LayerNorm's backward pass, embedding's gradient: partial rows (the same)
     void* d_xent = nullptr;           // cross entropy: one allocation (xent_sizes.h), or none
     XentSizes xent{};
     int xent_clusters = 0;            // resident CTA pairs of its kernels, 0 before the first call
@@ -112,6 +113,7 @@ void free_ws(are_ws* ws) {
     cudaFree(ws->d_cons);
     cudaFree(ws->d_xent);
     cudaFree(ws->d_sort);
+    cudaFree(ws->d_two_sums);
     if (ws->h_chunk_gen) cudaFreeHost(ws->h_chunk_gen);
     delete ws;
 }
@@ -473,6 +475,10 @@ are_status are_workspace_create(are_ws** out, const are_caps* caps) {
     if (e != cudaSuccess) return from_cuda(e);
     if (prop.major != 10 || prop.minor != 3) return ARE_ENODEV;
 
+    // no device holds 2^48 bytes, and below them no size here wraps
+    if ((caps->K_max > 0 || caps->N_max <= 32768) && (double)caps->M_max * (double)caps->N_max > (double)(1ll << 46))
+        return ARE_ENOMEM;
+
     are_ws* ws = new (std::nothrow) are_ws;
     if (!ws) return ARE_ENOMEM;
     ws->device = dev;
@@ -512,7 +518,6 @@ are_status are_workspace_create(are_ws** out, const are_caps* caps) {
     }
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_tokens, caps->R_max * kQweightScratch);
     if (e == cudaSuccess) e = cudaMalloc(&ws->d_dgamma, norm_backward_scratch_words(caps->N_max, ws->num_sms) * 4);
-    if (e == cudaSuccess) e = cudaMalloc(&ws->d_sort, embed_sort_bytes(caps->M_max));
     if (e != cudaSuccess) {
         are_status st = from_cuda(e);
         free_ws(ws);
@@ -802,6 +807,20 @@ cudaError_t prepare_rows(are_ws* ws) {
     ws->rows_ready = e == cudaSuccess;
     return e;
 }
+
+// A buffer of an operation that most workspaces never see, allocated by its first call.  That may be captured: in relaxed mode
+// an allocation leaves captures, this thread's and others', alone.
+cudaError_t on_first_call(void** buffer, size_t bytes) {
+    if (*buffer) return cudaSuccess;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    e = cudaMalloc(buffer, bytes);
+    if (e != cudaSuccess) *buffer = nullptr;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    return e;
+}
+cudaError_t two_sums(are_ws* ws) { return on_first_call(&ws->d_two_sums, two_sums_words(ws->caps.N_max, ws->num_sms) * 4); }
 
 cudaError_t prepare_layernorm(are_ws* ws) {
     if (ws->layernorm_ready) return cudaSuccess;
@@ -1170,7 +1189,8 @@ are_status are_allreduce_layernorm_backward(const are_bf16* const dy[], const ar
         }
         return ARE_OK;
     }
-    const cudaError_t e = prepare_layernorm(ws);
+    cudaError_t e = prepare_layernorm(ws);
+    if (e == cudaSuccess && (dgamma || dbeta)) e = two_sums(ws);
     if (e != cudaSuccess) return from_cuda(e);
 
     RowsParams p;
@@ -1184,9 +1204,9 @@ are_status are_allreduce_layernorm_backward(const are_bf16* const dy[], const ar
     p.backward = 1;
     RowsPlan plan = layernorm_plan(p, ws->num_sms);
     // two rows of partial sums a block
-    plan.grid = (int)std::min<int64_t>(plan.grid, (int64_t)norm_backward_scratch_words(ws->caps.N_max, ws->num_sms) / (2 * N));
+    plan.grid = (int)std::min<int64_t>(plan.grid, (int64_t)two_sums_words(ws->caps.N_max, ws->num_sms) / (2 * N));
     ws->last = are_launch_info{p.lanes ? ARE_KERNEL_LAYERNORM_BACKWARD_NARROW : ARE_KERNEL_LAYERNORM_BACKWARD_ROWS, plan.grid, plan.threads, 1, 0, plan.ppt, 0, 0};
-    return from_cuda(launch_layernorm_backward_rows(p, plan, ws->d_dgamma, dgamma, dbeta, s));
+    return from_cuda(launch_layernorm_backward_rows(p, plan, static_cast<float*>(ws->d_two_sums), dgamma, dbeta, s));
 }
 
 are_status are_embedding_ar(const void* ids, int index_format, const are_bf16* const table[], float scale, are_bf16* out,
@@ -1246,12 +1266,17 @@ are_status are_embedding_ar_backward(const void* ids, int index_format, const ar
         if (e != cudaSuccess) return from_cuda(e);
         ws->embed_ready = true;
     }
+    if (M > kEmbedFew) {
+        cudaError_t e = on_first_call(&ws->d_sort, embed_sort_bytes(ws->caps.M_max));
+        if (e == cudaSuccess) e = two_sums(ws);
+        if (e != cudaSuccess) return from_cuda(e);
+    }
     EmbedParams p{};
     embed_common(p, ids, index_format, scale, dtable, R, M, N, V);
     p.dy = dy;
     p.accumulate = accumulate != 0;
     int grid = 0;
-    const cudaError_t e = launch_embedding_backward(p, ws->d_sort, ws->d_dgamma, ws->num_sms, &grid,
+    const cudaError_t e = launch_embedding_backward(p, ws->d_sort, static_cast<float*>(ws->d_two_sums), ws->num_sms, &grid,
                                                     reinterpret_cast<cudaStream_t>(stream));
     const bool few = M > 0 && M <= kEmbedFew;
     ws->last = are_launch_info{few ? ARE_KERNEL_EMBEDDING_BACKWARD_FEW : ARE_KERNEL_EMBEDDING_BACKWARD, grid, few ? 256 : 1024,

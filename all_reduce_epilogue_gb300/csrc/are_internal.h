@@ -134,11 +134,13 @@ cudaError_t launch_norm_quant_rows(const RowsParams& p, const RowsPlan& plan, bo
 cudaError_t launch_norm_backward_rows(RowsParams& p, const RowsPlan& plan, float* scratch, float* dgamma,
                                       cudaStream_t stream);
 size_t norm_backward_scratch_words(int64_t n_max, int num_sms);
+// Of the LayerNorm's, which sums dbeta too, and of the embedding's.
+inline size_t two_sums_words(int64_t n_max, int num_sms) { return 2 * norm_backward_scratch_words(n_max, num_sms); }
 
 // The columns' sums over `rows` partial rows [rows, N], and with `second` over as many right behind them.
 cudaError_t launch_row_sums(const float* part, float* first, float* second, int rows, int N, cudaStream_t stream);
 
-// LayerNorm on the same rows (layernorm.cu).
+// LayerNorm on the same rows (layernorm.cu).  scratch: two_sums_words() floats; dgamma and dbeta may be nullptr.
 RowsPlan layernorm_plan(RowsParams& p, int num_sms);
 cudaError_t layernorm_prepare();
 cudaError_t launch_layernorm_rows(const RowsParams& p, const RowsPlan& plan, cudaStream_t stream);
@@ -274,7 +276,7 @@ constexpr int kEmbedFew = 512;  // tokens whose gradient is one launch
 cudaError_t embed_prepare();
 size_t embed_sort_bytes(int64_t M_max);
 cudaError_t launch_embedding(const EmbedParams& p, int* grid, cudaStream_t stream);
-// sort: embed_sort_bytes(M); scratch: norm_backward_scratch_words(N, num_sms) floats.
+// sort: embed_sort_bytes(M); scratch: two_sums_words(N, num_sms) floats.  Up to kEmbedFew tokens need neither.
 cudaError_t launch_embedding_backward(EmbedParams& p, void* sort, float* scratch, int num_sms, int* grid, cudaStream_t stream);
 
 // ------------------------------------------------------------------ cross entropy (cross_entropy.cu)

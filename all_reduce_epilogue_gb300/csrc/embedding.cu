@@ -642,7 +642,7 @@ cudaError_t launch_embedding_backward(EmbedParams& p, void* sort, float* scratch
     // as many chunks as run at once (16384 x 4096: 222 of 74 tokens, 32 us; 373 of 44, which take a second round, 36),
     // two partial rows each, of those that a workspace of this width has, so that the order of the sums goes by the
     // sizes alone
-    const int64_t rows = (int64_t)norm_backward_scratch_words(p.N, num_sms) / p.N;
+    const int64_t rows = (int64_t)two_sums_words(p.N, num_sms) / p.N;
     const int64_t most = std::min<int64_t>(rows / 2, (int64_t)num_sms * kSumBlocks / slabs * p.block_chunks);
     p.chunk = std::max<int64_t>(8, (p.M + most - 1) / most);
     p.chunks = (p.M + p.chunk - 1) / p.chunk;

@@ -461,8 +461,7 @@ size_t norm_backward_scratch_words(int64_t n_max, int num_sms) {
     // N <= 8 nt, less than 8 * kRowsThreads columns; with two, N > 2048 and nt >= 160, three blocks at most and less than
     // twice that
     const int64_t n = n_max < kBackwardMaxN ? n_max : kBackwardMaxN, most = 8 * kRowsThreads;
-    // (and twice that for the LayerNorm, which sums dbeta too)
-    return 2 * (size_t)std::max(std::max(2 * n, std::min(3 * n, 2 * most)), std::min(kRowsThreads / 64 * n, most)) * num_sms;
+    return (size_t)std::max(std::max(2 * n, std::min(3 * n, 2 * most)), std::min(kRowsThreads / 64 * n, most)) * num_sms;
 }
 
 }  // namespace are

@@ -48,7 +48,8 @@
  *    are_embedding_ar_backward, are_gemm_ar_qweight and
  *    are_gemm_ar_qweight_qx may be captured into a CUDA graph once
  *    their workspace exists: they only enqueue work on `stream` (kernels;
- *    memsets for an empty contraction), and the state they leave for the next call
+ *    memsets for an empty contraction; a first call may allocate, which capture
+ *    allows, where its text says so), and the state they leave for the next call
  *    (tile masks at 0, staging words at -0.0) is restored inside those
  *    kernels, never by a host step, so every replay finds it as the capture
  *    did.  Workspace creation, reset and snapshots are not capturable.
@@ -266,8 +267,9 @@ ARE_API are_status are_supports(int op, int R, int64_t M, int64_t N, int64_t K);
 /* Create a workspace on the current CUDA device: tile masks, the per-rank
  * partial buffer, the Lamport staging buffer (filled with the sentinel, on a
  * private stream, synchronously), partial sums of dgamma, 2 MiB a rank of
- * staged tokens for the 4-bit linear, 17 * M_max bytes of sorted tokens, and
- * the device status word.
+ * staged tokens for the 4-bit linear, and the device status word.  Buffers that one operation alone needs are not among
+ * them: the cross entropy's (are_workspace_set_vocab_piece), and those that the
+ * first are_allreduce_layernorm_backward and are_embedding_ar_backward allocate.
  * ROCm/mori PR #662, review threads: every capacity is validated before the
  * first allocation; buffer offsets are sized from the capacities, never from
  * a call's M, so the layout does not move between calls; a set-up that fails
@@ -611,9 +613,11 @@ ARE_API are_status are_allreduce_layernorm(const are_bf16* const partials[], con
  *            dgamma_j = sum_i dy_ij * xhat_ij, dbeta_j = sum_i dy_ij, in fp32, in
  *            an order that depends on M, N, R, whether dres is given and the
  *            device's SM count alone.
- * beta does not enter.  M == 0 writes zeros to dgamma and dbeta.  Uses a buffer
- * of the workspace for partial sums: N must not exceed N_max (ARE_ECAPACITY), R
- * not R_max.
+ * beta does not enter.  M == 0 writes zeros to dgamma and dbeta.  N must not
+ * exceed N_max (ARE_ECAPACITY), R not R_max.  The first call of a workspace that
+ * asks for a gradient of gamma or beta allocates twice the buffer that the
+ * RMSNorm's has for partial sums (40 MB at N_max >= 16384), also while a stream is
+ * captured, and returns ARE_ENOMEM if there is no room.
  */
 ARE_API are_status are_allreduce_layernorm_backward(const are_bf16* const dy[], const are_bf16* h, const float* gamma,
                                                     float eps, const are_bf16* dres, are_bf16* dh, float* dgamma,
@@ -651,7 +655,9 @@ ARE_API are_status are_embedding_ar(const void* ids, int index_format, const are
  *             order that depends on the ids, M, N and the device's SM count alone;
  *             dtable_v = bf16( s_v * scale ), accumulating bf16( s_v * scale + f32(dtable_v) ).
  * Tables that overlap one another, dy or ids are refused (ARE_EINVAL).  Needs
- * M <= M_max, N <= N_max, R <= R_max.
+ * M <= M_max, N <= N_max, R <= R_max.  The first call of more than 512 tokens
+ * allocates 17 * M_max bytes for the sorted tokens, and the buffer of
+ * are_allreduce_layernorm_backward, as it does.
  */
 ARE_API are_status are_embedding_ar_backward(const void* ids, int index_format, const are_bf16* dy, float scale,
                                              int accumulate, are_bf16* const dtable[], int R, int64_t M, int64_t N,

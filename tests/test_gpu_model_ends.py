@@ -221,3 +221,52 @@ def test_first_calls_captured():
     """).replace("ROOT", repr(ROOT))
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "ok" in r.stdout, r.stdout + r.stderr
+
+
+def test_workspaces_without_what_one_operation_needs():
+    """The partial rows of LayerNorm's gradients and the sorted tokens take no memory before a call needs them."""
+    need_gpu()
+
+    def held():
+        torch.cuda.synchronize()
+        return torch.cuda.mem_get_info()[0]
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    M, N = 1 << 20, 16384
+    x, dh, g = torch.randn((600, 64), device="cuda").to(torch.bfloat16), torch.empty((600, 64), **bf), torch.ones(64, device="cuda")
+    dg, db, ids = torch.empty_like(g), torch.empty_like(g), torch.arange(600, device="cuda") % 50
+    table = torch.empty((50, 64), **bf)
+    with are.Workspace(R_max=1, M_max=600, N_max=64) as ws:   # (kernels are loaded by their first launch)
+        for rows in (64, 600):
+            are.allreduce_layernorm_backward([x[:rows]], x[:rows], g, 1e-5, dh[:rows], dg, db, ws)
+        for rows in (512, 600):
+            are.embedding_ar_backward(ids[:rows], x[:rows], [table], ws)
+    before = held()
+    with are.Workspace(R_max=1, M_max=64, N_max=N) as ws:
+        made = held()
+        assert before - made < 30 << 20   # 20 MB for the RMSNorm's partial sums, 4 MB of staging, 2 MB of tokens
+        are.allreduce_layernorm_backward([x[:64]], x[:64], g, 1e-5, dh[:64], None, None, ws)
+        assert held() == made
+        are.allreduce_layernorm_backward([x[:64]], x[:64], g, 1e-5, dh[:64], dg, db, ws)
+        assert 38 << 20 <= made - held() < 50 << 20   # 4 * 16384 * 152 words are 38 MiB
+    before = held()
+    with are.Workspace(R_max=1, M_max=M, N_max=64) as ws:
+        made = held()
+        assert before - made < 270 << 20  # 256 MB of staging
+        are.embedding_ar_backward(ids[:512], x[:512], [table], ws)
+        assert held() == made
+        are.embedding_ar_backward(ids, x, [table], ws)
+        assert made - held() > 17 * M
+        now = held()
+        are.embedding_ar_backward(ids, x, [table], ws)
+        are.allreduce_layernorm_backward([x], x, g, 1e-5, dh, dg, db, ws)
+        assert held() == now
+        want = torch.zeros((50, 64), dtype=torch.float64, device="cuda").index_add_(0, ids, x.double())
+        assert ((table.double() - want).abs() <= want.abs() * 2.0 ** -8 + 1e-4).all()
+
+
+def test_capacities_past_64_bits_are_refused():
+    need_gpu()
+    for M, N, K in ((1 << 60, 8, 0), (1 << 62, 32768, 0), (1 << 61, 8, 8), (8, 1 << 62, 8)):
+        with pytest.raises(are.AreError) as e:
+            are.Workspace(R_max=8, M_max=M, N_max=N, K_max=K)
+        assert e.value.status == are.ENOMEM
