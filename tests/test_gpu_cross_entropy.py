@@ -404,3 +404,32 @@ def test_zeros_whatever_the_other_operand_holds(ws, M):
     assert (dw[vocab:] == 0).all() and dw[:vocab].isnan().any() and (dh[none] == 0).all()
     with are.Workspace(R_max=R, M_max=M, N_max=8, K_max=K, vocab_piece=1) as small:   # (1000 rows: fp32 sums over pieces)
         assert (run(small, h, bad, t, dloss, vocab=vocab)[2][none] == 0).all()
+
+
+@pytest.mark.parametrize("M", [40, 300])
+def test_graph_replays_of_a_padded_vocabulary(ws, M):
+    """Zeros for whole ranks behind the vocabulary stand before the kernels; several pieces, both numbers of parts."""
+    R, N, K, vocab = 4, 2100, 64, 5000
+    h, w, t, dloss = inputs(R, M, N, K, M, vocab=vocab)
+    loss, lse = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    dh, dw = torch.empty_like(h), torch.empty((R, N, K), dtype=torch.bfloat16, device="cuda")
+    run(ws, h, w, t, dloss, vocab=vocab)
+    graphs = []
+    for parts in (1, 2):
+        ws.set_logit_gradient(parts)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            are.gemm_cross_entropy(h, w, t, loss, lse, ws, vocab=vocab)
+            are.gemm_cross_entropy_backward(h, w, t, lse, dloss, dh, list(dw), ws, vocab=vocab)
+    for k in range(4):
+        h2, w2, t2, d2 = inputs(R, M, N, K, 60 + k, vocab=vocab)
+        for a, b in zip([h, t, dloss, *w], [h2, t2, d2, *w2]):
+            a.copy_(b)
+        dw.fill_(5)
+        graphs[k % 2].replay()
+        torch.cuda.synchronize()
+        compare((loss, lse, dh, dw), ref.cross_entropy64(h, w, t, vocab, dloss))
+        assert (dw.flatten(0, 1)[vocab:] == 0).all()
+        if k % 2:
+            eager = run(ws, h, w, t, dloss, vocab=vocab)
+            assert torch.equal(eager[2], dh) and torch.equal(eager[3], dw)
