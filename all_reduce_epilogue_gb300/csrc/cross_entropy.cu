@@ -7,7 +7,8 @@
 //   dh     = d W                                   dW_r = d_r^T h
 //
 // Four products on the tensor cores, which are what bounds it (2 M V K operations
-// forward, three times that backward, the logits being formed a second time):
+// forward, three times that backward, the logits being formed a second time, and five
+// times with d in two parts):
 //   kLogSum   z, whose epilogue leaves the maximum of 64 or 128 columns of a row and the
 //             sum of exp(z - maximum): 8 bytes for what would be 256 and more.  A small
 //             kernel joins the tiles' pairs; pieces of the vocabulary as large as the
@@ -32,12 +33,11 @@
 // Tiles are taken in groups of rows whose operand stays in L2 while the other one
 // streams past (16 rows of tiles: forward 1055 us, 8: 1076).
 //
-// Measured, 4096 tokens, K = 4096, vocabulary 65536 over 8 ranks: forward 1.05 to 1.09 ms, 2.0
-// to 2.1 PFLOP/s; forward and backward 5.1 to 5.3 ms, 1.7 PFLOP/s, the rate that the power limit
-// leaves a library's product (5.5 ms in a long run).  One token, K = 2048, vocabulary 32000: 27 us,
-// 4.8 TB/s, of which 7 are the two kernels' starts and ends.  77 tokens, K = 1000,
-// vocabulary 11001, both directions: 41 us, the latencies of five kernels (33 at K = 1024,
-// whose rows are whole lines).
+// Measured, 4096 tokens, K = 4096, vocabulary 65536 over 8 ranks: forward 1.07 ms, 2.05 PFLOP/s, in
+// a long run 1.25; forward and backward 7.8 to 7.9 ms, 1.67 to 1.7 PFLOP/s of what is multiplied, the
+// rate that the power limit leaves a library's product (8.1 to 8.3 ms in a long run; d in one part 5.2 to 5.4).  One
+// token, K = 2048, vocabulary 32000: 28.3 us, 4.6 TB/s, of which 7 are the two kernels' starts and
+// ends.  77 tokens, K = 1000, vocabulary 11001, both directions: 48 us, the latencies of five kernels (d in one part 43).
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -192,7 +192,8 @@ struct Stager {
 
 // The hidden states with zeros in the rows that have no target: d is 0 there, but 0 times an infinity or a NaN, which padding
 // may hold, is none.  dW's product reads the copy in h's place.  kXentDLogits' epilogue warps make it before their first tile,
-// under its products (a launch of its own took 10 us of 5 ms at 4096 x 4096, 2 of 40 at 77 x 1000).
+// under its products (a launch of its own took 10 us of 5 ms at 4096 x 4096, 2 of 40 at 77 x 1000).  Its warps are those of the
+// first piece's tiles: for a vocabulary of a few hundred they are few (128 tokens, K = 8192, vocabulary 100: 125 us for all).
 __device__ __forceinline__ void copy_rows(const XentParams& p, int warp, int warps) {
     const int lane = threadIdx.x & 31, packs = p.K >> 3;
     for (int64_t row = warp; row < p.M; row += warps) {

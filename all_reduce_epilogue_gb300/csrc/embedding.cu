@@ -23,9 +23,10 @@
 // that the zeros wait for the sort (with the rest of the zeros in step 3 the three took 159 us).
 // Up to 512 tokens a kernel of its own does all of it.
 //
-// Measured, 16384 x 4096, vocabulary 65536 over 8 ranks: lookup 31 us, 8.6 TB/s (rows that come
-// again are in L2); gradient 123 us, 5.5 TB/s of the bytes it cannot do without: zeros 82 us, the
-// sort below them, sums 33, join 8; added to tables that are there 95 us (with one CTA's sort 132).
+// Measured, 16384 x 4096, vocabulary 65536 over 8 ranks, 6000 of them in the text: lookup 31.5 us, 5.8 TB/s of
+// the bytes it cannot do without (8.6 with the rows that come again, which are in L2); gradient 124 us,
+// 5.3 TB/s: zeros 82 us, the sort below them, sums 33, join 8; added to tables that are there 76 us for
+// 33: sort 16, sums 52 (a row of the table is loaded where its sum ends, and nothing runs under that), join 8.
 // 300 x 1032, vocabulary 11001: 8.7 us; 16384 x 1032: 34 (one CTA's sort 63).
 #include <algorithm>
 
