@@ -270,3 +270,24 @@ def test_capacities_past_64_bits_are_refused():
         with pytest.raises(are.AreError) as e:
             are.Workspace(R_max=8, M_max=M, N_max=N, K_max=K)
         assert e.value.status == are.ENOMEM
+
+
+def test_a_refused_allocation_leaves_no_error_behind():
+    """A workspace, or the cross entropy's buffers, that the device has no room for: a status, and nothing that the next
+    launch of the process reports."""
+    need_gpu()
+    x = torch.ones(8, device="cuda")
+    with are.Workspace(R_max=1, M_max=65536, N_max=8, K_max=8) as ws:
+        with pytest.raises(are.AreError) as e:
+            ws.set_vocab_piece(1 << 27)      # 2^45 bytes
+        assert e.value.status == are.ENOMEM
+        assert (x + 1 == 2).all()
+        with pytest.raises(are.AreError) as e:
+            are.Workspace(R_max=1, M_max=1 << 40, N_max=8)
+        assert e.value.status == are.ENOMEM
+        assert (x * 2 == 2).all()
+        ws.set_vocab_piece(256)
+        h = torch.zeros((4, 8), dtype=torch.bfloat16, device="cuda")
+        loss, lse, t = torch.empty(4, device="cuda"), torch.empty(4, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda")
+        are.gemm_cross_entropy(h, [h], t, loss, lse, ws)
+        assert ((loss - torch.log(torch.tensor(4.0, device="cuda"))).abs() < 1e-6).all()
